@@ -307,6 +307,169 @@ PVL_API pvl_status adaln_bwd(const pvl_bf16* x, const float* scale, const pvl_bf
                              pvl_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * pack_build_positions — position of each token inside its packed segment,
+ * the companion of pack_build_seq_ids for position embeddings.
+ *
+ * seg_frames, B, K, tokens_per_frame (T), L: as pack_build_seq_ids (valid
+ *   frames play no part: padding frames continue their segment).  With i the
+ *   token's offset from the start of its segment, the axes written are
+ *   axes = 1: i;  axes = 2: i / T, i % T (frame, token of the frame);
+ *   axes = 3: i / T, (i % T) / row_width, (i % T) % row_width (frame, row,
+ *   column).  Tokens past the last segment get zeros.
+ * positions: dev int32 [B * L * axes], written completely.
+ * Errors: as pack_build_seq_ids; INVALID_ARG for axes outside 1..3 or, with
+ *   three axes, row_width < 1.
+ * ---------------------------------------------------------------------- */
+PVL_API pvl_status pack_build_positions(const int32_t* seg_frames, int B, int K, int tokens_per_frame, int axes,
+                                        int row_width, int L, int32_t* positions, pvl_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * pack_rotary_fwd / pack_rotary_bwd — rotary positions of the queries and
+ * keys that masked_attn_fwd takes, with the RMS norm that precedes them.
+ *
+ * Each head vector x [D] is optionally normalised, z = x r w with
+ * r = 1 / sqrt(mean x^2 + eps) over the head (PVL_NORM_HEAD) or over all
+ * heads of the token (PVL_NORM_TOKEN; queries and keys apart), and its first
+ * R features are rotated: pair i (i < R / 2) is the features (i, i + R / 2)
+ * in the half layout and (2 i, 2 i + 1) in the interleaved one, its angle is
+ * positions[b, l, axis of i] times the pair's frequency, and
+ *   (a, b) -> gain (a cos - b sin, a sin + b cos).
+ * Features from R on pass through (normalised, not scaled by gain).
+ *
+ * turns: dev uint64 [R / 2], the pair's frequency in turns (cycles) per
+ *   position, as a fraction of 2^64: the angle of an int32 position is then
+ *   exact to 2^-32 turns however far it lies.  Pairs before section_1 take
+ *   axis 0, before section_2 axis 1, the rest axis 2 (set both to R / 2 for
+ *   one axis, section_2 to R / 2 for two).
+ * positions: dev int32 [B, L, axes]; any value, negative ones included.
+ * q_weight, k_weight: dev fp32, [D] for the norm per head and [H * D],
+ *   [Hk * D] for the norm per token; null: no weight.
+ * pvl_heads: bf16 [B, L, heads, D] with D contiguous and any other strides
+ *   (in elements), so that slices of a fused projection need no copy.  k may
+ *   be absent (null pointer with Hk = 0).  An output may be the input of the
+ *   same pass (pointer and strides equal); any other overlap is undefined.
+ * Backward: dq_out, dk_out are the gradients of the outputs; q, k (the
+ *   forward's inputs) and the weights are read only with a norm; dq, dk and,
+ *   where the weights are given, dq_weight, dk_weight are written.  The
+ *   weight gradients are added in a fixed order (repeated calls on one GPU
+ *   give the same bits).  ws: pack_rotary_bwd_ws_bytes of the same
+ *   description (0 without weights), 16-byte aligned, one call at a time.
+ * Limits (UNSUPPORTED): D and R even, D at most 256, H + Hk at most
+ *   PVL_MAX_ROTARY_HEADS, and a token whose (H + Hk) D features the norm per
+ *   token cannot hold in a block (12,288 always fit).  Tensors whose D, R,
+ *   strides and addresses allow 16-byte (else 8-byte) vectors run fastest.
+ * Errors: INVALID_ARG for null pointers,
+ *   sizes < 1, inconsistent sections, unknown layout or norm, a short
+ *   workspace; CUDA for launch failures.
+ * ---------------------------------------------------------------------- */
+typedef enum pvl_norm {
+  PVL_NORM_NONE = 0,
+  PVL_NORM_LAYER = 1,
+  PVL_NORM_RMS = 2,
+  PVL_NORM_HEAD = 3, /* RMS over each head */
+  PVL_NORM_TOKEN = 4 /* RMS over all heads of the token */
+} pvl_norm;
+
+typedef enum pvl_rotary_layout { PVL_ROTARY_HALF = 0, PVL_ROTARY_INTERLEAVED = 1 } pvl_rotary_layout;
+
+#define PVL_MAX_ROTARY_HEADS 4096
+
+typedef struct pvl_rotary {
+  int32_t B, L, H, Hk, D;
+  int32_t R, layout, axes, section_1, section_2;
+  float gain;
+  int32_t norm; /* PVL_NORM_NONE, _HEAD or _TOKEN */
+  float eps;
+  const uint64_t* turns;
+  const int32_t* positions;
+  const float* q_weight;
+  const float* k_weight;
+} pvl_rotary;
+
+typedef struct pvl_heads {
+  void* data;
+  int64_t stride_b, stride_l, stride_h;
+} pvl_heads;
+
+PVL_API pvl_status pack_rotary_fwd(const pvl_rotary* how, const pvl_heads* q, const pvl_heads* k,
+                                   const pvl_heads* q_out, const pvl_heads* k_out, pvl_stream_t stream);
+
+PVL_API size_t pack_rotary_bwd_ws_bytes(const pvl_rotary* how);
+
+PVL_API pvl_status pack_rotary_bwd(const pvl_rotary* how, const pvl_heads* dq_out, const pvl_heads* dk_out,
+                                   const pvl_heads* q, const pvl_heads* k, const pvl_heads* dq, const pvl_heads* dk,
+                                   float* dq_weight, float* dk_weight, void* ws, size_t ws_bytes,
+                                   pvl_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * adaln_residual_fwd / adaln_residual_bwd — the gated residual after a block
+ * and the modulated norm before the next one, fused; with a post norm, also
+ * the norm of the block's output.  Per token with modulation row s:
+ *   u = h, or post(h) post_weight,
+ *   x_out = alpha x + gate_s u,
+ *   y = (norm(x_out) weight + bias)(1 + scale_s) + shift_s,
+ * post, norm: layer norm, (v - mean) / sqrt(var + eps), or RMS norm,
+ * v / sqrt(mean v^2 + eps), over the D features.  Every factor that is null
+ * drops out.  h null: no branch (y is the modulated norm of x and x_out is
+ * not written; gate, post norm and alpha != 1 are refused).
+ *
+ * x, x_out: dev [B, N, D], bf16 or fp32 (stream_dtype); h, y: dev bf16
+ * [B, N, D]; gate, shift, scale: dev fp32 [S, D]; weight, bias, post_weight:
+ * dev fp32 [D].  y and the statistics come from x_out before its rounding.
+ * mod_id: dev int32 [B, N], the modulation row of each token, e.g. the
+ *   seq_ids of pack_build_seq_ids (one modulation per packed episode) or a
+ *   frame index; a negative id is padding: x_out = x and y = 0, whatever h
+ *   holds.  Null: row b for batch row b (S = B).  An id of S or more is
+ *   recorded in the device error record (PVL_ERR_INVALID_ARG from
+ *   pvl_device_error) and its token handled as padding; without any table
+ *   every non-negative id is a valid token.
+ *
+ * Backward, from dx_out (null: zeros; type of x_out), dy, the forward's
+ * x_out and h (needed with a gate or a post norm): dx = d loss / d x (type of
+ * x_out), dh (bf16; with has_branch), and one gradient for each table and
+ * vector that is given.  Padding: dx = dx_out, dh = 0, no part in the sums.
+ *   The ids must not decrease along the rows (padding aside), as those of
+ * pack_build_seq_ids do not: the sums of a run of equal ids are kept apart
+ * by (CTA, id), added in a fixed order without atomics (repeated calls on
+ * one GPU give the same bits).  Ids out of order that would mix two rows'
+ * sums are recorded in the device error record and make every table and
+ * vector gradient NaN.
+ * ws: adaln_residual_bwd_ws_bytes(B, N, D, S) bytes (S = 1 without tables;
+ *   null without tables and vectors), one call at a time.
+ * D a multiple of 8, at most 8192; S at most PVL_MAX_MOD_ROWS.  All pointers
+ * 16-byte aligned (mod_id 4-byte).  Errors: as adaln_fwd.
+ * ---------------------------------------------------------------------- */
+#define PVL_MAX_MOD_ROWS 65535
+
+typedef enum pvl_dtype { PVL_BF16 = 0, PVL_F32 = 1 } pvl_dtype;
+
+typedef struct pvl_residual {
+  int32_t B, N, D, S;
+  int32_t stream_dtype; /* pvl_dtype of x, x_out and their gradients */
+  int32_t norm;         /* PVL_NORM_LAYER or _RMS */
+  int32_t post_norm;    /* PVL_NORM_NONE, _LAYER or _RMS */
+  float alpha, eps;
+  const float *gate, *shift, *scale;
+  const float *weight, *bias, *post_weight;
+  const int32_t* mod_id;
+} pvl_residual;
+
+typedef struct pvl_residual_grads {
+  float *dgate, *dshift, *dscale;
+  float *dweight, *dbias, *dpost_weight;
+} pvl_residual_grads;
+
+PVL_API pvl_status adaln_residual_fwd(const pvl_residual* how, const void* x, const pvl_bf16* h, void* x_out,
+                                      pvl_bf16* y, pvl_stream_t stream);
+
+PVL_API size_t adaln_residual_bwd_ws_bytes(int B, int N, int D, int S);
+
+PVL_API pvl_status adaln_residual_bwd(const pvl_residual* how, const void* dx_out, const pvl_bf16* dy,
+                                      const void* x_out, const pvl_bf16* h, int has_branch, void* dx, pvl_bf16* dh,
+                                      const pvl_residual_grads* grads, void* ws, size_t ws_bytes,
+                                      pvl_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * masked_mse_loss / masked_mse_loss_bwd — the squared-error loss averaged
  * over valid frames only, and its gradient ("lingbot_va_packing" §2.1,
  * compute_loss: frame_valid = f < valid_frames[b], latent and action
@@ -349,7 +512,8 @@ PVL_API pvl_status masked_mse_loss_bwd(const pvl_bf16* pred, const pvl_bf16* tar
  * Device error record.  Synchronises `stream`, reads and clears the current
  * device's error record.  Returns PVL_OK, PVL_ERR_TIMEOUT (a bounded wait ran
  * out; the kernel released its resources and returned), PVL_ERR_INVALID_ARG
- * (tile map of another shape) or PVL_ERR_CUDA (the synchronisation failed).
+ * (tile map of another shape; modulation ids of adaln_residual_* outside the
+ * table or, backward, out of order) or PVL_ERR_CUDA (the synchronisation failed).
  * info (optional, host int32[4]): code, where, block, thread of the first
  * failure.
  * ---------------------------------------------------------------------- */

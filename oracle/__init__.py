@@ -31,6 +31,11 @@ What it computes, written from the LingBot-VA packing reports:
   dimension followed by the AdaLN modulation y = xh (1 + scale) + shift, and
   its gradient with the modulation gradients summed over the sequence
   ("AdaptiveLoad" §2.B, the fused LayerNorm-Modulate kernel).
+- ``rotary.positions`` / ``rotary.rotary_fwd`` / ``rotary.rotary_bwd``:
+  positions of tokens inside their packed segments, and rotary positions of
+  queries and keys after an optional RMS norm, with the gradient.
+- ``residual.residual_fwd`` / ``residual.residual_bwd``: the gated residual
+  of a block with the norms on both sides, one modulation row per token.
 
 Every function is pinned by tests under ``tests/`` against brute force,
 finite differences, closed forms, library routines (torch fp64 autograd and
@@ -40,5 +45,7 @@ scaled_dot_product_attention) and the pages' packed == separate invariant.
 from .adaln import adaln_bwd, adaln_fwd  # noqa: F401
 from .attention import attention_bwd, attention_fwd, effective_pairs  # noqa: F401
 from .loss import frame_valid_tokens, masked_mse, masked_mse_grad, valid_from_seq_id  # noqa: F401
+from .residual import residual_bwd, residual_fwd  # noqa: F401
+from .rotary import positions, rotary_angles, rotary_bwd, rotary_fwd  # noqa: F401
 from .seq_ids import build_seq_ids  # noqa: F401
 from .tile_map import EMPTY, FULL, PARTIAL, build_tile_map, tile_stats  # noqa: F401

@@ -11,11 +11,16 @@ from .api import (  # noqa: F401
     EMPTY,
     FULL,
     PARTIAL,
+    AdalnResidualGrads,
     PvlError,
+    RotaryPlan,
     TileMap,
     adaln_bwd,
     adaln_bwd_ws_bytes,
     adaln_fwd,
+    adaln_residual_bwd,
+    adaln_residual_bwd_ws_bytes,
+    adaln_residual_fwd,
     device_error,
     masked_attn_bwd,
     masked_attn_bwd_no_alloc,
@@ -25,11 +30,15 @@ from .api import (  # noqa: F401
     masked_mse_loss_bwd,
     masked_mse_ws_bytes,
     mark_next_bwd_main,
+    pack_build_positions,
     pack_build_seq_ids,
+    pack_rotary_bwd,
+    pack_rotary_fwd,
+    rotary_plan,
     set_attn_wait_timeout_ns,
     tile_map_build,
     tile_map_ws_bytes,
     version,
 )
 from . import adaptive_load  # noqa: F401  (host-side dual-constraint bucketing)
-from .autograd import adaln_modulate, frame_valid_mse, packed_attention  # noqa: F401
+from .autograd import adaln_modulate, frame_valid_mse, gated_residual, packed_attention, packed_rotary  # noqa: F401

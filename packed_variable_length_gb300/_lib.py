@@ -16,6 +16,35 @@ _c_size = ctypes.c_size_t
 _c_float = ctypes.c_float
 _p = ctypes.c_void_p
 
+_i32 = ctypes.c_int32
+
+
+class Rotary(ctypes.Structure):
+    """pvl_rotary"""
+    _fields_ = [("B", _i32), ("L", _i32), ("H", _i32), ("Hk", _i32), ("D", _i32), ("R", _i32), ("layout", _i32),
+                ("axes", _i32), ("section_1", _i32), ("section_2", _i32), ("gain", _c_float), ("norm", _i32),
+                ("eps", _c_float), ("turns", _p), ("positions", _p), ("q_weight", _p), ("k_weight", _p)]
+
+
+class Heads(ctypes.Structure):
+    """pvl_heads"""
+    _fields_ = [("data", _p), ("stride_b", ctypes.c_int64), ("stride_l", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64)]
+
+
+class Residual(ctypes.Structure):
+    """pvl_residual"""
+    _fields_ = [("B", _i32), ("N", _i32), ("D", _i32), ("S", _i32), ("stream_dtype", _i32), ("norm", _i32),
+                ("post_norm", _i32), ("alpha", _c_float), ("eps", _c_float), ("gate", _p), ("shift", _p),
+                ("scale", _p), ("weight", _p), ("bias", _p), ("post_weight", _p), ("mod_id", _p)]
+
+
+class ResidualGrads(ctypes.Structure):
+    """pvl_residual_grads"""
+    _fields_ = [("dgate", _p), ("dshift", _p), ("dscale", _p), ("dweight", _p), ("dbias", _p),
+                ("dpost_weight", _p)]
+
+
 # name -> (restype, argtypes); mirrors include/pvl.h
 SIGNATURES = {
     "pack_build_seq_ids": (_c_int, [_p, _p, _c_int, _c_int, _c_int, _c_int, _p, _p]),
@@ -39,6 +68,13 @@ SIGNATURES = {
     "adaln_fwd": (_c_int, [_p, _p, _p, _c_int, _c_int, _c_int, _c_float, _p, _p, _p, _p]),
     "adaln_bwd_ws_bytes": (_c_size, [_c_int, _c_int, _c_int]),
     "adaln_bwd": (_c_int, [_p, _p, _p, _c_int, _c_int, _c_int, _c_float, _p, _p, _p, _p, _c_size, _p]),
+    "pack_build_positions": (_c_int, [_p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _p, _p]),
+    "pack_rotary_fwd": (_c_int, [_p, _p, _p, _p, _p, _p]),
+    "pack_rotary_bwd_ws_bytes": (_c_size, [_p]),
+    "pack_rotary_bwd": (_c_int, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _c_size, _p]),
+    "adaln_residual_fwd": (_c_int, [_p, _p, _p, _p, _p, _p]),
+    "adaln_residual_bwd_ws_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int]),
+    "adaln_residual_bwd": (_c_int, [_p, _p, _p, _p, _p, _c_int, _p, _p, _p, _p, _c_size, _p]),
     "masked_mse_ws_bytes": (_c_size, [_c_int, _c_int, _c_int]),
     "masked_mse_loss": (_c_int, [_p, _p, _p, _c_int, _c_int, _c_int, _p, _p, _c_float, _p, _c_size, _p]),
     "masked_mse_loss_bwd": (_c_int, [_p, _p, _p, _c_int, _c_int, _c_int, _p, _p, _p, _c_size, _p]),

@@ -8,9 +8,12 @@ library's CUDA kernels; nothing here computes attention, seq_ids or tile maps.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from dataclasses import dataclass
+from decimal import Decimal, localcontext
+from typing import NamedTuple
 
 import numpy as np
 import torch
@@ -58,6 +61,27 @@ def _need_cuda(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> No
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _need_same_device(device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+@contextlib.contextmanager
+def _launch(device, stream):
+    """Makes the device current and, with a stream given, that stream, so that
+    what is allocated inside belongs to the stream the kernels run on; yields
+    the stream's handle."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream().cuda_stream
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(_stream(stream))
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
 # ------------------------------------------------------------------ seq_ids
 def pack_build_seq_ids(seg_frames, seg_valid, tokens_per_frame: int, L: int, out: torch.Tensor | None = None,
                        device=None, stream=None) -> torch.Tensor:
@@ -73,6 +97,28 @@ def pack_build_seq_ids(seg_frames, seg_valid, tokens_per_frame: int, L: int, out
     with torch.cuda.device(out.device):
         _check(_lib.load().pack_build_seq_ids(frames.ctypes.data, valid.ctypes.data, B, K, int(tokens_per_frame),
                                               int(L), out.data_ptr(), _stream(stream)))
+    return out
+
+
+def pack_build_positions(seg_frames, tokens_per_frame: int, L: int, axes: int = 1, row_width: int | None = None,
+                         out: torch.Tensor | None = None, device=None, stream=None) -> torch.Tensor:
+    """int32 [B, L, axes] position of each token inside its packed segment,
+    from the host [B, K] frame table: its offset (axes=1), its frame and its
+    token of the frame (2), or its frame, row and column with row_width tokens
+    a row (3).  Positions restart in every segment; the tail gets zeros."""
+    frames = np.ascontiguousarray(np.asarray(seg_frames, dtype=np.int32))
+    if frames.ndim != 2:
+        raise ValueError("seg_frames must be [B, K]")
+    if axes == 3 and row_width is None:
+        raise ValueError("three axes need row_width")
+    B, K = frames.shape
+    device = torch.device(device or "cuda") if out is None else out.device
+    with _launch(device, stream) as handle:
+        if out is None:
+            out = torch.empty((B, int(L), int(axes)), dtype=torch.int32, device=device)
+        _need_cuda(out, "out", torch.int32, (B, int(L), int(axes)))
+        _check(_lib.load().pack_build_positions(frames.ctypes.data, B, K, int(tokens_per_frame), int(axes),
+                                                int(row_width or 1), int(L), out.data_ptr(), handle))
     return out
 
 
@@ -344,6 +390,302 @@ def adaln_bwd(x, scale, dy, eps: float = 1e-6, dx=None, dshift=None, dscale=None
         _check(lib.adaln_bwd(x.data_ptr(), scale.data_ptr(), dy.data_ptr(), B, N, D, float(eps), dx.data_ptr(),
                              dshift.data_ptr(), dscale.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
     return dx, dshift, dscale
+
+
+# ------------------------------------------------------- rotary positions
+_NORMS = {None: 0, "layer": 1, "rms": 2, "head": 3, "token": 4}
+_TWO_PI = Decimal("6.283185307179586476925286766559005768394338798750211641949889")
+
+
+@dataclass
+class RotaryPlan:
+    """Frequencies of rotary positions, made once by rotary_plan and shared by
+    all calls: turns is an int64 [rotary_dim / 2] device tensor, each pair's
+    frequency in turns per position as a fraction of 2^64; sections counts the
+    pairs of each position axis."""
+    turns: torch.Tensor
+    rotary_dim: int
+    layout: str
+    sections: tuple
+    gain: float
+
+
+def rotary_plan(rotary_dim: int, base: float = 10000.0, layout: str = "half", sections=None,
+                scaling: str | None = None, factor: float = 1.0, length: int | None = None, slow: float = 1.0,
+                fast: float = 32.0, gain: float | None = None, device=None) -> RotaryPlan:
+    """Plan of rotary positions over the first rotary_dim features of a head.
+
+    layout: "half" pairs feature i with i + rotary_dim / 2, "interleaved" 2 i
+    with 2 i + 1.  sections: pairs of each position axis (1 to 3 of them,
+    summing to rotary_dim / 2; one axis by default); pair j of an axis of n
+    pairs has frequency base^(-j / n) in radians per position.
+
+    scaling, for contexts factor times longer than trained: "linear" divides
+    every frequency by factor; "ntk" raises base to base factor^(n / (n - 1)),
+    which leaves the fastest pair and divides the slowest by factor; "parts"
+    keeps the pairs that turn at least `fast` times within the trained
+    `length`, divides by factor those that turn at most `slow` times, blends
+    between, and multiplies the rotated features by 0.1 ln(factor) + 1.  gain
+    overrides that multiplier (1 otherwise)."""
+    R = int(rotary_dim)
+    if R < 2 or R % 2:
+        raise ValueError("rotary_dim must be even and at least 2")
+    if layout not in ("half", "interleaved"):
+        raise ValueError(f"layout must be 'half' or 'interleaved', got {layout!r}")
+    sections = (R // 2,) if sections is None else tuple(int(n) for n in sections)
+    if not 1 <= len(sections) <= 3 or min(sections) < 0 or sum(sections) != R // 2:
+        raise ValueError(f"sections must be 1 to 3 counts that sum to {R // 2}, got {sections}")
+    if scaling not in (None, "none", "linear", "ntk", "parts"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if not (math.isfinite(base) and base > 0.0) or not (math.isfinite(factor) and factor > 0.0):
+        raise ValueError("base and factor must be positive and finite")
+    if scaling == "parts" and (length is None or length < 1 or not fast > slow >= 0.0):
+        raise ValueError("scaling 'parts' needs the trained length and fast > slow >= 0")
+    turns = []
+    with localcontext() as ctx:
+        ctx.prec = 50
+        s = Decimal(factor)
+        for n in sections:
+            b = Decimal(base)
+            if scaling == "ntk" and n > 1:
+                b *= (s.ln() * n / (n - 1)).exp()
+            for j in range(n):
+                t = (-b.ln() * j / n).exp() / _TWO_PI
+                if scaling == "linear":
+                    t /= s
+                elif scaling == "parts":
+                    keep = (length * t - Decimal(slow)) / (Decimal(fast) - Decimal(slow))
+                    keep = min(max(keep, Decimal(0)), Decimal(1))
+                    t = t * keep + t / s * (1 - keep)
+                whole = int((t * (1 << 64)).to_integral_value()) % (1 << 64)
+                turns.append(whole - (1 << 64) if whole >> 63 else whole)
+    if gain is None:
+        gain = 0.1 * math.log(factor) + 1.0 if scaling == "parts" and factor > 1.0 else 1.0
+    table = torch.tensor(turns, dtype=torch.int64).to(device or "cuda")
+    return RotaryPlan(table, R, layout, sections, float(gain))
+
+
+def _heads_view(t: torch.Tensor, name: str, shape) -> _lib.Heads:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    sb, sl, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    B, L, H, _ = t.shape  # the stride of a single entry means nothing
+    return _lib.Heads(t.data_ptr(), sb if B > 1 else 0, sl if L > 1 else 0, sh if H > 1 else 0)
+
+
+def _rotary(like_q, like_k, positions, plan: RotaryPlan, norm, q_weight, k_weight, eps):
+    """Checked description of a rotary call."""
+    if like_q.dim() != 4 or (like_k is not None and like_k.dim() != 4):
+        raise ValueError("q and k must be [B, L, heads, D]")
+    B, L, H, D = like_q.shape
+    Hk = 0 if like_k is None else int(like_k.shape[2])
+    if like_k is not None and (tuple(like_k.shape) != (B, L, Hk, D) or Hk < 1):
+        raise ValueError(f"k must be [{B}, {L}, Hk, {D}], got {tuple(like_k.shape)}")
+    if norm not in (None, "head", "token"):
+        raise ValueError(f"norm must be None, 'head' or 'token', got {norm!r}")
+    axes = len(plan.sections)
+    if axes == 1 and positions.dim() == 2:
+        positions = positions.unsqueeze(2)
+    _need_cuda(positions, "positions", torch.int32, (B, L, axes))
+    for name, w, n in (("q_weight", q_weight, H), ("k_weight", k_weight, Hk)):
+        if w is None:
+            continue
+        if norm is None or (n == 0):
+            raise ValueError(f"{name} needs a norm and its heads")
+        _need_cuda(w, name, torch.float32)
+        if w.numel() != (n * D if norm == "token" else D):
+            raise ValueError(f"{name} must hold {n * D if norm == 'token' else D} values, got {w.numel()}")
+    _need_same_device(like_q.device, k=like_k, positions=positions, plan=plan.turns, q_weight=q_weight,
+                      k_weight=k_weight)
+    s = plan.sections
+    s1 = s[0]
+    s2 = s1 + (s[1] if axes > 1 else 0)
+    return _lib.Rotary(B, L, H, Hk, D, plan.rotary_dim, 0 if plan.layout == "half" else 1, axes, s1, s2, plan.gain,
+                       _NORMS[norm], float(eps), plan.turns.data_ptr(), positions.data_ptr(), _ptr(q_weight),
+                       _ptr(k_weight)), (B, L, H, D), (B, L, Hk, D)
+
+
+def pack_rotary_fwd(q, k, positions, plan: RotaryPlan, norm: str | None = None, q_weight=None, k_weight=None,
+                    eps: float = 1e-6, q_out=None, k_out=None, stream=None):
+    """(q_out, k_out): the rotary positions of bf16 q [B, L, H, D] and k
+    [B, L, Hk, D] (or None) at int32 positions [B, L, axes] ([B, L] for one
+    axis), after the RMS norm of each head (norm="head", weights fp32 [D]) or
+    of all heads of the token (norm="token", weights fp32 [H * D], [Hk * D]);
+    a weight of None is 1.  q and k may be slices with any strides but that of
+    D; the outputs are contiguous unless given, and may be q and k."""
+    how, qs, ks = _rotary(q, k, positions, plan, norm, q_weight, k_weight, eps)
+    _need_same_device(q.device, q_out=q_out, k_out=k_out)
+    with _launch(q.device, stream) as handle:
+        if q_out is None:
+            q_out = torch.empty(qs, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(ks, dtype=k.dtype, device=k.device)
+        views = [_heads_view(q, "q", qs), None if k is None else _heads_view(k, "k", ks),
+                 _heads_view(q_out, "q_out", qs), None if k is None else _heads_view(k_out, "k_out", ks)]
+        _check(_lib.load().pack_rotary_fwd(ctypes.byref(how), *(None if v is None else ctypes.byref(v) for v in views),
+                                           handle))
+    return q_out, k_out
+
+
+def pack_rotary_bwd(dq_out, dk_out, positions, plan: RotaryPlan, norm: str | None = None, q=None, k=None,
+                    q_weight=None, k_weight=None, eps: float = 1e-6, dq=None, dk=None, stream=None):
+    """(dq, dk, dq_weight, dk_weight) of pack_rotary_fwd from the gradients of
+    its outputs; q, k (its inputs) are needed with a norm.  dk is None without
+    keys, a weight's gradient (fp32) is None without that weight."""
+    how, qs, ks = _rotary(dq_out, dk_out, positions, plan, norm, q_weight, k_weight, eps)
+    keys = dk_out is not None
+    if norm is not None and (q is None or (keys and k is None)):
+        raise ValueError("the backward of a norm needs q and k")
+    if norm is None:
+        q = k = None
+    _need_same_device(dq_out.device, q=q, k=k, dq=dq, dk=dk)
+    lib = _lib.load()
+    with _launch(dq_out.device, stream) as handle:
+        if dq is None:
+            dq = torch.empty(qs, dtype=dq_out.dtype, device=dq_out.device)
+        if keys and dk is None:
+            dk = torch.empty(ks, dtype=dk_out.dtype, device=dk_out.device)
+        dq_weight = None if q_weight is None else torch.empty_like(q_weight)
+        dk_weight = None if k_weight is None else torch.empty_like(k_weight)
+        nbytes = int(lib.pack_rotary_bwd_ws_bytes(ctypes.byref(how)))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dq_out.device) if nbytes else None
+        views = [_heads_view(dq_out, "dq_out", qs), _heads_view(dk_out, "dk_out", ks) if keys else None,
+                 None if q is None else _heads_view(q, "q", qs),
+                 _heads_view(k, "k", ks) if keys and k is not None else None,
+                 _heads_view(dq, "dq", qs), _heads_view(dk, "dk", ks) if keys else None]
+        _check(lib.pack_rotary_bwd(ctypes.byref(how), *(None if v is None else ctypes.byref(v) for v in views),
+                                   _ptr(dq_weight), _ptr(dk_weight), _ptr(ws), nbytes, handle))
+    return dq, (dk if keys else None), dq_weight, dk_weight
+
+
+# ------------------------------------------------- gated residual and norms
+class AdalnResidualGrads(NamedTuple):
+    """Gradients of adaln_residual_fwd; None for what the call did not have."""
+    dx: torch.Tensor
+    dh: torch.Tensor | None
+    dgate: torch.Tensor | None
+    dshift: torch.Tensor | None
+    dscale: torch.Tensor | None
+    dweight: torch.Tensor | None
+    dbias: torch.Tensor | None
+    dpost_weight: torch.Tensor | None
+
+
+def _residual(x, gate, shift, scale, mod_id, weight, bias, post_weight, norm, post_norm, alpha, eps):
+    """Checked description of a gated residual call; returns (description, modulation rows)."""
+    if x.dim() != 3:
+        raise ValueError("x must be [B, N, D]")
+    B, N, D = x.shape
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"x must be {torch.bfloat16} or {torch.float32}, got {x.dtype}")
+    _need_cuda(x, "x", x.dtype, (B, N, D))
+    if norm not in ("layer", "rms"):
+        raise ValueError(f"norm must be 'layer' or 'rms', got {norm!r}")
+    if post_norm not in (None, "layer", "rms"):
+        raise ValueError(f"post_norm must be None, 'layer' or 'rms', got {post_norm!r}")
+    S = None
+    for name, t in (("gate", gate), ("shift", shift), ("scale", scale)):
+        if t is None:
+            continue
+        if t.dim() != 2:
+            raise ValueError(f"{name} must be [S, D]")
+        S = int(t.shape[0]) if S is None else S
+        _need_cuda(t, name, torch.float32, (S, D))
+    if mod_id is not None:
+        _need_cuda(mod_id, "mod_id", torch.int32, (B, N))
+    elif S is not None and S != B:
+        raise ValueError(f"without mod_id the modulation tables must have B = {B} rows, got {S}")
+    for name, t in (("weight", weight), ("bias", bias), ("post_weight", post_weight)):
+        if t is not None:
+            _need_cuda(t, name, torch.float32, (D,))
+    _need_same_device(x.device, gate=gate, shift=shift, scale=scale, mod_id=mod_id, weight=weight, bias=bias,
+                      post_weight=post_weight)
+    return _lib.Residual(B, N, D, S or 1, 1 if x.dtype == torch.float32 else 0, _NORMS[norm], _NORMS[post_norm],
+                         float(alpha), float(eps), _ptr(gate), _ptr(shift), _ptr(scale), _ptr(weight), _ptr(bias),
+                         _ptr(post_weight), _ptr(mod_id)), S or 1
+
+
+def adaln_residual_fwd(x, h=None, gate=None, shift=None, scale=None, *, mod_id=None, weight=None, bias=None,
+                       post_weight=None, norm: str = "layer", post_norm: str | None = None, alpha: float = 1.0,
+                       eps: float = 1e-6, x_out=None, y=None, stream=None):
+    """(x_out, y): x_out = alpha x + gate_s u with u = h, or post_norm(h)
+    post_weight, and y = (norm(x_out) weight + bias)(1 + scale_s) + shift_s, the
+    gated residual after a block and the modulated norm before the next.
+
+    x [B, N, D] bf16 or fp32 (x_out alike), h and y bf16, gate / shift / scale
+    fp32 [S, D], weight / bias / post_weight fp32 [D]; what is None drops out.
+    mod_id int32 [B, N] is each token's row s (the seq_ids of
+    pack_build_seq_ids: one modulation per packed episode), negative for
+    padding: x_out = x, y = 0.  Without it row b serves batch row b (S = B).
+    Without h, x_out is x itself and y its modulated norm."""
+    how, _ = _residual(x, gate, shift, scale, mod_id, weight, bias, post_weight, norm, post_norm, alpha, eps)
+    if h is not None:
+        _need_cuda(h, "h", torch.bfloat16, x.shape)
+    _need_same_device(x.device, h=h, x_out=x_out, y=y)
+    with _launch(x.device, stream) as handle:
+        if h is None:
+            x_out = x
+        elif x_out is None:
+            x_out = torch.empty_like(x)
+        if y is None:
+            y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        _need_cuda(x_out, "x_out", x.dtype, x.shape)
+        _need_cuda(y, "y", torch.bfloat16, x.shape)
+        _check(_lib.load().adaln_residual_fwd(ctypes.byref(how), x.data_ptr(), _ptr(h), x_out.data_ptr(), y.data_ptr(),
+                                              handle))
+    return x_out, y
+
+
+def adaln_residual_bwd_ws_bytes(B: int, N: int, D: int, S: int) -> int:
+    return int(_lib.load().adaln_residual_bwd_ws_bytes(B, N, D, S))
+
+
+def adaln_residual_bwd(dx_out, dy, x_out, h=None, gate=None, shift=None, scale=None, *, mod_id=None, weight=None,
+                       bias=None, post_weight=None, norm: str = "layer", post_norm: str | None = None,
+                       alpha: float = 1.0, eps: float = 1e-6, branch: bool | None = None, dx=None, dh=None, ws=None,
+                       stream=None) -> AdalnResidualGrads:
+    """Gradients of adaln_residual_fwd from dx_out (like x_out, or None for
+    zero), dy (bf16) and the forward's x_out, h, tables and vectors (shift's
+    and bias's values are not used, only whether they are there).  h is needed
+    with a gate or a post norm; branch=True asks for dh without it.  The ids of
+    mod_id must not decrease along the rows, padding aside; device_error
+    reports a call that broke this, whose table gradients are NaN."""
+    how, S = _residual(x_out, gate, shift, scale, mod_id, weight, bias, post_weight, norm, post_norm, alpha, eps)
+    B, N, D = x_out.shape
+    branch = h is not None if branch is None else bool(branch)
+    if h is not None:
+        _need_cuda(h, "h", torch.bfloat16, x_out.shape)
+    _need_cuda(dy, "dy", torch.bfloat16, x_out.shape)
+    if dx_out is not None:
+        _need_cuda(dx_out, "dx_out", x_out.dtype, x_out.shape)
+    _need_same_device(x_out.device, h=h, dy=dy, dx_out=dx_out, dx=dx, dh=dh, ws=ws)
+    lib = _lib.load()
+    with _launch(x_out.device, stream) as handle:
+        if dx is None:
+            dx = torch.empty_like(x_out)
+        if branch and dh is None:
+            dh = torch.empty(x_out.shape, dtype=torch.bfloat16, device=x_out.device)
+        _need_cuda(dx, "dx", x_out.dtype, x_out.shape)
+        if branch:
+            _need_cuda(dh, "dh", torch.bfloat16, x_out.shape)
+        params = (gate, shift, scale, weight, bias, post_weight)
+        grads = [None if t is None else torch.empty_like(t) for t in params]
+        nbytes = 0
+        if any(t is not None for t in params):
+            nbytes = int(lib.adaln_residual_bwd_ws_bytes(B, N, D, S))
+            if ws is None:
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=x_out.device)
+        out = _lib.ResidualGrads(*(_ptr(t) for t in grads))
+        _check(lib.adaln_residual_bwd(ctypes.byref(how), _ptr(dx_out), dy.data_ptr(), x_out.data_ptr(), _ptr(h),
+                                      int(branch), dx.data_ptr(), _ptr(dh) if branch else None, ctypes.byref(out),
+                                      _ptr(ws), 0 if ws is None else ws.numel(), handle))
+    return AdalnResidualGrads(dx, dh if branch else None, *grads)
 
 
 # ------------------------------------------------------------ masked loss

@@ -60,6 +60,70 @@ def adaln_modulate(x, shift, scale, eps: float = 1e-6):
     return _AdaLNModulate.apply(x, shift, scale, eps)
 
 
+class _PackedRotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, positions, plan, norm, q_weight, k_weight, eps):
+        q_out, k_out = api.pack_rotary_fwd(q, k, positions, plan, norm, q_weight, k_weight, eps)
+        normed = norm is not None
+        ctx.save_for_backward(q if normed else None, k if normed else None, positions, q_weight, k_weight)
+        ctx.how = (plan, norm, eps)
+        return q_out if k is None else (q_out, k_out)
+
+    @staticmethod
+    def backward(ctx, dq_out, dk_out=None):
+        q, k, positions, q_weight, k_weight = ctx.saved_tensors
+        plan, norm, eps = ctx.how
+        dq_out, dk_out = (t if t is None or t.stride(3) == 1 else t.contiguous() for t in (dq_out, dk_out))
+        dq, dk, dqw, dkw = api.pack_rotary_bwd(dq_out, dk_out, positions, plan, norm, q, k, q_weight, k_weight, eps)
+        return dq, dk, None, None, None, dqw, dkw, None
+
+
+def packed_rotary(q, k, positions, plan, norm=None, q_weight=None, k_weight=None, eps: float = 1e-6):
+    """Rotary positions of bf16 q [B, L, H, D] and k [B, L, Hk, D] (k may be
+    None: the result is then the rotated q alone), with the RMS norm before
+    them, differentiable in q, k and the norm weights (see
+    api.pack_rotary_fwd); the outputs are what packed_attention takes."""
+    return _PackedRotary.apply(q, k, positions, plan, norm, q_weight, k_weight, eps)
+
+
+class _GatedResidual(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, h, gate, shift, scale, weight, bias, post_weight, mod_id, how):
+        x_out, y = api.adaln_residual_fwd(x, h, gate, shift, scale, mod_id=mod_id, weight=weight, bias=bias,
+                                          post_weight=post_weight, **how)
+        # without a gate or a post norm no gradient depends on h
+        kept = h if h is not None and (gate is not None or how["post_norm"] is not None) else None
+        ctx.save_for_backward(x_out, kept, gate, shift, scale, weight, bias, post_weight, mod_id)
+        ctx.how = how
+        ctx.branch = h is not None
+        ctx.set_materialize_grads(False)
+        return y if h is None else (x_out, y)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        x_out, h, gate, shift, scale, weight, bias, post_weight, mod_id = ctx.saved_tensors
+        dx_out, dy = grads if ctx.branch else (None, grads[0])
+        if dy is None:
+            dy = torch.zeros(x_out.shape, dtype=torch.bfloat16, device=x_out.device)
+        if dx_out is not None:
+            dx_out = dx_out.contiguous()
+        g = api.adaln_residual_bwd(dx_out, dy.contiguous(), x_out, h, gate, shift, scale, mod_id=mod_id, weight=weight,
+                                   bias=bias, post_weight=post_weight, branch=ctx.branch, **ctx.how)
+        return (*g, None, None)
+
+
+def gated_residual(x, h=None, gate=None, shift=None, scale=None, *, mod_id=None, weight=None, bias=None,
+                   post_weight=None, norm: str = "layer", post_norm: str | None = None, alpha: float = 1.0,
+                   eps: float = 1e-6):
+    """(x_out, y) of api.adaln_residual_fwd, differentiable in every floating
+    input: the gated residual after a block and the modulated norm before the
+    next, with one modulation row per packed episode (mod_id).  Without h,
+    x_out is x itself."""
+    how = dict(norm=norm, post_norm=post_norm, alpha=alpha, eps=eps)
+    out = _GatedResidual.apply(x, h, gate, shift, scale, weight, bias, post_weight, mod_id, how)
+    return (x, out) if h is None else out
+
+
 class _MaskedMSE(torch.autograd.Function):
     @staticmethod
     def forward(ctx, pred, target, seq_id):

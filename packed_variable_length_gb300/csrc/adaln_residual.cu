@@ -1,0 +1,1008 @@
+// adaln_residual_fwd / adaln_residual_bwd: the gated residual of a block and
+// the norms on both sides of it, fused, for sm_103a.
+//
+// What it computes, per token n with modulation row s:
+//   u = h, or post(h) w2          (post: RMS or layer norm of the block's output)
+//   t = alpha x + gate_s u        (the residual stream after the block: x_out)
+//   y = (xh w + b)(1 + scale_s) + shift_s,  xh = norm(t)   (the next block's input)
+// and backward, from dt0 = d x_out, dy, x_out and h, with g = dy w (1 + scale_s):
+//   t' = dt0 + r (g - [mean g] - xh mean(g xh)),  dx = alpha t',
+//   dz = t' gate_s w2,  dh = dz, or rh (dz - [mean dz] - hh mean(dz hh)),
+//   A_s = sum dy xh,  B_s = sum dy,  C_s = sum t' hh  over the tokens of row s:
+//   dscale = w A + b B, dshift = B, dgate = w2 C,
+//   dw = sum_s (1 + scale_s) A_s, db = sum_s (1 + scale_s) B_s, dw2 = sum_s gate_s C_s
+// ([.] only for the layer norm; a token with id -1 is padding: x_out = x,
+// y = 0, dx = d x_out, dh = 0).
+//
+// Design.  HBM bound: 8 bytes an element forward and 12 backward with a bf16
+// stream, each touched once.
+//   - Persistent CTAs walk contiguous row ranges.  Thread 0 streams the rows
+//     of every input into a ring of shared-memory stages with bulk copies;
+//     each thread owns the same 8-wide feature groups of every row.  Padding
+//     rows skip the copies of what they do not use (their ids are read one
+//     row ahead, so that the test costs no latency).
+//   - Forward, the three tables of the current modulation row (gate w2,
+//     w (1 + scale), b (1 + scale) + shift) stay in registers and are loaded
+//     again where the id changes.  Backward the registers hold the sums A, B
+//     and C of the current modulation row, and the tables come from L1.
+//   - A row's statistics are sums shifted by the row's first element K (as in
+//     adaln.cu: one pass, the cancellation bounded because K is a sample of
+//     the row); the RMS norm takes K = 0.  One block reduction per norm.
+//   - The sums of a CTA's run of equal ids go to slot (CTA + id): with ids
+//     that do not decrease along the rows no two runs share a slot, so the
+//     partial sums need n_cta + S rows and no atomics on values; a small
+//     kernel adds the slots of each id in CTA order (deterministic).  A slot
+//     claimed twice (ids out of order) is detected, recorded as an error and
+//     turns every table gradient into NaN.
+// Every wait is bounded, as in the other kernels.
+#include <cuda_runtime.h>
+
+#include "pvl_device.cuh"
+
+namespace pvl {
+namespace {
+
+constexpr int kMaxStages = 8;
+constexpr int kMaxWarps = 32;
+constexpr int kMaxCtas = 1216;  // CTAs per launch at most (bounds the partial-sum slots)
+constexpr int kMaxD = 8192;
+
+enum ResidualSite : uint32_t { kSiteResRowFull = 51, kSiteModId = 52, kSiteModOrder = 53 };
+
+// What the block adds: nothing (h absent), h, or post(h).
+enum Branch : int { kNoBranch = 0, kPlain = 1, kPost = 2 };
+
+struct ResidualParams {
+  const void* x;                // forward x, backward x_out (TX)
+  const __nv_bfloat16* h;       // null: not read
+  const float *gate, *shift, *scale;  // [S, D] or null
+  const float *w, *b, *w2;            // [D] or null
+  const int32_t* ids;           // null: row / N
+  void* x_out;                  // forward (TX)
+  __nv_bfloat16* y;             // forward
+  const void* dxo;              // backward (TX), null: zeros
+  const __nv_bfloat16* dy;      // backward
+  void* dx;                     // backward (TX)
+  __nv_bfloat16* dh;            // backward
+  float* part;                  // backward: [3][n_slots][D], null: no table or vector gradients
+  unsigned int* lo;             // backward: first CTA of each id [S]
+  int* hi;                      // backward: last CTA of each id [S]
+  int* tag;                     // backward: id whose sums a slot holds [n_slots]
+  int* ordered;                 // backward: -1 until ids are found out of order
+  DeviceError* err;
+  int N, D, S;
+  bool one_row;                 // no [S, D] table: every valid id stands for row 0
+  bool rms, post_rms;
+  long long rows, rows_per_cta;
+  int n_slots;
+  int stages;
+  float alpha, eps;
+  uint64_t timeout_ns;
+};
+
+__device__ __forceinline__ void note_error(DeviceError* e, uint32_t code, uint32_t where) {
+  if (atomicCAS(&e->code, 0u, code) == 0u) {
+    e->where = where;
+    e->block = blockIdx.x;
+    e->thread = threadIdx.x;
+  }
+}
+
+// CTA-wide sums of kN values, the same bits in every thread.  In a warp the
+// values are reduce-scattered (each halving step sends half of what remains),
+// lane group lane / (32 / kN) ends with one value; one lane of each stores it
+// in red, and after the barrier every warp adds the table.  red holds
+// kMaxWarps * kN floats and is not written again before every thread has
+// passed another barrier.
+template <int kN>
+__device__ __forceinline__ void block_sum(float (&a)[kN], float* red, int nwarps) {
+  const int lane = threadIdx.x & 31;
+  int o = 16;
+#pragma unroll
+  for (int n = kN; n > 1; n >>= 1, o >>= 1) {
+    const bool hi = lane & o;
+#pragma unroll
+    for (int j = 0; j < n / 2; ++j) {
+      const float keep = hi ? a[j + n / 2] : a[j];
+      const float send = hi ? a[j] : a[j + n / 2];
+      a[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+#pragma unroll
+  for (int q = 16 / kN; q >= 1; q >>= 1) a[0] += __shfl_xor_sync(0xffffffffu, a[0], q);
+  constexpr int kGroup = 32 / kN;
+  float t = a[0];
+  if (nwarps == 1) {
+#pragma unroll
+    for (int q = 0; q < kN; ++q) a[q] = __shfl_sync(0xffffffffu, t, q * kGroup);
+    return;
+  }
+  if ((lane & (kGroup - 1)) == 0) red[(threadIdx.x >> 5) * kN + lane / kGroup] = t;
+  __syncthreads();
+  t = 0.0f;
+  for (int i = lane; i < nwarps * kN; i += 32) t += red[i];
+#pragma unroll
+  for (int q = kN; q < 32; q <<= 1) t += __shfl_xor_sync(0xffffffffu, t, q);
+#pragma unroll
+  for (int q = 0; q < kN; ++q) a[q] = __shfl_sync(0xffffffffu, t, q);
+}
+
+__device__ __forceinline__ void unpack8(const uint4 u, float2 (&f)[4]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+
+// group v (8 features) of a row of the residual stream, in shared memory
+__device__ __forceinline__ void row8(const __nv_bfloat16* row, int v, float2 (&f)[4]) {
+  unpack8(reinterpret_cast<const uint4*>(row)[v], f);
+}
+__device__ __forceinline__ void row8(const float* row, int v, float2 (&f)[4]) {
+  const float4 a = reinterpret_cast<const float4*>(row)[2 * v];
+  const float4 c = reinterpret_cast<const float4*>(row)[2 * v + 1];
+  f[0] = make_float2(a.x, a.y);
+  f[1] = make_float2(a.z, a.w);
+  f[2] = make_float2(c.x, c.y);
+  f[3] = make_float2(c.z, c.w);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* row, int v, const float2 (&f)[4]) {
+  reinterpret_cast<uint4*>(row)[v] = make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
+                                                pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
+}
+__device__ __forceinline__ void store8(float* row, int v, const float2 (&f)[4]) {
+  reinterpret_cast<float4*>(row)[2 * v] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+  reinterpret_cast<float4*>(row)[2 * v + 1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+}
+// 8 entries of a table or vector in global memory, or `fill` where it is absent
+__device__ __forceinline__ void table8(const float* t, size_t at, float fill, float2 (&f)[4]) {
+  if (t == nullptr) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = make_float2(fill, fill);
+    return;
+  }
+  const float4 a = __ldg(reinterpret_cast<const float4*>(t + at));
+  const float4 c = __ldg(reinterpret_cast<const float4*>(t + at) + 1);
+  f[0] = make_float2(a.x, a.y);
+  f[1] = make_float2(a.z, a.w);
+  f[2] = make_float2(c.x, c.y);
+  f[3] = make_float2(c.z, c.w);
+}
+__device__ __forceinline__ float first(const __nv_bfloat16* row) { return __bfloat162float(row[0]); }
+__device__ __forceinline__ float first(const float* row) { return row[0]; }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// gate w2 of a modulation row: the factor of the (normalised) block output
+__device__ __forceinline__ void gate8(const ResidualParams& p, int id, int v, float2 (&f)[4]) {
+  float2 q[4];
+  table8(p.gate, static_cast<size_t>(id) * p.D + v * 8, 1.0f, f);
+  if (p.w2) {
+    table8(p.w2, v * 8, 1.0f, q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = fmul2(f[e], q[e]);
+  }
+}
+// w (1 + scale) of a modulation row: the factor of xh
+__device__ __forceinline__ void factor8(const ResidualParams& p, int id, int v, float2 (&f)[4]) {
+  float2 q[4];
+  table8(p.scale, static_cast<size_t>(id) * p.D + v * 8, 0.0f, f);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f[e] = fadd2(f[e], both(1.0f));
+  if (p.w) {
+    table8(p.w, v * 8, 1.0f, q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = fmul2(f[e], q[e]);
+  }
+}
+
+__host__ __device__ constexpr size_t align128(size_t n) { return (n + 127) / 128 * 128; }
+
+// Stage layout: x (TX), h, and backward dy, dxo (TX); each part 128-byte aligned.
+template <typename TX, bool kBwd>
+struct Stage {
+  size_t x_bytes, h_bytes;
+  __host__ __device__ explicit Stage(int D) : x_bytes(align128(sizeof(TX) * D)), h_bytes(align128(2 * D)) {}
+  __host__ __device__ size_t h() const { return x_bytes; }
+  __host__ __device__ size_t dy() const { return x_bytes + h_bytes; }
+  __host__ __device__ size_t dxo() const { return x_bytes + 2 * h_bytes; }
+  __host__ __device__ size_t bytes() const { return kBwd ? 2 * x_bytes + 2 * h_bytes : x_bytes + h_bytes; }
+};
+
+// Thread 0's view of the CTA's row stream: which row to copy next, the id of
+// that row (read one row ahead), and what has been issued.
+template <typename TX, bool kBwd>
+struct Producer {
+  const ResidualParams& p;
+  uint8_t* smem;
+  uint64_t* full;
+  int* ids_s;
+  long long next, end;
+  int32_t next_id;
+  uint32_t issued;
+  int st;
+
+  __device__ Producer(const ResidualParams& q, uint8_t* sm, uint64_t* f, int* is, long long begin, long long e)
+      : p(q), smem(sm), full(f), ids_s(is), next(begin), end(e), next_id(0), issued(0), st(0) {
+    if (next < end) next_id = id_of(next);
+  }
+  __device__ int32_t id_of(long long r) const { return p.ids ? __ldg(p.ids + r) : static_cast<int32_t>(r / p.N); }
+  __device__ void issue() {
+    if (next >= end) return;
+    const Stage<TX, kBwd> lay(p.D);
+    const long long r = next++;
+    int32_t id = next_id;
+    if (next < end) next_id = id_of(next);
+    if (p.one_row) id = id < 0 ? -1 : 0;
+    if (id >= p.S) {
+      note_error(p.err, kDevErrModId, kSiteModId);
+      id = -1;
+    }
+    id = id < 0 ? -1 : id;
+    ids_s[st] = id;
+    uint8_t* dst = smem + st * lay.bytes();
+    const uint32_t xb = sizeof(TX) * p.D, hb = 2 * p.D;
+    const bool live = id >= 0;
+    uint32_t bytes = 0;
+    const bool want_x = !kBwd || live, want_h = p.h && live, want_dy = kBwd && live, want_dxo = kBwd && p.dxo;
+    bytes += (want_x ? xb : 0) + (want_h ? hb : 0) + (want_dy ? hb : 0) + (want_dxo ? xb : 0);
+    mbar_arrive_expect_tx(&full[st], bytes);
+    if (want_x) bulk_load(dst, static_cast<const TX*>(p.x) + r * p.D, xb, &full[st]);
+    if (want_h) bulk_load(dst + lay.h(), p.h + r * p.D, hb, &full[st]);
+    if (want_dy) bulk_load(dst + lay.dy(), p.dy + r * p.D, hb, &full[st]);
+    if (want_dxo) bulk_load(dst + lay.dxo(), static_cast<const TX*>(p.dxo) + r * p.D, xb, &full[st]);
+    ++issued;
+    if (++st == p.stages) st = 0;
+  }
+};
+
+template <int kV, bool kBwd>
+constexpr int max_regs() {
+  return kBwd ? (kV == 1 ? 64 : 96) : (kV == 1 ? 64 : 96);
+}
+
+// Shared state of both directions' kernels.
+struct Shared {
+  uint64_t full[kMaxStages];
+  int ids[kMaxStages];
+  float red[2][kMaxWarps * 8];
+  int abort;
+};
+
+template <typename TX, int kV, int kBranch>
+__global__ void __maxnreg__((max_regs<kV, false>())) residual_fwd_kernel(const ResidualParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Shared sh;
+  const Stage<TX, false> lay(p.D);
+  const int D = p.D, nvec = D / 8, t = threadIdx.x, nthr = blockDim.x, nwarps = nthr / 32;
+  const float inv_d = 1.0f / static_cast<float>(D);
+  const KernelCtl ctl{p.err, &sh.abort, p.timeout_ns};
+  const long long r_begin = static_cast<long long>(blockIdx.x) * p.rows_per_cta;
+  const long long r_end = min(r_begin + p.rows_per_cta, p.rows);
+  if (t == 0) {
+    sh.abort = 0;
+    for (int s = 0; s < p.stages; ++s) mbar_init(&sh.full[s], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  Producer<TX, false> prod(p, smem, sh.full, sh.ids, r_begin, t == 0 ? r_end : r_begin);
+  if (t == 0)
+    for (int s = 0; s < p.stages; ++s) prod.issue();
+
+  uint32_t used = 0, ph = 0;
+  int st = 0, cur = -1;
+  float2 gt[kV][4], fa[kV][4], ad[kV][4];  // gate w2, w (1 + scale), b (1 + scale) + shift
+  float g0 = 0.0f;                         // gate w2 of feature 0
+  for (long long r = r_begin; r < r_end; ++r) {
+    if (!__syncthreads_and(mbar_wait(&sh.full[st], ph, ctl, kSiteResRowFull))) break;
+    // every thread is past the previous row: its stage and the reduction
+    // tables are free
+    if (t == 0 && used > 0) prod.issue();
+    const uint8_t* src = smem + st * lay.bytes();
+    const TX* xs = reinterpret_cast<const TX*>(src);
+    const __nv_bfloat16* hs = reinterpret_cast<const __nv_bfloat16*>(src + lay.h());
+    TX* xo = static_cast<TX*>(p.x_out) + r * D;
+    __nv_bfloat16* yo = p.y + r * D;
+    const int id = sh.ids[st];
+    if (id < 0) {
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        const int v = t + i * nthr;
+        if (v < nvec) {
+          float2 f[4];
+          if (kBranch != kNoBranch) {
+            row8(xs, v, f);
+            store8(xo, v, f);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] = both(0.0f);
+          store8(yo, v, f);
+        }
+      }
+    } else {
+      if (id != cur) {
+        cur = id;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+          const int v = t + i * nthr;
+          if (v < nvec) {
+            const size_t at = static_cast<size_t>(id) * D + v * 8;
+            if (kBranch != kNoBranch) gate8(p, id, v, gt[i]);
+            factor8(p, id, v, fa[i]);
+            table8(p.shift, at, 0.0f, ad[i]);
+            if (p.b) {
+              float2 q[4], sc[4];
+              table8(p.b, v * 8, 0.0f, q);
+              table8(p.scale, at, 0.0f, sc);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) ad[i][e] = fadd2(ad[i][e], ffma2(q[e], sc[e], q[e]));
+            }
+          }
+        }
+        if (kBranch != kNoBranch) {
+          g0 = p.gate ? __ldg(p.gate + static_cast<size_t>(id) * D) : 1.0f;
+          if (p.w2) g0 *= __ldg(p.w2);
+        }
+      }
+      // the branch's own norm
+      float hm = 0.0f, hr = 1.0f;
+      if (kBranch == kPost) {
+        const float K = p.post_rms ? 0.0f : first(hs);
+        float2 s1 = both(0.0f), s2 = both(0.0f);
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+          const int v = t + i * nthr;
+          if (v < nvec) {
+            float2 f[4];
+            row8(hs, v, f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 d = fadd2(f[e], both(-K));
+              s1 = fadd2(s1, d);
+              s2 = ffma2(d, d, s2);
+            }
+          }
+        }
+        float sums[2] = {s1.x + s1.y, s2.x + s2.y};
+        block_sum<2>(sums, sh.red[1], nwarps);
+        const float m1 = p.post_rms ? 0.0f : sums[0] * inv_d;
+        hr = rsqrtf(fmaxf(fmaf(-m1, m1, sums[1] * inv_d), 0.0f) + p.eps);
+        hm = K + m1;
+      }
+      // the residual, kept as its difference from the row's first element
+      float K = 0.0f;
+      if (!p.rms) {
+        K = first(xs);
+        if (kBranch != kNoBranch) K = fmaf((first(hs) - hm) * hr, g0, p.alpha * K);
+      }
+      float2 d[kV][4];
+      float2 s1 = both(0.0f), s2 = both(0.0f);
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        const int v = t + i * nthr;
+        if (v < nvec) {
+          float2 f[4];
+          row8(xs, v, f);
+          if (kBranch != kNoBranch) {
+            float2 q[4];
+            row8(hs, v, q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float2 u = q[e];
+              if (kBranch == kPost) u = fmul2(fadd2(u, both(-hm)), both(hr));
+              f[e] = ffma2(u, gt[i][e], fmul2(f[e], both(p.alpha)));
+            }
+            store8(xo, v, f);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            d[i][e] = fadd2(f[e], both(-K));
+            s1 = fadd2(s1, d[i][e]);
+            s2 = ffma2(d[i][e], d[i][e], s2);
+          }
+        }
+      }
+      float sums[2] = {s1.x + s1.y, s2.x + s2.y};
+      block_sum<2>(sums, sh.red[0], nwarps);
+      const float m1 = p.rms ? 0.0f : sums[0] * inv_d;
+      const float rs = rsqrtf(fmaxf(fmaf(-m1, m1, sums[1] * inv_d), 0.0f) + p.eps);
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        const int v = t + i * nthr;
+        if (v < nvec) {
+          float2 f[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] = ffma2(fmul2(fadd2(d[i][e], both(-m1)), both(rs)), fa[i][e], ad[i][e]);
+          store8(yo, v, f);
+        }
+      }
+    }
+    ++used;
+    if (++st == p.stages) {
+      st = 0;
+      ph ^= 1u;
+    }
+  }
+  // copies still in flight land before the CTA leaves
+  __syncthreads();
+  if (t == 0)
+    for (uint32_t n = used; n < prod.issued; ++n) mbar_drain(&sh.full[n % p.stages], (n / p.stages) & 1, 100000000ull);
+  __syncthreads();
+}
+
+template <typename TX, int kV, int kBranch>
+__global__ void __maxnreg__((max_regs<kV, true>())) residual_bwd_kernel(const ResidualParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Shared sh;
+  const Stage<TX, true> lay(p.D);
+  const int D = p.D, nvec = D / 8, t = threadIdx.x, nthr = blockDim.x, nwarps = nthr / 32;
+  const float inv_d = 1.0f / static_cast<float>(D);
+  const KernelCtl ctl{p.err, &sh.abort, p.timeout_ns};
+  const long long r_begin = static_cast<long long>(blockIdx.x) * p.rows_per_cta;
+  const long long r_end = min(r_begin + p.rows_per_cta, p.rows);
+  if (t == 0) {
+    sh.abort = 0;
+    for (int s = 0; s < p.stages; ++s) mbar_init(&sh.full[s], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  Producer<TX, true> prod(p, smem, sh.full, sh.ids, r_begin, t == 0 ? r_end : r_begin);
+  if (t == 0)
+    for (int s = 0; s < p.stages; ++s) prod.issue();
+
+  uint32_t used = 0, ph = 0;
+  int st = 0, cur = -1;
+  float2 aa[kV][4], ab[kV][4], ac[kV][4];  // A, B and C of the current modulation row
+  // the run's sums go to slot (CTA + id)
+  auto flush = [&]() {
+    if (cur < 0 || p.part == nullptr) return;
+    const int slot = static_cast<int>(blockIdx.x) + cur;
+    if (t == 0) {
+      if (atomicExch(&p.tag[slot], cur) != -1) {
+        *p.ordered = 0;
+        note_error(p.err, kDevErrModOrder, kSiteModOrder);
+      }
+      atomicMin(&p.lo[cur], blockIdx.x);
+      atomicMax(&p.hi[cur], static_cast<int>(blockIdx.x));
+    }
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      const int v = t + i * nthr;
+      if (v < nvec) {
+        float* q = p.part + static_cast<size_t>(slot) * D;
+        const size_t next = static_cast<size_t>(p.n_slots) * D;
+        store8(q, v, aa[i]);
+        store8(q + next, v, ab[i]);
+        if (kBranch != kNoBranch) store8(q + 2 * next, v, ac[i]);
+      }
+    }
+  };
+  for (long long r = r_begin; r < r_end; ++r) {
+    if (!__syncthreads_and(mbar_wait(&sh.full[st], ph, ctl, kSiteResRowFull))) break;
+    if (t == 0 && used > 0) prod.issue();
+    const uint8_t* src = smem + st * lay.bytes();
+    const TX* xs = reinterpret_cast<const TX*>(src);
+    const __nv_bfloat16* hs = reinterpret_cast<const __nv_bfloat16*>(src + lay.h());
+    const __nv_bfloat16* ys = reinterpret_cast<const __nv_bfloat16*>(src + lay.dy());
+    const TX* us = reinterpret_cast<const TX*>(src + lay.dxo());
+    TX* dxo = static_cast<TX*>(p.dx) + r * D;
+    __nv_bfloat16* dho = kBranch == kNoBranch ? nullptr : p.dh + r * D;
+    const int id = sh.ids[st];
+    if (id < 0) {
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        const int v = t + i * nthr;
+        if (v < nvec) {
+          float2 f[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] = both(0.0f);
+          if (kBranch != kNoBranch) store8(dho, v, f);
+          if (p.dxo) row8(us, v, f);
+          store8(dxo, v, f);
+        }
+      }
+    } else {
+      if (id != cur) {
+        flush();
+        cur = id;
+#pragma unroll
+        for (int i = 0; i < kV; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) aa[i][e] = ab[i][e] = ac[i][e] = both(0.0f);
+      }
+      // sums over the row: of d = x_out - K, d^2, g = dy w (1 + scale) and g d;
+      // with a post norm also those of the branch
+      const float K = p.rms ? 0.0f : first(xs);
+      const float Kh = kBranch == kPost && !p.post_rms ? first(hs) : 0.0f;
+      float2 s1 = both(0.0f), s2 = both(0.0f), sg = both(0.0f), sgd = both(0.0f), h1 = both(0.0f), h2 = both(0.0f);
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        const int v = t + i * nthr;
+        if (v < nvec) {
+          float2 f[4], q[4], m[4];
+          row8(xs, v, f);
+          row8(ys, v, q);
+          factor8(p, id, v, m);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 d = fadd2(f[e], both(-K));
+            const float2 g = fmul2(q[e], m[e]);
+            s1 = fadd2(s1, d);
+            s2 = ffma2(d, d, s2);
+            sg = fadd2(sg, g);
+            sgd = ffma2(g, d, sgd);
+          }
+          if (kBranch == kPost) {
+            row8(hs, v, f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 d = fadd2(f[e], both(-Kh));
+              h1 = fadd2(h1, d);
+              h2 = ffma2(d, d, h2);
+            }
+          }
+        }
+      }
+      float m1, rs, mean_g, mean_gxh, hm = 0.0f, hr = 1.0f;
+      if (kBranch == kPost) {
+        float sums[8] = {s1.x + s1.y, s2.x + s2.y, sg.x + sg.y, sgd.x + sgd.y, h1.x + h1.y, h2.x + h2.y, 0.0f, 0.0f};
+        block_sum<8>(sums, sh.red[0], nwarps);
+        m1 = sums[0], rs = sums[1], mean_g = sums[2], mean_gxh = sums[3];
+        const float hm1 = p.post_rms ? 0.0f : sums[4] * inv_d;
+        hr = rsqrtf(fmaxf(fmaf(-hm1, hm1, sums[5] * inv_d), 0.0f) + p.eps);
+        hm = Kh + hm1;
+      } else {
+        float sums[4] = {s1.x + s1.y, s2.x + s2.y, sg.x + sg.y, sgd.x + sgd.y};
+        block_sum<4>(sums, sh.red[0], nwarps);
+        m1 = sums[0], rs = sums[1], mean_g = sums[2], mean_gxh = sums[3];
+      }
+      m1 = p.rms ? 0.0f : m1 * inv_d;
+      rs = rsqrtf(fmaxf(fmaf(-m1, m1, rs * inv_d), 0.0f) + p.eps);
+      mean_gxh = rs * fmaf(-m1, mean_g, mean_gxh) * inv_d;
+      mean_g = p.rms ? 0.0f : mean_g * inv_d;
+      const float2 ca = both(-rs * mean_gxh), cc = both(-rs * mean_g), rs2 = both(rs), sub = both(-(K + m1));
+      float2 z1 = both(0.0f), z2 = both(0.0f);
+      float2 tp[kBranch == kPost ? kV : 1][4];
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        const int v = t + i * nthr;
+        if (v < nvec) {
+          float2 f[4], q[4], m[4], u[4], b[4];
+          row8(xs, v, f);
+          row8(ys, v, q);
+          factor8(p, id, v, m);
+          if (p.dxo) {
+            row8(us, v, u);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[e] = both(0.0f);
+          }
+          if (kBranch != kNoBranch) {
+            if (p.h) {
+              row8(hs, v, b);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) b[e] = both(0.0f);
+            }
+          }
+          float2 gt[4];
+          if (kBranch != kNoBranch) gate8(p, id, v, gt);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 xh = fmul2(fadd2(f[e], sub), rs2);
+            const float2 g = fmul2(q[e], m[e]);
+            const float2 tt = fadd2(u[e], ffma2(g, rs2, ffma2(xh, ca, cc)));
+            aa[i][e] = ffma2(q[e], xh, aa[i][e]);
+            ab[i][e] = fadd2(ab[i][e], q[e]);
+            f[e] = fmul2(tt, both(p.alpha));
+            if (kBranch == kPost) {
+              const float2 hd = fadd2(b[e], both(-hm));
+              const float2 dz = fmul2(tt, gt[e]);
+              ac[i][e] = ffma2(tt, fmul2(hd, both(hr)), ac[i][e]);
+              z1 = fadd2(z1, dz);
+              z2 = ffma2(dz, hd, z2);
+              tp[kBranch == kPost ? i : 0][e] = dz;
+            } else if (kBranch == kPlain) {
+              ac[i][e] = ffma2(tt, b[e], ac[i][e]);
+              u[e] = fmul2(tt, gt[e]);
+            }
+          }
+          store8(dxo, v, f);
+          if (kBranch == kPlain) store8(dho, v, u);
+        }
+      }
+      if (kBranch == kPost) {
+        float sums[2] = {z1.x + z1.y, z2.x + z2.y};
+        block_sum<2>(sums, sh.red[1], nwarps);
+        // dh = rh (dz - [mean dz] - hh mean(dz hh)), hh = (h - hm) rh
+        const float2 c0 = both(p.post_rms ? 0.0f : -hr * sums[0] * inv_d);
+        const float2 c1 = both(-hr * hr * hr * sums[1] * inv_d);
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+          const int v = t + i * nthr;
+          if (v < nvec) {
+            float2 b[4];
+            row8(hs, v, b);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              b[e] = ffma2(tp[kBranch == kPost ? i : 0][e], both(hr), ffma2(fadd2(b[e], both(-hm)), c1, c0));
+            store8(dho, v, b);
+          }
+        }
+      }
+    }
+    ++used;
+    if (++st == p.stages) {
+      st = 0;
+      ph ^= 1u;
+    }
+  }
+  flush();
+  __syncthreads();
+  if (t == 0)
+    for (uint32_t n = used; n < prod.issued; ++n) mbar_drain(&sh.full[n % p.stages], (n / p.stages) & 1, 100000000ull);
+  __syncthreads();
+}
+
+// Sums A, B and C of each modulation row from the slots of the CTAs lo..hi
+// that met it, in CTA order.  A CTA takes one id and 128 features: lane l the
+// float4 at feature 4 l, warp w the CTAs lo + w, lo + w + W, ...; warp 0 adds
+// the warps' sums in order.  Writes the table gradients, and the plain sums
+// to `tot` ([3][S][D]) where vector gradients follow.
+struct FinalParams {
+  const float* part;
+  const unsigned int* lo;
+  const int* hi;
+  const int* tag;
+  const int* ordered;
+  const float *gate, *scale, *w, *b, *w2;
+  float *dgate, *dshift, *dscale, *dw, *db, *dw2;
+  float* tot;
+  int D, S, n_slots;
+  bool branch;
+};
+constexpr int kFinWarps = 8;
+
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+__device__ __forceinline__ float4 fma4(float4 a, float4 b, float4 c) {
+  return make_float4(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y), fmaf(a.z, b.z, c.z), fmaf(a.w, b.w, c.w));
+}
+__device__ __forceinline__ float4 vec4(const float* p, int d, float fill) {
+  return p ? __ldg(reinterpret_cast<const float4*>(p + d)) : make_float4(fill, fill, fill, fill);
+}
+
+__global__ void __launch_bounds__(32 * kFinWarps) residual_rows_kernel(const FinalParams p) {
+  __shared__ float4 acc[kFinWarps][3][32];
+  const int lane = threadIdx.x, w = threadIdx.y, W = blockDim.y;
+  const int s = blockIdx.x;
+  const int d = blockIdx.y * 128 + lane * 4;
+  const int c0 = static_cast<int>(p.lo[s]), c1 = p.hi[s];  // none: lo = 0xffffffff, hi = -1
+  const int sums = p.branch ? 3 : 2;
+  float4 a[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (d < p.D && c1 >= 0) {
+    for (int c = c0 + w; c <= c1; c += W) {
+      const int slot = c + s;
+      if (p.tag[slot] != s) continue;  // a CTA of padding between two that met the id
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (k < sums)
+          a[k] = add4(a[k], __ldg(reinterpret_cast<const float4*>(
+                                p.part + (static_cast<size_t>(k) * p.n_slots + slot) * p.D + d)));
+    }
+  }
+  if (W > 1) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) acc[w][k][lane] = a[k];
+    __syncthreads();
+    if (w > 0) return;
+    for (int i = 1; i < W; ++i)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) a[k] = add4(a[k], acc[i][k][lane]);
+  }
+  if (d >= p.D) return;
+  if (*p.ordered != -1) {
+    const float nan = __int_as_float(0x7fffffff);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) a[k] = make_float4(nan, nan, nan, nan);
+  }
+  const size_t at = static_cast<size_t>(s) * p.D + d;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p.tot)
+    for (int k = 0; k < sums; ++k) *reinterpret_cast<float4*>(p.tot + static_cast<size_t>(k) * p.S * p.D + at) = a[k];
+  if (p.dshift) *reinterpret_cast<float4*>(p.dshift + at) = a[1];
+  if (p.dscale) {
+    float4 o = fma4(a[0], vec4(p.w, d, 1.0f), zero);
+    if (p.b) o = fma4(a[1], vec4(p.b, d, 0.0f), o);
+    *reinterpret_cast<float4*>(p.dscale + at) = o;
+  }
+  if (p.dgate) *reinterpret_cast<float4*>(p.dgate + at) = fma4(a[2], vec4(p.w2, d, 1.0f), zero);
+}
+
+// dw, db, dw2 = sums over the modulation rows of factor times A, B, C.  A CTA
+// takes 32 features of one vector (blockIdx.y): lane group of 8 the float4s
+// of one row, 32 rows at a time, added in a fixed order.
+__global__ void __launch_bounds__(256) residual_vectors_kernel(const FinalParams p) {
+  __shared__ float4 acc[32][8];
+  const int k = blockIdx.y;
+  float* out = k == 0 ? p.dw : k == 1 ? p.db : p.dw2;
+  if (!out) return;
+  const float* table = k == 2 ? p.gate : p.scale;
+  const float one = k == 2 ? 0.0f : 1.0f;  // 1 + scale, or gate
+  const int lane = threadIdx.x & 7, g = threadIdx.x >> 3;
+  const int d = blockIdx.x * 32 + lane * 4;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (d < p.D) {
+    const float* tot = p.tot + static_cast<size_t>(k) * p.S * p.D + d;
+#pragma unroll 4
+    for (int s = g; s < p.S; s += 32) {
+      const size_t at = static_cast<size_t>(s) * p.D;
+      float4 f = table ? __ldg(reinterpret_cast<const float4*>(table + at + d))
+                       : make_float4(1.0f - one, 1.0f - one, 1.0f - one, 1.0f - one);
+      f = add4(f, make_float4(one, one, one, one));
+      a = fma4(f, __ldg(reinterpret_cast<const float4*>(tot + at)), a);
+    }
+  }
+  acc[g][lane] = a;
+  __syncthreads();
+  if (g == 0 && d < p.D) {
+    for (int i = 1; i < 32; ++i) a = add4(a, acc[i][lane]);
+    *reinterpret_cast<float4*>(out + d) = a;
+  }
+}
+
+// Launch shape: threads cover the row's 8-wide groups, kV each, in whole
+// warps; as many CTAs per SM as registers and two stages each allow.
+template <typename TX, int kV, int kBranch, bool kBwd>
+pvl_status launch_rows(ResidualParams p, cudaStream_t s, const char* who) {
+  const void* fn;
+  if constexpr (kBwd) fn = reinterpret_cast<const void*>(&residual_bwd_kernel<TX, kV, kBranch>);
+  else fn = reinterpret_cast<const void*>(&residual_fwd_kernel<TX, kV, kBranch>);
+  const int threads = ((p.D / 8 + kV - 1) / kV + 31) / 32 * 32;
+  const int stage_bytes = static_cast<int>(Stage<TX, kBwd>(p.D).bytes());
+  int dev = 0, smem_sm = 0, occ = 0;
+  const int sms = sm_count();
+  pvl_status st = check_cuda(cudaGetDevice(&dev), who);
+  if (st == PVL_OK)
+    st = check_cuda(cudaDeviceGetAttribute(&smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev), who);
+  if (st == PVL_OK) st = check_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, threads, 0), who);
+  if (st != PVL_OK) return st;
+  if (sms <= 0 || occ <= 0) return fail(PVL_ERR_CUDA, "%s: no usable CUDA device", who);
+  constexpr int kReserve = 1024 + static_cast<int>(align128(sizeof(Shared)));  // per CTA: the system's share, static
+  int stages = 0;
+  for (; occ >= 1; --occ) {
+    stages = (smem_sm / occ - kReserve) / stage_bytes;
+    if (stages >= 2) break;
+  }
+  if (occ < 1) return fail(PVL_ERR_UNSUPPORTED, "%s: D = %d does not fit in shared memory", who, p.D);
+  p.stages = stages < kMaxStages ? stages : kMaxStages;
+  long long grid = static_cast<long long>(occ) * sms;
+  if (grid > kMaxCtas) grid = kMaxCtas;
+  if (grid > p.rows) grid = p.rows;
+  p.rows_per_cta = (p.rows + grid - 1) / grid;
+  grid = (p.rows + p.rows_per_cta - 1) / p.rows_per_cta;
+  if (p.stages > p.rows_per_cta) p.stages = p.rows_per_cta < 2 ? 2 : static_cast<int>(p.rows_per_cta);
+  const int smem = p.stages * stage_bytes;
+  st = check_cuda(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), who);
+  if (st != PVL_OK) return st;
+  if constexpr (kBwd) residual_bwd_kernel<TX, kV, kBranch><<<static_cast<unsigned>(grid), threads, smem, s>>>(p);
+  else residual_fwd_kernel<TX, kV, kBranch><<<static_cast<unsigned>(grid), threads, smem, s>>>(p);
+  return check_cuda(cudaGetLastError(), who);
+}
+
+template <typename TX, int kBranch, bool kBwd>
+pvl_status pick_width(const ResidualParams& p, cudaStream_t s, const char* who) {
+  return p.D / 8 >= 64 ? launch_rows<TX, 2, kBranch, kBwd>(p, s, who) : launch_rows<TX, 1, kBranch, kBwd>(p, s, who);
+}
+
+template <bool kBwd>
+pvl_status dispatch(const ResidualParams& p, bool fp32, int branch, cudaStream_t s, const char* who) {
+  if (fp32) {
+    if (branch == kPost) return pick_width<float, kPost, kBwd>(p, s, who);
+    if (branch == kPlain) return pick_width<float, kPlain, kBwd>(p, s, who);
+    return pick_width<float, kNoBranch, kBwd>(p, s, who);
+  }
+  if (branch == kPost) return pick_width<__nv_bfloat16, kPost, kBwd>(p, s, who);
+  if (branch == kPlain) return pick_width<__nv_bfloat16, kPlain, kBwd>(p, s, who);
+  return pick_width<__nv_bfloat16, kNoBranch, kBwd>(p, s, who);
+}
+
+// The checks both directions share; fills the parameters they have in common.
+pvl_status common(const char* who, const pvl_residual* a, ResidualParams& p, int* branch) {
+  if (!a) return fail(PVL_ERR_INVALID_ARG, "%s: null description", who);
+  if (a->B < 1 || a->N < 1 || a->D < 1) return fail(PVL_ERR_INVALID_ARG, "%s: B, N and D must be >= 1", who);
+  if (!(a->eps >= 0.0f) || !(a->eps < 1e30f))
+    return fail(PVL_ERR_INVALID_ARG, "%s: eps must be >= 0 and finite", who);
+  if (!(a->alpha > -1e30f && a->alpha < 1e30f)) return fail(PVL_ERR_INVALID_ARG, "%s: alpha must be finite", who);
+  if (a->stream_dtype != PVL_BF16 && a->stream_dtype != PVL_F32)
+    return fail(PVL_ERR_INVALID_ARG, "%s: stream_dtype %d", who, a->stream_dtype);
+  if (a->norm != PVL_NORM_LAYER && a->norm != PVL_NORM_RMS)
+    return fail(PVL_ERR_INVALID_ARG, "%s: norm %d (layer or RMS)", who, a->norm);
+  if (a->post_norm != PVL_NORM_NONE && a->post_norm != PVL_NORM_LAYER && a->post_norm != PVL_NORM_RMS)
+    return fail(PVL_ERR_INVALID_ARG, "%s: post_norm %d", who, a->post_norm);
+  if (a->post_weight && a->post_norm == PVL_NORM_NONE)
+    return fail(PVL_ERR_INVALID_ARG, "%s: post_weight without a post norm", who);
+  if (a->D % 8 != 0 || a->D > kMaxD)
+    return fail(PVL_ERR_UNSUPPORTED, "%s: D = %d (supported: multiples of 8 up to %d)", who, a->D, kMaxD);
+  const long long rows = static_cast<long long>(a->B) * a->N;
+  if (rows >= (1ll << 31) || rows * a->D >= (1ll << 40)) return fail(PVL_ERR_UNSUPPORTED, "%s: tensor too large", who);
+  const bool tables = a->gate || a->shift || a->scale;
+  if (tables && (a->S < 1 || a->S > PVL_MAX_MOD_ROWS))
+    return fail(a->S < 1 ? PVL_ERR_INVALID_ARG : PVL_ERR_UNSUPPORTED, "%s: %d modulation rows (1 to %d)", who, a->S,
+                PVL_MAX_MOD_ROWS);
+  if (tables && !a->mod_id && a->S != a->B)
+    return fail(PVL_ERR_INVALID_ARG, "%s: without mod_id the tables need B = %d rows, not %d", who, a->B, a->S);
+  const void* ptrs[] = {a->gate, a->shift, a->scale, a->weight, a->bias, a->post_weight};
+  for (const void* q : ptrs)
+    if (reinterpret_cast<uintptr_t>(q) % 16 != 0)
+      return fail(PVL_ERR_UNSUPPORTED, "%s: a table or vector is not 16-byte aligned", who);
+  if (reinterpret_cast<uintptr_t>(a->mod_id) % 4 != 0)
+    return fail(PVL_ERR_UNSUPPORTED, "%s: mod_id is not 4-byte aligned", who);
+  p.gate = a->gate;
+  p.shift = a->shift;
+  p.scale = a->scale;
+  p.w = a->weight;
+  p.b = a->bias;
+  p.w2 = a->post_weight;
+  p.ids = a->mod_id;
+  p.N = a->N;
+  p.D = a->D;
+  p.one_row = !tables;
+  p.S = tables ? a->S : 1;
+  p.rms = a->norm == PVL_NORM_RMS;
+  p.post_rms = a->post_norm == PVL_NORM_RMS;
+  p.rows = rows;
+  p.alpha = a->alpha;
+  p.eps = a->eps;
+  p.timeout_ns = kDefaultTimeoutNs;
+  *branch = a->post_norm != PVL_NORM_NONE ? kPost : kPlain;
+  return PVL_OK;
+}
+
+pvl_status aligned(const char* who, const void* const* ptrs, int n) {
+  for (int i = 0; i < n; ++i)
+    if (reinterpret_cast<uintptr_t>(ptrs[i]) % 16 != 0)
+      return fail(PVL_ERR_UNSUPPORTED, "%s: pointer argument %d is not 16-byte aligned", who, i);
+  return PVL_OK;
+}
+
+// Workspace of the backward: the slots' sums [3][n_slots][D], the totals
+// [3][S][D], then the integers lo [S], hi [S], tag [n_slots], ordered, which
+// one memset sets to all ones.
+struct WsLayout {
+  size_t tot, ints, total;
+  int n_slots;
+  size_t n_ints;
+};
+WsLayout ws_layout(long long rows, int S, int D) {
+  WsLayout w{};
+  w.n_slots = static_cast<int>(rows < kMaxCtas ? rows : kMaxCtas) + S - 1;
+  w.tot = align256(3ull * w.n_slots * D * sizeof(float));
+  w.ints = w.tot + align256(3ull * S * D * sizeof(float));
+  w.n_ints = 2ull * S + w.n_slots + 1;
+  w.total = w.ints + align256(w.n_ints * sizeof(int));
+  return w;
+}
+
+}  // namespace
+}  // namespace pvl
+
+using namespace pvl;
+
+extern "C" pvl_status adaln_residual_fwd(const pvl_residual* a, const void* x, const pvl_bf16* h, void* x_out,
+                                         pvl_bf16* y, pvl_stream_t stream) {
+  const char* who = "adaln_residual_fwd";
+  ResidualParams p{};
+  int branch = 0;
+  pvl_status st = common(who, a, p, &branch);
+  if (st != PVL_OK) return st;
+  if (!x || !y) return fail(PVL_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!h) {
+    if (a->gate || a->post_norm != PVL_NORM_NONE || a->alpha != 1.0f)
+      return fail(PVL_ERR_INVALID_ARG, "%s: gate, post norm and alpha need a branch h", who);
+    branch = kNoBranch;
+  } else if (!x_out) {
+    return fail(PVL_ERR_INVALID_ARG, "%s: null x_out", who);
+  }
+  const void* ptrs[] = {x, h, x_out, y};
+  st = aligned(who, ptrs, 4);
+  if (st != PVL_OK) return st;
+  p.err = device_error_record();
+  if (!p.err) return fail(PVL_ERR_CUDA, "%s: no usable CUDA device", who);
+  p.x = x;
+  p.h = reinterpret_cast<const __nv_bfloat16*>(h);
+  p.x_out = x_out;
+  p.y = reinterpret_cast<__nv_bfloat16*>(y);
+  return dispatch<false>(p, a->stream_dtype == PVL_F32, branch, reinterpret_cast<cudaStream_t>(stream), who);
+}
+
+extern "C" size_t adaln_residual_bwd_ws_bytes(int B, int N, int D, int S) {
+  if (B < 1 || N < 1 || D < 1 || S < 1) return 0;
+  return ws_layout(static_cast<long long>(B) * N, S, D).total;
+}
+
+extern "C" pvl_status adaln_residual_bwd(const pvl_residual* a, const void* dx_out, const pvl_bf16* dy,
+                                         const void* x_out, const pvl_bf16* h, int has_branch, void* dx, pvl_bf16* dh,
+                                         const pvl_residual_grads* g, void* ws, size_t ws_bytes, pvl_stream_t stream) {
+  const char* who = "adaln_residual_bwd";
+  ResidualParams p{};
+  int branch = 0;
+  pvl_status st = common(who, a, p, &branch);
+  if (st != PVL_OK) return st;
+  if (!dy || !x_out || !dx || !g) return fail(PVL_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!has_branch) {
+    if (a->gate || a->post_norm != PVL_NORM_NONE || a->alpha != 1.0f)
+      return fail(PVL_ERR_INVALID_ARG, "%s: gate, post norm and alpha need a branch h", who);
+    branch = kNoBranch;
+  } else if (!dh) {
+    return fail(PVL_ERR_INVALID_ARG, "%s: null dh", who);
+  }
+  if (has_branch && !h && (a->gate || a->post_norm != PVL_NORM_NONE))
+    return fail(PVL_ERR_INVALID_ARG, "%s: h is needed with a gate or a post norm", who);
+  if ((!!g->dgate != !!a->gate) || (!!g->dshift != !!a->shift) || (!!g->dscale != !!a->scale) ||
+      (!!g->dweight != !!a->weight) || (!!g->dbias != !!a->bias) || (!!g->dpost_weight != !!a->post_weight))
+    return fail(PVL_ERR_INVALID_ARG, "%s: one gradient for each table and vector, and no others", who);
+  const bool vectors = a->weight || a->bias || a->post_weight;
+  const bool sums = a->gate || a->shift || a->scale || vectors;
+  const void* ptrs[] = {dx_out, dy, x_out, h, dx, dh, g->dgate, g->dshift, g->dscale, g->dweight, g->dbias,
+                        g->dpost_weight, ws};
+  st = aligned(who, ptrs, 13);
+  if (st != PVL_OK) return st;
+  const WsLayout lay = ws_layout(p.rows, p.S, p.D);
+  if (sums && (!ws || ws_bytes < lay.total))
+    return fail(PVL_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu needed", who, ws ? ws_bytes : 0, lay.total);
+  p.err = device_error_record();
+  if (!p.err) return fail(PVL_ERR_CUDA, "%s: no usable CUDA device", who);
+  p.x = x_out;
+  // without a gate or a post norm nothing depends on h
+  p.h = branch == kPost || a->gate ? reinterpret_cast<const __nv_bfloat16*>(h) : nullptr;
+  p.dxo = dx_out;
+  p.dy = reinterpret_cast<const __nv_bfloat16*>(dy);
+  p.dx = dx;
+  p.dh = reinterpret_cast<__nv_bfloat16*>(dh);
+  p.n_slots = lay.n_slots;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  char* base = static_cast<char*>(ws);
+  if (sums) {
+    p.part = static_cast<float*>(ws);
+    p.lo = reinterpret_cast<unsigned int*>(base + lay.ints);
+    p.hi = reinterpret_cast<int*>(p.lo) + p.S;
+    p.tag = p.hi + p.S;
+    p.ordered = p.tag + lay.n_slots;
+    st = check_cuda(cudaMemsetAsync(p.lo, 0xFF, lay.n_ints * sizeof(int), s), who);
+    if (st != PVL_OK) return st;
+  }
+  st = dispatch<true>(p, a->stream_dtype == PVL_F32, branch, s, who);
+  if (st != PVL_OK || !sums) return st;
+  FinalParams f{};
+  f.part = p.part;
+  f.lo = p.lo;
+  f.hi = p.hi;
+  f.tag = p.tag;
+  f.ordered = p.ordered;
+  f.gate = a->gate;
+  f.scale = a->scale;
+  f.w = a->weight;
+  f.b = a->bias;
+  f.w2 = a->post_weight;
+  f.dgate = g->dgate;
+  f.dshift = g->dshift;
+  f.dscale = g->dscale;
+  f.dw = g->dweight;
+  f.db = g->dbias;
+  f.dw2 = g->dpost_weight;
+  f.tot = vectors ? reinterpret_cast<float*>(base + lay.tot) : nullptr;
+  f.D = p.D;
+  f.S = p.S;
+  f.n_slots = lay.n_slots;
+  f.branch = branch != kNoBranch;
+  // warps for the CTAs an id meets on average
+  const int per_id = 1 + (lay.n_slots - p.S) / p.S;
+  const int warps = per_id >= 8 ? 8 : per_id >= 4 ? 4 : per_id >= 2 ? 2 : 1;
+  residual_rows_kernel<<<dim3(p.S, (p.D + 127) / 128), dim3(32, warps), 0, s>>>(f);
+  st = check_cuda(cudaGetLastError(), who);
+  if (st != PVL_OK || !vectors) return st;
+  residual_vectors_kernel<<<dim3((p.D + 31) / 32, 3), 256, 0, s>>>(f);
+  return check_cuda(cudaGetLastError(), who);
+}

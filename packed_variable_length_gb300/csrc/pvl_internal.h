@@ -17,6 +17,8 @@ namespace pvl {
 // ------------------------------------------------------------ device errors
 constexpr uint32_t kDevErrTimeout = 1;  // a bounded wait ran out
 constexpr uint32_t kDevErrTileMap = 2;  // tile map header does not match the call
+constexpr uint32_t kDevErrModId = 3;    // modulation id past the tables
+constexpr uint32_t kDevErrModOrder = 4; // modulation ids out of order
 
 struct DeviceError {
   unsigned int code;

@@ -232,6 +232,9 @@ extern "C" pvl_status pvl_device_error_detail(pvl_stream_t stream, int32_t* info
     return fail(PVL_ERR_TIMEOUT, "device wait timed out (site %u, block %u, thread %u)", h.where, h.block, h.thread);
   if (h.code == kDevErrTileMap)
     return fail(PVL_ERR_INVALID_ARG, "tile map was built for another shape or block size");
+  if (h.code == kDevErrModId) return fail(PVL_ERR_INVALID_ARG, "a modulation id lies past the modulation tables");
+  if (h.code == kDevErrModOrder)
+    return fail(PVL_ERR_INVALID_ARG, "modulation ids decrease along the rows: their gradients are not separable");
   if (h.code != 0) return fail(PVL_ERR_CUDA, "unknown device error code %u", h.code);
   return PVL_OK;
 }

@@ -52,6 +52,44 @@ __global__ void __launch_bounds__(kThreads) seq_ids_kernel(const __grid_constant
   seq_id[static_cast<size_t>(b) * L + p] = id;
 }
 
+// Position of each token inside its segment.  The host passes the segments'
+// ends (running token counts), so that a row needs no scan here.
+struct SegmentEnds {
+  int32_t end[PVL_MAX_SEGMENTS];
+};
+
+// grid (ceil(L / 256), B): every thread finds its token's segment by binary
+// search (the number of ends <= p) and writes the token's axes.
+__global__ void __launch_bounds__(kThreads) positions_kernel(const __grid_constant__ SegmentEnds tab, int K, int T,
+                                                             int axes, int row_width, int L,
+                                                             int32_t* __restrict__ positions) {
+  extern __shared__ int32_t ends[];  // K entries
+  const int b = blockIdx.y;
+  for (int k = threadIdx.x; k < K; k += kThreads) ends[k] = tab.end[b * K + k];
+  __syncthreads();
+  const int p = blockIdx.x * kThreads + threadIdx.x;
+  if (p >= L) return;
+  int lo = 0, hi = K;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (ends[mid] <= p) lo = mid + 1; else hi = mid;
+  }
+  const int i = lo == K ? 0 : p - (lo ? ends[lo - 1] : 0);
+  int32_t* out = positions + (static_cast<size_t>(b) * L + p) * axes;
+  if (axes == 1) {
+    out[0] = i;
+    return;
+  }
+  const int frame = i / T, slot = i - frame * T;
+  out[0] = frame;
+  if (axes == 2) {
+    out[1] = slot;
+  } else {
+    out[1] = slot / row_width;
+    out[2] = slot % row_width;
+  }
+}
+
 }  // namespace
 }  // namespace pvl
 
@@ -85,4 +123,34 @@ extern "C" pvl_status pack_build_seq_ids(const int32_t* seg_frames, const int32_
   seq_ids_kernel<<<grid, kThreads, (K + 1) * sizeof(int32_t), reinterpret_cast<cudaStream_t>(stream)>>>(
       tab, K, tokens_per_frame, L, seq_id);
   return check_cuda(cudaGetLastError(), "pack_build_seq_ids launch");
+}
+
+extern "C" pvl_status pack_build_positions(const int32_t* seg_frames, int B, int K, int tokens_per_frame, int axes,
+                                           int row_width, int L, int32_t* positions, pvl_stream_t stream) {
+  if (!seg_frames || !positions) return fail(PVL_ERR_INVALID_ARG, "pack_build_positions: null pointer");
+  if (B < 1 || K < 1 || L < 1 || tokens_per_frame < 1)
+    return fail(PVL_ERR_INVALID_ARG, "pack_build_positions: B, K, L and tokens_per_frame must be >= 1");
+  if (axes < 1 || axes > 3) return fail(PVL_ERR_INVALID_ARG, "pack_build_positions: axes = %d (1 to 3)", axes);
+  if (axes == 3 && row_width < 1) return fail(PVL_ERR_INVALID_ARG, "pack_build_positions: row_width must be >= 1");
+  if (static_cast<long long>(B) * K > PVL_MAX_SEGMENTS)
+    return fail(PVL_ERR_UNSUPPORTED, "pack_build_positions: B*K = %lld exceeds %d", static_cast<long long>(B) * K,
+                PVL_MAX_SEGMENTS);
+  if (L > PVL_MAX_L) return fail(PVL_ERR_UNSUPPORTED, "pack_build_positions: L = %d exceeds %d", L, PVL_MAX_L);
+  SegmentEnds tab;
+  for (int b = 0; b < B; ++b) {
+    long long tokens = 0;
+    for (int k = 0; k < K; ++k) {
+      const int f = seg_frames[b * K + k];
+      if (f < 0)
+        return fail(PVL_ERR_INVALID_ARG, "pack_build_positions: row %d segment %d has %d frames", b, k, f);
+      tokens += static_cast<long long>(f) * tokens_per_frame;
+      if (tokens > L)
+        return fail(PVL_ERR_INVALID_ARG, "pack_build_positions: row %d needs %lld tokens > L = %d", b, tokens, L);
+      tab.end[b * K + k] = static_cast<int32_t>(tokens);
+    }
+  }
+  dim3 grid((L + kThreads - 1) / kThreads, B);
+  positions_kernel<<<grid, kThreads, K * sizeof(int32_t), reinterpret_cast<cudaStream_t>(stream)>>>(
+      tab, K, tokens_per_frame, axes, row_width, L, positions);
+  return check_cuda(cudaGetLastError(), "pack_build_positions launch");
 }
