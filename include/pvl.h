@@ -434,8 +434,8 @@ PVL_API pvl_status pack_rotary_bwd(const pvl_rotary* how, const pvl_heads* dq_ou
  * one GPU give the same bits).  Ids out of order that would mix two rows'
  * sums are recorded in the device error record and make every table and
  * vector gradient NaN.
- * ws: adaln_residual_bwd_ws_bytes(B, N, D, S) bytes (S = 1 without tables;
- *   null without tables and vectors), one call at a time.
+ * ws: adaln_residual_bwd_ws_bytes(B, N, D, S) bytes (S = 1 without tables),
+ *   one call at a time.
  * D a multiple of 8, at most 8192; S at most PVL_MAX_MOD_ROWS.  All pointers
  * 16-byte aligned (mod_id 4-byte).  Errors: as adaln_fwd.
  * ---------------------------------------------------------------------- */

@@ -676,15 +676,12 @@ def adaln_residual_bwd(dx_out, dy, x_out, h=None, gate=None, shift=None, scale=N
             _need_cuda(dh, "dh", torch.bfloat16, x_out.shape)
         params = (gate, shift, scale, weight, bias, post_weight)
         grads = [None if t is None else torch.empty_like(t) for t in params]
-        nbytes = 0
-        if any(t is not None for t in params):
-            nbytes = int(lib.adaln_residual_bwd_ws_bytes(B, N, D, S))
-            if ws is None:
-                ws = torch.empty(nbytes, dtype=torch.uint8, device=x_out.device)
+        if ws is None:
+            ws = torch.empty(adaln_residual_bwd_ws_bytes(B, N, D, S), dtype=torch.uint8, device=x_out.device)
         out = _lib.ResidualGrads(*(_ptr(t) for t in grads))
         _check(lib.adaln_residual_bwd(ctypes.byref(how), _ptr(dx_out), dy.data_ptr(), x_out.data_ptr(), _ptr(h),
                                       int(branch), dx.data_ptr(), _ptr(dh) if branch else None, ctypes.byref(out),
-                                      _ptr(ws), 0 if ws is None else ws.numel(), handle))
+                                      ws.data_ptr(), ws.numel(), handle))
     return AdalnResidualGrads(dx, dh if branch else None, *grads)
 
 

@@ -37,6 +37,8 @@
 // Every wait is bounded, as in the other kernels.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "pvl_device.cuh"
 
 namespace pvl {
@@ -47,7 +49,8 @@ constexpr int kMaxWarps = 32;
 constexpr int kMaxCtas = 1216;  // CTAs per launch at most (bounds the partial-sum slots)
 constexpr int kMaxD = 8192;
 
-enum ResidualSite : uint32_t { kSiteResRowFull = 51, kSiteModId = 52, kSiteModOrder = 53 };
+enum ResidualSite : uint32_t { kSiteResRowFull = 51, kSiteModId = 52, kSiteModOrder = 53, kSiteResReady = 54, kSiteResEmpty = 55,
+                                kSiteResTable = 56 };
 
 // What the block adds: nothing (h absent), h, or post(h).
 enum Branch : int { kNoBranch = 0, kPlain = 1, kPost = 2 };
@@ -76,6 +79,8 @@ struct ResidualParams {
   long long rows, rows_per_cta;
   int n_slots;
   int stages;
+  int stats_warps, tables;      // backward: warps for the rows' statistics, table slots in shared memory
+  const float *factors, *gates; // backward: w (1 + scale) and gate w2 as [S, D]
   float alpha, eps;
   uint64_t timeout_ns;
 };
@@ -88,14 +93,14 @@ __device__ __forceinline__ void note_error(DeviceError* e, uint32_t code, uint32
   }
 }
 
-// CTA-wide sums of kN values, the same bits in every thread.  In a warp the
-// values are reduce-scattered (each halving step sends half of what remains),
-// lane group lane / (32 / kN) ends with one value; one lane of each stores it
-// in red, and after the barrier every warp adds the table.  red holds
-// kMaxWarps * kN floats and is not written again before every thread has
-// passed another barrier.
+// CTA-wide sums of kN values in two halves around a barrier that the caller
+// has anyway.  warp_part: in a warp the values are reduce-scattered (each
+// halving step sends half of what remains), lane group lane / (32 / kN) ends
+// with one value, and one lane of each stores it in red.  all_parts, after the
+// barrier: every warp adds the table, the same bits in every thread.  red
+// holds kMaxWarps * kN floats.
 template <int kN>
-__device__ __forceinline__ void block_sum(float (&a)[kN], float* red, int nwarps) {
+__device__ __forceinline__ void warp_part(float (&a)[kN], float* red) {
   const int lane = threadIdx.x & 31;
   int o = 16;
 #pragma unroll
@@ -111,15 +116,12 @@ __device__ __forceinline__ void block_sum(float (&a)[kN], float* red, int nwarps
 #pragma unroll
   for (int q = 16 / kN; q >= 1; q >>= 1) a[0] += __shfl_xor_sync(0xffffffffu, a[0], q);
   constexpr int kGroup = 32 / kN;
-  float t = a[0];
-  if (nwarps == 1) {
-#pragma unroll
-    for (int q = 0; q < kN; ++q) a[q] = __shfl_sync(0xffffffffu, t, q * kGroup);
-    return;
-  }
-  if ((lane & (kGroup - 1)) == 0) red[(threadIdx.x >> 5) * kN + lane / kGroup] = t;
-  __syncthreads();
-  t = 0.0f;
+  if ((lane & (kGroup - 1)) == 0) red[(threadIdx.x >> 5) * kN + lane / kGroup] = a[0];
+}
+template <int kN>
+__device__ __forceinline__ void all_parts(float (&a)[kN], const float* red, int nwarps) {
+  const int lane = threadIdx.x & 31;
+  float t = 0.0f;
   for (int i = lane; i < nwarps * kN; i += 32) t += red[i];
 #pragma unroll
   for (int q = kN; q < 32; q <<= 1) t += __shfl_xor_sync(0xffffffffu, t, q);
@@ -225,18 +227,20 @@ struct Producer {
     if (next < end) next_id = id_of(next);
   }
   __device__ int32_t id_of(long long r) const { return p.ids ? __ldg(p.ids + r) : static_cast<int32_t>(r / p.N); }
+  // modulation row of the next row to issue, -1 for padding
+  __device__ int32_t peek() const {
+    if (next_id < 0) return -1;
+    if (p.one_row) return 0;
+    if (next_id < p.S) return next_id;
+    note_error(p.err, kDevErrModId, kSiteModId);
+    return -1;
+  }
   __device__ void issue() {
     if (next >= end) return;
     const Stage<TX, kBwd> lay(p.D);
     const long long r = next++;
-    int32_t id = next_id;
+    const int32_t id = peek();
     if (next < end) next_id = id_of(next);
-    if (p.one_row) id = id < 0 ? -1 : 0;
-    if (id >= p.S) {
-      note_error(p.err, kDevErrModId, kSiteModId);
-      id = -1;
-    }
-    id = id < 0 ? -1 : id;
     ids_s[st] = id;
     uint8_t* dst = smem + st * lay.bytes();
     const uint32_t xb = sizeof(TX) * p.D, hb = 2 * p.D;
@@ -254,11 +258,6 @@ struct Producer {
   }
 };
 
-template <int kV, bool kBwd>
-constexpr int max_regs() {
-  return kBwd ? (kV == 1 ? 64 : 96) : (kV == 1 ? 64 : 96);
-}
-
 // Shared state of both directions' kernels.
 struct Shared {
   uint64_t full[kMaxStages];
@@ -267,16 +266,35 @@ struct Shared {
   int abort;
 };
 
-template <typename TX, int kV, int kBranch>
-__global__ void __maxnreg__((max_regs<kV, false>())) residual_fwd_kernel(const ResidualParams p) {
+// A row on its way through the phases: which, its stage, its id, and the
+// statistics known so far.
+struct Flight {
+  bool on;
+  int row, st, id;
+  float m, r;    // forward: mean and 1 / deviation of x_out past its K; backward: of x_out
+  float hm, hr;  // mean and 1 / deviation of the branch (post norm)
+  float c0, c1;  // backward: the means that the gradient subtracts
+};
+
+// Every row goes through phases: a first one sums what its first statistics
+// need, the later ones use them.  One iteration of the loop runs the last
+// phase of one row, the first of the next (with a post norm, whose statistics
+// the others wait for, three rows are on the way), and has one barrier, which
+// makes the sums visible and frees the finished row's stage: no phase waits
+// for a reduction of its own row.
+template <typename TX, int kV, int kRegs, int kBranch>
+__global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Shared sh;
+  constexpr bool kThree = kBranch == kPost;
+  constexpr int kN = kThree ? 4 : 2;
   const Stage<TX, false> lay(p.D);
   const int D = p.D, nvec = D / 8, t = threadIdx.x, nthr = blockDim.x, nwarps = nthr / 32;
   const float inv_d = 1.0f / static_cast<float>(D);
   const KernelCtl ctl{p.err, &sh.abort, p.timeout_ns};
-  const long long r_begin = static_cast<long long>(blockIdx.x) * p.rows_per_cta;
-  const long long r_end = min(r_begin + p.rows_per_cta, p.rows);
+  const int r_begin = static_cast<int>(blockIdx.x * p.rows_per_cta);
+  const int r_end = static_cast<int>(min(blockIdx.x * p.rows_per_cta + p.rows_per_cta, p.rows));
+  if (t < kMaxStages) sh.ids[t] = -1;
   if (t == 0) {
     sh.abort = 0;
     for (int s = 0; s < p.stages; ++s) mbar_init(&sh.full[s], 1);
@@ -287,38 +305,105 @@ __global__ void __maxnreg__((max_regs<kV, false>())) residual_fwd_kernel(const R
   if (t == 0)
     for (int s = 0; s < p.stages; ++s) prod.issue();
 
-  uint32_t used = 0, ph = 0;
-  int st = 0, cur = -1;
-  float2 gt[kV][4], fa[kV][4], ad[kV][4];  // gate w2, w (1 + scale), b (1 + scale) + shift
+  float2 gt[kV][4], fa[kV][4], ad[kV][4];  // gate w2, w (1 + scale), b (1 + scale) + shift of row cur
   float g0 = 0.0f;                         // gate w2 of feature 0
-  for (long long r = r_begin; r < r_end; ++r) {
-    if (!__syncthreads_and(mbar_wait(&sh.full[st], ph, ctl, kSiteResRowFull))) break;
-    // every thread is past the previous row: its stage and the reduction
-    // tables are free
-    if (t == 0 && used > 0) prod.issue();
-    const uint8_t* src = smem + st * lay.bytes();
-    const TX* xs = reinterpret_cast<const TX*>(src);
-    const __nv_bfloat16* hs = reinterpret_cast<const __nv_bfloat16*>(src + lay.h());
-    TX* xo = static_cast<TX*>(p.x_out) + r * D;
-    __nv_bfloat16* yo = p.y + r * D;
-    const int id = sh.ids[st];
-    if (id < 0) {
+  int cur = -1;
+  // the residual's 8 features of group v, from the stage
+  auto residual8 = [&](const uint8_t* src, int i, int v, float hm, float hr, float2 (&f)[4]) {
+    row8(reinterpret_cast<const TX*>(src), v, f);
+    if (kBranch != kNoBranch) {
+      float2 q[4];
+      row8(reinterpret_cast<const __nv_bfloat16*>(src + lay.h()), v, q);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (kBranch == kPost) q[e] = fmul2(fadd2(q[e], both(-hm)), both(hr));
+        f[e] = ffma2(q[e], gt[i][e], fmul2(f[e], both(p.alpha)));
+      }
+    }
+  };
+  auto shift_of = [&](const uint8_t* src, float hm, float hr) {
+    if (p.rms) return 0.0f;
+    const float x0 = first(reinterpret_cast<const TX*>(src));
+    if (kBranch == kNoBranch) return x0;
+    return fmaf((first(reinterpret_cast<const __nv_bfloat16*>(src + lay.h())) - hm) * hr, g0, p.alpha * x0);
+  };
+  // x_out of a row, and the sums of its difference from K
+  auto stream = [&](const Flight& f, float& sum1, float& sum2) {
+    const uint8_t* src = smem + f.st * lay.bytes();
+    TX* out = static_cast<TX*>(p.x_out) + static_cast<size_t>(f.row) * D;
+    if (f.id < 0) {
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        const int v = t + i * nthr;
+        if (kBranch != kNoBranch && v < nvec) {
+          float2 q[4];
+          row8(reinterpret_cast<const TX*>(src), v, q);
+          store8(out, v, q);
+        }
+      }
+      return;
+    }
+    const float K = shift_of(src, f.hm, f.hr);
+    float2 s1 = both(0.0f), s2 = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      const int v = t + i * nthr;
+      if (v < nvec) {
+        float2 q[4];
+        residual8(src, i, v, f.hm, f.hr, q);
+        if (kBranch != kNoBranch) store8(out, v, q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          q[e] = fadd2(q[e], both(-K));
+          s1 = fadd2(s1, q[e]);
+          s2 = ffma2(q[e], q[e], s2);
+        }
+      }
+    }
+    sum1 = s1.x + s1.y;
+    sum2 = s2.x + s2.y;
+  };
+
+  Flight b{}, c{};  // the rows after their first and (post norm) second phase
+  b.hr = c.hr = 1.0f;
+  int next = r_begin, st = 0, turn = 0;
+  uint32_t ph = 0, freed = 0;
+  while (next < r_end || b.on || c.on) {
+    // last phase: y
+    const Flight& z = kThree ? c : b;
+    if (z.on) {
+      const uint8_t* src = smem + z.st * lay.bytes();
+      __nv_bfloat16* out = p.y + static_cast<size_t>(z.row) * D;
+      const float sub = z.id < 0 ? 0.0f : shift_of(src, z.hm, z.hr) + z.m;
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
         const int v = t + i * nthr;
         if (v < nvec) {
           float2 f[4];
-          if (kBranch != kNoBranch) {
-            row8(xs, v, f);
-            store8(xo, v, f);
-          }
+          if (z.id < 0) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) f[e] = both(0.0f);
-          store8(yo, v, f);
+            for (int e = 0; e < 4; ++e) f[e] = both(0.0f);
+          } else {
+            residual8(src, i, v, z.hm, z.hr, f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = ffma2(fmul2(fadd2(f[e], both(-sub)), both(z.r)), fa[i][e], ad[i][e]);
+          }
+          store8(out, v, f);
         }
       }
-    } else {
-      if (id != cur) {
+    }
+    float sums[kN] = {};
+    if (kThree && b.on) stream(b, sums[kN - 2], sums[kN - 1]);
+    // a new row enters unless rows of another id still need the tables or
+    // its stage has not been issued
+    Flight a{};
+    a.hr = 1.0f;
+    bool ok = true;
+    if (next < r_end && static_cast<int>(b.on) + static_cast<int>(c.on) < p.stages) {
+      ok = mbar_wait(&sh.full[st], ph, ctl, kSiteResRowFull);
+      const int id = sh.ids[st];
+      a = Flight{id < 0 || id == cur || !kThree || !b.on, next, st, id, 0.0f, 0.0f, 0.0f, 1.0f, 0.0f, 0.0f};
+      if (a.on && id >= 0 && id != cur) {
         cur = id;
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
@@ -342,9 +427,12 @@ __global__ void __maxnreg__((max_regs<kV, false>())) residual_fwd_kernel(const R
           if (p.w2) g0 *= __ldg(p.w2);
         }
       }
-      // the branch's own norm
-      float hm = 0.0f, hr = 1.0f;
-      if (kBranch == kPost) {
+    }
+    if (a.on) {
+      if (!kThree) {
+        stream(a, sums[0], sums[1]);
+      } else if (a.id >= 0) {
+        const __nv_bfloat16* hs = reinterpret_cast<const __nv_bfloat16*>(smem + a.st * lay.bytes() + lay.h());
         const float K = p.post_rms ? 0.0f : first(hs);
         float2 s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll
@@ -355,291 +443,401 @@ __global__ void __maxnreg__((max_regs<kV, false>())) residual_fwd_kernel(const R
             row8(hs, v, f);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float2 d = fadd2(f[e], both(-K));
-              s1 = fadd2(s1, d);
-              s2 = ffma2(d, d, s2);
+              f[e] = fadd2(f[e], both(-K));
+              s1 = fadd2(s1, f[e]);
+              s2 = ffma2(f[e], f[e], s2);
             }
           }
         }
-        float sums[2] = {s1.x + s1.y, s2.x + s2.y};
-        block_sum<2>(sums, sh.red[1], nwarps);
-        const float m1 = p.post_rms ? 0.0f : sums[0] * inv_d;
-        hr = rsqrtf(fmaxf(fmaf(-m1, m1, sums[1] * inv_d), 0.0f) + p.eps);
-        hm = K + m1;
-      }
-      // the residual, kept as its difference from the row's first element
-      float K = 0.0f;
-      if (!p.rms) {
-        K = first(xs);
-        if (kBranch != kNoBranch) K = fmaf((first(hs) - hm) * hr, g0, p.alpha * K);
-      }
-      float2 d[kV][4];
-      float2 s1 = both(0.0f), s2 = both(0.0f);
-#pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        const int v = t + i * nthr;
-        if (v < nvec) {
-          float2 f[4];
-          row8(xs, v, f);
-          if (kBranch != kNoBranch) {
-            float2 q[4];
-            row8(hs, v, q);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float2 u = q[e];
-              if (kBranch == kPost) u = fmul2(fadd2(u, both(-hm)), both(hr));
-              f[e] = ffma2(u, gt[i][e], fmul2(f[e], both(p.alpha)));
-            }
-            store8(xo, v, f);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            d[i][e] = fadd2(f[e], both(-K));
-            s1 = fadd2(s1, d[i][e]);
-            s2 = ffma2(d[i][e], d[i][e], s2);
-          }
-        }
-      }
-      float sums[2] = {s1.x + s1.y, s2.x + s2.y};
-      block_sum<2>(sums, sh.red[0], nwarps);
-      const float m1 = p.rms ? 0.0f : sums[0] * inv_d;
-      const float rs = rsqrtf(fmaxf(fmaf(-m1, m1, sums[1] * inv_d), 0.0f) + p.eps);
-#pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        const int v = t + i * nthr;
-        if (v < nvec) {
-          float2 f[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) f[e] = ffma2(fmul2(fadd2(d[i][e], both(-m1)), both(rs)), fa[i][e], ad[i][e]);
-          store8(yo, v, f);
-        }
+        sums[0] = s1.x + s1.y;
+        sums[1] = s2.x + s2.y;
+        a.hm = K;
       }
     }
-    ++used;
-    if (++st == p.stages) {
-      st = 0;
-      ph ^= 1u;
+    warp_part<kN>(sums, sh.red[turn]);
+    if (!__syncthreads_and(ok)) break;
+    all_parts<kN>(sums, sh.red[turn], nwarps);
+    turn ^= 1;
+    if (z.on) {
+      ++freed;
+      if (t == 0) prod.issue();
+    }
+    // statistics of x_out: past the phase that summed it
+    Flight& y = kThree ? b : a;
+    y.m = p.rms ? 0.0f : sums[kN - 2] * inv_d;
+    y.r = rsqrtf(fmaxf(fmaf(-y.m, y.m, sums[kN - 1] * inv_d), 0.0f) + p.eps);
+    if (kThree) {
+      const float m1 = p.post_rms ? 0.0f : sums[0] * inv_d;
+      a.hr = rsqrtf(fmaxf(fmaf(-m1, m1, sums[1] * inv_d), 0.0f) + p.eps);
+      a.hm += m1;
+      c = b;
+    }
+    b = a;
+    if (a.on) {
+      ++next;
+      if (++st == p.stages) {
+        st = 0;
+        ph ^= 1u;
+      }
     }
   }
   // copies still in flight land before the CTA leaves
   __syncthreads();
   if (t == 0)
-    for (uint32_t n = used; n < prod.issued; ++n) mbar_drain(&sh.full[n % p.stages], (n / p.stages) & 1, 100000000ull);
+    for (uint32_t n = freed; n < prod.issued; ++n) mbar_drain(&sh.full[n % p.stages], (n / p.stages) & 1, 100000000ull);
   __syncthreads();
 }
 
-template <typename TX, int kV, int kBranch>
-__global__ void __maxnreg__((max_regs<kV, true>())) residual_bwd_kernel(const ResidualParams p) {
+// ------------------------------------------------------------- backward
+// Warp roles.  One warp's lane streams the rows into the ring (Producer).
+// kStats warps take whole rows in turn: a row's statistics are sums of one
+// warp, so they need shuffles but no barrier, and a post norm's second sums
+// simply follow its first.  The other warps own feature groups: they wait for
+// a row's statistics, write its dx and dh and add to their groups' A, B and C.
+// Nothing is CTA-wide; the roles meet at the stages' mbarriers only (full:
+// copies landed; ready: statistics written; empty: every group warp done).
+struct RowStats {
+  float m, r;    // mean and 1 / deviation of x_out
+  float c0, c1;  // mean g, mean g xh
+  float hm, hr;  // mean and 1 / deviation of the branch
+  float z0, z1;  // dh's means: -rh mean dz, -rh^3 mean dz (h - hm)
+};
+
+constexpr int kMaxTables = 2;
+
+struct BwdShared {
+  uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages], table[kMaxTables];
+  RowStats stats[kMaxStages];
+  int ids[kMaxStages];
+  int slot[kMaxStages];  // of the row's tables: slot, and the parity of its load in bit 8
+  int abort;
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// A wait of a whole warp: the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const KernelCtl& ctl, uint32_t where) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctl, where));
+}
+__device__ __forceinline__ float total(float2 v) { return warp_sum(v.x + v.y); }
+
+template <typename TX, int kV, int kRegs, int kBranch>
+__global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Shared sh;
+  __shared__ BwdShared sh;
   const Stage<TX, true> lay(p.D);
-  const int D = p.D, nvec = D / 8, t = threadIdx.x, nthr = blockDim.x, nwarps = nthr / 32;
+  const int D = p.D, nvec = D / 8, S = p.stages;
+  const uint32_t table_bytes = align128(4 * static_cast<size_t>(D)) * (kBranch == kPost ? 2 : 1);
+  uint8_t* const ring = smem + p.tables * table_bytes;  // the rows' stages, behind the tables
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group_warps = blockDim.x / 32 - 1 - p.stats_warps;
   const float inv_d = 1.0f / static_cast<float>(D);
   const KernelCtl ctl{p.err, &sh.abort, p.timeout_ns};
-  const long long r_begin = static_cast<long long>(blockIdx.x) * p.rows_per_cta;
-  const long long r_end = min(r_begin + p.rows_per_cta, p.rows);
-  if (t == 0) {
+  const int r_begin = static_cast<int>(blockIdx.x * p.rows_per_cta);
+  const int rows = static_cast<int>(min(p.rows_per_cta, p.rows - blockIdx.x * p.rows_per_cta));
+  if (threadIdx.x == 0) {
     sh.abort = 0;
-    for (int s = 0; s < p.stages; ++s) mbar_init(&sh.full[s], 1);
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.ready[s], 1);
+      mbar_init(&sh.empty[s], group_warps);
+    }
+    for (int s = 0; s < p.tables; ++s) mbar_init(&sh.table[s], 1);
     fence_barrier_init();
   }
   __syncthreads();
-  Producer<TX, true> prod(p, smem, sh.full, sh.ids, r_begin, t == 0 ? r_end : r_begin);
-  if (t == 0)
-    for (int s = 0; s < p.stages; ++s) prod.issue();
 
-  uint32_t used = 0, ph = 0;
-  int st = 0, cur = -1;
-  float2 aa[kV][4], ab[kV][4], ac[kV][4];  // A, B and C of the current modulation row
-  // the run's sums go to slot (CTA + id)
-  auto flush = [&]() {
-    if (cur < 0 || p.part == nullptr) return;
-    const int slot = static_cast<int>(blockIdx.x) + cur;
-    if (t == 0) {
-      if (atomicExch(&p.tag[slot], cur) != -1) {
-        *p.ordered = 0;
-        note_error(p.err, kDevErrModOrder, kSiteModOrder);
+  if (warp < group_warps) {
+    const int t = threadIdx.x, nthr = group_warps * 32;
+    float2 gt[kV][4], fa[kV][4];             // gate w2 and w (1 + scale) of modulation row cur
+    float2 aa[kV][4], ab[kV][4], ac[kV][4];  // its sums A, B and C
+    int cur = -1;
+    // the run's sums go to slot (CTA + id)
+    auto flush = [&]() {
+      if (cur < 0 || p.part == nullptr) return;
+      const int slot = static_cast<int>(blockIdx.x) + cur;
+      if (t == 0) {
+        if (atomicExch(&p.tag[slot], cur) != -1) {
+          *p.ordered = 0;
+          note_error(p.err, kDevErrModOrder, kSiteModOrder);
+        }
+        atomicMin(&p.lo[cur], blockIdx.x);
+        atomicMax(&p.hi[cur], static_cast<int>(blockIdx.x));
       }
-      atomicMin(&p.lo[cur], blockIdx.x);
-      atomicMax(&p.hi[cur], static_cast<int>(blockIdx.x));
-    }
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      const int v = t + i * nthr;
-      if (v < nvec) {
-        float* q = p.part + static_cast<size_t>(slot) * D;
-        const size_t next = static_cast<size_t>(p.n_slots) * D;
-        store8(q, v, aa[i]);
-        store8(q + next, v, ab[i]);
-        if (kBranch != kNoBranch) store8(q + 2 * next, v, ac[i]);
-      }
-    }
-  };
-  for (long long r = r_begin; r < r_end; ++r) {
-    if (!__syncthreads_and(mbar_wait(&sh.full[st], ph, ctl, kSiteResRowFull))) break;
-    if (t == 0 && used > 0) prod.issue();
-    const uint8_t* src = smem + st * lay.bytes();
-    const TX* xs = reinterpret_cast<const TX*>(src);
-    const __nv_bfloat16* hs = reinterpret_cast<const __nv_bfloat16*>(src + lay.h());
-    const __nv_bfloat16* ys = reinterpret_cast<const __nv_bfloat16*>(src + lay.dy());
-    const TX* us = reinterpret_cast<const TX*>(src + lay.dxo());
-    TX* dxo = static_cast<TX*>(p.dx) + r * D;
-    __nv_bfloat16* dho = kBranch == kNoBranch ? nullptr : p.dh + r * D;
-    const int id = sh.ids[st];
-    if (id < 0) {
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
         const int v = t + i * nthr;
         if (v < nvec) {
-          float2 f[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) f[e] = both(0.0f);
-          if (kBranch != kNoBranch) store8(dho, v, f);
-          if (p.dxo) row8(us, v, f);
-          store8(dxo, v, f);
+          float* q = p.part + static_cast<size_t>(slot) * D;
+          const size_t next = static_cast<size_t>(p.n_slots) * D;
+          store8(q, v, aa[i]);
+          store8(q + next, v, ab[i]);
+          if (kBranch != kNoBranch) store8(q + 2 * next, v, ac[i]);
         }
       }
-    } else {
-      if (id != cur) {
-        flush();
-        cur = id;
+    };
+    int st = 0;
+    uint32_t ph = 0;
+    for (int n = 0; n < rows; ++n) {
+      if (!warp_wait(&sh.ready[st], ph, ctl, kSiteResReady)) break;
+      if (!warp_wait(&sh.full[st], ph, ctl, kSiteResRowFull)) break;
+      const uint8_t* src = ring + st * lay.bytes();
+      const TX* xs = reinterpret_cast<const TX*>(src);
+      const __nv_bfloat16* hs = reinterpret_cast<const __nv_bfloat16*>(src + lay.h());
+      const __nv_bfloat16* ys = reinterpret_cast<const __nv_bfloat16*>(src + lay.dy());
+      const TX* us = reinterpret_cast<const TX*>(src + lay.dxo());
+      TX* dxo = static_cast<TX*>(p.dx) + static_cast<size_t>(r_begin + n) * D;
+      __nv_bfloat16* dho = kBranch == kNoBranch ? nullptr : p.dh + static_cast<size_t>(r_begin + n) * D;
+      const int id = sh.ids[st];
+      if (id < 0) {
 #pragma unroll
-        for (int i = 0; i < kV; ++i)
+        for (int i = 0; i < kV; ++i) {
+          const int v = t + i * nthr;
+          if (v < nvec) {
+            float2 f[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) aa[i][e] = ab[i][e] = ac[i][e] = both(0.0f);
+            for (int e = 0; e < 4; ++e) f[e] = both(0.0f);
+            if (kBranch != kNoBranch) store8(dho, v, f);
+            if (p.dxo) row8(us, v, f);
+            store8(dxo, v, f);
+          }
+        }
+      } else {
+        if (id != cur) {
+          flush();
+          cur = id;
+#pragma unroll
+          for (int i = 0; i < kV; ++i) {
+            const int v = t + i * nthr;
+            if (v < nvec) {
+              const size_t at = static_cast<size_t>(id) * D + v * 8;
+              if (kBranch != kNoBranch) table8(p.gates, at, 1.0f, gt[i]);
+              table8(p.factors, at, 1.0f, fa[i]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) aa[i][e] = ab[i][e] = ac[i][e] = both(0.0f);
+          }
+        }
+        const RowStats q = sh.stats[st];
+        const float2 ca = both(-q.r * q.c1), cc = both(-q.r * q.c0), rs = both(q.r), sub = both(-q.m);
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+          const int v = t + i * nthr;
+          if (v < nvec) {
+            float2 f[4], g[4];
+            row8(xs, v, f);
+            row8(ys, v, g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              f[e] = fmul2(fadd2(f[e], sub), rs);  // xh
+              aa[i][e] = ffma2(g[e], f[e], aa[i][e]);
+              ab[i][e] = fadd2(ab[i][e], g[e]);
+              f[e] = ffma2(fmul2(g[e], fa[i][e]), rs, ffma2(f[e], ca, cc));
+            }
+            if (p.dxo) {
+              row8(us, v, g);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) f[e] = fadd2(f[e], g[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) g[e] = fmul2(f[e], both(p.alpha));
+            store8(dxo, v, g);
+            if (kBranch == kPost) {
+              row8(hs, v, g);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                g[e] = fadd2(g[e], both(-q.hm));
+                ac[i][e] = ffma2(f[e], fmul2(g[e], both(q.hr)), ac[i][e]);
+                f[e] = ffma2(fmul2(f[e], gt[i][e]), both(q.hr), ffma2(g[e], both(q.z1), both(q.z0)));
+              }
+              store8(dho, v, f);
+            } else if (kBranch == kPlain) {
+              if (p.h) {
+                row8(hs, v, g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ac[i][e] = ffma2(f[e], g[e], ac[i][e]);
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) f[e] = fmul2(f[e], gt[i][e]);
+              store8(dho, v, f);
+            }
+          }
+        }
       }
-      // sums over the row: of d = x_out - K, d^2, g = dy w (1 + scale) and g d;
-      // with a post norm also those of the branch
-      const float K = p.rms ? 0.0f : first(xs);
-      const float Kh = kBranch == kPost && !p.post_rms ? first(hs) : 0.0f;
-      float2 s1 = both(0.0f), s2 = both(0.0f), sg = both(0.0f), sgd = both(0.0f), h1 = both(0.0f), h2 = both(0.0f);
-#pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        const int v = t + i * nthr;
-        if (v < nvec) {
-          float2 f[4], q[4], m[4];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.empty[st]);
+      if (++st == S) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+    flush();
+  } else if (warp < group_warps + p.stats_warps) {
+    // a warp keeps to its stages, so that it sees every phase of their barriers
+    int st = 0;
+    uint32_t ph = 0;
+    auto step = [&]() {
+      if (++st == S) {
+        st = 0;
+        ph ^= 1u;
+      }
+    };
+    for (int n = 0; n < rows; ++n, step()) {
+      if (st % p.stats_warps != warp - group_warps) continue;
+      if (!warp_wait(&sh.full[st], ph, ctl, kSiteResRowFull)) break;
+      const uint8_t* src = ring + st * lay.bytes();
+      const TX* xs = reinterpret_cast<const TX*>(src);
+      const __nv_bfloat16* hs = reinterpret_cast<const __nv_bfloat16*>(src + lay.h());
+      const __nv_bfloat16* ys = reinterpret_cast<const __nv_bfloat16*>(src + lay.dy());
+      const TX* us = reinterpret_cast<const TX*>(src + lay.dxo());
+      const int id = sh.ids[st];
+      if (id >= 0) {
+        // sums of d = x_out - K, d^2, g = dy w (1 + scale) and g d; with a
+        // post norm also those of the branch
+        RowStats q{};
+        q.hr = 1.0f;
+        const float K = p.rms ? 0.0f : first(xs);
+        const float Kh = kBranch == kPost && !p.post_rms ? first(hs) : 0.0f;
+        const int slot = sh.slot[st];
+        if (p.tables && !warp_wait(&sh.table[slot & 255], slot >> 8, ctl, kSiteResTable)) break;
+        const float* fac = reinterpret_cast<const float*>(smem + (slot & 255) * table_bytes);
+        const float* gat = fac + align128(4 * static_cast<size_t>(D)) / 4;
+        if (kRegs == 96 && p.tables == 0) {  // rows so wide that no table fits beside them: from L2
+          fac = p.factors + static_cast<size_t>(id) * D;
+          gat = p.gates + static_cast<size_t>(id) * D;
+        }
+        float2 s1 = both(0.0f), s2 = both(0.0f), sg = both(0.0f), sgd = both(0.0f), h1 = both(0.0f), h2 = both(0.0f);
+#pragma unroll 2
+        for (int v = lane; v < nvec; v += 32) {
+          float2 f[4], g[4], m[4];
+          row8(fac, v, m);
           row8(xs, v, f);
-          row8(ys, v, q);
-          factor8(p, id, v, m);
+          row8(ys, v, g);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 d = fadd2(f[e], both(-K));
-            const float2 g = fmul2(q[e], m[e]);
-            s1 = fadd2(s1, d);
-            s2 = ffma2(d, d, s2);
-            sg = fadd2(sg, g);
-            sgd = ffma2(g, d, sgd);
+            f[e] = fadd2(f[e], both(-K));
+            g[e] = fmul2(g[e], m[e]);
+            s1 = fadd2(s1, f[e]);
+            s2 = ffma2(f[e], f[e], s2);
+            sg = fadd2(sg, g[e]);
+            sgd = ffma2(g[e], f[e], sgd);
           }
           if (kBranch == kPost) {
             row8(hs, v, f);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float2 d = fadd2(f[e], both(-Kh));
-              h1 = fadd2(h1, d);
-              h2 = ffma2(d, d, h2);
+              f[e] = fadd2(f[e], both(-Kh));
+              h1 = fadd2(h1, f[e]);
+              h2 = ffma2(f[e], f[e], h2);
             }
           }
         }
-      }
-      float m1, rs, mean_g, mean_gxh, hm = 0.0f, hr = 1.0f;
-      if (kBranch == kPost) {
-        float sums[8] = {s1.x + s1.y, s2.x + s2.y, sg.x + sg.y, sgd.x + sgd.y, h1.x + h1.y, h2.x + h2.y, 0.0f, 0.0f};
-        block_sum<8>(sums, sh.red[0], nwarps);
-        m1 = sums[0], rs = sums[1], mean_g = sums[2], mean_gxh = sums[3];
-        const float hm1 = p.post_rms ? 0.0f : sums[4] * inv_d;
-        hr = rsqrtf(fmaxf(fmaf(-hm1, hm1, sums[5] * inv_d), 0.0f) + p.eps);
-        hm = Kh + hm1;
-      } else {
-        float sums[4] = {s1.x + s1.y, s2.x + s2.y, sg.x + sg.y, sgd.x + sgd.y};
-        block_sum<4>(sums, sh.red[0], nwarps);
-        m1 = sums[0], rs = sums[1], mean_g = sums[2], mean_gxh = sums[3];
-      }
-      m1 = p.rms ? 0.0f : m1 * inv_d;
-      rs = rsqrtf(fmaxf(fmaf(-m1, m1, rs * inv_d), 0.0f) + p.eps);
-      mean_gxh = rs * fmaf(-m1, mean_g, mean_gxh) * inv_d;
-      mean_g = p.rms ? 0.0f : mean_g * inv_d;
-      const float2 ca = both(-rs * mean_gxh), cc = both(-rs * mean_g), rs2 = both(rs), sub = both(-(K + m1));
-      float2 z1 = both(0.0f), z2 = both(0.0f);
-      float2 tp[kBranch == kPost ? kV : 1][4];
-#pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        const int v = t + i * nthr;
-        if (v < nvec) {
-          float2 f[4], q[4], m[4], u[4], b[4];
-          row8(xs, v, f);
-          row8(ys, v, q);
-          factor8(p, id, v, m);
-          if (p.dxo) {
-            row8(us, v, u);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) u[e] = both(0.0f);
-          }
-          if (kBranch != kNoBranch) {
-            if (p.h) {
-              row8(hs, v, b);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) b[e] = both(0.0f);
-            }
-          }
-          float2 gt[4];
-          if (kBranch != kNoBranch) gate8(p, id, v, gt);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 xh = fmul2(fadd2(f[e], sub), rs2);
-            const float2 g = fmul2(q[e], m[e]);
-            const float2 tt = fadd2(u[e], ffma2(g, rs2, ffma2(xh, ca, cc)));
-            aa[i][e] = ffma2(q[e], xh, aa[i][e]);
-            ab[i][e] = fadd2(ab[i][e], q[e]);
-            f[e] = fmul2(tt, both(p.alpha));
-            if (kBranch == kPost) {
-              const float2 hd = fadd2(b[e], both(-hm));
-              const float2 dz = fmul2(tt, gt[e]);
-              ac[i][e] = ffma2(tt, fmul2(hd, both(hr)), ac[i][e]);
-              z1 = fadd2(z1, dz);
-              z2 = ffma2(dz, hd, z2);
-              tp[kBranch == kPost ? i : 0][e] = dz;
-            } else if (kBranch == kPlain) {
-              ac[i][e] = ffma2(tt, b[e], ac[i][e]);
-              u[e] = fmul2(tt, gt[e]);
-            }
-          }
-          store8(dxo, v, f);
-          if (kBranch == kPlain) store8(dho, v, u);
-        }
-      }
-      if (kBranch == kPost) {
-        float sums[2] = {z1.x + z1.y, z2.x + z2.y};
-        block_sum<2>(sums, sh.red[1], nwarps);
-        // dh = rh (dz - [mean dz] - hh mean(dz hh)), hh = (h - hm) rh
-        const float2 c0 = both(p.post_rms ? 0.0f : -hr * sums[0] * inv_d);
-        const float2 c1 = both(-hr * hr * hr * sums[1] * inv_d);
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-          const int v = t + i * nthr;
-          if (v < nvec) {
-            float2 b[4];
-            row8(hs, v, b);
+        const float m1 = p.rms ? 0.0f : total(s1) * inv_d;
+        q.r = rsqrtf(fmaxf(fmaf(-m1, m1, total(s2) * inv_d), 0.0f) + p.eps);
+        q.m = K + m1;
+        const float sum_g = total(sg);
+        q.c0 = p.rms ? 0.0f : sum_g * inv_d;
+        q.c1 = q.r * fmaf(-m1, sum_g, total(sgd)) * inv_d;
+        if (kBranch == kPost) {
+          const float hm1 = p.post_rms ? 0.0f : total(h1) * inv_d;
+          q.hr = rsqrtf(fmaxf(fmaf(-hm1, hm1, total(h2) * inv_d), 0.0f) + p.eps);
+          q.hm = Kh + hm1;
+          // dz = t' gate w2: its sum, and that of dz (h - hm)
+          const float2 ca = both(-q.r * q.c1), cc = both(-q.r * q.c0), rs = both(q.r), sub = both(-q.m);
+          float2 z1 = both(0.0f), z2 = both(0.0f);
+#pragma unroll 2
+          for (int v = lane; v < nvec; v += 32) {
+            float2 f[4], g[4], m[4];
+            row8(fac, v, m);
+            row8(xs, v, f);
+            row8(ys, v, g);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              b[e] = ffma2(tp[kBranch == kPost ? i : 0][e], both(hr), ffma2(fadd2(b[e], both(-hm)), c1, c0));
-            store8(dho, v, b);
+              f[e] = ffma2(fmul2(g[e], m[e]), rs, ffma2(fmul2(fadd2(f[e], sub), rs), ca, cc));
+            if (p.dxo) {
+              row8(us, v, g);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) f[e] = fadd2(f[e], g[e]);
+            }
+            row8(gat, v, m);
+            row8(hs, v, g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              f[e] = fmul2(f[e], m[e]);
+              z1 = fadd2(z1, f[e]);
+              z2 = ffma2(f[e], fadd2(g[e], both(-q.hm)), z2);
+            }
           }
+          q.z0 = p.post_rms ? 0.0f : -q.hr * total(z1) * inv_d;
+          q.z1 = -q.hr * q.hr * q.hr * total(z2) * inv_d;
         }
+        if (lane == 0) sh.stats[st] = q;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.ready[st]);
+    }
+  } else if (lane == 0) {
+    Producer<TX, true> prod(p, ring, sh.full, sh.ids, r_begin, r_begin + rows);
+    int st = 0, slot = p.tables - 1, held = -1;  // held: the id whose tables the slot has
+    uint32_t ph = 1;                             // parity of the stage's last empty phase, from the second round on
+    uint32_t loads = 0;                          // table loads so far
+    int last[kMaxTables];                        // the last row that uses each slot
+#pragma unroll
+    for (int i = 0; i < kMaxTables; ++i) last[i] = -1;
+    for (int n = 0; n < rows; ++n) {
+      if (n >= S && !mbar_wait(&sh.empty[st], ph, ctl, kSiteResEmpty)) break;
+      const int id = prod.peek();
+      if (p.tables && id >= 0 && id != held) {
+        held = id;
+        slot = slot + 1 == p.tables ? 0 : slot + 1;
+        // the rows that used the slot have their statistics; one more than
+        // S rows back has left its stage
+        const int row = slot == 0 ? last[0] : last[1];
+        if (row >= 0 && n - row < S && !mbar_wait(&sh.ready[row % S], (row / S) & 1, ctl, kSiteResTable)) break;
+        uint8_t* dst = smem + slot * table_bytes;
+        mbar_arrive_expect_tx(&sh.table[slot], 4 * D * (kBranch == kPost ? 2 : 1));
+        bulk_load(dst, p.factors + static_cast<size_t>(id) * D, 4 * D, &sh.table[slot]);
+        if (kBranch == kPost)
+          bulk_load(dst + align128(4 * static_cast<size_t>(D)), p.gates + static_cast<size_t>(id) * D, 4 * D,
+                    &sh.table[slot]);
+        ++loads;
+      }
+      if (id >= 0) (slot == 0 ? last[0] : last[1]) = n;
+      sh.slot[st] = slot | (p.tables ? static_cast<int>(((loads - 1) / p.tables) & 1) << 8 : 0);
+      prod.issue();
+      if (++st == S) {
+        st = 0;
+        ph ^= 1u;
       }
     }
-    ++used;
-    if (++st == p.stages) {
-      st = 0;
-      ph ^= 1u;
-    }
+    // copies still in flight land before the CTA leaves
+    for (int n = max(0, static_cast<int>(prod.issued) - S); n < static_cast<int>(prod.issued); ++n)
+      mbar_drain(&sh.full[n % S], (n / S) & 1, 100000000ull);
+    for (uint32_t n = loads > static_cast<uint32_t>(p.tables) ? loads - p.tables : 0; n < loads; ++n)
+      mbar_drain(&sh.table[n % p.tables], (n / p.tables) & 1, 100000000ull);
   }
-  flush();
   __syncthreads();
-  if (t == 0)
-    for (uint32_t n = used; n < prod.issued; ++n) mbar_drain(&sh.full[n % p.stages], (n / p.stages) & 1, 100000000ull);
-  __syncthreads();
+}
+
+// The backward's tables w (1 + scale) and gate w2 as [S, D], and its control
+// words (all ones).
+__global__ void __launch_bounds__(256) residual_tables_kernel(const ResidualParams p, float* factors, float* gates,
+                                                              int* ints, size_t n_ints) {
+  const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i < n_ints) ints[i] = -1;
+  const int per = p.D / 8;
+  if (i >= static_cast<size_t>(p.S) * per) return;
+  const int id = static_cast<int>(i / per), v = static_cast<int>(i - static_cast<size_t>(id) * per);
+  float2 f[4];
+  factor8(p, id, v, f);
+  store8(factors + static_cast<size_t>(id) * p.D, v, f);
+  if (gates) {
+    gate8(p, id, v, f);
+    store8(gates + static_cast<size_t>(id) * p.D, v, f);
+  }
 }
 
 // Sums A, B and C of each modulation row from the slots of the CTAs lo..hi
@@ -754,12 +952,19 @@ __global__ void __launch_bounds__(256) residual_vectors_kernel(const FinalParams
 
 // Launch shape: threads cover the row's 8-wide groups, kV each, in whole
 // warps; as many CTAs per SM as registers and two stages each allow.
-template <typename TX, int kV, int kBranch, bool kBwd>
+constexpr int kStatsWarps = 2;
+template <typename TX, int kV, int kRegs, int kBranch, bool kBwd>
 pvl_status launch_rows(ResidualParams p, cudaStream_t s, const char* who) {
   const void* fn;
-  if constexpr (kBwd) fn = reinterpret_cast<const void*>(&residual_bwd_kernel<TX, kV, kBranch>);
-  else fn = reinterpret_cast<const void*>(&residual_fwd_kernel<TX, kV, kBranch>);
-  const int threads = ((p.D / 8 + kV - 1) / kV + 31) / 32 * 32;
+  if constexpr (kBwd) fn = reinterpret_cast<const void*>(&residual_bwd_kernel<TX, kV, kRegs, kBranch>);
+  else fn = reinterpret_cast<const void*>(&residual_fwd_kernel<TX, kV, kRegs, kBranch>);
+  int threads = ((p.D / 8 + kV - 1) / kV + 31) / 32 * 32;
+  if (kBwd) {
+    // registers are a quarter of the SM's per scheduler, warps whole
+    constexpr int kMostWarps = 4 * (512 / kRegs);
+    p.stats_warps = std::min(kStatsWarps, kMostWarps - threads / 32 - 1);
+    threads += 32 * (p.stats_warps + 1);
+  }
   const int stage_bytes = static_cast<int>(Stage<TX, kBwd>(p.D).bytes());
   int dev = 0, smem_sm = 0, occ = 0;
   const int sms = sm_count();
@@ -769,10 +974,21 @@ pvl_status launch_rows(ResidualParams p, cudaStream_t s, const char* who) {
   if (st == PVL_OK) st = check_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, threads, 0), who);
   if (st != PVL_OK) return st;
   if (sms <= 0 || occ <= 0) return fail(PVL_ERR_CUDA, "%s: no usable CUDA device", who);
-  constexpr int kReserve = 1024 + static_cast<int>(align128(sizeof(Shared)));  // per CTA: the system's share, static
+  constexpr int kReserve = 1024 + static_cast<int>(align128(kBwd ? sizeof(BwdShared) : sizeof(Shared)));  // per CTA: the system's share, static
+  const int table_bytes = kBwd ? static_cast<int>(align128(4 * p.D)) * (kBranch == kPost ? 2 : 1) : 0;
   int stages = 0;
   for (; occ >= 1; --occ) {
-    stages = (smem_sm / occ - kReserve) / stage_bytes;
+    // two table slots where they leave five stages, else one
+    p.tables = kBwd ? 2 : 0;
+    stages = (smem_sm / occ - kReserve - p.tables * table_bytes) / stage_bytes;
+    if (kBwd && stages < 5) {
+      p.tables = 1;
+      stages = (smem_sm / occ - kReserve - table_bytes) / stage_bytes;
+    }
+    if (kBwd && kRegs == 96 && stages < 2 && occ == 1) {
+      p.tables = 0;
+      stages = (smem_sm - kReserve) / stage_bytes;
+    }
     if (stages >= 2) break;
   }
   if (occ < 1) return fail(PVL_ERR_UNSUPPORTED, "%s: D = %d does not fit in shared memory", who, p.D);
@@ -783,17 +999,25 @@ pvl_status launch_rows(ResidualParams p, cudaStream_t s, const char* who) {
   p.rows_per_cta = (p.rows + grid - 1) / grid;
   grid = (p.rows + p.rows_per_cta - 1) / p.rows_per_cta;
   if (p.stages > p.rows_per_cta) p.stages = p.rows_per_cta < 2 ? 2 : static_cast<int>(p.rows_per_cta);
-  const int smem = p.stages * stage_bytes;
+  if (p.stats_warps > p.stages) p.stats_warps = p.stages;  // the others find no stage
+  const int smem = p.stages * stage_bytes + p.tables * table_bytes;
   st = check_cuda(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), who);
   if (st != PVL_OK) return st;
-  if constexpr (kBwd) residual_bwd_kernel<TX, kV, kBranch><<<static_cast<unsigned>(grid), threads, smem, s>>>(p);
-  else residual_fwd_kernel<TX, kV, kBranch><<<static_cast<unsigned>(grid), threads, smem, s>>>(p);
+  if constexpr (kBwd) residual_bwd_kernel<TX, kV, kRegs, kBranch><<<static_cast<unsigned>(grid), threads, smem, s>>>(p);
+  else residual_fwd_kernel<TX, kV, kRegs, kBranch><<<static_cast<unsigned>(grid), threads, smem, s>>>(p);
   return check_cuda(cudaGetLastError(), who);
 }
 
 template <typename TX, int kBranch, bool kBwd>
 pvl_status pick_width(const ResidualParams& p, cudaStream_t s, const char* who) {
-  return p.D / 8 >= 64 ? launch_rows<TX, 2, kBranch, kBwd>(p, s, who) : launch_rows<TX, 1, kBranch, kBwd>(p, s, who);
+  if constexpr (!kBwd) {
+    if (p.D < 512) return launch_rows<TX, 1, 96, kBranch, kBwd>(p, s, who);
+    return launch_rows<TX, 2, kBranch == kPost ? 128 : 96, kBranch, kBwd>(p, s, who);
+  } else {
+    if (p.D > 5120) return launch_rows<TX, 2, 96, kBranch, kBwd>(p, s, who);
+    if (p.D >= 512) return launch_rows<TX, 2, 128, kBranch, kBwd>(p, s, who);
+    return launch_rows<TX, 1, 80, kBranch, kBwd>(p, s, who);
+  }
 }
 
 template <bool kBwd>
@@ -868,10 +1092,10 @@ pvl_status aligned(const char* who, const void* const* ptrs, int n) {
 }
 
 // Workspace of the backward: the slots' sums [3][n_slots][D], the totals
-// [3][S][D], then the integers lo [S], hi [S], tag [n_slots], ordered, which
-// one memset sets to all ones.
+// [3][S][D], the tables [2][S][D], then the integers lo [S], hi [S], tag
+// [n_slots], ordered.
 struct WsLayout {
-  size_t tot, ints, total;
+  size_t tot, tables, ints, total;
   int n_slots;
   size_t n_ints;
 };
@@ -879,7 +1103,8 @@ WsLayout ws_layout(long long rows, int S, int D) {
   WsLayout w{};
   w.n_slots = static_cast<int>(rows < kMaxCtas ? rows : kMaxCtas) + S - 1;
   w.tot = align256(3ull * w.n_slots * D * sizeof(float));
-  w.ints = w.tot + align256(3ull * S * D * sizeof(float));
+  w.tables = w.tot + align256(3ull * S * D * sizeof(float));
+  w.ints = w.tables + align256(2ull * S * D * sizeof(float));
   w.n_ints = 2ull * S + w.n_slots + 1;
   w.total = w.ints + align256(w.n_ints * sizeof(int));
   return w;
@@ -950,7 +1175,7 @@ extern "C" pvl_status adaln_residual_bwd(const pvl_residual* a, const void* dx_o
   st = aligned(who, ptrs, 13);
   if (st != PVL_OK) return st;
   const WsLayout lay = ws_layout(p.rows, p.S, p.D);
-  if (sums && (!ws || ws_bytes < lay.total))
+  if (!ws || ws_bytes < lay.total)
     return fail(PVL_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu needed", who, ws ? ws_bytes : 0, lay.total);
   p.err = device_error_record();
   if (!p.err) return fail(PVL_ERR_CUDA, "%s: no usable CUDA device", who);
@@ -964,15 +1189,20 @@ extern "C" pvl_status adaln_residual_bwd(const pvl_residual* a, const void* dx_o
   p.n_slots = lay.n_slots;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   char* base = static_cast<char*>(ws);
-  if (sums) {
-    p.part = static_cast<float*>(ws);
-    p.lo = reinterpret_cast<unsigned int*>(base + lay.ints);
-    p.hi = reinterpret_cast<int*>(p.lo) + p.S;
-    p.tag = p.hi + p.S;
-    p.ordered = p.tag + lay.n_slots;
-    st = check_cuda(cudaMemsetAsync(p.lo, 0xFF, lay.n_ints * sizeof(int), s), who);
-    if (st != PVL_OK) return st;
-  }
+  p.lo = reinterpret_cast<unsigned int*>(base + lay.ints);
+  p.hi = reinterpret_cast<int*>(p.lo) + p.S;
+  p.tag = p.hi + p.S;
+  p.ordered = p.tag + lay.n_slots;
+  p.part = sums ? static_cast<float*>(ws) : nullptr;
+  float* tables = reinterpret_cast<float*>(base + lay.tables);
+  p.factors = tables;
+  p.gates = tables + static_cast<size_t>(p.S) * p.D;
+  const size_t items = std::max(lay.n_ints, static_cast<size_t>(p.S) * (p.D / 8));
+  residual_tables_kernel<<<static_cast<unsigned>((items + 255) / 256), 256, 0, s>>>(
+      p, tables, branch == kNoBranch ? nullptr : tables + static_cast<size_t>(p.S) * p.D,
+      reinterpret_cast<int*>(p.lo), lay.n_ints);
+  st = check_cuda(cudaGetLastError(), who);
+  if (st != PVL_OK) return st;
   st = dispatch<true>(p, a->stream_dtype == PVL_F32, branch, s, who);
   if (st != PVL_OK || !sums) return st;
   FinalParams f{};
