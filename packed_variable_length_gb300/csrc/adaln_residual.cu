@@ -135,62 +135,88 @@ __device__ __forceinline__ void unpack8(const uint4 u, float2 (&f)[4]) {
   for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
 
-// group v (8 features) of a row of the residual stream, in shared memory
-__device__ __forceinline__ void row8(const __nv_bfloat16* row, int v, float2 (&f)[4]) {
-  unpack8(reinterpret_cast<const uint4*>(row)[v], f);
+// A thread's unit of work is a group of 8 features, v of nvec.  kSplit says
+// which: with a bf16 stream features 8 v .. 8 v + 7, one 16-byte vector; with
+// an fp32 stream the quads v and nvec + v of the row, so that every fp32
+// access of a warp covers 512 contiguous bytes (8 adjacent floats a lane
+// would be two accesses at a stride of 32 bytes, each a two-way bank conflict
+// in shared memory).
+template <bool kSplit>
+__device__ __forceinline__ void row8(const __nv_bfloat16* row, int v, int nvec, float2 (&f)[4]) {
+  if (kSplit) {
+    const uint2 a = reinterpret_cast<const uint2*>(row)[v], c = reinterpret_cast<const uint2*>(row)[nvec + v];
+    unpack8(make_uint4(a.x, a.y, c.x, c.y), f);
+  } else {
+    unpack8(reinterpret_cast<const uint4*>(row)[v], f);
+  }
 }
-__device__ __forceinline__ void row8(const float* row, int v, float2 (&f)[4]) {
-  const float4 a = reinterpret_cast<const float4*>(row)[2 * v];
-  const float4 c = reinterpret_cast<const float4*>(row)[2 * v + 1];
+template <bool kSplit>
+__device__ __forceinline__ void row8(const float* row, int v, int nvec, float2 (&f)[4]) {
+  const float4 a = reinterpret_cast<const float4*>(row)[kSplit ? v : 2 * v];
+  const float4 c = reinterpret_cast<const float4*>(row)[kSplit ? nvec + v : 2 * v + 1];
   f[0] = make_float2(a.x, a.y);
   f[1] = make_float2(a.z, a.w);
   f[2] = make_float2(c.x, c.y);
   f[3] = make_float2(c.z, c.w);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* row, int v, const float2 (&f)[4]) {
-  reinterpret_cast<uint4*>(row)[v] = make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
-                                                pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
+template <bool kSplit>
+__device__ __forceinline__ void store8(__nv_bfloat16* row, int v, int nvec, const float2 (&f)[4]) {
+  const uint4 u = make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                             pack_bf16x2(f[3].x, f[3].y));
+  if (kSplit) {
+    reinterpret_cast<uint2*>(row)[v] = make_uint2(u.x, u.y);
+    reinterpret_cast<uint2*>(row)[nvec + v] = make_uint2(u.z, u.w);
+  } else {
+    reinterpret_cast<uint4*>(row)[v] = u;
+  }
 }
-__device__ __forceinline__ void store8(float* row, int v, const float2 (&f)[4]) {
-  reinterpret_cast<float4*>(row)[2 * v] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-  reinterpret_cast<float4*>(row)[2 * v + 1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+template <bool kSplit>
+__device__ __forceinline__ void store8(float* row, int v, int nvec, const float2 (&f)[4]) {
+  reinterpret_cast<float4*>(row)[kSplit ? v : 2 * v] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+  reinterpret_cast<float4*>(row)[kSplit ? nvec + v : 2 * v + 1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
 }
-// 8 entries of a table or vector in global memory, or `fill` where it is absent
-__device__ __forceinline__ void table8(const float* t, size_t at, float fill, float2 (&f)[4]) {
-  if (t == nullptr) {
+// a group of a table's row or of a vector in global memory, or `fill` where it is absent
+template <bool kSplit>
+__device__ __forceinline__ void table8(const float* row, int v, int nvec, float fill, float2 (&f)[4]) {
+  if (row == nullptr) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) f[e] = make_float2(fill, fill);
     return;
   }
-  const float4 a = __ldg(reinterpret_cast<const float4*>(t + at));
-  const float4 c = __ldg(reinterpret_cast<const float4*>(t + at) + 1);
+  const float4 a = __ldg(reinterpret_cast<const float4*>(row) + (kSplit ? v : 2 * v));
+  const float4 c = __ldg(reinterpret_cast<const float4*>(row) + (kSplit ? nvec + v : 2 * v + 1));
   f[0] = make_float2(a.x, a.y);
   f[1] = make_float2(a.z, a.w);
   f[2] = make_float2(c.x, c.y);
   f[3] = make_float2(c.z, c.w);
+}
+__device__ __forceinline__ const float* at_row(const float* table, int id, int D) {
+  return table ? table + static_cast<size_t>(id) * D : nullptr;
 }
 __device__ __forceinline__ float first(const __nv_bfloat16* row) { return __bfloat162float(row[0]); }
 __device__ __forceinline__ float first(const float* row) { return row[0]; }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // gate w2 of a modulation row: the factor of the (normalised) block output
-__device__ __forceinline__ void gate8(const ResidualParams& p, int id, int v, float2 (&f)[4]) {
+template <bool kSplit>
+__device__ __forceinline__ void gate8(const ResidualParams& p, int id, int v, int nvec, float2 (&f)[4]) {
   float2 q[4];
-  table8(p.gate, static_cast<size_t>(id) * p.D + v * 8, 1.0f, f);
+  table8<kSplit>(at_row(p.gate, id, p.D), v, nvec, 1.0f, f);
   if (p.w2) {
-    table8(p.w2, v * 8, 1.0f, q);
+    table8<kSplit>(p.w2, v, nvec, 1.0f, q);
 #pragma unroll
     for (int e = 0; e < 4; ++e) f[e] = fmul2(f[e], q[e]);
   }
 }
 // w (1 + scale) of a modulation row: the factor of xh
-__device__ __forceinline__ void factor8(const ResidualParams& p, int id, int v, float2 (&f)[4]) {
+template <bool kSplit>
+__device__ __forceinline__ void factor8(const ResidualParams& p, int id, int v, int nvec, float2 (&f)[4]) {
   float2 q[4];
-  table8(p.scale, static_cast<size_t>(id) * p.D + v * 8, 0.0f, f);
+  table8<kSplit>(at_row(p.scale, id, p.D), v, nvec, 0.0f, f);
 #pragma unroll
   for (int e = 0; e < 4; ++e) f[e] = fadd2(f[e], both(1.0f));
   if (p.w) {
-    table8(p.w, v * 8, 1.0f, q);
+    table8<kSplit>(p.w, v, nvec, 1.0f, q);
 #pragma unroll
     for (int e = 0; e < 4; ++e) f[e] = fmul2(f[e], q[e]);
   }
@@ -284,6 +310,7 @@ struct Flight {
 // for a reduction of its own row.
 template <typename TX, int kV, int kRegs, int kBranch>
 __global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
+  constexpr bool kSplit = sizeof(TX) == 4;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Shared sh;
   constexpr bool kThree = kBranch == kPost;
@@ -310,10 +337,10 @@ __global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
   int cur = -1;
   // the residual's 8 features of group v, from the stage
   auto residual8 = [&](const uint8_t* src, int i, int v, float hm, float hr, float2 (&f)[4]) {
-    row8(reinterpret_cast<const TX*>(src), v, f);
+    row8<kSplit>(reinterpret_cast<const TX*>(src), v, nvec, f);
     if (kBranch != kNoBranch) {
       float2 q[4];
-      row8(reinterpret_cast<const __nv_bfloat16*>(src + lay.h()), v, q);
+      row8<kSplit>(reinterpret_cast<const __nv_bfloat16*>(src + lay.h()), v, nvec, q);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (kBranch == kPost) q[e] = fmul2(fadd2(q[e], both(-hm)), both(hr));
@@ -337,8 +364,8 @@ __global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
         const int v = t + i * nthr;
         if (kBranch != kNoBranch && v < nvec) {
           float2 q[4];
-          row8(reinterpret_cast<const TX*>(src), v, q);
-          store8(out, v, q);
+          row8<kSplit>(reinterpret_cast<const TX*>(src), v, nvec, q);
+          store8<kSplit>(out, v, nvec, q);
         }
       }
       return;
@@ -351,7 +378,7 @@ __global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
       if (v < nvec) {
         float2 q[4];
         residual8(src, i, v, f.hm, f.hr, q);
-        if (kBranch != kNoBranch) store8(out, v, q);
+        if (kBranch != kNoBranch) store8<kSplit>(out, v, nvec, q);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           q[e] = fadd2(q[e], both(-K));
@@ -388,7 +415,7 @@ __global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[e] = ffma2(fmul2(fadd2(f[e], both(-sub)), both(z.r)), fa[i][e], ad[i][e]);
           }
-          store8(out, v, f);
+          store8<kSplit>(out, v, nvec, f);
         }
       }
     }
@@ -409,14 +436,13 @@ __global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
         for (int i = 0; i < kV; ++i) {
           const int v = t + i * nthr;
           if (v < nvec) {
-            const size_t at = static_cast<size_t>(id) * D + v * 8;
-            if (kBranch != kNoBranch) gate8(p, id, v, gt[i]);
-            factor8(p, id, v, fa[i]);
-            table8(p.shift, at, 0.0f, ad[i]);
+            if (kBranch != kNoBranch) gate8<kSplit>(p, id, v, nvec, gt[i]);
+            factor8<kSplit>(p, id, v, nvec, fa[i]);
+            table8<kSplit>(at_row(p.shift, id, D), v, nvec, 0.0f, ad[i]);
             if (p.b) {
               float2 q[4], sc[4];
-              table8(p.b, v * 8, 0.0f, q);
-              table8(p.scale, at, 0.0f, sc);
+              table8<kSplit>(p.b, v, nvec, 0.0f, q);
+              table8<kSplit>(at_row(p.scale, id, D), v, nvec, 0.0f, sc);
 #pragma unroll
               for (int e = 0; e < 4; ++e) ad[i][e] = fadd2(ad[i][e], ffma2(q[e], sc[e], q[e]));
             }
@@ -440,7 +466,7 @@ __global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
           const int v = t + i * nthr;
           if (v < nvec) {
             float2 f[4];
-            row8(hs, v, f);
+            row8<kSplit>(hs, v, nvec, f);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               f[e] = fadd2(f[e], both(-K));
@@ -526,6 +552,7 @@ __device__ __forceinline__ float total(float2 v) { return warp_sum(v.x + v.y); }
 
 template <typename TX, int kV, int kRegs, int kBranch>
 __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
+  constexpr bool kSplit = sizeof(TX) == 4;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ BwdShared sh;
   const Stage<TX, true> lay(p.D);
@@ -573,9 +600,9 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
         if (v < nvec) {
           float* q = p.part + static_cast<size_t>(slot) * D;
           const size_t next = static_cast<size_t>(p.n_slots) * D;
-          store8(q, v, aa[i]);
-          store8(q + next, v, ab[i]);
-          if (kBranch != kNoBranch) store8(q + 2 * next, v, ac[i]);
+          store8<kSplit>(q, v, nvec, aa[i]);
+          store8<kSplit>(q + next, v, nvec, ab[i]);
+          if (kBranch != kNoBranch) store8<kSplit>(q + 2 * next, v, nvec, ac[i]);
         }
       }
     };
@@ -600,9 +627,9 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
             float2 f[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[e] = both(0.0f);
-            if (kBranch != kNoBranch) store8(dho, v, f);
-            if (p.dxo) row8(us, v, f);
-            store8(dxo, v, f);
+            if (kBranch != kNoBranch) store8<kSplit>(dho, v, nvec, f);
+            if (p.dxo) row8<kSplit>(us, v, nvec, f);
+            store8<kSplit>(dxo, v, nvec, f);
           }
         }
       } else {
@@ -613,9 +640,8 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
           for (int i = 0; i < kV; ++i) {
             const int v = t + i * nthr;
             if (v < nvec) {
-              const size_t at = static_cast<size_t>(id) * D + v * 8;
-              if (kBranch != kNoBranch) table8(p.gates, at, 1.0f, gt[i]);
-              table8(p.factors, at, 1.0f, fa[i]);
+              if (kBranch != kNoBranch) table8<true>(at_row(p.gates, id, D), v, nvec, 1.0f, gt[i]);
+              table8<true>(at_row(p.factors, id, D), v, nvec, 1.0f, fa[i]);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) aa[i][e] = ab[i][e] = ac[i][e] = both(0.0f);
@@ -628,8 +654,8 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
           const int v = t + i * nthr;
           if (v < nvec) {
             float2 f[4], g[4];
-            row8(xs, v, f);
-            row8(ys, v, g);
+            row8<kSplit>(xs, v, nvec, f);
+            row8<kSplit>(ys, v, nvec, g);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               f[e] = fmul2(fadd2(f[e], sub), rs);  // xh
@@ -638,31 +664,31 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
               f[e] = ffma2(fmul2(g[e], fa[i][e]), rs, ffma2(f[e], ca, cc));
             }
             if (p.dxo) {
-              row8(us, v, g);
+              row8<kSplit>(us, v, nvec, g);
 #pragma unroll
               for (int e = 0; e < 4; ++e) f[e] = fadd2(f[e], g[e]);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) g[e] = fmul2(f[e], both(p.alpha));
-            store8(dxo, v, g);
+            store8<kSplit>(dxo, v, nvec, g);
             if (kBranch == kPost) {
-              row8(hs, v, g);
+              row8<kSplit>(hs, v, nvec, g);
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 g[e] = fadd2(g[e], both(-q.hm));
                 ac[i][e] = ffma2(f[e], fmul2(g[e], both(q.hr)), ac[i][e]);
                 f[e] = ffma2(fmul2(f[e], gt[i][e]), both(q.hr), ffma2(g[e], both(q.z1), both(q.z0)));
               }
-              store8(dho, v, f);
+              store8<kSplit>(dho, v, nvec, f);
             } else if (kBranch == kPlain) {
               if (p.h) {
-                row8(hs, v, g);
+                row8<kSplit>(hs, v, nvec, g);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) ac[i][e] = ffma2(f[e], g[e], ac[i][e]);
               }
 #pragma unroll
               for (int e = 0; e < 4; ++e) f[e] = fmul2(f[e], gt[i][e]);
-              store8(dho, v, f);
+              store8<kSplit>(dho, v, nvec, f);
             }
           }
         }
@@ -713,9 +739,9 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
 #pragma unroll 2
         for (int v = lane; v < nvec; v += 32) {
           float2 f[4], g[4], m[4];
-          row8(fac, v, m);
-          row8(xs, v, f);
-          row8(ys, v, g);
+          row8<true>(fac, v, nvec, m);
+          row8<kSplit>(xs, v, nvec, f);
+          row8<kSplit>(ys, v, nvec, g);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             f[e] = fadd2(f[e], both(-K));
@@ -726,7 +752,7 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
             sgd = ffma2(g[e], f[e], sgd);
           }
           if (kBranch == kPost) {
-            row8(hs, v, f);
+            row8<kSplit>(hs, v, nvec, f);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               f[e] = fadd2(f[e], both(-Kh));
@@ -751,19 +777,19 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
 #pragma unroll 2
           for (int v = lane; v < nvec; v += 32) {
             float2 f[4], g[4], m[4];
-            row8(fac, v, m);
-            row8(xs, v, f);
-            row8(ys, v, g);
+            row8<true>(fac, v, nvec, m);
+            row8<kSplit>(xs, v, nvec, f);
+            row8<kSplit>(ys, v, nvec, g);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               f[e] = ffma2(fmul2(g[e], m[e]), rs, ffma2(fmul2(fadd2(f[e], sub), rs), ca, cc));
             if (p.dxo) {
-              row8(us, v, g);
+              row8<kSplit>(us, v, nvec, g);
 #pragma unroll
               for (int e = 0; e < 4; ++e) f[e] = fadd2(f[e], g[e]);
             }
-            row8(gat, v, m);
-            row8(hs, v, g);
+            row8<true>(gat, v, nvec, m);
+            row8<kSplit>(hs, v, nvec, g);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               f[e] = fmul2(f[e], m[e]);
@@ -793,10 +819,14 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
       if (p.tables && id >= 0 && id != held) {
         held = id;
         slot = slot + 1 == p.tables ? 0 : slot + 1;
-        // the rows that used the slot have their statistics; one more than
-        // S rows back has left its stage
-        const int row = slot == 0 ? last[0] : last[1];
-        if (row >= 0 && n - row < S && !mbar_wait(&sh.ready[row % S], (row / S) & 1, ctl, kSiteResTable)) break;
+        // every row that used the slot must have its statistics: those of
+        // the last S - 1 rows are waited for one by one (different warps
+        // take them, in no order), older ones have left their stages
+        const int end = slot == 0 ? last[0] : last[1];
+        bool free = true;
+        for (int row = max(0, n - S + 1); row <= end && free; ++row)
+          free = mbar_wait(&sh.ready[row % S], (row / S) & 1, ctl, kSiteResTable);
+        if (!free) break;
         uint8_t* dst = smem + slot * table_bytes;
         mbar_arrive_expect_tx(&sh.table[slot], 4 * D * (kBranch == kPost ? 2 : 1));
         bulk_load(dst, p.factors + static_cast<size_t>(id) * D, 4 * D, &sh.table[slot]);
@@ -823,7 +853,9 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
 }
 
 // The backward's tables w (1 + scale) and gate w2 as [S, D], and its control
-// words (all ones).
+// words (all ones).  A row's quads stand in the order in which the kernel
+// reads them: the first quads of all groups, then the second ones.
+template <bool kSplit>
 __global__ void __launch_bounds__(256) residual_tables_kernel(const ResidualParams p, float* factors, float* gates,
                                                               int* ints, size_t n_ints) {
   const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -832,11 +864,11 @@ __global__ void __launch_bounds__(256) residual_tables_kernel(const ResidualPara
   if (i >= static_cast<size_t>(p.S) * per) return;
   const int id = static_cast<int>(i / per), v = static_cast<int>(i - static_cast<size_t>(id) * per);
   float2 f[4];
-  factor8(p, id, v, f);
-  store8(factors + static_cast<size_t>(id) * p.D, v, f);
+  factor8<kSplit>(p, id, v, per, f);
+  store8<true>(factors + static_cast<size_t>(id) * p.D, v, per, f);
   if (gates) {
-    gate8(p, id, v, f);
-    store8(gates + static_cast<size_t>(id) * p.D, v, f);
+    gate8<kSplit>(p, id, v, per, f);
+    store8<true>(gates + static_cast<size_t>(id) * p.D, v, per, f);
   }
 }
 
@@ -907,8 +939,10 @@ __global__ void __launch_bounds__(32 * kFinWarps) residual_rows_kernel(const Fin
   }
   const size_t at = static_cast<size_t>(s) * p.D + d;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (p.tot)
-    for (int k = 0; k < sums; ++k) *reinterpret_cast<float4*>(p.tot + static_cast<size_t>(k) * p.S * p.D + at) = a[k];
+  const float* vectors[3] = {p.w, p.b, p.w2};
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (vectors[k]) *reinterpret_cast<float4*>(p.tot + static_cast<size_t>(k) * p.S * p.D + at) = a[k];
   if (p.dshift) *reinterpret_cast<float4*>(p.dshift + at) = a[1];
   if (p.dscale) {
     float4 o = fma4(a[0], vec4(p.w, d, 1.0f), zero);
@@ -919,35 +953,34 @@ __global__ void __launch_bounds__(32 * kFinWarps) residual_rows_kernel(const Fin
 }
 
 // dw, db, dw2 = sums over the modulation rows of factor times A, B, C.  A CTA
-// takes 32 features of one vector (blockIdx.y): lane group of 8 the float4s
-// of one row, 32 rows at a time, added in a fixed order.
+// takes 16 features of one vector (blockIdx.y): lane group of 4 the float4s of
+// one row, 64 rows at a time; then the 64 sums in a fixed tree.
 __global__ void __launch_bounds__(256) residual_vectors_kernel(const FinalParams p) {
-  __shared__ float4 acc[32][8];
+  __shared__ float4 acc[64][4];
   const int k = blockIdx.y;
   float* out = k == 0 ? p.dw : k == 1 ? p.db : p.dw2;
   if (!out) return;
   const float* table = k == 2 ? p.gate : p.scale;
-  const float one = k == 2 ? 0.0f : 1.0f;  // 1 + scale, or gate
-  const int lane = threadIdx.x & 7, g = threadIdx.x >> 3;
-  const int d = blockIdx.x * 32 + lane * 4;
+  const float one = k == 2 && p.gate ? 0.0f : 1.0f;  // 1 + scale, gate, or 1
+  const int lane = threadIdx.x & 3, g = threadIdx.x >> 2;
+  const int d = blockIdx.x * 16 + lane * 4;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   if (d < p.D) {
     const float* tot = p.tot + static_cast<size_t>(k) * p.S * p.D + d;
-#pragma unroll 4
-    for (int s = g; s < p.S; s += 32) {
+#pragma unroll 8
+    for (int s = g; s < p.S; s += 64) {
       const size_t at = static_cast<size_t>(s) * p.D;
-      float4 f = table ? __ldg(reinterpret_cast<const float4*>(table + at + d))
-                       : make_float4(1.0f - one, 1.0f - one, 1.0f - one, 1.0f - one);
-      f = add4(f, make_float4(one, one, one, one));
-      a = fma4(f, __ldg(reinterpret_cast<const float4*>(tot + at)), a);
+      const float4 f = table ? __ldg(reinterpret_cast<const float4*>(table + at + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      a = fma4(add4(f, make_float4(one, one, one, one)), __ldg(reinterpret_cast<const float4*>(tot + at)), a);
     }
   }
   acc[g][lane] = a;
-  __syncthreads();
-  if (g == 0 && d < p.D) {
-    for (int i = 1; i < 32; ++i) a = add4(a, acc[i][lane]);
-    *reinterpret_cast<float4*>(out + d) = a;
+#pragma unroll
+  for (int n = 32; n; n >>= 1) {
+    __syncthreads();
+    if (g < n) acc[g][lane] = add4(acc[g][lane], acc[g + n][lane]);
   }
+  if (g == 0 && d < p.D) *reinterpret_cast<float4*>(out + d) = acc[0][lane];
 }
 
 // Launch shape: threads cover the row's 8-wide groups, kV each, in whole
@@ -1015,7 +1048,7 @@ pvl_status pick_width(const ResidualParams& p, cudaStream_t s, const char* who) 
     return launch_rows<TX, 2, kBranch == kPost ? 128 : 96, kBranch, kBwd>(p, s, who);
   } else {
     if (p.D > 5120) return launch_rows<TX, 2, 96, kBranch, kBwd>(p, s, who);
-    if (p.D >= 512) return launch_rows<TX, 2, 128, kBranch, kBwd>(p, s, who);
+    if (p.D >= 1536) return launch_rows<TX, 3, 168, kBranch, kBwd>(p, s, who);
     return launch_rows<TX, 1, 80, kBranch, kBwd>(p, s, who);
   }
 }
@@ -1198,7 +1231,8 @@ extern "C" pvl_status adaln_residual_bwd(const pvl_residual* a, const void* dx_o
   p.factors = tables;
   p.gates = tables + static_cast<size_t>(p.S) * p.D;
   const size_t items = std::max(lay.n_ints, static_cast<size_t>(p.S) * (p.D / 8));
-  residual_tables_kernel<<<static_cast<unsigned>((items + 255) / 256), 256, 0, s>>>(
+  (a->stream_dtype == PVL_F32 ? residual_tables_kernel<true> : residual_tables_kernel<false>)<<<
+      static_cast<unsigned>((items + 255) / 256), 256, 0, s>>>(
       p, tables, branch == kNoBranch ? nullptr : tables + static_cast<size_t>(p.S) * p.D,
       reinterpret_cast<int*>(p.lo), lay.n_ints);
   st = check_cuda(cudaGetLastError(), who);
@@ -1233,6 +1267,6 @@ extern "C" pvl_status adaln_residual_bwd(const pvl_residual* a, const void* dx_o
   residual_rows_kernel<<<dim3(p.S, (p.D + 127) / 128), dim3(32, warps), 0, s>>>(f);
   st = check_cuda(cudaGetLastError(), who);
   if (st != PVL_OK || !vectors) return st;
-  residual_vectors_kernel<<<dim3((p.D + 31) / 32, 3), 256, 0, s>>>(f);
+  residual_vectors_kernel<<<dim3((p.D + 15) / 16, 3), 256, 0, s>>>(f);
   return check_cuda(cudaGetLastError(), who);
 }
