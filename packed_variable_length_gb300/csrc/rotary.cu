@@ -5,7 +5,8 @@
 // for each pair (a, b) of the first R features, with t = position x frequency,
 //   (a, b) -> gain (a cos t - b sin t, a sin t + b cos t).
 // Backward, with g the upstream gradient turned by -t (times gain):
-//   no norm: dx = g;  else, n the features the norm runs over,
+//   no norm: dx = g (the forward with the sine negated);  else, n the features
+//   the norm runs over,
 //   dx = r (g w - xh mean_n(g w xh)),  xh = x r,   dw = sum g xh.
 //
 // Angles.  A frequency is given in turns per position as a fraction F of
@@ -15,14 +16,21 @@
 // by about 2^-21, far below the 2^-9 of the bf16 result.
 //
 // Layout of the work.  HBM bound: 4 bytes an element forward, 6 backward with
-// a norm.  A unit is the 2 V features of V pairs: two V-wide vectors, R / 2
-// apart in the half layout, adjacent in the interleaved one.  A team of
-// threads takes one token: a thread owns one unit column of the head (so its
-// angles, computed once a token, serve all its heads) and every hpi-th head,
-// kM of them at a time; queries and keys are one run of heads.  The kM heads'
-// vectors are all loaded before the first is used; the norm over the token
-// holds all of its heads at once.  Teams are whole warps, or a
-// power of two below 32 for tokens of few units.
+// a norm.
+//   - A unit is two V-wide vectors of a head, R / (2 V) vectors apart, so that
+//     neighbouring threads read neighbouring 16 bytes in both layouts: in the
+//     half layout the vectors hold the two sides of V pairs, in the
+//     interleaved one V / 2 pairs each.  Its 2 V values are kept as packed
+//     fp32 pairs A (first sides) and B (second sides), two pairs to a float2.
+//   - A team of threads takes one token: a thread owns one unit column of the
+//     head and every hpi-th head, kM of them at a time; queries and keys are
+//     one run of heads.  The kM heads' vectors are all loaded before the
+//     first is used.  Teams are whole warps, or a power of two below 32.
+//   - A warp (or smaller team) computes its token's R / 2 angles once, one or
+//     two a lane, into shared memory, from where each thread takes its V.
+//   - The norm over the token holds all of a token's heads at once; its
+//     weights stand in shared memory in the order in which the threads read
+//     them.  Its sums cross warps only where a team has several: one barrier.
 #include <cuda_runtime.h>
 
 #include "pvl_device.cuh"
@@ -32,25 +40,27 @@ namespace {
 
 constexpr int kMaxBlock = 512;
 constexpr int kMaxD = 256;
-constexpr int kMaxPartials = 1216;  // blocks of a backward that sums weight gradients
+constexpr int kMaxPartials = 1216;  // rows of partial weight gradients at most
+constexpr float kRadians = 1.4629180792671596e-9f;  // 2 pi / 2^32
 
 struct RotaryParams {
-  pvl_heads x[2];    // q, k: the forward's input (backward: with a norm)
-  pvl_heads g[2];    // backward: gradients of the outputs
-  pvl_heads out[2];  // forward: rotated; backward: dq, dk
+  pvl_heads x[2];    // q, k: what is rotated (backward of a norm: the forward's input)
+  pvl_heads g[2];    // backward of a norm: gradients of the outputs
+  pvl_heads out[2];  // rotated, or dq, dk
   const uint64_t* turns;
   const int32_t* positions;
   const float* w[2];
-  float* part;       // backward: [blocks][width] partial weight gradients, null: none
-  int L, H, Ht, D, R;
-  int half, axes, section_1, section_2;
+  float* part;       // backward: [rows][width] partial weight gradients, null: none
+  uint32_t L, tokens;  // tokens = B * L
+  int H, Ht, D, R;
+  int axes, section_1, section_2;
   int units;         // units of a head, D / (2 V)
   int turned;        // units of a head that are rotated, R / (2 V)
   int hpi;           // heads a team takes at once
   int team, teams;   // threads of a team, teams of a block
-  uint32_t tokens;   // B * L
   int width;         // columns of part
-  float gain, eps;
+  float gain, sign;  // sign: of the sine
+  float eps;
 };
 
 template <int V>
@@ -68,52 +78,66 @@ struct Vec<1> {
   using T = uint16_t;
 };
 
+__device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// A unit's values: kP packed pairs of first and of second sides.
 template <int V>
-__device__ __forceinline__ void unpack(const typename Vec<V>::T& u, float* f) {
+struct Unit {
+  static constexpr int kP = V > 1 ? V / 2 : 1;
+  float2 a[kP], b[kP];
+};
+
+template <int V, bool kHalf>
+__device__ __forceinline__ void unpack(const typename Vec<V>::T& u0, const typename Vec<V>::T& u1, Unit<V>& z) {
   if constexpr (V == 1) {
-    f[0] = __uint_as_float(static_cast<uint32_t>(u) << 16);
+    z.a[0] = make_float2(__uint_as_float(static_cast<uint32_t>(u0) << 16), 0.0f);
+    z.b[0] = make_float2(__uint_as_float(static_cast<uint32_t>(u1) << 16), 0.0f);
   } else {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(&u);
+    const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&u0);
+    const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&u1);
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      if (kHalf) {
+        z.a[i] = make_float2(lo(w0[i]), hi(w0[i]));
+        z.b[i] = make_float2(lo(w1[i]), hi(w1[i]));
+      } else {
+        const uint32_t* w = i < V / 4 ? w0 + 2 * i : w1 + 2 * i - V / 2;
+        z.a[i] = make_float2(lo(w[0]), lo(w[1]));
+        z.b[i] = make_float2(hi(w[0]), hi(w[1]));
+      }
     }
   }
 }
-template <int V>
-__device__ __forceinline__ typename Vec<V>::T pack(const float* f) {
-  typename Vec<V>::T u;
+template <int V, bool kHalf>
+__device__ __forceinline__ void pack(const Unit<V>& z, typename Vec<V>::T& u0, typename Vec<V>::T& u1) {
   if constexpr (V == 1) {
-    u = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+    u0 = __bfloat16_as_ushort(__float2bfloat16_rn(z.a[0].x));
+    u1 = __bfloat16_as_ushort(__float2bfloat16_rn(z.b[0].x));
   } else {
-    uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+    uint32_t* w0 = reinterpret_cast<uint32_t*>(&u0);
+    uint32_t* w1 = reinterpret_cast<uint32_t*>(&u1);
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    for (int i = 0; i < V / 2; ++i) {
+      if (kHalf) {
+        w0[i] = pack_bf16x2(z.a[i].x, z.a[i].y);
+        w1[i] = pack_bf16x2(z.b[i].x, z.b[i].y);
+      } else {
+        uint32_t* w = i < V / 4 ? w0 + 2 * i : w1 + 2 * i - V / 2;
+        w[0] = pack_bf16x2(z.a[i].x, z.b[i].x);
+        w[1] = pack_bf16x2(z.a[i].y, z.b[i].y);
+      }
+    }
   }
-  return u;
 }
 
-constexpr float kRadians = 1.4629180792671596e-9f;  // 2 pi / 2^32
-
-// Rotates one unit (z[0..V) the first vector, z[V..2V) the second).
-template <int V>
-__device__ __forceinline__ void rotate(float* z, const float* c, const float* s, bool half) {
-  if (half) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float a = z[e], b = z[V + e];
-      z[e] = fmaf(a, c[e], -(b * s[e]));
-      z[V + e] = fmaf(a, s[e], b * c[e]);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float a = z[2 * e], b = z[2 * e + 1];
-      z[2 * e] = fmaf(a, c[e], -(b * s[e]));
-      z[2 * e + 1] = fmaf(a, s[e], b * c[e]);
-    }
-  }
+// Feature of value k of a unit (k < kP * 2: first sides, then second sides),
+// from the offsets of its vectors.
+template <int V, bool kHalf>
+__device__ __forceinline__ int feature(int k, int e0, int e1) {
+  const int e = k % (V > 1 ? V : 1), side = k / (V > 1 ? V : 1);
+  if (kHalf || V == 1) return (side ? e1 : e0) + e;
+  return e < V / 2 ? e0 + 2 * e + side : e1 + 2 * e - V + side;
 }
 
 // Sum over the `n` threads of an aligned power-of-two lane group.
@@ -122,244 +146,352 @@ __device__ __forceinline__ float lane_sum(float v, int n) {
   return v;
 }
 
-// kNorm: PVL_NORM_NONE, _HEAD or _TOKEN.
-template <int V, int kM, int kNorm, bool kBwd>
-__global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const RotaryParams p) {
+// Shared memory, in floats: the angles' cosines and sines of each warp or
+// smaller team, the norm's weights, the sums that cross threads (backward of
+// the norm per head also uses that part, at the end, for its weight gradients).
+struct SmemPlan {
+  int angles, weights, sums, total;  // offsets
+};
+__host__ __device__ inline SmemPlan smem_plan(int V, int kM, int norm, bool bwd, int R, int D, int units, int hpi,
+                                              int team, int teams, int threads) {
+  SmemPlan s{};
+  const int group = team < 32 ? team : 32;
+  const int per = 2 * (V > 1 ? V : 2);  // floats of a unit's angles (V = 1: a pair and an unused one)
+  s.angles = 0;
+  s.weights = threads / group * (R / (2 * V)) * per;
+  const int unit_floats = 2 * (V > 1 ? V : 2);
+  const int weights = norm == PVL_NORM_TOKEN ? kM * team * unit_floats : norm == PVL_NORM_HEAD ? 2 * units * unit_floats : 0;
+  s.sums = s.weights + weights;
+  int sums = 0;
+  if (norm == PVL_NORM_TOKEN) sums = 2 * (threads / 32 + 1) * 4;
+  if (norm == PVL_NORM_HEAD) {
+    const bool lanes = (units & (units - 1)) == 0 && units <= 32;
+    if (!lanes) sums = threads * kM * (bwd ? 2 : 1);
+    if (bwd && teams * hpi * D > sums) sums = teams * hpi * D;
+  }
+  s.total = s.sums + sums;
+  return s;
+}
+
+// kNorm: PVL_NORM_NONE, _HEAD or _TOKEN; kBwd only with a norm.
+template <int V, int kM, int kNorm, bool kBwd, bool kHalf>
+__global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant__ RotaryParams p) {
   using T = typename Vec<V>::T;
+  constexpr int kP = Unit<V>::kP;
   constexpr bool kHead = kNorm == PVL_NORM_HEAD, kToken = kNorm == PVL_NORM_TOKEN, kAny = kHead || kToken;
-  constexpr int kSums = kBwd ? 2 : 1;      // sum x^2, and backward sum g w x
-  extern __shared__ float table[];         // reductions, and at the end the head norm's weight gradients
+  constexpr int kSums = kBwd ? 2 : 1;  // sum x^2, and backward sum g w x
+  extern __shared__ __align__(16) float smem[];
+  const SmemPlan plan = smem_plan(V, kM, kNorm, kBwd, p.R, p.D, p.units, p.hpi, p.team, p.teams, blockDim.x);
   const int tid = threadIdx.x;
-  const int slot = tid / p.team, lane = tid % p.team;
-  const int u = lane % p.units, hl = lane / p.units;
+  const int slot = tid / p.team, lane = tid - slot * p.team;
+  const int hl = lane / p.units, u = lane - hl * p.units;
   const bool on = slot < p.teams && hl < p.hpi;
   const bool turned = u < p.turned;
-  // features of the unit's two vectors
-  const int e0 = turned && p.half ? u * V : 2 * u * V;
-  const int e1 = turned && p.half ? u * V + p.R / 2 : e0 + V;
-  uint64_t turns[V];
-  uint32_t axis = 0;  // 2 bits a pair
-  if (turned) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const int pair = u * V + e;
-      turns[e] = __ldg(p.turns + pair);
-      axis |= (pair < p.section_1 ? 0u : pair < p.section_2 ? 1u : 2u) << (2 * e);
+  // features of the unit's two vectors: half a head's turned (or other) part apart
+  int e0, e1;
+  if (V == 1) {
+    e0 = turned && kHalf ? u : 2 * u;
+    e1 = turned && kHalf ? u + p.R / 2 : e0 + 1;
+  } else if (turned) {
+    e0 = u * V;
+    e1 = u * V + p.R / 2;
+  } else {
+    e0 = p.R + (u - p.turned) * V;
+    e1 = e0 + (p.D - p.R) / 2;
+  }
+  const int group = p.team < 32 ? p.team : 32, in_group = tid & (group - 1);
+  float4* const angles = reinterpret_cast<float4*>(smem) + tid / group * p.turned * kP;
+  float4* const weights = reinterpret_cast<float4*>(smem + plan.weights);
+  float* const sums_s = smem + plan.sums;
+
+  // the norm's weights, (a.x, a.y, b.x, b.y) of each pair of a unit: for the
+  // norm per token [kM][kP][team], per head [queries, keys][kP][units]
+  if (kAny) {
+    const int n = kToken ? kM * p.team : 2 * p.units;
+    for (int i = tid; i < n; i += blockDim.x) {
+      const int m = kToken ? i / p.team : i / p.units;
+      const int t = kToken ? i - m * p.team : i - m * p.units;
+      const int ul = kToken ? t % p.units : t;
+      const int h = kToken ? t / p.units + m * p.hpi : 0;
+      const bool key = kToken ? h >= p.H : m == 1;
+      const bool real = !kToken || (t / p.units < p.hpi && h < p.Ht);
+      const float* w = key ? p.w[1] : p.w[0];
+      if (kToken && w) w += (key ? h - p.H : h) * p.D;
+      int f0, f1;
+      if (V == 1) {
+        f0 = ul < p.turned && kHalf ? ul : 2 * ul;
+        f1 = ul < p.turned && kHalf ? ul + p.R / 2 : f0 + 1;
+      } else if (ul < p.turned) {
+        f0 = ul * V;
+        f1 = ul * V + p.R / 2;
+      } else {
+        f0 = p.R + (ul - p.turned) * V;
+        f1 = f0 + (p.D - p.R) / 2;
+      }
+      for (int q = 0; q < kP; ++q) {
+        float v[4];
+        for (int c = 0; c < 4; ++c) {
+          const int e = 2 * q + (c & 1);  // pair of the unit
+          v[c] = w && real && (V > 1 || !(c & 1)) ? __ldg(w + feature<V, kHalf>((c >> 1) * (V > 1 ? V : 1) + e, f0, f1)) : 1.0f;
+        }
+        weights[kToken ? (m * kP + q) * p.team + t : (m * kP + q) * p.units + t] = make_float4(v[0], v[1], v[2], v[3]);
+      }
     }
+    __syncthreads();
   }
-  float acc[kBwd && kAny ? (kToken ? kM : 2) : 1][2 * V];
-  if (kBwd && kAny) {
+  // weights of the unit in round m of head h
+  auto weight = [&](int m, int h, int q) {
+    return kToken ? weights[(m * kP + q) * p.team + lane] : weights[((h >= p.H) * kP + q) * p.units + u];
+  };
+
+  constexpr int kAcc = kBwd ? (kToken ? kM : 2) : 1;
+  Unit<V> acc[kAcc];
+  if (kBwd) {
 #pragma unroll
-    for (int i = 0; i < (kToken ? kM : 2); ++i)
+    for (int i = 0; i < kAcc; ++i)
 #pragma unroll
-      for (int e = 0; e < 2 * V; ++e) acc[kBwd && kAny ? i : 0][e] = 0.0f;
+      for (int q = 0; q < kP; ++q) acc[i].a[q] = acc[i].b[q] = make_float2(0.0f, 0.0f);
   }
-  // a head of the run of queries and keys: address of its vectors in a view
+  // the unit's first vector of head h (of the run of queries and keys) in a view
   auto at = [&](const pvl_heads (&v)[2], int h, uint32_t b, uint32_t l) {
     const bool key = h >= p.H;
     const int64_t off = b * (key ? v[1].stride_b : v[0].stride_b) + l * (key ? v[1].stride_l : v[0].stride_l) +
                         (key ? (h - p.H) * v[1].stride_h : h * v[0].stride_h);
     return static_cast<__nv_bfloat16*>(key ? v[1].data : v[0].data) + off;
   };
-  // the norm weight of the unit's feature e of head h
-  auto weight = [&](int h, int e) {
-    const bool key = h >= p.H;
-    const float* w = key ? p.w[1] : p.w[0];
-    if (w == nullptr) return 1.0f;
-    return __ldg(w + (kToken ? (key ? h - p.H : h) * p.D : 0) + (e < V ? e0 + e : e1 + e - V));
+  auto position = [&](uint32_t token, int a) {
+    return a < p.axes && token < p.tokens ? __ldg(p.positions + static_cast<size_t>(token) * p.axes + a) : 0;
   };
   const uint32_t step = gridDim.x * p.teams;
-  for (uint32_t base = blockIdx.x * p.teams; base < p.tokens; base += step) {
-    const uint32_t token = base + slot;
+  uint32_t token = blockIdx.x * p.teams + slot;
+  int32_t pos[3];
+#pragma unroll
+  for (int a = 0; a < 3; ++a) pos[a] = position(token, a);
+  int turn = 0;
+  for (uint32_t base = blockIdx.x * p.teams; base < p.tokens; base += step, token += step) {
     const bool live = on && token < p.tokens;
     const uint32_t b = token / p.L, l = token - b * p.L;
-    float c[V], s[V];
-    if (turned && live) {
-      int32_t pos[3] = {0, 0, 0};
-#pragma unroll
-      for (int a = 0; a < 3; ++a)
-        if (a < p.axes) pos[a] = __ldg(p.positions + static_cast<size_t>(token) * p.axes + a);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const uint32_t a = (axis >> (2 * e)) & 3u;
-        const int32_t n = a == 0 ? pos[0] : a == 1 ? pos[1] : pos[2];
-        const uint64_t frac = turns[e] * static_cast<uint64_t>(static_cast<int64_t>(n));  // mod 1 turn
-        const float angle = static_cast<float>(static_cast<int32_t>(frac >> 32)) * kRadians;
-        c[e] = __cosf(angle) * p.gain;
-        s[e] = __sinf(angle) * (kBwd ? -p.gain : p.gain);
-      }
-    }
     for (int h0 = hl; h0 - hl < p.Ht; h0 += kM * p.hpi) {
-    // the heads' loads first
-    T xa[kM], xb[kM], ga[kM], gb[kM];
-#pragma unroll
-    for (int m = 0; m < kM; ++m) {
-      const int h = h0 + m * p.hpi;
-      if (live && h < p.Ht) {
-        if (!kBwd || kAny) {
-          const __nv_bfloat16* row = at(p.x, h, b, l);
-          xa[m] = *reinterpret_cast<const T*>(row + e0);
-          xb[m] = *reinterpret_cast<const T*>(row + e1);
-        }
-        if (kBwd) {
-          const __nv_bfloat16* row = at(p.g, h, b, l);
-          ga[m] = *reinterpret_cast<const T*>(row + e0);
-          gb[m] = *reinterpret_cast<const T*>(row + e1);
-        }
-      }
-    }
-    // the norms' sums
-    float r[kM], mean[kM];  // 1 / rms; backward r^3 mean(g w x)
-    if (kAny) {
-      float part[kM][kSums];
+      // the heads' loads first
+      T x0[kM], x1[kM], g0[kM], g1[kM];
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
         const int h = h0 + m * p.hpi;
-        part[m][0] = 0.0f;
-        if (kBwd) part[m][kSums - 1] = 0.0f;
         if (live && h < p.Ht) {
-          float x[2 * V];
-          unpack<V>(xa[m], x);
-          unpack<V>(xb[m], x + V);
-          float q = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) q = fmaf(x[e], x[e], q);
-          part[m][0] = q;
+          const __nv_bfloat16* row = at(p.x, h, b, l);
+          x0[m] = *reinterpret_cast<const T*>(row + e0);
+          x1[m] = *reinterpret_cast<const T*>(row + e1);
           if (kBwd) {
-            float g[2 * V];
-            unpack<V>(ga[m], g);
-            unpack<V>(gb[m], g + V);
-            if (turned) rotate<V>(g, c, s, p.half);
-            q = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 2 * V; ++e) q = fmaf(g[e] * weight(h, e), x[e], q);
-            part[m][kSums - 1] = q;
+            row = at(p.g, h, b, l);
+            g0[m] = *reinterpret_cast<const T*>(row + e0);
+            g1[m] = *reinterpret_cast<const T*>(row + e1);
           }
         }
       }
-      const bool pow2 = (p.units & (p.units - 1)) == 0 && p.units <= 32;
-      if (kHead) {
-        if (pow2) {
-#pragma unroll
-          for (int m = 0; m < kM; ++m)
-#pragma unroll
-            for (int k = 0; k < kSums; ++k) part[m][k] = lane_sum(part[m][k], p.units);
-        } else {
-          const int n = blockDim.x;
-          __syncthreads();
-#pragma unroll
-          for (int m = 0; m < kM; ++m)
-#pragma unroll
-            for (int k = 0; k < kSums; ++k) table[(m * kSums + k) * n + tid] = part[m][k];
-          __syncthreads();
-#pragma unroll
-          for (int m = 0; m < kM; ++m)
-#pragma unroll
-            for (int k = 0; k < kSums; ++k) {
-              const float* q = table + (m * kSums + k) * n + tid - u;
-              float t = 0.0f;
-              if (on)
-                for (int i = 0; i < p.units; ++i) t += q[i];
-              part[m][k] = t;
-            }
+      if (h0 == hl) {
+        // the token's angles
+        __syncwarp();
+        for (int i = in_group; i < p.R / 2; i += group) {
+          int unit, e;
+          if constexpr (kHalf || V == 1) {
+            unit = i / V;
+            e = i % V;
+          } else {
+            const int side = i >= p.R / 4, j = i - side * (p.R / 4);
+            unit = j / (V / 2);
+            e = j % (V / 2) + side * (V / 2);
+          }
+          const int32_t n = i < p.section_1 ? pos[0] : i < p.section_2 ? pos[1] : pos[2];
+          const uint64_t frac = __ldg(p.turns + i) * static_cast<uint64_t>(static_cast<int64_t>(n));  // mod 1 turn
+          const float t = static_cast<float>(static_cast<int32_t>(frac >> 32)) * kRadians;
+          float* q = reinterpret_cast<float*>(angles + (e / 2) * p.turned + unit) + (e & 1);
+          q[0] = __cosf(t) * p.gain;
+          q[2] = __sinf(t) * p.sign;
         }
-      } else {
-        // queries and keys apart
-        float sum[2][kSums];
+        __syncwarp();
 #pragma unroll
-        for (int k = 0; k < kSums; ++k) sum[0][k] = sum[1][k] = 0.0f;
+        for (int a = 0; a < 3; ++a) pos[a] = position(token + step, a);
+      }
+      auto rotate = [&](Unit<V>& z) {
+#pragma unroll
+        for (int q = 0; q < kP; ++q) {
+          const float4 t = angles[q * p.turned + u];
+          const float2 c = make_float2(t.x, t.y), s = make_float2(t.z, t.w), a = z.a[q];
+          z.a[q] = ffma2(a, c, fmul2(z.b[q], make_float2(-s.x, -s.y)));
+          z.b[q] = ffma2(a, s, fmul2(z.b[q], c));
+        }
+      };
+      // the norms' sums; backward the gradient is turned back on the way
+      float r[kM], mean[kM];  // 1 / rms; backward -r^3 mean(g w x)
+      Unit<V> g[kBwd ? kM : 1];
+      if (kAny) {
+        float part[kM][kSums];
 #pragma unroll
         for (int m = 0; m < kM; ++m) {
-          const bool key = h0 + m * p.hpi >= p.H;
+          const int h = h0 + m * p.hpi;
+          part[m][0] = part[m][kSums - 1] = 0.0f;
+          if (live && h < p.Ht) {
+            Unit<V> x;
+            unpack<V, kHalf>(x0[m], x1[m], x);
+            float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-          for (int k = 0; k < kSums; ++k) {
-            sum[0][k] += key ? 0.0f : part[m][k];
-            sum[1][k] += key ? part[m][k] : 0.0f;
+            for (int q = 0; q < kP; ++q) s = ffma2(x.a[q], x.a[q], ffma2(x.b[q], x.b[q], s));
+            part[m][0] = s.x + s.y;
+            if (kBwd) {
+              Unit<V>& z = g[kBwd ? m : 0];
+              unpack<V, kHalf>(g0[m], g1[m], z);
+              if (turned) rotate(z);
+              s = make_float2(0.0f, 0.0f);
+#pragma unroll
+              for (int q = 0; q < kP; ++q) {
+                const float4 w = weight(m, h, q);
+                s = ffma2(fmul2(z.a[q], make_float2(w.x, w.y)), x.a[q], s);
+                s = ffma2(fmul2(z.b[q], make_float2(w.z, w.w)), x.b[q], s);
+              }
+              part[m][kSums - 1] = s.x + s.y;
+            }
           }
         }
+        if (kHead) {
+          if ((p.units & (p.units - 1)) == 0 && p.units <= 32) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+            for (int m = 0; m < kM; ++m)
 #pragma unroll
-          for (int k = 0; k < kSums; ++k) sum[i][k] = lane_sum(sum[i][k], p.team < 32 ? p.team : 32);
-        if (p.team > 32) {
-          const int warps = p.team / 32, first_warp = slot * warps;
-          __syncthreads();
-          if ((tid & 31) == 0) {
+              for (int k = 0; k < kSums; ++k) part[m][k] = lane_sum(part[m][k], p.units);
+          } else {
+            const int n = blockDim.x;
+            __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int m = 0; m < kM; ++m)
 #pragma unroll
-              for (int k = 0; k < kSums; ++k) table[(tid >> 5) * 2 * kSums + i * kSums + k] = sum[i][k];
+              for (int k = 0; k < kSums; ++k) sums_s[(m * kSums + k) * n + tid] = part[m][k];
+            __syncthreads();
+#pragma unroll
+            for (int m = 0; m < kM; ++m)
+#pragma unroll
+              for (int k = 0; k < kSums; ++k) {
+                const float* q = sums_s + (m * kSums + k) * n + tid - u;
+                float t = 0.0f;
+                if (on)
+                  for (int i = 0; i < p.units; ++i) t += q[i];
+                part[m][k] = t;
+              }
           }
-          __syncthreads();
+        } else {
+          // queries and keys apart
+          float sum[2][kSums];
+#pragma unroll
+          for (int k = 0; k < kSums; ++k) sum[0][k] = sum[1][k] = 0.0f;
+#pragma unroll
+          for (int m = 0; m < kM; ++m) {
+            const bool key = h0 + m * p.hpi >= p.H;
+#pragma unroll
+            for (int k = 0; k < kSums; ++k) {
+              sum[0][k] += key ? 0.0f : part[m][k];
+              sum[1][k] += key ? part[m][k] : 0.0f;
+            }
+          }
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int k = 0; k < kSums; ++k) sum[i][k] = 0.0f;
-          for (int w = 0; w < warps; ++w) {
+            for (int k = 0; k < kSums; ++k) sum[i][k] = lane_sum(sum[i][k], group);
+          if (p.team > 32) {
+            // one float4 a warp, in two tables by turns: one barrier a token
+            const int warps = p.team / 32;
+            float4* q = reinterpret_cast<float4*>(sums_s) + turn * (blockDim.x / 32);
+            if ((tid & 31) == 0) q[tid >> 5] = make_float4(sum[0][0], sum[1][0], sum[0][kSums - 1], sum[1][kSums - 1]);
+            __syncthreads();
+            q += slot * warps;
+            float4 t = q[0];
+            for (int w = 1; w < warps; ++w) {
+              const float4 v = q[w];
+              t.x += v.x;
+              t.y += v.y;
+              t.z += v.z;
+              t.w += v.w;
+            }
+            sum[0][0] = t.x;
+            sum[1][0] = t.y;
+            sum[0][kSums - 1] = t.z;
+            sum[1][kSums - 1] = t.w;
+            if (!kBwd) {
+              sum[0][0] = t.x;
+              sum[1][0] = t.y;
+            }
+            turn ^= 1;
+          }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+          for (int m = 0; m < kM; ++m) {
+            const bool key = h0 + m * p.hpi >= p.H;
 #pragma unroll
-              for (int k = 0; k < kSums; ++k) sum[i][k] += table[(first_warp + w) * 2 * kSums + i * kSums + k];
+            for (int k = 0; k < kSums; ++k) part[m][k] = key ? sum[1][k] : sum[0][k];
           }
         }
 #pragma unroll
         for (int m = 0; m < kM; ++m) {
           const bool key = h0 + m * p.hpi >= p.H;
-#pragma unroll
-          for (int k = 0; k < kSums; ++k) part[m][k] = key ? sum[1][k] : sum[0][k];
+          const float inv_n = __frcp_rn(static_cast<float>(kHead ? p.D : p.D * (key ? p.Ht - p.H : p.H)));
+          r[m] = rsqrtf(fmaf(part[m][0], inv_n, p.eps));
+          mean[m] = kBwd ? -r[m] * r[m] * r[m] * (part[m][kSums - 1] * inv_n) : 0.0f;
         }
       }
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
-        const bool key = h0 + m * p.hpi >= p.H;
-        const float n = static_cast<float>(kHead ? p.D : p.D * (key ? p.Ht - p.H : p.H));
-        r[m] = rsqrtf(part[m][0] / n + p.eps);
-        mean[m] = kBwd ? r[m] * r[m] * r[m] * (part[m][kSums - 1] / n) : 0.0f;
-      }
-    }
+        const int h = h0 + m * p.hpi;
+        if (live && h < p.Ht) {
+          Unit<V> z;
+          unpack<V, kHalf>(x0[m], x1[m], z);
+          if (kBwd) {
+            const Unit<V>& d = g[kBwd ? m : 0];
+            const float2 rr = make_float2(r[m], r[m]), mm = make_float2(mean[m], mean[m]);
 #pragma unroll
-    for (int m = 0; m < kM; ++m) {
-      const int h = h0 + m * p.hpi;
-      if (live && h < p.Ht) {
-        float z[2 * V];
-        if (!kBwd) {
-          unpack<V>(xa[m], z);
-          unpack<V>(xb[m], z + V);
-          if (kAny) {
-#pragma unroll
-            for (int e = 0; e < 2 * V; ++e) z[e] = z[e] * r[m] * weight(h, e);
-          }
-          if (turned) rotate<V>(z, c, s, p.half);
-        } else {
-          unpack<V>(ga[m], z);
-          unpack<V>(gb[m], z + V);
-          if (turned) rotate<V>(z, c, s, p.half);
-          if (kAny) {
-            float x[2 * V];
-            unpack<V>(xa[m], x);
-            unpack<V>(xb[m], x + V);
-#pragma unroll
-            for (int e = 0; e < 2 * V; ++e) {
-              const float d = z[e] * x[e] * r[m];  // g xh
+            for (int q = 0; q < kP; ++q) {
+              const float4 w = weight(m, h, q);
+              const float2 da = fmul2(fmul2(z.a[q], rr), d.a[q]), db = fmul2(fmul2(z.b[q], rr), d.b[q]);  // g xh
               if (kToken) {
-                acc[m][e] += d;
+                acc[kAcc > 1 ? m : 0].a[q] = fadd2(acc[kAcc > 1 ? m : 0].a[q], da);
+                acc[kAcc > 1 ? m : 0].b[q] = fadd2(acc[kAcc > 1 ? m : 0].b[q], db);
               } else {
-                acc[0][e] += h >= p.H ? 0.0f : d;
-                acc[1][e] += h >= p.H ? d : 0.0f;
+                const bool key = h >= p.H;
+                const float2 zero = make_float2(0.0f, 0.0f);
+                acc[0].a[q] = fadd2(acc[0].a[q], key ? zero : da);
+                acc[0].b[q] = fadd2(acc[0].b[q], key ? zero : db);
+                acc[kAcc - 1].a[q] = fadd2(acc[kAcc - 1].a[q], key ? da : zero);
+                acc[kAcc - 1].b[q] = fadd2(acc[kAcc - 1].b[q], key ? db : zero);
               }
-              z[e] = fmaf(z[e] * weight(h, e), r[m], -x[e] * mean[m]);
+              z.a[q] = ffma2(fmul2(d.a[q], make_float2(w.x, w.y)), rr, fmul2(z.a[q], mm));
+              z.b[q] = ffma2(fmul2(d.b[q], make_float2(w.z, w.w)), rr, fmul2(z.b[q], mm));
             }
+          } else {
+            if (kAny) {
+              const float2 rr = make_float2(r[m], r[m]);
+#pragma unroll
+              for (int q = 0; q < kP; ++q) {
+                const float4 w = weight(m, h, q);
+                z.a[q] = fmul2(fmul2(z.a[q], rr), make_float2(w.x, w.y));
+                z.b[q] = fmul2(fmul2(z.b[q], rr), make_float2(w.z, w.w));
+              }
+            }
+            if (turned) rotate(z);
           }
+          __nv_bfloat16* row = at(p.out, h, b, l);
+          T o0, o1;
+          pack<V, kHalf>(z, o0, o1);
+          *reinterpret_cast<T*>(row + e0) = o0;
+          *reinterpret_cast<T*>(row + e1) = o1;
         }
-        __nv_bfloat16* row = at(p.out, h, b, l);
-        *reinterpret_cast<T*>(row + e0) = pack<V>(z);
-        *reinterpret_cast<T*>(row + e1) = pack<V>(z + V);
       }
-    }
     }
   }
-  if (kBwd && kAny) {
+  if (kBwd) {
     if (p.part == nullptr) return;
+    constexpr int kValues = V > 1 ? 2 * V : 2;
+    // value k of a unit's sums
+    auto value = [](const Unit<V>& s, int k) {
+      const int e = k % (V > 1 ? V : 1), side = k / (V > 1 ? V : 1);
+      const float2 t = side ? s.b[e / 2] : s.a[e / 2];
+      return e & 1 ? t.y : t.x;
+    };
     if (kToken) {
       // one row of partial sums for each team
       if (on) {
@@ -369,28 +501,27 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const RotaryParams p)
           const int h = hl + m * p.hpi;
           if (h < p.Ht) {
 #pragma unroll
-            for (int e = 0; e < 2 * V; ++e)
-              row[static_cast<size_t>(h) * p.D + (e < V ? e0 + e : e1 + e - V)] = acc[kBwd && kAny ? m : 0][e];
+            for (int k = 0; k < kValues; ++k)
+              row[static_cast<size_t>(h) * p.D + feature<V, kHalf>(k, e0, e1)] = value(acc[kAcc > 1 ? m : 0], k);
           }
         }
       }
     } else {
       // the block's teams and heads added feature by feature, queries then keys
       float* row = p.part + static_cast<size_t>(blockIdx.x) * p.width;
-      const int per = p.hpi;  // threads of a team that own one feature
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int i = 0; i < 2; ++i) {
         __syncthreads();
         if (on) {
 #pragma unroll
-          for (int e = 0; e < 2 * V; ++e)
-            table[(slot * per + hl) * p.D + (e < V ? e0 + e : e1 + e - V)] = acc[kBwd && kAny ? k : 0][e];
+          for (int k = 0; k < kValues; ++k)
+            sums_s[(slot * p.hpi + hl) * p.D + feature<V, kHalf>(k, e0, e1)] = value(acc[i ? kAcc - 1 : 0], k);
         }
         __syncthreads();
         for (int d = tid; d < p.D; d += blockDim.x) {
           float t = 0.0f;
-          for (int i = 0; i < p.teams * per; ++i) t += table[i * p.D + d];
-          row[k * p.D + d] = t;
+          for (int j = 0; j < p.teams * p.hpi; ++j) t += sums_s[j * p.D + d];
+          row[i * p.D + d] = t;
         }
       }
     }
@@ -456,20 +587,61 @@ bool team_of(int V, int kM, int Ht, int D, bool whole, Shape* s) {
   return true;
 }
 
-template <int V, int kM, bool kBwd>
-pvl_status launch_norm(const RotaryParams& p, int norm, int threads, size_t smem, int grid_limit, int* grid_out,
-                       cudaStream_t s, const char* who) {
-  const void* fn = norm == PVL_NORM_NONE ? reinterpret_cast<const void*>(&rotary_kernel<V, kM, PVL_NORM_NONE, kBwd>)
-                                         : reinterpret_cast<const void*>(&rotary_kernel<V, kM, PVL_NORM_HEAD, kBwd>);
-  if constexpr (V < 8 || kM <= 2)
-    if (norm == PVL_NORM_TOKEN) fn = reinterpret_cast<const void*>(&rotary_kernel<V, kM, PVL_NORM_TOKEN, kBwd>);
+struct Kernel {
+  const void* fn;
+  int V, kM, norm;
+  bool bwd, half;
+};
+
+template <int V, int kM, int kNorm, bool kBwd>
+constexpr Kernel kernel_of(bool half) {
+  return {half ? reinterpret_cast<const void*>(&rotary_kernel<V, kM, kNorm, kBwd, true>)
+               : reinterpret_cast<const void*>(&rotary_kernel<V, kM, kNorm, kBwd, false>),
+          V, kM, kNorm, kBwd, half};
+}
+
+// The kernels that exist (shape_of picks among the same).
+const void* find_kernel(const Shape& s, int norm, bool bwd, bool half) {
+#define PVL_ROTARY_KERNEL(VV, MM, NN, BB) \
+  if (s.V == VV && s.kM == MM && norm == NN && bwd == BB) return kernel_of<VV, MM, NN, BB>(half).fn
+  PVL_ROTARY_KERNEL(8, 1, PVL_NORM_NONE, false);
+  PVL_ROTARY_KERNEL(8, 3, PVL_NORM_NONE, false);
+  PVL_ROTARY_KERNEL(4, 4, PVL_NORM_NONE, false);
+  PVL_ROTARY_KERNEL(1, 16, PVL_NORM_NONE, false);
+  PVL_ROTARY_KERNEL(8, 1, PVL_NORM_HEAD, false);
+  PVL_ROTARY_KERNEL(8, 3, PVL_NORM_HEAD, false);
+  PVL_ROTARY_KERNEL(4, 4, PVL_NORM_HEAD, false);
+  PVL_ROTARY_KERNEL(1, 16, PVL_NORM_HEAD, false);
+  PVL_ROTARY_KERNEL(8, 1, PVL_NORM_HEAD, true);
+  PVL_ROTARY_KERNEL(8, 2, PVL_NORM_HEAD, true);
+  PVL_ROTARY_KERNEL(4, 4, PVL_NORM_HEAD, true);
+  PVL_ROTARY_KERNEL(1, 16, PVL_NORM_HEAD, true);
+  PVL_ROTARY_KERNEL(8, 1, PVL_NORM_TOKEN, false);
+  PVL_ROTARY_KERNEL(8, 2, PVL_NORM_TOKEN, false);
+  PVL_ROTARY_KERNEL(8, 6, PVL_NORM_TOKEN, false);
+  PVL_ROTARY_KERNEL(4, 4, PVL_NORM_TOKEN, false);
+  PVL_ROTARY_KERNEL(1, 16, PVL_NORM_TOKEN, false);
+  PVL_ROTARY_KERNEL(8, 1, PVL_NORM_TOKEN, true);
+  PVL_ROTARY_KERNEL(8, 2, PVL_NORM_TOKEN, true);
+  PVL_ROTARY_KERNEL(4, 4, PVL_NORM_TOKEN, true);
+  PVL_ROTARY_KERNEL(1, 16, PVL_NORM_TOKEN, true);
+#undef PVL_ROTARY_KERNEL
+  return nullptr;
+}
+
+pvl_status launch(const RotaryParams& p, const Shape& sh, int norm, bool bwd, bool half, int grid_limit, int* grid_out,
+                  cudaStream_t s, const char* who) {
+  const void* fn = find_kernel(sh, norm, bwd, half);
+  if (!fn) return fail(PVL_ERR_UNSUPPORTED, "%s: no kernel for this shape", who);
+  const size_t smem =
+      sizeof(float) * smem_plan(sh.V, sh.kM, norm, bwd, p.R, p.D, sh.units, sh.hpi, sh.team, sh.teams, sh.threads).total;
   pvl_status st = PVL_OK;
   if (smem > 48 * 1024) {
     st = check_cuda(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)), who);
     if (st != PVL_OK) return st;
   }
   int occ = 0;
-  st = check_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, threads, smem), who);
+  st = check_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, sh.threads, smem), who);
   if (st != PVL_OK) return st;
   const int sms = sm_count();
   if (sms <= 0 || occ <= 0) return fail(PVL_ERR_CUDA, "%s: no usable CUDA device", who);
@@ -480,32 +652,7 @@ pvl_status launch_norm(const RotaryParams& p, int norm, int threads, size_t smem
   *grid_out = static_cast<int>(grid);
   RotaryParams q = p;
   void* args[] = {&q};
-  st = check_cuda(cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(threads), args, smem, s), who);
-  return st;
-}
-
-template <bool kBwd>
-pvl_status launch(const RotaryParams& p, const Shape& sh, int norm, int grid_limit, int* grid_out, cudaStream_t s,
-                  const char* who) {
-  // reductions: a float for each thread, head and sum; the weight gradients of
-  // the norm per head: one row of D for each thread group that shares a unit
-  size_t smem = 0;
-  if (norm == PVL_NORM_TOKEN) smem = 32 * 4 * sizeof(float);
-  if (norm == PVL_NORM_HEAD) {
-    smem = static_cast<size_t>(sh.threads) * sh.kM * (kBwd ? 2 : 1) * sizeof(float);
-    const size_t rows = static_cast<size_t>(sh.teams) * sh.hpi * p.D * sizeof(float);
-    if (kBwd && rows > smem) smem = rows;
-  }
-#define PVL_ROTARY_CASE(VV, MM) \
-  if (sh.V == VV && sh.kM == MM) return launch_norm<VV, MM, kBwd>(p, norm, sh.threads, smem, grid_limit, grid_out, s, who)
-  PVL_ROTARY_CASE(8, 1);
-  PVL_ROTARY_CASE(8, 2);
-  PVL_ROTARY_CASE(8, 3);
-  PVL_ROTARY_CASE(8, 4);
-  PVL_ROTARY_CASE(4, 4);
-  PVL_ROTARY_CASE(1, 16);
-#undef PVL_ROTARY_CASE
-  return fail(PVL_ERR_UNSUPPORTED, "%s: no kernel for this shape", who);
+  return check_cuda(cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(sh.threads), args, smem, s), who);
 }
 
 // Widest vector that divides the head, its rotated part, every stride and
@@ -523,28 +670,17 @@ int widest(const pvl_rotary* a, const pvl_heads* const* views, int n) {
 }
 
 // Heads a thread at a time.  One while the tokens leave SMs without a block
-// (latency counts: most threads, fewest dependent steps); else the count that
-// leaves the fewest threads without a head, the larger one where equal.
-bool shape_of(const pvl_rotary* a, int V, Shape* s) {
+// (latency counts: most threads, fewest dependent steps); else the largest
+// count that a kernel exists for whose registers hold it.
+bool shape_of(const pvl_rotary* a, int V, bool bwd, Shape* s) {
   const int Ht = a->H + a->Hk;
   const bool whole = a->norm == PVL_NORM_TOKEN;
   if (V != 8) return team_of(V, V == 4 ? 4 : 16, Ht, a->D, whole, s);
   const long long tokens = static_cast<long long>(a->B) * a->L;
   if (tokens <= 2 * 152 && team_of(8, 1, Ht, a->D, whole, s)) return true;
-  bool found = false;
-  double best = 0.0;
-  for (int m = whole ? 2 : 4; m >= 1; --m) {
-    Shape t{};
-    if (!team_of(8, m, Ht, a->D, whole, &t)) continue;
-    const int rounds = (Ht + t.hpi * m - 1) / (t.hpi * m);
-    const double used = static_cast<double>(Ht) * t.units / (static_cast<double>(t.team) * m * rounds);
-    if (!found || used > best + 1e-9) {
-      best = used;
-      *s = t;
-    }
-    found = true;
-  }
-  return found;
+  if (!whole) return team_of(8, bwd ? 2 : 3, Ht, a->D, whole, s);
+  if (!bwd && team_of(8, 6, Ht, a->D, whole, s)) return true;
+  return team_of(8, 2, Ht, a->D, whole, s);
 }
 
 pvl_status check_views(const char* who, const pvl_rotary* a, const pvl_heads* v, int which, const char* name) {
@@ -594,12 +730,11 @@ pvl_status common(const char* who, const pvl_rotary* a, RotaryParams& p) {
   p.Ht = a->H + a->Hk;
   p.D = a->D;
   p.R = a->R;
-  p.half = a->layout == PVL_ROTARY_HALF;
   p.axes = a->axes;
   p.section_1 = a->section_1;
   p.section_2 = a->section_2;
   p.tokens = static_cast<uint32_t>(static_cast<long long>(a->B) * a->L);
-  p.gain = a->gain;
+  p.gain = p.sign = a->gain;
   p.eps = a->eps;
   return PVL_OK;
 }
@@ -630,7 +765,7 @@ extern "C" pvl_status pack_rotary_fwd(const pvl_rotary* a, const pvl_heads* q, c
   if (st != PVL_OK) return st;
   const pvl_heads* views[] = {q, a->Hk ? k : nullptr, q_out, a->Hk ? k_out : nullptr};
   Shape s{};
-  if (!shape_of(a, widest(a, views, 4), &s))
+  if (!shape_of(a, widest(a, views, 4), false, &s))
     return fail(PVL_ERR_UNSUPPORTED, "%s: a token of %d heads of %d features does not fit a block", who, p.Ht, p.D);
   fill(p, a, s);
   p.x[0] = *q;
@@ -640,7 +775,8 @@ extern "C" pvl_status pack_rotary_fwd(const pvl_rotary* a, const pvl_heads* q, c
     p.out[1] = *k_out;
   }
   int grid = 0;
-  return launch<false>(p, s, a->norm, 1 << 30, &grid, reinterpret_cast<cudaStream_t>(stream), who);
+  return launch(p, s, a->norm, false, a->layout == PVL_ROTARY_HALF, 1 << 30, &grid,
+                reinterpret_cast<cudaStream_t>(stream), who);
 }
 
 extern "C" size_t pack_rotary_bwd_ws_bytes(const pvl_rotary* a) {
@@ -679,15 +815,16 @@ extern "C" pvl_status pack_rotary_bwd(const pvl_rotary* a, const pvl_heads* dq_o
   const pvl_heads* views[] = {dq_out, a->Hk ? dk_out : nullptr, dq, a->Hk ? dk : nullptr, norm ? q : nullptr,
                               norm && a->Hk ? k : nullptr};
   Shape s{};
-  if (!shape_of(a, widest(a, views, 6), &s))
+  if (!shape_of(a, widest(a, views, 6), norm, &s))
     return fail(PVL_ERR_UNSUPPORTED, "%s: a token of %d heads of %d features does not fit a block", who, p.Ht, p.D);
   fill(p, a, s);
-  p.g[0] = *dq_out;
+  p.sign = -a->gain;  // turned back
   p.out[0] = *dq;
-  if (a->Hk) {
-    p.g[1] = *dk_out;
-    p.out[1] = *dk;
-  }
+  if (a->Hk) p.out[1] = *dk;
+  // without a norm the gradient is rotated in the input's place
+  pvl_heads* up = norm ? p.g : p.x;
+  up[0] = *dq_out;
+  if (a->Hk) up[1] = *dk_out;
   if (norm) {
     p.x[0] = *q;
     if (a->Hk) p.x[1] = *k;
@@ -705,7 +842,7 @@ extern "C" pvl_status pack_rotary_bwd(const pvl_rotary* a, const pvl_heads* dq_o
   }
   int grid = 0;
   cudaStream_t stm = reinterpret_cast<cudaStream_t>(stream);
-  st = launch<true>(p, s, a->norm, limit, &grid, stm, who);
+  st = launch(p, s, a->norm, norm, a->layout == PVL_ROTARY_HALF, limit, &grid, stm, who);
   if (st != PVL_OK || !weights) return st;
   const int q_width = a->norm == PVL_NORM_TOKEN ? a->H * a->D : a->D;
   const int rows = grid * (a->norm == PVL_NORM_TOKEN ? p.teams : 1);
