@@ -33,6 +33,8 @@
 //     them.  Its sums cross warps only where a team has several: one barrier.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "pvl_device.cuh"
 
 namespace pvl {
@@ -43,19 +45,26 @@ constexpr int kMaxD = 256;
 constexpr int kMaxPartials = 1216;  // rows of partial weight gradients at most
 constexpr float kRadians = 1.4629180792671596e-9f;  // 2 pi / 2^32
 
+// A tensor's address and strides in bytes.
+struct View {
+  char* data;
+  int64_t b, l;
+  int32_t h;
+};
+
 struct RotaryParams {
-  pvl_heads x[2];    // q, k: what is rotated (backward of a norm: the forward's input)
-  pvl_heads g[2];    // backward of a norm: gradients of the outputs
-  pvl_heads out[2];  // rotated, or dq, dk
+  View x[2];    // q, k: what is rotated (backward of a norm: the forward's input)
+  View g[2];    // backward of a norm: gradients of the outputs
+  View out[2];  // rotated, or dq, dk
   const uint64_t* turns;
   const int32_t* positions;
   const float* w[2];
   float* part;       // backward: [rows][width] partial weight gradients, null: none
-  uint32_t L, tokens;  // tokens = B * L
+  int L, rows;       // tokens of a row; rows (one where the strides let all tokens be one row)
   int H, Ht, D, R;
   int axes, section_1, section_2;
   int units;         // units of a head, D / (2 V)
-  int turned;        // units of a head that are rotated, R / (2 V)
+  int turned;        // units of a head that are rotated: all, or in the half layout R / (2 V)
   int hpi;           // heads a team takes at once
   int team, teams;   // threads of a team, teams of a block
   int width;         // columns of part
@@ -72,6 +81,10 @@ struct Vec<8> {
 template <>
 struct Vec<4> {
   using T = uint2;
+};
+template <>
+struct Vec<2> {
+  using T = uint32_t;
 };
 template <>
 struct Vec<1> {
@@ -102,9 +115,10 @@ __device__ __forceinline__ void unpack(const typename Vec<V>::T& u0, const typen
         z.a[i] = make_float2(lo(w0[i]), hi(w0[i]));
         z.b[i] = make_float2(lo(w1[i]), hi(w1[i]));
       } else {
-        const uint32_t* w = i < V / 4 ? w0 + 2 * i : w1 + 2 * i - V / 2;
-        z.a[i] = make_float2(lo(w[0]), lo(w[1]));
-        z.b[i] = make_float2(hi(w[0]), hi(w[1]));
+        const uint32_t v0 = V == 2 ? w0[0] : i < V / 4 ? w0[2 * i] : w1[2 * i - V / 2];
+        const uint32_t v1 = V == 2 ? w1[0] : i < V / 4 ? w0[2 * i + 1] : w1[2 * i + 1 - V / 2];
+        z.a[i] = make_float2(lo(v0), lo(v1));
+        z.b[i] = make_float2(hi(v0), hi(v1));
       }
     }
   }
@@ -123,9 +137,8 @@ __device__ __forceinline__ void pack(const Unit<V>& z, typename Vec<V>::T& u0, t
         w0[i] = pack_bf16x2(z.a[i].x, z.a[i].y);
         w1[i] = pack_bf16x2(z.b[i].x, z.b[i].y);
       } else {
-        uint32_t* w = i < V / 4 ? w0 + 2 * i : w1 + 2 * i - V / 2;
-        w[0] = pack_bf16x2(z.a[i].x, z.b[i].x);
-        w[1] = pack_bf16x2(z.a[i].y, z.b[i].y);
+        (V == 2 ? w0[0] : i < V / 4 ? w0[2 * i] : w1[2 * i - V / 2]) = pack_bf16x2(z.a[i].x, z.b[i].x);
+        (V == 2 ? w1[0] : i < V / 4 ? w0[2 * i + 1] : w1[2 * i + 1 - V / 2]) = pack_bf16x2(z.a[i].y, z.b[i].y);
       }
     }
   }
@@ -140,6 +153,24 @@ __device__ __forceinline__ int feature(int k, int e0, int e1) {
   return e < V / 2 ? e0 + 2 * e + side : e1 + 2 * e - V + side;
 }
 
+// Offsets of the two vectors of unit u.  Interleaved pairs lie inside a
+// vector, so all units are the same: R may end anywhere (the pairs past it
+// get angle 0 and no gain).  In the half layout the units past the rotated
+// part are their own.
+template <int V, bool kHalf>
+__device__ __forceinline__ void vectors_of(const RotaryParams& p, int u, int* e0, int* e1) {
+  if (!kHalf) {
+    *e0 = V > 1 ? u * V : 2 * u;
+    *e1 = V > 1 ? u * V + p.D / 2 : 2 * u + 1;
+  } else if (u < p.turned) {
+    *e0 = u * V;
+    *e1 = u * V + p.R / 2;
+  } else {
+    *e0 = p.R + (u - p.turned) * V;
+    *e1 = *e0 + (p.D - p.R) / 2;
+  }
+}
+
 // Sum over the `n` threads of an aligned power-of-two lane group.
 __device__ __forceinline__ float lane_sum(float v, int n) {
   for (int o = 1; o < n; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -152,13 +183,13 @@ __device__ __forceinline__ float lane_sum(float v, int n) {
 struct SmemPlan {
   int angles, weights, sums, total;  // offsets
 };
-__host__ __device__ inline SmemPlan smem_plan(int V, int kM, int norm, bool bwd, int R, int D, int units, int hpi,
+__host__ __device__ inline SmemPlan smem_plan(int V, int kM, int norm, bool bwd, int turned, int D, int units, int hpi,
                                               int team, int teams, int threads) {
   SmemPlan s{};
   const int group = team < 32 ? team : 32;
   const int per = 2 * (V > 1 ? V : 2);  // floats of a unit's angles (V = 1: a pair and an unused one)
   s.angles = 0;
-  s.weights = threads / group * (R / (2 * V)) * per;
+  s.weights = threads / group * turned * per;
   const int unit_floats = 2 * (V > 1 ? V : 2);
   const int weights = norm == PVL_NORM_TOKEN ? kM * team * unit_floats : norm == PVL_NORM_HEAD ? 2 * units * unit_floats : 0;
   s.sums = s.weights + weights;
@@ -181,24 +212,14 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
   constexpr bool kHead = kNorm == PVL_NORM_HEAD, kToken = kNorm == PVL_NORM_TOKEN, kAny = kHead || kToken;
   constexpr int kSums = kBwd ? 2 : 1;  // sum x^2, and backward sum g w x
   extern __shared__ __align__(16) float smem[];
-  const SmemPlan plan = smem_plan(V, kM, kNorm, kBwd, p.R, p.D, p.units, p.hpi, p.team, p.teams, blockDim.x);
+  const SmemPlan plan = smem_plan(V, kM, kNorm, kBwd, p.turned, p.D, p.units, p.hpi, p.team, p.teams, blockDim.x);
   const int tid = threadIdx.x;
   const int slot = tid / p.team, lane = tid - slot * p.team;
   const int hl = lane / p.units, u = lane - hl * p.units;
   const bool on = slot < p.teams && hl < p.hpi;
   const bool turned = u < p.turned;
-  // features of the unit's two vectors: half a head's turned (or other) part apart
-  int e0, e1;
-  if (V == 1) {
-    e0 = turned && kHalf ? u : 2 * u;
-    e1 = turned && kHalf ? u + p.R / 2 : e0 + 1;
-  } else if (turned) {
-    e0 = u * V;
-    e1 = u * V + p.R / 2;
-  } else {
-    e0 = p.R + (u - p.turned) * V;
-    e1 = e0 + (p.D - p.R) / 2;
-  }
+  int e0, e1;  // features of the unit's two vectors
+  vectors_of<V, kHalf>(p, u, &e0, &e1);
   const int group = p.team < 32 ? p.team : 32, in_group = tid & (group - 1);
   float4* const angles = reinterpret_cast<float4*>(smem) + tid / group * p.turned * kP;
   float4* const weights = reinterpret_cast<float4*>(smem + plan.weights);
@@ -218,16 +239,7 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
       const float* w = key ? p.w[1] : p.w[0];
       if (kToken && w) w += (key ? h - p.H : h) * p.D;
       int f0, f1;
-      if (V == 1) {
-        f0 = ul < p.turned && kHalf ? ul : 2 * ul;
-        f1 = ul < p.turned && kHalf ? ul + p.R / 2 : f0 + 1;
-      } else if (ul < p.turned) {
-        f0 = ul * V;
-        f1 = ul * V + p.R / 2;
-      } else {
-        f0 = p.R + (ul - p.turned) * V;
-        f1 = f0 + (p.D - p.R) / 2;
-      }
+      vectors_of<V, kHalf>(p, ul, &f0, &f1);
       for (int q = 0; q < kP; ++q) {
         float v[4];
         for (int c = 0; c < 4; ++c) {
@@ -252,65 +264,80 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
 #pragma unroll
       for (int q = 0; q < kP; ++q) acc[i].a[q] = acc[i].b[q] = make_float2(0.0f, 0.0f);
   }
-  // the unit's first vector of head h (of the run of queries and keys) in a view
-  auto at = [&](const pvl_heads (&v)[2], int h, uint32_t b, uint32_t l) {
-    const bool key = h >= p.H;
-    const int64_t off = b * (key ? v[1].stride_b : v[0].stride_b) + l * (key ? v[1].stride_l : v[0].stride_l) +
-                        (key ? (h - p.H) * v[1].stride_h : h * v[0].stride_h);
-    return static_cast<__nv_bfloat16*>(key ? v[1].data : v[0].data) + off;
+  int turn = 0;
+  for (int row = blockIdx.y; row < p.rows; row += gridDim.y) {
+  const int32_t* const positions = p.positions + static_cast<size_t>(row) * p.L * p.axes;
+  auto position = [&](int l, int a) {
+    return a < p.axes && l < p.L ? __ldg(positions + static_cast<size_t>(l) * p.axes + a) : 0;
   };
-  auto position = [&](uint32_t token, int a) {
-    return a < p.axes && token < p.tokens ? __ldg(p.positions + static_cast<size_t>(token) * p.axes + a) : 0;
-  };
-  const uint32_t step = gridDim.x * p.teams;
-  uint32_t token = blockIdx.x * p.teams + slot;
+  const int step = gridDim.x * p.teams;
+  int l = blockIdx.x * p.teams + slot;
   int32_t pos[3];
 #pragma unroll
-  for (int a = 0; a < 3; ++a) pos[a] = position(token, a);
-  int turn = 0;
-  for (uint32_t base = blockIdx.x * p.teams; base < p.tokens; base += step, token += step) {
-    const bool live = on && token < p.tokens;
-    const uint32_t b = token / p.L, l = token - b * p.L;
+  for (int a = 0; a < 3; ++a) pos[a] = position(l, a);
+  for (int base = blockIdx.x * p.teams; base < p.L; base += step, l += step) {
+    // a thread without a token or a head works on the last one of each, and
+    // neither adds to sums nor writes
+    const bool live = on && l < p.L;
+    const int lc = l < p.L ? l : p.L - 1;
+    // the unit's first vector in head 0 of queries and keys, less H heads
+    auto heads_at = [&](const View (&v)[2], char* (&to)[2]) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        to[i] = v[i].data + row * v[i].b + lc * v[i].l + 2 * e0 - (i ? static_cast<int64_t>(p.H) * v[1].h : 0);
+    };
+    auto head_at = [&](const View (&v)[2], char* const (&to)[2], int h) {
+      const bool key = h >= p.H;
+      return (key ? to[1] : to[0]) + static_cast<int64_t>(h) * (key ? v[1].h : v[0].h);
+    };
+    const int apart = 2 * (e1 - e0);
+    char *xp[2], *gp[2], *op[2];
+    heads_at(p.x, xp);
+    if (kBwd) heads_at(p.g, gp);
+    heads_at(p.out, op);
     for (int h0 = hl; h0 - hl < p.Ht; h0 += kM * p.hpi) {
       // the heads' loads first
       T x0[kM], x1[kM], g0[kM], g1[kM];
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
-        const int h = h0 + m * p.hpi;
-        if (live && h < p.Ht) {
-          const __nv_bfloat16* row = at(p.x, h, b, l);
-          x0[m] = *reinterpret_cast<const T*>(row + e0);
-          x1[m] = *reinterpret_cast<const T*>(row + e1);
-          if (kBwd) {
-            row = at(p.g, h, b, l);
-            g0[m] = *reinterpret_cast<const T*>(row + e0);
-            g1[m] = *reinterpret_cast<const T*>(row + e1);
-          }
+        const int h = min(h0 + m * p.hpi, p.Ht - 1);
+        const char* q = head_at(p.x, xp, h);
+        x0[m] = *reinterpret_cast<const T*>(q);
+        x1[m] = *reinterpret_cast<const T*>(q + apart);
+        if (kBwd) {
+          q = head_at(p.g, gp, h);
+          g0[m] = *reinterpret_cast<const T*>(q);
+          g1[m] = *reinterpret_cast<const T*>(q + apart);
         }
       }
       if (h0 == hl) {
         // the token's angles
         __syncwarp();
-        for (int i = in_group; i < p.R / 2; i += group) {
+        for (int i = in_group; i < p.turned * V; i += group) {
           int unit, e;
           if constexpr (kHalf || V == 1) {
             unit = i / V;
             e = i % V;
           } else {
-            const int side = i >= p.R / 4, j = i - side * (p.R / 4);
+            const int side = i >= p.D / 4, j = i - side * (p.D / 4);
             unit = j / (V / 2);
             e = j % (V / 2) + side * (V / 2);
           }
-          const int32_t n = i < p.section_1 ? pos[0] : i < p.section_2 ? pos[1] : pos[2];
-          const uint64_t frac = __ldg(p.turns + i) * static_cast<uint64_t>(static_cast<int64_t>(n));  // mod 1 turn
-          const float t = static_cast<float>(static_cast<int32_t>(frac >> 32)) * kRadians;
           float* q = reinterpret_cast<float*>(angles + (e / 2) * p.turned + unit) + (e & 1);
-          q[0] = __cosf(t) * p.gain;
-          q[2] = __sinf(t) * p.sign;
+          if (kHalf || i < p.R / 2) {
+            const int32_t n = i < p.section_1 ? pos[0] : i < p.section_2 ? pos[1] : pos[2];
+            const uint64_t frac = __ldg(p.turns + i) * static_cast<uint64_t>(static_cast<int64_t>(n));  // mod 1 turn
+            const float t = static_cast<float>(static_cast<int32_t>(frac >> 32)) * kRadians;
+            q[0] = __cosf(t) * p.gain;
+            q[2] = __sinf(t) * p.sign;
+          } else {
+            q[0] = 1.0f;
+            q[2] = 0.0f;
+          }
         }
         __syncwarp();
 #pragma unroll
-        for (int a = 0; a < 3; ++a) pos[a] = position(token + step, a);
+        for (int a = 0; a < 3; ++a) pos[a] = position(l + step, a);
       }
       auto rotate = [&](Unit<V>& z) {
 #pragma unroll
@@ -329,27 +356,25 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
 #pragma unroll
         for (int m = 0; m < kM; ++m) {
           const int h = h0 + m * p.hpi;
-          part[m][0] = part[m][kSums - 1] = 0.0f;
-          if (live && h < p.Ht) {
-            Unit<V> x;
-            unpack<V, kHalf>(x0[m], x1[m], x);
-            float2 s = make_float2(0.0f, 0.0f);
+          const bool real = live && h < p.Ht;
+          Unit<V> x;
+          unpack<V, kHalf>(x0[m], x1[m], x);
+          float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int q = 0; q < kP; ++q) s = ffma2(x.a[q], x.a[q], ffma2(x.b[q], x.b[q], s));
-            part[m][0] = s.x + s.y;
-            if (kBwd) {
-              Unit<V>& z = g[kBwd ? m : 0];
-              unpack<V, kHalf>(g0[m], g1[m], z);
-              if (turned) rotate(z);
-              s = make_float2(0.0f, 0.0f);
+          for (int q = 0; q < kP; ++q) s = ffma2(x.a[q], x.a[q], ffma2(x.b[q], x.b[q], s));
+          part[m][0] = real ? s.x + s.y : 0.0f;
+          if (kBwd) {
+            Unit<V>& z = g[kBwd ? m : 0];
+            unpack<V, kHalf>(g0[m], g1[m], z);
+            if (turned) rotate(z);
+            s = make_float2(0.0f, 0.0f);
 #pragma unroll
-              for (int q = 0; q < kP; ++q) {
-                const float4 w = weight(m, h, q);
-                s = ffma2(fmul2(z.a[q], make_float2(w.x, w.y)), x.a[q], s);
-                s = ffma2(fmul2(z.b[q], make_float2(w.z, w.w)), x.b[q], s);
-              }
-              part[m][kSums - 1] = s.x + s.y;
+            for (int q = 0; q < kP; ++q) {
+              const float4 w = weight(m, h, q);
+              s = ffma2(fmul2(z.a[q], make_float2(w.x, w.y)), x.a[q], s);
+              s = ffma2(fmul2(z.b[q], make_float2(w.z, w.w)), x.b[q], s);
             }
+            part[m][kSums - 1] = real ? s.x + s.y : 0.0f;
           }
         }
         if (kHead) {
@@ -438,7 +463,8 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
         const int h = h0 + m * p.hpi;
-        if (live && h < p.Ht) {
+        const bool real = live && h < p.Ht;
+        {
           Unit<V> z;
           unpack<V, kHalf>(x0[m], x1[m], z);
           if (kBwd) {
@@ -447,13 +473,15 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
 #pragma unroll
             for (int q = 0; q < kP; ++q) {
               const float4 w = weight(m, h, q);
-              const float2 da = fmul2(fmul2(z.a[q], rr), d.a[q]), db = fmul2(fmul2(z.b[q], rr), d.b[q]);  // g xh
+              const float2 zero = make_float2(0.0f, 0.0f);
+              float2 da = fmul2(fmul2(z.a[q], rr), d.a[q]), db = fmul2(fmul2(z.b[q], rr), d.b[q]);  // g xh
+              da = real ? da : zero;
+              db = real ? db : zero;
               if (kToken) {
                 acc[kAcc > 1 ? m : 0].a[q] = fadd2(acc[kAcc > 1 ? m : 0].a[q], da);
                 acc[kAcc > 1 ? m : 0].b[q] = fadd2(acc[kAcc > 1 ? m : 0].b[q], db);
               } else {
                 const bool key = h >= p.H;
-                const float2 zero = make_float2(0.0f, 0.0f);
                 acc[0].a[q] = fadd2(acc[0].a[q], key ? zero : da);
                 acc[0].b[q] = fadd2(acc[0].b[q], key ? zero : db);
                 acc[kAcc - 1].a[q] = fadd2(acc[kAcc - 1].a[q], key ? da : zero);
@@ -474,14 +502,17 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
             }
             if (turned) rotate(z);
           }
-          __nv_bfloat16* row = at(p.out, h, b, l);
           T o0, o1;
           pack<V, kHalf>(z, o0, o1);
-          *reinterpret_cast<T*>(row + e0) = o0;
-          *reinterpret_cast<T*>(row + e1) = o1;
+          if (real) {
+            char* q = head_at(p.out, op, h);
+            *reinterpret_cast<T*>(q) = o0;
+            *reinterpret_cast<T*>(q + apart) = o1;
+          }
         }
       }
     }
+  }
   }
   if (kBwd) {
     if (p.part == nullptr) return;
@@ -495,7 +526,7 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
     if (kToken) {
       // one row of partial sums for each team
       if (on) {
-        float* row = p.part + (static_cast<size_t>(blockIdx.x) * p.teams + slot) * p.width;
+        float* row = p.part + (static_cast<size_t>(blockIdx.y * gridDim.x + blockIdx.x) * p.teams + slot) * p.width;
 #pragma unroll
         for (int m = 0; m < kM; ++m) {
           const int h = hl + m * p.hpi;
@@ -508,7 +539,7 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
       }
     } else {
       // the block's teams and heads added feature by feature, queries then keys
-      float* row = p.part + static_cast<size_t>(blockIdx.x) * p.width;
+      float* row = p.part + static_cast<size_t>(blockIdx.y * gridDim.x + blockIdx.x) * p.width;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         __syncthreads();
@@ -607,23 +638,31 @@ const void* find_kernel(const Shape& s, int norm, bool bwd, bool half) {
   PVL_ROTARY_KERNEL(8, 1, PVL_NORM_NONE, false);
   PVL_ROTARY_KERNEL(8, 3, PVL_NORM_NONE, false);
   PVL_ROTARY_KERNEL(4, 4, PVL_NORM_NONE, false);
-  PVL_ROTARY_KERNEL(1, 16, PVL_NORM_NONE, false);
+  PVL_ROTARY_KERNEL(2, 8, PVL_NORM_NONE, false);
+  PVL_ROTARY_KERNEL(1, 8, PVL_NORM_NONE, false);
   PVL_ROTARY_KERNEL(8, 1, PVL_NORM_HEAD, false);
   PVL_ROTARY_KERNEL(8, 3, PVL_NORM_HEAD, false);
   PVL_ROTARY_KERNEL(4, 4, PVL_NORM_HEAD, false);
-  PVL_ROTARY_KERNEL(1, 16, PVL_NORM_HEAD, false);
+  PVL_ROTARY_KERNEL(2, 8, PVL_NORM_HEAD, false);
+  PVL_ROTARY_KERNEL(1, 8, PVL_NORM_HEAD, false);
   PVL_ROTARY_KERNEL(8, 1, PVL_NORM_HEAD, true);
   PVL_ROTARY_KERNEL(8, 2, PVL_NORM_HEAD, true);
   PVL_ROTARY_KERNEL(4, 4, PVL_NORM_HEAD, true);
-  PVL_ROTARY_KERNEL(1, 16, PVL_NORM_HEAD, true);
+  PVL_ROTARY_KERNEL(2, 8, PVL_NORM_HEAD, true);
+  PVL_ROTARY_KERNEL(1, 8, PVL_NORM_HEAD, true);
   PVL_ROTARY_KERNEL(8, 1, PVL_NORM_TOKEN, false);
   PVL_ROTARY_KERNEL(8, 2, PVL_NORM_TOKEN, false);
+  PVL_ROTARY_KERNEL(8, 3, PVL_NORM_TOKEN, false);
   PVL_ROTARY_KERNEL(8, 6, PVL_NORM_TOKEN, false);
   PVL_ROTARY_KERNEL(4, 4, PVL_NORM_TOKEN, false);
+  PVL_ROTARY_KERNEL(2, 8, PVL_NORM_TOKEN, false);
+  PVL_ROTARY_KERNEL(1, 8, PVL_NORM_TOKEN, false);
   PVL_ROTARY_KERNEL(1, 16, PVL_NORM_TOKEN, false);
   PVL_ROTARY_KERNEL(8, 1, PVL_NORM_TOKEN, true);
   PVL_ROTARY_KERNEL(8, 2, PVL_NORM_TOKEN, true);
   PVL_ROTARY_KERNEL(4, 4, PVL_NORM_TOKEN, true);
+  PVL_ROTARY_KERNEL(2, 8, PVL_NORM_TOKEN, true);
+  PVL_ROTARY_KERNEL(1, 8, PVL_NORM_TOKEN, true);
   PVL_ROTARY_KERNEL(1, 16, PVL_NORM_TOKEN, true);
 #undef PVL_ROTARY_KERNEL
   return nullptr;
@@ -634,7 +673,7 @@ pvl_status launch(const RotaryParams& p, const Shape& sh, int norm, bool bwd, bo
   const void* fn = find_kernel(sh, norm, bwd, half);
   if (!fn) return fail(PVL_ERR_UNSUPPORTED, "%s: no kernel for this shape", who);
   const size_t smem =
-      sizeof(float) * smem_plan(sh.V, sh.kM, norm, bwd, p.R, p.D, sh.units, sh.hpi, sh.team, sh.teams, sh.threads).total;
+      sizeof(float) * smem_plan(sh.V, sh.kM, norm, bwd, p.turned, p.D, sh.units, sh.hpi, sh.team, sh.teams, sh.threads).total;
   pvl_status st = PVL_OK;
   if (smem > 48 * 1024) {
     st = check_cuda(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)), who);
@@ -647,19 +686,21 @@ pvl_status launch(const RotaryParams& p, const Shape& sh, int norm, bool bwd, bo
   if (sms <= 0 || occ <= 0) return fail(PVL_ERR_CUDA, "%s: no usable CUDA device", who);
   long long grid = static_cast<long long>(occ) * sms;
   if (grid > grid_limit) grid = grid_limit;
-  const long long need = (static_cast<long long>(p.tokens) + p.teams - 1) / p.teams;
-  if (grid > need) grid = need;
-  *grid_out = static_cast<int>(grid);
+  const long long gy = std::min<long long>({p.rows, grid, 65535});
+  const long long gx = std::min<long long>(grid / gy, (static_cast<long long>(p.L) + p.teams - 1) / p.teams);
+  *grid_out = static_cast<int>(gx * gy);
   RotaryParams q = p;
   void* args[] = {&q};
-  return check_cuda(cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(sh.threads), args, smem, s), who);
+  return check_cuda(cudaLaunchKernel(fn, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), dim3(sh.threads),
+                                     args, smem, s),
+                    who);
 }
 
-// Widest vector that divides the head, its rotated part, every stride and
-// every address.
+// Widest vector that divides the head, its rotated part (half layout), every
+// stride and every address.
 int widest(const pvl_rotary* a, const pvl_heads* const* views, int n) {
-  for (int V : {8, 4}) {
-    bool ok = a->D % (2 * V) == 0 && a->R % (2 * V) == 0;
+  for (int V : {8, 4, 2}) {
+    bool ok = a->D % (2 * V) == 0 && (a->layout != PVL_ROTARY_HALF || a->R % (2 * V) == 0);
     for (int i = 0; i < n && ok; ++i)
       if (views[i])
         ok = reinterpret_cast<uintptr_t>(views[i]->data) % (2 * V) == 0 && views[i]->stride_b % V == 0 &&
@@ -675,7 +716,7 @@ int widest(const pvl_rotary* a, const pvl_heads* const* views, int n) {
 bool shape_of(const pvl_rotary* a, int V, bool bwd, Shape* s) {
   const int Ht = a->H + a->Hk;
   const bool whole = a->norm == PVL_NORM_TOKEN;
-  if (V != 8) return team_of(V, V == 4 ? 4 : 16, Ht, a->D, whole, s);
+  if (V != 8) return team_of(V, V == 4 ? 4 : 8, Ht, a->D, whole, s) || team_of(V, 16, Ht, a->D, whole, s);
   const long long tokens = static_cast<long long>(a->B) * a->L;
   if (tokens <= 2 * 152 && team_of(8, 1, Ht, a->D, whole, s)) return true;
   if (!whole) return team_of(8, bwd ? 2 : 3, Ht, a->D, whole, s);
@@ -726,6 +767,7 @@ pvl_status common(const char* who, const pvl_rotary* a, RotaryParams& p) {
   p.w[0] = a->q_weight;
   p.w[1] = a->k_weight;
   p.L = a->L;
+  p.rows = a->B;
   p.H = a->H;
   p.Ht = a->H + a->Hk;
   p.D = a->D;
@@ -733,15 +775,36 @@ pvl_status common(const char* who, const pvl_rotary* a, RotaryParams& p) {
   p.axes = a->axes;
   p.section_1 = a->section_1;
   p.section_2 = a->section_2;
-  p.tokens = static_cast<uint32_t>(static_cast<long long>(a->B) * a->L);
   p.gain = p.sign = a->gain;
   p.eps = a->eps;
   return PVL_OK;
 }
 
+// A view in bytes; an absent tensor's stays zero.
+bool view(const pvl_heads* h, View* v) {
+  if (!h) return true;
+  if (h->stride_h >= 1 << 30 || h->stride_h <= -(1 << 30)) return false;
+  *v = View{static_cast<char*>(h->data), 2 * h->stride_b, 2 * h->stride_l, static_cast<int32_t>(2 * h->stride_h)};
+  return true;
+}
+
+// All tokens as one row where every tensor's batch stride continues its tokens.
+void flatten(RotaryParams& p, bool grads) {
+  const View* all[] = {&p.x[0], &p.x[1], &p.out[0], &p.out[1], grads ? &p.g[0] : nullptr, grads ? &p.g[1] : nullptr};
+  for (const View* v : all)
+    if (v && v->data && v->b != v->l * p.L && p.rows > 1) {
+      if (p.L > 1) return;
+    }
+  if (p.L == 1)
+    for (const View* v : all)
+      if (v && v->data) const_cast<View*>(v)->l = v->b;
+  p.L *= p.rows;
+  p.rows = 1;
+}
+
 void fill(RotaryParams& p, const pvl_rotary* a, const Shape& s) {
   p.units = s.units;
-  p.turned = a->R / (2 * s.V);
+  p.turned = a->layout == PVL_ROTARY_HALF ? a->R / (2 * s.V) : s.units;
   p.hpi = s.hpi;
   p.team = s.team;
   p.teams = s.teams;
@@ -763,17 +826,15 @@ extern "C" pvl_status pack_rotary_fwd(const pvl_rotary* a, const pvl_heads* q, c
   if (st == PVL_OK) st = check_views(who, a, q_out, 0, "q_out");
   if (st == PVL_OK) st = check_views(who, a, k_out, 1, "k_out");
   if (st != PVL_OK) return st;
-  const pvl_heads* views[] = {q, a->Hk ? k : nullptr, q_out, a->Hk ? k_out : nullptr};
+  if (!a->Hk) k = k_out = nullptr;
+  const pvl_heads* views[] = {q, k, q_out, k_out};
   Shape s{};
   if (!shape_of(a, widest(a, views, 4), false, &s))
     return fail(PVL_ERR_UNSUPPORTED, "%s: a token of %d heads of %d features does not fit a block", who, p.Ht, p.D);
   fill(p, a, s);
-  p.x[0] = *q;
-  p.out[0] = *q_out;
-  if (a->Hk) {
-    p.x[1] = *k;
-    p.out[1] = *k_out;
-  }
+  if (!view(q, &p.x[0]) || !view(k, &p.x[1]) || !view(q_out, &p.out[0]) || !view(k_out, &p.out[1]))
+    return fail(PVL_ERR_UNSUPPORTED, "%s: a head stride of 2^30 elements or more", who);
+  flatten(p, false);
   int grid = 0;
   return launch(p, s, a->norm, false, a->layout == PVL_ROTARY_HALF, 1 << 30, &grid,
                 reinterpret_cast<cudaStream_t>(stream), who);
@@ -812,27 +873,24 @@ extern "C" pvl_status pack_rotary_bwd(const pvl_rotary* a, const pvl_heads* dq_o
     return fail(PVL_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu needed", who, ws ? ws_bytes : 0, need);
   if (reinterpret_cast<uintptr_t>(ws) % 16 != 0)
     return fail(PVL_ERR_UNSUPPORTED, "%s: the workspace is not 16-byte aligned", who);
-  const pvl_heads* views[] = {dq_out, a->Hk ? dk_out : nullptr, dq, a->Hk ? dk : nullptr, norm ? q : nullptr,
-                              norm && a->Hk ? k : nullptr};
+  if (!a->Hk) dk_out = dk = k = nullptr;
+  if (!norm) q = k = nullptr;
+  const pvl_heads* views[] = {dq_out, dk_out, dq, dk, q, k};
   Shape s{};
   if (!shape_of(a, widest(a, views, 6), norm, &s))
     return fail(PVL_ERR_UNSUPPORTED, "%s: a token of %d heads of %d features does not fit a block", who, p.Ht, p.D);
   fill(p, a, s);
   p.sign = -a->gain;  // turned back
-  p.out[0] = *dq;
-  if (a->Hk) p.out[1] = *dk;
   // without a norm the gradient is rotated in the input's place
-  pvl_heads* up = norm ? p.g : p.x;
-  up[0] = *dq_out;
-  if (a->Hk) up[1] = *dk_out;
-  if (norm) {
-    p.x[0] = *q;
-    if (a->Hk) p.x[1] = *k;
-  }
+  View* up = norm ? p.g : p.x;
+  if (!view(dq_out, &up[0]) || !view(dk_out, &up[1]) || !view(dq, &p.out[0]) || !view(dk, &p.out[1]) ||
+      (norm && (!view(q, &p.x[0]) || !view(k, &p.x[1]))))
+    return fail(PVL_ERR_UNSUPPORTED, "%s: a head stride of 2^30 elements or more", who);
+  flatten(p, norm);
   p.part = weights ? static_cast<float*>(ws) : nullptr;
   // a partial row for each team (norm per token) or block (norm per head)
   const int rows_per_block = a->norm == PVL_NORM_TOKEN ? s.teams : 1;
-  const long long tokens = p.tokens;
+  const long long tokens = static_cast<long long>(a->B) * a->L;
   const long long rows_max = tokens < kMaxPartials ? tokens : kMaxPartials;
   int limit = weights ? static_cast<int>(rows_max / rows_per_block) : 1 << 30;
   if (limit < 1) limit = 1;
