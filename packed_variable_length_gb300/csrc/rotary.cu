@@ -171,17 +171,53 @@ __device__ __forceinline__ void vectors_of(const RotaryParams& p, int u, int* e0
   }
 }
 
+// Head (of those a team takes at once) and unit of thread t of a team; false
+// for a thread without one.  With the norm per head, heads do not straddle
+// warps where a warp holds at least one, so that their sums are shuffles.
+__host__ __device__ inline bool place(bool per_head, int units, int hpi, int team, int t, int* hl, int* u) {
+  if (per_head && team > 32 && units <= 32) {
+    const int per = 32 / units, i = t % 32;
+    *hl = t / 32 * per + i / units;
+    *u = i % units;
+    return i < per * units && *hl < hpi;
+  }
+  *hl = t / units;
+  *u = t % units;
+  return *hl < hpi;
+}
+
 // Sum over the `n` threads of an aligned power-of-two lane group.
 __device__ __forceinline__ float lane_sum(float v, int n) {
   for (int o = 1; o < n; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+// Sum over a head's lanes u = 0 .. units - 1 (neighbours in a warp), in all of them.
+__device__ __forceinline__ float head_sum(float v, int u, int units) {
+  for (int o = 1; o < units; o <<= 1) {
+    const float w = __shfl_down_sync(0xffffffffu, v, o);
+    v += u + o < units ? w : 0.0f;
+  }
+  return __shfl_sync(0xffffffffu, v, (threadIdx.x & 31) - u);
+}
+
+// 16, 8 or 4 bytes into shared memory without passing registers.
+template <typename T>
+__device__ __forceinline__ void copy_async(T* dst, const char* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(sizeof(T)) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Stages of a thread's ring of vectors.
+constexpr int kRing = 2;
 
 // Shared memory, in floats: the angles' cosines and sines of each warp or
 // smaller team, the norm's weights, the sums that cross threads (backward of
 // the norm per head also uses that part, at the end, for its weight gradients).
 struct SmemPlan {
-  int angles, weights, sums, total;  // offsets
+  int angles, weights, sums, ring, total;  // offsets
 };
 __host__ __device__ inline SmemPlan smem_plan(int V, int kM, int norm, bool bwd, int turned, int D, int units, int hpi,
                                               int team, int teams, int threads) {
@@ -196,11 +232,12 @@ __host__ __device__ inline SmemPlan smem_plan(int V, int kM, int norm, bool bwd,
   int sums = 0;
   if (norm == PVL_NORM_TOKEN) sums = 2 * (threads / 32 + 1) * 4;
   if (norm == PVL_NORM_HEAD) {
-    const bool lanes = (units & (units - 1)) == 0 && units <= 32;
-    if (!lanes) sums = threads * kM * (bwd ? 2 : 1);
-    if (bwd && teams * hpi * D > sums) sums = teams * hpi * D;
+    if (units > 32) sums = threads * kM * (bwd ? 2 : 1);
   }
-  s.total = s.sums + sums;
+  s.ring = s.sums + (sums + 3) / 4 * 4;
+  // the threads' rings; the weight gradients of the norm per head come after them
+  s.total = s.ring + (V > 1 && norm != PVL_NORM_NONE ? kRing * kM * (bwd ? 4 : 2) * threads * V / 2 : 0);
+  if (norm == PVL_NORM_HEAD && bwd && s.ring + teams * hpi * D > s.total) s.total = s.ring + teams * hpi * D;
   return s;
 }
 
@@ -215,8 +252,8 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
   const SmemPlan plan = smem_plan(V, kM, kNorm, kBwd, p.turned, p.D, p.units, p.hpi, p.team, p.teams, blockDim.x);
   const int tid = threadIdx.x;
   const int slot = tid / p.team, lane = tid - slot * p.team;
-  const int hl = lane / p.units, u = lane - hl * p.units;
-  const bool on = slot < p.teams && hl < p.hpi;
+  int hl, u;
+  const bool on = place(kHead, p.units, p.hpi, p.team, lane, &hl, &u) && slot < p.teams;
   const bool turned = u < p.turned;
   int e0, e1;  // features of the unit's two vectors
   vectors_of<V, kHalf>(p, u, &e0, &e1);
@@ -232,10 +269,14 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
     for (int i = tid; i < n; i += blockDim.x) {
       const int m = kToken ? i / p.team : i / p.units;
       const int t = kToken ? i - m * p.team : i - m * p.units;
-      const int ul = kToken ? t % p.units : t;
-      const int h = kToken ? t / p.units + m * p.hpi : 0;
+      int h = 0, ul = t;
+      bool real = true;
+      if (kToken) {
+        real = place(kHead, p.units, p.hpi, p.team, t, &h, &ul);
+        h += m * p.hpi;
+        real = real && h < p.Ht;
+      }
       const bool key = kToken ? h >= p.H : m == 1;
-      const bool real = !kToken || (t / p.units < p.hpi && h < p.Ht);
       const float* w = key ? p.w[1] : p.w[0];
       if (kToken && w) w += (key ? h - p.H : h) * p.D;
       int f0, f1;
@@ -264,53 +305,108 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
 #pragma unroll
       for (int q = 0; q < kP; ++q) acc[i].a[q] = acc[i].b[q] = make_float2(0.0f, 0.0f);
   }
-  int turn = 0;
-  for (int row = blockIdx.y; row < p.rows; row += gridDim.y) {
-  const int32_t* const positions = p.positions + static_cast<size_t>(row) * p.L * p.axes;
-  auto position = [&](int l, int a) {
-    return a < p.axes && l < p.L ? __ldg(positions + static_cast<size_t>(l) * p.axes + a) : 0;
+  // The block's work as one sequence of items: kM heads a thread of one token
+  // a team; a token's heads in turn, then the next token, then the next row.
+  struct Item {
+    int row, base, chunk;
   };
-  const int step = gridDim.x * p.teams;
-  int l = blockIdx.x * p.teams + slot;
+  const int step = gridDim.x * p.teams, chunks = (p.Ht + kM * p.hpi - 1) / (kM * p.hpi);
+  auto advance = [&](Item& i) {
+    if (++i.chunk < chunks) return;
+    i.chunk = 0;
+    i.base += step;
+    if (i.base < p.L) return;
+    i.base = blockIdx.x * p.teams;
+    i.row += gridDim.y;
+  };
+  const int apart = 2 * (e1 - e0);
+  // Address of the unit's first vector: a thread without a token or a head
+  // works on the last one of each, and neither adds to sums nor writes.
+  auto heads_at = [&](const View (&v)[2], const Item& i, char* (&to)[2]) {
+    const int l = min(i.base + slot, p.L - 1);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      to[k] = v[k].data + i.row * v[k].b + l * v[k].l + 2 * e0 - (k ? static_cast<int64_t>(p.H) * v[1].h : 0);
+  };
+  auto head_at = [&](const View (&v)[2], char* const (&to)[2], int h) {
+    const bool key = h >= p.H;
+    return (key ? to[1] : to[0]) + static_cast<int64_t>(h) * (key ? v[1].h : v[0].h);
+  };
+  // A thread's vectors of an item (x0, x1, and backward g0, g1 of each head),
+  // copied kRing - 1 items ahead into its own part of the ring: no other
+  // thread reads it, so waiting for the copies is all the synchronisation.
+  constexpr bool kAsync = V > 1 && kAny;
+  constexpr int kVecs = kBwd ? 4 : 2;
+  T* const ring = reinterpret_cast<T*>(smem + plan.ring) + tid;
+  auto fetch = [&](const Item& i, int stage) {
+    char *xp[2], *gp[2];
+    heads_at(p.x, i, xp);
+    if (kBwd) heads_at(p.g, i, gp);
+    T* to = ring + stage * kM * kVecs * blockDim.x;
+#pragma unroll
+    for (int m = 0; m < kM; ++m) {
+      const int h = min(hl + (i.chunk * kM + m) * p.hpi, p.Ht - 1);
+      const char* q = head_at(p.x, xp, h);
+      copy_async(to + (m * kVecs) * blockDim.x, q);
+      copy_async(to + (m * kVecs + 1) * blockDim.x, q + apart);
+      if (kBwd) {
+        q = head_at(p.g, gp, h);
+        copy_async(to + (m * kVecs + 2) * blockDim.x, q);
+        copy_async(to + (m * kVecs + 3) * blockDim.x, q + apart);
+      }
+    }
+  };
+  auto position = [&](const Item& i, int a) {
+    const int l = i.base + slot;
+    return a < p.axes && i.row < p.rows && l < p.L
+               ? __ldg(p.positions + (static_cast<size_t>(i.row) * p.L + l) * p.axes + a)
+               : 0;
+  };
+  Item it{static_cast<int>(blockIdx.y), static_cast<int>(blockIdx.x) * p.teams, 0}, ahead = it;
+  if constexpr (kAsync) {
+#pragma unroll
+    for (int s = 0; s < kRing - 1; ++s) {
+      if (ahead.row < p.rows) fetch(ahead, s);
+      copy_commit();
+      advance(ahead);
+    }
+  }
   int32_t pos[3];
 #pragma unroll
-  for (int a = 0; a < 3; ++a) pos[a] = position(l, a);
-  for (int base = blockIdx.x * p.teams; base < p.L; base += step, l += step) {
-    // a thread without a token or a head works on the last one of each, and
-    // neither adds to sums nor writes
-    const bool live = on && l < p.L;
-    const int lc = l < p.L ? l : p.L - 1;
-    // the unit's first vector in head 0 of queries and keys, less H heads
-    auto heads_at = [&](const View (&v)[2], char* (&to)[2]) {
+  for (int a = 0; a < 3; ++a) pos[a] = position(it, a);
+  int turn = 0, stage = 0;
+  while (it.row < p.rows) {
+    const bool live = on && it.base + slot < p.L;
+    {
+      const int h0 = hl + it.chunk * kM * p.hpi;
+      T vx[kAsync ? 1 : kM][kVecs]{};
+      const T* held = ring + stage * kM * kVecs * blockDim.x;
+      if constexpr (kAsync) {
+        copy_wait<kRing - 2>();
+        int to = stage + kRing - 1;
+        to = to >= kRing ? to - kRing : to;
+        if (ahead.row < p.rows) fetch(ahead, to);
+        copy_commit();
+        advance(ahead);
+      } else {
+        char *xp[2], *gp[2];
+        heads_at(p.x, it, xp);
+        if (kBwd) heads_at(p.g, it, gp);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        to[i] = v[i].data + row * v[i].b + lc * v[i].l + 2 * e0 - (i ? static_cast<int64_t>(p.H) * v[1].h : 0);
-    };
-    auto head_at = [&](const View (&v)[2], char* const (&to)[2], int h) {
-      const bool key = h >= p.H;
-      return (key ? to[1] : to[0]) + static_cast<int64_t>(h) * (key ? v[1].h : v[0].h);
-    };
-    const int apart = 2 * (e1 - e0);
-    char *xp[2], *gp[2], *op[2];
-    heads_at(p.x, xp);
-    if (kBwd) heads_at(p.g, gp);
-    heads_at(p.out, op);
-    for (int h0 = hl; h0 - hl < p.Ht; h0 += kM * p.hpi) {
-      // the heads' loads first
-      T x0[kM], x1[kM], g0[kM], g1[kM];
-#pragma unroll
-      for (int m = 0; m < kM; ++m) {
-        const int h = min(h0 + m * p.hpi, p.Ht - 1);
-        const char* q = head_at(p.x, xp, h);
-        x0[m] = *reinterpret_cast<const T*>(q);
-        x1[m] = *reinterpret_cast<const T*>(q + apart);
-        if (kBwd) {
-          q = head_at(p.g, gp, h);
-          g0[m] = *reinterpret_cast<const T*>(q);
-          g1[m] = *reinterpret_cast<const T*>(q + apart);
+        for (int m = 0; m < kM; ++m) {
+          const int h = min(h0 + m * p.hpi, p.Ht - 1);
+          const char* q = head_at(p.x, xp, h);
+          vx[kAsync ? 0 : m][0] = *reinterpret_cast<const T*>(q);
+          vx[kAsync ? 0 : m][1] = *reinterpret_cast<const T*>(q + apart);
+          if (kBwd) {
+            q = head_at(p.g, gp, h);
+            vx[kAsync ? 0 : m][kVecs - 2] = *reinterpret_cast<const T*>(q);
+            vx[kAsync ? 0 : m][kVecs - 1] = *reinterpret_cast<const T*>(q + apart);
+          }
         }
       }
-      if (h0 == hl) {
+      auto vec = [&](int m, int j) { return kAsync ? held[(m * kVecs + j) * blockDim.x] : vx[kAsync ? 0 : m][j]; };
+      if (it.chunk == 0) {
         // the token's angles
         __syncwarp();
         for (int i = in_group; i < p.turned * V; i += group) {
@@ -336,8 +432,11 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
           }
         }
         __syncwarp();
+        Item next = it;
+        next.chunk = chunks - 1;
+        advance(next);
 #pragma unroll
-        for (int a = 0; a < 3; ++a) pos[a] = position(l + step, a);
+        for (int a = 0; a < 3; ++a) pos[a] = position(next, a);
       }
       auto rotate = [&](Unit<V>& z) {
 #pragma unroll
@@ -358,14 +457,14 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
           const int h = h0 + m * p.hpi;
           const bool real = live && h < p.Ht;
           Unit<V> x;
-          unpack<V, kHalf>(x0[m], x1[m], x);
+          unpack<V, kHalf>(vec(m, 0), vec(m, 1), x);
           float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int q = 0; q < kP; ++q) s = ffma2(x.a[q], x.a[q], ffma2(x.b[q], x.b[q], s));
           part[m][0] = real ? s.x + s.y : 0.0f;
           if (kBwd) {
             Unit<V>& z = g[kBwd ? m : 0];
-            unpack<V, kHalf>(g0[m], g1[m], z);
+            unpack<V, kHalf>(vec(m, kVecs - 2), vec(m, kVecs - 1), z);
             if (turned) rotate(z);
             s = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -378,11 +477,11 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
           }
         }
         if (kHead) {
-          if ((p.units & (p.units - 1)) == 0 && p.units <= 32) {
+          if (p.units <= 32) {
 #pragma unroll
             for (int m = 0; m < kM; ++m)
 #pragma unroll
-              for (int k = 0; k < kSums; ++k) part[m][k] = lane_sum(part[m][k], p.units);
+              for (int k = 0; k < kSums; ++k) part[m][k] = head_sum(part[m][k], u, p.units);
           } else {
             const int n = blockDim.x;
             __syncthreads();
@@ -460,13 +559,15 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
           mean[m] = kBwd ? -r[m] * r[m] * r[m] * (part[m][kSums - 1] * inv_n) : 0.0f;
         }
       }
+      char* op[2];
+      heads_at(p.out, it, op);
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
         const int h = h0 + m * p.hpi;
         const bool real = live && h < p.Ht;
         {
           Unit<V> z;
-          unpack<V, kHalf>(x0[m], x1[m], z);
+          unpack<V, kHalf>(vec(m, 0), vec(m, 1), z);
           if (kBwd) {
             const Unit<V>& d = g[kBwd ? m : 0];
             const float2 rr = make_float2(r[m], r[m]), mm = make_float2(mean[m], mean[m]);
@@ -512,8 +613,10 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
         }
       }
     }
+    advance(it);
+    if (++stage == kRing) stage = 0;
   }
-  }
+  if constexpr (kAsync) copy_wait<0>();
   if (kBwd) {
     if (p.part == nullptr) return;
     constexpr int kValues = V > 1 ? 2 * V : 2;
@@ -540,18 +643,19 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
     } else {
       // the block's teams and heads added feature by feature, queries then keys
       float* row = p.part + static_cast<size_t>(blockIdx.y * gridDim.x + blockIdx.x) * p.width;
+      float* sums = smem + plan.ring;  // the ring is done with
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         __syncthreads();
         if (on) {
 #pragma unroll
           for (int k = 0; k < kValues; ++k)
-            sums_s[(slot * p.hpi + hl) * p.D + feature<V, kHalf>(k, e0, e1)] = value(acc[i ? kAcc - 1 : 0], k);
+            sums[(slot * p.hpi + hl) * p.D + feature<V, kHalf>(k, e0, e1)] = value(acc[i ? kAcc - 1 : 0], k);
         }
         __syncthreads();
         for (int d = tid; d < p.D; d += blockDim.x) {
           float t = 0.0f;
-          for (int j = 0; j < p.teams * p.hpi; ++j) t += sums_s[j * p.D + d];
+          for (int j = 0; j < p.teams * p.hpi; ++j) t += sums[j * p.D + d];
           row[i * p.D + d] = t;
         }
       }
@@ -593,25 +697,24 @@ int round32(int n) { return (n + 31) / 32 * 32; }
 
 // The team of a token for vectors V wide and kM heads a thread: a power of
 // two below 32 threads, or whole warps.  False where one pass over a token's
-// heads does not fit a block and `whole` asks for it.
-bool team_of(int V, int kM, int Ht, int D, bool whole, Shape* s) {
+// heads does not fit a block and the norm per token needs it.
+bool team_of(int V, int kM, int Ht, int D, int norm, Shape* s) {
   s->V = V;
   s->kM = kM;
   s->units = D / (2 * V);
-  s->hpi = (Ht + kM - 1) / kM;
-  if (s->units * s->hpi > kMaxBlock) {
-    if (whole) return false;
-    s->hpi = kMaxBlock / s->units;  // units <= 128
-  }
-  const int n = s->units * s->hpi;
-  if (n >= 17) {
-    s->team = round32(n);
-    // heads that the rounding leaves room for
-    const int fit = s->team / s->units;
-    s->hpi = fit < Ht ? fit : Ht;
-  } else {
+  const int want = (Ht + kM - 1) / kM;  // heads at once
+  if (s->units * want <= 32) {
     s->team = 1;
-    while (s->team < n) s->team <<= 1;
+    while (s->team < s->units * want) s->team <<= 1;
+    s->hpi = std::min(Ht, s->team / s->units);
+  } else {
+    const int per = norm == PVL_NORM_HEAD ? 32 / s->units : 0;  // heads of a warp, where they keep to one
+    const int most = per ? per * (kMaxBlock / 32) : kMaxBlock / s->units;
+    if (want > most && norm == PVL_NORM_TOKEN) return false;
+    s->hpi = std::min(want, most);
+    s->team = per ? (s->hpi + per - 1) / per * 32 : round32(s->units * s->hpi);
+    // heads that the rounding leaves room for
+    s->hpi = std::min(Ht, per ? s->team / 32 * per : s->team / s->units);
   }
   s->teams = s->team >= 128 ? 1 : 128 / s->team;
   s->threads = s->team * s->teams;
@@ -716,12 +819,12 @@ int widest(const pvl_rotary* a, const pvl_heads* const* views, int n) {
 bool shape_of(const pvl_rotary* a, int V, bool bwd, Shape* s) {
   const int Ht = a->H + a->Hk;
   const bool whole = a->norm == PVL_NORM_TOKEN;
-  if (V != 8) return team_of(V, V == 4 ? 4 : 8, Ht, a->D, whole, s) || team_of(V, 16, Ht, a->D, whole, s);
+  if (V != 8) return team_of(V, V == 4 ? 4 : 8, Ht, a->D, a->norm, s) || team_of(V, 16, Ht, a->D, a->norm, s);
   const long long tokens = static_cast<long long>(a->B) * a->L;
-  if (tokens <= 2 * 152 && team_of(8, 1, Ht, a->D, whole, s)) return true;
-  if (!whole) return team_of(8, bwd ? 2 : 3, Ht, a->D, whole, s);
-  if (!bwd && team_of(8, 6, Ht, a->D, whole, s)) return true;
-  return team_of(8, 2, Ht, a->D, whole, s);
+  if (tokens <= 2 * 152 && team_of(8, 1, Ht, a->D, a->norm, s)) return true;
+  if (!whole) return team_of(8, bwd ? 2 : 3, Ht, a->D, a->norm, s);
+  if (!bwd && team_of(8, 6, Ht, a->D, a->norm, s)) return true;
+  return team_of(8, 2, Ht, a->D, a->norm, s);
 }
 
 pvl_status check_views(const char* who, const pvl_rotary* a, const pvl_heads* v, int which, const char* name) {
