@@ -49,6 +49,7 @@ constexpr float kRadians = 1.4629180792671596e-9f;  // 2 pi / 2^32
 struct View {
   char* data;
   int64_t b, l;
+  int64_t step;  // of a block's next token
   int32_t h;
 };
 
@@ -65,7 +66,7 @@ struct RotaryParams {
   int axes, section_1, section_2;
   int units;         // units of a head, D / (2 V)
   int turned;        // units of a head that are rotated: all, or in the half layout R / (2 V)
-  int hpi;           // heads a team takes at once
+  int hpi, chunks;   // heads a team takes at once; rounds of kM hpi heads
   int team, teams;   // threads of a team, teams of a block
   int width;         // columns of part
   float gain, sign;  // sign: of the sine
@@ -214,28 +215,26 @@ __device__ __forceinline__ void copy_wait() {
 constexpr int kRing = 2;
 
 // Shared memory, in floats: the angles' cosines and sines of each warp or
-// smaller team, the norm's weights, the sums that cross threads (backward of
-// the norm per head also uses that part, at the end, for its weight gradients).
+// smaller team, the norm's weights, the sums that cross threads, the threads'
+// rings of vectors (at the end their place holds the weight gradients of the
+// norm per head).
 struct SmemPlan {
-  int angles, weights, sums, ring, total;  // offsets
+  int weights, sums, ring, total;  // offsets; the angles are first
 };
-__host__ __device__ inline SmemPlan smem_plan(int V, int kM, int norm, bool bwd, int turned, int D, int units, int hpi,
-                                              int team, int teams, int threads) {
+__host__ __device__ inline SmemPlan smem_plan(int V, int kM, int norm, bool bwd, int D, int units, int hpi, int team,
+                                              int teams, int threads) {
   SmemPlan s{};
   const int group = team < 32 ? team : 32;
-  const int per = 2 * (V > 1 ? V : 2);  // floats of a unit's angles (V = 1: a pair and an unused one)
-  s.angles = 0;
-  s.weights = threads / group * turned * per;
-  const int unit_floats = 2 * (V > 1 ? V : 2);
-  const int weights = norm == PVL_NORM_TOKEN ? kM * team * unit_floats : norm == PVL_NORM_HEAD ? 2 * units * unit_floats : 0;
+  const int unit = 2 * (V > 1 ? V : 2), column = kMaxD / (2 * V);  // floats of a unit (V = 1: half unused); units kept
+  s.weights = threads / group * column * unit;
+  const int weights = norm == PVL_NORM_TOKEN ? (team + 31) / 32 * 32 * kM * unit
+                      : norm == PVL_NORM_HEAD ? 2 * column * unit
+                                              : 0;
   s.sums = s.weights + weights;
   int sums = 0;
-  if (norm == PVL_NORM_TOKEN) sums = 2 * (threads / 32 + 1) * 4;
-  if (norm == PVL_NORM_HEAD) {
-    if (units > 32) sums = threads * kM * (bwd ? 2 : 1);
-  }
-  s.ring = s.sums + (sums + 3) / 4 * 4;
-  // the threads' rings; the weight gradients of the norm per head come after them
+  if (norm == PVL_NORM_TOKEN) sums = 2 * (threads / 32) * 4;
+  if (norm == PVL_NORM_HEAD && units > 32) sums = (threads * kM * (bwd ? 2 : 1) + 3) / 4 * 4;
+  s.ring = s.sums + sums;
   s.total = s.ring + (V > 1 && norm != PVL_NORM_NONE ? kRing * kM * (bwd ? 4 : 2) * threads * V / 2 : 0);
   if (norm == PVL_NORM_HEAD && bwd && s.ring + teams * hpi * D > s.total) s.total = s.ring + teams * hpi * D;
   return s;
@@ -245,12 +244,12 @@ __host__ __device__ inline SmemPlan smem_plan(int V, int kM, int norm, bool bwd,
 template <int V, int kM, int kNorm, bool kBwd, bool kHalf>
 __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant__ RotaryParams p) {
   using T = typename Vec<V>::T;
-  constexpr int kP = Unit<V>::kP;
+  constexpr int kP = Unit<V>::kP, kColumn = kMaxD / (2 * V);
   constexpr bool kHead = kNorm == PVL_NORM_HEAD, kToken = kNorm == PVL_NORM_TOKEN, kAny = kHead || kToken;
   constexpr int kSums = kBwd ? 2 : 1;  // sum x^2, and backward sum g w x
   extern __shared__ __align__(16) float smem[];
-  const SmemPlan plan = smem_plan(V, kM, kNorm, kBwd, p.turned, p.D, p.units, p.hpi, p.team, p.teams, blockDim.x);
-  const int tid = threadIdx.x;
+  const SmemPlan plan = smem_plan(V, kM, kNorm, kBwd, p.D, p.units, p.hpi, p.team, p.teams, blockDim.x);
+  const int tid = threadIdx.x, lane32 = tid & 31;
   const int slot = tid / p.team, lane = tid - slot * p.team;
   int hl, u;
   const bool on = place(kHead, p.units, p.hpi, p.team, lane, &hl, &u) && slot < p.teams;
@@ -258,12 +257,13 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
   int e0, e1;  // features of the unit's two vectors
   vectors_of<V, kHalf>(p, u, &e0, &e1);
   const int group = p.team < 32 ? p.team : 32, in_group = tid & (group - 1);
-  float4* const angles = reinterpret_cast<float4*>(smem) + tid / group * p.turned * kP;
+  float4* const angles = reinterpret_cast<float4*>(smem) + tid / group * kP * kColumn;  // [kP][kColumn]
   float4* const weights = reinterpret_cast<float4*>(smem + plan.weights);
   float* const sums_s = smem + plan.sums;
 
   // the norm's weights, (a.x, a.y, b.x, b.y) of each pair of a unit: for the
-  // norm per token [kM][kP][team], per head [queries, keys][kP][units]
+  // norm per token [warp of the team][kM][kP][lane], per head [queries,
+  // keys][kP][unit]
   if (kAny) {
     const int n = kToken ? kM * p.team : 2 * p.units;
     for (int i = tid; i < n; i += blockDim.x) {
@@ -287,14 +287,16 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
           const int e = 2 * q + (c & 1);  // pair of the unit
           v[c] = w && real && (V > 1 || !(c & 1)) ? __ldg(w + feature<V, kHalf>((c >> 1) * (V > 1 ? V : 1) + e, f0, f1)) : 1.0f;
         }
-        weights[kToken ? (m * kP + q) * p.team + t : (m * kP + q) * p.units + t] = make_float4(v[0], v[1], v[2], v[3]);
+        weights[kToken ? ((t / 32 * kM + m) * kP + q) * 32 + t % 32 : (m * kP + q) * kColumn + t] =
+            make_float4(v[0], v[1], v[2], v[3]);
       }
     }
     __syncthreads();
   }
-  // weights of the unit in round m of head h
-  auto weight = [&](int m, int h, int q) {
-    return kToken ? weights[(m * kP + q) * p.team + lane] : weights[((h >= p.H) * kP + q) * p.units + u];
+  const float4* const my_weights = kToken ? weights + lane / 32 * kM * kP * 32 + lane % 32 : weights + u;
+  // weights of the unit's pairs q in round m of a head
+  auto weight = [&](int m, bool key, int q) {
+    return kToken ? my_weights[(m * kP + q) * 32] : my_weights[(key ? kP * kColumn : 0) + q * kColumn];
   };
 
   constexpr int kAcc = kBwd ? (kToken ? kM : 2) : 1;
@@ -305,318 +307,338 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
 #pragma unroll
       for (int q = 0; q < kP; ++q) acc[i].a[q] = acc[i].b[q] = make_float2(0.0f, 0.0f);
   }
-  // The block's work as one sequence of items: kM heads a thread of one token
-  // a team; a token's heads in turn, then the next token, then the next row.
-  struct Item {
-    int row, base, chunk;
-  };
-  const int step = gridDim.x * p.teams, chunks = (p.Ht + kM * p.hpi - 1) / (kM * p.hpi);
-  auto advance = [&](Item& i) {
-    if (++i.chunk < chunks) return;
-    i.chunk = 0;
-    i.base += step;
-    if (i.base < p.L) return;
-    i.base = blockIdx.x * p.teams;
-    i.row += gridDim.y;
-  };
+  const float inv_nq = 1.0f / static_cast<float>(kHead ? p.D : p.D * p.H);
+  const float inv_nk = 1.0f / static_cast<float>(kHead ? p.D : p.D * max(p.Ht - p.H, 1));
+  const int step = gridDim.x * p.teams;
+  const int chunks = kToken ? 1 : p.chunks;
   const int apart = 2 * (e1 - e0);
-  // Address of the unit's first vector: a thread without a token or a head
-  // works on the last one of each, and neither adds to sums nor writes.
-  auto heads_at = [&](const View (&v)[2], const Item& i, char* (&to)[2]) {
-    const int l = min(i.base + slot, p.L - 1);
+  // The unit's first vector in head 0 (keys: head -H) of token l of a row.
+  auto start_at = [&](const View (&v)[2], int row, int l, char* (&to)[2]) {
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-      to[k] = v[k].data + i.row * v[k].b + l * v[k].l + 2 * e0 - (k ? static_cast<int64_t>(p.H) * v[1].h : 0);
+      to[k] = v[k].data + row * v[k].b + l * v[k].l + 2 * e0 - (k ? static_cast<int64_t>(p.H) * v[1].h : 0);
+  };
+  auto step_on = [&](const View (&v)[2], char* (&to)[2]) {
+    to[0] += v[0].step;
+    to[1] += v[1].step;
   };
   auto head_at = [&](const View (&v)[2], char* const (&to)[2], int h) {
     const bool key = h >= p.H;
     return (key ? to[1] : to[0]) + static_cast<int64_t>(h) * (key ? v[1].h : v[0].h);
   };
-  // A thread's vectors of an item (x0, x1, and backward g0, g1 of each head),
-  // copied kRing - 1 items ahead into its own part of the ring: no other
-  // thread reads it, so waiting for the copies is all the synchronisation.
+  // A thread's vectors of kM heads (x0, x1, and backward g0, g1 of each).
+  // With a norm they are copied one item (a token's kM heads a thread) ahead
+  // into the thread's own part of a ring: no other thread reads it, so waiting
+  // for the copies is all the synchronisation.  Without a norm a thread works
+  // so little on them that direct loads and more threads are faster (64k pack:
+  // 127 us against 146).
   constexpr bool kAsync = V > 1 && kAny;
   constexpr int kVecs = kBwd ? 4 : 2;
-  T* const ring = reinterpret_cast<T*>(smem + plan.ring) + tid;
-  auto fetch = [&](const Item& i, int stage) {
-    char *xp[2], *gp[2];
-    heads_at(p.x, i, xp);
-    if (kBwd) heads_at(p.g, i, gp);
-    T* to = ring + stage * kM * kVecs * blockDim.x;
+  T* const ring = reinterpret_cast<T*>(smem + plan.ring) + (tid >> 5) * kRing * kM * kVecs * 32 + lane32;
+  int turn = 0;
+  for (int row = blockIdx.y; row < p.rows; row += gridDim.y) {
+    const int base0 = blockIdx.x * p.teams;
+    int l = base0 + slot, lf = l, cf = 0, held = 0, to = 0;  // token; token and heads of the next copies; ring stages
+    char *xp[2], *gp[2], *op[2];
+    start_at(p.x, row, l, xp);
+    if (kBwd) start_at(p.g, row, l, gp);
+    start_at(p.out, row, l, op);
+    auto fetch = [&]() {
+      T* dst = ring + to * kM * kVecs * 32;
 #pragma unroll
-    for (int m = 0; m < kM; ++m) {
-      const int h = min(hl + (i.chunk * kM + m) * p.hpi, p.Ht - 1);
-      const char* q = head_at(p.x, xp, h);
-      copy_async(to + (m * kVecs) * blockDim.x, q);
-      copy_async(to + (m * kVecs + 1) * blockDim.x, q + apart);
-      if (kBwd) {
-        q = head_at(p.g, gp, h);
-        copy_async(to + (m * kVecs + 2) * blockDim.x, q);
-        copy_async(to + (m * kVecs + 3) * blockDim.x, q + apart);
-      }
-    }
-  };
-  auto position = [&](const Item& i, int a) {
-    const int l = i.base + slot;
-    return a < p.axes && i.row < p.rows && l < p.L
-               ? __ldg(p.positions + (static_cast<size_t>(i.row) * p.L + l) * p.axes + a)
-               : 0;
-  };
-  Item it{static_cast<int>(blockIdx.y), static_cast<int>(blockIdx.x) * p.teams, 0}, ahead = it;
-  if constexpr (kAsync) {
-#pragma unroll
-    for (int s = 0; s < kRing - 1; ++s) {
-      if (ahead.row < p.rows) fetch(ahead, s);
-      copy_commit();
-      advance(ahead);
-    }
-  }
-  int32_t pos[3];
-#pragma unroll
-  for (int a = 0; a < 3; ++a) pos[a] = position(it, a);
-  int turn = 0, stage = 0;
-  while (it.row < p.rows) {
-    const bool live = on && it.base + slot < p.L;
-    {
-      const int h0 = hl + it.chunk * kM * p.hpi;
-      T vx[kAsync ? 1 : kM][kVecs]{};
-      const T* held = ring + stage * kM * kVecs * blockDim.x;
-      if constexpr (kAsync) {
-        copy_wait<kRing - 2>();
-        int to = stage + kRing - 1;
-        to = to >= kRing ? to - kRing : to;
-        if (ahead.row < p.rows) fetch(ahead, to);
-        copy_commit();
-        advance(ahead);
-      } else {
-        char *xp[2], *gp[2];
-        heads_at(p.x, it, xp);
-        if (kBwd) heads_at(p.g, it, gp);
-#pragma unroll
-        for (int m = 0; m < kM; ++m) {
-          const int h = min(h0 + m * p.hpi, p.Ht - 1);
+      for (int m = 0; m < kM; ++m) {
+        const int h = hl + (cf * kM + m) * p.hpi;
+        if (on && lf < p.L && h < p.Ht) {
           const char* q = head_at(p.x, xp, h);
-          vx[kAsync ? 0 : m][0] = *reinterpret_cast<const T*>(q);
-          vx[kAsync ? 0 : m][1] = *reinterpret_cast<const T*>(q + apart);
+          copy_async(dst + (m * kVecs) * 32, q);
+          copy_async(dst + (m * kVecs + 1) * 32, q + apart);
           if (kBwd) {
             q = head_at(p.g, gp, h);
-            vx[kAsync ? 0 : m][kVecs - 2] = *reinterpret_cast<const T*>(q);
-            vx[kAsync ? 0 : m][kVecs - 1] = *reinterpret_cast<const T*>(q + apart);
+            copy_async(dst + (m * kVecs + 2) * 32, q);
+            copy_async(dst + (m * kVecs + 3) * 32, q + apart);
           }
         }
       }
-      auto vec = [&](int m, int j) { return kAsync ? held[(m * kVecs + j) * blockDim.x] : vx[kAsync ? 0 : m][j]; };
-      if (it.chunk == 0) {
-        // the token's angles
-        __syncwarp();
-        for (int i = in_group; i < p.turned * V; i += group) {
-          int unit, e;
-          if constexpr (kHalf || V == 1) {
-            unit = i / V;
-            e = i % V;
-          } else {
-            const int side = i >= p.D / 4, j = i - side * (p.D / 4);
-            unit = j / (V / 2);
-            e = j % (V / 2) + side * (V / 2);
-          }
-          float* q = reinterpret_cast<float*>(angles + (e / 2) * p.turned + unit) + (e & 1);
-          if (kHalf || i < p.R / 2) {
-            const int32_t n = i < p.section_1 ? pos[0] : i < p.section_2 ? pos[1] : pos[2];
-            const uint64_t frac = __ldg(p.turns + i) * static_cast<uint64_t>(static_cast<int64_t>(n));  // mod 1 turn
-            const float t = static_cast<float>(static_cast<int32_t>(frac >> 32)) * kRadians;
-            q[0] = __cosf(t) * p.gain;
-            q[2] = __sinf(t) * p.sign;
-          } else {
-            q[0] = 1.0f;
-            q[2] = 0.0f;
-          }
-        }
-        __syncwarp();
-        Item next = it;
-        next.chunk = chunks - 1;
-        advance(next);
-#pragma unroll
-        for (int a = 0; a < 3; ++a) pos[a] = position(next, a);
+      copy_commit();
+      to = to + 1 == kRing ? 0 : to + 1;
+      if (++cf == chunks) {
+        cf = 0;
+        lf += step;
+        step_on(p.x, xp);
+        if (kBwd) step_on(p.g, gp);
       }
-      auto rotate = [&](Unit<V>& z) {
+    };
+    if constexpr (kAsync) {
 #pragma unroll
-        for (int q = 0; q < kP; ++q) {
-          const float4 t = angles[q * p.turned + u];
-          const float2 c = make_float2(t.x, t.y), s = make_float2(t.z, t.w), a = z.a[q];
-          z.a[q] = ffma2(a, c, fmul2(z.b[q], make_float2(-s.x, -s.y)));
-          z.b[q] = ffma2(a, s, fmul2(z.b[q], c));
+      for (int s = 0; s < kRing - 1; ++s) fetch();
+    }
+    const int32_t* pp = p.positions + (static_cast<size_t>(row) * p.L + l) * p.axes;
+    int32_t pos[3] = {0, 0, 0};
+    auto positions = [&](bool some) {
+#pragma unroll
+      for (int a = 0; a < 3; ++a)
+        if (some && a < p.axes) pos[a] = __ldg(pp + a);
+      pp += static_cast<size_t>(step) * p.axes;
+    };
+    positions(l < p.L);
+    for (int base = base0; base < p.L; base += step, l += step) {
+      const bool live = on && l < p.L;
+      for (int chunk = 0; chunk < chunks; ++chunk) {
+        const int h0 = hl + chunk * kM * p.hpi;
+        T vx[kAsync ? 1 : kM][kVecs]{};
+        if constexpr (kAsync) {
+          fetch();
+          copy_wait<kRing - 1>();
+        } else {
+#pragma unroll
+          for (int m = 0; m < kM; ++m) {
+            const int h = h0 + m * p.hpi;
+            if (live && h < p.Ht) {
+              const char* q = head_at(p.x, xp, h);
+              vx[kAsync ? 0 : m][0] = *reinterpret_cast<const T*>(q);
+              vx[kAsync ? 0 : m][1] = *reinterpret_cast<const T*>(q + apart);
+              if (kBwd) {
+                q = head_at(p.g, gp, h);
+                vx[kAsync ? 0 : m][kVecs - 2] = *reinterpret_cast<const T*>(q);
+                vx[kAsync ? 0 : m][kVecs - 1] = *reinterpret_cast<const T*>(q + apart);
+              }
+            }
+          }
         }
-      };
-      // the norms' sums; backward the gradient is turned back on the way
-      float r[kM], mean[kM];  // 1 / rms; backward -r^3 mean(g w x)
-      Unit<V> g[kBwd ? kM : 1];
-      if (kAny) {
-        float part[kM][kSums];
+        const T* const mine = ring + held * kM * kVecs * 32;
+        auto vec = [&](int m, int j) { return kAsync ? mine[(m * kVecs + j) * 32] : vx[kAsync ? 0 : m][j]; };
+        if (chunk == 0) {
+          // the token's angles
+          __syncwarp();
+          for (int i = in_group; i < p.turned * V; i += group) {
+            int unit, e;
+            if constexpr (kHalf || V == 1) {
+              unit = i / V;
+              e = i % V;
+            } else {
+              const int side = i >= p.D / 4, j = i - side * (p.D / 4);
+              unit = j / (V / 2);
+              e = j % (V / 2) + side * (V / 2);
+            }
+            float* q = reinterpret_cast<float*>(angles + (e / 2) * kColumn + unit) + (e & 1);
+            if (kHalf || i < p.R / 2) {
+              const int32_t n = i < p.section_1 ? pos[0] : i < p.section_2 ? pos[1] : pos[2];
+              // the product mod 2^64, its upper half: n times the lower word
+              // carries, a negative n borrows
+              const uint64_t f = __ldg(p.turns + i);
+              const uint32_t flo = static_cast<uint32_t>(f), fhi = static_cast<uint32_t>(f >> 32);
+              const uint32_t un = static_cast<uint32_t>(n);
+              const uint32_t frac = __umulhi(flo, un) + fhi * un - (n < 0 ? flo : 0u);
+              const float t = static_cast<float>(static_cast<int32_t>(frac)) * kRadians;
+              q[0] = __cosf(t) * p.gain;
+              q[2] = __sinf(t) * p.sign;
+            } else {
+              q[0] = 1.0f;
+              q[2] = 0.0f;
+            }
+          }
+          __syncwarp();
+          positions(l + step < p.L);  // the next token's
+        }
+        auto rotate = [&](Unit<V>& z) {
+#pragma unroll
+          for (int q = 0; q < kP; ++q) {
+            const float4 t = angles[q * kColumn + u];
+            const float2 c = make_float2(t.x, t.y), s = make_float2(t.z, t.w), a = z.a[q];
+            z.a[q] = ffma2(a, c, fmul2(z.b[q], make_float2(-s.x, -s.y)));
+            z.b[q] = ffma2(a, s, fmul2(z.b[q], c));
+          }
+        };
+        // the norms' sums; backward the gradient is turned back on the way
+        float r[kM], mean[kM];  // 1 / rms; backward -mean(g w xh) / rms
+        Unit<V> g[kBwd ? kM : 1];
+        if (kAny) {
+          float part[kM][kSums];
+#pragma unroll
+          for (int m = 0; m < kM; ++m) {
+            const int h = h0 + m * p.hpi;
+            const bool real = live && h < p.Ht;
+            Unit<V> x;
+            unpack<V, kHalf>(vec(m, 0), vec(m, 1), x);
+            float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int q = 0; q < kP; ++q) s = ffma2(x.a[q], x.a[q], ffma2(x.b[q], x.b[q], s));
+            part[m][0] = real ? s.x + s.y : 0.0f;
+            if (kBwd) {
+              Unit<V>& z = g[kBwd ? m : 0];
+              unpack<V, kHalf>(vec(m, kVecs - 2), vec(m, kVecs - 1), z);
+              if (turned) rotate(z);
+              s = make_float2(0.0f, 0.0f);
+#pragma unroll
+              for (int q = 0; q < kP; ++q) {
+                const float4 w = weight(m, h >= p.H, q);
+                s = ffma2(fmul2(z.a[q], make_float2(w.x, w.y)), x.a[q], s);
+                s = ffma2(fmul2(z.b[q], make_float2(w.z, w.w)), x.b[q], s);
+              }
+              part[m][kSums - 1] = real ? s.x + s.y : 0.0f;
+            }
+          }
+          if (kHead) {
+            if (p.units == 8) {
+#pragma unroll
+              for (int m = 0; m < kM; ++m)
+#pragma unroll
+                for (int k = 0; k < kSums; ++k)
+#pragma unroll
+                  for (int o = 1; o < 8; o <<= 1) part[m][k] += __shfl_xor_sync(0xffffffffu, part[m][k], o);
+            } else if (p.units <= 32) {
+#pragma unroll
+              for (int m = 0; m < kM; ++m)
+#pragma unroll
+                for (int k = 0; k < kSums; ++k) part[m][k] = head_sum(part[m][k], u, p.units);
+            } else {
+              const int n = blockDim.x;
+              __syncthreads();
+#pragma unroll
+              for (int m = 0; m < kM; ++m)
+#pragma unroll
+                for (int k = 0; k < kSums; ++k) sums_s[(m * kSums + k) * n + tid] = part[m][k];
+              __syncthreads();
+#pragma unroll
+              for (int m = 0; m < kM; ++m)
+#pragma unroll
+                for (int k = 0; k < kSums; ++k) {
+                  const float* q = sums_s + (m * kSums + k) * n + tid - u;
+                  float t = 0.0f;
+                  if (on)
+                    for (int i = 0; i < p.units; ++i) t += q[i];
+                  part[m][k] = t;
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < kM; ++m) {
+              r[m] = rsqrtf(fmaf(part[m][0], inv_nq, p.eps));
+              mean[m] = kBwd ? -r[m] * r[m] * (part[m][kSums - 1] * inv_nq) : 0.0f;
+            }
+          } else {
+            // queries and keys apart: sums of x^2 of both, then of g w x
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int m = 0; m < kM; ++m) {
+              const bool key = h0 + m * p.hpi >= p.H;
+#pragma unroll
+              for (int k = 0; k < kSums; ++k) {
+                sum[2 * k] += key ? 0.0f : part[m][k];
+                sum[2 * k + 1] += key ? part[m][k] : 0.0f;
+              }
+            }
+            if (p.team >= 32) {
+              // halves of the values are exchanged until a lane holds one
+              int o = 16;
+#pragma unroll
+              for (int n = 2 * kSums; n > 1; n >>= 1, o >>= 1) {
+                const bool up = lane32 & o;
+#pragma unroll
+                for (int j = 0; j < n / 2; ++j) {
+                  const float keep = up ? sum[j + n / 2] : sum[j], send = up ? sum[j] : sum[j + n / 2];
+                  sum[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                }
+              }
+#pragma unroll
+              for (int q = 16 / (2 * kSums); q >= 1; q >>= 1) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], q);
+              constexpr int kLanes = 32 / (2 * kSums);  // that hold one value
+              if (p.team == 32) {
+                const float t = sum[0];
+#pragma unroll
+                for (int k = 0; k < 2 * kSums; ++k) sum[k] = __shfl_sync(0xffffffffu, t, k * kLanes);
+              } else {
+                // a warp's values side by side, in two tables by turns: one
+                // barrier a token
+                float* q = sums_s + turn * (blockDim.x / 32) * 4;
+                if ((lane32 & (kLanes - 1)) == 0) q[(tid >> 5) * 4 + lane32 / kLanes] = sum[0];
+                __syncthreads();
+                const float4* t = reinterpret_cast<const float4*>(q) + slot * (p.team / 32);
+                float4 v = t[0];
+                for (int w = 1; w < p.team / 32; ++w) {
+                  const float4 x = t[w];
+                  v.x += x.x;
+                  v.y += x.y;
+                  v.z += x.z;
+                  v.w += x.w;
+                }
+                sum[0] = v.x;
+                sum[1] = v.y;
+                sum[2] = v.z;
+                sum[3] = v.w;
+                turn ^= 1;
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 2 * kSums; ++k) sum[k] = lane_sum(sum[k], group);
+            }
+            const float rq = rsqrtf(fmaf(sum[0], inv_nq, p.eps)), rk = rsqrtf(fmaf(sum[1], inv_nk, p.eps));
+            const float mq = kBwd ? -rq * rq * (sum[2] * inv_nq) : 0.0f, mk = kBwd ? -rk * rk * (sum[3] * inv_nk) : 0.0f;
+#pragma unroll
+            for (int m = 0; m < kM; ++m) {
+              const bool key = h0 + m * p.hpi >= p.H;
+              r[m] = key ? rk : rq;
+              mean[m] = key ? mk : mq;
+            }
+          }
+        }
 #pragma unroll
         for (int m = 0; m < kM; ++m) {
           const int h = h0 + m * p.hpi;
-          const bool real = live && h < p.Ht;
-          Unit<V> x;
-          unpack<V, kHalf>(vec(m, 0), vec(m, 1), x);
-          float2 s = make_float2(0.0f, 0.0f);
-#pragma unroll
-          for (int q = 0; q < kP; ++q) s = ffma2(x.a[q], x.a[q], ffma2(x.b[q], x.b[q], s));
-          part[m][0] = real ? s.x + s.y : 0.0f;
-          if (kBwd) {
-            Unit<V>& z = g[kBwd ? m : 0];
-            unpack<V, kHalf>(vec(m, kVecs - 2), vec(m, kVecs - 1), z);
-            if (turned) rotate(z);
-            s = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int q = 0; q < kP; ++q) {
-              const float4 w = weight(m, h, q);
-              s = ffma2(fmul2(z.a[q], make_float2(w.x, w.y)), x.a[q], s);
-              s = ffma2(fmul2(z.b[q], make_float2(w.z, w.w)), x.b[q], s);
-            }
-            part[m][kSums - 1] = real ? s.x + s.y : 0.0f;
-          }
-        }
-        if (kHead) {
-          if (p.units <= 32) {
-#pragma unroll
-            for (int m = 0; m < kM; ++m)
-#pragma unroll
-              for (int k = 0; k < kSums; ++k) part[m][k] = head_sum(part[m][k], u, p.units);
-          } else {
-            const int n = blockDim.x;
-            __syncthreads();
-#pragma unroll
-            for (int m = 0; m < kM; ++m)
-#pragma unroll
-              for (int k = 0; k < kSums; ++k) sums_s[(m * kSums + k) * n + tid] = part[m][k];
-            __syncthreads();
-#pragma unroll
-            for (int m = 0; m < kM; ++m)
-#pragma unroll
-              for (int k = 0; k < kSums; ++k) {
-                const float* q = sums_s + (m * kSums + k) * n + tid - u;
-                float t = 0.0f;
-                if (on)
-                  for (int i = 0; i < p.units; ++i) t += q[i];
-                part[m][k] = t;
-              }
-          }
-        } else {
-          // queries and keys apart
-          float sum[2][kSums];
-#pragma unroll
-          for (int k = 0; k < kSums; ++k) sum[0][k] = sum[1][k] = 0.0f;
-#pragma unroll
-          for (int m = 0; m < kM; ++m) {
-            const bool key = h0 + m * p.hpi >= p.H;
-#pragma unroll
-            for (int k = 0; k < kSums; ++k) {
-              sum[0][k] += key ? 0.0f : part[m][k];
-              sum[1][k] += key ? part[m][k] : 0.0f;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int k = 0; k < kSums; ++k) sum[i][k] = lane_sum(sum[i][k], group);
-          if (p.team > 32) {
-            // one float4 a warp, in two tables by turns: one barrier a token
-            const int warps = p.team / 32;
-            float4* q = reinterpret_cast<float4*>(sums_s) + turn * (blockDim.x / 32);
-            if ((tid & 31) == 0) q[tid >> 5] = make_float4(sum[0][0], sum[1][0], sum[0][kSums - 1], sum[1][kSums - 1]);
-            __syncthreads();
-            q += slot * warps;
-            float4 t = q[0];
-            for (int w = 1; w < warps; ++w) {
-              const float4 v = q[w];
-              t.x += v.x;
-              t.y += v.y;
-              t.z += v.z;
-              t.w += v.w;
-            }
-            sum[0][0] = t.x;
-            sum[1][0] = t.y;
-            sum[0][kSums - 1] = t.z;
-            sum[1][kSums - 1] = t.w;
-            if (!kBwd) {
-              sum[0][0] = t.x;
-              sum[1][0] = t.y;
-            }
-            turn ^= 1;
-          }
-#pragma unroll
-          for (int m = 0; m < kM; ++m) {
-            const bool key = h0 + m * p.hpi >= p.H;
-#pragma unroll
-            for (int k = 0; k < kSums; ++k) part[m][k] = key ? sum[1][k] : sum[0][k];
-          }
-        }
-#pragma unroll
-        for (int m = 0; m < kM; ++m) {
-          const bool key = h0 + m * p.hpi >= p.H;
-          const float inv_n = __frcp_rn(static_cast<float>(kHead ? p.D : p.D * (key ? p.Ht - p.H : p.H)));
-          r[m] = rsqrtf(fmaf(part[m][0], inv_n, p.eps));
-          mean[m] = kBwd ? -r[m] * r[m] * r[m] * (part[m][kSums - 1] * inv_n) : 0.0f;
-        }
-      }
-      char* op[2];
-      heads_at(p.out, it, op);
-#pragma unroll
-      for (int m = 0; m < kM; ++m) {
-        const int h = h0 + m * p.hpi;
-        const bool real = live && h < p.Ht;
-        {
-          Unit<V> z;
-          unpack<V, kHalf>(vec(m, 0), vec(m, 1), z);
-          if (kBwd) {
-            const Unit<V>& d = g[kBwd ? m : 0];
-            const float2 rr = make_float2(r[m], r[m]), mm = make_float2(mean[m], mean[m]);
-#pragma unroll
-            for (int q = 0; q < kP; ++q) {
-              const float4 w = weight(m, h, q);
-              const float2 zero = make_float2(0.0f, 0.0f);
-              float2 da = fmul2(fmul2(z.a[q], rr), d.a[q]), db = fmul2(fmul2(z.b[q], rr), d.b[q]);  // g xh
-              da = real ? da : zero;
-              db = real ? db : zero;
-              if (kToken) {
-                acc[kAcc > 1 ? m : 0].a[q] = fadd2(acc[kAcc > 1 ? m : 0].a[q], da);
-                acc[kAcc > 1 ? m : 0].b[q] = fadd2(acc[kAcc > 1 ? m : 0].b[q], db);
-              } else {
-                const bool key = h >= p.H;
-                acc[0].a[q] = fadd2(acc[0].a[q], key ? zero : da);
-                acc[0].b[q] = fadd2(acc[0].b[q], key ? zero : db);
-                acc[kAcc - 1].a[q] = fadd2(acc[kAcc - 1].a[q], key ? da : zero);
-                acc[kAcc - 1].b[q] = fadd2(acc[kAcc - 1].b[q], key ? db : zero);
-              }
-              z.a[q] = ffma2(fmul2(d.a[q], make_float2(w.x, w.y)), rr, fmul2(z.a[q], mm));
-              z.b[q] = ffma2(fmul2(d.b[q], make_float2(w.z, w.w)), rr, fmul2(z.b[q], mm));
-            }
-          } else {
-            if (kAny) {
-              const float2 rr = make_float2(r[m], r[m]);
+          if (live && h < p.Ht) {
+            const bool key = h >= p.H;
+            Unit<V> z;
+            unpack<V, kHalf>(vec(m, 0), vec(m, 1), z);
+            if (kBwd) {
+              const Unit<V>& d = g[kBwd ? m : 0];
+              const float2 rr = make_float2(r[m], r[m]), mm = make_float2(mean[m], mean[m]);
 #pragma unroll
               for (int q = 0; q < kP; ++q) {
-                const float4 w = weight(m, h, q);
-                z.a[q] = fmul2(fmul2(z.a[q], rr), make_float2(w.x, w.y));
-                z.b[q] = fmul2(fmul2(z.b[q], rr), make_float2(w.z, w.w));
+                const float4 w = weight(m, key, q);
+                z.a[q] = fmul2(z.a[q], rr);  // xh
+                z.b[q] = fmul2(z.b[q], rr);
+                if (kToken) {
+                  Unit<V>& s = acc[kAcc > 1 ? m : 0];
+                  s.a[q] = ffma2(z.a[q], d.a[q], s.a[q]);
+                  s.b[q] = ffma2(z.b[q], d.b[q], s.b[q]);
+                } else if (key) {
+                  acc[kAcc - 1].a[q] = ffma2(z.a[q], d.a[q], acc[kAcc - 1].a[q]);
+                  acc[kAcc - 1].b[q] = ffma2(z.b[q], d.b[q], acc[kAcc - 1].b[q]);
+                } else {
+                  acc[0].a[q] = ffma2(z.a[q], d.a[q], acc[0].a[q]);
+                  acc[0].b[q] = ffma2(z.b[q], d.b[q], acc[0].b[q]);
+                }
+                z.a[q] = ffma2(fmul2(d.a[q], make_float2(w.x, w.y)), rr, fmul2(z.a[q], mm));
+                z.b[q] = ffma2(fmul2(d.b[q], make_float2(w.z, w.w)), rr, fmul2(z.b[q], mm));
               }
+            } else {
+              if (kAny) {
+                const float2 rr = make_float2(r[m], r[m]);
+#pragma unroll
+                for (int q = 0; q < kP; ++q) {
+                  const float4 w = weight(m, key, q);
+                  z.a[q] = fmul2(fmul2(z.a[q], rr), make_float2(w.x, w.y));
+                  z.b[q] = fmul2(fmul2(z.b[q], rr), make_float2(w.z, w.w));
+                }
+              }
+              if (turned) rotate(z);
             }
-            if (turned) rotate(z);
-          }
-          T o0, o1;
-          pack<V, kHalf>(z, o0, o1);
-          if (real) {
+            T o0, o1;
+            pack<V, kHalf>(z, o0, o1);
             char* q = head_at(p.out, op, h);
             *reinterpret_cast<T*>(q) = o0;
             *reinterpret_cast<T*>(q + apart) = o1;
           }
         }
+        held = held + 1 == kRing ? 0 : held + 1;
+      }
+      step_on(p.out, op);
+      if constexpr (!kAsync) {
+        step_on(p.x, xp);
+        if (kBwd) step_on(p.g, gp);
       }
     }
-    advance(it);
-    if (++stage == kRing) stage = 0;
+    if constexpr (kAsync) copy_wait<0>();
   }
-  if constexpr (kAsync) copy_wait<0>();
   if (kBwd) {
     if (p.part == nullptr) return;
     constexpr int kValues = V > 1 ? 2 * V : 2;
@@ -716,7 +738,7 @@ bool team_of(int V, int kM, int Ht, int D, int norm, Shape* s) {
     // heads that the rounding leaves room for
     s->hpi = std::min(Ht, per ? s->team / 32 * per : s->team / s->units);
   }
-  s->teams = s->team >= 128 ? 1 : 128 / s->team;
+  s->teams = s->team >= 128 ? 1 : (s->team < 32 ? 64 : 128) / s->team;
   s->threads = s->team * s->teams;
   return true;
 }
@@ -776,7 +798,7 @@ pvl_status launch(const RotaryParams& p, const Shape& sh, int norm, bool bwd, bo
   const void* fn = find_kernel(sh, norm, bwd, half);
   if (!fn) return fail(PVL_ERR_UNSUPPORTED, "%s: no kernel for this shape", who);
   const size_t smem =
-      sizeof(float) * smem_plan(sh.V, sh.kM, norm, bwd, p.turned, p.D, sh.units, sh.hpi, sh.team, sh.teams, sh.threads).total;
+      sizeof(float) * smem_plan(sh.V, sh.kM, norm, bwd, p.D, sh.units, sh.hpi, sh.team, sh.teams, sh.threads).total;
   pvl_status st = PVL_OK;
   if (smem > 48 * 1024) {
     st = check_cuda(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)), who);
@@ -793,6 +815,8 @@ pvl_status launch(const RotaryParams& p, const Shape& sh, int norm, bool bwd, bo
   const long long gx = std::min<long long>(grid / gy, (static_cast<long long>(p.L) + p.teams - 1) / p.teams);
   *grid_out = static_cast<int>(gx * gy);
   RotaryParams q = p;
+  for (View* v : {q.x, q.g, q.out})
+    for (int i = 0; i < 2; ++i) v[i].step = gx * p.teams * v[i].l;
   void* args[] = {&q};
   return check_cuda(cudaLaunchKernel(fn, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), dim3(sh.threads),
                                      args, smem, s),
@@ -863,7 +887,7 @@ pvl_status common(const char* who, const pvl_rotary* a, RotaryParams& p) {
   if (a->Hk == 0 && a->k_weight) return fail(PVL_ERR_INVALID_ARG, "%s: k_weight without keys", who);
   if (static_cast<long long>(a->H) + a->Hk > PVL_MAX_ROTARY_HEADS)
     return fail(PVL_ERR_UNSUPPORTED, "%s: %d + %d heads", who, a->H, a->Hk);
-  if (static_cast<long long>(a->B) * a->L >= (1ll << 31))
+  if (static_cast<long long>(a->B) * a->L >= (1ll << 30))
     return fail(PVL_ERR_UNSUPPORTED, "%s: too many tokens", who);
   p.turns = a->turns;
   p.positions = a->positions;
@@ -887,7 +911,7 @@ pvl_status common(const char* who, const pvl_rotary* a, RotaryParams& p) {
 bool view(const pvl_heads* h, View* v) {
   if (!h) return true;
   if (h->stride_h >= 1 << 30 || h->stride_h <= -(1 << 30)) return false;
-  *v = View{static_cast<char*>(h->data), 2 * h->stride_b, 2 * h->stride_l, static_cast<int32_t>(2 * h->stride_h)};
+  *v = View{static_cast<char*>(h->data), 2 * h->stride_b, 2 * h->stride_l, 0, static_cast<int32_t>(2 * h->stride_h)};
   return true;
 }
 
@@ -909,6 +933,7 @@ void fill(RotaryParams& p, const pvl_rotary* a, const Shape& s) {
   p.units = s.units;
   p.turned = a->layout == PVL_ROTARY_HALF ? a->R / (2 * s.V) : s.units;
   p.hpi = s.hpi;
+  p.chunks = (p.Ht + s.kM * s.hpi - 1) / (s.kM * s.hpi);
   p.team = s.team;
   p.teams = s.teams;
   p.width = a->norm == PVL_NORM_TOKEN ? (a->H + a->Hk) * a->D : 2 * a->D;
