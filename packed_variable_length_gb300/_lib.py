@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpvl.so")
 
@@ -16,34 +17,12 @@ _c_size = ctypes.c_size_t
 _c_float = ctypes.c_float
 _p = ctypes.c_void_p
 
-_i32 = ctypes.c_int32
-
-
-class Rotary(ctypes.Structure):
-    """pvl_rotary"""
-    _fields_ = [("B", _i32), ("L", _i32), ("H", _i32), ("Hk", _i32), ("D", _i32), ("R", _i32), ("layout", _i32),
-                ("axes", _i32), ("section_1", _i32), ("section_2", _i32), ("gain", _c_float), ("norm", _i32),
-                ("eps", _c_float), ("turns", _p), ("positions", _p), ("q_weight", _p), ("k_weight", _p)]
-
-
-class Heads(ctypes.Structure):
-    """pvl_heads"""
-    _fields_ = [("data", _p), ("stride_b", ctypes.c_int64), ("stride_l", ctypes.c_int64),
-                ("stride_h", ctypes.c_int64)]
-
-
-class Residual(ctypes.Structure):
-    """pvl_residual"""
-    _fields_ = [("B", _i32), ("N", _i32), ("D", _i32), ("S", _i32), ("stream_dtype", _i32), ("norm", _i32),
-                ("post_norm", _i32), ("alpha", _c_float), ("eps", _c_float), ("gate", _p), ("shift", _p),
-                ("scale", _p), ("weight", _p), ("bias", _p), ("post_weight", _p), ("mod_id", _p)]
-
-
-class ResidualGrads(ctypes.Structure):
-    """pvl_residual_grads"""
-    _fields_ = [("dgate", _p), ("dshift", _p), ("dscale", _p), ("dweight", _p), ("dbias", _p),
-                ("dpost_weight", _p)]
-
+# Descriptions passed by pointer, packed into bytes (a bytes object is taken
+# as a pointer argument): native alignment, as the C compiler lays them out.
+PACK_ROTARY = struct.Struct("@10ififPPPP").pack        # pvl_rotary
+PACK_HEADS = struct.Struct("@Pqqq").pack               # pvl_heads
+PACK_RESIDUAL = struct.Struct("@7iffPPPPPPP").pack     # pvl_residual
+PACK_RESIDUAL_GRADS = struct.Struct("@PPPPPP").pack    # pvl_residual_grads
 
 # name -> (restype, argtypes); mirrors include/pvl.h
 SIGNATURES = {

@@ -61,17 +61,38 @@ def _need_cuda(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> No
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _need(t, name: str, dtype: torch.dtype, shape) -> None:
+    """_need_cuda at the price of four attribute reads where all is well."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous() and t.shape == shape):
+        _need_cuda(t, name, dtype, shape)
+
+
 def _need_same_device(device, **tensors) -> None:
     for name, t in tensors.items():
         if t is not None and t.device != device:
             raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
+_current_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+class _Here:
+    """The current device and stream: nothing to set, nothing to restore."""
+    __slots__ = ("handle",)
+
+    def __init__(self, handle):
+        self.handle = handle
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *exc):
+        return False
+
+
 @contextlib.contextmanager
-def _launch(device, stream):
-    """Makes the device current and, with a stream given, that stream, so that
-    what is allocated inside belongs to the stream the kernels run on; yields
-    the stream's handle."""
+def _there(device, stream):
     with torch.cuda.device(device):
         if stream is None:
             yield torch.cuda.current_stream().cuda_stream
@@ -80,6 +101,17 @@ def _launch(device, stream):
                 stream = torch.cuda.ExternalStream(_stream(stream))
             with torch.cuda.stream(stream):
                 yield stream.cuda_stream
+
+
+def _launch(device, stream):
+    """Context that makes the device current and, with a stream given, that
+    stream, so that what is allocated inside belongs to the stream the kernels
+    run on; gives the stream's handle."""
+    if stream is None:
+        index = torch.cuda.current_device()
+        if device.index is None or device.index == index:
+            return _Here(_current_stream_handle(index))
+    return _there(device, stream)
 
 
 # ------------------------------------------------------------------ seq_ids
@@ -106,7 +138,7 @@ def pack_build_positions(seg_frames, tokens_per_frame: int, L: int, axes: int = 
     from the host [B, K] frame table: its offset (axes=1), its frame and its
     token of the frame (2), or its frame, row and column with row_width tokens
     a row (3).  Positions restart in every segment; the tail gets zeros."""
-    frames = np.ascontiguousarray(np.asarray(seg_frames, dtype=np.int32))
+    frames = np.asarray(seg_frames, dtype=np.int32)
     if frames.ndim != 2:
         raise ValueError("seg_frames must be [B, K]")
     if axes == 3 and row_width is None:
@@ -116,8 +148,9 @@ def pack_build_positions(seg_frames, tokens_per_frame: int, L: int, axes: int = 
     with _launch(device, stream) as handle:
         if out is None:
             out = torch.empty((B, int(L), int(axes)), dtype=torch.int32, device=device)
-        _need_cuda(out, "out", torch.int32, (B, int(L), int(axes)))
-        _check(_lib.load().pack_build_positions(frames.ctypes.data, B, K, int(tokens_per_frame), int(axes),
+        else:
+            _need(out, "out", torch.int32, (B, int(L), int(axes)))
+        _check(_lib.load().pack_build_positions(frames.tobytes(), B, K, int(tokens_per_frame), int(axes),
                                                 int(row_width or 1), int(L), out.data_ptr(), handle))
     return out
 
@@ -449,8 +482,10 @@ def rotary_plan(rotary_dim: int, base: float = 10000.0, layout: str = "half", se
             b = Decimal(base)
             if scaling == "ntk" and n > 1:
                 b *= (s.ln() * n / (n - 1)).exp()
+            ratio, power = (-b.ln() / n).exp() if n else Decimal(1), Decimal(1)
             for j in range(n):
-                t = (-b.ln() * j / n).exp() / _TWO_PI
+                t = power / _TWO_PI
+                power *= ratio
                 if scaling == "linear":
                     t /= s
                 elif scaling == "parts":
@@ -465,18 +500,24 @@ def rotary_plan(rotary_dim: int, base: float = 10000.0, layout: str = "half", se
     return RotaryPlan(table, R, layout, sections, float(gain))
 
 
-def _heads_view(t: torch.Tensor, name: str, shape) -> _lib.Heads:
+def _heads_view(t, name: str, shape) -> bytes | None:
+    if t is None:
+        return None
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     sb, sl, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    B, L, H, _ = t.shape  # the stride of a single entry means nothing
-    return _lib.Heads(t.data_ptr(), sb if B > 1 else 0, sl if L > 1 else 0, sh if H > 1 else 0)
+    B, L, H, _ = shape  # the stride of a single entry means nothing
+    return _lib.PACK_HEADS(t.data_ptr(), sb if B > 1 else 0, sl if L > 1 else 0, sh if H > 1 else 0)
+
+
+def _addr(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _rotary(like_q, like_k, positions, plan: RotaryPlan, norm, q_weight, k_weight, eps):
@@ -485,20 +526,20 @@ def _rotary(like_q, like_k, positions, plan: RotaryPlan, norm, q_weight, k_weigh
         raise ValueError("q and k must be [B, L, heads, D]")
     B, L, H, D = like_q.shape
     Hk = 0 if like_k is None else int(like_k.shape[2])
-    if like_k is not None and (tuple(like_k.shape) != (B, L, Hk, D) or Hk < 1):
+    if like_k is not None and (like_k.shape != (B, L, Hk, D) or Hk < 1):
         raise ValueError(f"k must be [{B}, {L}, Hk, {D}], got {tuple(like_k.shape)}")
     if norm not in (None, "head", "token"):
         raise ValueError(f"norm must be None, 'head' or 'token', got {norm!r}")
     axes = len(plan.sections)
     if axes == 1 and positions.dim() == 2:
         positions = positions.unsqueeze(2)
-    _need_cuda(positions, "positions", torch.int32, (B, L, axes))
+    _need(positions, "positions", torch.int32, (B, L, axes))
     for name, w, n in (("q_weight", q_weight, H), ("k_weight", k_weight, Hk)):
         if w is None:
             continue
         if norm is None or (n == 0):
             raise ValueError(f"{name} needs a norm and its heads")
-        _need_cuda(w, name, torch.float32)
+        _need(w, name, torch.float32, w.shape)
         if w.numel() != (n * D if norm == "token" else D):
             raise ValueError(f"{name} must hold {n * D if norm == 'token' else D} values, got {w.numel()}")
     _need_same_device(like_q.device, k=like_k, positions=positions, plan=plan.turns, q_weight=q_weight,
@@ -506,9 +547,10 @@ def _rotary(like_q, like_k, positions, plan: RotaryPlan, norm, q_weight, k_weigh
     s = plan.sections
     s1 = s[0]
     s2 = s1 + (s[1] if axes > 1 else 0)
-    return _lib.Rotary(B, L, H, Hk, D, plan.rotary_dim, 0 if plan.layout == "half" else 1, axes, s1, s2, plan.gain,
-                       _NORMS[norm], float(eps), plan.turns.data_ptr(), positions.data_ptr(), _ptr(q_weight),
-                       _ptr(k_weight)), (B, L, H, D), (B, L, Hk, D)
+    how = _lib.PACK_ROTARY(B, L, H, Hk, D, plan.rotary_dim, 0 if plan.layout == "half" else 1, axes, s1, s2, plan.gain,
+                           _NORMS[norm], float(eps), plan.turns.data_ptr(), positions.data_ptr(), _addr(q_weight),
+                           _addr(k_weight))
+    return how, (B, L, H, D), (B, L, Hk, D)
 
 
 def pack_rotary_fwd(q, k, positions, plan: RotaryPlan, norm: str | None = None, q_weight=None, k_weight=None,
@@ -526,11 +568,10 @@ def pack_rotary_fwd(q, k, positions, plan: RotaryPlan, norm: str | None = None, 
             q_out = torch.empty(qs, dtype=q.dtype, device=q.device)
         if k is not None and k_out is None:
             k_out = torch.empty(ks, dtype=k.dtype, device=k.device)
-        views = [_heads_view(q, "q", qs), None if k is None else _heads_view(k, "k", ks),
-                 _heads_view(q_out, "q_out", qs), None if k is None else _heads_view(k_out, "k_out", ks)]
-        _check(_lib.load().pack_rotary_fwd(ctypes.byref(how), *(None if v is None else ctypes.byref(v) for v in views),
-                                           handle))
-    return q_out, k_out
+        _check(_lib.load().pack_rotary_fwd(how, _heads_view(q, "q", qs), _heads_view(k, "k", ks),
+                                           _heads_view(q_out, "q_out", qs),
+                                           None if k is None else _heads_view(k_out, "k_out", ks), handle))
+    return q_out, (None if k is None else k_out)
 
 
 def pack_rotary_bwd(dq_out, dk_out, positions, plan: RotaryPlan, norm: str | None = None, q=None, k=None,
@@ -553,13 +594,11 @@ def pack_rotary_bwd(dq_out, dk_out, positions, plan: RotaryPlan, norm: str | Non
             dk = torch.empty(ks, dtype=dk_out.dtype, device=dk_out.device)
         dq_weight = None if q_weight is None else torch.empty_like(q_weight)
         dk_weight = None if k_weight is None else torch.empty_like(k_weight)
-        nbytes = int(lib.pack_rotary_bwd_ws_bytes(ctypes.byref(how)))
+        nbytes = int(lib.pack_rotary_bwd_ws_bytes(how))
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dq_out.device) if nbytes else None
-        views = [_heads_view(dq_out, "dq_out", qs), _heads_view(dk_out, "dk_out", ks) if keys else None,
-                 None if q is None else _heads_view(q, "q", qs),
-                 _heads_view(k, "k", ks) if keys and k is not None else None,
-                 _heads_view(dq, "dq", qs), _heads_view(dk, "dk", ks) if keys else None]
-        _check(lib.pack_rotary_bwd(ctypes.byref(how), *(None if v is None else ctypes.byref(v) for v in views),
+        _check(lib.pack_rotary_bwd(how, _heads_view(dq_out, "dq_out", qs), _heads_view(dk_out, "dk_out", ks),
+                                   _heads_view(q, "q", qs), _heads_view(k, "k", ks) if keys else None,
+                                   _heads_view(dq, "dq", qs), _heads_view(dk, "dk", ks) if keys else None,
                                    _ptr(dq_weight), _ptr(dk_weight), _ptr(ws), nbytes, handle))
     return dq, (dk if keys else None), dq_weight, dk_weight
 
@@ -584,7 +623,7 @@ def _residual(x, gate, shift, scale, mod_id, weight, bias, post_weight, norm, po
     B, N, D = x.shape
     if x.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"x must be {torch.bfloat16} or {torch.float32}, got {x.dtype}")
-    _need_cuda(x, "x", x.dtype, (B, N, D))
+    _need(x, "x", x.dtype, x.shape)
     if norm not in ("layer", "rms"):
         raise ValueError(f"norm must be 'layer' or 'rms', got {norm!r}")
     if post_norm not in (None, "layer", "rms"):
@@ -596,19 +635,19 @@ def _residual(x, gate, shift, scale, mod_id, weight, bias, post_weight, norm, po
         if t.dim() != 2:
             raise ValueError(f"{name} must be [S, D]")
         S = int(t.shape[0]) if S is None else S
-        _need_cuda(t, name, torch.float32, (S, D))
+        _need(t, name, torch.float32, (S, D))
     if mod_id is not None:
-        _need_cuda(mod_id, "mod_id", torch.int32, (B, N))
+        _need(mod_id, "mod_id", torch.int32, (B, N))
     elif S is not None and S != B:
         raise ValueError(f"without mod_id the modulation tables must have B = {B} rows, got {S}")
     for name, t in (("weight", weight), ("bias", bias), ("post_weight", post_weight)):
         if t is not None:
-            _need_cuda(t, name, torch.float32, (D,))
+            _need(t, name, torch.float32, (D,))
     _need_same_device(x.device, gate=gate, shift=shift, scale=scale, mod_id=mod_id, weight=weight, bias=bias,
                       post_weight=post_weight)
-    return _lib.Residual(B, N, D, S or 1, 1 if x.dtype == torch.float32 else 0, _NORMS[norm], _NORMS[post_norm],
-                         float(alpha), float(eps), _ptr(gate), _ptr(shift), _ptr(scale), _ptr(weight), _ptr(bias),
-                         _ptr(post_weight), _ptr(mod_id)), S or 1
+    return _lib.PACK_RESIDUAL(B, N, D, S or 1, 1 if x.dtype == torch.float32 else 0, _NORMS[norm], _NORMS[post_norm],
+                         float(alpha), float(eps), _addr(gate), _addr(shift), _addr(scale), _addr(weight), _addr(bias),
+                         _addr(post_weight), _addr(mod_id)), S or 1
 
 
 def adaln_residual_fwd(x, h=None, gate=None, shift=None, scale=None, *, mod_id=None, weight=None, bias=None,
@@ -626,7 +665,7 @@ def adaln_residual_fwd(x, h=None, gate=None, shift=None, scale=None, *, mod_id=N
     Without h, x_out is x itself and y its modulated norm."""
     how, _ = _residual(x, gate, shift, scale, mod_id, weight, bias, post_weight, norm, post_norm, alpha, eps)
     if h is not None:
-        _need_cuda(h, "h", torch.bfloat16, x.shape)
+        _need(h, "h", torch.bfloat16, x.shape)
     _need_same_device(x.device, h=h, x_out=x_out, y=y)
     with _launch(x.device, stream) as handle:
         if h is None:
@@ -635,9 +674,9 @@ def adaln_residual_fwd(x, h=None, gate=None, shift=None, scale=None, *, mod_id=N
             x_out = torch.empty_like(x)
         if y is None:
             y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-        _need_cuda(x_out, "x_out", x.dtype, x.shape)
-        _need_cuda(y, "y", torch.bfloat16, x.shape)
-        _check(_lib.load().adaln_residual_fwd(ctypes.byref(how), x.data_ptr(), _ptr(h), x_out.data_ptr(), y.data_ptr(),
+        _need(x_out, "x_out", x.dtype, x.shape)
+        _need(y, "y", torch.bfloat16, x.shape)
+        _check(_lib.load().adaln_residual_fwd(how, x.data_ptr(), _ptr(h), x_out.data_ptr(), y.data_ptr(),
                                               handle))
     return x_out, y
 
@@ -660,10 +699,10 @@ def adaln_residual_bwd(dx_out, dy, x_out, h=None, gate=None, shift=None, scale=N
     B, N, D = x_out.shape
     branch = h is not None if branch is None else bool(branch)
     if h is not None:
-        _need_cuda(h, "h", torch.bfloat16, x_out.shape)
-    _need_cuda(dy, "dy", torch.bfloat16, x_out.shape)
+        _need(h, "h", torch.bfloat16, x_out.shape)
+    _need(dy, "dy", torch.bfloat16, x_out.shape)
     if dx_out is not None:
-        _need_cuda(dx_out, "dx_out", x_out.dtype, x_out.shape)
+        _need(dx_out, "dx_out", x_out.dtype, x_out.shape)
     _need_same_device(x_out.device, h=h, dy=dy, dx_out=dx_out, dx=dx, dh=dh, ws=ws)
     lib = _lib.load()
     with _launch(x_out.device, stream) as handle:
@@ -671,16 +710,16 @@ def adaln_residual_bwd(dx_out, dy, x_out, h=None, gate=None, shift=None, scale=N
             dx = torch.empty_like(x_out)
         if branch and dh is None:
             dh = torch.empty(x_out.shape, dtype=torch.bfloat16, device=x_out.device)
-        _need_cuda(dx, "dx", x_out.dtype, x_out.shape)
+        _need(dx, "dx", x_out.dtype, x_out.shape)
         if branch:
-            _need_cuda(dh, "dh", torch.bfloat16, x_out.shape)
+            _need(dh, "dh", torch.bfloat16, x_out.shape)
         params = (gate, shift, scale, weight, bias, post_weight)
         grads = [None if t is None else torch.empty_like(t) for t in params]
         if ws is None:
             ws = torch.empty(adaln_residual_bwd_ws_bytes(B, N, D, S), dtype=torch.uint8, device=x_out.device)
-        out = _lib.ResidualGrads(*(_ptr(t) for t in grads))
-        _check(lib.adaln_residual_bwd(ctypes.byref(how), _ptr(dx_out), dy.data_ptr(), x_out.data_ptr(), _ptr(h),
-                                      int(branch), dx.data_ptr(), _ptr(dh) if branch else None, ctypes.byref(out),
+        out = _lib.PACK_RESIDUAL_GRADS(*(_addr(t) for t in grads))
+        _check(lib.adaln_residual_bwd(how, _ptr(dx_out), dy.data_ptr(), x_out.data_ptr(), _ptr(h),
+                                      int(branch), dx.data_ptr(), _ptr(dh) if branch else None, out,
                                       ws.data_ptr(), ws.numel(), handle))
     return AdalnResidualGrads(dx, dh if branch else None, *grads)
 

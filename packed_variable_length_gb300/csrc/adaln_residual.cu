@@ -999,14 +999,9 @@ pvl_status launch_rows(ResidualParams p, cudaStream_t s, const char* who) {
     threads += 32 * (p.stats_warps + 1);
   }
   const int stage_bytes = static_cast<int>(Stage<TX, kBwd>(p.D).bytes());
-  int dev = 0, smem_sm = 0, occ = 0;
-  const int sms = sm_count();
-  pvl_status st = check_cuda(cudaGetDevice(&dev), who);
-  if (st == PVL_OK)
-    st = check_cuda(cudaDeviceGetAttribute(&smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev), who);
-  if (st == PVL_OK) st = check_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, threads, 0), who);
-  if (st != PVL_OK) return st;
-  if (sms <= 0 || occ <= 0) return fail(PVL_ERR_CUDA, "%s: no usable CUDA device", who);
+  const int sms = sm_count(), smem_sm = smem_per_sm();
+  int occ = blocks_per_sm(fn, threads, 0);
+  if (sms <= 0 || smem_sm <= 0 || occ <= 0) return fail(PVL_ERR_CUDA, "%s: no usable CUDA device", who);
   constexpr int kReserve = 1024 + static_cast<int>(align128(kBwd ? sizeof(BwdShared) : sizeof(Shared)));  // per CTA: the system's share, static
   const int table_bytes = kBwd ? static_cast<int>(align128(4 * p.D)) * (kBranch == kPost ? 2 : 1) : 0;
   int stages = 0;
@@ -1034,8 +1029,8 @@ pvl_status launch_rows(ResidualParams p, cudaStream_t s, const char* who) {
   if (p.stages > p.rows_per_cta) p.stages = p.rows_per_cta < 2 ? 2 : static_cast<int>(p.rows_per_cta);
   if (p.stats_warps > p.stages) p.stats_warps = p.stages;  // the others find no stage
   const int smem = p.stages * stage_bytes + p.tables * table_bytes;
-  st = check_cuda(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), who);
-  if (st != PVL_OK) return st;
+  // the exact size, so that the kernel is allowed it
+  if (blocks_per_sm(fn, threads, smem) <= 0) return fail(PVL_ERR_CUDA, "%s: no usable CUDA device", who);
   if constexpr (kBwd) residual_bwd_kernel<TX, kV, kRegs, kBranch><<<static_cast<unsigned>(grid), threads, smem, s>>>(p);
   else residual_fwd_kernel<TX, kV, kRegs, kBranch><<<static_cast<unsigned>(grid), threads, smem, s>>>(p);
   return check_cuda(cudaGetLastError(), who);

@@ -127,6 +127,12 @@ pvl_status fail(pvl_status s, const char* fmt, ...);
 pvl_status check_cuda(int err, const char* what);  // err is a cudaError_t
 DeviceError* device_error_record();                // current device, null on failure
 int sm_count();                                    // current device, 0 on failure
+// Blocks of `fn` that fit an SM of the current device at `threads` threads and
+// `smem` bytes of dynamic shared memory, which the kernel is allowed on the
+// way; asked of the runtime once for each such triple.  0 on failure.
+int blocks_per_sm(const void* fn, int threads, size_t smem);
+// Shared memory of an SM of the current device, 0 on failure.
+int smem_per_sm();
 // Bound on any single wait of the attention kernels launched now
 // (kDefaultTimeoutNs unless pvl_set_attn_wait_timeout_ns changed it).
 uint64_t attn_wait_timeout_ns();

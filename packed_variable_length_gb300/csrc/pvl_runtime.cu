@@ -84,6 +84,57 @@ int sm_count() {
   return g_sms[dev];
 }
 
+namespace {
+struct ShapeKey {
+  const void* fn;
+  int threads, dev;
+  size_t smem;
+  bool operator==(const ShapeKey& o) const {
+    return fn == o.fn && threads == o.threads && dev == o.dev && smem == o.smem;
+  }
+};
+struct ShapeHash {
+  size_t operator()(const ShapeKey& k) const {
+    return std::hash<const void*>{}(k.fn) ^ (k.smem * 0x9E3779B97F4A7C15ull) ^ (static_cast<size_t>(k.threads) << 20) ^
+           static_cast<size_t>(k.dev);
+  }
+};
+std::unordered_map<ShapeKey, int, ShapeHash> g_blocks;
+std::unordered_map<ShapeKey, size_t, ShapeHash> g_allowed;  // threads = smem = 0: most dynamic shared memory allowed
+int g_smem_sm[kMaxDevices] = {};
+}  // namespace
+
+int blocks_per_sm(const void* fn, int threads, size_t smem) {
+  const int dev = current_device();
+  if (dev < 0) return 0;
+  std::lock_guard<std::mutex> lock(g_mu);
+  const ShapeKey key{fn, threads, dev, smem};
+  const auto found = g_blocks.find(key);
+  if (found != g_blocks.end()) return found->second;
+  size_t& allowed = g_allowed[ShapeKey{fn, 0, dev, 0}];
+  if (smem > 32 * 1024 && smem > allowed) {  // 48 KB together with the static part need no leave
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+      return 0;
+    allowed = smem;
+  }
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem) != cudaSuccess) return 0;
+  if (n > 0) g_blocks.emplace(key, n);
+  return n;
+}
+
+int smem_per_sm() {
+  const int dev = current_device();
+  if (dev < 0) return 0;
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (!g_smem_sm[dev]) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev) != cudaSuccess) return 0;
+    g_smem_sm[dev] = n;
+  }
+  return g_smem_sm[dev];
+}
+
 uint64_t attn_wait_timeout_ns() { return g_attn_wait_ns.load(std::memory_order_relaxed); }
 
 unsigned int* fwd_sched_counter(void* stream) {

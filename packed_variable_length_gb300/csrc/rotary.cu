@@ -240,9 +240,12 @@ __host__ __device__ inline SmemPlan smem_plan(int V, int kM, int norm, bool bwd,
   return s;
 }
 
-// kNorm: PVL_NORM_NONE, _HEAD or _TOKEN; kBwd only with a norm.
+// kNorm: PVL_NORM_NONE, _HEAD or _TOKEN; kBwd only with a norm.  Forward takes
+// 96 registers: left to itself the compiler stays at 64 for the sake of warps
+// that the shared memory leaves no room for (norm per head, 64k pack: 154 us
+// at 64, 132 at 96).
 template <int V, int kM, int kNorm, bool kBwd, bool kHalf>
-__global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __maxnreg__(kBwd ? 128 : 96) rotary_kernel(const __grid_constant__ RotaryParams p) {
   using T = typename Vec<V>::T;
   constexpr int kP = Unit<V>::kP, kColumn = kMaxD / (2 * V);
   constexpr bool kHead = kNorm == PVL_NORM_HEAD, kToken = kNorm == PVL_NORM_TOKEN, kAny = kHead || kToken;
@@ -385,22 +388,22 @@ __global__ void __launch_bounds__(kMaxBlock) rotary_kernel(const __grid_constant
       const bool live = on && l < p.L;
       for (int chunk = 0; chunk < chunks; ++chunk) {
         const int h0 = hl + chunk * kM * p.hpi;
-        T vx[kAsync ? 1 : kM][kVecs]{};
+        T vx[kAsync ? 1 : kM][kVecs];
+        if (kAsync) vx[0][0] = vx[0][1] = T{};  // not used
         if constexpr (kAsync) {
           fetch();
           copy_wait<kRing - 1>();
         } else {
 #pragma unroll
           for (int m = 0; m < kM; ++m) {
-            const int h = h0 + m * p.hpi;
-            if (live && h < p.Ht) {
-              const char* q = head_at(p.x, xp, h);
+            const int h = min(h0 + m * p.hpi, p.Ht - 1);
+            const char *q = head_at(p.x, xp, h), *d = kBwd ? head_at(p.g, gp, h) : nullptr;
+            if (live) {
               vx[kAsync ? 0 : m][0] = *reinterpret_cast<const T*>(q);
               vx[kAsync ? 0 : m][1] = *reinterpret_cast<const T*>(q + apart);
               if (kBwd) {
-                q = head_at(p.g, gp, h);
-                vx[kAsync ? 0 : m][kVecs - 2] = *reinterpret_cast<const T*>(q);
-                vx[kAsync ? 0 : m][kVecs - 1] = *reinterpret_cast<const T*>(q + apart);
+                vx[kAsync ? 0 : m][kVecs - 2] = *reinterpret_cast<const T*>(d);
+                vx[kAsync ? 0 : m][kVecs - 1] = *reinterpret_cast<const T*>(d + apart);
               }
             }
           }
@@ -799,15 +802,7 @@ pvl_status launch(const RotaryParams& p, const Shape& sh, int norm, bool bwd, bo
   if (!fn) return fail(PVL_ERR_UNSUPPORTED, "%s: no kernel for this shape", who);
   const size_t smem =
       sizeof(float) * smem_plan(sh.V, sh.kM, norm, bwd, p.D, sh.units, sh.hpi, sh.team, sh.teams, sh.threads).total;
-  pvl_status st = PVL_OK;
-  if (smem > 48 * 1024) {
-    st = check_cuda(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)), who);
-    if (st != PVL_OK) return st;
-  }
-  int occ = 0;
-  st = check_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, sh.threads, smem), who);
-  if (st != PVL_OK) return st;
-  const int sms = sm_count();
+  const int occ = blocks_per_sm(fn, sh.threads, smem), sms = sm_count();
   if (sms <= 0 || occ <= 0) return fail(PVL_ERR_CUDA, "%s: no usable CUDA device", who);
   long long grid = static_cast<long long>(occ) * sms;
   if (grid > grid_limit) grid = grid_limit;
