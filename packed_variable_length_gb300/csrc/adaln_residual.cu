@@ -1022,7 +1022,7 @@ pvl_status launch_rows(ResidualParams p, cudaStream_t s, const char* who) {
   if (occ < 1) return fail(PVL_ERR_UNSUPPORTED, "%s: D = %d does not fit in shared memory", who, p.D);
   p.stages = stages < kMaxStages ? stages : kMaxStages;
   long long grid = static_cast<long long>(occ) * sms;
-  if (grid > kMaxCtas) grid = kMaxCtas;
+  if (kBwd && grid > kMaxCtas) grid = kMaxCtas;
   if (grid > p.rows) grid = p.rows;
   p.rows_per_cta = (p.rows + grid - 1) / grid;
   grid = (p.rows + p.rows_per_cta - 1) / p.rows_per_cta;

@@ -95,18 +95,50 @@ struct Vec<1> {
 __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// A unit's values: kP packed pairs of first and of second sides.
+// A unit's values: kP packed pairs of first and of second sides (one plain
+// pair where V is 1), and the arithmetic on either kind.
 template <int V>
 struct Unit {
-  static constexpr int kP = V > 1 ? V / 2 : 1;
-  float2 a[kP], b[kP];
+  using F = float2;
+  static constexpr int kP = V / 2;
+  F a[kP], b[kP];
 };
+template <>
+struct Unit<1> {
+  using F = float;
+  static constexpr int kP = 1;
+  F a[1], b[1];
+};
+using pvl::ffma2;
+using pvl::fmul2;
+__device__ __forceinline__ float fmul2(float a, float b) { return a * b; }
+__device__ __forceinline__ float ffma2(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float both_of(float2 v) { return v.x + v.y; }
+__device__ __forceinline__ float both_of(float v) { return v; }
+template <typename F>
+__device__ __forceinline__ F splat(float v) {
+  if constexpr (sizeof(F) == 8) return make_float2(v, v);
+  else return v;
+}
+// first and second sides of a pair's (a.x, a.y, b.x, b.y)
+template <typename F>
+__device__ __forceinline__ F side_a(const float4& t) {
+  if constexpr (sizeof(F) == 8) return make_float2(t.x, t.y);
+  else return t.x;
+}
+template <typename F>
+__device__ __forceinline__ F side_b(const float4& t) {
+  if constexpr (sizeof(F) == 8) return make_float2(t.z, t.w);
+  else return t.z;
+}
+__device__ __forceinline__ float2 minus(float2 v) { return make_float2(-v.x, -v.y); }
+__device__ __forceinline__ float minus(float v) { return -v; }
 
 template <int V, bool kHalf>
 __device__ __forceinline__ void unpack(const typename Vec<V>::T& u0, const typename Vec<V>::T& u1, Unit<V>& z) {
   if constexpr (V == 1) {
-    z.a[0] = make_float2(__uint_as_float(static_cast<uint32_t>(u0) << 16), 0.0f);
-    z.b[0] = make_float2(__uint_as_float(static_cast<uint32_t>(u1) << 16), 0.0f);
+    z.a[0] = __uint_as_float(static_cast<uint32_t>(u0) << 16);
+    z.b[0] = __uint_as_float(static_cast<uint32_t>(u1) << 16);
   } else {
     const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&u0);
     const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&u1);
@@ -127,8 +159,8 @@ __device__ __forceinline__ void unpack(const typename Vec<V>::T& u0, const typen
 template <int V, bool kHalf>
 __device__ __forceinline__ void pack(const Unit<V>& z, typename Vec<V>::T& u0, typename Vec<V>::T& u1) {
   if constexpr (V == 1) {
-    u0 = __bfloat16_as_ushort(__float2bfloat16_rn(z.a[0].x));
-    u1 = __bfloat16_as_ushort(__float2bfloat16_rn(z.b[0].x));
+    u0 = __bfloat16_as_ushort(__float2bfloat16_rn(z.a[0]));
+    u1 = __bfloat16_as_ushort(__float2bfloat16_rn(z.b[0]));
   } else {
     uint32_t* w0 = reinterpret_cast<uint32_t*>(&u0);
     uint32_t* w1 = reinterpret_cast<uint32_t*>(&u1);
@@ -247,6 +279,7 @@ __host__ __device__ inline SmemPlan smem_plan(int V, int kM, int norm, bool bwd,
 template <int V, int kM, int kNorm, bool kBwd, bool kHalf>
 __global__ void __maxnreg__(kBwd ? 128 : 96) rotary_kernel(const __grid_constant__ RotaryParams p) {
   using T = typename Vec<V>::T;
+  using F = typename Unit<V>::F;
   constexpr int kP = Unit<V>::kP, kColumn = kMaxD / (2 * V);
   constexpr bool kHead = kNorm == PVL_NORM_HEAD, kToken = kNorm == PVL_NORM_TOKEN, kAny = kHead || kToken;
   constexpr int kSums = kBwd ? 2 : 1;  // sum x^2, and backward sum g w x
@@ -308,7 +341,7 @@ __global__ void __maxnreg__(kBwd ? 128 : 96) rotary_kernel(const __grid_constant
 #pragma unroll
     for (int i = 0; i < kAcc; ++i)
 #pragma unroll
-      for (int q = 0; q < kP; ++q) acc[i].a[q] = acc[i].b[q] = make_float2(0.0f, 0.0f);
+      for (int q = 0; q < kP; ++q) acc[i].a[q] = acc[i].b[q] = splat<F>(0.0f);
   }
   const float inv_nq = 1.0f / static_cast<float>(kHead ? p.D : p.D * p.H);
   const float inv_nk = 1.0f / static_cast<float>(kHead ? p.D : p.D * max(p.Ht - p.H, 1));
@@ -447,8 +480,8 @@ __global__ void __maxnreg__(kBwd ? 128 : 96) rotary_kernel(const __grid_constant
 #pragma unroll
           for (int q = 0; q < kP; ++q) {
             const float4 t = angles[q * kColumn + u];
-            const float2 c = make_float2(t.x, t.y), s = make_float2(t.z, t.w), a = z.a[q];
-            z.a[q] = ffma2(a, c, fmul2(z.b[q], make_float2(-s.x, -s.y)));
+            const F c = side_a<F>(t), s = side_b<F>(t), a = z.a[q];
+            z.a[q] = ffma2(a, c, fmul2(z.b[q], minus(s)));
             z.b[q] = ffma2(a, s, fmul2(z.b[q], c));
           }
         };
@@ -463,22 +496,22 @@ __global__ void __maxnreg__(kBwd ? 128 : 96) rotary_kernel(const __grid_constant
             const bool real = live && h < p.Ht;
             Unit<V> x;
             unpack<V, kHalf>(vec(m, 0), vec(m, 1), x);
-            float2 s = make_float2(0.0f, 0.0f);
+            F s = splat<F>(0.0f);
 #pragma unroll
             for (int q = 0; q < kP; ++q) s = ffma2(x.a[q], x.a[q], ffma2(x.b[q], x.b[q], s));
-            part[m][0] = real ? s.x + s.y : 0.0f;
+            part[m][0] = real ? both_of(s) : 0.0f;
             if (kBwd) {
               Unit<V>& z = g[kBwd ? m : 0];
               unpack<V, kHalf>(vec(m, kVecs - 2), vec(m, kVecs - 1), z);
               if (turned) rotate(z);
-              s = make_float2(0.0f, 0.0f);
+              s = splat<F>(0.0f);
 #pragma unroll
               for (int q = 0; q < kP; ++q) {
                 const float4 w = weight(m, h >= p.H, q);
-                s = ffma2(fmul2(z.a[q], make_float2(w.x, w.y)), x.a[q], s);
-                s = ffma2(fmul2(z.b[q], make_float2(w.z, w.w)), x.b[q], s);
+                s = ffma2(fmul2(z.a[q], side_a<F>(w)), x.a[q], s);
+                s = ffma2(fmul2(z.b[q], side_b<F>(w)), x.b[q], s);
               }
-              part[m][kSums - 1] = real ? s.x + s.y : 0.0f;
+              part[m][kSums - 1] = real ? both_of(s) : 0.0f;
             }
           }
           if (kHead) {
@@ -593,7 +626,7 @@ __global__ void __maxnreg__(kBwd ? 128 : 96) rotary_kernel(const __grid_constant
             unpack<V, kHalf>(vec(m, 0), vec(m, 1), z);
             if (kBwd) {
               const Unit<V>& d = g[kBwd ? m : 0];
-              const float2 rr = make_float2(r[m], r[m]), mm = make_float2(mean[m], mean[m]);
+              const F rr = splat<F>(r[m]), mm = splat<F>(mean[m]);
 #pragma unroll
               for (int q = 0; q < kP; ++q) {
                 const float4 w = weight(m, key, q);
@@ -610,17 +643,17 @@ __global__ void __maxnreg__(kBwd ? 128 : 96) rotary_kernel(const __grid_constant
                   acc[0].a[q] = ffma2(z.a[q], d.a[q], acc[0].a[q]);
                   acc[0].b[q] = ffma2(z.b[q], d.b[q], acc[0].b[q]);
                 }
-                z.a[q] = ffma2(fmul2(d.a[q], make_float2(w.x, w.y)), rr, fmul2(z.a[q], mm));
-                z.b[q] = ffma2(fmul2(d.b[q], make_float2(w.z, w.w)), rr, fmul2(z.b[q], mm));
+                z.a[q] = ffma2(fmul2(d.a[q], side_a<F>(w)), rr, fmul2(z.a[q], mm));
+                z.b[q] = ffma2(fmul2(d.b[q], side_b<F>(w)), rr, fmul2(z.b[q], mm));
               }
             } else {
               if (kAny) {
-                const float2 rr = make_float2(r[m], r[m]);
+                const F rr = splat<F>(r[m]);
 #pragma unroll
                 for (int q = 0; q < kP; ++q) {
                   const float4 w = weight(m, key, q);
-                  z.a[q] = fmul2(fmul2(z.a[q], rr), make_float2(w.x, w.y));
-                  z.b[q] = fmul2(fmul2(z.b[q], rr), make_float2(w.z, w.w));
+                  z.a[q] = fmul2(fmul2(z.a[q], rr), side_a<F>(w));
+                  z.b[q] = fmul2(fmul2(z.b[q], rr), side_b<F>(w));
                 }
               }
               if (turned) rotate(z);
@@ -648,8 +681,9 @@ __global__ void __maxnreg__(kBwd ? 128 : 96) rotary_kernel(const __grid_constant
     // value k of a unit's sums
     auto value = [](const Unit<V>& s, int k) {
       const int e = k % (V > 1 ? V : 1), side = k / (V > 1 ? V : 1);
-      const float2 t = side ? s.b[e / 2] : s.a[e / 2];
-      return e & 1 ? t.y : t.x;
+      const F t = side ? s.b[e / 2] : s.a[e / 2];
+      if constexpr (V > 1) return e & 1 ? t.y : t.x;
+      else return t;
     };
     if (kToken) {
       // one row of partial sums for each team
