@@ -79,6 +79,8 @@ struct ResidualParams {
   long long rows, rows_per_cta;
   int n_slots;
   int stages;
+  const int* valid;             // backward: valid rows of each of kSegments row segments, null: rows split evenly
+  int seg_rows, pad_weight;     // rows of a segment; cost of a padding row in sixteenths of a valid one
   int stats_warps, tables;      // backward: warps for the rows' statistics, table slots in shared memory
   const float *factors, *gates; // backward: w (1 + scale) and gate w2 as [S, D]
   float alpha, eps;
@@ -530,12 +532,14 @@ struct RowStats {
 };
 
 constexpr int kMaxTables = 2;
+constexpr int kSegments = 512;  // a multiple of 128: a lane reads its part as int4
 
 struct BwdShared {
   uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages], table[kMaxTables];
   RowStats stats[kMaxStages];
   int ids[kMaxStages];
   int slot[kMaxStages];  // of the row's tables: slot, and the parity of its load in bit 8
+  int range[2];
   int abort;
 };
 
@@ -550,6 +554,61 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
 }
 __device__ __forceinline__ float total(float2 v) { return warp_sum(v.x + v.y); }
 
+// Rows of a CTA where padding is cheaper than valid rows: with segment s's
+// cost w_s = pad rows + (16 - pad) valid rows and P_s the cost before it, the
+// k-th boundary is the row at cost k T / n_cta of the total T, taken as evenly
+// spread within a segment.  One warp; every CTA computes the same boundaries.
+// (In four padded episodes with a fifth of the rows padding at half the cost,
+// the CTAs of valid rows would end 10 % after the mean.)
+__device__ void split_rows(const ResidualParams& p, int lane, int* range) {
+  constexpr int kPer = kSegments / 32;
+  int w[kPer];
+  long long sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; i += 4) {
+    const int4 v = __ldg(reinterpret_cast<const int4*>(p.valid + lane * kPer + i));
+    w[i] = v.x;
+    w[i + 1] = v.y;
+    w[i + 2] = v.z;
+    w[i + 3] = v.w;
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const long long first = static_cast<long long>(lane * kPer + i) * p.seg_rows;
+    const long long len = max(0ll, min(static_cast<long long>(p.seg_rows), p.rows - first));
+    w[i] = static_cast<int>(len) * p.pad_weight + w[i] * (16 - p.pad_weight);
+    sum += w[i];
+  }
+  long long before = sum;  // inclusive, then exclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
+  }
+  const long long all = __shfl_sync(0xffffffffu, before, 31);
+  before -= sum;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const long long want = (static_cast<long long>(blockIdx.x) + k) * all / gridDim.x;
+    if (want >= all) {
+      if (lane == 0) range[k] = static_cast<int>(p.rows);
+    } else if (want >= before && want < before + sum) {
+      long long at = before;
+      bool found = false;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (!found && want < at + w[i]) {
+          const long long first = static_cast<long long>(lane * kPer + i) * p.seg_rows;
+          const long long len = min(static_cast<long long>(p.seg_rows), p.rows - first);
+          range[k] = static_cast<int>(first + (want - at) * len / w[i]);
+          found = true;
+        }
+        at += w[i];
+      }
+    }
+  }
+}
+
 template <typename TX, int kV, int kRegs, int kBranch>
 __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
   constexpr bool kSplit = sizeof(TX) == 4;
@@ -563,8 +622,7 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
   const int group_warps = blockDim.x / 32 - 1 - p.stats_warps;
   const float inv_d = 1.0f / static_cast<float>(D);
   const KernelCtl ctl{p.err, &sh.abort, p.timeout_ns};
-  const int r_begin = static_cast<int>(blockIdx.x * p.rows_per_cta);
-  const int rows = static_cast<int>(min(p.rows_per_cta, p.rows - blockIdx.x * p.rows_per_cta));
+  if (p.valid && warp == 1) split_rows(p, lane, sh.range);
   if (threadIdx.x == 0) {
     sh.abort = 0;
     for (int s = 0; s < S; ++s) {
@@ -574,8 +632,13 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
     }
     for (int s = 0; s < p.tables; ++s) mbar_init(&sh.table[s], 1);
     fence_barrier_init();
+    if (!p.valid) {
+      sh.range[0] = static_cast<int>(blockIdx.x * p.rows_per_cta);
+      sh.range[1] = static_cast<int>(min(blockIdx.x * p.rows_per_cta + p.rows_per_cta, p.rows));
+    }
   }
   __syncthreads();
+  const int r_begin = sh.range[0], rows = sh.range[1] - r_begin;
 
   if (warp < group_warps) {
     const int t = threadIdx.x, nthr = group_warps * 32;
@@ -857,8 +920,28 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
 // reads them: the first quads of all groups, then the second ones.
 template <bool kSplit>
 __global__ void __launch_bounds__(256) residual_tables_kernel(const ResidualParams p, float* factors, float* gates,
-                                                              int* ints, size_t n_ints) {
-  const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+                                                              int* ints, size_t n_ints, int* valid,
+                                                              int count_blocks) {
+  if (blockIdx.x < count_blocks) {
+    // valid rows of one segment
+    __shared__ int part[8];
+    const long long first = static_cast<long long>(blockIdx.x) * p.seg_rows;
+    const long long end = min(first + p.seg_rows, p.rows);
+    int n = 0;
+    for (long long r = first + threadIdx.x; r < end; r += 256) {
+      const int id = __ldg(p.ids + r);
+      n += id >= 0 && (p.one_row || id < p.S);
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = n;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < 8; ++i) n += part[i];
+      valid[blockIdx.x] = n;
+    }
+    return;
+  }
+  const size_t i = static_cast<size_t>(blockIdx.x - count_blocks) * 256 + threadIdx.x;
   if (i < n_ints) ints[i] = -1;
   const int per = p.D / 8;
   if (i >= static_cast<size_t>(p.S) * per) return;
@@ -1120,10 +1203,10 @@ pvl_status aligned(const char* who, const void* const* ptrs, int n) {
 }
 
 // Workspace of the backward: the slots' sums [3][n_slots][D], the totals
-// [3][S][D], the tables [2][S][D], then the integers lo [S], hi [S], tag
+// [3][S][D], the tables [2][S][D], the segments' valid rows, then the integers lo [S], hi [S], tag
 // [n_slots], ordered.
 struct WsLayout {
-  size_t tot, tables, ints, total;
+  size_t tot, tables, valid, ints, total;
   int n_slots;
   size_t n_ints;
 };
@@ -1132,7 +1215,8 @@ WsLayout ws_layout(long long rows, int S, int D) {
   w.n_slots = static_cast<int>(rows < kMaxCtas ? rows : kMaxCtas) + S - 1;
   w.tot = align256(3ull * w.n_slots * D * sizeof(float));
   w.tables = w.tot + align256(3ull * S * D * sizeof(float));
-  w.ints = w.tables + align256(2ull * S * D * sizeof(float));
+  w.valid = w.tables + align256(2ull * S * D * sizeof(float));
+  w.ints = w.valid + kSegments * sizeof(int);
   w.n_ints = 2ull * S + w.n_slots + 1;
   w.total = w.ints + align256(w.n_ints * sizeof(int));
   return w;
@@ -1225,11 +1309,19 @@ extern "C" pvl_status adaln_residual_bwd(const pvl_residual* a, const void* dx_o
   float* tables = reinterpret_cast<float*>(base + lay.tables);
   p.factors = tables;
   p.gates = tables + static_cast<size_t>(p.S) * p.D;
+  // padding is worth the splitting kernel's microsecond from some ten rows a CTA on
+  const bool split = a->mod_id && p.rows >= 16 * kSegments;
+  const int count_blocks = split ? kSegments : 0;
+  int* valid = reinterpret_cast<int*>(base + lay.valid);
+  p.valid = split ? valid : nullptr;
+  p.seg_rows = static_cast<int>((p.rows + kSegments - 1) / kSegments);
+  const int xb = a->stream_dtype == PVL_F32 ? 4 : 2;
+  p.pad_weight = 16 * ((dx_out ? xb : 0) + xb + 2) / ((dx_out ? 3 : 2) * xb + (p.h ? 6 : 4));
   const size_t items = std::max(lay.n_ints, static_cast<size_t>(p.S) * (p.D / 8));
   (a->stream_dtype == PVL_F32 ? residual_tables_kernel<true> : residual_tables_kernel<false>)<<<
-      static_cast<unsigned>((items + 255) / 256), 256, 0, s>>>(
+      static_cast<unsigned>(count_blocks + (items + 255) / 256), 256, 0, s>>>(
       p, tables, branch == kNoBranch ? nullptr : tables + static_cast<size_t>(p.S) * p.D,
-      reinterpret_cast<int*>(p.lo), lay.n_ints);
+      reinterpret_cast<int*>(p.lo), lay.n_ints, valid, count_blocks);
   st = check_cuda(cudaGetLastError(), who);
   if (st != PVL_OK) return st;
   st = dispatch<true>(p, a->stream_dtype == PVL_F32, branch, s, who);

@@ -40,7 +40,7 @@
 namespace pvl {
 namespace {
 
-constexpr int kMaxBlock = 512;
+constexpr int kMaxBlock = 384;  // 168 registers a thread, the most that a kernel here takes
 constexpr int kMaxD = 256;
 constexpr int kMaxPartials = 1216;  // rows of partial weight gradients at most
 constexpr float kRadians = 1.4629180792671596e-9f;  // 2 pi / 2^32
@@ -233,10 +233,14 @@ __device__ __forceinline__ float head_sum(float v, int u, int units) {
   return __shfl_sync(0xffffffffu, v, (threadIdx.x & 31) - u);
 }
 
-// 16, 8 or 4 bytes into shared memory without passing registers.
-template <typename T>
+// 16, 8 or 4 bytes into shared memory without passing registers; past L1
+// where kPast and the width allow it.
+template <bool kPast, typename T>
 __device__ __forceinline__ void copy_async(T* dst, const char* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(sizeof(T)) : "memory");
+  if constexpr (kPast && sizeof(T) == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(sizeof(T)) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -253,7 +257,7 @@ constexpr int kRing = 2;
 struct SmemPlan {
   int weights, sums, ring, total;  // offsets; the angles are first
 };
-__host__ __device__ inline SmemPlan smem_plan(int V, int kM, int norm, bool bwd, int D, int units, int hpi, int team,
+__host__ __device__ inline SmemPlan smem_plan(int V, int kM, int norm, bool bwd, int Ht, int D, int units, int hpi, int team,
                                               int teams, int threads) {
   SmemPlan s{};
   const int group = team < 32 ? team : 32;
@@ -268,7 +272,8 @@ __host__ __device__ inline SmemPlan smem_plan(int V, int kM, int norm, bool bwd,
   if (norm == PVL_NORM_HEAD && units > 32) sums = (threads * kM * (bwd ? 2 : 1) + 3) / 4 * 4;
   s.ring = s.sums + sums;
   s.total = s.ring + (V > 1 && norm != PVL_NORM_NONE ? kRing * kM * (bwd ? 4 : 2) * threads * V / 2 : 0);
-  if (norm == PVL_NORM_HEAD && bwd && s.ring + teams * hpi * D > s.total) s.total = s.ring + teams * hpi * D;
+  const int gradients = !bwd ? 0 : norm == PVL_NORM_HEAD ? teams * hpi * D : teams > 1 ? teams * Ht * D : 0;
+  if (s.ring + gradients > s.total) s.total = s.ring + gradients;
   return s;
 }
 
@@ -277,14 +282,14 @@ __host__ __device__ inline SmemPlan smem_plan(int V, int kM, int norm, bool bwd,
 // that the shared memory leaves no room for (norm per head, 64k pack: 154 us
 // at 64, 132 at 96).
 template <int V, int kM, int kNorm, bool kBwd, bool kHalf>
-__global__ void __maxnreg__(kBwd ? 128 : 96) rotary_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __maxnreg__(!kBwd ? 96 : V == 8 || V == 1 ? 168 : 128) rotary_kernel(const __grid_constant__ RotaryParams p) {
   using T = typename Vec<V>::T;
   using F = typename Unit<V>::F;
   constexpr int kP = Unit<V>::kP, kColumn = kMaxD / (2 * V);
   constexpr bool kHead = kNorm == PVL_NORM_HEAD, kToken = kNorm == PVL_NORM_TOKEN, kAny = kHead || kToken;
   constexpr int kSums = kBwd ? 2 : 1;  // sum x^2, and backward sum g w x
   extern __shared__ __align__(16) float smem[];
-  const SmemPlan plan = smem_plan(V, kM, kNorm, kBwd, p.D, p.units, p.hpi, p.team, p.teams, blockDim.x);
+  const SmemPlan plan = smem_plan(V, kM, kNorm, kBwd, p.Ht, p.D, p.units, p.hpi, p.team, p.teams, blockDim.x);
   const int tid = threadIdx.x, lane32 = tid & 31;
   const int slot = tid / p.team, lane = tid - slot * p.team;
   int hl, u;
@@ -386,12 +391,12 @@ __global__ void __maxnreg__(kBwd ? 128 : 96) rotary_kernel(const __grid_constant
         const int h = hl + (cf * kM + m) * p.hpi;
         if (on && lf < p.L && h < p.Ht) {
           const char* q = head_at(p.x, xp, h);
-          copy_async(dst + (m * kVecs) * 32, q);
-          copy_async(dst + (m * kVecs + 1) * 32, q + apart);
+          copy_async<kBwd>(dst + (m * kVecs) * 32, q);
+          copy_async<kBwd>(dst + (m * kVecs + 1) * 32, q + apart);
           if (kBwd) {
             q = head_at(p.g, gp, h);
-            copy_async(dst + (m * kVecs + 2) * 32, q);
-            copy_async(dst + (m * kVecs + 3) * 32, q + apart);
+            copy_async<kBwd>(dst + (m * kVecs + 2) * 32, q);
+            copy_async<kBwd>(dst + (m * kVecs + 3) * 32, q + apart);
           }
         }
       }
@@ -685,37 +690,44 @@ __global__ void __maxnreg__(kBwd ? 128 : 96) rotary_kernel(const __grid_constant
       if constexpr (V > 1) return e & 1 ? t.y : t.x;
       else return t;
     };
+    // the block's sums, in the ring's place (it is done with): of its teams,
+    // and with the norm per head of all heads, queries and keys in turn
+    float* out = p.part + static_cast<size_t>(blockIdx.y * gridDim.x + blockIdx.x) * p.width;
+    float* const table = smem + plan.ring;
     if (kToken) {
-      // one row of partial sums for each team
       if (on) {
-        float* row = p.part + (static_cast<size_t>(blockIdx.y * gridDim.x + blockIdx.x) * p.teams + slot) * p.width;
 #pragma unroll
         for (int m = 0; m < kM; ++m) {
           const int h = hl + m * p.hpi;
           if (h < p.Ht) {
 #pragma unroll
             for (int k = 0; k < kValues; ++k)
-              row[static_cast<size_t>(h) * p.D + feature<V, kHalf>(k, e0, e1)] = value(acc[kAcc > 1 ? m : 0], k);
+              (p.teams == 1 ? out : table + slot * p.width)[h * p.D + feature<V, kHalf>(k, e0, e1)] =
+                  value(acc[kAcc > 1 ? m : 0], k);
           }
         }
       }
+      if (p.teams == 1) return;
+      __syncthreads();
+      for (int d = tid; d < p.width; d += blockDim.x) {
+        float t = 0.0f;
+        for (int j = 0; j < p.teams; ++j) t += table[j * p.width + d];
+        out[d] = t;
+      }
     } else {
-      // the block's teams and heads added feature by feature, queries then keys
-      float* row = p.part + static_cast<size_t>(blockIdx.y * gridDim.x + blockIdx.x) * p.width;
-      float* sums = smem + plan.ring;  // the ring is done with
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         __syncthreads();
         if (on) {
 #pragma unroll
           for (int k = 0; k < kValues; ++k)
-            sums[(slot * p.hpi + hl) * p.D + feature<V, kHalf>(k, e0, e1)] = value(acc[i ? kAcc - 1 : 0], k);
+            table[(slot * p.hpi + hl) * p.D + feature<V, kHalf>(k, e0, e1)] = value(acc[i ? kAcc - 1 : 0], k);
         }
         __syncthreads();
         for (int d = tid; d < p.D; d += blockDim.x) {
           float t = 0.0f;
-          for (int j = 0; j < p.teams * p.hpi; ++j) t += sums[j * p.D + d];
-          row[i * p.D + d] = t;
+          for (int j = 0; j < p.teams * p.hpi; ++j) t += table[j * p.D + d];
+          out[i * p.D + d] = t;
         }
       }
     }
@@ -813,7 +825,6 @@ const void* find_kernel(const Shape& s, int norm, bool bwd, bool half) {
   PVL_ROTARY_KERNEL(2, 8, PVL_NORM_HEAD, true);
   PVL_ROTARY_KERNEL(1, 8, PVL_NORM_HEAD, true);
   PVL_ROTARY_KERNEL(8, 1, PVL_NORM_TOKEN, false);
-  PVL_ROTARY_KERNEL(8, 2, PVL_NORM_TOKEN, false);
   PVL_ROTARY_KERNEL(8, 3, PVL_NORM_TOKEN, false);
   PVL_ROTARY_KERNEL(8, 6, PVL_NORM_TOKEN, false);
   PVL_ROTARY_KERNEL(4, 4, PVL_NORM_TOKEN, false);
@@ -821,7 +832,7 @@ const void* find_kernel(const Shape& s, int norm, bool bwd, bool half) {
   PVL_ROTARY_KERNEL(1, 8, PVL_NORM_TOKEN, false);
   PVL_ROTARY_KERNEL(1, 16, PVL_NORM_TOKEN, false);
   PVL_ROTARY_KERNEL(8, 1, PVL_NORM_TOKEN, true);
-  PVL_ROTARY_KERNEL(8, 2, PVL_NORM_TOKEN, true);
+  PVL_ROTARY_KERNEL(8, 3, PVL_NORM_TOKEN, true);
   PVL_ROTARY_KERNEL(4, 4, PVL_NORM_TOKEN, true);
   PVL_ROTARY_KERNEL(2, 8, PVL_NORM_TOKEN, true);
   PVL_ROTARY_KERNEL(1, 8, PVL_NORM_TOKEN, true);
@@ -835,7 +846,7 @@ pvl_status launch(const RotaryParams& p, const Shape& sh, int norm, bool bwd, bo
   const void* fn = find_kernel(sh, norm, bwd, half);
   if (!fn) return fail(PVL_ERR_UNSUPPORTED, "%s: no kernel for this shape", who);
   const size_t smem =
-      sizeof(float) * smem_plan(sh.V, sh.kM, norm, bwd, p.D, sh.units, sh.hpi, sh.team, sh.teams, sh.threads).total;
+      sizeof(float) * smem_plan(sh.V, sh.kM, norm, bwd, p.Ht, p.D, sh.units, sh.hpi, sh.team, sh.teams, sh.threads).total;
   const int occ = blocks_per_sm(fn, sh.threads, smem), sms = sm_count();
   if (sms <= 0 || occ <= 0) return fail(PVL_ERR_CUDA, "%s: no usable CUDA device", who);
   long long grid = static_cast<long long>(occ) * sms;
@@ -876,8 +887,10 @@ bool shape_of(const pvl_rotary* a, int V, bool bwd, Shape* s) {
   const long long tokens = static_cast<long long>(a->B) * a->L;
   if (tokens <= 2 * 152 && team_of(8, 1, Ht, a->D, a->norm, s)) return true;
   if (!whole) return team_of(8, bwd ? 2 : 3, Ht, a->D, a->norm, s);
-  if (!bwd && team_of(8, 6, Ht, a->D, a->norm, s)) return true;
-  return team_of(8, 2, Ht, a->D, a->norm, s);
+  // six while a token stays within two warps, else more warps count for more
+  // (10,240 features a token: 215 us at six, 178 at three; 6,144: 165, 177)
+  if (!bwd && Ht * a->D <= 6144 && team_of(8, 6, Ht, a->D, a->norm, s)) return true;
+  return team_of(8, 3, Ht, a->D, a->norm, s);
 }
 
 pvl_status check_views(const char* who, const pvl_rotary* a, const pvl_heads* v, int which, const char* name) {
@@ -1045,22 +1058,14 @@ extern "C" pvl_status pack_rotary_bwd(const pvl_rotary* a, const pvl_heads* dq_o
     return fail(PVL_ERR_UNSUPPORTED, "%s: a head stride of 2^30 elements or more", who);
   flatten(p, norm);
   p.part = weights ? static_cast<float*>(ws) : nullptr;
-  // a partial row for each team (norm per token) or block (norm per head)
-  const int rows_per_block = a->norm == PVL_NORM_TOKEN ? s.teams : 1;
+  // a row of partial sums for each block
   const long long tokens = static_cast<long long>(a->B) * a->L;
-  const long long rows_max = tokens < kMaxPartials ? tokens : kMaxPartials;
-  int limit = weights ? static_cast<int>(rows_max / rows_per_block) : 1 << 30;
-  if (limit < 1) limit = 1;
-  if (weights && static_cast<long long>(rows_per_block) > rows_max) {
-    // fewer tokens than teams: one block, and only the teams that the workspace has rows for
-    p.teams = static_cast<int>(rows_max);
-  }
+  const int limit = weights ? static_cast<int>(std::min<long long>(tokens, kMaxPartials)) : 1 << 30;
   int grid = 0;
   cudaStream_t stm = reinterpret_cast<cudaStream_t>(stream);
   st = launch(p, s, a->norm, norm, a->layout == PVL_ROTARY_HALF, limit, &grid, stm, who);
   if (st != PVL_OK || !weights) return st;
   const int q_width = a->norm == PVL_NORM_TOKEN ? a->H * a->D : a->D;
-  const int rows = grid * (a->norm == PVL_NORM_TOKEN ? p.teams : 1);
-  rotary_weights_kernel<<<(p.width + 31) / 32, 1024, 0, stm>>>(p.part, rows, p.width, q_width, dq_weight, dk_weight);
+  rotary_weights_kernel<<<(p.width + 31) / 32, 1024, 0, stm>>>(p.part, grid, p.width, q_width, dq_weight, dk_weight);
   return check_cuda(cudaGetLastError(), who);
 }
