@@ -224,6 +224,23 @@ __device__ __forceinline__ void factor8(const ResidualParams& p, int id, int v, 
   }
 }
 
+// The forward's tables of a modulation row: gate w2, w (1 + scale) and
+// b (1 + scale) + shift.
+template <bool kSplit>
+__device__ __forceinline__ void load_tables(const ResidualParams& p, int id, int v, int nvec, float2 (&gt)[4],
+                                            float2 (&fa)[4], float2 (&ad)[4]) {
+  gate8<kSplit>(p, id, v, nvec, gt);
+  factor8<kSplit>(p, id, v, nvec, fa);
+  table8<kSplit>(at_row(p.shift, id, p.D), v, nvec, 0.0f, ad);
+  if (p.b) {
+    float2 q[4], sc[4];
+    table8<kSplit>(p.b, v, nvec, 0.0f, q);
+    table8<kSplit>(at_row(p.scale, id, p.D), v, nvec, 0.0f, sc);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ad[e] = fadd2(ad[e], ffma2(q[e], sc[e], q[e]));
+  }
+}
+
 __host__ __device__ constexpr size_t align128(size_t n) { return (n + 127) / 128 * 128; }
 
 // Stage layout: x (TX), h, and backward dy, dxo (TX); each part 128-byte aligned.
@@ -286,37 +303,33 @@ struct Producer {
   }
 };
 
-// Shared state of both directions' kernels.
+// Shared state of the forward below.
 struct Shared {
   uint64_t full[kMaxStages];
   int ids[kMaxStages];
-  float red[2][kMaxWarps * 8];
+  float red[2][kMaxWarps * 2];
   int abort;
 };
 
-// A row on its way through the phases: which, its stage, its id, and the
-// statistics known so far.
+// A row between its two phases: which, its stage, its id, and the mean (past
+// its K) and 1 / deviation of x_out.
 struct Flight {
   bool on;
   int row, st, id;
-  float m, r;    // forward: mean and 1 / deviation of x_out past its K; backward: of x_out
-  float hm, hr;  // mean and 1 / deviation of the branch (post norm)
-  float c0, c1;  // backward: the means that the gradient subtracts
+  float m, r;
 };
 
-// Every row goes through phases: a first one sums what its first statistics
-// need, the later ones use them.  One iteration of the loop runs the last
-// phase of one row, the first of the next (with a post norm, whose statistics
-// the others wait for, three rows are on the way), and has one barrier, which
-// makes the sums visible and frees the finished row's stage: no phase waits
-// for a reduction of its own row.
+// Forward without a post norm.  Every row has two phases: the first writes
+// x_out and sums what the statistics need, the second writes y.  One iteration
+// of the loop runs the second phase of a row and the first of the next and has
+// one barrier, which makes the sums visible and frees the finished row's
+// stage: no phase waits for a reduction of its own row (496 us at 64,000 x
+// 5120 with a row at a time, 405 so).
 template <typename TX, int kV, int kRegs, int kBranch>
 __global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
   constexpr bool kSplit = sizeof(TX) == 4;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Shared sh;
-  constexpr bool kThree = kBranch == kPost;
-  constexpr int kN = kThree ? 4 : 2;
   const Stage<TX, false> lay(p.D);
   const int D = p.D, nvec = D / 8, t = threadIdx.x, nthr = blockDim.x, nwarps = nthr / 32;
   const float inv_d = 1.0f / static_cast<float>(D);
@@ -334,172 +347,105 @@ __global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
   if (t == 0)
     for (int s = 0; s < p.stages; ++s) prod.issue();
 
-  float2 gt[kV][4], fa[kV][4], ad[kV][4];  // gate w2, w (1 + scale), b (1 + scale) + shift of row cur
-  float g0 = 0.0f;                         // gate w2 of feature 0
+  float2 gt[kV][4], fa[kV][4], ad[kV][4];  // gate, w (1 + scale), b (1 + scale) + shift of row cur
+  float g0 = 0.0f;                         // gate of feature 0
   int cur = -1;
   // the residual's 8 features of group v, from the stage
-  auto residual8 = [&](const uint8_t* src, int i, int v, float hm, float hr, float2 (&f)[4]) {
+  auto residual8 = [&](const uint8_t* src, int i, int v, float2 (&f)[4]) {
     row8<kSplit>(reinterpret_cast<const TX*>(src), v, nvec, f);
     if (kBranch != kNoBranch) {
       float2 q[4];
       row8<kSplit>(reinterpret_cast<const __nv_bfloat16*>(src + lay.h()), v, nvec, q);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (kBranch == kPost) q[e] = fmul2(fadd2(q[e], both(-hm)), both(hr));
-        f[e] = ffma2(q[e], gt[i][e], fmul2(f[e], both(p.alpha)));
-      }
+      for (int e = 0; e < 4; ++e) f[e] = ffma2(q[e], gt[i][e], fmul2(f[e], both(p.alpha)));
     }
   };
-  auto shift_of = [&](const uint8_t* src, float hm, float hr) {
+  // the row's first element: what its sums are shifted by
+  auto shift_of = [&](const uint8_t* src) {
     if (p.rms) return 0.0f;
     const float x0 = first(reinterpret_cast<const TX*>(src));
     if (kBranch == kNoBranch) return x0;
-    return fmaf((first(reinterpret_cast<const __nv_bfloat16*>(src + lay.h())) - hm) * hr, g0, p.alpha * x0);
-  };
-  // x_out of a row, and the sums of its difference from K
-  auto stream = [&](const Flight& f, float& sum1, float& sum2) {
-    const uint8_t* src = smem + f.st * lay.bytes();
-    TX* out = static_cast<TX*>(p.x_out) + static_cast<size_t>(f.row) * D;
-    if (f.id < 0) {
-#pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        const int v = t + i * nthr;
-        if (kBranch != kNoBranch && v < nvec) {
-          float2 q[4];
-          row8<kSplit>(reinterpret_cast<const TX*>(src), v, nvec, q);
-          store8<kSplit>(out, v, nvec, q);
-        }
-      }
-      return;
-    }
-    const float K = shift_of(src, f.hm, f.hr);
-    float2 s1 = both(0.0f), s2 = both(0.0f);
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      const int v = t + i * nthr;
-      if (v < nvec) {
-        float2 q[4];
-        residual8(src, i, v, f.hm, f.hr, q);
-        if (kBranch != kNoBranch) store8<kSplit>(out, v, nvec, q);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          q[e] = fadd2(q[e], both(-K));
-          s1 = fadd2(s1, q[e]);
-          s2 = ffma2(q[e], q[e], s2);
-        }
-      }
-    }
-    sum1 = s1.x + s1.y;
-    sum2 = s2.x + s2.y;
+    return fmaf(first(reinterpret_cast<const __nv_bfloat16*>(src + lay.h())), g0, p.alpha * x0);
   };
 
-  Flight b{}, c{};  // the rows after their first and (post norm) second phase
-  b.hr = c.hr = 1.0f;
+  Flight b{};
   int next = r_begin, st = 0, turn = 0;
   uint32_t ph = 0, freed = 0;
-  while (next < r_end || b.on || c.on) {
-    // last phase: y
-    const Flight& z = kThree ? c : b;
-    if (z.on) {
-      const uint8_t* src = smem + z.st * lay.bytes();
-      __nv_bfloat16* out = p.y + static_cast<size_t>(z.row) * D;
-      const float sub = z.id < 0 ? 0.0f : shift_of(src, z.hm, z.hr) + z.m;
+  while (next < r_end || b.on) {
+    if (b.on) {  // y
+      const uint8_t* src = smem + b.st * lay.bytes();
+      __nv_bfloat16* out = p.y + static_cast<size_t>(b.row) * D;
+      const float sub = b.id < 0 ? 0.0f : shift_of(src) + b.m;
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
         const int v = t + i * nthr;
         if (v < nvec) {
           float2 f[4];
-          if (z.id < 0) {
+          if (b.id < 0) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[e] = both(0.0f);
           } else {
-            residual8(src, i, v, z.hm, z.hr, f);
+            residual8(src, i, v, f);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = ffma2(fmul2(fadd2(f[e], both(-sub)), both(z.r)), fa[i][e], ad[i][e]);
+            for (int e = 0; e < 4; ++e) f[e] = ffma2(fmul2(fadd2(f[e], both(-sub)), both(b.r)), fa[i][e], ad[i][e]);
           }
           store8<kSplit>(out, v, nvec, f);
         }
       }
     }
-    float sums[kN] = {};
-    if (kThree && b.on) stream(b, sums[kN - 2], sums[kN - 1]);
-    // a new row enters unless rows of another id still need the tables or
-    // its stage has not been issued
+    float2 s1 = both(0.0f), s2 = both(0.0f);
     Flight a{};
-    a.hr = 1.0f;
     bool ok = true;
-    if (next < r_end && static_cast<int>(b.on) + static_cast<int>(c.on) < p.stages) {
+    if (next < r_end) {
       ok = mbar_wait(&sh.full[st], ph, ctl, kSiteResRowFull);
       const int id = sh.ids[st];
-      a = Flight{id < 0 || id == cur || !kThree || !b.on, next, st, id, 0.0f, 0.0f, 0.0f, 1.0f, 0.0f, 0.0f};
-      if (a.on && id >= 0 && id != cur) {
+      a = Flight{true, next, st, id, 0.0f, 0.0f};
+      if (id >= 0 && id != cur) {  // the row before is done with its tables
         cur = id;
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
           const int v = t + i * nthr;
-          if (v < nvec) {
-            if (kBranch != kNoBranch) gate8<kSplit>(p, id, v, nvec, gt[i]);
-            factor8<kSplit>(p, id, v, nvec, fa[i]);
-            table8<kSplit>(at_row(p.shift, id, D), v, nvec, 0.0f, ad[i]);
-            if (p.b) {
-              float2 q[4], sc[4];
-              table8<kSplit>(p.b, v, nvec, 0.0f, q);
-              table8<kSplit>(at_row(p.scale, id, D), v, nvec, 0.0f, sc);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) ad[i][e] = fadd2(ad[i][e], ffma2(q[e], sc[e], q[e]));
-            }
-          }
+          if (v < nvec) load_tables<kSplit>(p, id, v, nvec, gt[i], fa[i], ad[i]);
         }
-        if (kBranch != kNoBranch) {
-          g0 = p.gate ? __ldg(p.gate + static_cast<size_t>(id) * D) : 1.0f;
-          if (p.w2) g0 *= __ldg(p.w2);
-        }
+        g0 = p.gate ? __ldg(p.gate + static_cast<size_t>(id) * D) : 1.0f;
       }
-    }
-    if (a.on) {
-      if (!kThree) {
-        stream(a, sums[0], sums[1]);
-      } else if (a.id >= 0) {
-        const __nv_bfloat16* hs = reinterpret_cast<const __nv_bfloat16*>(smem + a.st * lay.bytes() + lay.h());
-        const float K = p.post_rms ? 0.0f : first(hs);
-        float2 s1 = both(0.0f), s2 = both(0.0f);
+      const uint8_t* src = smem + st * lay.bytes();
+      TX* out = static_cast<TX*>(p.x_out) + static_cast<size_t>(next) * D;
+      const float K = id < 0 ? 0.0f : shift_of(src);
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-          const int v = t + i * nthr;
-          if (v < nvec) {
-            float2 f[4];
-            row8<kSplit>(hs, v, nvec, f);
+      for (int i = 0; i < kV; ++i) {
+        const int v = t + i * nthr;
+        if (v < nvec) {
+          float2 q[4];
+          if (id < 0) {
+            if (kBranch != kNoBranch) {
+              row8<kSplit>(reinterpret_cast<const TX*>(src), v, nvec, q);
+              store8<kSplit>(out, v, nvec, q);
+            }
+          } else {
+            residual8(src, i, v, q);
+            if (kBranch != kNoBranch) store8<kSplit>(out, v, nvec, q);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              f[e] = fadd2(f[e], both(-K));
-              s1 = fadd2(s1, f[e]);
-              s2 = ffma2(f[e], f[e], s2);
+              q[e] = fadd2(q[e], both(-K));
+              s1 = fadd2(s1, q[e]);
+              s2 = ffma2(q[e], q[e], s2);
             }
           }
         }
-        sums[0] = s1.x + s1.y;
-        sums[1] = s2.x + s2.y;
-        a.hm = K;
       }
     }
-    warp_part<kN>(sums, sh.red[turn]);
+    float sums[2] = {s1.x + s1.y, s2.x + s2.y};
+    warp_part<2>(sums, sh.red[turn]);
     if (!__syncthreads_and(ok)) break;
-    all_parts<kN>(sums, sh.red[turn], nwarps);
+    all_parts<2>(sums, sh.red[turn], nwarps);
     turn ^= 1;
-    if (z.on) {
+    if (b.on) {
       ++freed;
       if (t == 0) prod.issue();
     }
-    // statistics of x_out: past the phase that summed it
-    Flight& y = kThree ? b : a;
-    y.m = p.rms ? 0.0f : sums[kN - 2] * inv_d;
-    y.r = rsqrtf(fmaxf(fmaf(-y.m, y.m, sums[kN - 1] * inv_d), 0.0f) + p.eps);
-    if (kThree) {
-      const float m1 = p.post_rms ? 0.0f : sums[0] * inv_d;
-      a.hr = rsqrtf(fmaxf(fmaf(-m1, m1, sums[1] * inv_d), 0.0f) + p.eps);
-      a.hm += m1;
-      c = b;
-    }
+    a.m = p.rms ? 0.0f : sums[0] * inv_d;
+    a.r = rsqrtf(fmaxf(fmaf(-a.m, a.m, sums[1] * inv_d), 0.0f) + p.eps);
     b = a;
     if (a.on) {
       ++next;
@@ -516,26 +462,28 @@ __global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
   __syncthreads();
 }
 
-// ------------------------------------------------------------- backward
-// Warp roles.  One warp's lane streams the rows into the ring (Producer).
-// kStats warps take whole rows in turn: a row's statistics are sums of one
-// warp, so they need shuffles but no barrier, and a post norm's second sums
-// simply follow its first.  The other warps own feature groups: they wait for
-// a row's statistics, write its dx and dh and add to their groups' A, B and C.
-// Nothing is CTA-wide; the roles meet at the stages' mbarriers only (full:
-// copies landed; ready: statistics written; empty: every group warp done).
+// ------------------------------------------------------------- warp roles
+// The backward, and the forward with a post norm.  One warp's lane streams
+// the rows (and, where the modulation row changes, the tables that statistics
+// need) into shared memory.  p.stats_warps warps take whole rows in turn: a
+// row's statistics are sums of one warp, so they need shuffles but no barrier,
+// and sums that need earlier ones (a post norm's) simply follow them.  The
+// other warps own feature groups: they wait for a row's statistics and write
+// its results.  Nothing is CTA-wide; the roles meet at the stages' mbarriers
+// only (full: copies landed; ready: statistics written; empty: every group
+// warp done).
 struct RowStats {
   float m, r;    // mean and 1 / deviation of x_out
-  float c0, c1;  // mean g, mean g xh
+  float c0, c1;  // backward: mean g, mean g xh
   float hm, hr;  // mean and 1 / deviation of the branch
-  float z0, z1;  // dh's means: -rh mean dz, -rh^3 mean dz (h - hm)
+  float z0, z1;  // backward: dh's means, -rh mean dz and -rh^3 mean dz (h - hm)
 };
 
 constexpr int kMaxTables = 2;
 constexpr int kSegments = 512;  // a multiple of 128: a lane reads its part as int4
 
-struct BwdShared {
-  uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages], table[kMaxTables];
+struct RoleShared {
+  uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages], table[kMaxTables], w2;
   RowStats stats[kMaxStages];
   int ids[kMaxStages];
   int slot[kMaxStages];  // of the row's tables: slot, and the parity of its load in bit 8
@@ -548,12 +496,250 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+__device__ __forceinline__ float total(float2 v) { return warp_sum(v.x + v.y); }
 // A wait of a whole warp: the same answer in every lane.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const KernelCtl& ctl, uint32_t where) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctl, where));
 }
-__device__ __forceinline__ float total(float2 v) { return warp_sum(v.x + v.y); }
 
+__device__ __forceinline__ void init_roles(const ResidualParams& p, RoleShared& sh, int group_warps) {
+  sh.abort = 0;
+  for (int s = 0; s < p.stages; ++s) {
+    mbar_init(&sh.full[s], 1);
+    mbar_init(&sh.ready[s], 1);
+    mbar_init(&sh.empty[s], group_warps);
+  }
+  for (int s = 0; s < p.tables; ++s) mbar_init(&sh.table[s], 1);
+  mbar_init(&sh.w2, 1);
+  fence_barrier_init();
+}
+
+// The copying lane: rows [r_begin, r_begin + rows) into the ring, the rows of
+// the tables t0 and t1 (null: none) of each new modulation row into the next
+// table slot.
+template <typename TX, bool kBwd>
+__device__ __forceinline__ void stream_rows(const ResidualParams& p, RoleShared& sh, uint8_t* tables,
+                                            uint32_t table_bytes, uint8_t* ring, const float* t0, const float* t1,
+                                            int r_begin, int rows, const KernelCtl& ctl) {
+  const int D = p.D, S = p.stages;
+  Producer<TX, kBwd> prod(p, ring, sh.full, sh.ids, r_begin, r_begin + rows);
+  int st = 0, slot = p.tables - 1, held = -1;  // held: the id whose tables the slot has
+  uint32_t ph = 1;                             // parity of the stage's last empty phase, from the second round on
+  uint32_t loads = 0;                          // table loads so far
+  int last[kMaxTables];                        // the last row that uses each slot
+#pragma unroll
+  for (int i = 0; i < kMaxTables; ++i) last[i] = -1;
+  for (int n = 0; n < rows; ++n) {
+    if (n >= S && !mbar_wait(&sh.empty[st], ph, ctl, kSiteResEmpty)) break;
+    const int id = prod.peek();
+    if (p.tables && id >= 0 && id != held) {
+      held = id;
+      slot = slot + 1 == p.tables ? 0 : slot + 1;
+      // every row that used the slot must have its statistics: those of
+      // the last S - 1 rows are waited for one by one (different warps
+      // take them, in no order), older ones have left their stages
+      const int end = slot == 0 ? last[0] : last[1];
+      bool free = true;
+      for (int row = max(0, n - S + 1); row <= end && free; ++row)
+        free = mbar_wait(&sh.ready[row % S], (row / S) & 1, ctl, kSiteResTable);
+      if (!free) break;
+      uint8_t* dst = tables + slot * table_bytes;
+      mbar_arrive_expect_tx(&sh.table[slot], 4 * D * ((t0 ? 1 : 0) + (t1 ? 1 : 0)));
+      if (t0) bulk_load(dst, t0 + static_cast<size_t>(id) * D, 4 * D, &sh.table[slot]);
+      if (t1) bulk_load(dst + (t0 ? align128(4 * static_cast<size_t>(D)) : 0), t1 + static_cast<size_t>(id) * D, 4 * D,
+                        &sh.table[slot]);
+      ++loads;
+    }
+    if (id >= 0) (slot == 0 ? last[0] : last[1]) = n;
+    sh.slot[st] = slot | (p.tables ? static_cast<int>(((loads - 1) / p.tables) & 1) << 8 : 0);
+    prod.issue();
+    if (++st == S) {
+      st = 0;
+      ph ^= 1u;
+    }
+  }
+  // copies still in flight land before the CTA leaves
+  for (int n = max(0, static_cast<int>(prod.issued) - S); n < static_cast<int>(prod.issued); ++n)
+    mbar_drain(&sh.full[n % S], (n / S) & 1, 100000000ull);
+  for (uint32_t n = loads > static_cast<uint32_t>(p.tables) ? loads - p.tables : 0; n < loads; ++n)
+    mbar_drain(&sh.table[n % p.tables], (n / p.tables) & 1, 100000000ull);
+}
+
+// The forward with a post norm: statistics of the branch, then of the
+// residual, need the row twice in order, which the phases of the kernel above
+// would spread over three iterations (64,000 x 5120: 719 us there).
+template <typename TX, int kV, int kRegs>
+__global__ void __maxnreg__(kRegs) residual_post_fwd_kernel(const ResidualParams p) {
+  constexpr bool kSplit = sizeof(TX) == 4;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ RoleShared sh;
+  const Stage<TX, false> lay(p.D);
+  const int D = p.D, nvec = D / 8, S = p.stages;
+  // shared memory: w2 (if there is one), the gate's slots, the rows' stages
+  const uint32_t table_bytes = align128(4 * static_cast<size_t>(D));
+  uint8_t* const slots = smem + (p.w2 ? table_bytes : 0);
+  uint8_t* const ring = slots + p.tables * table_bytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group_warps = blockDim.x / 32 - 1 - p.stats_warps;
+  const float inv_d = 1.0f / static_cast<float>(D);
+  const KernelCtl ctl{p.err, &sh.abort, p.timeout_ns};
+  const int r_begin = static_cast<int>(blockIdx.x * p.rows_per_cta);
+  const int rows = static_cast<int>(min(p.rows_per_cta, p.rows - blockIdx.x * p.rows_per_cta));
+  if (threadIdx.x == 0) init_roles(p, sh, group_warps);
+  __syncthreads();
+
+  if (warp < group_warps) {
+    const int t = threadIdx.x, nthr = group_warps * 32;
+    float2 gt[kV][4], fa[kV][4], ad[kV][4];  // gate w2, w (1 + scale), b (1 + scale) + shift of row cur
+    int cur = -1, st = 0;
+    uint32_t ph = 0;
+    for (int n = 0; n < rows; ++n) {
+      if (!warp_wait(&sh.ready[st], ph, ctl, kSiteResReady)) break;
+      if (!warp_wait(&sh.full[st], ph, ctl, kSiteResRowFull)) break;
+      const uint8_t* src = ring + st * lay.bytes();
+      const TX* xs = reinterpret_cast<const TX*>(src);
+      const __nv_bfloat16* hs = reinterpret_cast<const __nv_bfloat16*>(src + lay.h());
+      TX* xo = static_cast<TX*>(p.x_out) + static_cast<size_t>(r_begin + n) * D;
+      __nv_bfloat16* yo = p.y + static_cast<size_t>(r_begin + n) * D;
+      const int id = sh.ids[st];
+      if (id < 0) {
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+          const int v = t + i * nthr;
+          if (v < nvec) {
+            float2 f[4];
+            row8<kSplit>(xs, v, nvec, f);
+            store8<kSplit>(xo, v, nvec, f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = both(0.0f);
+            store8<kSplit>(yo, v, nvec, f);
+          }
+        }
+      } else {
+        if (id != cur) {
+          cur = id;
+#pragma unroll
+          for (int i = 0; i < kV; ++i) {
+            const int v = t + i * nthr;
+            if (v < nvec) load_tables<kSplit>(p, id, v, nvec, gt[i], fa[i], ad[i]);
+          }
+        }
+        const RowStats q = sh.stats[st];
+        const float2 hr = both(q.hr), hsub = both(-q.hm), rs = both(q.r), sub = both(-q.m), al = both(p.alpha);
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+          const int v = t + i * nthr;
+          if (v < nvec) {
+            float2 f[4], g[4];
+            row8<kSplit>(xs, v, nvec, f);
+            row8<kSplit>(hs, v, nvec, g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = ffma2(fmul2(fadd2(g[e], hsub), hr), gt[i][e], fmul2(f[e], al));
+            store8<kSplit>(xo, v, nvec, f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = ffma2(fmul2(fadd2(f[e], sub), rs), fa[i][e], ad[i][e]);
+            store8<kSplit>(yo, v, nvec, f);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.empty[st]);
+      if (++st == S) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+  } else if (warp < group_warps + p.stats_warps) {
+    // a warp keeps to its stages, so that it sees every phase of their barriers
+    int st = 0;
+    uint32_t ph = 0;
+    auto step = [&]() {
+      if (++st == S) {
+        st = 0;
+        ph ^= 1u;
+      }
+    };
+    bool alive = !p.w2 || warp_wait(&sh.w2, 0, ctl, kSiteResTable);
+    const float* w2 = reinterpret_cast<const float*>(smem);
+    for (int n = 0; n < rows && alive; ++n, step()) {
+      if (st % p.stats_warps != warp - group_warps) continue;
+      if (!warp_wait(&sh.full[st], ph, ctl, kSiteResRowFull)) break;
+      const uint8_t* src = ring + st * lay.bytes();
+      const TX* xs = reinterpret_cast<const TX*>(src);
+      const __nv_bfloat16* hs = reinterpret_cast<const __nv_bfloat16*>(src + lay.h());
+      if (sh.ids[st] >= 0) {
+        const int slot = sh.slot[st];
+        if (p.tables && !warp_wait(&sh.table[slot & 255], slot >> 8, ctl, kSiteResTable)) break;
+        const float* gate = reinterpret_cast<const float*>(slots + (slot & 255) * table_bytes);
+        RowStats q{};
+        const float Kh = p.post_rms ? 0.0f : first(hs);
+        float2 s1 = both(0.0f), s2 = both(0.0f);
+#pragma unroll 2
+        for (int v = lane; v < nvec; v += 32) {
+          float2 f[4];
+          row8<true>(hs, v, nvec, f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[e] = fadd2(f[e], both(-Kh));
+            s1 = fadd2(s1, f[e]);
+            s2 = ffma2(f[e], f[e], s2);
+          }
+        }
+        const float hm1 = p.post_rms ? 0.0f : total(s1) * inv_d;
+        q.hr = rsqrtf(fmaxf(fmaf(-hm1, hm1, total(s2) * inv_d), 0.0f) + p.eps);
+        q.hm = Kh + hm1;
+        // the residual's difference from its first element
+        float K = 0.0f;
+        if (!p.rms) {
+          const float g0 = (p.tables ? gate[0] : 1.0f) * (p.w2 ? w2[0] : 1.0f);
+          K = fmaf((first(hs) - q.hm) * q.hr, g0, p.alpha * first(xs));
+        }
+        const float2 hr = both(q.hr), hsub = both(-q.hm), al = both(p.alpha);
+        s1 = s2 = both(0.0f);
+#pragma unroll 2
+        for (int v = lane; v < nvec; v += 32) {
+          float2 f[4], g[4], m[4];
+          row8<true>(xs, v, nvec, f);
+          row8<true>(hs, v, nvec, g);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) g[e] = fmul2(fadd2(g[e], hsub), hr);
+          if (p.w2) {
+            row8<true>(w2, v, nvec, m);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) g[e] = fmul2(g[e], m[e]);
+          }
+          if (p.tables) {
+            row8<true>(gate, v, nvec, m);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) g[e] = fmul2(g[e], m[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[e] = fadd2(ffma2(f[e], al, g[e]), both(-K));
+            s1 = fadd2(s1, f[e]);
+            s2 = ffma2(f[e], f[e], s2);
+          }
+        }
+        const float m1 = p.rms ? 0.0f : total(s1) * inv_d;
+        q.r = rsqrtf(fmaxf(fmaf(-m1, m1, total(s2) * inv_d), 0.0f) + p.eps);
+        q.m = K + m1;
+        if (lane == 0) sh.stats[st] = q;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.ready[st]);
+    }
+  } else if (lane == 0) {
+    if (p.w2) {
+      mbar_arrive_expect_tx(&sh.w2, 4 * D);
+      bulk_load(smem, p.w2, 4 * D, &sh.w2);
+    }
+    stream_rows<TX, false>(p, sh, slots, table_bytes, ring, p.gate, nullptr, r_begin, rows, ctl);
+    if (p.w2) mbar_drain(&sh.w2, 0, 100000000ull);
+  }
+  __syncthreads();
+}
+
+// --------------------------------------------------------------- backward
 // Rows of a CTA where padding is cheaper than valid rows: with segment s's
 // cost w_s = pad rows + (16 - pad) valid rows and P_s the cost before it, the
 // k-th boundary is the row at cost k T / n_cta of the total T, taken as evenly
@@ -613,7 +799,7 @@ template <typename TX, int kV, int kRegs, int kBranch>
 __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
   constexpr bool kSplit = sizeof(TX) == 4;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ BwdShared sh;
+  __shared__ RoleShared sh;
   const Stage<TX, true> lay(p.D);
   const int D = p.D, nvec = D / 8, S = p.stages;
   const uint32_t table_bytes = align128(4 * static_cast<size_t>(D)) * (kBranch == kPost ? 2 : 1);
@@ -624,14 +810,7 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
   const KernelCtl ctl{p.err, &sh.abort, p.timeout_ns};
   if (p.valid && warp == 1) split_rows(p, lane, sh.range);
   if (threadIdx.x == 0) {
-    sh.abort = 0;
-    for (int s = 0; s < S; ++s) {
-      mbar_init(&sh.full[s], 1);
-      mbar_init(&sh.ready[s], 1);
-      mbar_init(&sh.empty[s], group_warps);
-    }
-    for (int s = 0; s < p.tables; ++s) mbar_init(&sh.table[s], 1);
-    fence_barrier_init();
+    init_roles(p, sh, group_warps);
     if (!p.valid) {
       sh.range[0] = static_cast<int>(blockIdx.x * p.rows_per_cta);
       sh.range[1] = static_cast<int>(min(blockIdx.x * p.rows_per_cta + p.rows_per_cta, p.rows));
@@ -869,48 +1048,8 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
       if (lane == 0) mbar_arrive(&sh.ready[st]);
     }
   } else if (lane == 0) {
-    Producer<TX, true> prod(p, ring, sh.full, sh.ids, r_begin, r_begin + rows);
-    int st = 0, slot = p.tables - 1, held = -1;  // held: the id whose tables the slot has
-    uint32_t ph = 1;                             // parity of the stage's last empty phase, from the second round on
-    uint32_t loads = 0;                          // table loads so far
-    int last[kMaxTables];                        // the last row that uses each slot
-#pragma unroll
-    for (int i = 0; i < kMaxTables; ++i) last[i] = -1;
-    for (int n = 0; n < rows; ++n) {
-      if (n >= S && !mbar_wait(&sh.empty[st], ph, ctl, kSiteResEmpty)) break;
-      const int id = prod.peek();
-      if (p.tables && id >= 0 && id != held) {
-        held = id;
-        slot = slot + 1 == p.tables ? 0 : slot + 1;
-        // every row that used the slot must have its statistics: those of
-        // the last S - 1 rows are waited for one by one (different warps
-        // take them, in no order), older ones have left their stages
-        const int end = slot == 0 ? last[0] : last[1];
-        bool free = true;
-        for (int row = max(0, n - S + 1); row <= end && free; ++row)
-          free = mbar_wait(&sh.ready[row % S], (row / S) & 1, ctl, kSiteResTable);
-        if (!free) break;
-        uint8_t* dst = smem + slot * table_bytes;
-        mbar_arrive_expect_tx(&sh.table[slot], 4 * D * (kBranch == kPost ? 2 : 1));
-        bulk_load(dst, p.factors + static_cast<size_t>(id) * D, 4 * D, &sh.table[slot]);
-        if (kBranch == kPost)
-          bulk_load(dst + align128(4 * static_cast<size_t>(D)), p.gates + static_cast<size_t>(id) * D, 4 * D,
-                    &sh.table[slot]);
-        ++loads;
-      }
-      if (id >= 0) (slot == 0 ? last[0] : last[1]) = n;
-      sh.slot[st] = slot | (p.tables ? static_cast<int>(((loads - 1) / p.tables) & 1) << 8 : 0);
-      prod.issue();
-      if (++st == S) {
-        st = 0;
-        ph ^= 1u;
-      }
-    }
-    // copies still in flight land before the CTA leaves
-    for (int n = max(0, static_cast<int>(prod.issued) - S); n < static_cast<int>(prod.issued); ++n)
-      mbar_drain(&sh.full[n % S], (n / S) & 1, 100000000ull);
-    for (uint32_t n = loads > static_cast<uint32_t>(p.tables) ? loads - p.tables : 0; n < loads; ++n)
-      mbar_drain(&sh.table[n % p.tables], (n / p.tables) & 1, 100000000ull);
+    stream_rows<TX, true>(p, sh, smem, table_bytes, ring, p.factors, kBranch == kPost ? p.gates : nullptr, r_begin, rows,
+                          ctl);
   }
   __syncthreads();
 }
@@ -989,20 +1128,24 @@ __global__ void __launch_bounds__(32 * kFinWarps) residual_rows_kernel(const Fin
   const int lane = threadIdx.x, w = threadIdx.y, W = blockDim.y;
   const int s = blockIdx.x;
   const int d = blockIdx.y * 128 + lane * 4;
-  const int c0 = static_cast<int>(p.lo[s]), c1 = p.hi[s];  // none: lo = 0xffffffff, hi = -1
+  const int c0 = static_cast<int>(__ldg(p.lo + s)), c1 = __ldg(p.hi + s);  // none: lo = 0xffffffff, hi = -1
+  const int ordered = __ldg(p.ordered);
   const int sums = p.branch ? 3 : 2;
   float4 a[3];
 #pragma unroll
   for (int k = 0; k < 3; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (d < p.D && c1 >= 0) {
     for (int c = c0 + w; c <= c1; c += W) {
-      const int slot = c + s;
-      if (p.tag[slot] != s) continue;  // a CTA of padding between two that met the id
+      const int slot = c + s, tag = __ldg(p.tag + slot);
+      float4 v[3];
 #pragma unroll
       for (int k = 0; k < 3; ++k)
         if (k < sums)
-          a[k] = add4(a[k], __ldg(reinterpret_cast<const float4*>(
-                                p.part + (static_cast<size_t>(k) * p.n_slots + slot) * p.D + d)));
+          v[k] = __ldg(reinterpret_cast<const float4*>(p.part + (static_cast<size_t>(k) * p.n_slots + slot) * p.D + d));
+      if (tag != s) continue;  // not this id's: a CTA of padding between two that met it
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (k < sums) a[k] = add4(a[k], v[k]);
     }
   }
   if (W > 1) {
@@ -1015,7 +1158,7 @@ __global__ void __launch_bounds__(32 * kFinWarps) residual_rows_kernel(const Fin
       for (int k = 0; k < 3; ++k) a[k] = add4(a[k], acc[i][k][lane]);
   }
   if (d >= p.D) return;
-  if (*p.ordered != -1) {
+  if (ordered != -1) {
     const float nan = __int_as_float(0x7fffffff);
 #pragma unroll
     for (int k = 0; k < 3; ++k) a[k] = make_float4(nan, nan, nan, nan);
@@ -1067,38 +1210,48 @@ __global__ void __launch_bounds__(256) residual_vectors_kernel(const FinalParams
 }
 
 // Launch shape: threads cover the row's 8-wide groups, kV each, in whole
-// warps; as many CTAs per SM as registers and two stages each allow.
-constexpr int kStatsWarps = 2;
+// warps; as many CTAs per SM as registers and two stages each allow.  kRoles:
+// the kernels with warp roles have their statistics and copying warps besides.
 template <typename TX, int kV, int kRegs, int kBranch, bool kBwd>
 pvl_status launch_rows(ResidualParams p, cudaStream_t s, const char* who) {
-  const void* fn;
-  if constexpr (kBwd) fn = reinterpret_cast<const void*>(&residual_bwd_kernel<TX, kV, kRegs, kBranch>);
-  else fn = reinterpret_cast<const void*>(&residual_fwd_kernel<TX, kV, kRegs, kBranch>);
+  constexpr bool kRoles = kBwd || kBranch == kPost;
+  void (*fn)(ResidualParams);
+  if constexpr (kBwd) fn = &residual_bwd_kernel<TX, kV, kRegs, kBranch>;
+  else if constexpr (kRoles) fn = &residual_post_fwd_kernel<TX, kV, kRegs>;
+  else fn = &residual_fwd_kernel<TX, kV, kRegs, kBranch>;
   int threads = ((p.D / 8 + kV - 1) / kV + 31) / 32 * 32;
-  if (kBwd) {
+  if (kRoles) {
     // registers are a quarter of the SM's per scheduler, warps whole
     constexpr int kMostWarps = 4 * (512 / kRegs);
-    p.stats_warps = std::min(kStatsWarps, kMostWarps - threads / 32 - 1);
+    // four statistics warps where a row needs two passes of theirs; two where
+    // one does, or where two more would cost a CTA of few warps its neighbour
+    const int stats = kBranch == kPost && (!kBwd || threads >= 160) ? 4 : 2;
+    p.stats_warps = std::min(stats, kMostWarps - threads / 32 - 1);
     threads += 32 * (p.stats_warps + 1);
   }
   const int stage_bytes = static_cast<int>(Stage<TX, kBwd>(p.D).bytes());
   const int sms = sm_count(), smem_sm = smem_per_sm();
-  int occ = blocks_per_sm(fn, threads, 0);
+  int occ = blocks_per_sm(reinterpret_cast<const void*>(fn), threads, 0);
   if (sms <= 0 || smem_sm <= 0 || occ <= 0) return fail(PVL_ERR_CUDA, "%s: no usable CUDA device", who);
-  constexpr int kReserve = 1024 + static_cast<int>(align128(kBwd ? sizeof(BwdShared) : sizeof(Shared)));  // per CTA: the system's share, static
-  const int table_bytes = kBwd ? static_cast<int>(align128(4 * p.D)) * (kBranch == kPost ? 2 : 1) : 0;
+  // per CTA: the system's share, the static shared memory, and what is kept of the tables
+  const int row_bytes = static_cast<int>(align128(4 * p.D));
+  const int reserve = 1024 + static_cast<int>(align128(kRoles ? sizeof(RoleShared) : sizeof(Shared)));
+  const int fixed = kRoles && !kBwd && p.w2 ? row_bytes : 0;
+  const int table_bytes = row_bytes * (kBwd && kBranch == kPost ? 2 : 1);
+  const bool tables = kBwd || (kRoles && p.gate);
   int stages = 0;
   for (; occ >= 1; --occ) {
+    const int room = smem_sm / occ - reserve - fixed;
     // two table slots where they leave five stages, else one
-    p.tables = kBwd ? 2 : 0;
-    stages = (smem_sm / occ - kReserve - p.tables * table_bytes) / stage_bytes;
-    if (kBwd && stages < 5) {
+    p.tables = tables ? 2 : 0;
+    stages = (room - p.tables * table_bytes) / stage_bytes;
+    if (tables && stages < 5) {
       p.tables = 1;
-      stages = (smem_sm / occ - kReserve - table_bytes) / stage_bytes;
+      stages = (room - table_bytes) / stage_bytes;
     }
     if (kBwd && kRegs == 96 && stages < 2 && occ == 1) {
       p.tables = 0;
-      stages = (smem_sm - kReserve) / stage_bytes;
+      stages = room / stage_bytes;
     }
     if (stages >= 2) break;
   }
@@ -1110,20 +1263,25 @@ pvl_status launch_rows(ResidualParams p, cudaStream_t s, const char* who) {
   p.rows_per_cta = (p.rows + grid - 1) / grid;
   grid = (p.rows + p.rows_per_cta - 1) / p.rows_per_cta;
   if (p.stages > p.rows_per_cta) p.stages = p.rows_per_cta < 2 ? 2 : static_cast<int>(p.rows_per_cta);
-  if (p.stats_warps > p.stages) p.stats_warps = p.stages;  // the others find no stage
-  const int smem = p.stages * stage_bytes + p.tables * table_bytes;
+  // each statistics warp has stages of its own; one too many works on groups
+  if (p.stats_warps > p.stages) p.stats_warps = p.stages;
+  const int smem = p.stages * stage_bytes + p.tables * table_bytes + fixed;
   // the exact size, so that the kernel is allowed it
-  if (blocks_per_sm(fn, threads, smem) <= 0) return fail(PVL_ERR_CUDA, "%s: no usable CUDA device", who);
-  if constexpr (kBwd) residual_bwd_kernel<TX, kV, kRegs, kBranch><<<static_cast<unsigned>(grid), threads, smem, s>>>(p);
-  else residual_fwd_kernel<TX, kV, kRegs, kBranch><<<static_cast<unsigned>(grid), threads, smem, s>>>(p);
+  if (blocks_per_sm(reinterpret_cast<const void*>(fn), threads, smem) <= 0)
+    return fail(PVL_ERR_CUDA, "%s: no usable CUDA device", who);
+  fn<<<static_cast<unsigned>(grid), threads, smem, s>>>(p);
   return check_cuda(cudaGetLastError(), who);
 }
 
+// Groups a thread and registers.  Three groups a thread need the fewest
+// warps, whose work on a row beyond its features (waits, statistics) is then
+// paid least often; short rows take one (64k x 1024 backward: 247 us against
+// 297), rows past 5120 features two backward (D = 8192: 404 us, 466 with three).
 template <typename TX, int kBranch, bool kBwd>
 pvl_status pick_width(const ResidualParams& p, cudaStream_t s, const char* who) {
   if constexpr (!kBwd) {
-    if (p.D < 512) return launch_rows<TX, 1, 96, kBranch, kBwd>(p, s, who);
-    return launch_rows<TX, 2, kBranch == kPost ? 128 : 96, kBranch, kBwd>(p, s, who);
+    if (p.D < 512) return launch_rows<TX, 1, 80, kBranch, kBwd>(p, s, who);
+    return launch_rows<TX, 3, 128, kBranch, kBwd>(p, s, who);
   } else {
     if (p.D > 5120) return launch_rows<TX, 2, 96, kBranch, kBwd>(p, s, who);
     if (p.D >= 1536) return launch_rows<TX, 3, 168, kBranch, kBwd>(p, s, who);
