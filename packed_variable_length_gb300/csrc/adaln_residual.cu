@@ -254,6 +254,26 @@ struct Stage {
   __host__ __device__ size_t bytes() const { return kBwd ? 2 * x_bytes + 2 * h_bytes : x_bytes + h_bytes; }
 };
 
+// mbar_wait behind some tests without suspension: a suspended thread takes
+// longer to wake than the waits of a well-fed pipeline last (64,000 x 5120:
+// forward 419 -> 401 us, backward 595 -> 587).  Not for the kernels with a post
+// norm, whose statistics warps need the issue slots (900 us, 927 with tests).
+__device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity, const KernelCtl& ctl, uint32_t where) {
+#pragma unroll 1
+  for (int i = 0; i < 30; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+  }
+  return mbar_wait(bar, parity, ctl, where);
+}
+
 // Thread 0's view of the CTA's row stream: which row to copy next, the id of
 // that row (read one row ahead), and what has been issued.
 template <typename TX, bool kBwd>
@@ -397,7 +417,7 @@ __global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
     Flight a{};
     bool ok = true;
     if (next < r_end) {
-      ok = mbar_wait(&sh.full[st], ph, ctl, kSiteResRowFull);
+      ok = test_wait(&sh.full[st], ph, ctl, kSiteResRowFull);
       const int id = sh.ids[st];
       a = Flight{true, next, st, id, 0.0f, 0.0f};
       if (id >= 0 && id != cur) {  // the row before is done with its tables
@@ -498,8 +518,9 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 __device__ __forceinline__ float total(float2 v) { return warp_sum(v.x + v.y); }
 // A wait of a whole warp: the same answer in every lane.
+template <bool kTest>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const KernelCtl& ctl, uint32_t where) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctl, where));
+  return __all_sync(0xffffffffu, kTest ? test_wait(bar, parity, ctl, where) : mbar_wait(bar, parity, ctl, where));
 }
 
 __device__ __forceinline__ void init_roles(const ResidualParams& p, RoleShared& sh, int group_warps) {
@@ -594,8 +615,8 @@ __global__ void __maxnreg__(kRegs) residual_post_fwd_kernel(const ResidualParams
     int cur = -1, st = 0;
     uint32_t ph = 0;
     for (int n = 0; n < rows; ++n) {
-      if (!warp_wait(&sh.ready[st], ph, ctl, kSiteResReady)) break;
-      if (!warp_wait(&sh.full[st], ph, ctl, kSiteResRowFull)) break;
+      if (!warp_wait<false>(&sh.ready[st], ph, ctl, kSiteResReady)) break;
+      if (!warp_wait<false>(&sh.full[st], ph, ctl, kSiteResRowFull)) break;
       const uint8_t* src = ring + st * lay.bytes();
       const TX* xs = reinterpret_cast<const TX*>(src);
       const __nv_bfloat16* hs = reinterpret_cast<const __nv_bfloat16*>(src + lay.h());
@@ -659,22 +680,22 @@ __global__ void __maxnreg__(kRegs) residual_post_fwd_kernel(const ResidualParams
         ph ^= 1u;
       }
     };
-    bool alive = !p.w2 || warp_wait(&sh.w2, 0, ctl, kSiteResTable);
+    bool alive = !p.w2 || warp_wait<false>(&sh.w2, 0, ctl, kSiteResTable);
     const float* w2 = reinterpret_cast<const float*>(smem);
     for (int n = 0; n < rows && alive; ++n, step()) {
       if (st % p.stats_warps != warp - group_warps) continue;
-      if (!warp_wait(&sh.full[st], ph, ctl, kSiteResRowFull)) break;
+      if (!warp_wait<false>(&sh.full[st], ph, ctl, kSiteResRowFull)) break;
       const uint8_t* src = ring + st * lay.bytes();
       const TX* xs = reinterpret_cast<const TX*>(src);
       const __nv_bfloat16* hs = reinterpret_cast<const __nv_bfloat16*>(src + lay.h());
       if (sh.ids[st] >= 0) {
         const int slot = sh.slot[st];
-        if (p.tables && !warp_wait(&sh.table[slot & 255], slot >> 8, ctl, kSiteResTable)) break;
+        if (p.tables && !warp_wait<false>(&sh.table[slot & 255], slot >> 8, ctl, kSiteResTable)) break;
         const float* gate = reinterpret_cast<const float*>(slots + (slot & 255) * table_bytes);
         RowStats q{};
         const float Kh = p.post_rms ? 0.0f : first(hs);
         float2 s1 = both(0.0f), s2 = both(0.0f);
-#pragma unroll 2
+#pragma unroll 3
         for (int v = lane; v < nvec; v += 32) {
           float2 f[4];
           row8<true>(hs, v, nvec, f);
@@ -696,7 +717,7 @@ __global__ void __maxnreg__(kRegs) residual_post_fwd_kernel(const ResidualParams
         }
         const float2 hr = both(q.hr), hsub = both(-q.hm), al = both(p.alpha);
         s1 = s2 = both(0.0f);
-#pragma unroll 2
+#pragma unroll 3
         for (int v = lane; v < nvec; v += 32) {
           float2 f[4], g[4], m[4];
           row8<true>(xs, v, nvec, f);
@@ -851,8 +872,8 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
     int st = 0;
     uint32_t ph = 0;
     for (int n = 0; n < rows; ++n) {
-      if (!warp_wait(&sh.ready[st], ph, ctl, kSiteResReady)) break;
-      if (!warp_wait(&sh.full[st], ph, ctl, kSiteResRowFull)) break;
+      if (!warp_wait<kBranch != kPost>(&sh.ready[st], ph, ctl, kSiteResReady)) break;
+      if (!warp_wait<kBranch != kPost>(&sh.full[st], ph, ctl, kSiteResRowFull)) break;
       const uint8_t* src = ring + st * lay.bytes();
       const TX* xs = reinterpret_cast<const TX*>(src);
       const __nv_bfloat16* hs = reinterpret_cast<const __nv_bfloat16*>(src + lay.h());
@@ -955,7 +976,7 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
     };
     for (int n = 0; n < rows; ++n, step()) {
       if (st % p.stats_warps != warp - group_warps) continue;
-      if (!warp_wait(&sh.full[st], ph, ctl, kSiteResRowFull)) break;
+      if (!warp_wait<kBranch != kPost>(&sh.full[st], ph, ctl, kSiteResRowFull)) break;
       const uint8_t* src = ring + st * lay.bytes();
       const TX* xs = reinterpret_cast<const TX*>(src);
       const __nv_bfloat16* hs = reinterpret_cast<const __nv_bfloat16*>(src + lay.h());
@@ -970,7 +991,7 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
         const float K = p.rms ? 0.0f : first(xs);
         const float Kh = kBranch == kPost && !p.post_rms ? first(hs) : 0.0f;
         const int slot = sh.slot[st];
-        if (p.tables && !warp_wait(&sh.table[slot & 255], slot >> 8, ctl, kSiteResTable)) break;
+        if (p.tables && !warp_wait<kBranch != kPost>(&sh.table[slot & 255], slot >> 8, ctl, kSiteResTable)) break;
         const float* fac = reinterpret_cast<const float*>(smem + (slot & 255) * table_bytes);
         const float* gat = fac + align128(4 * static_cast<size_t>(D)) / 4;
         if (kRegs == 96 && p.tables == 0) {  // rows so wide that no table fits beside them: from L2
