@@ -1116,10 +1116,13 @@ __global__ void __launch_bounds__(256) residual_tables_kernel(const ResidualPara
 }
 
 // Sums A, B and C of each modulation row from the slots of the CTAs lo..hi
-// that met it, in CTA order.  A CTA takes one id and 128 features: lane l the
-// float4 at feature 4 l, warp w the CTAs lo + w, lo + w + W, ...; warp 0 adds
-// the warps' sums in order.  Writes the table gradients, and the plain sums
-// to `tot` ([3][S][D]) where vector gradients follow.
+// that met it.  A CTA takes one id and 4 kLanes features: lane l the float4 at
+// feature 4 l, thread row g of G the CTAs lo + g, lo + g + G, ...; the thread
+// rows' sums are then added in order.  Many ids with a CTA or two each take 32
+// lanes and as many thread rows as an id has CTAs; few ids with hundreds each
+// take 8 lanes and 32 thread rows (one id, 900 CTAs: one warp a 128 features
+// took 60 us).  Writes the table gradients, and the plain sums to `tot`
+// ([3][S][D]) where vector gradients follow.
 struct FinalParams {
   const float* part;
   const unsigned int* lo;
@@ -1132,7 +1135,7 @@ struct FinalParams {
   int D, S, n_slots;
   bool branch;
 };
-constexpr int kFinWarps = 8;
+constexpr int kFinRows = 32;
 
 __device__ __forceinline__ float4 add4(float4 a, float4 b) {
   return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
@@ -1144,11 +1147,12 @@ __device__ __forceinline__ float4 vec4(const float* p, int d, float fill) {
   return p ? __ldg(reinterpret_cast<const float4*>(p + d)) : make_float4(fill, fill, fill, fill);
 }
 
-__global__ void __launch_bounds__(32 * kFinWarps) residual_rows_kernel(const FinalParams p) {
-  __shared__ float4 acc[kFinWarps][3][32];
-  const int lane = threadIdx.x, w = threadIdx.y, W = blockDim.y;
+template <int kLanes>
+__global__ void __launch_bounds__(256) residual_rows_kernel(const FinalParams p) {
+  __shared__ float4 acc[256 / kLanes][3][kLanes];
+  const int lane = threadIdx.x, g = threadIdx.y, G = blockDim.y;
   const int s = blockIdx.x;
-  const int d = blockIdx.y * 128 + lane * 4;
+  const int d = (blockIdx.y * kLanes + lane) * 4;
   const int c0 = static_cast<int>(__ldg(p.lo + s)), c1 = __ldg(p.hi + s);  // none: lo = 0xffffffff, hi = -1
   const int ordered = __ldg(p.ordered);
   const int sums = p.branch ? 3 : 2;
@@ -1156,25 +1160,26 @@ __global__ void __launch_bounds__(32 * kFinWarps) residual_rows_kernel(const Fin
 #pragma unroll
   for (int k = 0; k < 3; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (d < p.D && c1 >= 0) {
-    for (int c = c0 + w; c <= c1; c += W) {
+#pragma unroll 4
+    for (int c = c0 + g; c <= c1; c += G) {
       const int slot = c + s, tag = __ldg(p.tag + slot);
       float4 v[3];
 #pragma unroll
       for (int k = 0; k < 3; ++k)
         if (k < sums)
           v[k] = __ldg(reinterpret_cast<const float4*>(p.part + (static_cast<size_t>(k) * p.n_slots + slot) * p.D + d));
-      if (tag != s) continue;  // not this id's: a CTA of padding between two that met it
+      // a slot that is not this id's: a CTA of padding between two that met it
 #pragma unroll
       for (int k = 0; k < 3; ++k)
-        if (k < sums) a[k] = add4(a[k], v[k]);
+        if (k < sums && tag == s) a[k] = add4(a[k], v[k]);
     }
   }
-  if (W > 1) {
+  if (G > 1) {
 #pragma unroll
-    for (int k = 0; k < 3; ++k) acc[w][k][lane] = a[k];
+    for (int k = 0; k < 3; ++k) acc[g][k][lane] = a[k];
     __syncthreads();
-    if (w > 0) return;
-    for (int i = 1; i < W; ++i)
+    if (g > 0) return;
+    for (int i = 1; i < G; ++i)
 #pragma unroll
       for (int k = 0; k < 3; ++k) a[k] = add4(a[k], acc[i][k][lane]);
   }
@@ -1297,14 +1302,15 @@ pvl_status launch_rows(ResidualParams p, cudaStream_t s, const char* who) {
 // Groups a thread and registers.  Three groups a thread need the fewest
 // warps, whose work on a row beyond its features (waits, statistics) is then
 // paid least often; short rows take one (64k x 1024 backward: 247 us against
-// 297), rows past 5120 features two backward (D = 8192: 404 us, 466 with three).
+// 297), rows past 6912 features, whose nine warps of three groups leave no room for
+// the others, two backward.
 template <typename TX, int kBranch, bool kBwd>
 pvl_status pick_width(const ResidualParams& p, cudaStream_t s, const char* who) {
   if constexpr (!kBwd) {
     if (p.D < 512) return launch_rows<TX, 1, 80, kBranch, kBwd>(p, s, who);
     return launch_rows<TX, 3, 128, kBranch, kBwd>(p, s, who);
   } else {
-    if (p.D > 5120) return launch_rows<TX, 2, 96, kBranch, kBwd>(p, s, who);
+    if (p.D > 6912) return launch_rows<TX, 2, 96, kBranch, kBwd>(p, s, who);
     if (p.D >= 1536) return launch_rows<TX, 3, 168, kBranch, kBwd>(p, s, who);
     return launch_rows<TX, 1, 80, kBranch, kBwd>(p, s, who);
   }
@@ -1527,10 +1533,12 @@ extern "C" pvl_status adaln_residual_bwd(const pvl_residual* a, const void* dx_o
   f.S = p.S;
   f.n_slots = lay.n_slots;
   f.branch = branch != kNoBranch;
-  // warps for the CTAs an id meets on average
+  // CTAs that an id meets on average
   const int per_id = 1 + (lay.n_slots - p.S) / p.S;
-  const int warps = per_id >= 8 ? 8 : per_id >= 4 ? 4 : per_id >= 2 ? 2 : 1;
-  residual_rows_kernel<<<dim3(p.S, (p.D + 127) / 128), dim3(32, warps), 0, s>>>(f);
+  if (per_id > 8)
+    residual_rows_kernel<8><<<dim3(p.S, (p.D + 31) / 32), dim3(8, kFinRows), 0, s>>>(f);
+  else
+    residual_rows_kernel<32><<<dim3(p.S, (p.D + 127) / 128), dim3(32, per_id >= 4 ? 4 : per_id >= 2 ? 2 : 1), 0, s>>>(f);
   st = check_cuda(cudaGetLastError(), who);
   if (st != PVL_OK || !vectors) return st;
   residual_vectors_kernel<<<dim3((p.D + 15) / 16, 3), 256, 0, s>>>(f);
