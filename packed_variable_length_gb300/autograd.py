@@ -8,6 +8,7 @@ sees the mask of its own forward (the class-attribute block-mask hazard of
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import api
 
@@ -70,6 +71,7 @@ class _PackedRotary(torch.autograd.Function):
         return q_out if k is None else (q_out, k_out)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq_out, dk_out=None):
         q, k, positions, q_weight, k_weight = ctx.saved_tensors
         plan, norm, eps = ctx.how
@@ -100,6 +102,7 @@ class _GatedResidual(torch.autograd.Function):
         return y if h is None else (x_out, y)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, *grads):
         x_out, h, gate, shift, scale, weight, bias, post_weight, mod_id = ctx.saved_tensors
         dx_out, dy = grads if ctx.branch else (None, grads[0])

@@ -1250,8 +1250,10 @@ pvl_status launch_rows(ResidualParams p, cudaStream_t s, const char* who) {
     // registers are a quarter of the SM's per scheduler, warps whole
     constexpr int kMostWarps = 4 * (512 / kRegs);
     // four statistics warps where a row needs two passes of theirs; two where
-    // one does, or where two more would cost a CTA of few warps its neighbour
-    const int stats = kBranch == kPost && (!kBwd || threads >= 160) ? 4 : 2;
+    // one does, or where two more would cost a CTA of few warps its neighbour;
+    // half as many for short rows
+    int stats = kBranch == kPost && (!kBwd || threads >= 160) ? 4 : 2;
+    if (threads <= 64 && !(kBwd && kBranch == kPost)) stats /= 2;
     p.stats_warps = std::min(stats, kMostWarps - threads / 32 - 1);
     threads += 32 * (p.stats_warps + 1);
   }

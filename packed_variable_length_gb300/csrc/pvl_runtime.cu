@@ -104,7 +104,7 @@ std::unordered_map<ShapeKey, size_t, ShapeHash> g_allowed;  // threads = smem = 
 int g_smem_sm[kMaxDevices] = {};
 }  // namespace
 
-int blocks_per_sm(const void* fn, int threads, size_t smem) {
+int blocks_per_sm(const void* fn, int threads, size_t smem) try {
   const int dev = current_device();
   if (dev < 0) return 0;
   std::lock_guard<std::mutex> lock(g_mu);
@@ -121,6 +121,8 @@ int blocks_per_sm(const void* fn, int threads, size_t smem) {
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem) != cudaSuccess) return 0;
   if (n > 0) g_blocks.emplace(key, n);
   return n;
+} catch (...) {  // no memory for the table: no exception leaves a C entry point
+  return 0;
 }
 
 int smem_per_sm() {

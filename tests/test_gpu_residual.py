@@ -360,6 +360,38 @@ def test_autograd(pvl):
     assert torch.equal(g, torch.where(live, 0.75, 1.0).expand_as(g))
 
 
+def test_offsets_past_32_bits(pvl):
+    """2.3 G elements: the last rows, and the gradients of the last modulation row, are those of the same rows alone."""
+    N, D, n = 450001, 5120, 61
+    x = torch.ones(1, N, D, dtype=torch.bfloat16, device="cuda")
+    h = torch.ones(1, N, D, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(15)
+    x[:, -n:] = torch.randn(1, n, D, generator=g, device="cuda").to(torch.bfloat16)
+    h[:, -n:] = torch.randn(1, n, D, generator=g, device="cuda").to(torch.bfloat16)
+    ids = torch.zeros(1, N, dtype=torch.int32, device="cuda")
+    ids[:, -n:] = 1
+    tabs = [torch.randn(2, D, generator=g, device="cuda") for _ in range(3)]
+    x_out, y = pvl.adaln_residual_fwd(x, h, *tabs, mod_id=ids)
+    tail = [t[:, -n:].contiguous() for t in (x, h, ids)]
+    a, b = pvl.adaln_residual_fwd(tail[0], tail[1], *tabs, mod_id=tail[2])
+    assert torch.equal(x_out[:, -n:], a) and torch.equal(y[:, -n:], b)
+    del y
+    G = pvl.adaln_residual_bwd(x_out, h, x_out, h, *tabs, mod_id=ids)
+    T = pvl.adaln_residual_bwd(a, tail[1], a, tail[1], *tabs, mod_id=tail[2])
+    assert torch.equal(G.dx[:, -n:], T.dx) and torch.equal(G.dh[:, -n:], T.dh)
+    for u, v in zip(G[2:5], T[2:5]):    # other CTAs share the rows: another order of 61 fp32 additions
+        assert float((u[1] - v[1]).norm()) <= 61 * 2.0 ** -23 * float(v[1].norm()) * 8
+    pvl.device_error()
+
+
+def test_more_ids_than_rows_a_cta(pvl):
+    """Every token its own modulation row, on a batch of many CTAs, then one row for all."""
+    t, args, how = make(1, 6000, 64, "token", "layer", "rms", "bf16", 16)
+    check(pvl, t, args, how)
+    t, args, how = make(1, 30000, 64, "batch", "rms", None, "bf16", 17)
+    check(pvl, t, args, how)
+
+
 def test_block_together(pvl):
     """One attention block on a packed row, forward and backward, against the formulas in fp64: positions, rotary
     with a norm over the token, masked attention, then the gated residual and the next norm.  Its bf16

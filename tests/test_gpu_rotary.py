@@ -288,3 +288,35 @@ def test_autograd(pvl, norm):
     g = torch.autograd.grad(qo.float().sum(), leaves[0])[0]           # expanded ones come back
     assert torch.equal(g, pvl.pack_rotary_bwd(torch.ones_like(dq), torch.zeros_like(dk), pos, plan, norm, q, k, wq,
                                               wk)[0])
+
+
+def test_offsets_past_32_bits(pvl):
+    """A projection of 2.4 G elements: the last tokens are what the same call gives on a copy of them."""
+    L, H, D = 524289, 12, 128
+    qkv = torch.empty(1, L, 3 * H, D, dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn(1, 77, 3 * H, D, device="cuda").to(torch.bfloat16)
+    qkv[:, :-77] = 1.0
+    qkv[:, -77:] = tail
+    pos = torch.arange(L, dtype=torch.int32, device="cuda")[None]
+    plan = pvl.rotary_plan(D)
+    for norm in (None, "token"):
+        a, b = pvl.pack_rotary_fwd(qkv[:, :, H:2 * H], qkv[:, :, 2 * H:], pos, plan, norm)
+        c, d = pvl.pack_rotary_fwd(tail[:, :, H:2 * H], tail[:, :, 2 * H:], pos[:, -77:].contiguous(), plan, norm)
+        # one team a token either way, but other lanes may add its squares: half a step apart at most
+        assert torch.equal(a[:, -77:], c) if norm is None else bool(((a[:, -77:] - c).abs() <= 2.0 ** -7 * c.abs()).all())
+        assert torch.equal(b[:, -77:], d) if norm is None else bool(((b[:, -77:] - d).abs() <= 2.0 ** -7 * d.abs()).all())
+        del a, b
+    pvl.device_error()
+
+
+def test_one_token_of_many_rows(pvl):
+    """Serving: one token of each of 70,000 sequences, heads first in memory."""
+    B, H, D = 70000, 2, 32
+    q = torch.randn(B, H, 1, D, device="cuda").to(torch.bfloat16).transpose(1, 2)
+    k = torch.randn(B, 1, 1, D, device="cuda").to(torch.bfloat16)
+    pos = torch.randint(0, 1 << 20, (B, 1), dtype=torch.int32, device="cuda")
+    plan = pvl.rotary_plan(D)
+    a, b = pvl.pack_rotary_fwd(q, k, pos, plan, "head")
+    c, d = pvl.pack_rotary_fwd(q.transpose(0, 1).contiguous(), k.transpose(0, 1).contiguous(), pos.t().contiguous(), plan,
+                               "head")
+    assert torch.equal(a.transpose(0, 1), c) and torch.equal(b.transpose(0, 1), d)
