@@ -61,16 +61,13 @@ def _need_cuda(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> No
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _need(t, name: str, dtype: torch.dtype, shape) -> None:
-    """_need_cuda at the price of four attribute reads where all is well."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous() and t.shape == shape):
-        _need_cuda(t, name, dtype, shape)
-
-
-def _need_same_device(device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+def _need(t, name: str, dtype: torch.dtype, shape, device: torch.device) -> None:
+    """_need_cuda, on a given device, at the price of a few attribute reads where all is well."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.shape == shape and (
+            t.is_contiguous()):
+        return
+    _need_cuda(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
 _current_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -149,7 +146,7 @@ def pack_build_positions(seg_frames, tokens_per_frame: int, L: int, axes: int = 
         if out is None:
             out = torch.empty((B, int(L), int(axes)), dtype=torch.int32, device=device)
         else:
-            _need(out, "out", torch.int32, (B, int(L), int(axes)))
+            _need_cuda(out, "out", torch.int32, (B, int(L), int(axes)))
         _check(_lib.load().pack_build_positions(frames.tobytes(), B, K, int(tokens_per_frame), int(axes),
                                                 int(row_width or 1), int(L), out.data_ptr(), handle))
     return out
@@ -500,11 +497,13 @@ def rotary_plan(rotary_dim: int, base: float = 10000.0, layout: str = "half", se
     return RotaryPlan(table, R, layout, sections, float(gain))
 
 
-def _heads_view(t, name: str, shape) -> bytes | None:
+def _heads_view(t, name: str, shape, device) -> bytes | None:
     if t is None:
         return None
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
     if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.shape != shape:
@@ -525,6 +524,7 @@ def _rotary(like_q, like_k, positions, plan: RotaryPlan, norm, q_weight, k_weigh
     if like_q.dim() != 4 or (like_k is not None and like_k.dim() != 4):
         raise ValueError("q and k must be [B, L, heads, D]")
     B, L, H, D = like_q.shape
+    device = like_q.device
     Hk = 0 if like_k is None else int(like_k.shape[2])
     if like_k is not None and (like_k.shape != (B, L, Hk, D) or Hk < 1):
         raise ValueError(f"k must be [{B}, {L}, Hk, {D}], got {tuple(like_k.shape)}")
@@ -533,17 +533,17 @@ def _rotary(like_q, like_k, positions, plan: RotaryPlan, norm, q_weight, k_weigh
     axes = len(plan.sections)
     if axes == 1 and positions.dim() == 2:
         positions = positions.unsqueeze(2)
-    _need(positions, "positions", torch.int32, (B, L, axes))
+    _need(positions, "positions", torch.int32, (B, L, axes), device)
     for name, w, n in (("q_weight", q_weight, H), ("k_weight", k_weight, Hk)):
         if w is None:
             continue
         if norm is None or (n == 0):
             raise ValueError(f"{name} needs a norm and its heads")
-        _need(w, name, torch.float32, w.shape)
+        _need(w, name, torch.float32, w.shape, device)
         if w.numel() != (n * D if norm == "token" else D):
             raise ValueError(f"{name} must hold {n * D if norm == 'token' else D} values, got {w.numel()}")
-    _need_same_device(like_q.device, k=like_k, positions=positions, plan=plan.turns, q_weight=q_weight,
-                      k_weight=k_weight)
+    if plan.turns.device != device:
+        raise ValueError(f"the plan is on {plan.turns.device}, not on {device}")
     s = plan.sections
     s1 = s[0]
     s2 = s1 + (s[1] if axes > 1 else 0)
@@ -562,15 +562,15 @@ def pack_rotary_fwd(q, k, positions, plan: RotaryPlan, norm: str | None = None, 
     a weight of None is 1.  q and k may be slices with any strides but that of
     D; the outputs are contiguous unless given, and may be q and k."""
     how, qs, ks = _rotary(q, k, positions, plan, norm, q_weight, k_weight, eps)
-    _need_same_device(q.device, q_out=q_out, k_out=k_out)
-    with _launch(q.device, stream) as handle:
+    dev = q.device
+    with _launch(dev, stream) as handle:
         if q_out is None:
-            q_out = torch.empty(qs, dtype=q.dtype, device=q.device)
+            q_out = torch.empty(qs, dtype=torch.bfloat16, device=dev)
         if k is not None and k_out is None:
-            k_out = torch.empty(ks, dtype=k.dtype, device=k.device)
-        _check(_lib.load().pack_rotary_fwd(how, _heads_view(q, "q", qs), _heads_view(k, "k", ks),
-                                           _heads_view(q_out, "q_out", qs),
-                                           None if k is None else _heads_view(k_out, "k_out", ks), handle))
+            k_out = torch.empty(ks, dtype=torch.bfloat16, device=dev)
+        _check(_lib.load().pack_rotary_fwd(how, _heads_view(q, "q", qs, dev), _heads_view(k, "k", ks, dev),
+                                           _heads_view(q_out, "q_out", qs, dev),
+                                           None if k is None else _heads_view(k_out, "k_out", ks, dev), handle))
     return q_out, (None if k is None else k_out)
 
 
@@ -585,20 +585,19 @@ def pack_rotary_bwd(dq_out, dk_out, positions, plan: RotaryPlan, norm: str | Non
         raise ValueError("the backward of a norm needs q and k")
     if norm is None:
         q = k = None
-    _need_same_device(dq_out.device, q=q, k=k, dq=dq, dk=dk)
-    lib = _lib.load()
-    with _launch(dq_out.device, stream) as handle:
+    lib, dev = _lib.load(), dq_out.device
+    with _launch(dev, stream) as handle:
         if dq is None:
-            dq = torch.empty(qs, dtype=dq_out.dtype, device=dq_out.device)
+            dq = torch.empty(qs, dtype=torch.bfloat16, device=dev)
         if keys and dk is None:
-            dk = torch.empty(ks, dtype=dk_out.dtype, device=dk_out.device)
+            dk = torch.empty(ks, dtype=torch.bfloat16, device=dev)
         dq_weight = None if q_weight is None else torch.empty_like(q_weight)
         dk_weight = None if k_weight is None else torch.empty_like(k_weight)
         nbytes = int(lib.pack_rotary_bwd_ws_bytes(how))
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dq_out.device) if nbytes else None
-        _check(lib.pack_rotary_bwd(how, _heads_view(dq_out, "dq_out", qs), _heads_view(dk_out, "dk_out", ks),
-                                   _heads_view(q, "q", qs), _heads_view(k, "k", ks) if keys else None,
-                                   _heads_view(dq, "dq", qs), _heads_view(dk, "dk", ks) if keys else None,
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        _check(lib.pack_rotary_bwd(how, _heads_view(dq_out, "dq_out", qs, dev), _heads_view(dk_out, "dk_out", ks, dev),
+                                   _heads_view(q, "q", qs, dev), _heads_view(k, "k", ks, dev) if keys else None,
+                                   _heads_view(dq, "dq", qs, dev), _heads_view(dk, "dk", ks, dev) if keys else None,
                                    _ptr(dq_weight), _ptr(dk_weight), _ptr(ws), nbytes, handle))
     return dq, (dk if keys else None), dq_weight, dk_weight
 
@@ -621,9 +620,10 @@ def _residual(x, gate, shift, scale, mod_id, weight, bias, post_weight, norm, po
     if x.dim() != 3:
         raise ValueError("x must be [B, N, D]")
     B, N, D = x.shape
+    device = x.device
     if x.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"x must be {torch.bfloat16} or {torch.float32}, got {x.dtype}")
-    _need(x, "x", x.dtype, x.shape)
+    _need_cuda(x, "x", x.dtype)
     if norm not in ("layer", "rms"):
         raise ValueError(f"norm must be 'layer' or 'rms', got {norm!r}")
     if post_norm not in (None, "layer", "rms"):
@@ -635,16 +635,14 @@ def _residual(x, gate, shift, scale, mod_id, weight, bias, post_weight, norm, po
         if t.dim() != 2:
             raise ValueError(f"{name} must be [S, D]")
         S = int(t.shape[0]) if S is None else S
-        _need(t, name, torch.float32, (S, D))
+        _need(t, name, torch.float32, (S, D), device)
     if mod_id is not None:
-        _need(mod_id, "mod_id", torch.int32, (B, N))
+        _need(mod_id, "mod_id", torch.int32, (B, N), device)
     elif S is not None and S != B:
         raise ValueError(f"without mod_id the modulation tables must have B = {B} rows, got {S}")
     for name, t in (("weight", weight), ("bias", bias), ("post_weight", post_weight)):
         if t is not None:
-            _need(t, name, torch.float32, (D,))
-    _need_same_device(x.device, gate=gate, shift=shift, scale=scale, mod_id=mod_id, weight=weight, bias=bias,
-                      post_weight=post_weight)
+            _need(t, name, torch.float32, (D,), device)
     return _lib.PACK_RESIDUAL(B, N, D, S or 1, 1 if x.dtype == torch.float32 else 0, _NORMS[norm], _NORMS[post_norm],
                          float(alpha), float(eps), _addr(gate), _addr(shift), _addr(scale), _addr(weight), _addr(bias),
                          _addr(post_weight), _addr(mod_id)), S or 1
@@ -665,17 +663,18 @@ def adaln_residual_fwd(x, h=None, gate=None, shift=None, scale=None, *, mod_id=N
     Without h, x_out is x itself and y its modulated norm."""
     how, _ = _residual(x, gate, shift, scale, mod_id, weight, bias, post_weight, norm, post_norm, alpha, eps)
     if h is not None:
-        _need(h, "h", torch.bfloat16, x.shape)
-    _need_same_device(x.device, h=h, x_out=x_out, y=y)
+        _need(h, "h", torch.bfloat16, x.shape, x.device)
     with _launch(x.device, stream) as handle:
         if h is None:
             x_out = x
         elif x_out is None:
             x_out = torch.empty_like(x)
+        else:
+            _need(x_out, "x_out", x.dtype, x.shape, x.device)
         if y is None:
             y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-        _need(x_out, "x_out", x.dtype, x.shape)
-        _need(y, "y", torch.bfloat16, x.shape)
+        else:
+            _need(y, "y", torch.bfloat16, x.shape, x.device)
         _check(_lib.load().adaln_residual_fwd(how, x.data_ptr(), _ptr(h), x_out.data_ptr(), y.data_ptr(),
                                               handle))
     return x_out, y
@@ -699,23 +698,25 @@ def adaln_residual_bwd(dx_out, dy, x_out, h=None, gate=None, shift=None, scale=N
     B, N, D = x_out.shape
     branch = h is not None if branch is None else bool(branch)
     if h is not None:
-        _need(h, "h", torch.bfloat16, x_out.shape)
-    _need(dy, "dy", torch.bfloat16, x_out.shape)
+        _need(h, "h", torch.bfloat16, x_out.shape, x_out.device)
+    _need(dy, "dy", torch.bfloat16, x_out.shape, x_out.device)
     if dx_out is not None:
-        _need(dx_out, "dx_out", x_out.dtype, x_out.shape)
-    _need_same_device(x_out.device, h=h, dy=dy, dx_out=dx_out, dx=dx, dh=dh, ws=ws)
+        _need(dx_out, "dx_out", x_out.dtype, x_out.shape, x_out.device)
     lib = _lib.load()
     with _launch(x_out.device, stream) as handle:
         if dx is None:
             dx = torch.empty_like(x_out)
+        else:
+            _need(dx, "dx", x_out.dtype, x_out.shape, x_out.device)
         if branch and dh is None:
             dh = torch.empty(x_out.shape, dtype=torch.bfloat16, device=x_out.device)
-        _need(dx, "dx", x_out.dtype, x_out.shape)
-        if branch:
-            _need(dh, "dh", torch.bfloat16, x_out.shape)
+        elif branch:
+            _need(dh, "dh", torch.bfloat16, x_out.shape, x_out.device)
         params = (gate, shift, scale, weight, bias, post_weight)
         grads = [None if t is None else torch.empty_like(t) for t in params]
-        if ws is None:
+        if ws is not None:
+            _need(ws, "ws", torch.uint8, ws.shape, x_out.device)
+        else:
             ws = torch.empty(adaln_residual_bwd_ws_bytes(B, N, D, S), dtype=torch.uint8, device=x_out.device)
         out = _lib.PACK_RESIDUAL_GRADS(*(_addr(t) for t in grads))
         _check(lib.adaln_residual_bwd(how, _ptr(dx_out), dy.data_ptr(), x_out.data_ptr(), _ptr(h),

@@ -16,24 +16,40 @@
 //
 // Design.  HBM bound: 8 bytes an element forward and 12 backward with a bf16
 // stream, each touched once.
-//   - Persistent CTAs walk contiguous row ranges.  Thread 0 streams the rows
-//     of every input into a ring of shared-memory stages with bulk copies;
-//     each thread owns the same 8-wide feature groups of every row.  Padding
-//     rows skip the copies of what they do not use (their ids are read one
-//     row ahead, so that the test costs no latency).
+//   - Persistent CTAs walk contiguous row ranges.  One lane streams the rows of
+//     every input into a ring of shared-memory stages with bulk copies; each
+//     thread owns the same 8-wide feature groups of every row.  Padding rows
+//     skip the copies of what they do not use (their ids are read one row
+//     ahead, so that the test costs no latency).
+//   - What bounds a row's time is its chain of waits and reductions, not its
+//     arithmetic, so two schemes take the reductions off it: the forward
+//     without a post norm overlaps the phases of neighbouring rows
+//     (residual_fwd_kernel), the others have warps of their own for the
+//     statistics (the warp roles below).
 //   - Forward, the three tables of the current modulation row (gate w2,
 //     w (1 + scale), b (1 + scale) + shift) stay in registers and are loaded
 //     again where the id changes.  Backward the registers hold the sums A, B
-//     and C of the current modulation row, and the tables come from L1.
+//     and C of the current modulation row and two tables, which a small kernel
+//     has prepared so that the statistics' warps can have them copied into
+//     shared memory.
 //   - A row's statistics are sums shifted by the row's first element K (as in
 //     adaln.cu: one pass, the cancellation bounded because K is a sample of
-//     the row); the RMS norm takes K = 0.  One block reduction per norm.
+//     the row); the RMS norm takes K = 0.
 //   - The sums of a CTA's run of equal ids go to slot (CTA + id): with ids
 //     that do not decrease along the rows no two runs share a slot, so the
 //     partial sums need n_cta + S rows and no atomics on values; a small
 //     kernel adds the slots of each id in CTA order (deterministic).  A slot
 //     claimed twice (ids out of order) is detected, recorded as an error and
 //     turns every table gradient into NaN.
+// Roundings to fewer than 32 bits: x_out and dx to the stream's type, y and dh
+// to bf16, each once and last.
+//
+// Measured (of 6770 GB/s, the card's copy rate): 64,000 x 5120, bf16, seven
+// episodes: forward 400 us = 97 %, backward 587 us = 99 %; with an RMS post norm
+// 422 and 900 us (92 %, 65 %: there the statistics' two passes over a row hold
+// one of its four stages too long).  Four padded rows of 10,944 x 1536, fp32
+// stream, RMS norms on both sides, 1152 modulation rows: 137 and 227 us (86 %,
+// 74 %, of which 31 us are the tables and the sums of the modulation rows).
 // Every wait is bounded, as in the other kernels.
 #include <cuda_runtime.h>
 

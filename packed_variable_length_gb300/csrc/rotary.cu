@@ -16,7 +16,11 @@
 // by about 2^-21, far below the 2^-9 of the bf16 result.
 //
 // Layout of the work.  HBM bound: 4 bytes an element forward, 6 backward with
-// a norm.
+// a norm.  Measured (of 6770 GB/s, the card's copy rate), 65,536 tokens of 12 +
+// 12 heads of 128 out of a fused projection: forward 138 us without a norm
+// (86 %), 130 with the norm per head (91 %), 136 over the token (88 %); backward
+// 209 us per head (85 %), 227 over the token (79 %: the chain of sum, norm and
+// product of a token at twelve warps an SM, not the bytes).
 //   - A unit is two V-wide vectors of a head, R / (2 V) vectors apart, so that
 //     neighbouring threads read neighbouring 16 bytes in both layouts: in the
 //     half layout the vectors hold the two sides of V pairs, in the

@@ -149,3 +149,18 @@ def test_plan_refusals():
             pvl.rotary_plan(**{"rotary_dim": 64, "device": "cpu", **kw})
     plan = pvl.rotary_plan(64, device="cpu", sections=(12, 10, 10))
     assert plan.turns.shape == (32,) and plan.gain == 1.0 and plan.sections == (12, 10, 10)
+
+
+def test_tensors_of_the_host_are_refused():
+    """Nothing of a call whose tensors are all on the host reaches the library."""
+    import torch
+
+    import packed_variable_length_gb300 as pvl
+    x = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    q, pos = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16), torch.zeros(1, 4, dtype=torch.int32)
+    plan = pvl.rotary_plan(64, device="cpu")
+    for call in (lambda: pvl.adaln_residual_fwd(x, x), lambda: pvl.adaln_residual_bwd(x, x, x, x),
+                 lambda: pvl.pack_rotary_fwd(q, q, pos, plan), lambda: pvl.pack_rotary_bwd(q, q, pos, plan),
+                 lambda: pvl.pack_build_positions([[1]], 4, 4, out=torch.zeros(1, 4, 1, dtype=torch.int32))):
+        with pytest.raises((ValueError, AssertionError, RuntimeError)):
+            call()
