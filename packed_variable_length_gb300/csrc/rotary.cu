@@ -17,8 +17,8 @@
 //
 // Layout of the work.  HBM bound: 4 bytes an element forward, 6 backward with
 // a norm.  Measured (of 6770 GB/s, the card's copy rate), 65,536 tokens of 12 +
-// 12 heads of 128 out of a fused projection: forward 138 us without a norm
-// (86 %), 130 with the norm per head (91 %), 136 over the token (88 %); backward
+// 12 heads of 128 out of a fused projection: forward 126 us without a norm
+// (95 %), 131 with the norm per head (91 %), 136 over the token (88 %); backward
 // 209 us per head (85 %), 227 over the token (79 %: the chain of sum, norm and
 // product of a token at twelve warps an SM, not the bytes).
 //   - A unit is two V-wide vectors of a head, R / (2 V) vectors apart, so that
@@ -375,8 +375,8 @@ __global__ void __maxnreg__(!kBwd ? 96 : V == 8 || V == 1 ? 168 : 128) rotary_ke
   // With a norm they are copied one item (a token's kM heads a thread) ahead
   // into the thread's own part of a ring: no other thread reads it, so waiting
   // for the copies is all the synchronisation.  Without a norm a thread works
-  // so little on them that direct loads and more threads are faster (64k pack:
-  // 127 us against 146).
+  // so little on them that direct loads and more threads are faster (64k pack,
+  // blocks of four warps: 138 us against 146).
   constexpr bool kAsync = V > 1 && kAny;
   constexpr int kVecs = kBwd ? 4 : 2;
   T* const ring = reinterpret_cast<T*>(smem + plan.ring) + (tid >> 5) * kRing * kM * kVecs * 32 + lane32;
@@ -791,7 +791,13 @@ bool team_of(int V, int kM, int Ht, int D, int norm, Shape* s) {
     // heads that the rounding leaves room for
     s->hpi = std::min(Ht, per ? s->team / 32 * per : s->team / s->units);
   }
-  s->teams = s->team >= 128 ? 1 : (s->team < 32 ? 64 : 128) / s->team;
+  // Without a norm teams share nothing but the block, and 8-wide vectors want
+  // eight warps of them (64k pack, 12 + 12 heads of 128: 126 us; four warps 138,
+  // twelve 137; heads of 64: 67, 72, 75); 4-wide ones four (129; eight 132), and
+  // teams of part of a warp two (2 + 1 heads: 28; eight 31).  Few tokens (one
+  // head a thread) want many blocks.
+  const int threads = norm == PVL_NORM_NONE && V == 8 && kM > 1 && s->team >= 32 ? 256 : s->team < 32 ? 64 : 128;
+  s->teams = s->team >= threads ? 1 : threads / s->team;
   s->threads = s->team * s->teams;
   return true;
 }
