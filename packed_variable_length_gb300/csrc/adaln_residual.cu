@@ -46,9 +46,9 @@
 //
 // Measured (of 6770 GB/s, the card's copy rate): 64,000 x 5120, bf16, seven
 // episodes: forward 400 us = 97 %, backward 587 us = 99 %; with an RMS post norm
-// 422 and 900 us (92 %, 65 %: there the statistics' two passes over a row hold
+// 410 and 898 us (94 %, 65 %: there the statistics' two passes over a row hold
 // one of its four stages too long).  Four padded rows of 10,944 x 1536, fp32
-// stream, RMS norms on both sides, 1152 modulation rows: 137 and 227 us (86 %,
+// stream, RMS norms on both sides, 1152 modulation rows: 138 and 228 us (86 %,
 // 74 %, of which 31 us are the tables and the sums of the modulation rows).
 // Every wait is bounded, as in the other kernels.
 #include <cuda_runtime.h>
@@ -1267,9 +1267,14 @@ pvl_status launch_rows(ResidualParams p, cudaStream_t s, const char* who) {
     constexpr int kMostWarps = 4 * (512 / kRegs);
     // four statistics warps where a row needs two passes of theirs; two where
     // one does, or where two more would cost a CTA of few warps its neighbour;
-    // half as many for short rows
+    // half as many for short rows, where the group warps are what a CTA lacks:
+    // forward by the bytes that a row has them read (64,000 rows, bf16 stream:
+    // 1024 features 137 us, four warps 152; 1536 157, 169; fp32 stream, four rows
+    // of 10,944: 1024 96, 108; 1280 125, 119; 1536 152, 138)
+    const bool narrow = kBwd ? kBranch != kPost && threads <= 64
+                             : (sizeof(TX) + 2) * static_cast<size_t>(p.D) <= 6144;
     int stats = kBranch == kPost && (!kBwd || threads >= 160) ? 4 : 2;
-    if (threads <= 64 && !(kBwd && kBranch == kPost)) stats /= 2;
+    if (narrow) stats /= 2;
     p.stats_warps = std::min(stats, kMostWarps - threads / 32 - 1);
     threads += 32 * (p.stats_warps + 1);
   }
