@@ -348,6 +348,7 @@ PVL_API pvl_status pack_build_positions(const int32_t* seg_frames, int B, int K,
  *   (in elements), so that slices of a fused projection need no copy.  k may
  *   be absent (null pointer with Hk = 0).  An output may be the input of the
  *   same pass (pointer and strides equal); any other overlap is undefined.
+ *   An input may be broadcast (a stride of 0), an output may not.
  * Backward: dq_out, dk_out are the gradients of the outputs; q, k (the
  *   forward's inputs) and the weights are read only with a norm; dq, dk and,
  *   where the weights are given, dq_weight, dk_weight are written.  The
@@ -356,11 +357,12 @@ PVL_API pvl_status pack_build_positions(const int32_t* seg_frames, int B, int K,
  *   description (0 without weights), 16-byte aligned, one call at a time.
  * Limits (UNSUPPORTED): D and R even, D at most 256, H + Hk at most
  *   PVL_MAX_ROTARY_HEADS, and a token whose (H + Hk) D features the norm per
- *   token cannot hold in a block (12,288 always fit).  Tensors whose D, R,
+ *   token cannot hold in a block (12,288 always fit); B L and the strides
+ *   between heads below 2^30.  Tensors whose D, R,
  *   strides and addresses allow 16-byte (else 8-byte) vectors run fastest.
  * Errors: INVALID_ARG for null pointers,
- *   sizes < 1, inconsistent sections, unknown layout or norm, a short
- *   workspace; CUDA for launch failures.
+ *   sizes < 1, inconsistent sections, unknown layout or norm, a broadcast
+ *   output, a short workspace; CUDA for launch failures.
  * ---------------------------------------------------------------------- */
 typedef enum pvl_norm {
   PVL_NORM_NONE = 0,

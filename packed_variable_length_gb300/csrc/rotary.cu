@@ -903,12 +903,16 @@ bool shape_of(const pvl_rotary* a, int V, bool bwd, Shape* s) {
   return team_of(8, 3, Ht, a->D, a->norm, s);
 }
 
-pvl_status check_views(const char* who, const pvl_rotary* a, const pvl_heads* v, int which, const char* name) {
+pvl_status check_views(const char* who, const pvl_rotary* a, const pvl_heads* v, int which, const char* name,
+                       bool written = false) {
   const int heads = which ? a->Hk : a->H;
   if (heads == 0) return PVL_OK;
   if (!v || !v->data) return fail(PVL_ERR_INVALID_ARG, "%s: %s is null", who, name);
   if (reinterpret_cast<uintptr_t>(v->data) % 2 != 0)
     return fail(PVL_ERR_UNSUPPORTED, "%s: %s is not 2-byte aligned", who, name);
+  // several threads would write one place
+  if (written && ((a->B > 1 && v->stride_b == 0) || (a->L > 1 && v->stride_l == 0) || (heads > 1 && v->stride_h == 0)))
+    return fail(PVL_ERR_INVALID_ARG, "%s: %s is broadcast (a stride of 0)", who, name);
   return PVL_OK;
 }
 
@@ -1003,8 +1007,8 @@ extern "C" pvl_status pack_rotary_fwd(const pvl_rotary* a, const pvl_heads* q, c
   pvl_status st = common(who, a, p);
   if (st == PVL_OK) st = check_views(who, a, q, 0, "q");
   if (st == PVL_OK) st = check_views(who, a, k, 1, "k");
-  if (st == PVL_OK) st = check_views(who, a, q_out, 0, "q_out");
-  if (st == PVL_OK) st = check_views(who, a, k_out, 1, "k_out");
+  if (st == PVL_OK) st = check_views(who, a, q_out, 0, "q_out", true);
+  if (st == PVL_OK) st = check_views(who, a, k_out, 1, "k_out", true);
   if (st != PVL_OK) return st;
   if (!a->Hk) k = k_out = nullptr;
   const pvl_heads* views[] = {q, k, q_out, k_out};
@@ -1037,8 +1041,8 @@ extern "C" pvl_status pack_rotary_bwd(const pvl_rotary* a, const pvl_heads* dq_o
   pvl_status st = common(who, a, p);
   if (st == PVL_OK) st = check_views(who, a, dq_out, 0, "dq_out");
   if (st == PVL_OK) st = check_views(who, a, dk_out, 1, "dk_out");
-  if (st == PVL_OK) st = check_views(who, a, dq, 0, "dq");
-  if (st == PVL_OK) st = check_views(who, a, dk, 1, "dk");
+  if (st == PVL_OK) st = check_views(who, a, dq, 0, "dq", true);
+  if (st == PVL_OK) st = check_views(who, a, dk, 1, "dk", true);
   const bool norm = st == PVL_OK && a->norm != PVL_NORM_NONE;
   if (norm) st = check_views(who, a, q, 0, "q");
   if (norm && st == PVL_OK) st = check_views(who, a, k, 1, "k");

@@ -82,6 +82,17 @@ def test_rotary_views_and_workspace(lib):  # noqa: F811
     assert lib.pack_rotary_bwd(*args, None, P, P, need, None) == INVALID          # a weight without its gradient
     assert lib.pack_rotary_bwd(*args, P, P, P + 8, need, None) == UNSUPPORTED
     assert lib.pack_rotary_bwd(normed, heads(), heads(), None, heads(), heads(), heads(), P, P, P, need, None) == INVALID
+    # an output that several threads would write; an input may be broadcast (refused here for its null partner)
+    for zero in ({"t": 0}, {"h": 0}):
+        assert lib.pack_rotary_fwd(how, heads(), heads(), heads(**zero), heads(), None) == INVALID
+        assert b"broadcast" in lib.pvl_last_error_message()
+        assert lib.pack_rotary_fwd(how, heads(), heads(), heads(), heads(**zero), None) == INVALID
+        assert b"broadcast" in lib.pvl_last_error_message()
+        assert lib.pack_rotary_bwd(how, heads(), heads(), None, None, heads(**zero), heads(), None, None, None, 0,
+                                   None) == INVALID
+        assert b"broadcast" in lib.pvl_last_error_message()
+        assert lib.pack_rotary_fwd(how, heads(**zero), None, heads(), heads(), None) == INVALID
+        assert b"k is null" in lib.pvl_last_error_message()
     # a token that no block holds
     assert lib.pack_rotary_fwd(rotary(norm=4, H=600, Hk=0, D=66, R=66, s1=33, s2=33), heads(), None, heads(), None,
                                None) == UNSUPPORTED
