@@ -699,6 +699,9 @@ __global__ void __maxnreg__(!kBwd ? 96 : V == 8 || V == 1 ? 168 : 128) rotary_ke
     float* out = p.part + static_cast<size_t>(blockIdx.y * gridDim.x + blockIdx.x) * p.width;
     float* const table = smem + plan.ring;
     if (kToken) {
+      // teams are not in step behind their last barrier (of one warp or less
+      // they never are): every ring is done with before a table overwrites it
+      if (p.teams > 1) __syncthreads();
       if (on) {
 #pragma unroll
         for (int m = 0; m < kM; ++m) {
