@@ -103,7 +103,9 @@ def _there(device, stream):
 def _launch(device, stream):
     """Context that makes the device current and, with a stream given, that
     stream, so that what is allocated inside belongs to the stream the kernels
-    run on; gives the stream's handle."""
+    run on; gives the stream's handle.  A device that is not CUDA is refused."""
+    if device.type != "cuda":
+        raise ValueError(f"the kernels run on CUDA devices, not on {device}")
     if stream is None:
         index = torch.cuda.current_device()
         if device.index is None or device.index == index:
