@@ -140,8 +140,8 @@ def pack_build_positions(seg_frames, tokens_per_frame: int, L: int, axes: int = 
     frames = np.asarray(seg_frames, dtype=np.int32)
     if frames.ndim != 2:
         raise ValueError("seg_frames must be [B, K]")
-    if axes == 3 and row_width is None:
-        raise ValueError("three axes need row_width")
+    if axes == 3 and (row_width is None or int(row_width) < 1):
+        raise ValueError(f"three axes need a row_width of at least 1, got {row_width}")
     B, K = frames.shape
     device = torch.device(device or "cuda") if out is None else out.device
     with _launch(device, stream) as handle:
@@ -150,7 +150,7 @@ def pack_build_positions(seg_frames, tokens_per_frame: int, L: int, axes: int = 
         else:
             _need_cuda(out, "out", torch.int32, (B, int(L), int(axes)))
         _check(_lib.load().pack_build_positions(frames.tobytes(), B, K, int(tokens_per_frame), int(axes),
-                                                int(row_width or 1), int(L), out.data_ptr(), handle))
+                                                int(row_width) if axes == 3 else 1, int(L), out.data_ptr(), handle))
     return out
 
 

@@ -19,3 +19,12 @@ def test_devices_that_are_not_cuda_are_refused(closed):
                dict(out=torch.zeros(1, 4, 1, dtype=torch.int32)), dict(device="cpu", stream=0)):
         with pytest.raises(ValueError):
             pvl.pack_build_positions([[1]], 4, 4, **kw)
+
+
+def test_three_axes_need_a_row_width(closed):
+    """Refused for the row width, not for the device that comes after it; two axes do without."""
+    for width in (None, 0, -1):
+        with pytest.raises(ValueError, match="row_width"):
+            pvl.pack_build_positions([[1]], 4, 4, axes=3, row_width=width, device="cpu")
+    with pytest.raises(ValueError, match="CUDA"):
+        pvl.pack_build_positions([[1]], 4, 4, axes=2, row_width=0, device="cpu")
