@@ -214,6 +214,9 @@ __device__ __forceinline__ const float* at_row(const float* table, int id, int D
 __device__ __forceinline__ float first(const __nv_bfloat16* row) { return __bfloat162float(row[0]); }
 __device__ __forceinline__ float first(const float* row) { return row[0]; }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+// 1 / deviation; a variance that rounding has left below zero is zero, a NaN
+// of the row's (fmaxf would drop it) makes the row NaN
+__device__ __forceinline__ float inv_deviation(float var, float eps) { return rsqrtf((var < 0.0f ? 0.0f : var) + eps); }
 
 // gate w2 of a modulation row: the factor of the (normalised) block output
 template <bool kSplit>
@@ -481,7 +484,7 @@ __global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
       if (t == 0) prod.issue();
     }
     a.m = p.rms ? 0.0f : sums[0] * inv_d;
-    a.r = rsqrtf(fmaxf(fmaf(-a.m, a.m, sums[1] * inv_d), 0.0f) + p.eps);
+    a.r = inv_deviation(fmaf(-a.m, a.m, sums[1] * inv_d), p.eps);
     b = a;
     if (a.on) {
       ++next;
@@ -723,7 +726,7 @@ __global__ void __maxnreg__(kRegs) residual_post_fwd_kernel(const ResidualParams
           }
         }
         const float hm1 = p.post_rms ? 0.0f : total(s1) * inv_d;
-        q.hr = rsqrtf(fmaxf(fmaf(-hm1, hm1, total(s2) * inv_d), 0.0f) + p.eps);
+        q.hr = inv_deviation(fmaf(-hm1, hm1, total(s2) * inv_d), p.eps);
         q.hm = Kh + hm1;
         // the residual's difference from its first element
         float K = 0.0f;
@@ -758,7 +761,7 @@ __global__ void __maxnreg__(kRegs) residual_post_fwd_kernel(const ResidualParams
           }
         }
         const float m1 = p.rms ? 0.0f : total(s1) * inv_d;
-        q.r = rsqrtf(fmaxf(fmaf(-m1, m1, total(s2) * inv_d), 0.0f) + p.eps);
+        q.r = inv_deviation(fmaf(-m1, m1, total(s2) * inv_d), p.eps);
         q.m = K + m1;
         if (lane == 0) sh.stats[st] = q;
       }
@@ -1041,14 +1044,14 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
           }
         }
         const float m1 = p.rms ? 0.0f : total(s1) * inv_d;
-        q.r = rsqrtf(fmaxf(fmaf(-m1, m1, total(s2) * inv_d), 0.0f) + p.eps);
+        q.r = inv_deviation(fmaf(-m1, m1, total(s2) * inv_d), p.eps);
         q.m = K + m1;
         const float sum_g = total(sg);
         q.c0 = p.rms ? 0.0f : sum_g * inv_d;
         q.c1 = q.r * fmaf(-m1, sum_g, total(sgd)) * inv_d;
         if (kBranch == kPost) {
           const float hm1 = p.post_rms ? 0.0f : total(h1) * inv_d;
-          q.hr = rsqrtf(fmaxf(fmaf(-hm1, hm1, total(h2) * inv_d), 0.0f) + p.eps);
+          q.hr = inv_deviation(fmaf(-hm1, hm1, total(h2) * inv_d), p.eps);
           q.hm = Kh + hm1;
           // dz = t' gate w2: its sum, and that of dz (h - hm)
           const float2 ca = both(-q.r * q.c1), cc = both(-q.r * q.c0), rs = both(q.r), sub = both(-q.m);

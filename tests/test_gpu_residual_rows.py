@@ -1,0 +1,54 @@
+"""Rows of the gated residual whose statistics are special, against the fp64 oracle (GPU)."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from test_gpu_residual import f64, host, make, pvl  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+KINDS = [("layer", None), ("rms", None), ("rms", "rms"), ("layer", "layer"), ("layer", "rms")]
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("stream", ["bf16", "fp32"])
+@pytest.mark.parametrize("norm,post", KINDS)
+@pytest.mark.parametrize("D", [64, 1536, 5120])
+def test_a_value_that_is_not_finite_fills_its_row_alone(pvl, D, norm, post, stream, value):  # noqa: F811
+    """One NaN or infinity in a live row: NaN where the formulas have it, forward and backward; every other row keeps
+    its bits."""
+    t, args, how = make(2, 60, D, "episode", norm, post, stream, D)
+    ids = how["mod_id"]
+    b, n = (int(i) for i in torch.nonzero(ids >= 0)[7])
+    others = torch.ones_like(ids, dtype=torch.bool)
+    others[b, n] = False
+    which = "h" if post else "x"
+
+    def run(t):
+        x_out, y = pvl.adaln_residual_fwd(t["x"], t["h"], *args, **how)
+        return x_out, y
+
+    a = run(t)
+    g = pvl.adaln_residual_bwd(t["dx_out"], t["dy"], a[0], t["h"], *args, **how)
+    bad = {**t, which: t[which].clone()}
+    bad[which][b, n, D // 3] = value
+    c = run(bad)
+    hh, ha = host(how, args)
+    with np.errstate(invalid="ignore"):
+        X, Y, _, _ = oracle.residual_fwd(bad["x"].cpu(), bad["h"].cpu(), *ha, **hh)
+    assert np.isnan(Y[b, n]).any()
+    for got, ref, whole in zip(c, (X, Y), a):
+        assert np.array_equal(np.isnan(f64(got)), np.isnan(ref))
+        assert torch.equal(got[others], whole[others])
+    # backward: the value in x_out, and with a post norm also in h
+    for x_out, h in ((c[0], t["h"]), (a[0], bad["h"])):
+        G = pvl.adaln_residual_bwd(t["dx_out"], t["dy"], x_out, h, *args, **how)
+        with np.errstate(invalid="ignore"):
+            R = oracle.residual_bwd(t["dx_out"].cpu(), t["dy"].cpu(), x_out.cpu(), h.cpu(), *ha, **hh)
+        for name in ("dx", "dh"):
+            got = getattr(G, name)
+            assert np.array_equal(np.isnan(f64(got)), np.isnan(R[name])), name
+            assert torch.equal(got[others], getattr(g, name)[others]), name
+    pvl.device_error()
