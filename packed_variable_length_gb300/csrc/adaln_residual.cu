@@ -32,9 +32,12 @@
 //     and C of the current modulation row and two tables, which a small kernel
 //     has prepared so that the statistics' warps can have them copied into
 //     shared memory.
-//   - A row's statistics are sums shifted by the row's first element K (as in
-//     adaln.cu: one pass, the cancellation bounded because K is a sample of
-//     the row); the RMS norm takes K = 0.
+//   - A row's statistics are one-pass sums shifted by K, the median of the
+//     row's first three elements; the RMS norm takes K = 0.  The variance's rounding
+//     grows with (mean - K)^2 over the variance: a common offset of the row
+//     cancels in it, and one outlier channel, as residual streams have them,
+//     cannot be the median (taken for K itself it would make that ratio D - 1:
+//     1 / deviation off by 2^-10 at 5120 features, 2^-20 without).
 //   - The sums of a CTA's run of equal ids go to slot (CTA + id): with ids
 //     that do not decrease along the rows no two runs share a slot, so the
 //     partial sums need n_cta + S rows and no atomics on values; a small
@@ -211,8 +214,22 @@ __device__ __forceinline__ void table8(const float* row, int v, int nvec, float 
 __device__ __forceinline__ const float* at_row(const float* table, int id, int D) {
   return table ? table + static_cast<size_t>(id) * D : nullptr;
 }
-__device__ __forceinline__ float first(const __nv_bfloat16* row) { return __bfloat162float(row[0]); }
-__device__ __forceinline__ float first(const float* row) { return row[0]; }
+// The elements that a row's shift K is taken from, its first three (one load),
+// and their median.
+struct Sample {
+  float v[3];
+};
+__device__ __forceinline__ Sample sample(const __nv_bfloat16* row) {
+  const uint2 u = *reinterpret_cast<const uint2*>(row);
+  return Sample{{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16)}};
+}
+__device__ __forceinline__ Sample sample(const float* row) {
+  const float4 u = *reinterpret_cast<const float4*>(row);
+  return Sample{{u.x, u.y, u.z}};
+}
+__device__ __forceinline__ float median(const Sample& s) {
+  return fmaxf(fminf(s.v[0], s.v[1]), fminf(fmaxf(s.v[0], s.v[1]), s.v[2]));
+}
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 // 1 / deviation; a variance that rounding has left below zero is zero, a NaN
 // of the row's (fmaxf would drop it) makes the row NaN
@@ -350,8 +367,8 @@ struct Shared {
   int abort;
 };
 
-// A row between its two phases: which, its stage, its id, and the mean (past
-// its K) and 1 / deviation of x_out.
+// A row between its two phases: which, its stage, its id, and the mean and
+// 1 / deviation of x_out.
 struct Flight {
   bool on;
   int row, st, id;
@@ -387,7 +404,7 @@ __global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
     for (int s = 0; s < p.stages; ++s) prod.issue();
 
   float2 gt[kV][4], fa[kV][4], ad[kV][4];  // gate, w (1 + scale), b (1 + scale) + shift of row cur
-  float g0 = 0.0f;                         // gate of feature 0
+  Sample g0{};                             // gate of the features that K is taken from
   int cur = -1;
   // the residual's 8 features of group v, from the stage
   auto residual8 = [&](const uint8_t* src, int i, int v, float2 (&f)[4]) {
@@ -399,12 +416,16 @@ __global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
       for (int e = 0; e < 4; ++e) f[e] = ffma2(q[e], gt[i][e], fmul2(f[e], both(p.alpha)));
     }
   };
-  // the row's first element: what its sums are shifted by
+  // what the row's sums are shifted by
   auto shift_of = [&](const uint8_t* src) {
     if (p.rms) return 0.0f;
-    const float x0 = first(reinterpret_cast<const TX*>(src));
-    if (kBranch == kNoBranch) return x0;
-    return fmaf(first(reinterpret_cast<const __nv_bfloat16*>(src + lay.h())), g0, p.alpha * x0);
+    Sample x = sample(reinterpret_cast<const TX*>(src));
+    if (kBranch != kNoBranch) {
+      const Sample h = sample(reinterpret_cast<const __nv_bfloat16*>(src + lay.h()));
+#pragma unroll
+      for (int j = 0; j < 3; ++j) x.v[j] = fmaf(h.v[j], g0.v[j], p.alpha * x.v[j]);
+    }
+    return median(x);
   };
 
   Flight b{};
@@ -414,7 +435,6 @@ __global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
     if (b.on) {  // y
       const uint8_t* src = smem + b.st * lay.bytes();
       __nv_bfloat16* out = p.y + static_cast<size_t>(b.row) * D;
-      const float sub = b.id < 0 ? 0.0f : shift_of(src) + b.m;
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
         const int v = t + i * nthr;
@@ -426,7 +446,7 @@ __global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
           } else {
             residual8(src, i, v, f);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = ffma2(fmul2(fadd2(f[e], both(-sub)), both(b.r)), fa[i][e], ad[i][e]);
+            for (int e = 0; e < 4; ++e) f[e] = ffma2(fmul2(fadd2(f[e], both(-b.m)), both(b.r)), fa[i][e], ad[i][e]);
           }
           store8<kSplit>(out, v, nvec, f);
         }
@@ -434,6 +454,7 @@ __global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
     }
     float2 s1 = both(0.0f), s2 = both(0.0f);
     Flight a{};
+    float K = 0.0f;
     bool ok = true;
     if (next < r_end) {
       ok = test_wait(&sh.full[st], ph, ctl, kSiteResRowFull);
@@ -446,11 +467,11 @@ __global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
           const int v = t + i * nthr;
           if (v < nvec) load_tables<kSplit>(p, id, v, nvec, gt[i], fa[i], ad[i]);
         }
-        g0 = p.gate ? __ldg(p.gate + static_cast<size_t>(id) * D) : 1.0f;
+        if (kBranch != kNoBranch) g0 = p.gate ? sample(p.gate + static_cast<size_t>(id) * D) : Sample{{1.0f, 1.0f, 1.0f}};
       }
       const uint8_t* src = smem + st * lay.bytes();
       TX* out = static_cast<TX*>(p.x_out) + static_cast<size_t>(next) * D;
-      const float K = id < 0 ? 0.0f : shift_of(src);
+      if (id >= 0) K = shift_of(src);
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
         const int v = t + i * nthr;
@@ -483,8 +504,9 @@ __global__ void __maxnreg__(kRegs) residual_fwd_kernel(const ResidualParams p) {
       ++freed;
       if (t == 0) prod.issue();
     }
-    a.m = p.rms ? 0.0f : sums[0] * inv_d;
-    a.r = inv_deviation(fmaf(-a.m, a.m, sums[1] * inv_d), p.eps);
+    const float m1 = p.rms ? 0.0f : sums[0] * inv_d;
+    a.m = K + m1;
+    a.r = inv_deviation(fmaf(-m1, m1, sums[1] * inv_d), p.eps);
     b = a;
     if (a.on) {
       ++next;
@@ -712,7 +734,7 @@ __global__ void __maxnreg__(kRegs) residual_post_fwd_kernel(const ResidualParams
         if (p.tables && !warp_wait<false>(&sh.table[slot & 255], slot >> 8, ctl, kSiteResTable)) break;
         const float* gate = reinterpret_cast<const float*>(slots + (slot & 255) * table_bytes);
         RowStats q{};
-        const float Kh = p.post_rms ? 0.0f : first(hs);
+        const float Kh = p.post_rms ? 0.0f : median(sample(hs));
         float2 s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll 3
         for (int v = lane; v < nvec; v += 32) {
@@ -728,11 +750,15 @@ __global__ void __maxnreg__(kRegs) residual_post_fwd_kernel(const ResidualParams
         const float hm1 = p.post_rms ? 0.0f : total(s1) * inv_d;
         q.hr = inv_deviation(fmaf(-hm1, hm1, total(s2) * inv_d), p.eps);
         q.hm = Kh + hm1;
-        // the residual's difference from its first element
+        // the residual's difference from its K
         float K = 0.0f;
         if (!p.rms) {
-          const float g0 = (p.tables ? gate[0] : 1.0f) * (p.w2 ? w2[0] : 1.0f);
-          K = fmaf((first(hs) - q.hm) * q.hr, g0, p.alpha * first(xs));
+          Sample x = sample(xs);
+          const Sample h = sample(hs), one{{1.0f, 1.0f, 1.0f}};
+          const Sample g = p.tables ? sample(gate) : one, w = p.w2 ? sample(w2) : one;
+#pragma unroll
+          for (int j = 0; j < 3; ++j) x.v[j] = fmaf((h.v[j] - q.hm) * q.hr, g.v[j] * w.v[j], p.alpha * x.v[j]);
+          K = median(x);
         }
         const float2 hr = both(q.hr), hsub = both(-q.hm), al = both(p.alpha);
         s1 = s2 = both(0.0f);
@@ -1007,8 +1033,8 @@ __global__ void __maxnreg__(kRegs) residual_bwd_kernel(const ResidualParams p) {
         // post norm also those of the branch
         RowStats q{};
         q.hr = 1.0f;
-        const float K = p.rms ? 0.0f : first(xs);
-        const float Kh = kBranch == kPost && !p.post_rms ? first(hs) : 0.0f;
+        const float K = p.rms ? 0.0f : median(sample(xs));
+        const float Kh = kBranch == kPost && !p.post_rms ? median(sample(hs)) : 0.0f;
         const int slot = sh.slot[st];
         if (p.tables && !warp_wait<kBranch != kPost>(&sh.table[slot & 255], slot >> 8, ctl, kSiteResTable)) break;
         const float* fac = reinterpret_cast<const float*>(smem + (slot & 255) * table_bytes);

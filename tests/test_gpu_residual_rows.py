@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import oracle
-from test_gpu_residual import f64, host, make, pvl  # noqa: F401
+from test_gpu_residual import check, f64, host, make, pvl  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +52,22 @@ def test_a_value_that_is_not_finite_fills_its_row_alone(pvl, D, norm, post, stre
             assert np.array_equal(np.isnan(f64(got)), np.isnan(R[name])), name
             assert torch.equal(got[others], getattr(g, name)[others]), name
     pvl.device_error()
+
+
+@pytest.mark.parametrize("stream", ["bf16", "fp32"])
+@pytest.mark.parametrize("norm,post", [("layer", None), ("layer", "layer"), ("rms", "layer")])
+@pytest.mark.parametrize("D", [1536, 5120, 8192])
+@pytest.mark.parametrize("place", ["first", "third", "last"])
+def test_one_outlier_channel_on_a_common_offset(pvl, D, norm, post, stream, place):  # noqa: F811
+    """Rows with one large channel, as residual streams have them, and with an offset of all: the statistics are as
+    near as for other rows.  The tolerances are test_gpu_residual's; they also hold for chains of 128 + 6 additions
+    (the longest here, 2^-17 of the sum of magnitudes): the sums are shifted by an ordinary element of the row, so
+    (mean - K)^2 is below 15 variances, the variance off by 2^-13, the root by 2^-14, xh by 2^-13 (1 + |xh|)."""
+    at = {"first": 0, "third": 2, "last": D - 1}[place]
+    t, args, how = make(2, 40, D, "episode", norm, post, stream, D + at)
+    for name, big, offset in (("x", 1000.0, 20.0), ("h", -700.0, -9.0)):
+        v = t[name].float() + offset
+        v[..., at] = big
+        t[name] = v.to(t[name].dtype)
+    check(pvl, t, args, how)
+    check(pvl, {**t, "dx_out": None}, args, how)
