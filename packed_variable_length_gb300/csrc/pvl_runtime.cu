@@ -104,6 +104,13 @@ std::unordered_map<ShapeKey, size_t, ShapeHash> g_allowed;  // threads = smem = 
 int g_smem_sm[kMaxDevices] = {};
 }  // namespace
 
+// A query that failed is reported by its value; its error must not be left for
+// the check of the next launch.
+static int no_value() {
+  cudaGetLastError();
+  return 0;
+}
+
 int blocks_per_sm(const void* fn, int threads, size_t smem) try {
   const int dev = current_device();
   if (dev < 0) return 0;
@@ -114,11 +121,11 @@ int blocks_per_sm(const void* fn, int threads, size_t smem) try {
   size_t& allowed = g_allowed[ShapeKey{fn, 0, dev, 0}];
   if (smem > 32 * 1024 && smem > allowed) {  // 48 KB together with the static part need no leave
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-      return 0;
+      return no_value();
     allowed = smem;
   }
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem) != cudaSuccess) return 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem) != cudaSuccess) return no_value();
   if (n > 0) g_blocks.emplace(key, n);
   return n;
 } catch (...) {  // no memory for the table: no exception leaves a C entry point
@@ -131,7 +138,8 @@ int smem_per_sm() {
   std::lock_guard<std::mutex> lock(g_mu);
   if (!g_smem_sm[dev]) {
     int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev) != cudaSuccess) return 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev) != cudaSuccess)
+      return no_value();
     g_smem_sm[dev] = n;
   }
   return g_smem_sm[dev];

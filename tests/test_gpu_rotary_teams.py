@@ -102,3 +102,20 @@ def test_one_head_a_thread_and_several(pvl, norm):
     """The same heads on both sides of the token count from which a thread takes several of them."""
     for L in (303, 304, 305, 309, 5001):
         check(pvl, L, 5, 3, 128, 128, "half", norm, seed=L)
+
+
+def test_a_refused_call_leaves_no_error_behind(pvl):
+    """A backward whose token does not fit a block is refused, and the calls after it succeed."""
+    L, H, Hk, D = 9, 128, 8, 128
+    q, k = (torch.randn(1, L, n, D, device="cuda").to(torch.bfloat16) for n in (H, Hk))
+    pos = torch.arange(L, dtype=torch.int32, device="cuda")[None]
+    plan = pvl.rotary_plan(D)
+    with pytest.raises(pvl.PvlError):
+        pvl.pack_rotary_bwd(q, k, pos, plan, "token", q, k)
+    got = pvl.pack_build_positions([[3]], 3, L)
+    assert got.flatten().tolist() == list(range(L))
+    pvl.pack_rotary_fwd(q, k, pos, plan, "token")       # the forward does fit
+    x = torch.randn(1, 4, 64, device="cuda").to(torch.bfloat16)
+    pvl.adaln_fwd(x, torch.zeros(1, 64, device="cuda"), torch.zeros(1, 64, device="cuda"))
+    pvl.adaln_residual_fwd(x)
+    pvl.device_error()
