@@ -46,6 +46,7 @@ namespace {
 
 constexpr int kMaxBlock = 384;  // 168 registers a thread, the most that a kernel here takes
 constexpr int kMaxD = 256;
+constexpr size_t kMaxSmem = 227 * 1024;  // of a block
 constexpr int kMaxPartials = 1216;  // rows of partial weight gradients at most
 constexpr float kRadians = 1.4629180792671596e-9f;  // 2 pi / 2^32
 
@@ -775,8 +776,10 @@ int round32(int n) { return (n + 31) / 32 * 32; }
 
 // The team of a token for vectors V wide and kM heads a thread: a power of
 // two below 32 threads, or whole warps.  False where one pass over a token's
-// heads does not fit a block and the norm per token needs it.
-bool team_of(int V, int kM, int Ht, int D, int norm, Shape* s) {
+// heads does not fit a block and the norm per token needs it: by its threads,
+// or backward, with 384 of them on 8-wide vectors (from 16,800 features on),
+// by its shared memory.
+bool team_of(int V, int kM, int Ht, int D, int norm, bool bwd, Shape* s) {
   s->V = V;
   s->kM = kM;
   s->units = D / (2 * V);
@@ -802,7 +805,7 @@ bool team_of(int V, int kM, int Ht, int D, int norm, Shape* s) {
   const int threads = norm == PVL_NORM_NONE && V == 8 && kM > 1 && s->team >= 32 ? 256 : s->team < 32 ? 64 : 128;
   s->teams = s->team >= threads ? 1 : threads / s->team;
   s->threads = s->team * s->teams;
-  return true;
+  return sizeof(float) * smem_plan(V, kM, norm, bwd, Ht, D, s->units, s->hpi, s->team, s->teams, s->threads).total <= kMaxSmem;
 }
 
 struct Kernel {
@@ -896,14 +899,14 @@ int widest(const pvl_rotary* a, const pvl_heads* const* views, int n) {
 bool shape_of(const pvl_rotary* a, int V, bool bwd, Shape* s) {
   const int Ht = a->H + a->Hk;
   const bool whole = a->norm == PVL_NORM_TOKEN;
-  if (V != 8) return team_of(V, V == 4 ? 4 : 8, Ht, a->D, a->norm, s) || team_of(V, 16, Ht, a->D, a->norm, s);
+  if (V != 8) return team_of(V, V == 4 ? 4 : 8, Ht, a->D, a->norm, bwd, s) || team_of(V, 16, Ht, a->D, a->norm, bwd, s);
   const long long tokens = static_cast<long long>(a->B) * a->L;
-  if (tokens <= 2 * 152 && team_of(8, 1, Ht, a->D, a->norm, s)) return true;
-  if (!whole) return team_of(8, bwd ? 2 : 3, Ht, a->D, a->norm, s);
+  if (tokens <= 2 * 152 && team_of(8, 1, Ht, a->D, a->norm, bwd, s)) return true;
+  if (!whole) return team_of(8, bwd ? 2 : 3, Ht, a->D, a->norm, bwd, s);
   // six while a token stays within two warps, else more warps count for more
   // (10,240 features a token: 215 us at six, 178 at three; 6,144: 165, 177)
-  if (!bwd && Ht * a->D <= 6144 && team_of(8, 6, Ht, a->D, a->norm, s)) return true;
-  return team_of(8, 3, Ht, a->D, a->norm, s);
+  if (!bwd && Ht * a->D <= 6144 && team_of(8, 6, Ht, a->D, a->norm, bwd, s)) return true;
+  return team_of(8, 3, Ht, a->D, a->norm, bwd, s);
 }
 
 pvl_status check_views(const char* who, const pvl_rotary* a, const pvl_heads* v, int which, const char* name,
