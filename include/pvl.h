@@ -356,10 +356,14 @@ PVL_API pvl_status pack_build_positions(const int32_t* seg_frames, int B, int K,
  *   give the same bits).  ws: pack_rotary_bwd_ws_bytes of the same
  *   description (0 without weights), 16-byte aligned, one call at a time.
  * Limits (UNSUPPORTED): D and R even, D at most 256, H + Hk at most
- *   PVL_MAX_ROTARY_HEADS, and a token whose (H + Hk) D features the norm per
- *   token cannot hold in a block (12,288 always fit); B L and the strides
- *   between heads below 2^30.  Tensors whose D, R,
- *   strides and addresses allow 16-byte (else 8-byte) vectors run fastest.
+ *   PVL_MAX_ROTARY_HEADS; B L and the strides between heads below 2^30; and a
+ *   token whose heads the norm per token cannot hold in a block.  With V the
+ *   widest of 8, 4, 2 and 1 features for which 2 V divides D (half layout: and
+ *   R) and V every stride and the offset of every address, and u = D / (2 V),
+ *   it holds n floor(384 / u) heads, n = 3, 4, 8, 16 for V = 8, 4, 2, 1
+ *   (backward at V = 8: 352 for 384).  So H + Hk heads of up to 9,500 features
+ *   in all always fit; at V = 2, 4 and 8 up to 10,700, 11,700 and 16,700.  The
+ *   wider the vectors, the faster.
  * Errors: INVALID_ARG for null pointers,
  *   sizes < 1, inconsistent sections, unknown layout or norm, a broadcast
  *   output, a short workspace; CUDA for launch failures.

@@ -805,7 +805,8 @@ bool team_of(int V, int kM, int Ht, int D, int norm, bool bwd, Shape* s) {
   const int threads = norm == PVL_NORM_NONE && V == 8 && kM > 1 && s->team >= 32 ? 256 : s->team < 32 ? 64 : 128;
   s->teams = s->team >= threads ? 1 : threads / s->team;
   s->threads = s->team * s->teams;
-  return sizeof(float) * smem_plan(V, kM, norm, bwd, Ht, D, s->units, s->hpi, s->team, s->teams, s->threads).total <= kMaxSmem;
+  const SmemPlan plan = smem_plan(V, kM, norm, bwd, Ht, D, s->units, s->hpi, s->team, s->teams, s->threads);
+  return sizeof(float) * plan.total <= kMaxSmem;
 }
 
 struct Kernel {
@@ -899,7 +900,8 @@ int widest(const pvl_rotary* a, const pvl_heads* const* views, int n) {
 bool shape_of(const pvl_rotary* a, int V, bool bwd, Shape* s) {
   const int Ht = a->H + a->Hk;
   const bool whole = a->norm == PVL_NORM_TOKEN;
-  if (V != 8) return team_of(V, V == 4 ? 4 : 8, Ht, a->D, a->norm, bwd, s) || team_of(V, 16, Ht, a->D, a->norm, bwd, s);
+  if (V != 8 && team_of(V, V == 4 ? 4 : 8, Ht, a->D, a->norm, bwd, s)) return true;
+  if (V != 8) return V == 1 && team_of(V, 16, Ht, a->D, a->norm, bwd, s);
   const long long tokens = static_cast<long long>(a->B) * a->L;
   if (tokens <= 2 * 152 && team_of(8, 1, Ht, a->D, a->norm, bwd, s)) return true;
   if (!whole) return team_of(8, bwd ? 2 : 3, Ht, a->D, a->norm, bwd, s);

@@ -44,7 +44,8 @@ def near(name, got, ref, mag, step=STEP):
     got = got.double()
     assert bool(got.isfinite().all()), name
     err = (got - ref).abs() - step * ref.abs() - mag
-    assert float(err.max()) <= 0, f"{name}: {int((err > 0).sum())} values out of tolerance, worst by {float(err.max()):.3e}"
+    worst = float(err.max())
+    assert worst <= 0, f"{name}: {int((err > 0).sum())} values out of tolerance, worst by {worst:.3e}"
 
 
 def check(pvl, L, H, Hk, D, R, layout, norm, seed):
@@ -74,7 +75,8 @@ def check(pvl, L, H, Hk, D, R, layout, norm, seed):
         up = turned(dout.double(), -angle, R, layout)
         g0 = pair_magnitude(up, R, layout)
         sums = (0, 1) if wide else (0, 1, 2)
-        near("dw" + name, dw, (up * xh).sum(sums).flatten(), 2.0 ** -13 * (g0 * xh.abs()).sum(sums).flatten(), 2.0 ** -24)
+        near("dw" + name, dw, (up * xh).sum(sums).flatten(), 2.0 ** -13 * (g0 * xh.abs()).sum(sums).flatten(),
+             step=2.0 ** -24)
         ref = r * (up * w - xh * (up * w * xh).mean(over, keepdim=True))
         g0 = g0 * w.abs()
         near("d" + name, dx, ref, 2.0 ** -14 * r * (g0 + xh.abs() * (g0 * xh.abs()).mean(over, keepdim=True)))
@@ -119,3 +121,11 @@ def test_a_refused_call_leaves_no_error_behind(pvl):
     pvl.adaln_fwd(x, torch.zeros(1, 64, device="cuda"), torch.zeros(1, 64, device="cuda"))
     pvl.adaln_residual_fwd(x)
     pvl.device_error()
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("H,Hk,D", [(100, 32, 128), (44, 8, 232), (40, 8, 220), (40, 8, 194), (44, 4, 254)])
+def test_the_widest_tokens(pvl, H, Hk, D, layout):
+    """As many heads as the norm over the token holds, backward too, at every width of vectors."""
+    for L in (7, 700):
+        check(pvl, L, H, Hk, D, D, layout, "token", seed=D)
