@@ -469,10 +469,11 @@ def rotary_plan(rotary_dim: int, base: float = 10000.0, layout: str = "half", se
         raise ValueError(f"sections must be 1 to 3 counts that sum to {R // 2}, got {sections}")
     if scaling not in (None, "none", "linear", "ntk", "parts"):
         raise ValueError(f"unknown scaling {scaling!r}")
+    base, factor, slow, fast = (float(v) for v in (base, factor, slow, fast))
     if not (math.isfinite(base) and base > 0.0) or not (math.isfinite(factor) and factor > 0.0):
         raise ValueError("base and factor must be positive and finite")
-    if scaling == "parts" and (length is None or length < 1 or not fast > slow >= 0.0):
-        raise ValueError("scaling 'parts' needs the trained length and fast > slow >= 0")
+    if scaling == "parts" and (length is None or not 1 <= length < math.inf or not math.inf > fast > slow >= 0.0):
+        raise ValueError("scaling 'parts' needs the trained length and fast > slow >= 0, all finite")
     turns = []
     with localcontext() as ctx:
         ctx.prec = 50
@@ -488,7 +489,7 @@ def rotary_plan(rotary_dim: int, base: float = 10000.0, layout: str = "half", se
                 if scaling == "linear":
                     t /= s
                 elif scaling == "parts":
-                    keep = (length * t - Decimal(slow)) / (Decimal(fast) - Decimal(slow))
+                    keep = (Decimal(float(length)) * t - Decimal(slow)) / (Decimal(fast) - Decimal(slow))
                     keep = min(max(keep, Decimal(0)), Decimal(1))
                     t = t * keep + t / s * (1 - keep)
                 whole = int((t * (1 << 64)).to_integral_value()) % (1 << 64)

@@ -1,5 +1,6 @@
 """Arguments of the binding's block operators that are refused before the library or a device is reached (CPU only)."""
 
+import numpy as np
 import pytest
 import torch
 
@@ -28,3 +29,18 @@ def test_three_axes_need_a_row_width(closed):
             pvl.pack_build_positions([[1]], 4, 4, axes=3, row_width=width, device="cpu")
     with pytest.raises(ValueError, match="CUDA"):
         pvl.pack_build_positions([[1]], 4, 4, axes=2, row_width=0, device="cpu")
+
+
+@pytest.mark.parametrize("kind", [int, float, np.int64, np.float32, np.float64])
+def test_plan_arguments_of_any_kind_of_number(kind):
+    ref = pvl.rotary_plan(64, base=10000.0, scaling="parts", factor=4.0, length=4096, slow=1.0, fast=32.0, device="cpu")
+    got = pvl.rotary_plan(64, base=kind(10000), scaling="parts", factor=kind(4), length=kind(4096), slow=kind(1),
+                          fast=kind(32), device="cpu")
+    assert torch.equal(got.turns, ref.turns) and got.gain == ref.gain
+
+
+def test_plan_numbers_that_are_not_finite():
+    for kw in (dict(length=float("inf")), dict(length=float("nan")), dict(length=0.5), dict(fast=float("inf")),
+               dict(slow=float("nan")), dict(factor=float("nan")), dict(base=float("nan"))):
+        with pytest.raises(ValueError):
+            pvl.rotary_plan(64, **{**dict(scaling="parts", factor=4.0, length=4096, device="cpu"), **kw})
