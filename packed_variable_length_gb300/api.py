@@ -545,8 +545,9 @@ def _rotary(like_q, like_k, positions, plan: RotaryPlan, norm, q_weight, k_weigh
         _need(w, name, torch.float32, w.shape, device)
         if w.numel() != (n * D if norm == "token" else D):
             raise ValueError(f"{name} must hold {n * D if norm == 'token' else D} values, got {w.numel()}")
-    if plan.turns.device != device:
-        raise ValueError(f"the plan is on {plan.turns.device}, not on {device}")
+    _need(plan.turns, "plan.turns", torch.int64, (plan.rotary_dim // 2,), device)
+    if plan.layout not in ("half", "interleaved"):
+        raise ValueError(f"the plan's layout must be 'half' or 'interleaved', got {plan.layout!r}")
     s = plan.sections
     s1 = s[0]
     s2 = s1 + (s[1] if axes > 1 else 0)

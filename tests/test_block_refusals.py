@@ -1,5 +1,7 @@
 """Arguments of the binding's block operators that are refused before the library or a device is reached (CPU only)."""
 
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
@@ -44,3 +46,20 @@ def test_plan_numbers_that_are_not_finite():
                dict(slow=float("nan")), dict(factor=float("nan")), dict(base=float("nan"))):
         with pytest.raises(ValueError):
             pvl.rotary_plan(64, **{**dict(scaling="parts", factor=4.0, length=4096, device="cpu"), **kw})
+
+
+def test_plans_that_do_not_hold_what_they_say(closed):
+    """A plan made by hand whose table is shorter than its rotary_dim, of another type or not contiguous, or whose
+    layout is unknown: the kernel would read past it or take another layout."""
+    q, pos = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16), torch.zeros(1, 4, dtype=torch.int32)
+    plan = pvl.rotary_plan(64, device="cpu")
+    for change in (dict(turns=plan.turns[:16]), dict(turns=plan.turns.int()), dict(turns=plan.turns.double()),
+                   dict(turns=plan.turns.repeat_interleave(2)[::2]), dict(turns=plan.turns[None]), dict(rotary_dim=128)):
+        bad = dataclasses.replace(plan, **change)
+        for call in (pvl.pack_rotary_fwd, pvl.pack_rotary_bwd):
+            with pytest.raises(ValueError, match="turns"):
+                call(q, q, pos, bad)
+    with pytest.raises(ValueError, match="layout"):
+        pvl.pack_rotary_fwd(q, q, pos, dataclasses.replace(plan, layout="other"))
+    with pytest.raises(ValueError, match="CUDA"):
+        pvl.pack_rotary_fwd(q, q, pos, plan)
