@@ -46,6 +46,7 @@ namespace {
 
 constexpr int kMaxBlock = 384;  // 168 registers a thread, the most that a kernel here takes
 constexpr int kMaxD = 256;
+constexpr int kPart = 2;        // beside pvl_rotary_layout: interleaved, R < D
 constexpr size_t kMaxSmem = 227 * 1024;  // of a block
 constexpr int kMaxPartials = 1216;  // rows of partial weight gradients at most
 constexpr float kRadians = 1.4629180792671596e-9f;  // 2 pi / 2^32
@@ -138,6 +139,14 @@ __device__ __forceinline__ F side_b(const float4& t) {
 }
 __device__ __forceinline__ float2 minus(float2 v) { return make_float2(-v.x, -v.y); }
 __device__ __forceinline__ float minus(float v) { return -v; }
+// v into `to`, but where a bit of `not_these` is set
+__device__ __forceinline__ void take_unless(uint32_t not_these, float2 v, float2& to) {
+  if (!(not_these & 1)) to.x = v.x;
+  if (!(not_these & 2)) to.y = v.y;
+}
+__device__ __forceinline__ void take_unless(uint32_t not_these, float v, float& to) {
+  if (!(not_these & 1)) to = v;
+}
 
 template <int V, bool kHalf>
 __device__ __forceinline__ void unpack(const typename Vec<V>::T& u0, const typename Vec<V>::T& u1, Unit<V>& z) {
@@ -192,9 +201,8 @@ __device__ __forceinline__ int feature(int k, int e0, int e1) {
 }
 
 // Offsets of the two vectors of unit u.  Interleaved pairs lie inside a
-// vector, so all units are the same: R may end anywhere (the pairs past it
-// get angle 0 and no gain).  In the half layout the units past the rotated
-// part are their own.
+// vector, so all units are the same: R may end anywhere (pairs_past).  In the
+// half layout the units past the rotated part are their own.
 template <int V, bool kHalf>
 __device__ __forceinline__ void vectors_of(const RotaryParams& p, int u, int* e0, int* e1) {
   if (!kHalf) {
@@ -207,6 +215,22 @@ __device__ __forceinline__ void vectors_of(const RotaryParams& p, int u, int* e0
     *e0 = p.R + (u - p.turned) * V;
     *e1 = *e0 + (p.D - p.R) / 2;
   }
+}
+
+// The pairs of an interleaved unit that lie past R, one bit each.  They are not
+// turned by an angle of 0, which would make a NaN of an infinity beside them.
+// Kernels of their own (kPart) have the test: in those of a whole head it cost
+// 3 % (64k pack, norm over the token: forward 138 us, 136 without, backward 233,
+// 226).
+template <int V>
+__device__ __forceinline__ uint32_t pairs_past(const RotaryParams& p, int u) {
+  uint32_t past = 0;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const int pair = V == 1 ? u : e < V / 2 ? u * (V / 2) + e : p.D / 4 + u * (V / 2) + e - V / 2;
+    past |= (pair >= p.R / 2 ? 1u : 0u) << e;
+  }
+  return past;
 }
 
 // Head (of those a team takes at once) and unit of thread t of a team; false
@@ -286,10 +310,11 @@ __host__ __device__ inline SmemPlan smem_plan(int V, int kM, int norm, bool bwd,
 // 96 registers: left to itself the compiler stays at 64 for the sake of warps
 // that the shared memory leaves no room for (norm per head, 64k pack: 154 us
 // at 64, 132 at 96).
-template <int V, int kM, int kNorm, bool kBwd, bool kHalf>
+template <int V, int kM, int kNorm, bool kBwd, int kLayout>
 __global__ void __maxnreg__(!kBwd ? 96 : V == 8 || V == 1 ? 168 : 128) rotary_kernel(const __grid_constant__ RotaryParams p) {
   using T = typename Vec<V>::T;
   using F = typename Unit<V>::F;
+  constexpr bool kHalf = kLayout == PVL_ROTARY_HALF;
   constexpr int kP = Unit<V>::kP, kColumn = kMaxD / (2 * V);
   constexpr bool kHead = kNorm == PVL_NORM_HEAD, kToken = kNorm == PVL_NORM_TOKEN, kAny = kHead || kToken;
   constexpr int kSums = kBwd ? 2 : 1;  // sum x^2, and backward sum g w x
@@ -302,6 +327,7 @@ __global__ void __maxnreg__(!kBwd ? 96 : V == 8 || V == 1 ? 168 : 128) rotary_ke
   const bool turned = u < p.turned;
   int e0, e1;  // features of the unit's two vectors
   vectors_of<V, kHalf>(p, u, &e0, &e1);
+  const uint32_t past = kLayout == kPart ? pairs_past<V>(p, u) : 0u;
   const int group = p.team < 32 ? p.team : 32, in_group = tid & (group - 1);
   float4* const angles = reinterpret_cast<float4*>(smem) + tid / group * kP * kColumn;  // [kP][kColumn]
   float4* const weights = reinterpret_cast<float4*>(smem + plan.weights);
@@ -487,12 +513,23 @@ __global__ void __maxnreg__(!kBwd ? 96 : V == 8 || V == 1 ? 168 : 128) rotary_ke
           positions(l + step < p.L);  // the next token's
         }
         auto rotate = [&](Unit<V>& z) {
+          auto turn_pair = [&](int q, F& a, F& b) {
+            const float4 t = angles[q * kColumn + u];
+            const F c = side_a<F>(t), s = side_b<F>(t), a0 = a;
+            a = ffma2(a0, c, fmul2(b, minus(s)));
+            b = ffma2(a0, s, fmul2(b, c));
+          };
 #pragma unroll
           for (int q = 0; q < kP; ++q) {
-            const float4 t = angles[q * kColumn + u];
-            const F c = side_a<F>(t), s = side_b<F>(t), a = z.a[q];
-            z.a[q] = ffma2(a, c, fmul2(z.b[q], minus(s)));
-            z.b[q] = ffma2(a, s, fmul2(z.b[q], c));
+            F a = z.a[q], b = z.b[q];
+            turn_pair(q, a, b);
+            if (kLayout == kPart) {
+              take_unless(past >> 2 * q, a, z.a[q]);
+              take_unless(past >> 2 * q, b, z.b[q]);
+            } else {
+              z.a[q] = a;
+              z.b[q] = b;
+            }
           }
         };
         // the norms' sums; backward the gradient is turned back on the way
@@ -809,23 +846,18 @@ bool team_of(int V, int kM, int Ht, int D, int norm, bool bwd, Shape* s) {
   return sizeof(float) * plan.total <= kMaxSmem;
 }
 
-struct Kernel {
-  const void* fn;
-  int V, kM, norm;
-  bool bwd, half;
-};
-
 template <int V, int kM, int kNorm, bool kBwd>
-constexpr Kernel kernel_of(bool half) {
-  return {half ? reinterpret_cast<const void*>(&rotary_kernel<V, kM, kNorm, kBwd, true>)
-               : reinterpret_cast<const void*>(&rotary_kernel<V, kM, kNorm, kBwd, false>),
-          V, kM, kNorm, kBwd, half};
+const void* kernel_of(int layout) {
+  if (layout == PVL_ROTARY_HALF)
+    return reinterpret_cast<const void*>(&rotary_kernel<V, kM, kNorm, kBwd, PVL_ROTARY_HALF>);
+  if (layout == kPart) return reinterpret_cast<const void*>(&rotary_kernel<V, kM, kNorm, kBwd, kPart>);
+  return reinterpret_cast<const void*>(&rotary_kernel<V, kM, kNorm, kBwd, PVL_ROTARY_INTERLEAVED>);
 }
 
 // The kernels that exist (shape_of picks among the same).
-const void* find_kernel(const Shape& s, int norm, bool bwd, bool half) {
+const void* find_kernel(const Shape& s, int norm, bool bwd, int layout) {
 #define PVL_ROTARY_KERNEL(VV, MM, NN, BB) \
-  if (s.V == VV && s.kM == MM && norm == NN && bwd == BB) return kernel_of<VV, MM, NN, BB>(half).fn
+  if (s.V == VV && s.kM == MM && norm == NN && bwd == BB) return kernel_of<VV, MM, NN, BB>(layout)
   PVL_ROTARY_KERNEL(8, 1, PVL_NORM_NONE, false);
   PVL_ROTARY_KERNEL(8, 3, PVL_NORM_NONE, false);
   PVL_ROTARY_KERNEL(4, 4, PVL_NORM_NONE, false);
@@ -858,9 +890,9 @@ const void* find_kernel(const Shape& s, int norm, bool bwd, bool half) {
   return nullptr;
 }
 
-pvl_status launch(const RotaryParams& p, const Shape& sh, int norm, bool bwd, bool half, int grid_limit, int* grid_out,
+pvl_status launch(const RotaryParams& p, const Shape& sh, int norm, bool bwd, int layout, int grid_limit, int* grid_out,
                   cudaStream_t s, const char* who) {
-  const void* fn = find_kernel(sh, norm, bwd, half);
+  const void* fn = find_kernel(sh, norm, bwd, layout == PVL_ROTARY_INTERLEAVED && p.R < p.D ? kPart : layout);
   if (!fn) return fail(PVL_ERR_UNSUPPORTED, "%s: no kernel for this shape", who);
   const size_t smem =
       sizeof(float) * smem_plan(sh.V, sh.kM, norm, bwd, p.Ht, p.D, sh.units, sh.hpi, sh.team, sh.teams, sh.threads).total;
@@ -1028,7 +1060,7 @@ extern "C" pvl_status pack_rotary_fwd(const pvl_rotary* a, const pvl_heads* q, c
     return fail(PVL_ERR_UNSUPPORTED, "%s: a head stride of 2^30 elements or more", who);
   flatten(p, false);
   int grid = 0;
-  return launch(p, s, a->norm, false, a->layout == PVL_ROTARY_HALF, 1 << 30, &grid,
+  return launch(p, s, a->norm, false, a->layout, 1 << 30, &grid,
                 reinterpret_cast<cudaStream_t>(stream), who);
 }
 
@@ -1085,7 +1117,7 @@ extern "C" pvl_status pack_rotary_bwd(const pvl_rotary* a, const pvl_heads* dq_o
   const int limit = weights ? static_cast<int>(std::min<long long>(tokens, kMaxPartials)) : 1 << 30;
   int grid = 0;
   cudaStream_t stm = reinterpret_cast<cudaStream_t>(stream);
-  st = launch(p, s, a->norm, norm, a->layout == PVL_ROTARY_HALF, limit, &grid, stm, who);
+  st = launch(p, s, a->norm, norm, a->layout, limit, &grid, stm, who);
   if (st != PVL_OK || !weights) return st;
   const int q_width = a->norm == PVL_NORM_TOKEN ? a->H * a->D : a->D;
   rotary_weights_kernel<<<(p.width + 31) / 32, 1024, 0, stm>>>(p.part, grid, p.width, q_width, dq_weight, dk_weight);
