@@ -88,6 +88,12 @@ def packed_rotary(q, k, positions, plan, norm=None, q_weight=None, k_weight=None
     return _PackedRotary.apply(q, k, positions, plan, norm, q_weight, k_weight, eps)
 
 
+def _dense(t):
+    """t contiguous and on a 16-byte boundary, where a gradient that comes as a part of another need not be."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _GatedResidual(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, h, gate, shift, scale, weight, bias, post_weight, mod_id, how):
@@ -109,8 +115,8 @@ class _GatedResidual(torch.autograd.Function):
         if dy is None:
             dy = torch.zeros(x_out.shape, dtype=torch.bfloat16, device=x_out.device)
         if dx_out is not None:
-            dx_out = dx_out.contiguous()
-        g = api.adaln_residual_bwd(dx_out, dy.contiguous(), x_out, h, gate, shift, scale, mod_id=mod_id, weight=weight,
+            dx_out = _dense(dx_out)
+        g = api.adaln_residual_bwd(dx_out, _dense(dy), x_out, h, gate, shift, scale, mod_id=mod_id, weight=weight,
                                    bias=bias, post_weight=post_weight, branch=ctx.branch, **ctx.how)
         return (*g, None, None)
 

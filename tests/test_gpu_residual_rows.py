@@ -71,3 +71,21 @@ def test_one_outlier_channel_on_a_common_offset(pvl, D, norm, post, stream, plac
         t[name] = v.to(t[name].dtype)
     check(pvl, t, args, how)
     check(pvl, {**t, "dx_out": None}, args, how)
+
+
+@pytest.mark.parametrize("stream", ["bf16", "fp32"])
+def test_gradients_that_are_parts_of_others(pvl, stream):  # noqa: F811
+    """Gradients of outputs that were joined behind one more element start off the kernels' 16-byte boundary."""
+    t, args, how = make(2, 30, 256, "episode", "layer", "rms", stream, 3)
+    x = t["x"].clone().requires_grad_()
+    h = t["h"].clone().requires_grad_()
+    x_out, y = pvl.gated_residual(x, h, *args, **how)
+    ref = torch.autograd.grad([x_out, y], [x, h], [t["dx_out"], t["dy"]])
+    x_out, y = pvl.gated_residual(x, h, *args, **how)
+    joined, ups = [], []
+    for out, up in ((x_out, t["dx_out"]), (y, t["dy"])):
+        one = torch.ones(1, dtype=out.dtype, device="cuda")
+        joined.append(torch.cat([one, out.flatten()]))
+        ups.append(torch.cat([one, up.flatten()]))
+    for a, b in zip(ref, torch.autograd.grad(joined, [x, h], ups)):
+        assert torch.equal(a, b)
