@@ -926,16 +926,19 @@ int widest(const pvl_rotary* a, const pvl_heads* const* views, int n) {
   return 1;
 }
 
-// Heads a thread at a time.  One while the tokens leave SMs without a block
-// (latency counts: most threads, fewest dependent steps); else the largest
-// count that a kernel exists for whose registers hold it.
+// Heads a thread at a time.  One up to two tokens an SM, where latency counts
+// (most threads, fewest dependent steps; 12 + 12 heads of 128, 304 tokens and,
+// past the border, 305, in a graph: forward without a norm 2.65 and 2.68 us, per
+// head 3.26 and 3.41, over the token 3.58 and 4.15; backward per head 3.70 and
+// 3.99, over the token 3.98 and 4.57); else the largest count that a kernel
+// exists for whose registers hold it.
 bool shape_of(const pvl_rotary* a, int V, bool bwd, Shape* s) {
   const int Ht = a->H + a->Hk;
   const bool whole = a->norm == PVL_NORM_TOKEN;
   if (V != 8 && team_of(V, V == 4 ? 4 : 8, Ht, a->D, a->norm, bwd, s)) return true;
   if (V != 8) return V == 1 && team_of(V, 16, Ht, a->D, a->norm, bwd, s);
   const long long tokens = static_cast<long long>(a->B) * a->L;
-  if (tokens <= 2 * 152 && team_of(8, 1, Ht, a->D, a->norm, bwd, s)) return true;
+  if (tokens <= 2ll * sm_count() && team_of(8, 1, Ht, a->D, a->norm, bwd, s)) return true;
   if (!whole) return team_of(8, bwd ? 2 : 3, Ht, a->D, a->norm, bwd, s);
   // six while a token stays within two warps, else more warps count for more
   // (10,240 features a token: 215 us at six, 178 at three; 6,144: 165, 177)
