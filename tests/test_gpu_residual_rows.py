@@ -89,3 +89,11 @@ def test_gradients_that_are_parts_of_others(pvl, stream):  # noqa: F811
         ups.append(torch.cat([one, up.flatten()]))
     for a, b in zip(ref, torch.autograd.grad(joined, [x, h], ups)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("stream", ["bf16", "fp32"])
+@pytest.mark.parametrize("norm,post", [("layer", None), ("rms", "layer")])
+@pytest.mark.parametrize("D", [504, 512, 1280, 1328, 1528, 2304, 2344, 2560, 3584, 3800, 4096, 4608, 5616, 6912, 6920])
+def test_widths(pvl, D, norm, post, stream):  # noqa: F811
+    """Widths on both sides of every change of launch shape, and those between; more rows than the device has SMs."""
+    check(pvl, *make(2, 90, D, "frame", norm, post, stream, seed=D))
