@@ -515,11 +515,231 @@ PVL_API pvl_status masked_mse_loss_bwd(const pvl_bf16* pred, const pvl_bf16* tar
                                        pvl_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * pack_logprob_* — log-probabilities of given tokens under rows of logits,
+ * the entropy of each row, and the gradient to the logits: what the losses
+ * over packed episodes below are made of.
+ *
+ * With z = logits / temperature over the V logits of a token,
+ *   lse  = log sum_i exp(z_i)
+ *   logp = z_target - lse
+ *   entropy = lse - sum_i p_i z_i,            p_i = exp(z_i - lse)
+ *   dlogits_i = (dlogp (1[i = target] - p_i)
+ *                - dentropy p_i (z_i - lse + entropy)) / temperature
+ * A token is valid if seq_id >= 0 (all are where seq_id is null) and its
+ * target lies in [0, V).  Tokens that are not valid have logp, lse and
+ * entropy 0 and a zero gradient; their logits are not read.  A logit of -inf
+ * has probability 0; a row of nothing else has no distribution (lse -inf,
+ * logp and entropy NaN).  NaN and +inf spread over their row.
+ *
+ * logits: dev [B, L, V], bf16 (dtype 0) or fp32 (1); token (b, l) starts at
+ *   b * batch_stride + l * token_stride elements, its V logits are dense; no
+ *   alignment beyond an element's.  targets: dev int32 or int64 [B, L];
+ *   seq_id: dev int32 [B, L] or null; logp, lse, entropy, dlogp, dentropy:
+ *   dev fp32 [B, L].
+ * pack_logprob_fwd writes logp, lse and, where it is not null, the entropy.
+ * pack_logprob_bwd takes lse (and, for dentropy, entropy) of the forward and
+ *   writes dlogits, of the logits' type, at its own strides; it may be the
+ *   logits themselves (same address and strides), not a shifted part of them.
+ *   dlogp or dentropy may be null: zero.
+ * Statistics are held in fp32; logp and entropy do not lose to a common offset
+ * of a row's logits.  The gradient takes probabilities from lse, whose rounding
+ * is theirs: relative to 2^-24 |lse|, so that a row of nothing but a type's
+ * lowest value has none.  It is rounded once to its type, and probabilities
+ * below 2^-126 count as 0 in it.
+ * Errors: INVALID_ARG for null pointers, sizes < 1, types, a temperature that
+ * is not positive and finite, overlapping rows of dlogits; UNSUPPORTED for
+ * V > 2^28, B L >= 2^27, B L V >= 2^42 or an address off its elements.
+ * ---------------------------------------------------------------------- */
+typedef struct pvl_logprob {
+  int32_t B, L, V;
+  int32_t dtype;        /* of the logits: 0 bf16, 1 fp32 */
+  int32_t wide_targets; /* 0: int32, 1: int64 */
+  float temperature;
+  const void* logits;
+  const void* targets;
+  const int32_t* seq_id;
+  int64_t batch_stride, token_stride; /* elements */
+} pvl_logprob;
+
+PVL_API pvl_status pack_logprob_fwd(const pvl_logprob* how, float* logp, float* lse, float* entropy,
+                                    pvl_stream_t stream);
+PVL_API pvl_status pack_logprob_bwd(const pvl_logprob* how, const float* lse, const float* entropy,
+                                    const float* dlogp, const float* dentropy, void* dlogits, int64_t batch_stride,
+                                    int64_t token_stride, pvl_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * pack_preference_* — preference loss over pairs of packed episodes.
+ *
+ * seq_id names each token's episode (pack_build_seq_ids: unique in a pack);
+ * tokens with a negative id take no part and are not used, whatever they
+ * hold.  With D_e = sum of (logp - ref_logp) over the tokens of episode e
+ * (ref_logp null: of logp), divided by their number if `mean` (an episode
+ * without tokens has D_e = 0), and h = D_c - D_r - margin for a pair (c, r)
+ * of a chosen and a rejected episode:
+ *   SIGMOID  -(1 - smoothing) log sigmoid(beta h) - smoothing log sigmoid(-beta h)
+ *   SQUARED  (h - 1 / (2 beta))^2
+ *   HINGE    max(0, 1 - beta h)
+ * loss is the mean over the pairs.  A pair with a negative id is left out
+ * (rewards 0); no pair at all gives loss 0.  An episode may stand in any
+ * number of pairs.
+ *
+ * logp, ref_logp: dev fp32 [tokens]; seq_id: dev int32 [tokens]; pairs: dev
+ * int32 [n_pairs, 2]; loss: dev fp32 [1]; rewards: dev fp32 [n_pairs, 2],
+ * beta D_c and beta D_r; coef: dev fp32 [episodes], d loss / d logp of the
+ * tokens of each episode.  pack_preference_bwd spreads it: dlogp = dloss[0]
+ * coef[seq_id] on tokens with an id, 0 on the others (dloss dev fp32 [1], or
+ * null for 1).  Ids of tokens or pairs at or past `episodes` are left out and
+ * reported by pvl_device_error.  ws: pack_preference_ws_bytes(episodes)
+ * bytes, 16-byte aligned, contents on entry ignored, one per call in flight.
+ * D_e is exact to 2^-41 a token.  The results do not depend on the order in
+ * which blocks run.  Errors: INVALID_ARG for null pointers, counts < 1, a kind
+ * or parameters outside their range, a short workspace; UNSUPPORTED for more
+ * than 2^23 tokens, 2^16 episodes or 2^20 pairs, or an address off its
+ * elements.
+ * ---------------------------------------------------------------------- */
+enum { PVL_PREFERENCE_SIGMOID = 0, PVL_PREFERENCE_SQUARED = 1, PVL_PREFERENCE_HINGE = 2 };
+
+typedef struct pvl_preference {
+  int64_t tokens;
+  int32_t episodes, n_pairs, kind, mean;
+  double beta, smoothing, margin;
+  const float* logp;
+  const float* ref_logp;
+  const int32_t* seq_id;
+  const int32_t* pairs;
+} pvl_preference;
+
+PVL_API size_t pack_preference_ws_bytes(int episodes);
+PVL_API pvl_status pack_preference_fwd(const pvl_preference* how, float* loss, float* rewards, float* coef, void* ws,
+                                       size_t ws_bytes, pvl_stream_t stream);
+PVL_API pvl_status pack_preference_bwd(const float* dloss, const float* coef, const int32_t* seq_id, int64_t tokens,
+                                       int episodes, float* dlogp, pvl_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * pack_policy_* — clipped policy loss with a divergence term over packed
+ * episodes.
+ *
+ * On tokens with seq_id >= 0, d = logp - old_logp (0 where old_logp is null),
+ * with ratio 1 its mean over the token's episode, r = exp(d), A the advantage:
+ *   l = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *       + kl_weight (exp(f) - f - 1),          f = ref_logp - logp
+ * (the first term is 0 where A = 0).  loss is the mean over these tokens (mean
+ * 0) or over the episodes' own means (mean 1; episodes without tokens left
+ * out); 0 where there is no token.
+ *   d loss / d logp: -r A, or 0 where the clipped ratio is the smaller, plus
+ *   kl_weight (1 - exp(f)), each over the count it is averaged by.
+ *
+ * logp, old_logp, ref_logp: dev fp32 [tokens], the latter two may be null;
+ * advantages: dev fp32 [tokens] (token_advantages 1) or [episodes] (0, needed
+ * with ratio 1); seq_id: dev int32 [tokens].  loss: dev fp32 [1]; stats: dev
+ * fp32 [2], the divergence (averaged as the loss) and the share of clipped
+ * tokens (with ratio 1: of episodes); coef: dev fp32 [episodes, 2], 8-byte
+ * aligned, for pack_policy_bwd, which reads the same inputs and writes dlogp =
+ * dloss[0] d loss / d logp, 0 on tokens without an id (dloss null: 1).  Ids,
+ * workspace (pack_policy_ws_bytes), limits and errors as pack_preference_*;
+ * also INVALID_ARG unless 0 <= clip_low < 1, 0 <= clip_high and kl_weight >= 0
+ * are finite, and for a kl_weight above 0 without ref_logp.
+ * ---------------------------------------------------------------------- */
+typedef struct pvl_policy {
+  int64_t tokens;
+  int32_t episodes;
+  int32_t ratio;            /* 0: each token's, 1: its episode's */
+  int32_t mean;             /* 0: over tokens, 1: over episodes' means */
+  int32_t token_advantages; /* 1: one a token, 0: one an episode */
+  double clip_low, clip_high;
+  float kl_weight;
+  const float* logp;
+  const float* old_logp;
+  const float* ref_logp;
+  const float* advantages;
+  const int32_t* seq_id;
+} pvl_policy;
+
+PVL_API size_t pack_policy_ws_bytes(int episodes);
+PVL_API pvl_status pack_policy_fwd(const pvl_policy* how, float* loss, float* stats, float* coef, void* ws,
+                                   size_t ws_bytes, pvl_stream_t stream);
+PVL_API pvl_status pack_policy_bwd(const pvl_policy* how, const float* dloss, const float* coef, float* dlogp,
+                                   pvl_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * pvl_grad_norm — 2-norm of many tensors together: norm[0] = sqrt of the sum
+ * of the squares of all elements.
+ *
+ * grads: host array of `count` dev pointers to dense tensors of one type (0
+ * bf16, 1 fp32) of sizes[i] elements; norm: dev fp32 [1]; ws:
+ * pvl_grad_norm_ws_bytes() bytes, 16-byte aligned, contents on entry ignored,
+ * one per call in flight.  Finite gradients whose squares leave fp32 are
+ * summed in 64 bits; NaN and infinities reach the norm.  The same tensors
+ * give the same bits.  Errors: INVALID_ARG for null pointers, count < 1, an
+ * empty tensor, a short workspace; UNSUPPORTED for more than 131,072 tensors,
+ * 2^41 elements, or an address off its elements.
+ * ---------------------------------------------------------------------- */
+PVL_API size_t pvl_grad_norm_ws_bytes(void);
+PVL_API pvl_status pvl_grad_norm(const void* const* grads, const int64_t* sizes, int count, int dtype, float* norm,
+                                 void* ws, size_t ws_bytes, pvl_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * pvl_adamw_step — one AdamW step of many tensors, in a launch per 512.
+ *
+ * Per element of tensor i, with t = steps[slot] + 1 and c = 1, or min(1,
+ * max_norm / norm[0]) where norm is given:
+ *   g = c grad,  m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ * and steps[slot] = t.  A norm that is not finite leaves everything as it is.
+ *
+ * list: host array of `count` tensors; param and grad: dev, dense, of
+ *   `size` elements, all params of one type (param_dtype) and all grads
+ *   (grad_dtype); no two entries may share a param, a block or a slot.
+ * States: tensor i owns blocks `block` .. block + ceil(size / 256) - 1 of 256
+ *   elements of m, v and master; elements after its end are 0 and stay so.
+ *   bits 32: m, v dev fp32.  bits 8: m, v dev e4m3 bytes, m_scale, v_scale dev
+ *   fp32 one a block: m = code m_scale, v = (code v_scale)^2.  Both are rounded
+ *   stochastically, by bits that depend on seed, step and place alone; a code
+ *   of v that is not 0 stays at least 2^-9; blocks whose largest |m| or sqrt(v)
+ *   is below 2^-100 become 0.
+ *   master: dev fp32, for bf16 parameters, which are then its rounded copy and
+ *   are not read; null for fp32 parameters.
+ * steps: dev int32; done: dev uint32 that is 0 before the first step (the
+ *   library leaves it so); lr_dev: dev fp32 [1] or null (then lr).  m, v,
+ *   master 16-byte aligned.  Steps that share states must follow one another.
+ * Errors: INVALID_ARG for null pointers, counts, sizes, types, bits or
+ * parameters outside their range; UNSUPPORTED for tensors of 2^38 elements and
+ * more, or alignment.
+ * ---------------------------------------------------------------------- */
+typedef struct pvl_adamw_tensor {
+  void* param;
+  const void* grad;
+  int64_t size, block;
+  int32_t slot;
+  float decay;
+} pvl_adamw_tensor;
+
+typedef struct pvl_adamw {
+  int32_t param_dtype, grad_dtype; /* 0 bf16, 1 fp32 */
+  int32_t bits;                    /* of the moments: 32 or 8 */
+  uint32_t seed;
+  double beta1, beta2;
+  float lr, eps, max_norm;
+  const float* lr_dev;
+  const float* norm;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  float* master;
+  int32_t* steps;
+  uint32_t* done;
+} pvl_adamw;
+
+PVL_API pvl_status pvl_adamw_step(const pvl_adamw* how, const pvl_adamw_tensor* list, int count, pvl_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Device error record.  Synchronises `stream`, reads and clears the current
  * device's error record.  Returns PVL_OK, PVL_ERR_TIMEOUT (a bounded wait ran
  * out; the kernel released its resources and returned), PVL_ERR_INVALID_ARG
  * (tile map of another shape; modulation ids of adaln_residual_* outside the
- * table or, backward, out of order) or PVL_ERR_CUDA (the synchronisation failed).
+ * table or, backward, out of order; episode ids of pack_preference_* or
+ * pack_policy_* past their episodes) or PVL_ERR_CUDA (the synchronisation failed).
  * info (optional, host int32[4]): code, where, block, thread of the first
  * failure.
  * ---------------------------------------------------------------------- */

@@ -36,12 +36,16 @@ What it computes, written from the LingBot-VA packing reports:
   queries and keys after an optional RMS norm, with the gradient.
 - ``residual.residual_fwd`` / ``residual.residual_bwd``: the gated residual
   of a block with the norms on both sides, one modulation row per token.
+- ``objectives``: log-probabilities of tokens, the preference loss over pairs of
+  packed episodes and the clipped policy loss, with their gradients.
+- ``adamw``: the AdamW step, the norm of gradients, moments in 8 bits.
 
 Every function is pinned by tests under ``tests/`` against brute force,
 finite differences, closed forms, library routines (torch fp64 autograd and
 scaled_dot_product_attention) and the pages' packed == separate invariant.
 """
 
+from . import adamw, objectives  # noqa: F401
 from .adaln import adaln_bwd, adaln_fwd  # noqa: F401
 from .attention import attention_bwd, attention_fwd, effective_pairs  # noqa: F401
 from .loss import frame_valid_tokens, masked_mse, masked_mse_grad, valid_from_seq_id  # noqa: F401

@@ -41,4 +41,26 @@ from .api import (  # noqa: F401
     version,
 )
 from . import adaptive_load  # noqa: F401  (host-side dual-constraint bucketing)
-from .autograd import adaln_modulate, frame_valid_mse, gated_residual, packed_attention, packed_rotary  # noqa: F401
+from .autograd import (  # noqa: F401
+    adaln_modulate,
+    frame_valid_mse,
+    gated_residual,
+    packed_attention,
+    packed_rotary,
+    policy_loss,
+    preference_loss,
+    token_logprob,
+)
+from .objectives import (  # noqa: F401
+    PolicyLoss,
+    PreferenceLoss,
+    pack_logprob_bwd,
+    pack_logprob_fwd,
+    pack_policy_bwd,
+    pack_policy_fwd,
+    pack_policy_ws_bytes,
+    pack_preference_bwd,
+    pack_preference_fwd,
+    pack_preference_ws_bytes,
+)
+from .optim import AdamWState, adamw_state, adamw_step, grad_norm  # noqa: F401

@@ -24,6 +24,11 @@ PACK_HEADS = struct.Struct("@Pqqq").pack               # pvl_heads
 PACK_RESIDUAL = struct.Struct("@7iffPPPPPPP").pack     # pvl_residual
 PACK_RESIDUAL_GRADS = struct.Struct("@PPPPPP").pack    # pvl_residual_grads
 
+PACK_LOGPROB = struct.Struct("@5ifPPPqq").pack         # pvl_logprob
+PACK_PREFERENCE = struct.Struct("@q4idddPPPP").pack    # pvl_preference
+PACK_POLICY = struct.Struct("@q4iddfPPPPP").pack       # pvl_policy
+PACK_ADAMW = struct.Struct("@3iIddfffPPPPPPPPP").pack  # pvl_adamw
+
 # name -> (restype, argtypes); mirrors include/pvl.h
 SIGNATURES = {
     "pack_build_seq_ids": (_c_int, [_p, _p, _c_int, _c_int, _c_int, _c_int, _p, _p]),
@@ -57,6 +62,17 @@ SIGNATURES = {
     "masked_mse_ws_bytes": (_c_size, [_c_int, _c_int, _c_int]),
     "masked_mse_loss": (_c_int, [_p, _p, _p, _c_int, _c_int, _c_int, _p, _p, _c_float, _p, _c_size, _p]),
     "masked_mse_loss_bwd": (_c_int, [_p, _p, _p, _c_int, _c_int, _c_int, _p, _p, _p, _c_size, _p]),
+    "pack_logprob_fwd": (_c_int, [_p, _p, _p, _p, _p]),
+    "pack_logprob_bwd": (_c_int, [_p, _p, _p, _p, _p, _p, ctypes.c_int64, ctypes.c_int64, _p]),
+    "pack_preference_ws_bytes": (_c_size, [_c_int]),
+    "pack_preference_fwd": (_c_int, [_p, _p, _p, _p, _p, _c_size, _p]),
+    "pack_preference_bwd": (_c_int, [_p, _p, _p, ctypes.c_int64, _c_int, _p, _p]),
+    "pack_policy_ws_bytes": (_c_size, [_c_int]),
+    "pack_policy_fwd": (_c_int, [_p, _p, _p, _p, _p, _c_size, _p]),
+    "pack_policy_bwd": (_c_int, [_p, _p, _p, _p, _p]),
+    "pvl_grad_norm_ws_bytes": (_c_size, []),
+    "pvl_grad_norm": (_c_int, [_p, _p, _c_int, _c_int, _p, _p, _c_size, _p]),
+    "pvl_adamw_step": (_c_int, [_p, _p, _c_int, _p]),
     "pvl_selftest_wait_timeout": (_c_int, [ctypes.c_uint64, ctypes.c_uint64, _p, _p]),
     "pvl_set_attn_wait_timeout_ns": (_c_int, [ctypes.c_uint64]),
     "pvl_mark_next_bwd_main": (_c_int, [_p, _p]),

@@ -10,7 +10,7 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import api
+from . import api, objectives
 
 
 class _PackedAttention(torch.autograd.Function):
@@ -154,3 +154,81 @@ def frame_valid_mse(pred, target, seq_id):
     and target again and scales by the incoming gradient on the device."""
     return _MaskedMSE.apply(pred, target, seq_id)
 
+
+
+class _TokenLogprob(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, targets, seq_id, temperature, entropy):
+        logp, lse, ent = objectives.pack_logprob_fwd(logits, targets, seq_id, temperature=temperature, entropy=entropy)
+        ctx.save_for_backward(logits, targets, seq_id, lse, ent)
+        ctx.temperature = temperature
+        ctx.set_materialize_grads(False)
+        return (logp, ent) if entropy else logp
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dlogp, dent=None):
+        logits, targets, seq_id, lse, ent = ctx.saved_tensors
+        if dlogp is None and dent is None:
+            return None, None, None, None, None
+        dlogp, dent = (None if t is None else t.contiguous() for t in (dlogp, dent))
+        return objectives.pack_logprob_bwd(dlogp, logits, targets, lse, seq_id, temperature=ctx.temperature, ent=ent,
+                                           dent=dent), None, None, None, None
+
+
+def token_logprob(logits, targets, seq_id=None, *, temperature: float = 1.0, entropy: bool = False):
+    """fp32 [B, L] log-probabilities of targets under logits [B, L, V] (see
+    objectives.pack_logprob_fwd), with entropy=True (log-probabilities, entropy
+    of each row), differentiable in the logits."""
+    return _TokenLogprob.apply(logits, targets, seq_id, temperature, entropy)
+
+
+class _PreferenceLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logp, ref_logp, seq_id, pairs, episodes, how):
+        out = objectives.pack_preference_fwd(logp, ref_logp, seq_id, pairs, episodes, **how)
+        ctx.save_for_backward(out.coef, seq_id)
+        ctx.mark_non_differentiable(out.rewards)
+        return out.loss.view(()), out.rewards
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss, _):
+        coef, seq_id = ctx.saved_tensors
+        return (objectives.pack_preference_bwd(dloss.reshape(1).contiguous(), coef, seq_id),) + (None,) * 5
+
+
+def preference_loss(logp, ref_logp, seq_id, pairs, episodes: int, *, beta: float = 0.1, kind: str = "sigmoid",
+                    smoothing: float = 0.0, margin: float = 0.0, mean: bool = False):
+    """(loss, rewards) of objectives.pack_preference_fwd: the preference loss
+    over pairs of packed episodes, differentiable in logp, and the rewards of
+    each pair's episodes."""
+    how = dict(beta=beta, kind=kind, smoothing=smoothing, margin=margin, mean=mean)
+    return _PreferenceLoss.apply(logp, ref_logp, seq_id, pairs, episodes, how)
+
+
+class _PolicyLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logp, old_logp, advantages, seq_id, ref_logp, episodes, mean, how):
+        out = objectives.pack_policy_fwd(logp, old_logp, advantages, seq_id, episodes, ref_logp=ref_logp, mean=mean,
+                                         **how)
+        ctx.save_for_backward(logp, old_logp, advantages, seq_id, ref_logp, out.coef)
+        ctx.how = how
+        ctx.mark_non_differentiable(out.stats)
+        return out.loss.view(()), out.stats
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss, _):
+        logp, old_logp, advantages, seq_id, ref_logp, coef = ctx.saved_tensors
+        return (objectives.pack_policy_bwd(dloss.reshape(1).contiguous(), logp, old_logp, advantages, seq_id, coef,
+                                           ref_logp=ref_logp, **ctx.how),) + (None,) * 7
+
+
+def policy_loss(logp, old_logp, advantages, seq_id, episodes: int, *, ref_logp=None, clip_low: float = 0.2,
+                clip_high: float = 0.2, kl_weight: float = 0.0, ratio: str = "token", mean: str = "token"):
+    """(loss, stats) of objectives.pack_policy_fwd: the clipped policy loss with
+    its divergence term, differentiable in logp, and (divergence, share of
+    clipped ratios)."""
+    how = dict(clip_low=clip_low, clip_high=clip_high, kl_weight=kl_weight, ratio=ratio)
+    return _PolicyLoss.apply(logp, old_logp, advantages, seq_id, ref_logp, episodes, mean, how)

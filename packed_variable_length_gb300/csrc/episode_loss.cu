@@ -1,0 +1,835 @@
+// pack_preference_*, pack_policy_*: losses of a packed policy over whole
+// episodes, for sm_103a.
+//
+// Every token t of the pack carries an episode id e = seq_id[t] (negative:
+// padding or prompt, not trained on) and its log-probability.
+//
+// Preference.  D_e = sum over the episode's tokens of logp - ref (divided by
+// their number with `mean`); for a pair (c, r), h = D_c - D_r - margin, and
+//   sigmoid  l = -(1 - s) log sigmoid(beta h) - s log sigmoid(-beta h)
+//   squared  l = (h - 1 / (2 beta))^2
+//   hinge    l = max(0, 1 - beta h)
+// averaged over the pairs.  dl/dlogp_t = coef[e]: the forward leaves a table of
+// one factor an episode, the backward spreads it over the tokens.
+//
+// Policy.  With d = logp - old and r = exp d (d averaged over the episode
+// first where the ratio is the episode's), A the advantage,
+//   l = -min(r A, clip(r, 1 - low, 1 + high) A) + kl_weight (exp f - f - 1),
+// f = ref - logp, averaged over the valid tokens, or over the episodes' means.
+// The gradient of the first term is -r A, or 0 where the clipped ratio is the
+// smaller; of the second kl_weight (1 - exp f).
+//
+// Both are bound by latency: a 64k pack is 1.6 MB.  One kernel reads the
+// tokens, four a thread; blocks whose tokens belong to one episode add one sum,
+// others one per warp or per run of a thread's tokens.  The last block to
+// finish turns the episodes' sums into the loss and the table.
+//
+// Sums are integers, so that they are the same whatever order blocks finish in,
+// and exact.  A token's value in units of 2^-40 (rounded once; differences are
+// taken as exact pairs of fp32 values first) is added in 64 bits within the
+// block; an episode holds digits in base 2^40, from 2^-80 to 2^160, to which a
+// block, warp or run adds by integer atomics.  Values of 2^11 and more go to
+// the digits one by one, infinities and NaN to flags.  With at most 2^23 tokens
+// a digit's sum stays below 2^63.  64-bit floating point, of which this GPU
+// does little, is left to values that are large.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <initializer_list>
+
+#include "pvl_device.cuh"
+
+namespace pvl {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kTokens = 4 * kThreads;  // of a block
+constexpr int kBwdThreads = 256;
+constexpr uint32_t kSiteEpisode = 71, kSitePair = 72;
+constexpr long long kMaxTokens = 1ll << 23;
+constexpr int kMaxEpisodes = 1 << 16;
+constexpr int kMaxPairs = 1 << 20;
+constexpr unsigned kAll = 0xffffffffu;
+
+// ------------------------------------------------- pairs of fp32 values
+// hi + lo with |lo| at most half a step of hi; lo = 0 where hi is not finite.
+struct Pair {
+  float hi, lo;
+};
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
+
+// The exact sum of two fp32 values (Knuth's two-sum).
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  const float e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+  return {s, finite(s) ? e : 0.0f};
+}
+
+// hi + lo for a small lo (Dekker's fast two-sum).
+__device__ __forceinline__ Pair renormal(float hi, float lo) {
+  const float s = __fadd_rn(hi, lo);
+  return {s, finite(s) ? __fsub_rn(lo, __fsub_rn(s, hi)) : 0.0f};
+}
+
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  const Pair s = two_sum(a.hi, b.hi);
+  return renormal(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+
+__device__ __forceinline__ Pair times(float a, float b) {
+  const float p = __fmul_rn(a, b);
+  return {p, finite(p) ? fmaf(a, b, -p) : 0.0f};
+}
+
+__device__ __forceinline__ Pair over(Pair a, float n) {
+  const float q = __fdiv_rn(a.hi, n);
+  return finite(q) ? renormal(q, __fdiv_rn(__fadd_rn(fmaf(-q, n, a.hi), a.lo), n)) : Pair{q, 0.0f};
+}
+
+// ------------------------------------------------------------ exact sums
+constexpr double kUp = 1099511627776.0;     // 2^40
+constexpr float kFine = 1099511627776.0f;   // units of 2^-40
+constexpr long long kMask = (1ll << 40) - 1;
+
+struct Sum {
+  long long digit[6];  // of weight 2^120, 2^80, 2^40, 1, 2^-40, 2^-80
+};
+
+__device__ __forceinline__ void add_digit(long long* d, long long v) {
+  if (v) atomicAdd(reinterpret_cast<unsigned long long*>(d), static_cast<unsigned long long>(v));
+}
+
+// Adds v units of 2^-40.
+__device__ __forceinline__ void add_units(Sum* s, long long v) {
+  const unsigned long long m = v < 0 ? 0ull - static_cast<unsigned long long>(v) : static_cast<unsigned long long>(v);
+  const long long whole = static_cast<long long>(m >> 40), part = static_cast<long long>(m) & kMask;
+  add_digit(&s->digit[3], v < 0 ? -whole : whole);
+  add_digit(&s->digit[4], v < 0 ? -part : part);
+}
+
+// Adds any x; what is not finite goes into three bits of *flags at `shift`.
+__device__ __noinline__ void add_any(Sum* s, unsigned int* flags, int shift, double x) {
+  if (!(fabs(x) < 1e300)) {
+    atomicOr(flags, (x != x ? 1u : x > 0.0 ? 2u : 4u) << shift);
+    return;
+  }
+  double weight = kUp * kUp * kUp;
+#pragma unroll 1
+  for (int i = 0; i < 6; ++i, weight *= 1.0 / kUp) {
+    const double v = i < 5 ? trunc(x * (1.0 / weight)) : rint(x * (1.0 / weight));
+    add_digit(&s->digit[i], __double2ll_rn(v));
+    x -= v * weight;  // exact: a multiple of x's last bit, and no longer than x
+  }
+}
+
+// The digits with carries taken upwards and one sign: magnitude in d, returns
+// whether the sum is negative.
+__device__ __forceinline__ bool carry(long long (&d)[6]) {
+  bool negative = false;
+#pragma unroll
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll
+    for (int i = 5; i > 0; --i) {
+      d[i - 1] += d[i] >> 40;
+      d[i] &= kMask;
+    }
+    if (pass || d[0] >= 0) break;
+    negative = true;
+#pragma unroll
+    for (int i = 0; i < 6; ++i) d[i] = -d[i];
+  }
+  return negative;
+}
+
+__device__ __noinline__ double large_value(const long long (&digit)[6], unsigned int flags) {
+  if (flags) return flags == 2u ? __longlong_as_double(0x7FF0000000000000ll)
+                  : flags == 4u ? __longlong_as_double(0xFFF0000000000000ll)
+                                : __longlong_as_double(0x7FF8000000000000ll);
+  long long d[6];
+#pragma unroll
+  for (int i = 0; i < 6; ++i) d[i] = digit[i];
+  const bool negative = carry(d);
+  double v = 0.0, weight = 1.0 / (kUp * kUp);
+#pragma unroll
+  for (int i = 5; i >= 0; --i, weight *= kUp) v += static_cast<double>(d[i]) * weight;
+  return negative ? -v : v;
+}
+
+// A sum's value, as a pair and in 64 bits.
+struct Value {
+  Pair p;
+  double d;
+};
+
+__device__ __forceinline__ Value value(const Sum* s, unsigned int flags, int shift) {
+  flags = (flags >> shift) & 7u;
+  long long d[6];
+#pragma unroll
+  for (int i = 0; i < 6; ++i) d[i] = __ldcg(&s->digit[i]);
+  const long long next = d[4] + (d[5] >> 40), top = d[3] + (next >> 40);
+  if (!(flags | d[0] | d[1] | d[2]) && top < (1ll << 22) && top >= -(1ll << 22)) {
+    const long long whole = top * (1ll << 40) + (next & kMask);  // units of 2^-40
+    const float rest = __ll2float_rn(d[5] & kMask) * (1.0f / kFine);
+    const float hi = __ll2float_rn(whole);
+    const Pair u = renormal(hi, __ll2float_rn(whole - __float2ll_rn(hi)) + rest);
+    return {{u.hi * (1.0f / kFine), u.lo * (1.0f / kFine)},
+            (static_cast<double>(whole) + static_cast<double>(rest)) * (1.0 / kUp)};
+  }
+  const double v = large_value(d, flags);
+  const float hi = static_cast<float>(v);
+  return {{hi, finite(hi) ? static_cast<float>(v - hi) : 0.0f}, v};
+}
+
+// What is summed of an episode: two values, valid tokens, clipped tokens.
+struct Episode {
+  Sum a, b;
+  unsigned int n, cut, flags, unused;
+};
+static_assert(sizeof(Episode) == 112, "workspace layout");
+
+// A thread's, warp's or block's part of it, in units of 2^-40.
+struct Part {
+  long long a, b;
+  unsigned int n, cut;
+};
+
+__device__ __forceinline__ void add_part(Episode* e, const Part& p) {
+  add_units(&e->a, p.a);
+  add_units(&e->b, p.b);
+  if (p.n) atomicAdd(&e->n, p.n);
+  if (p.cut) atomicAdd(&e->cut, p.cut);
+}
+
+__device__ __forceinline__ Part operator+(const Part& x, const Part& y) {
+  return {x.a + y.a, x.b + y.b, x.n + y.n, x.cut + y.cut};
+}
+
+__device__ __forceinline__ Part warp_sum(Part p, bool two) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) p.a += __shfl_xor_sync(kAll, p.a, o);
+  if (two) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) p.b += __shfl_xor_sync(kAll, p.b, o);
+  }
+  p.n = __reduce_add_sync(kAll, p.n);
+  p.cut = __reduce_add_sync(kAll, p.cut);
+  return p;
+}
+
+// Sums over the block in a fixed order; every thread gets them.
+__device__ Pair block_sum(Pair v) {
+  __shared__ Pair part[kWarps];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = add(v, Pair{__shfl_xor_sync(kAll, v.hi, o), __shfl_xor_sync(kAll, v.lo, o)});
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
+  __syncthreads();
+  v = part[threadIdx.x % kWarps];
+#pragma unroll
+  for (int o = kWarps / 2; o > 0; o >>= 1)
+    v = add(v, Pair{__shfl_xor_sync(kAll, v.hi, o), __shfl_xor_sync(kAll, v.lo, o)});
+  return v;
+}
+
+__device__ unsigned int block_count(unsigned int n) {
+  __shared__ unsigned int part[kWarps];
+  n = __reduce_add_sync(kAll, n);
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = n;
+  __syncthreads();
+  return __reduce_add_sync(kAll, threadIdx.x % 32 < kWarps ? part[threadIdx.x % 32] : 0u);
+}
+
+// ------------------------------------------------------------- parameters
+struct LossParams {
+  const float* logp;
+  const float* old;
+  const float* ref;
+  const float* adv;
+  const int32_t* seq_id;
+  long long N;
+  int E;
+  // policy
+  bool by_token, adv_by_token, ratio_episode, mean_episode;
+  float bound_low, bound_high;  // 1 - low, 1 + high
+  Pair log_low, log_high;       // their logarithms
+  float kl_weight;
+  // preference
+  const int32_t* pairs;
+  int P, kind;
+  bool mean;
+  float beta, smoothing;
+  double beta_d, margin_d;
+  Pair margin, target;  // target: 1 / (2 beta)
+  float* rewards;
+  // results
+  float* loss;
+  float* stats;
+  float* coef;
+  const float* dloss;
+  float* dlogp;
+  // workspace
+  unsigned int* done;
+  Episode* episodes;
+  Sum* factors;  // preference: sums of the pairs' derivatives, one an episode
+  unsigned int* factor_flags;
+  Value* sums;   // D_e
+  DeviceError* err;
+};
+
+__device__ __forceinline__ void report(DeviceError* err, uint32_t where) {
+  if (atomicCAS(&err->code, 0u, kDevErrEpisode) == 0u) {
+    err->where = where;
+    err->block = blockIdx.x;
+    err->thread = threadIdx.x;
+  }
+}
+
+// Four tokens from `first` on; those at or past N get `other`.
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, long long first, long long N, T other, T (&v)[4]) {
+  if (first + 4 <= N && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p + first));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const T*>(&w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = first + i < N ? p[first + i] : other;
+  }
+}
+
+// exp f - f - 1 without cancellation: its series up to 0.5 (the next term is
+// below 2^-24 of the sum), else the formula.
+__device__ __forceinline__ float kl_term(float f) {
+  if (fabsf(f) < 0.5f) {
+    float s = 1.0f / 362880.0f;
+    s = fmaf(s, f, 1.0f / 40320.0f);
+    s = fmaf(s, f, 1.0f / 5040.0f);
+    s = fmaf(s, f, 1.0f / 720.0f);
+    s = fmaf(s, f, 1.0f / 120.0f);
+    s = fmaf(s, f, 1.0f / 24.0f);
+    s = fmaf(s, f, 1.0f / 6.0f);
+    s = fmaf(s, f, 0.5f);
+    return s * f * f;
+  }
+  return expf(f) - 1.0f - f;
+}
+
+// a > b, for pairs: the lower parts decide where the upper are equal.
+__device__ __forceinline__ bool above(Pair a, Pair b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
+
+// Whether the clipped ratio is the one that counts.
+__device__ __forceinline__ bool clipped(const LossParams& p, Pair d, float adv) {
+  return adv > 0.0f ? above(d, p.log_high) : adv < 0.0f && above(p.log_low, d);
+}
+
+// -min(r A, clip(r) A).  An advantage of 0 gives 0 whatever the ratio.
+__device__ __forceinline__ float policy_term(const LossParams& p, float d, float adv, bool cut) {
+  if (adv == 0.0f) return 0.0f;
+  return -(cut ? (adv > 0.0f ? p.bound_high : p.bound_low) : expf(d)) * adv;
+}
+
+// ------------------------------------------------------------- forward
+// A value in units of 2^-40; one that does not fit goes to the episode at once.
+__device__ __forceinline__ long long units(Pair v, Sum* s, unsigned int* flags, int shift) {
+  if (fabsf(v.hi) < 2048.0f) return __float2ll_rn(v.hi * kFine) + __float2ll_rn(v.lo * kFine);
+  add_any(s, flags, shift, static_cast<double>(v.hi) + static_cast<double>(v.lo));
+  return 0;
+}
+
+// Sums of this block's tokens into the episodes'.
+template <bool kPolicy>
+__device__ void sum_tokens(const LossParams& p) {
+  __shared__ int warp_lo[kWarps], warp_hi[kWarps];
+  __shared__ Part warp_part[kWarps];
+  const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+  const long long first = static_cast<long long>(blockIdx.x) * kTokens + threadIdx.x * 4;
+  int id[4];
+  float logp[4], old[4], ref[4], adv[4];
+  load4(p.seq_id, first, p.N, -1, id);
+  load4(p.logp, first, p.N, 0.0f, logp);
+  if (p.ref) load4(p.ref, first, p.N, 0.0f, ref);
+  if (kPolicy && p.old) load4(p.old, first, p.N, 0.0f, old);
+  if (kPolicy && p.adv_by_token) load4(p.adv, first, p.N, 0.0f, adv);
+  const bool two = kPolicy && p.ref;
+  Part t[4];
+  int lo = INT32_MAX, hi = -1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    t[i] = Part{0, 0, 0, 0};
+    if (id[i] >= p.E) {
+      report(p.err, kSiteEpisode);
+      id[i] = -1;
+    }
+    if (id[i] < 0) continue;
+    t[i].n = 1;
+    Pair a, b{0.0f, 0.0f};
+    int to = id[i];
+    if constexpr (kPolicy) {
+      a = p.old ? two_sum(logp[i], -old[i]) : Pair{0.0f, 0.0f};
+      if (p.ref) b = Pair{kl_term(__fsub_rn(ref[i], logp[i])), 0.0f};
+      if (!p.ratio_episode) {
+        const float v = p.adv_by_token ? adv[i] : __ldg(p.adv + id[i]);
+        const bool cut = clipped(p, a, v);
+        a = Pair{policy_term(p, a.hi, v, cut), 0.0f};
+        t[i].cut = cut;
+      }
+      if (p.by_token) to = 0;  // one sum over all tokens
+      id[i] = to;
+    } else {
+      a = p.ref ? two_sum(logp[i], -ref[i]) : Pair{logp[i], 0.0f};
+    }
+    Episode* e = p.episodes + to;
+    t[i].a = units(a, &e->a, &e->flags, 0);
+    if (two) t[i].b = units(b, &e->b, &e->flags, 3);
+    lo = min(lo, to);
+    hi = max(hi, to);
+  }
+  lo = __reduce_min_sync(kAll, lo);
+  hi = __reduce_max_sync(kAll, hi);
+  if (lane == 0) {
+    warp_lo[w] = lo;
+    warp_hi[w] = hi;
+  }
+  Part sum = warp_sum(t[0] + t[1] + t[2] + t[3], two);
+  if (lane == 0) warp_part[w] = sum;
+  __syncthreads();
+  const int block_lo = __reduce_min_sync(kAll, warp_lo[lane % kWarps]);
+  const int block_hi = __reduce_max_sync(kAll, warp_hi[lane % kWarps]);
+  if (block_hi < 0) return;
+  if (block_lo == block_hi) {
+    if (w == 0) {
+      sum = lane < kWarps ? warp_part[lane] : Part{0, 0, 0, 0};
+      sum = warp_sum(sum, two);
+      if (lane == 0) add_part(p.episodes + block_lo, sum);
+    }
+  } else if (lo == hi) {
+    if (lane == 0) add_part(p.episodes + lo, sum);
+  } else {
+    Part run = t[0];
+    int at = id[0];
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+      if (id[i] != at) {
+        if (at >= 0) add_part(p.episodes + at, run);
+        run = t[i];
+        at = id[i];
+      } else {
+        run = run + t[i];
+      }
+    }
+    if (at >= 0) add_part(p.episodes + at, run);
+  }
+}
+
+// Whether this block is the last of the grid to get here; it then sees what
+// all others wrote.
+__device__ bool last_block(const LossParams& p) {
+  __shared__ bool last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    last = atomicAdd(p.done, 1u) == gridDim.x - 1;
+    __threadfence();
+  }
+  __syncthreads();
+  return last;
+}
+
+__global__ void __launch_bounds__(kThreads) preference_kernel(const LossParams p) {
+  sum_tokens<false>(p);
+  if (!last_block(p)) return;
+  for (int e = threadIdx.x; e < p.E; e += kThreads) {
+    const Episode* q = p.episodes + e;
+    const unsigned int n = __ldcg(&q->n);
+    Value v = value(&q->a, __ldcg(&q->flags), 0);
+    if (p.mean && n) {
+      v.p = over(v.p, static_cast<float>(n));
+      v.d /= n;
+    }
+    p.sums[e] = v;
+  }
+  __syncthreads();
+  Pair loss{0.0f, 0.0f};
+  unsigned int count = 0;
+  for (int i = threadIdx.x; i < p.P; i += kThreads) {
+    const int c = p.pairs[2 * i], r = p.pairs[2 * i + 1];
+    if (c >= p.E || r >= p.E) report(p.err, kSitePair);
+    if (c < 0 || r < 0 || c >= p.E || r >= p.E) {
+      p.rewards[2 * i] = p.rewards[2 * i + 1] = 0.0f;
+      continue;
+    }
+    ++count;
+    const Value vc = p.sums[c], vr = p.sums[r];
+    Pair h;   // D_c - D_r - margin, to 2^-46 of its terms
+    float x;  // beta h
+    float rc = p.beta * vc.p.hi, rr = p.beta * vr.p.hi;
+    bool short_of;  // beta h < 1, decided in 64 bits
+    if (fabsf(vc.p.hi) < 1e6f && fabsf(vr.p.hi) < 1e6f && p.kind != PVL_PREFERENCE_HINGE) {
+      h = add(add(vc.p, Pair{-vr.p.hi, -vr.p.lo}), Pair{-p.margin.hi, -p.margin.lo});
+      x = p.beta * h.hi;
+      short_of = false;
+    } else {
+      const double d = vc.d - vr.d - p.margin_d;
+      const float hi = static_cast<float>(d);
+      h = {hi, finite(hi) ? static_cast<float>(d - hi) : 0.0f};
+      x = static_cast<float>(p.beta_d * d);
+      short_of = p.beta_d * d < 1.0;
+      rc = static_cast<float>(p.beta_d * vc.d);
+      rr = static_cast<float>(p.beta_d * vr.d);
+    }
+    p.rewards[2 * i] = rc;
+    p.rewards[2 * i + 1] = rr;
+    float l, up;  // up: the derivative to h, over beta but for the squared loss
+    if (p.kind == PVL_PREFERENCE_SIGMOID) {
+      const float e = expf(-fabsf(x)), soft = log1pf(e);
+      const float s = p.smoothing;
+      l = (1.0f - s) * (soft + fmaxf(-x, 0.0f));
+      if (s > 0.0f) l = fmaf(s, soft + fmaxf(x, 0.0f), l);  // not 0 times infinity
+      const float other = x >= 0.0f ? e / (1.0f + e) : 1.0f / (1.0f + e);  // sigmoid(-x)
+      up = s - other;
+    } else if (p.kind == PVL_PREFERENCE_SQUARED) {
+      const Pair miss = add(h, Pair{-p.target.hi, -p.target.lo});
+      l = miss.hi * miss.hi;
+      up = 2.0f * miss.hi;
+    } else {
+      l = short_of ? 1.0f - x : 0.0f;
+      up = short_of ? -1.0f : 0.0f;
+    }
+    if (x != x) l = up = x;
+    loss = add(loss, Pair{l, 0.0f});
+    if (c != r) {  // an episode against itself has no gradient
+      if (fabsf(up) < 2048.0f) {
+        const float fine = up * kFine;
+        const long long v = __float2ll_rn(fine), rest = __float2ll_rn((fine - __ll2float_rn(v)) * kFine);
+        add_units(p.factors + c, v);
+        add_units(p.factors + r, -v);
+        add_digit(&p.factors[c].digit[5], rest);
+        add_digit(&p.factors[r].digit[5], -rest);
+      } else {
+        add_any(p.factors + c, p.factor_flags + c, 0, up);
+        add_any(p.factors + r, p.factor_flags + r, 0, -up);
+      }
+    }
+  }
+  count = block_count(count);
+  loss = block_sum(loss);
+  const float share = count ? static_cast<float>(count) : 1.0f;
+  if (threadIdx.x == 0) p.loss[0] = over(loss, share).hi;
+  __threadfence();
+  __syncthreads();
+  const float slope = p.kind == PVL_PREFERENCE_SQUARED ? 1.0f : p.beta;
+  for (int e = threadIdx.x; e < p.E; e += kThreads) {
+    const unsigned int n = __ldcg(&p.episodes[e].n);
+    const float f = slope * over(value(p.factors + e, __ldcg(p.factor_flags + e), 0).p, share).hi;
+    p.coef[e] = p.mean && n ? f / static_cast<float>(n) : f;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) policy_kernel(const LossParams p) {
+  sum_tokens<true>(p);
+  if (!last_block(p)) return;
+  const int E = p.by_token ? 1 : p.E;
+  unsigned int tokens = 0, some = 0;
+  for (int e = threadIdx.x; e < E; e += kThreads) {
+    const unsigned int n = __ldcg(&p.episodes[e].n);
+    tokens += n;
+    some += n ? 1u : 0u;
+  }
+  tokens = block_count(tokens);
+  some = block_count(some);
+  // what sums are divided by at the end
+  const float whole = static_cast<float>(max(1u, p.mean_episode ? some : tokens));
+  Pair loss{0.0f, 0.0f}, kl{0.0f, 0.0f};
+  unsigned int cut = 0;
+  for (int e = threadIdx.x; e < E; e += kThreads) {
+    const Episode* q = p.episodes + e;
+    const unsigned int n = __ldcg(&q->n), flags = __ldcg(&q->flags);
+    float slope = 0.0f, weight = 0.0f;
+    if (n) {
+      const float fn = static_cast<float>(n);
+      const Pair a = value(&q->a, flags, 0).p;
+      weight = p.mean_episode ? 1.0f / (whole * fn) : 1.0f / whole;
+      if (p.ratio_episode) {
+        const Pair d = over(a, fn);
+        const float adv = p.adv[e];
+        const bool clip = clipped(p, d, adv);
+        const float term = policy_term(p, d.hi, adv, clip);
+        loss = add(loss, p.mean_episode ? Pair{term, 0.0f} : times(term, fn));
+        slope = clip ? 0.0f : weight * term;
+        cut += clip;
+      } else {
+        loss = add(loss, p.mean_episode ? over(a, fn) : a);
+        cut += __ldcg(&q->cut);
+      }
+      if (p.ref) {
+        const Pair b = value(&q->b, flags, 3).p;
+        kl = add(kl, p.mean_episode ? over(b, fn) : b);
+      }
+    }
+    if (!p.by_token) *reinterpret_cast<float2*>(p.coef + 2 * e) = make_float2(slope, weight);
+  }
+  cut = block_count(cut);
+  loss = over(block_sum(loss), whole);
+  kl = over(block_sum(kl), whole);
+  if (threadIdx.x == 0) {
+    // 0 times an infinite divergence is no part of the loss
+    if (p.kl_weight != 0.0f) {
+      Pair k = times(p.kl_weight, kl.hi);
+      k.lo = finite(k.hi) ? fmaf(p.kl_weight, kl.lo, k.lo) : 0.0f;
+      loss = add(loss, k);
+    }
+    p.loss[0] = loss.hi;
+    p.stats[0] = kl.hi;
+    p.stats[1] = static_cast<float>(cut) / static_cast<float>(max(1u, p.ratio_episode ? some : tokens));
+  }
+  if (p.by_token)
+    for (int e = threadIdx.x; e < p.E; e += kThreads)
+      *reinterpret_cast<float2*>(p.coef + 2 * e) = make_float2(0.0f, tokens ? 1.0f / whole : 0.0f);
+}
+
+// ------------------------------------------------------------- backward
+template <bool kPolicy>
+__global__ void __launch_bounds__(kBwdThreads) token_grad_kernel(const LossParams p) {
+  const long long first = (static_cast<long long>(blockIdx.x) * kBwdThreads + threadIdx.x) * 4;
+  if (first >= p.N) return;
+  int id[4];
+  float logp[4], old[4], ref[4], adv[4], g[4];
+  load4(p.seq_id, first, p.N, -1, id);
+  const bool kl = kPolicy && p.ref && p.kl_weight != 0.0f;
+  if constexpr (kPolicy) {
+    load4(p.logp, first, p.N, 0.0f, logp);
+    if (p.old && !p.ratio_episode) load4(p.old, first, p.N, 0.0f, old);
+    if (kl) load4(p.ref, first, p.N, 0.0f, ref);
+    if (p.adv_by_token) load4(p.adv, first, p.N, 0.0f, adv);
+  }
+  const float up = p.dloss ? __ldg(p.dloss) : 1.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    g[i] = 0.0f;
+    if (id[i] < 0 || id[i] >= p.E) continue;
+    if constexpr (kPolicy) {
+      const float2 c = __ldg(reinterpret_cast<const float2*>(p.coef) + id[i]);
+      float slope = c.x;
+      if (!p.ratio_episode) {
+        const Pair d = p.old ? two_sum(logp[i], -old[i]) : Pair{0.0f, 0.0f};
+        const float a = p.adv_by_token ? adv[i] : __ldg(p.adv + id[i]);
+        const bool cut = clipped(p, d, a);
+        slope = cut ? 0.0f : c.y * policy_term(p, d.hi, a, false);
+      }
+      if (kl) slope = fmaf(-c.y * p.kl_weight, expm1f(__fsub_rn(ref[i], logp[i])), slope);
+      g[i] = up * slope;
+    } else {
+      g[i] = up * __ldg(p.coef + id[i]);
+    }
+  }
+  if (first + 4 <= p.N && reinterpret_cast<uintptr_t>(p.dlogp) % 16 == 0) {
+    *reinterpret_cast<float4*>(p.dlogp + first) = make_float4(g[0], g[1], g[2], g[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (first + i < p.N) p.dlogp[first + i] = g[i];
+  }
+}
+
+// ------------------------------------------------------------------ host
+// Workspace: counter (cleared), episodes (cleared), factors and their flags
+// (cleared, preference), D_e (preference).
+struct Layout {
+  size_t episodes, factors, flags, clear, sums, total;
+};
+
+Layout layout(int E, bool preference) {
+  Layout l{};
+  l.episodes = 256;
+  l.factors = l.episodes + align256(static_cast<size_t>(E) * sizeof(Episode));
+  l.flags = l.factors + (preference ? align256(static_cast<size_t>(E) * sizeof(Sum)) : 0);
+  l.clear = l.flags + (preference ? align256(static_cast<size_t>(E) * 4) : 0);
+  l.sums = l.clear;
+  l.total = l.sums + (preference ? align256(static_cast<size_t>(E) * sizeof(Value)) : 0);
+  return l;
+}
+
+bool misaligned(std::initializer_list<const void*> ptrs, uintptr_t to) {
+  for (const void* q : ptrs)
+    if (reinterpret_cast<uintptr_t>(q) % to) return true;
+  return false;
+}
+
+Pair split(double v) {
+  const float hi = static_cast<float>(v);
+  return {hi, static_cast<float>(v - hi)};
+}
+
+pvl_status sizes(const char* who, int64_t N, int E) {
+  if (N < 1 || E < 1) return fail(PVL_ERR_INVALID_ARG, "%s: tokens and episodes must be >= 1", who);
+  if (N > kMaxTokens || E > kMaxEpisodes)
+    return fail(PVL_ERR_UNSUPPORTED, "%s: %lld tokens of %d episodes (at most %lld, %d)", who, static_cast<long long>(N),
+                E, kMaxTokens, kMaxEpisodes);
+  return PVL_OK;
+}
+
+// The workspace into p, its counters and sums cleared on the stream.
+pvl_status workspace(const char* who, LossParams& p, void* ws, size_t ws_bytes, bool preference, cudaStream_t s) {
+  const Layout l = layout(p.E, preference);
+  if (!ws) return fail(PVL_ERR_INVALID_ARG, "%s: null workspace", who);
+  if (ws_bytes < l.total) return fail(PVL_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu needed", who, ws_bytes, l.total);
+  if (misaligned({ws}, 16)) return fail(PVL_ERR_UNSUPPORTED, "%s: the workspace is not 16-byte aligned", who);
+  p.err = device_error_record();
+  if (!p.err) return fail(PVL_ERR_CUDA, "%s: no usable CUDA device", who);
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  p.done = reinterpret_cast<unsigned int*>(b);
+  p.episodes = reinterpret_cast<Episode*>(b + l.episodes);
+  p.factors = reinterpret_cast<Sum*>(b + l.factors);
+  p.factor_flags = reinterpret_cast<unsigned int*>(b + l.flags);
+  p.sums = reinterpret_cast<Value*>(b + l.sums);
+  return check_cuda(cudaMemsetAsync(ws, 0, l.clear, s), who);
+}
+
+pvl_status policy_params(const char* who, const pvl_policy* h, LossParams* p) {
+  if (!h || !h->logp || !h->advantages || !h->seq_id) return fail(PVL_ERR_INVALID_ARG, "%s: null pointer", who);
+  const pvl_status st = sizes(who, h->tokens, h->episodes);
+  if (st != PVL_OK) return st;
+  if ((h->ratio | h->mean | h->token_advantages) & ~1)
+    return fail(PVL_ERR_INVALID_ARG, "%s: ratio, mean and token_advantages are 0 or 1", who);
+  if (h->ratio == 1 && h->token_advantages)
+    return fail(PVL_ERR_INVALID_ARG, "%s: ratios of episodes need advantages of episodes", who);
+  if (!(h->clip_low >= 0.0 && h->clip_low < 1.0) || !(h->clip_high >= 0.0 && h->clip_high < 1e30))
+    return fail(PVL_ERR_INVALID_ARG, "%s: needs 0 <= clip_low < 1 and 0 <= clip_high", who);
+  if (!(h->kl_weight >= 0.0f) || !(h->kl_weight < 1e30f) || (h->kl_weight > 0.0f && !h->ref_logp))
+    return fail(PVL_ERR_INVALID_ARG, "%s: kl_weight must be finite, not negative, and needs ref_logp above 0", who);
+  if (misaligned({h->logp, h->old_logp, h->ref_logp, h->advantages, h->seq_id}, 4))
+    return fail(PVL_ERR_UNSUPPORTED, "%s: a pointer is not aligned to its elements", who);
+  p->logp = h->logp;
+  p->old = h->old_logp;
+  p->ref = h->ref_logp;
+  p->adv = h->advantages;
+  p->seq_id = h->seq_id;
+  p->N = h->tokens;
+  p->E = h->episodes;
+  p->ratio_episode = h->ratio == 1;
+  p->mean_episode = h->mean == 1;
+  p->by_token = !p->ratio_episode && !p->mean_episode;
+  p->adv_by_token = h->token_advantages != 0;
+  p->bound_low = static_cast<float>(1.0 - h->clip_low);
+  p->bound_high = static_cast<float>(1.0 + h->clip_high);
+  p->log_low = split(std::log1p(-h->clip_low));
+  p->log_high = split(std::log1p(h->clip_high));
+  p->kl_weight = h->kl_weight;
+  return PVL_OK;
+}
+
+unsigned blocks_of(long long n, int per) { return static_cast<unsigned>((n + per - 1) / per); }
+
+}  // namespace
+}  // namespace pvl
+
+using namespace pvl;
+
+extern "C" size_t pack_preference_ws_bytes(int episodes) {
+  return episodes < 1 || episodes > kMaxEpisodes ? 0 : layout(episodes, true).total;
+}
+
+extern "C" size_t pack_policy_ws_bytes(int episodes) {
+  return episodes < 1 || episodes > kMaxEpisodes ? 0 : layout(episodes, false).total;
+}
+
+extern "C" pvl_status pack_preference_fwd(const pvl_preference* h, float* loss, float* rewards, float* coef, void* ws,
+                                          size_t ws_bytes, pvl_stream_t stream) {
+  const char* who = "pack_preference_fwd";
+  if (!h || !h->logp || !h->seq_id || !h->pairs || !loss || !rewards || !coef)
+    return fail(PVL_ERR_INVALID_ARG, "%s: null pointer", who);
+  pvl_status st = sizes(who, h->tokens, h->episodes);
+  if (st != PVL_OK) return st;
+  if (h->n_pairs < 1) return fail(PVL_ERR_INVALID_ARG, "%s: needs a pair", who);
+  if (h->n_pairs > kMaxPairs) return fail(PVL_ERR_UNSUPPORTED, "%s: %d pairs (at most %d)", who, h->n_pairs, kMaxPairs);
+  if (h->kind < 0 || h->kind > 2) return fail(PVL_ERR_INVALID_ARG, "%s: kind %d (0 to 2)", who, h->kind);
+  if (h->mean & ~1) return fail(PVL_ERR_INVALID_ARG, "%s: mean is 0 or 1", who);
+  if (!(h->beta > 1e-30) || !(h->beta < 1e30) || !(std::fabs(h->margin) < 1e30))
+    return fail(PVL_ERR_INVALID_ARG, "%s: beta must be positive, beta and margin finite", who);
+  if (!(h->smoothing >= 0.0 && h->smoothing <= 0.5) || (h->smoothing > 0.0 && h->kind != PVL_PREFERENCE_SIGMOID))
+    return fail(PVL_ERR_INVALID_ARG, "%s: smoothing lies in [0, 0.5] and belongs to the sigmoid loss", who);
+  if (misaligned({h->logp, h->ref_logp, h->seq_id, h->pairs, loss, rewards, coef}, 4))
+    return fail(PVL_ERR_UNSUPPORTED, "%s: a pointer is not aligned to its elements", who);
+  LossParams p{};
+  p.logp = h->logp;
+  p.ref = h->ref_logp;
+  p.seq_id = h->seq_id;
+  p.N = h->tokens;
+  p.E = h->episodes;
+  p.pairs = h->pairs;
+  p.P = h->n_pairs;
+  p.kind = h->kind;
+  p.mean = h->mean != 0;
+  p.beta = static_cast<float>(h->beta);
+  p.beta_d = h->beta;
+  p.smoothing = static_cast<float>(h->smoothing);
+  p.margin = split(h->margin);
+  p.margin_d = h->margin;
+  p.target = split(0.5 / h->beta);
+  p.loss = loss;
+  p.rewards = rewards;
+  p.coef = coef;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = workspace(who, p, ws, ws_bytes, true, s);
+  if (st != PVL_OK) return st;
+  preference_kernel<<<blocks_of(p.N, kTokens), kThreads, 0, s>>>(p);
+  return check_cuda(cudaGetLastError(), "pack_preference_fwd launch");
+}
+
+extern "C" pvl_status pack_preference_bwd(const float* dloss, const float* coef, const int32_t* seq_id, int64_t tokens,
+                                          int episodes, float* dlogp, pvl_stream_t stream) {
+  const char* who = "pack_preference_bwd";
+  if (!coef || !seq_id || !dlogp) return fail(PVL_ERR_INVALID_ARG, "%s: null pointer", who);
+  const pvl_status st = sizes(who, tokens, episodes);
+  if (st != PVL_OK) return st;
+  if (misaligned({dloss, coef, seq_id, dlogp}, 4))
+    return fail(PVL_ERR_UNSUPPORTED, "%s: a pointer is not aligned to its elements", who);
+  LossParams p{};
+  p.dloss = dloss;
+  p.coef = const_cast<float*>(coef);
+  p.seq_id = seq_id;
+  p.N = tokens;
+  p.E = episodes;
+  p.dlogp = dlogp;
+  token_grad_kernel<false><<<blocks_of(p.N, 4 * kBwdThreads), kBwdThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return check_cuda(cudaGetLastError(), "pack_preference_bwd launch");
+}
+
+extern "C" pvl_status pack_policy_fwd(const pvl_policy* h, float* loss, float* stats, float* coef, void* ws,
+                                      size_t ws_bytes, pvl_stream_t stream) {
+  const char* who = "pack_policy_fwd";
+  LossParams p{};
+  pvl_status st = policy_params(who, h, &p);
+  if (st != PVL_OK) return st;
+  if (!loss || !stats || !coef) return fail(PVL_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (misaligned({loss, stats}, 4) || misaligned({coef}, 8))
+    return fail(PVL_ERR_UNSUPPORTED, "%s: loss and stats must be 4-byte and coef 8-byte aligned", who);
+  p.loss = loss;
+  p.stats = stats;
+  p.coef = coef;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = workspace(who, p, ws, ws_bytes, false, s);
+  if (st != PVL_OK) return st;
+  policy_kernel<<<blocks_of(p.N, kTokens), kThreads, 0, s>>>(p);
+  return check_cuda(cudaGetLastError(), "pack_policy_fwd launch");
+}
+
+extern "C" pvl_status pack_policy_bwd(const pvl_policy* h, const float* dloss, const float* coef, float* dlogp,
+                                      pvl_stream_t stream) {
+  const char* who = "pack_policy_bwd";
+  LossParams p{};
+  const pvl_status st = policy_params(who, h, &p);
+  if (st != PVL_OK) return st;
+  if (!coef || !dlogp) return fail(PVL_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (misaligned({dloss, dlogp}, 4) || misaligned({coef}, 8))
+    return fail(PVL_ERR_UNSUPPORTED, "%s: dloss and dlogp must be 4-byte and coef 8-byte aligned", who);
+  p.dloss = dloss;
+  p.coef = const_cast<float*>(coef);
+  p.dlogp = dlogp;
+  token_grad_kernel<true><<<blocks_of(p.N, 4 * kBwdThreads), kBwdThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return check_cuda(cudaGetLastError(), "pack_policy_bwd launch");
+}

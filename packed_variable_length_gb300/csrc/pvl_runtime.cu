@@ -296,6 +296,8 @@ extern "C" pvl_status pvl_device_error_detail(pvl_stream_t stream, int32_t* info
   if (h.code == kDevErrModId) return fail(PVL_ERR_INVALID_ARG, "a modulation id lies past the modulation tables");
   if (h.code == kDevErrModOrder)
     return fail(PVL_ERR_INVALID_ARG, "modulation ids decrease along the rows: their gradients are not separable");
+  if (h.code == kDevErrEpisode)
+    return fail(PVL_ERR_INVALID_ARG, "an episode id of a token or pair lies past the call's episodes");
   if (h.code != 0) return fail(PVL_ERR_CUDA, "unknown device error code %u", h.code);
   return PVL_OK;
 }

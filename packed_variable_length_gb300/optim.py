@@ -1,0 +1,220 @@
+"""Python binding of the parameter update: the norm of all gradients and the
+AdamW step over many tensors at once.
+
+The state of an update lives in buffers over all parameters (AdamWState); a
+step passes the addresses of parameters and gradients as kernel arguments and
+copies nothing to the device, so it can be captured into a CUDA graph.
+"""
+
+from __future__ import annotations
+
+import math
+from dataclasses import dataclass, field
+
+import numpy as np
+import torch
+
+from . import _lib
+from .api import _addr, _check, _launch, _need, _need_cuda
+
+BLOCK = 256     # elements that share a scale of the 8-bit moments
+
+# pvl_adamw_tensor of include/pvl.h
+_TENSOR = np.dtype([("param", np.uint64), ("grad", np.uint64), ("size", np.int64), ("block", np.int64),
+                    ("slot", np.int32), ("decay", np.float32)])
+_FLOATS = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _same_floats(tensors, name: str):
+    """The dtype and device that all of the list share; every tensor contiguous."""
+    dtype, dev = tensors[0].dtype, tensors[0].device
+    if dtype not in _FLOATS:
+        raise ValueError(f"{name} must be {torch.bfloat16} or {torch.float32}, got {dtype}")
+    for i, t in enumerate(tensors):
+        if t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+            _need_cuda(t, f"{name}[{i}]", dtype)
+            raise ValueError(f"{name}[{i}] is on {t.device}, not on {dev}")
+    return dtype, dev
+
+
+def grad_norm(grads, out=None, ws=None, stream=None) -> torch.Tensor:
+    """fp32 [1] device tensor: the 2-norm of all gradients together (bf16 or
+    fp32 tensors of one type; None and empty ones are skipped)."""
+    grads = [g for g in grads if g is not None and g.numel()]
+    if not grads:
+        raise ValueError("grad_norm needs a gradient")
+    dtype, dev = _same_floats(grads, "grads")
+    lib = _lib.load()
+    with _launch(dev, stream) as handle:
+        if out is None:
+            out = torch.empty(1, dtype=torch.float32, device=dev)
+        else:
+            _need(out, "out", torch.float32, (1,), dev)
+        nbytes = int(lib.pvl_grad_norm_ws_bytes())
+        if ws is None:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        else:
+            _need(ws, "ws", torch.uint8, ws.shape, dev)
+        ptrs = np.array([g.data_ptr() for g in grads], dtype=np.uint64)
+        sizes = np.array([g.numel() for g in grads], dtype=np.int64)
+        _check(lib.pvl_grad_norm(ptrs.ctypes.data, sizes.ctypes.data, len(grads), _FLOATS[dtype], out.data_ptr(),
+                                 ws.data_ptr(), ws.numel(), handle))
+    return out
+
+
+@dataclass
+class AdamWState:
+    """Moments, masters and step counts of the parameters that adamw_state was
+    given, in whole blocks of 256 elements a parameter.
+
+    bits 32: m and v are fp32.  bits 8: they are torch.float8_e4m3fn, with one
+    fp32 scale a block, and v holds the root: m = code m_scale, sqrt(v) = code
+    v_scale.  master holds bf16 parameters in fp32 (None for fp32 ones)."""
+    m: torch.Tensor
+    v: torch.Tensor
+    m_scale: torch.Tensor | None
+    v_scale: torch.Tensor | None
+    master: torch.Tensor | None
+    steps: torch.Tensor         # int32, one a parameter
+    done: torch.Tensor          # int32 [1], the kernels' own: 0 between steps
+    bits: int
+    seed: int
+    dtype: torch.dtype          # of the parameters
+    shapes: tuple
+    blocks: tuple               # first block of each parameter
+    table: np.ndarray = field(repr=False)
+
+    def _part(self, t, i: int):
+        n = math.prod(self.shapes[i])
+        return t[self.blocks[i] * BLOCK:][:n]
+
+    def moments(self, i: int):
+        """(m, v) of parameter i in fp32, of its shape."""
+        m, v = self._part(self.m, i).float(), self._part(self.v, i).float()
+        if self.bits == 8:
+            at = torch.arange(m.numel(), device=m.device) // BLOCK + self.blocks[i]
+            m, v = m * self.m_scale[at], (v * self.v_scale[at]).square()
+        return m.view(self.shapes[i]), v.view(self.shapes[i])
+
+    def masters(self, i: int):
+        """The fp32 master of bf16 parameter i: a view of its shape."""
+        return self._part(self.master, i).view(self.shapes[i])
+
+
+def adamw_state(params, *, bits: int = 32, seed: int = 0) -> AdamWState:
+    """State of AdamW for a list of parameters, all bf16 or all fp32: moments of
+    zero in 32 or 8 bits, step counts of zero and, for bf16 parameters, fp32
+    masters that start as their values.  seed chooses the random bits by which
+    8-bit moments are rounded."""
+    params = list(params)
+    if not params:
+        raise ValueError("adamw_state needs a parameter")
+    if bits not in (8, 32):
+        raise ValueError(f"bits must be 8 or 32, got {bits!r}")
+    if not 0 <= int(seed) < 1 << 32:
+        raise ValueError("seed must fit in 32 bits")
+    if params[0].device.type != "cuda":
+        raise ValueError(f"the kernels run on CUDA devices, not on {params[0].device}")
+    dtype, dev = _same_floats(params, "params")
+    _distinct([p.data_ptr() for p in params if p.numel()])
+    table = np.zeros(len(params), dtype=_TENSOR)
+    table["size"] = [p.numel() for p in params]
+    table["slot"] = np.arange(len(params))
+    counts = -(-table["size"] // BLOCK)
+    ends = np.cumsum(counts)
+    table["block"] = ends - counts
+    total = int(ends[-1])
+    moment = torch.float32 if bits == 32 else torch.uint8
+    m, v = (torch.zeros(total * BLOCK, dtype=moment, device=dev) for _ in range(2))
+    scales = (None, None)
+    if bits == 8:
+        m, v = m.view(torch.float8_e4m3fn), v.view(torch.float8_e4m3fn)
+        scales = tuple(torch.zeros(total, dtype=torch.float32, device=dev) for _ in range(2))
+    state = AdamWState(m, v, *scales, None, torch.zeros(len(params), dtype=torch.int32, device=dev),
+                       torch.zeros(1, dtype=torch.int32, device=dev), bits, int(seed), dtype,
+                       tuple(tuple(p.shape) for p in params), tuple(int(b) for b in table["block"]), table)
+    if dtype is torch.bfloat16:
+        state.master = torch.zeros(total * BLOCK, dtype=torch.float32, device=dev)
+        for i, p in enumerate(params):
+            state.masters(i).copy_(p.detach())
+    return state
+
+
+def _distinct(ptrs):
+    if len(set(ptrs)) != len(ptrs):
+        raise ValueError("a parameter stands in the list twice")
+
+
+def adamw_step(params, grads, state: AdamWState, lr, *, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01,
+               grad_norm=None, max_norm: float | None = None, stream=None) -> None:
+    """One AdamW step of `params` (the list that adamw_state was given) from
+    `grads` (bf16 or fp32, of one type, each like its parameter; None leaves
+    the parameter, its moments and its step count as they are).
+
+    lr is a number or an fp32 one-element device tensor (read when the kernel
+    runs); weight_decay a number or one a parameter, decoupled.  With grad_norm
+    (the device tensor of grad_norm()) the gradients are scaled by min(1,
+    max_norm / grad_norm), or with max_norm=None not at all, and a norm that is
+    NaN or infinite leaves everything as it is."""
+    params, grads = list(params), list(grads)
+    n = len(state.shapes)
+    if len(params) != n or len(grads) != n:
+        raise ValueError(f"the state is of {n} parameters, got {len(params)} and {len(grads)} gradients")
+    dev = state.m.device
+    if betas is None or len(betas) != 2:
+        raise ValueError("betas must be two numbers")
+    moment = torch.float32 if state.bits == 32 else torch.float8_e4m3fn
+    last = state.table[-1]
+    blocks = int(last["block"]) - (-int(last["size"]) // BLOCK)
+    for name in ("m", "v"):
+        _need(getattr(state, name), f"state.{name}", moment, (blocks * BLOCK,), dev)
+        if state.bits == 8:
+            _need(getattr(state, name + "_scale"), f"state.{name}_scale", torch.float32, (blocks,), dev)
+    if state.dtype is torch.bfloat16:
+        _need(state.master, "state.master", torch.float32, (blocks * BLOCK,), dev)
+    _need(state.steps, "state.steps", torch.int32, (n,), dev)
+    _need(state.done, "state.done", torch.int32, (1,), dev)
+    if grad_norm is not None:
+        _need(grad_norm, "grad_norm", torch.float32, (1,), dev)
+    elif max_norm is not None:
+        raise ValueError("max_norm needs grad_norm")
+    lr_dev = None
+    if isinstance(lr, torch.Tensor):
+        if lr.numel() != 1:
+            raise ValueError("lr must hold one element")
+        _need(lr, "lr", torch.float32, lr.shape, dev)
+        lr, lr_dev = 0.0, lr
+    kind = None
+    use = []
+    for i, (p, g, shape) in enumerate(zip(params, grads, state.shapes)):
+        if p.dtype is not state.dtype or p.device != dev or p.shape != shape or not p.is_contiguous():
+            _need(p, f"params[{i}]", state.dtype, shape, dev)
+        if g is None or not p.numel():
+            continue
+        kind = g.dtype if kind is None else kind
+        if kind not in _FLOATS:
+            raise ValueError(f"grads[{i}] must be {torch.bfloat16} or {torch.float32}, got {kind}")
+        if g.dtype is not kind or g.device != dev or g.shape != shape or not g.is_contiguous():
+            _need(g, f"grads[{i}]", kind, shape, dev)
+        use.append(i)
+    if not use:
+        return
+    table = state.table if len(use) == n else state.table[use]
+    table["param"] = [params[i].data_ptr() for i in use]
+    table["grad"] = [grads[i].data_ptr() for i in use]
+    _distinct(table["param"].tolist())
+    if isinstance(weight_decay, (int, float)):
+        table["decay"] = weight_decay
+    else:
+        decay = [float(d) for d in weight_decay]
+        if len(decay) != n:
+            raise ValueError(f"weight_decay must be a number or {n} of them")
+        table["decay"] = [decay[i] for i in use]
+    how = _lib.PACK_ADAMW(_FLOATS[state.dtype], _FLOATS[kind], state.bits, state.seed, float(betas[0]),
+                          float(betas[1]), float(lr), float(eps), math.inf if max_norm is None else float(max_norm),
+                          _addr(lr_dev), _addr(grad_norm), state.m.data_ptr(), state.v.data_ptr(),
+                          _addr(state.m_scale), _addr(state.v_scale), _addr(state.master), state.steps.data_ptr(),
+                          state.done.data_ptr())
+    with _launch(dev, stream) as handle:
+        _check(_lib.load().pvl_adamw_step(how, table.ctypes.data, len(use), handle))
+    torch.autograd.graph.increment_version([params[i] for i in use])
