@@ -206,7 +206,7 @@ def test_offsets_past_32_bits(pvl):
     g = torch.Generator(device="cuda").manual_seed(12)
     x[0, -3:] = torch.randn(3, V, generator=g, device="cuda").bfloat16() * 4
     t[0, -3:] = torch.tensor([5, 100, V - 1], dtype=torch.int32)
-    tail_x, tail_t = x[:, -3:].contiguous(), t[:, -3:].contiguous()
+    tail_x, tail_t = x[:, -3:].clone(), t[:, -3:].clone()     # x is overwritten below
     logp, lse, h, d = check(pvl, tail_x, tail_t)
     a, b, c = pvl.pack_logprob_fwd(x, t, entropy=True)
     # three rows go to a cluster each, many to a block each: other orders of the same sums
