@@ -701,7 +701,8 @@ PVL_API pvl_status pvl_grad_norm(const void* const* grads, const int64_t* sizes,
  *   are not read; null for fp32 parameters.
  * steps: dev int32; done: dev uint32 that is 0 before the first step (the
  *   library leaves it so); lr_dev: dev fp32 [1] or null (then lr).  m, v,
- *   master 16-byte aligned.  Steps that share states must follow one another.
+ *   master 32-byte aligned.  Steps that share states must follow one another.
+ *   eps is at least 1e-30.
  * Errors: INVALID_ARG for null pointers, counts, sizes, types, bits or
  * parameters outside their range; UNSUPPORTED for tensors of 2^38 elements and
  * more, or alignment.

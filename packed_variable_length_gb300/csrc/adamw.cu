@@ -24,9 +24,10 @@
 //
 // Bound by HBM: 16 bytes a parameter and step at least (bf16 parameter and
 // gradient, fp32 master, 8-bit moments), 28 with 32-bit moments.  A warp takes
-// a block, eight elements a lane, all its loads issued before the first is
-// used; the tables of tensors come as kernel parameters, so a step copies
-// nothing to the device and can be captured.  A tensor's step count is on the
+// a block at a time, eight elements a lane, all its loads issued before the
+// first is used, and arithmetic in packed pairs; the tables of tensors come as
+// kernel parameters, so a step copies nothing to the device and can be
+// captured.  A tensor's step count is on the
 // device and counted up by the last block of the grid to finish, when all have
 // read it.
 #include <cuda_fp8.h>
@@ -44,15 +45,17 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBlock = 256;        // elements that share a scale
 constexpr int kFew = 32, kMany = 512;  // tensors of a launch
 constexpr float kTop = 448.0f;     // largest e4m3 value
-constexpr int kNormUnit = 2048;    // elements a warp takes at a time for the norm
+constexpr int kNormUnit = 1024;    // elements a warp takes at a time for the norm
 constexpr int kMaxNormCtas = 4096;
 
+// Tensors of a launch.  A chunk is 2^shift blocks of a tensor (its last may be
+// shorter), what a warp takes at a time.
 template <int kT>
 struct Tensors {
-  uint32_t start[kT + 1];  // running count of blocks
+  uint32_t start[kT + 1];  // running count of chunks
   int32_t slot[kT];        // place in the step counts
   float decay[kT];
-  int32_t n;
+  int32_t n, shift;
   void* param[kT];
   const void* grad[kT];
   long long size[kT];
@@ -73,7 +76,7 @@ struct StepParams {
   unsigned int* done;
 };
 
-// Loads and stores that pass through once.
+// Loads that pass through once.
 __device__ __forceinline__ uint4 ld16(const void* p) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -89,43 +92,68 @@ __device__ __forceinline__ uint2 ld8(const void* p) {
   return v;
 }
 
-// Eight elements: 32 bytes of fp32, 16 of bf16.
+// Eight elements: 32 bytes of fp32, 16 of bf16.  32 bytes on their boundary move
+// in one instruction, a whole sector a lane; two of 16 with half a sector each
+// reached 79 % of the copy rate where this reaches more.
 struct Eight {
-  uint4 a, b;
+  uint32_t w[8];
 };
 
-template <typename T>
-__device__ __forceinline__ Eight load8(const T* p) {
+__device__ __forceinline__ Eight ld32(const void* p) {
   Eight e;
-  e.a = ld16(p);
-  if constexpr (sizeof(T) == 4) e.b = ld16(p + 4);
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(e.w[0]), "=r"(e.w[1]), "=r"(e.w[2]), "=r"(e.w[3]), "=r"(e.w[4]), "=r"(e.w[5]), "=r"(e.w[6]),
+                 "=r"(e.w[7])
+               : "l"(p)
+               : "memory");
   return e;
 }
 
-template <typename T>
-__device__ __forceinline__ void open8(const Eight& e, float (&f)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    const uint32_t w[8] = {e.a.x, e.a.y, e.a.z, e.a.w, e.b.x, e.b.y, e.b.z, e.b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+__device__ __forceinline__ void st32(void* p, const float (&f)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0]), "f"(f[1]), "f"(f[2]),
+               "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+               : "memory");
+}
+
+// kBy: what the address is a multiple of, for fp32 (16 or 32).
+template <typename T, int kBy>
+__device__ __forceinline__ Eight load8(const T* p) {
+  if constexpr (sizeof(T) == 4 && kBy == 32) {
+    return ld32(p);
   } else {
-    const uint32_t w[4] = {e.a.x, e.a.y, e.a.z, e.a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    Eight e;
+    const uint4 a = ld16(p);
+    e.w[0] = a.x, e.w[1] = a.y, e.w[2] = a.z, e.w[3] = a.w;
+    if constexpr (sizeof(T) == 4) {
+      const uint4 b = ld16(p + 4);
+      e.w[4] = b.x, e.w[5] = b.y, e.w[6] = b.z, e.w[7] = b.w;
     }
+    return e;
   }
 }
 
 template <typename T>
+__device__ __forceinline__ void open8(const Eight& e, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      f[i] = __uint_as_float(e.w[i]);
+    } else {
+      f[i] = __uint_as_float(i % 2 ? e.w[i / 2] & 0xFFFF0000u : e.w[i / 2] << 16);
+    }
+  }
+}
+
+template <typename T, int kBy>
 __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
-    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
+  if constexpr (sizeof(T) == 4 && kBy == 32) {
+    st32(p, f);
+  } else if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    *(reinterpret_cast<float4*>(p) + 1) = make_float4(f[4], f[5], f[6], f[7]);
   } else {
-    __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                                   pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                              pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
   }
 }
 
@@ -139,6 +167,18 @@ template <typename T>
 __device__ __forceinline__ void load_some(const T* p, int n, float (&f)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = i < n ? wide(p[i]) : 0.0f;
+}
+
+__device__ __forceinline__ float root_of(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float inverse(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // ------------------------------------------------------------- 8 bits
@@ -163,10 +203,8 @@ __device__ __forceinline__ uint32_t chance(uint32_t h) {
 // x in [0, 448] down to three fraction bits after `r` of 2^20 parts of a step
 // are added.  Below 2^-6 steps are 2^-9 throughout, as those of [2^-6, 2^-5).
 __device__ __forceinline__ float round_e4m3(float x, uint32_t r) {
-  const bool low = x < 0.015625f;
-  const float y = low ? x + 0.015625f : x;
-  const float q = __uint_as_float((__float_as_uint(y) + r) & 0xFFF00000u);
-  return low ? q - 0.015625f : q;
+  const float shift = x < 0.015625f ? 0.015625f : 0.0f;
+  return __uint_as_float((__float_as_uint(x + shift) + r) & 0xFFF00000u) - shift;
 }
 
 __device__ __forceinline__ void open_e4m3(uint2 q, float scale, float (&f)[8]) {
@@ -190,25 +228,121 @@ __device__ __forceinline__ uint2 close_e4m3(const float (&f)[8]) {
   return make_uint2(w[0], w[1]);
 }
 
-// Largest magnitude of a block; NaN is larger than all.
+// Largest magnitude of a block (NaN aside).
 __device__ __forceinline__ float block_top(const float (&f)[8]) {
-  uint32_t top = 0;
+  float top = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7FFFFFFFu);
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, top));
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
 }
 
 // ---------------------------------------------------------------- step
+// What a chunk's elements share.
+struct Shared {
+  float clip, rate, second, keep;
+  uint32_t key;
+};
+
+// One block: this lane's eight elements, n of which are the tensor's (kBy: all
+// eight, and the fp32 addresses are multiples of kBy).
+template <typename P, typename G, bool k8, int kBy>
+__device__ __forceinline__ void step_block(const StepParams& p, const Shared& c, P* param, const G* grad, long long sb,
+                                           int n) {
+  constexpr bool kMaster = sizeof(P) == 2;
+  const int lane = threadIdx.x % 32;
+  const long long st = sb * kBlock + lane * 8;
+  Eight qg, qp, qm, qv;
+  uint2 cm, cv;
+  float sm = 0.0f, sv = 0.0f;
+  if constexpr (kBy != 0) qg = load8<G, kBy>(grad);
+  if constexpr (kMaster) qp = ld32(p.master + st);
+  else if constexpr (kBy != 0) qp = load8<P, kBy>(param);
+  if constexpr (k8) {
+    cm = ld8(static_cast<const uint8_t*>(p.m) + st);
+    cv = ld8(static_cast<const uint8_t*>(p.v) + st);
+    sm = p.m_scale[sb];
+    sv = p.v_scale[sb];
+  } else {
+    qm = ld32(static_cast<const float*>(p.m) + st);
+    qv = ld32(static_cast<const float*>(p.v) + st);
+  }
+  float g[8], w[8], m[8], v[8], root[8];
+  if constexpr (kBy != 0) open8<G>(qg, g);
+  else load_some(grad, n, g);
+  if constexpr (kMaster) open8<float>(qp, w);
+  else if constexpr (kBy != 0) open8<P>(qp, w);
+  else load_some(param, n, w);
+  if constexpr (k8) {
+    open_e4m3(cm, sm, m);
+    open_e4m3(cv, sv, v);
+  } else {
+    open8<float>(qm, m);
+    open8<float>(qv, v);
+  }
+  const float2 b1 = make_float2(p.b1, p.b1), c1 = make_float2(p.c1, p.c1), b2 = make_float2(p.b2, p.b2),
+               c2 = make_float2(p.c2, p.c2), clip = make_float2(c.clip, c.clip), second = make_float2(c.second, c.second),
+               eps = make_float2(p.eps, p.eps), rate = make_float2(-c.rate, -c.rate), keep = make_float2(c.keep, c.keep);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float2 gc = fmul2(make_float2(g[i], g[i + 1]), clip);
+    const float2 mm = ffma2(b1, make_float2(m[i], m[i + 1]), fmul2(c1, gc));
+    float2 vv = make_float2(v[i], v[i + 1]);
+    if constexpr (k8) vv = fmul2(vv, vv);
+    vv = ffma2(fmul2(c2, gc), gc, fmul2(b2, vv));
+    const float2 r = make_float2(root_of(vv.x), root_of(vv.y));
+    const float2 d = ffma2(r, second, eps);
+    const float2 q = fmul2(mm, make_float2(inverse(d.x), inverse(d.y)));
+    const float2 ww = ffma2(make_float2(w[i], w[i + 1]), keep, fmul2(rate, q));
+    m[i] = mm.x, m[i + 1] = mm.y;
+    v[i] = vv.x, v[i + 1] = vv.y;
+    root[i] = r.x, root[i + 1] = r.y;
+    w[i] = ww.x, w[i + 1] = ww.y;
+  }
+  if constexpr (kMaster) st32(p.master + st, w);
+  if constexpr (kBy != 0) {
+    store8<P, kBy>(param, w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) narrow(param + i, w[i]);
+  }
+  if constexpr (k8) {
+    const float tm = block_top(m), tv = block_top(root);
+    // a block below 2^-100 becomes zeros: its scale would not be a normal number
+    const float im = tm < 0x1p-100f ? 0.0f : kTop * inverse(tm), iv = tv < 0x1p-100f ? 0.0f : kTop * inverse(tv);
+    const uint32_t h = mix((static_cast<uint32_t>(sb) * 32u + lane) ^ c.key);
+    const uint32_t rm[8] = {chance<1>(h), chance<2>(h), chance<3>(h), chance<4>(h),
+                            chance<5>(h), chance<6>(h), chance<7>(h), chance<8>(h)};
+    const uint32_t rv[8] = {chance<9>(h), chance<10>(h), chance<11>(h), chance<12>(h),
+                            chance<13>(h), chance<14>(h), chance<15>(h), chance<16>(h)};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      m[i] = copysignf(round_e4m3(fabsf(m[i]) * im, rm[i]), m[i]);
+      const float x = root[i] * iv;
+      v[i] = x > 0.0f ? fmaxf(round_e4m3(x, rv[i]), 0.001953125f) : x;
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.m) + st) = close_e4m3(m);
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.v) + st) = close_e4m3(v);
+    if (lane == 0) {
+      p.m_scale[sb] = tm < 0x1p-100f ? 0.0f : tm * (1.0f / kTop);
+      p.v_scale[sb] = tv < 0x1p-100f ? 0.0f : tv * (1.0f / kTop);
+    }
+  } else {
+    st32(static_cast<float*>(p.m) + st, m);
+    st32(static_cast<float*>(p.v) + st, v);
+  }
+}
+
 template <typename P, typename G, bool k8, int kT>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Tensors<kT> tab,
                                                          const __grid_constant__ StepParams p) {
-  constexpr bool kMaster = sizeof(P) == 2;
   const int lane = threadIdx.x % 32;
-  float clip = 1.0f;
+  Shared c;
+  c.clip = 1.0f;
   if (p.norm) {
     const float norm = __ldg(p.norm);
     if (!(norm < INFINITY)) return;  // NaN or infinite gradients: no step, the same for the whole grid
-    clip = norm > p.max_norm ? p.max_norm / norm : 1.0f;
+    c.clip = norm > p.max_norm ? p.max_norm / norm : 1.0f;
   }
   const float lr = p.lr_dev ? __ldg(p.lr_dev) : p.lr;
   const uint32_t total = tab.start[tab.n];
@@ -222,105 +356,35 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     }
   }
   int32_t step = -1;
-  float rate = 0.0f, second = 0.0f;
-  uint32_t key = 0;
   for (; u < total; u += gridDim.x * kWarps) {
     while (u >= tab.start[t + 1]) ++t;
-    const uint32_t b = u - tab.start[t];
-    const long long at = static_cast<long long>(b) * kBlock + lane * 8;       // in the tensor
-    const long long sb = tab.block[t] + b;                                    // block of the states
-    const long long st = sb * kBlock + lane * 8;
-    P* param = static_cast<P*>(tab.param[t]) + at;
-    const G* grad = static_cast<const G*>(tab.grad[t]) + at;
-    const long long left = tab.size[t] - at;
-    const int n = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
-    const bool whole = n == 8 && (reinterpret_cast<uintptr_t>(param) | reinterpret_cast<uintptr_t>(grad)) % 16 == 0;
-
-    Eight qg, qp, qm, qv;
-    uint2 cm, cv;
-    float sm = 0.0f, sv = 0.0f;
-    if (whole) qg = load8(grad);
-    if constexpr (kMaster) {
-      qp = load8(p.master + st);
-    } else if (whole) {
-      qp = load8(param);
-    }
-    if constexpr (k8) {
-      cm = ld8(static_cast<const uint8_t*>(p.m) + st);
-      cv = ld8(static_cast<const uint8_t*>(p.v) + st);
-      sm = p.m_scale[sb];
-      sv = p.v_scale[sb];
-    } else {
-      qm = load8(static_cast<const float*>(p.m) + st);
-      qv = load8(static_cast<const float*>(p.v) + st);
-    }
+    const long long b = static_cast<long long>(u - tab.start[t]) << tab.shift;  // block of the tensor
+    long long sb = tab.block[t] + b;                                           // block of the states
+    P* param = static_cast<P*>(tab.param[t]) + b * kBlock + lane * 8;
+    const G* grad = static_cast<const G*>(tab.grad[t]) + b * kBlock + lane * 8;
+    long long left = tab.size[t] - b * kBlock;
     const int32_t now = p.steps[tab.slot[t]] + 1;
     if (now != step) {
       step = now;
       const float s = static_cast<float>(now);
-      rate = lr / -expm1f(s * p.log_b1);
-      second = rsqrtf(-expm1f(s * p.log_b2));
-      key = mix(p.seed + static_cast<uint32_t>(now) * 0x9E3779B9u);
+      c.rate = lr / -expm1f(s * p.log_b1);
+      c.second = rsqrtf(-expm1f(s * p.log_b2));
+      c.key = mix(p.seed + static_cast<uint32_t>(now) * 0x9E3779B9u);
     }
-    float g[8], w[8], m[8], v[8], root[8];
-    if (whole) open8<G>(qg, g);
-    else load_some(grad, n, g);
-    if constexpr (kMaster) {
-      open8<float>(qp, w);
-    } else {
-      if (whole) open8<P>(qp, w);
-      else load_some(param, n, w);
+    c.keep = 1.0f - lr * tab.decay[t];
+    const uintptr_t where = reinterpret_cast<uintptr_t>(param) | reinterpret_cast<uintptr_t>(grad);
+    constexpr uintptr_t kSector = sizeof(P) == 4 || sizeof(G) == 4 ? 32 : 16;
+    if (left >= (static_cast<long long>(kBlock) << tab.shift) && where % kSector == 0) {
+      for (int j = 0; j < 1 << tab.shift; ++j, param += kBlock, grad += kBlock, ++sb)
+        step_block<P, G, k8, 32>(p, c, param, grad, sb, 8);
+      continue;
     }
-    if constexpr (k8) {
-      open_e4m3(cm, sm, m);
-      open_e4m3(cv, sv, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= v[i];
-    } else {
-      open8<float>(qm, m);
-      open8<float>(qv, v);
-    }
-    const float keep = 1.0f - lr * tab.decay[t];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float gc = g[i] * clip;
-      m[i] = fmaf(p.b1, m[i], p.c1 * gc);
-      v[i] = fmaf(p.b2, v[i], p.c2 * gc * gc);
-      root[i] = sqrtf(v[i]);
-      w[i] = fmaf(w[i], keep, -rate * __fdividef(m[i], fmaf(root[i], second, p.eps)));
-    }
-    if constexpr (kMaster) store8(p.master + st, w);
-    if (whole) {
-      store8(param, w);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) narrow(param + i, w[i]);
-    }
-    if constexpr (k8) {
-      const float tm = block_top(m), tv = block_top(root);
-      // a block below 2^-100 becomes zeros: its scale would not be a normal number
-      const float im = tm < 0x1p-100f ? 0.0f : kTop / tm, iv = tv < 0x1p-100f ? 0.0f : kTop / tv;
-      const uint32_t h = mix((static_cast<uint32_t>(sb) * 32u + lane) ^ key);
-      const uint32_t rm[8] = {chance<1>(h), chance<2>(h), chance<3>(h), chance<4>(h),
-                              chance<5>(h), chance<6>(h), chance<7>(h), chance<8>(h)};
-      const uint32_t rv[8] = {chance<9>(h), chance<10>(h), chance<11>(h), chance<12>(h),
-                              chance<13>(h), chance<14>(h), chance<15>(h), chance<16>(h)};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        m[i] = copysignf(round_e4m3(fabsf(m[i]) * im, rm[i]), m[i]);
-        const float x = root[i] * iv;
-        v[i] = x > 0.0f ? fmaxf(round_e4m3(x, rv[i]), 0.001953125f) : x;
-      }
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.m) + st) = close_e4m3(m);
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.v) + st) = close_e4m3(v);
-      if (lane == 0) {
-        p.m_scale[sb] = tm < 0x1p-100f ? 0.0f : tm / kTop;
-        p.v_scale[sb] = tv < 0x1p-100f ? 0.0f : tv / kTop;
-      }
-    } else {
-      store8(static_cast<float*>(p.m) + st, m);
-      store8(static_cast<float*>(p.v) + st, v);
+    for (int j = 0; j < 1 << tab.shift && left > 0; ++j, param += kBlock, grad += kBlock, ++sb, left -= kBlock) {
+      const long long mine = left - lane * 8;
+      if (kSector == 32 && left >= kBlock && where % 16 == 0)
+        step_block<P, G, k8, 16>(p, c, param, grad, sb, 8);
+      else
+        step_block<P, G, k8, 0>(p, c, param, grad, sb, mine >= 8 ? 8 : mine > 0 ? static_cast<int>(mine) : 0);
     }
   }
   // every block has read the step counts once it has counted itself
@@ -353,57 +417,45 @@ struct NormParams {
   float* norm;
 };
 
-// A lane's 64 elements of a unit: eight vectors of eight, a warp's vectors side
-// by side.  Squares are added in fp32; a sum that overflows, or that is so small
-// that squares may have been lost below the normal numbers, is taken again in
-// 64 bits.
+// A lane's 32 elements of a unit: four vectors of eight, a warp's vectors side
+// by side.  Squares are added in fp32, even and odd elements apart; a sum that
+// overflows, or that is so small that squares may have been lost below the
+// normal numbers, is taken again in 64 bits.
+template <typename G>
+__device__ __noinline__ double unit_again(const G* grad, int n) {
+  double d = 0.0;
+  for (int i = threadIdx.x % 32; i < n; i += 32) {
+    const float f = wide(grad[i]);
+    if (f != 0.0f) d = fma(static_cast<double>(f), static_cast<double>(f), d);  // zeros cost nothing
+  }
+  return d;
+}
+
 template <typename G>
 __device__ __forceinline__ double unit_squares(const G* grad, long long left) {
   const int lane = threadIdx.x % 32;
-  const bool aligned = reinterpret_cast<uintptr_t>(grad) % 16 == 0;
-  Eight q[8];
-  const bool whole = aligned && left >= kNormUnit;
-  float s = 0.0f;
-  if (whole) {
+  float2 s = make_float2(0.0f, 0.0f);
+  if (left >= kNormUnit && reinterpret_cast<uintptr_t>(grad) % (8 * sizeof(G)) == 0) {
+    Eight q[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = load8(grad + (i * 32 + lane) * 8);
+    for (int i = 0; i < 4; ++i) q[i] = load8<G, 32>(grad + (i * 32 + lane) * 8);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
       float f[8];
       open8<G>(q[i], f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s = fmaf(f[j], f[j], s);
+      for (int j = 0; j < 8; j += 2) s = ffma2(make_float2(f[j], f[j + 1]), make_float2(f[j], f[j + 1]), s);
     }
   } else {
     for (int i = lane; i < kNormUnit && i < left; i += 32) {
       const float f = wide(grad[i]);
-      s = fmaf(f, f, s);
+      s.x = fmaf(f, f, s.x);
     }
   }
-  if (s > 0x1p-60f && s < INFINITY) return static_cast<double>(s);
-  double d = 0.0;
-  if (whole) {
-    uint32_t any = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      any |= q[i].a.x | q[i].a.y | q[i].a.z | q[i].a.w;
-      if constexpr (sizeof(G) == 4) any |= q[i].b.x | q[i].b.y | q[i].b.z | q[i].b.w;
-    }
-    if ((any & (sizeof(G) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) == 0) return 0.0;  // zeros of either sign
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float f[8];
-      open8<G>(q[i], f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) d = fma(static_cast<double>(f[j]), static_cast<double>(f[j]), d);
-    }
-  } else {
-    for (int i = lane; i < kNormUnit && i < left; i += 32) {
-      const double f = static_cast<double>(wide(grad[i]));
-      d = fma(f, f, d);
-    }
-  }
-  return d;
+  const float sum = s.x + s.y;
+  // the warp's lanes take other elements in unit_again than here: all or none
+  if (__all_sync(0xffffffffu, sum > 0x1p-60f && sum < INFINITY)) return static_cast<double>(sum);
+  return unit_again(grad, left < kNormUnit ? static_cast<int>(left) : kNormUnit);
 }
 
 __device__ double block_sum(double v) {
@@ -455,32 +507,46 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
 }
 
 // ---------------------------------------------------------------- host
+long long blocks_of(long long n) { return (n + kBlock - 1) / kBlock; }
+
+// Chunks of four blocks once there are as many as warps that fit the device:
+// what a chunk looks up is then shared by 1024 elements.  Fewer blocks than that
+// are spread over as many warps as there are.
+constexpr int kChunkShift = 2;
+
 template <typename P, typename G, bool k8, int kT>
-pvl_status launch_step(const Tensors<kT>& tab, const StepParams& p, int sms, cudaStream_t s) {
+pvl_status launch_step(Tensors<kT>& tab, const StepParams& p, int sms, cudaStream_t s) {
   const void* fn = reinterpret_cast<const void*>(adamw_kernel<P, G, k8, kT>);
   const int fit = blocks_per_sm(fn, kThreads, 0);
   if (fit < 1) return fail(PVL_ERR_CUDA, "pvl_adamw_step: the kernel does not fit on an SM");
-  const long long need = (static_cast<long long>(tab.start[tab.n]) + kWarps - 1) / kWarps;
   const long long most = static_cast<long long>(fit) * sms;
+  long long blocks = 0;
+  for (int i = 0; i < tab.n; ++i) blocks += blocks_of(tab.size[i]);
+  tab.shift = blocks >= most * kWarps << kChunkShift ? kChunkShift : 0;
+  long long chunks = 0;
+  for (int i = 0; i < tab.n; ++i) {
+    tab.start[i] = static_cast<uint32_t>(chunks);
+    chunks += (blocks_of(tab.size[i]) + (1 << tab.shift) - 1) >> tab.shift;
+  }
+  tab.start[tab.n] = static_cast<uint32_t>(chunks);
+  const long long need = (chunks + kWarps - 1) / kWarps;
   adamw_kernel<P, G, k8, kT><<<static_cast<unsigned>(need < most ? need : most), kThreads, 0, s>>>(tab, p);
   return check_cuda(cudaGetLastError(), "pvl_adamw_step launch");
 }
 
 template <typename P, typename G, int kT>
-pvl_status step_bits(int bits, const Tensors<kT>& tab, const StepParams& p, int sms, cudaStream_t s) {
+pvl_status step_bits(int bits, Tensors<kT>& tab, const StepParams& p, int sms, cudaStream_t s) {
   return bits == 8 ? launch_step<P, G, true, kT>(tab, p, sms, s) : launch_step<P, G, false, kT>(tab, p, sms, s);
 }
 
 template <int kT>
-pvl_status step_types(const pvl_adamw* h, const Tensors<kT>& tab, const StepParams& p, int sms, cudaStream_t s) {
+pvl_status step_types(const pvl_adamw* h, Tensors<kT>& tab, const StepParams& p, int sms, cudaStream_t s) {
   if (h->param_dtype == 0)
     return h->grad_dtype == 0 ? step_bits<__nv_bfloat16, __nv_bfloat16, kT>(h->bits, tab, p, sms, s)
                               : step_bits<__nv_bfloat16, float, kT>(h->bits, tab, p, sms, s);
   return h->grad_dtype == 0 ? step_bits<float, __nv_bfloat16, kT>(h->bits, tab, p, sms, s)
                             : step_bits<float, float, kT>(h->bits, tab, p, sms, s);
 }
-
-long long blocks_of(long long n) { return (n + kBlock - 1) / kBlock; }
 
 // Tensors first.. of the list, as many as a launch takes: kT of them, and fewer
 // than 2^31 blocks.  Returns how many.
@@ -490,17 +556,15 @@ int fill(const pvl_adamw_tensor* list, int first, int count, Tensors<kT>* tab) {
   long long blocks = 0;
   for (; n < kT && first + n < count; ++n) {
     const pvl_adamw_tensor& q = list[first + n];
-    if (blocks + blocks_of(q.size) >= (1ll << 31)) break;
-    tab->start[n] = static_cast<uint32_t>(blocks);
+    blocks += blocks_of(q.size);
+    if (blocks >= (1ll << 31)) break;
     tab->param[n] = q.param;
     tab->grad[n] = q.grad;
     tab->size[n] = q.size;
     tab->block[n] = q.block;
     tab->slot[n] = q.slot;
     tab->decay[n] = q.decay;
-    blocks += blocks_of(q.size);
   }
-  tab->start[n] = static_cast<uint32_t>(blocks);
   tab->n = n;
   return n;
 }
@@ -564,14 +628,15 @@ extern "C" pvl_status pvl_adamw_step(const pvl_adamw* h, const pvl_adamw_tensor*
   if (!h->lr_dev && !(fabsf(h->lr) < 1e30f)) return fail(PVL_ERR_INVALID_ARG, "%s: lr must be finite", who);
   if (!(h->beta1 >= 0.0 && h->beta1 < 1.0 && h->beta2 >= 0.0 && h->beta2 < 1.0))
     return fail(PVL_ERR_INVALID_ARG, "%s: betas lie in [0, 1)", who);
-  if (!(h->eps > 0.0f && h->eps < 1e30f)) return fail(PVL_ERR_INVALID_ARG, "%s: eps must be positive and finite", who);
+  if (!(h->eps >= 1e-30f && h->eps < 1e30f))
+    return fail(PVL_ERR_INVALID_ARG, "%s: eps must be at least 1e-30 and finite", who);
   if (h->norm && !(h->max_norm > 0.0f)) return fail(PVL_ERR_INVALID_ARG, "%s: max_norm must be positive", who);
-  const uintptr_t wide16 = reinterpret_cast<uintptr_t>(h->m) | reinterpret_cast<uintptr_t>(h->v) |
+  const uintptr_t wide32 = reinterpret_cast<uintptr_t>(h->m) | reinterpret_cast<uintptr_t>(h->v) |
                            reinterpret_cast<uintptr_t>(h->master);
   const uintptr_t wide4 = reinterpret_cast<uintptr_t>(h->m_scale) | reinterpret_cast<uintptr_t>(h->v_scale) |
                           reinterpret_cast<uintptr_t>(h->steps) | reinterpret_cast<uintptr_t>(h->done) |
                           reinterpret_cast<uintptr_t>(h->lr_dev) | reinterpret_cast<uintptr_t>(h->norm);
-  if (wide16 % 16 || wide4 % 4) return fail(PVL_ERR_UNSUPPORTED, "%s: states must be 16-byte aligned", who);
+  if (wide32 % 32 || wide4 % 4) return fail(PVL_ERR_UNSUPPORTED, "%s: m, v and master must be 32-byte aligned", who);
   for (int i = 0; i < count; ++i) {
     const pvl_adamw_tensor& q = list[i];
     if (!q.param || !q.grad) return fail(PVL_ERR_INVALID_ARG, "%s: tensor %d has a null pointer", who, i);

@@ -20,9 +20,10 @@
 // or to a block; where rows are so few that a block each leaves SMs idle, to a
 // cluster of eight blocks that join their states through shared memory.
 //
-// Backward: elementwise, given lse and H: V elements read, V written.  A warp
-// takes a segment of 128 vectors of a row; rows of fewer than eight segments
-// go to a warp each.
+// Backward: elementwise, given lse and H: V elements read, V written.  A block
+// takes up to 4096 vectors of a row, so that what it looks up of the row is
+// shared by sixteen vectors a thread, the next four read while four are worked
+// on; rows of up to 512 vectors go to a warp each.
 //
 // Rows need no alignment: the elements up to the first 16-byte boundary and
 // those after the last whole vector go one by one.
@@ -40,7 +41,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFar = -1e30f;  // stands for -inf where it is multiplied by 0
 constexpr int kCluster = 8;
-constexpr int kSegVec = 128;  // vectors of a backward segment: four a lane
+constexpr int kSegVec = 16 * kThreads;  // vectors of a row that a backward block takes: sixteen a thread
 
 struct LogprobParams {
   const void* x;
@@ -63,12 +64,6 @@ struct LogprobParams {
   void* dx;
   int64_t db, dl;
 };
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // Not through the read-only path: the gradient may be written over the logits.
 __device__ __forceinline__ uint4 ld_once(const void* p) {
@@ -305,57 +300,66 @@ __device__ __forceinline__ float grad_of(float x, float inv_t, const RowGrad& g)
   return -pr * up;
 }
 
-// One warp: vectors first, first + 32, first + 64, first + 96 (lane by lane) of the row.
-template <typename T, bool kEnt, bool kSame>
-__device__ __forceinline__ void grad_segment(const LogprobParams& p, const RowGrad& g, const T* x, T* dx, int head,
-                                             int nvec, int first) {
+// Four vectors i, i + step, ... of a row: their logits.
+template <typename T, bool kSame>
+__device__ __forceinline__ void load_vectors(const T* x, int i, int step, int end, uint4 (&q)[4]) {
   constexpr int kN = Vec<T>::n;
-  const int lane = threadIdx.x % 32;
-  uint4 q[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const int i = first + u * 32 + lane;
-    if (i >= nvec || g.target < 0) continue;
+    if (i + u * step >= end) continue;
+    const T* at = x + static_cast<int64_t>(i + u * step) * kN;
     if (kSame) {
-      q[u] = ld_once(x + head + static_cast<int64_t>(i) * kN);
+      q[u] = ld_once(at);
     } else {  // the rows lie differently to the 16-byte boundaries: vectors of dx, elements of x
       float f[kN];
 #pragma unroll
-      for (int e = 0; e < kN; ++e) f[e] = Vec<T>::one(x + head + static_cast<int64_t>(i) * kN + e);
+      for (int e = 0; e < kN; ++e) f[e] = Vec<T>::one(at + e);
       q[u] = Vec<T>::close(f);
     }
   }
+}
+
+// Vectors first, first + step, ... below end of a row (x, dx: its first whole
+// vector of dx), the next four read while these are worked on.
+template <typename T, bool kEnt, bool kSame>
+__device__ __forceinline__ void grad_vectors(const RowGrad& g, float inv_t, const T* x, T* dx, int target, int first,
+                                             int step, int end) {
+  constexpr int kN = Vec<T>::n;
+  uint4 q[4], next[4];
+  load_vectors<T, kSame>(x, first, step, end, q);
+  for (int i = first; i < end; i += 4 * step) {
+    load_vectors<T, kSame>(x, i + 4 * step, step, end, next);
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int i = first + u * 32 + lane;
-    if (i >= nvec) continue;
-    float f[kN];
-    if (g.target < 0) {
-#pragma unroll
-      for (int e = 0; e < kN; ++e) f[e] = 0.0f;
-    } else {
+    for (int u = 0; u < 4; ++u) {
+      const int at = i + u * step;
+      if (at >= end) continue;
+      float f[kN];
       Vec<T>::open(q[u], f);
 #pragma unroll
-      for (int e = 0; e < kN; ++e) f[e] = grad_of<kEnt>(f[e], p.inv_t, g);
-      const int at = g.target - head - i * kN;
-      if (at >= 0 && at < kN) {
+      for (int e = 0; e < kN; ++e) f[e] = grad_of<kEnt>(f[e], inv_t, g);
+      const int here = target - at * kN;
+      if (here >= 0 && here < kN) {
 #pragma unroll
-        for (int e = 0; e < kN; ++e) f[e] += e == at ? g.up : 0.0f;
+        for (int e = 0; e < kN; ++e) f[e] += e == here ? g.up : 0.0f;
       }
+      *reinterpret_cast<uint4*>(dx + static_cast<int64_t>(at) * kN) = Vec<T>::close(f);
     }
-    __stcs(reinterpret_cast<uint4*>(dx + head + static_cast<int64_t>(i) * kN), Vec<T>::close(f));
+#pragma unroll
+    for (int u = 0; u < 4; ++u) q[u] = next[u];
   }
 }
 
-// per_row: blocks of a row (its segments go eight to a block), or 0: a warp
-// takes a whole row.
-template <typename T, bool kEnt>
-__global__ void __launch_bounds__(kThreads) logprob_bwd_kernel(const LogprobParams p, uint32_t per_row) {
+// kBlock: per_row blocks share a row, kSegVec vectors each; else a warp takes a
+// row.
+template <typename T, bool kEnt, bool kBlock>
+__global__ void __launch_bounds__(kThreads, 3) logprob_bwd_kernel(const LogprobParams p, uint32_t per_row) {
   constexpr int kN = Vec<T>::n;
-  const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
-  const int64_t row = per_row ? blockIdx.x / per_row : static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + w;
+  constexpr int kStep = kBlock ? kThreads : 32;
+  const int lane = threadIdx.x % kStep;
+  const int64_t row = kBlock ? blockIdx.x / per_row
+                             : static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
   if (row >= p.N) return;
-  const int seg = per_row ? static_cast<int>(blockIdx.x % per_row) * (kThreads / 32) + w : 0;
+  const int seg = kBlock ? static_cast<int>(blockIdx.x % per_row) : 0;
   const int64_t b = row / p.L, l = row - b * p.L;
   const T* x = static_cast<const T*>(p.x) + b * p.sb + l * p.sl;
   T* dx = static_cast<T*>(p.dx) + b * p.db + l * p.dl;
@@ -363,25 +367,26 @@ __global__ void __launch_bounds__(kThreads) logprob_bwd_kernel(const LogprobPara
   const bool same = (reinterpret_cast<uintptr_t>(x) - reinterpret_cast<uintptr_t>(dx)) % 16 == 0;
   const int head = off ? min(kN - off, p.V) : 0;
   const int nvec = (p.V - head) / kN;
+  const int first = seg * kSegVec + lane;
+  const int end = kBlock ? min(nvec, (seg + 1) * kSegVec) : nvec;
   const RowGrad g = row_grad<kEnt>(p, row);
-  const int step = per_row ? nvec + kSegVec : kSegVec;  // a segment, or all of them
-  for (int first = seg * kSegVec; first < nvec; first += step) {
-    if (same)
-      grad_segment<T, kEnt, true>(p, g, x, dx, head, nvec, first);
-    else
-      grad_segment<T, kEnt, false>(p, g, x, dx, head, nvec, first);
+  if (g.target < 0) {
+    for (int i = first; i < end; i += kStep)
+      *reinterpret_cast<uint4*>(dx + head + static_cast<int64_t>(i) * kN) = make_uint4(0u, 0u, 0u, 0u);
+  } else if (same) {
+    grad_vectors<T, kEnt, true>(g, p.inv_t, x + head, dx + head, g.target - head, first, kStep, end);
+  } else {
+    grad_vectors<T, kEnt, false>(g, p.inv_t, x + head, dx + head, g.target - head, first, kStep, end);
   }
-  if (seg == 0) {
-    const int rest = p.V - nvec * kN;
-    if (lane < rest) {
-      const int j = lane < head ? lane : nvec * kN + lane;
-      float f = 0.0f;
-      if (g.target >= 0) {
-        f = grad_of<kEnt>(Vec<T>::one(x + j), p.inv_t, g);
-        if (j == g.target) f += g.up;
-      }
-      dx[j] = Vec<T>::put(f);
+  const int rest = p.V - nvec * kN;
+  if (seg == 0 && lane < rest) {
+    const int j = lane < head ? lane : nvec * kN + lane;
+    float f = 0.0f;
+    if (g.target >= 0) {
+      f = grad_of<kEnt>(Vec<T>::one(x + j), p.inv_t, g);
+      if (j == g.target) f += g.up;
     }
+    dx[j] = Vec<T>::put(f);
   }
 }
 
@@ -444,18 +449,24 @@ pvl_status fwd(const LogprobParams& p, cudaStream_t s) {
   return launch_fwd<T, kThreads, false>(p, s);
 }
 
+template <typename T, bool kEnt>
+pvl_status launch_bwd(const LogprobParams& p, cudaStream_t s) {
+  const int64_t vectors = p.V / Vec<T>::n;
+  if (vectors > 512) {
+    const int64_t per_row = (vectors + kSegVec - 1) / kSegVec;
+    if (p.N * per_row >= (1ll << 31)) return fail(PVL_ERR_UNSUPPORTED, "pack_logprob_bwd: too many rows");
+    logprob_bwd_kernel<T, kEnt, true><<<static_cast<unsigned>(p.N * per_row), kThreads, 0, s>>>(
+        p, static_cast<uint32_t>(per_row));
+  } else {
+    constexpr int kRows = kThreads / 32;
+    logprob_bwd_kernel<T, kEnt, false><<<static_cast<unsigned>((p.N + kRows - 1) / kRows), kThreads, 0, s>>>(p, 1);
+  }
+  return check_cuda(cudaGetLastError(), "pack_logprob_bwd launch");
+}
+
 template <typename T>
 pvl_status bwd(const LogprobParams& p, cudaStream_t s) {
-  const int segments = (p.V / Vec<T>::n + kSegVec - 1) / kSegVec;
-  constexpr int kWarps = kThreads / 32;
-  const uint32_t per_row = segments >= kWarps ? (segments + kWarps - 1) / kWarps : 0;
-  const int64_t blocks = per_row ? p.N * per_row : (p.N + kWarps - 1) / kWarps;
-  if (blocks >= (1ll << 31)) return fail(PVL_ERR_UNSUPPORTED, "pack_logprob_bwd: too many rows");
-  if (p.dent)
-    logprob_bwd_kernel<T, true><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p, per_row);
-  else
-    logprob_bwd_kernel<T, false><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p, per_row);
-  return check_cuda(cudaGetLastError(), "pack_logprob_bwd launch");
+  return p.dent ? launch_bwd<T, true>(p, s) : launch_bwd<T, false>(p, s);
 }
 
 }  // namespace

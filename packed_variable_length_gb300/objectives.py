@@ -9,12 +9,21 @@ name; all arithmetic runs in the library's kernels.
 
 from __future__ import annotations
 
+from functools import lru_cache
 from typing import NamedTuple
 
 import torch
 
 from . import _lib
 from .api import _addr, _check, _launch, _need, _need_cuda, _ptr
+
+_F32, _BF16, _I32, _I64 = torch.float32, torch.bfloat16, torch.int32, torch.int64
+
+
+def _tensor(t, name: str, dtype, shape, dev) -> None:
+    """api._need, without a call where the tensor's type says the rest (these calls take microseconds)."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _need(t, name, dtype, shape, dev)
 
 
 # ------------------------------------------------------- log-probabilities
@@ -27,23 +36,38 @@ def _row_strides(t, name: str):
     return sb if B > 1 else 0, sl if L > 1 else 0
 
 
+def _kind(t, name: str, kinds) -> int:
+    """Which of two types a tensor has: 0 or 1."""
+    if isinstance(t, torch.Tensor):
+        if t.dtype is kinds[0]:
+            return 0
+        if t.dtype is kinds[1]:
+            return 1
+        raise ValueError(f"{name} must be {kinds[0]} or {kinds[1]}, got {t.dtype}")
+    raise ValueError(f"{name} must be a tensor")
+
+
 def _logprob(logits, targets, seq_id, temperature):
     """Checked description of a log-probability call."""
-    if not isinstance(logits, torch.Tensor) or logits.dim() != 3:
+    wide = _kind(logits, "logits", (_BF16, _F32))
+    if logits.dim() != 3:
         raise ValueError("logits must be [B, L, V]")
-    if logits.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"logits must be {torch.bfloat16} or {torch.float32}, got {logits.dtype}")
+    long = _kind(targets, "targets", (_I32, _I64))
     B, L, V = logits.shape
-    dev = logits.device
-    if not isinstance(targets, torch.Tensor) or targets.dtype not in (torch.int32, torch.int64):
-        raise ValueError(f"targets must be {torch.int32} or {torch.int64}")
-    _need(targets, "targets", targets.dtype, (B, L), dev)
+    dev, shape = logits.device, (B, L)
+    _tensor(targets, "targets", targets.dtype, shape, dev)
     if seq_id is not None:
-        _need(seq_id, "seq_id", torch.int32, (B, L), dev)
+        _need(seq_id, "seq_id", _I32, shape, dev)
     sb, sl = _row_strides(logits, "logits")
-    return _lib.PACK_LOGPROB(B, L, V, 1 if logits.dtype is torch.float32 else 0,
-                             1 if targets.dtype is torch.int64 else 0, float(temperature), logits.data_ptr(),
-                             targets.data_ptr(), _addr(seq_id), sb, sl)
+    return _lib.PACK_LOGPROB(B, L, V, wide, long, temperature, logits.data_ptr(), targets.data_ptr(), _addr(seq_id),
+                             sb, sl), dev, shape
+
+
+def _rows(t, name: str, shape, dev):
+    if t is None:
+        return torch.empty(shape, dtype=_F32, device=dev)
+    _need(t, name, _F32, shape, dev)
+    return t
 
 
 def pack_logprob_fwd(logits, targets, seq_id=None, *, temperature: float = 1.0, entropy: bool = False, logp=None,
@@ -56,20 +80,12 @@ def pack_logprob_fwd(logits, targets, seq_id=None, *, temperature: float = 1.0, 
     Rows may have any strides (logits[:, :-1], or a padded vocabulary's
     logits[..., :V]).  Tokens whose seq_id (int32 [B, L], optional) is negative
     or whose target lies outside [0, V) give zeros and are not read."""
-    how = _logprob(logits, targets, seq_id, temperature)
-    dev, shape = logits.device, targets.shape
+    how, dev, shape = _logprob(logits, targets, seq_id, temperature)
     with _launch(dev, stream) as handle:
-        out = []
-        for name, t, wanted in (("logp", logp, True), ("lse", lse, True), ("ent", ent, entropy)):
-            if not wanted:
-                t = None
-            elif t is None:
-                t = torch.empty(shape, dtype=torch.float32, device=dev)
-            else:
-                _need(t, name, torch.float32, shape, dev)
-            out.append(t)
-        _check(_lib.load().pack_logprob_fwd(how, out[0].data_ptr(), out[1].data_ptr(), _ptr(out[2]), handle))
-    return tuple(out)
+        logp, lse = _rows(logp, "logp", shape, dev), _rows(lse, "lse", shape, dev)
+        ent = _rows(ent, "ent", shape, dev) if entropy else None
+        _check(_lib.load().pack_logprob_fwd(how, logp.data_ptr(), lse.data_ptr(), _ptr(ent), handle))
+    return logp, lse, ent
 
 
 def pack_logprob_bwd(dlogp, logits, targets, lse, seq_id=None, *, temperature: float = 1.0, ent=None, dent=None,
@@ -78,8 +94,7 @@ def pack_logprob_bwd(dlogp, logits, targets, lse, seq_id=None, *, temperature: f
     (fp32 [B, L], or None for zero) and, with dent, from the gradient of the
     entropy (which needs ent, the forward's).  dlogits, where given, may have
     strides of its own; it may be the logits, which are then overwritten."""
-    how = _logprob(logits, targets, seq_id, temperature)
-    dev, shape = logits.device, targets.shape
+    how, dev, shape = _logprob(logits, targets, seq_id, temperature)
     if dlogp is None and dent is None:
         raise ValueError("dlogp or dent must be given")
     if dent is not None and ent is None:
@@ -111,14 +126,28 @@ class PreferenceLoss(NamedTuple):
     coef: torch.Tensor      # fp32 [episodes]: d loss / d logp of each episode's tokens
 
 
-def _tokens(logp, seq_id):
-    """Checks the tokens of a pack, of any shape; returns (device, shape)."""
-    if not isinstance(seq_id, torch.Tensor):
-        raise ValueError("seq_id must be a tensor")
-    _need_cuda(seq_id, "seq_id", torch.int32)
-    if logp is not None:
-        _need(logp, "logp", torch.float32, seq_id.shape, seq_id.device)
+def _tokens(seq_id):
+    """Checks the ids of a pack, of any shape; returns (device, shape)."""
+    if not isinstance(seq_id, torch.Tensor) or seq_id.dtype is not _I32 or not seq_id.is_contiguous() or (
+            not seq_id.is_cuda):
+        _need_cuda(seq_id, "seq_id", _I32)
     return seq_id.device, seq_id.shape
+
+
+def _of_tokens(t, name: str, shape, dev) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    _tensor(t, name, _F32, shape, dev)
+
+
+@lru_cache(maxsize=256)
+def _preference_ws_bytes(episodes: int) -> int:
+    return int(_lib.load().pack_preference_ws_bytes(episodes))
+
+
+@lru_cache(maxsize=256)
+def _policy_ws_bytes(episodes: int) -> int:
+    return int(_lib.load().pack_policy_ws_bytes(episodes))
 
 
 def _workspace(ws, nbytes: int, dev):
@@ -129,7 +158,7 @@ def _workspace(ws, nbytes: int, dev):
 
 
 def pack_preference_ws_bytes(episodes: int) -> int:
-    return int(_lib.load().pack_preference_ws_bytes(int(episodes)))
+    return _preference_ws_bytes(int(episodes))
 
 
 def pack_preference_fwd(logp, ref_logp, seq_id, pairs, episodes: int, *, beta: float = 0.1, kind: str = "sigmoid",
@@ -146,58 +175,49 @@ def pack_preference_fwd(logp, ref_logp, seq_id, pairs, episodes: int, *, beta: f
     "sigmoid": -(1 - smoothing) log sigmoid(beta h) - smoothing log
     sigmoid(-beta h); "squared": (h - 1 / (2 beta))^2; "hinge": max(0, 1 - beta
     h).  A pair with a negative id is left out."""
-    dev, shape = _tokens(logp, seq_id)
-    if logp is None:
-        raise ValueError("logp must be given")
+    dev, shape = _tokens(seq_id)
+    _of_tokens(logp, "logp", shape, dev)
     if ref_logp is not None:
-        _need(ref_logp, "ref_logp", torch.float32, shape, dev)
+        _of_tokens(ref_logp, "ref_logp", shape, dev)
     if kind not in _PREFERENCES:
         raise ValueError(f"kind must be one of {sorted(_PREFERENCES)}, got {kind!r}")
     if not isinstance(pairs, torch.Tensor) or pairs.dim() != 2 or pairs.shape[1] != 2:
         raise ValueError("pairs must be [P, 2]")
-    _need(pairs, "pairs", torch.int32, pairs.shape, dev)
-    E, P = int(episodes), int(pairs.shape[0])
-    how = _lib.PACK_PREFERENCE(seq_id.numel(), E, P, _PREFERENCES[kind], int(bool(mean)), float(beta),
-                               float(smoothing), float(margin), logp.data_ptr(), _addr(ref_logp), seq_id.data_ptr(),
-                               pairs.data_ptr())
-    lib = _lib.load()
+    _tensor(pairs, "pairs", _I32, pairs.shape, dev)
+    E, P = int(episodes), pairs.shape[0]
+    how = _lib.PACK_PREFERENCE(seq_id.numel(), E, P, _PREFERENCES[kind], 1 if mean else 0, beta, smoothing, margin,
+                               logp.data_ptr(), _addr(ref_logp), seq_id.data_ptr(), pairs.data_ptr())
+    nbytes = _preference_ws_bytes(E)
     with _launch(dev, stream) as handle:
-        ws = _workspace(ws, int(lib.pack_preference_ws_bytes(E)), dev)
-        out = torch.empty(1 + 2 * P + max(E, 1), dtype=torch.float32, device=dev)
-        loss, rewards, coef = out[:1], out[1:1 + 2 * P].view(P, 2), out[1 + 2 * P:]
-        _check(lib.pack_preference_fwd(how, loss.data_ptr(), rewards.data_ptr(), coef.data_ptr(), ws.data_ptr(),
-                                       ws.numel(), handle))
+        ws = _workspace(ws, nbytes, dev)
+        loss = torch.empty(1, dtype=_F32, device=dev)
+        rewards = torch.empty((P, 2), dtype=_F32, device=dev)
+        coef = torch.empty(max(E, 1), dtype=_F32, device=dev)
+        _check(_lib.load().pack_preference_fwd(how, loss.data_ptr(), rewards.data_ptr(), coef.data_ptr(),
+                                               ws.data_ptr(), ws.numel(), handle))
     return PreferenceLoss(loss, rewards, coef)
 
 
 def pack_preference_bwd(dloss, coef, seq_id, *, dlogp=None, stream=None):
     """d loss / d logp (fp32 like seq_id) from coef of pack_preference_fwd, times
     the device scalar dloss (fp32, one element; None for 1)."""
-    dev, shape = _tokens(None, seq_id)
+    dev, shape = _tokens(seq_id)
     if not isinstance(coef, torch.Tensor) or coef.dim() != 1:
         raise ValueError("coef must be [episodes]")
-    _need(coef, "coef", torch.float32, coef.shape, dev)
-    _scalar(dloss, dev)
+    _tensor(coef, "coef", _F32, coef.shape, dev)
+    if dloss is not None:
+        _scalar(dloss, dev)
     with _launch(dev, stream) as handle:
-        dlogp = _like_tokens(dlogp, shape, dev)
+        dlogp = _rows(dlogp, "dlogp", shape, dev)
         _check(_lib.load().pack_preference_bwd(_ptr(dloss), coef.data_ptr(), seq_id.data_ptr(), seq_id.numel(),
                                                coef.shape[0], dlogp.data_ptr(), handle))
     return dlogp
 
 
 def _scalar(dloss, dev):
-    if dloss is None:
-        return
     if not isinstance(dloss, torch.Tensor) or dloss.numel() != 1:
         raise ValueError("dloss must hold one element")
     _need(dloss, "dloss", torch.float32, dloss.shape, dev)
-
-
-def _like_tokens(t, shape, dev):
-    if t is None:
-        return torch.empty(shape, dtype=torch.float32, device=dev)
-    _need(t, "dlogp", torch.float32, shape, dev)
-    return t
 
 
 # ----------------------------------------------------------------- policy
@@ -212,26 +232,23 @@ _OVER = {"token": 0, "episode": 1}
 
 
 def _policy(logp, old_logp, advantages, seq_id, episodes, ref_logp, clip_low, clip_high, kl_weight, ratio, mean):
-    dev, shape = _tokens(logp, seq_id)
-    if logp is None:
-        raise ValueError("logp must be given")
-    for name, t in (("old_logp", old_logp), ("ref_logp", ref_logp)):
-        if t is not None:
-            _need(t, name, torch.float32, shape, dev)
-    for name, v in (("ratio", ratio), ("mean", mean)):
-        if v not in _OVER:
-            raise ValueError(f"{name} must be 'token' or 'episode', got {v!r}")
-    if not isinstance(advantages, torch.Tensor):
-        raise ValueError("advantages must be a tensor")
-    tokens = ratio == "token" and advantages.shape == shape
-    _need(advantages, "advantages", torch.float32, shape if tokens else (int(episodes),), dev)
-    return _lib.PACK_POLICY(seq_id.numel(), int(episodes), _OVER[ratio], _OVER[mean], int(tokens), float(clip_low),
-                            float(clip_high), float(kl_weight), logp.data_ptr(), _addr(old_logp), _addr(ref_logp),
-                            advantages.data_ptr(), seq_id.data_ptr()), dev, shape
+    dev, shape = _tokens(seq_id)
+    _of_tokens(logp, "logp", shape, dev)
+    if old_logp is not None:
+        _of_tokens(old_logp, "old_logp", shape, dev)
+    if ref_logp is not None:
+        _of_tokens(ref_logp, "ref_logp", shape, dev)
+    if ratio not in _OVER or mean not in _OVER:
+        raise ValueError(f"ratio and mean must be 'token' or 'episode', got {ratio!r} and {mean!r}")
+    tokens = ratio == "token" and isinstance(advantages, torch.Tensor) and advantages.shape == shape
+    _of_tokens(advantages, "advantages", shape if tokens else (episodes,), dev)
+    return _lib.PACK_POLICY(seq_id.numel(), episodes, _OVER[ratio], _OVER[mean], 1 if tokens else 0, clip_low, clip_high,
+                            kl_weight, logp.data_ptr(), _addr(old_logp), _addr(ref_logp), advantages.data_ptr(),
+                            seq_id.data_ptr()), dev, shape
 
 
 def pack_policy_ws_bytes(episodes: int) -> int:
-    return int(_lib.load().pack_policy_ws_bytes(int(episodes)))
+    return _policy_ws_bytes(int(episodes))
 
 
 def pack_policy_fwd(logp, old_logp, advantages, seq_id, episodes: int, *, ref_logp=None, clip_low: float = 0.2,
@@ -247,16 +264,16 @@ def pack_policy_fwd(logp, old_logp, advantages, seq_id, episodes: int, *, ref_lo
     -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_weight (exp(f) - f -
     1), f = ref_logp - logp; the loss is their mean (mean="episode": the mean of
     the episodes' means)."""
-    how, dev, _ = _policy(logp, old_logp, advantages, seq_id, episodes, ref_logp, clip_low, clip_high, kl_weight,
-                          ratio, mean)
     E = int(episodes)
-    lib = _lib.load()
+    how, dev, _ = _policy(logp, old_logp, advantages, seq_id, E, ref_logp, clip_low, clip_high, kl_weight, ratio, mean)
+    nbytes = _policy_ws_bytes(E)
     with _launch(dev, stream) as handle:
-        ws = _workspace(ws, int(lib.pack_policy_ws_bytes(E)), dev)
-        out = torch.empty(4 + 2 * max(E, 1), dtype=torch.float32, device=dev)
-        loss, stats, coef = out[:1], out[1:3], out[4:].view(-1, 2)
-        _check(lib.pack_policy_fwd(how, loss.data_ptr(), stats.data_ptr(), coef.data_ptr(), ws.data_ptr(), ws.numel(),
-                                   handle))
+        ws = _workspace(ws, nbytes, dev)
+        loss = torch.empty(1, dtype=_F32, device=dev)
+        stats = torch.empty(2, dtype=_F32, device=dev)
+        coef = torch.empty((max(E, 1), 2), dtype=_F32, device=dev)
+        _check(_lib.load().pack_policy_fwd(how, loss.data_ptr(), stats.data_ptr(), coef.data_ptr(), ws.data_ptr(),
+                                           ws.numel(), handle))
     return PolicyLoss(loss, stats, coef)
 
 
@@ -268,9 +285,10 @@ def pack_policy_bwd(dloss, logp, old_logp, advantages, seq_id, coef, *, ref_logp
         raise ValueError("coef must be [episodes, 2]")
     how, dev, shape = _policy(logp, old_logp, advantages, seq_id, coef.shape[0], ref_logp, clip_low, clip_high,
                               kl_weight, ratio, "token")
-    _need(coef, "coef", torch.float32, coef.shape, dev)
-    _scalar(dloss, dev)
+    _tensor(coef, "coef", _F32, coef.shape, dev)
+    if dloss is not None:
+        _scalar(dloss, dev)
     with _launch(dev, stream) as handle:
-        dlogp = _like_tokens(dlogp, shape, dev)
+        dlogp = _rows(dlogp, "dlogp", shape, dev)
         _check(_lib.load().pack_policy_bwd(how, _ptr(dloss), coef.data_ptr(), dlogp.data_ptr(), handle))
     return dlogp
