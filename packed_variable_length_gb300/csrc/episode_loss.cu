@@ -21,7 +21,8 @@
 //
 // Both are bound by latency: a 64k pack is 1.6 MB.  One kernel reads the
 // tokens, four a thread; blocks whose tokens belong to one episode add one sum,
-// others one per warp or per run of a thread's tokens.  The last block to
+// others one per warp, or one per episode and warp and one per run of a thread
+// whose tokens belong to several.  The last block to
 // finish turns the episodes' sums into the loss and the table.
 //
 // Sums are integers, so that they are the same whatever order blocks finish in,
@@ -157,29 +158,38 @@ __device__ __noinline__ double large_value(const long long (&digit)[6], unsigned
   return negative ? -v : v;
 }
 
-// A sum's value, as a pair and in 64 bits.
-struct Value {
-  Pair p;
-  double d;
+// The digits as they are, so that those of several sums can be on their way at
+// once.
+struct Digits {
+  long long d[6];
 };
 
-__device__ __forceinline__ Value value(const Sum* s, unsigned int flags, int shift) {
-  flags = (flags >> shift) & 7u;
-  long long d[6];
+__device__ __forceinline__ Digits digits(const Sum* s) {
+  Digits v;
 #pragma unroll
-  for (int i = 0; i < 6; ++i) d[i] = __ldcg(&s->digit[i]);
+  for (int i = 0; i < 6; ++i) v.d[i] = __ldcg(&s->digit[i]);
+  return v;
+}
+
+// A sum's value: a pair, and in 64 bits in *far where its magnitude is kNear and
+// more (or less: never without).
+constexpr float kNear = 1e6f;
+
+__device__ __forceinline__ Pair value(const Digits& s, unsigned int flags, int shift, double* far = nullptr) {
+  flags = (flags >> shift) & 7u;
+  const long long(&d)[6] = s.d;
   const long long next = d[4] + (d[5] >> 40), top = d[3] + (next >> 40);
-  if (!(flags | d[0] | d[1] | d[2]) && top < (1ll << 22) && top >= -(1ll << 22)) {
+  if (!(flags | d[0] | d[1] | d[2]) && top < (1ll << 19) && top >= -(1ll << 19)) {
     const long long whole = top * (1ll << 40) + (next & kMask);  // units of 2^-40
     const float rest = __ll2float_rn(d[5] & kMask) * (1.0f / kFine);
     const float hi = __ll2float_rn(whole);
     const Pair u = renormal(hi, __ll2float_rn(whole - __float2ll_rn(hi)) + rest);
-    return {{u.hi * (1.0f / kFine), u.lo * (1.0f / kFine)},
-            (static_cast<double>(whole) + static_cast<double>(rest)) * (1.0 / kUp)};
+    return {u.hi * (1.0f / kFine), u.lo * (1.0f / kFine)};
   }
   const double v = large_value(d, flags);
+  if (far) *far = v;
   const float hi = static_cast<float>(v);
-  return {{hi, finite(hi) ? static_cast<float>(v - hi) : 0.0f}, v};
+  return {hi, finite(hi) ? static_cast<float>(v - hi) : 0.0f};
 }
 
 // What is summed of an episode: two values, valid tokens, clipped tokens.
@@ -216,6 +226,16 @@ __device__ __forceinline__ Part warp_sum(Part p, bool two) {
   p.n = __reduce_add_sync(kAll, p.n);
   p.cut = __reduce_add_sync(kAll, p.cut);
   return p;
+}
+
+// The sum of v over the lanes of `mask`, which all call this: in pieces of 22
+// bits, whose sums fit in 32.
+__device__ __forceinline__ long long group_sum(unsigned mask, long long v) {
+  constexpr unsigned kPiece = (1u << 22) - 1;
+  const unsigned lo = __reduce_add_sync(mask, static_cast<unsigned>(v) & kPiece);
+  const unsigned mid = __reduce_add_sync(mask, static_cast<unsigned>(v >> 22) & kPiece);
+  const int hi = __reduce_add_sync(mask, static_cast<int>(v >> 44));
+  return (static_cast<long long>(hi) << 44) + (static_cast<long long>(mid) << 22) + lo;
 }
 
 // Sums over the block in a fixed order; every thread gets them.
@@ -275,7 +295,8 @@ struct LossParams {
   Episode* episodes;
   Sum* factors;  // preference: sums of the pairs' derivatives, one an episode
   unsigned int* factor_flags;
-  Value* sums;   // D_e
+  Pair* sums;    // D_e
+  double* far;   // D_e in 64 bits where it is kNear and more
   DeviceError* err;
 };
 
@@ -408,6 +429,16 @@ __device__ void sum_tokens(const LossParams& p) {
     }
   } else if (lo == hi) {
     if (lane == 0) add_part(p.episodes + lo, sum);
+  } else if (id[0] == id[1] && id[1] == id[2] && id[2] == id[3]) {
+    // lanes of one episode each: those of the same one add together
+    const unsigned mask = __match_any_sync(__activemask(), id[0]);
+    if (id[0] < 0) return;
+    sum = t[0] + t[1] + t[2] + t[3];
+    sum.a = group_sum(mask, sum.a);
+    if (two) sum.b = group_sum(mask, sum.b);
+    sum.n = __reduce_add_sync(mask, sum.n);
+    sum.cut = __reduce_add_sync(mask, sum.cut);
+    if (lane == __ffs(mask) - 1) add_part(p.episodes + id[0], sum);
   } else {
     Part run = t[0];
     int at = id[0];
@@ -423,6 +454,11 @@ __device__ void sum_tokens(const LossParams& p) {
     }
     if (at >= 0) add_part(p.episodes + at, run);
   }
+}
+
+// D_e in 64 bits.
+__device__ __forceinline__ double wide(const LossParams& p, int e, Pair v) {
+  return fabsf(v.hi) < kNear ? static_cast<double>(v.hi) + static_cast<double>(v.lo) : p.far[e];
 }
 
 // Whether this block is the last of the grid to get here; it then sees what
@@ -442,15 +478,28 @@ __device__ bool last_block(const LossParams& p) {
 __global__ void __launch_bounds__(kThreads) preference_kernel(const LossParams p) {
   sum_tokens<false>(p);
   if (!last_block(p)) return;
-  for (int e = threadIdx.x; e < p.E; e += kThreads) {
-    const Episode* q = p.episodes + e;
-    const unsigned int n = __ldcg(&q->n);
-    Value v = value(&q->a, __ldcg(&q->flags), 0);
-    if (p.mean && n) {
-      v.p = over(v.p, static_cast<float>(n));
-      v.d /= n;
+  // two episodes a thread and turn, whose digits are on their way together
+  for (int first = threadIdx.x; first < p.E; first += 2 * kThreads) {
+    Digits s[2];
+    unsigned int n[2], flags[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const Episode* q = p.episodes + min(first + i * kThreads, p.E - 1);
+      s[i] = digits(&q->a);
+      n[i] = __ldcg(&q->n);
+      flags[i] = __ldcg(&q->flags);
     }
-    p.sums[e] = v;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = first + i * kThreads;
+      if (e >= p.E) continue;
+      Pair v = value(s[i], flags[i], 0, p.far + e);
+      if (p.mean && n[i]) {
+        if (!(fabsf(v.hi) < kNear)) p.far[e] /= n[i];
+        v = over(v, static_cast<float>(n[i]));
+      }
+      p.sums[e] = v;
+    }
   }
   __syncthreads();
   Pair loss{0.0f, 0.0f};
@@ -463,23 +512,23 @@ __global__ void __launch_bounds__(kThreads) preference_kernel(const LossParams p
       continue;
     }
     ++count;
-    const Value vc = p.sums[c], vr = p.sums[r];
+    const Pair vc = p.sums[c], vr = p.sums[r];
     Pair h;   // D_c - D_r - margin, to 2^-46 of its terms
     float x;  // beta h
-    float rc = p.beta * vc.p.hi, rr = p.beta * vr.p.hi;
-    bool short_of;  // beta h < 1, decided in 64 bits
-    if (fabsf(vc.p.hi) < 1e6f && fabsf(vr.p.hi) < 1e6f && p.kind != PVL_PREFERENCE_HINGE) {
-      h = add(add(vc.p, Pair{-vr.p.hi, -vr.p.lo}), Pair{-p.margin.hi, -p.margin.lo});
+    float rc = p.beta * vc.hi, rr = p.beta * vr.hi;
+    bool short_of;  // beta h < 1
+    if (fabsf(vc.hi) < kNear && fabsf(vr.hi) < kNear) {
+      h = add(add(vc, Pair{-vr.hi, -vr.lo}), Pair{-p.margin.hi, -p.margin.lo});
       x = p.beta * h.hi;
-      short_of = false;
+      short_of = above(Pair{2.0f * p.target.hi, 2.0f * p.target.lo}, h);
     } else {
-      const double d = vc.d - vr.d - p.margin_d;
+      const double dc = wide(p, c, vc), dr = wide(p, r, vr), d = dc - dr - p.margin_d;
       const float hi = static_cast<float>(d);
       h = {hi, finite(hi) ? static_cast<float>(d - hi) : 0.0f};
       x = static_cast<float>(p.beta_d * d);
       short_of = p.beta_d * d < 1.0;
-      rc = static_cast<float>(p.beta_d * vc.d);
-      rr = static_cast<float>(p.beta_d * vr.d);
+      rc = static_cast<float>(p.beta_d * dc);
+      rr = static_cast<float>(p.beta_d * dr);
     }
     p.rewards[2 * i] = rc;
     p.rewards[2 * i + 1] = rr;
@@ -524,7 +573,7 @@ __global__ void __launch_bounds__(kThreads) preference_kernel(const LossParams p
   const float slope = p.kind == PVL_PREFERENCE_SQUARED ? 1.0f : p.beta;
   for (int e = threadIdx.x; e < p.E; e += kThreads) {
     const unsigned int n = __ldcg(&p.episodes[e].n);
-    const float f = slope * over(value(p.factors + e, __ldcg(p.factor_flags + e), 0).p, share).hi;
+    const float f = slope * over(value(digits(p.factors + e), __ldcg(p.factor_flags + e), 0), share).hi;
     p.coef[e] = p.mean && n ? f / static_cast<float>(n) : f;
   }
 }
@@ -551,7 +600,7 @@ __global__ void __launch_bounds__(kThreads) policy_kernel(const LossParams p) {
     float slope = 0.0f, weight = 0.0f;
     if (n) {
       const float fn = static_cast<float>(n);
-      const Pair a = value(&q->a, flags, 0).p;
+      const Pair a = value(digits(&q->a), flags, 0);
       weight = p.mean_episode ? 1.0f / (whole * fn) : 1.0f / whole;
       if (p.ratio_episode) {
         const Pair d = over(a, fn);
@@ -566,7 +615,7 @@ __global__ void __launch_bounds__(kThreads) policy_kernel(const LossParams p) {
         cut += __ldcg(&q->cut);
       }
       if (p.ref) {
-        const Pair b = value(&q->b, flags, 3).p;
+        const Pair b = value(digits(&q->b), flags, 3);
         kl = add(kl, p.mean_episode ? over(b, fn) : b);
       }
     }
@@ -639,7 +688,7 @@ __global__ void __launch_bounds__(kBwdThreads) token_grad_kernel(const LossParam
 // Workspace: counter (cleared), episodes (cleared), factors and their flags
 // (cleared, preference), D_e (preference).
 struct Layout {
-  size_t episodes, factors, flags, clear, sums, total;
+  size_t episodes, factors, flags, clear, sums, far, total;
 };
 
 Layout layout(int E, bool preference) {
@@ -649,7 +698,8 @@ Layout layout(int E, bool preference) {
   l.flags = l.factors + (preference ? align256(static_cast<size_t>(E) * sizeof(Sum)) : 0);
   l.clear = l.flags + (preference ? align256(static_cast<size_t>(E) * 4) : 0);
   l.sums = l.clear;
-  l.total = l.sums + (preference ? align256(static_cast<size_t>(E) * sizeof(Value)) : 0);
+  l.far = l.sums + (preference ? align256(static_cast<size_t>(E) * sizeof(Pair)) : 0);
+  l.total = l.far + (preference ? align256(static_cast<size_t>(E) * 8) : 0);
   return l;
 }
 
@@ -685,7 +735,8 @@ pvl_status workspace(const char* who, LossParams& p, void* ws, size_t ws_bytes, 
   p.episodes = reinterpret_cast<Episode*>(b + l.episodes);
   p.factors = reinterpret_cast<Sum*>(b + l.factors);
   p.factor_flags = reinterpret_cast<unsigned int*>(b + l.flags);
-  p.sums = reinterpret_cast<Value*>(b + l.sums);
+  p.sums = reinterpret_cast<Pair*>(b + l.sums);
+  p.far = reinterpret_cast<double*>(b + l.far);
   return check_cuda(cudaMemsetAsync(ws, 0, l.clear, s), who);
 }
 

@@ -134,10 +134,15 @@ def _tokens(seq_id):
     return seq_id.device, seq_id.shape
 
 
-def _of_tokens(t, name: str, shape, dev) -> None:
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name} must be a tensor")
-    _tensor(t, name, _F32, shape, dev)
+def _of_tokens(tensors, names, shape, dev) -> None:
+    """Every tensor of the list that is there is fp32, of the shape, contiguous and on the device; the first is there."""
+    for t, name in zip(tensors, names):
+        if t is None and name != "logp":
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a tensor")
+        if t.dtype is not _F32 or t.shape != shape or t.device != dev or not t.is_contiguous():
+            _need(t, name, _F32, shape, dev)
 
 
 @lru_cache(maxsize=256)
@@ -176,9 +181,7 @@ def pack_preference_fwd(logp, ref_logp, seq_id, pairs, episodes: int, *, beta: f
     sigmoid(-beta h); "squared": (h - 1 / (2 beta))^2; "hinge": max(0, 1 - beta
     h).  A pair with a negative id is left out."""
     dev, shape = _tokens(seq_id)
-    _of_tokens(logp, "logp", shape, dev)
-    if ref_logp is not None:
-        _of_tokens(ref_logp, "ref_logp", shape, dev)
+    _of_tokens((logp, ref_logp), ("logp", "ref_logp"), shape, dev)
     if kind not in _PREFERENCES:
         raise ValueError(f"kind must be one of {sorted(_PREFERENCES)}, got {kind!r}")
     if not isinstance(pairs, torch.Tensor) or pairs.dim() != 2 or pairs.shape[1] != 2:
@@ -233,15 +236,13 @@ _OVER = {"token": 0, "episode": 1}
 
 def _policy(logp, old_logp, advantages, seq_id, episodes, ref_logp, clip_low, clip_high, kl_weight, ratio, mean):
     dev, shape = _tokens(seq_id)
-    _of_tokens(logp, "logp", shape, dev)
-    if old_logp is not None:
-        _of_tokens(old_logp, "old_logp", shape, dev)
-    if ref_logp is not None:
-        _of_tokens(ref_logp, "ref_logp", shape, dev)
+    _of_tokens((logp, old_logp, ref_logp), ("logp", "old_logp", "ref_logp"), shape, dev)
     if ratio not in _OVER or mean not in _OVER:
         raise ValueError(f"ratio and mean must be 'token' or 'episode', got {ratio!r} and {mean!r}")
-    tokens = ratio == "token" and isinstance(advantages, torch.Tensor) and advantages.shape == shape
-    _of_tokens(advantages, "advantages", shape if tokens else (episodes,), dev)
+    if not isinstance(advantages, torch.Tensor):
+        raise ValueError("advantages must be a tensor")
+    tokens = ratio == "token" and advantages.shape == shape
+    _tensor(advantages, "advantages", _F32, shape if tokens else (episodes,), dev)
     return _lib.PACK_POLICY(seq_id.numel(), episodes, _OVER[ratio], _OVER[mean], 1 if tokens else 0, clip_low, clip_high,
                             kl_weight, logp.data_ptr(), _addr(old_logp), _addr(ref_logp), advantages.data_ptr(),
                             seq_id.data_ptr()), dev, shape

@@ -362,3 +362,13 @@ def test_most_tokens_and_many_episodes(pvl):
     assert torch.allclose(ends, torch.tensor([-0.5, 0.5]), rtol=1e-5) and out.coef[1:-1].abs().max() < 1e-10
     p = pvl.pack_policy_fwd(lp, lp, torch.ones(E, device="cuda"), sid, E, mean="episode", ratio="episode")
     assert p.loss.item() == -1.0
+
+
+@pytest.mark.parametrize("N", [127, 128, 129, 2047, 2048, 2049, 140000])
+def test_both_sides_of_a_warp_and_of_a_block(pvl, N):
+    """A warp takes 128 tokens, a block 2048."""
+    ids = pack(1, N, 9, N)
+    pairs = np.random.default_rng(N).integers(0, 9, size=(20, 2))
+    check_preference(pvl, ids, 9, pairs, mean=True)
+    check_policy(pvl, ids, 9, True, kl_weight=0.1)
+    check_policy(pvl, ids, 9, False, ratio="episode", mean="episode", clip_low=0.01, clip_high=0.01)
