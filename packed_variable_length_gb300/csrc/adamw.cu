@@ -48,14 +48,13 @@ constexpr float kTop = 448.0f;     // largest e4m3 value
 constexpr int kNormUnit = 1024;    // elements a warp takes at a time for the norm
 constexpr int kMaxNormCtas = 4096;
 
-// Tensors of a launch.  A chunk is 2^shift blocks of a tensor (its last may be
-// shorter), what a warp takes at a time.
+// Tensors of a launch.
 template <int kT>
 struct Tensors {
-  uint32_t start[kT + 1];  // running count of chunks
+  uint32_t start[kT + 1];  // running count of blocks
   int32_t slot[kT];        // place in the step counts
   float decay[kT];
-  int32_t n, shift;
+  int32_t n;
   void* param[kT];
   const void* grad[kT];
   long long size[kT];
@@ -256,8 +255,9 @@ struct Shared {
   uint32_t key;
 };
 
-// One block: this lane's eight elements, n of which are the tensor's (kBy: all
-// eight, and the fp32 addresses are multiples of kBy).
+// One block: this lane's eight elements, n of which are the tensor's.  kBy: what
+// fp32 addresses of the tensors are multiples of, or 0 where the block is not
+// whole or not aligned and elements go one by one.
 template <typename P, typename G, bool k8, int kBy>
 __device__ __forceinline__ void step_block(const StepParams& p, const Shared& c, P* param, const G* grad, long long sb,
                                            int n) {
@@ -363,7 +363,7 @@ __device__ __forceinline__ void step_block(const StepParams& p, const Shared& c,
 }
 
 template <typename P, typename G, bool k8, int kT>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Tensors<kT> tab,
+__global__ void __launch_bounds__(kThreads, k8 ? 4 : 2) adamw_kernel(const __grid_constant__ Tensors<kT> tab,
                                                          const __grid_constant__ StepParams p) {
   const int lane = threadIdx.x % 32;
   Shared c;
@@ -387,11 +387,12 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   int32_t step = -1;
   for (; u < total; u += gridDim.x * kWarps) {
     while (u >= tab.start[t + 1]) ++t;
-    const long long b = static_cast<long long>(u - tab.start[t]) << tab.shift;  // block of the tensor
-    long long sb = tab.block[t] + b;                                           // block of the states
-    P* param = static_cast<P*>(tab.param[t]) + b * kBlock + lane * 8;
-    const G* grad = static_cast<const G*>(tab.grad[t]) + b * kBlock + lane * 8;
-    long long left = tab.size[t] - b * kBlock;
+    const uint32_t b = u - tab.start[t];       // block of the tensor
+    const long long sb = tab.block[t] + b;     // block of the states
+    const long long at = static_cast<long long>(b) * kBlock + lane * 8;
+    P* param = static_cast<P*>(tab.param[t]) + at;
+    const G* grad = static_cast<const G*>(tab.grad[t]) + at;
+    const long long left = tab.size[t] - at;   // of this lane
     const int32_t now = p.steps[tab.slot[t]] + 1;
     if (now != step) {
       step = now;
@@ -401,20 +402,15 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       c.key = mix(p.seed + static_cast<uint32_t>(now) * 0x9E3779B9u);
     }
     c.keep = 1.0f - lr * tab.decay[t];
+    const bool whole = left + lane * 8 >= kBlock;
     const uintptr_t where = reinterpret_cast<uintptr_t>(param) | reinterpret_cast<uintptr_t>(grad);
     constexpr uintptr_t kSector = sizeof(P) == 4 || sizeof(G) == 4 ? 32 : 16;
-    if (left >= (static_cast<long long>(kBlock) << tab.shift) && where % kSector == 0) {
-      for (int j = 0; j < 1 << tab.shift; ++j, param += kBlock, grad += kBlock, ++sb)
-        step_block<P, G, k8, 32>(p, c, param, grad, sb, 8);
-      continue;
-    }
-    for (int j = 0; j < 1 << tab.shift && left > 0; ++j, param += kBlock, grad += kBlock, ++sb, left -= kBlock) {
-      const long long mine = left - lane * 8;
-      if (kSector == 32 && left >= kBlock && where % 16 == 0)
-        step_block<P, G, k8, 16>(p, c, param, grad, sb, 8);
-      else
-        step_block<P, G, k8, 0>(p, c, param, grad, sb, mine >= 8 ? 8 : mine > 0 ? static_cast<int>(mine) : 0);
-    }
+    if (whole && where % kSector == 0)
+      step_block<P, G, k8, 32>(p, c, param, grad, sb, 8);
+    else if (kSector == 32 && whole && where % 16 == 0)
+      step_block<P, G, k8, 16>(p, c, param, grad, sb, 8);
+    else
+      step_block<P, G, k8, 0>(p, c, param, grad, sb, left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0);
   }
   // every block has read the step counts once it has counted itself
   __shared__ bool last;
@@ -538,38 +534,24 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
 // ---------------------------------------------------------------- host
 long long blocks_of(long long n) { return (n + kBlock - 1) / kBlock; }
 
-// Chunks of four blocks once there are as many as warps that fit the device:
-// what a chunk looks up is then shared by 1024 elements.  Fewer blocks than that
-// are spread over as many warps as there are.
-constexpr int kChunkShift = 2;
-
 template <typename P, typename G, bool k8, int kT>
-pvl_status launch_step(Tensors<kT>& tab, const StepParams& p, int sms, cudaStream_t s) {
+pvl_status launch_step(const Tensors<kT>& tab, const StepParams& p, int sms, cudaStream_t s) {
   const void* fn = reinterpret_cast<const void*>(adamw_kernel<P, G, k8, kT>);
   const int fit = blocks_per_sm(fn, kThreads, 0);
   if (fit < 1) return fail(PVL_ERR_CUDA, "pvl_adamw_step: the kernel does not fit on an SM");
+  const long long need = (static_cast<long long>(tab.start[tab.n]) + kWarps - 1) / kWarps;
   const long long most = static_cast<long long>(fit) * sms;
-  long long blocks = 0;
-  for (int i = 0; i < tab.n; ++i) blocks += blocks_of(tab.size[i]);
-  tab.shift = blocks >= most * kWarps << kChunkShift ? kChunkShift : 0;
-  long long chunks = 0;
-  for (int i = 0; i < tab.n; ++i) {
-    tab.start[i] = static_cast<uint32_t>(chunks);
-    chunks += (blocks_of(tab.size[i]) + (1 << tab.shift) - 1) >> tab.shift;
-  }
-  tab.start[tab.n] = static_cast<uint32_t>(chunks);
-  const long long need = (chunks + kWarps - 1) / kWarps;
   adamw_kernel<P, G, k8, kT><<<static_cast<unsigned>(need < most ? need : most), kThreads, 0, s>>>(tab, p);
   return check_cuda(cudaGetLastError(), "pvl_adamw_step launch");
 }
 
 template <typename P, typename G, int kT>
-pvl_status step_bits(int bits, Tensors<kT>& tab, const StepParams& p, int sms, cudaStream_t s) {
+pvl_status step_bits(int bits, const Tensors<kT>& tab, const StepParams& p, int sms, cudaStream_t s) {
   return bits == 8 ? launch_step<P, G, true, kT>(tab, p, sms, s) : launch_step<P, G, false, kT>(tab, p, sms, s);
 }
 
 template <int kT>
-pvl_status step_types(const pvl_adamw* h, Tensors<kT>& tab, const StepParams& p, int sms, cudaStream_t s) {
+pvl_status step_types(const pvl_adamw* h, const Tensors<kT>& tab, const StepParams& p, int sms, cudaStream_t s) {
   if (h->param_dtype == 0)
     return h->grad_dtype == 0 ? step_bits<__nv_bfloat16, __nv_bfloat16, kT>(h->bits, tab, p, sms, s)
                               : step_bits<__nv_bfloat16, float, kT>(h->bits, tab, p, sms, s);
@@ -585,8 +567,9 @@ int fill(const pvl_adamw_tensor* list, int first, int count, Tensors<kT>* tab) {
   long long blocks = 0;
   for (; n < kT && first + n < count; ++n) {
     const pvl_adamw_tensor& q = list[first + n];
+    if (blocks + blocks_of(q.size) >= (1ll << 31)) break;
+    tab->start[n] = static_cast<uint32_t>(blocks);
     blocks += blocks_of(q.size);
-    if (blocks >= (1ll << 31)) break;
     tab->param[n] = q.param;
     tab->grad[n] = q.grad;
     tab->size[n] = q.size;
@@ -594,6 +577,7 @@ int fill(const pvl_adamw_tensor* list, int first, int count, Tensors<kT>* tab) {
     tab->slot[n] = q.slot;
     tab->decay[n] = q.decay;
   }
+  tab->start[n] = static_cast<uint32_t>(blocks);
   tab->n = n;
   return n;
 }

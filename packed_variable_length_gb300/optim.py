@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import math
 from dataclasses import dataclass, field
+from operator import attrgetter
 
 import numpy as np
 import torch
@@ -25,25 +26,39 @@ _TENSOR = np.dtype([("param", np.uint64), ("grad", np.uint64), ("size", np.int64
 _FLOATS = {torch.bfloat16: 0, torch.float32: 1}
 
 
+# A model has hundreds of parameters and a step looks at each: attributes of
+# whole lists are read by C loops, one list at a time.
+_dtype, _shape = attrgetter("dtype"), attrgetter("shape")
+_contiguous, _index, _address, _count = (torch.Tensor.is_contiguous, torch.Tensor.get_device, torch.Tensor.data_ptr,
+                                         torch.Tensor.numel)
+
+
 def _same_floats(tensors, name: str):
     """The dtype and device that all of the list share; every tensor contiguous."""
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name}[{i}] must be a tensor")
     dtype, dev = tensors[0].dtype, tensors[0].device
     if dtype not in _FLOATS:
         raise ValueError(f"{name} must be {torch.bfloat16} or {torch.float32}, got {dtype}")
-    for i, t in enumerate(tensors):
-        if t.dtype is not dtype or t.device != dev or not t.is_contiguous():
-            _need_cuda(t, f"{name}[{i}]", dtype)
-            raise ValueError(f"{name}[{i}] is on {t.device}, not on {dev}")
+    if set(map(_dtype, tensors)) != {dtype} or set(map(_index, tensors)) != {tensors[0].get_device()} or (
+            not all(map(_contiguous, tensors))):
+        for i, t in enumerate(tensors):
+            _need(t, f"{name}[{i}]", dtype, t.shape, dev)
     return dtype, dev
 
 
 def grad_norm(grads, out=None, ws=None, stream=None) -> torch.Tensor:
     """fp32 [1] device tensor: the 2-norm of all gradients together (bf16 or
     fp32 tensors of one type; None and empty ones are skipped)."""
-    grads = [g for g in grads if g is not None and g.numel()]
+    grads = [g for g in grads if g is not None]
+    dtype, dev = _same_floats(grads, "grads") if grads else (None, None)
+    counts = list(map(_count, grads))
+    if 0 in counts:
+        grads = [g for g, n in zip(grads, counts) if n]
+        counts = [n for n in counts if n]
     if not grads:
         raise ValueError("grad_norm needs a gradient")
-    dtype, dev = _same_floats(grads, "grads")
     lib = _lib.load()
     with _launch(dev, stream) as handle:
         if out is None:
@@ -55,8 +70,8 @@ def grad_norm(grads, out=None, ws=None, stream=None) -> torch.Tensor:
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         else:
             _need(ws, "ws", torch.uint8, ws.shape, dev)
-        ptrs = np.array([g.data_ptr() for g in grads], dtype=np.uint64)
-        sizes = np.array([g.numel() for g in grads], dtype=np.int64)
+        ptrs = np.array(list(map(_address, grads)), dtype=np.uint64)
+        sizes = np.array(counts, dtype=np.int64)
         _check(lib.pvl_grad_norm(ptrs.ctypes.data, sizes.ctypes.data, len(grads), _FLOATS[dtype], out.data_ptr(),
                                  ws.data_ptr(), ws.numel(), handle))
     return out
@@ -116,7 +131,7 @@ def adamw_state(params, *, bits: int = 32, seed: int = 0) -> AdamWState:
     if params[0].device.type != "cuda":
         raise ValueError(f"the kernels run on CUDA devices, not on {params[0].device}")
     dtype, dev = _same_floats(params, "params")
-    _distinct([p.data_ptr() for p in params if p.numel()])
+    _distinct([p.data_ptr() for p in params if p.numel()])     # empty ones have no address
     table = np.zeros(len(params), dtype=_TENSOR)
     table["size"] = [p.numel() for p in params]
     table["slot"] = np.arange(len(params))
@@ -138,6 +153,17 @@ def adamw_state(params, *, bits: int = 32, seed: int = 0) -> AdamWState:
         for i, p in enumerate(params):
             state.masters(i).copy_(p.detach())
     return state
+
+
+def _like(tensors, name: str, use, dtype, shapes, dev) -> None:
+    """Every tensor of the list has the dtype, its shape and the device, and is contiguous; `use`: their places."""
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name}[{i if use is None else use[i]}] must be a tensor")
+    if set(map(_dtype, tensors)) != {dtype} or set(map(_index, tensors)) != {dev.index} or (
+            not all(map(_contiguous, tensors)) or list(map(_shape, tensors)) != list(shapes)):
+        for i, (t, shape) in enumerate(zip(tensors, shapes)):
+            _need(t, f"{name}[{i if use is None else use[i]}]", dtype, shape, dev)
 
 
 def _distinct(ptrs):
@@ -184,37 +210,36 @@ def adamw_step(params, grads, state: AdamWState, lr, *, betas=(0.9, 0.999), eps:
             raise ValueError("lr must hold one element")
         _need(lr, "lr", torch.float32, lr.shape, dev)
         lr, lr_dev = 0.0, lr
-    kind = None
-    use = []
-    for i, (p, g, shape) in enumerate(zip(params, grads, state.shapes)):
-        if p.dtype is not state.dtype or p.device != dev or p.shape != shape or not p.is_contiguous():
-            _need(p, f"params[{i}]", state.dtype, shape, dev)
-        if g is None or not p.numel():
-            continue
-        kind = g.dtype if kind is None else kind
-        if kind not in _FLOATS:
-            raise ValueError(f"grads[{i}] must be {torch.bfloat16} or {torch.float32}, got {kind}")
-        if g.dtype is not kind or g.device != dev or g.shape != shape or not g.is_contiguous():
-            _need(g, f"grads[{i}]", kind, shape, dev)
-        use.append(i)
-    if not use:
-        return
-    table = state.table if len(use) == n else state.table[use]
-    table["param"] = [params[i].data_ptr() for i in use]
-    table["grad"] = [grads[i].data_ptr() for i in use]
-    _distinct(table["param"].tolist())
+    use = None      # which parameters step: None for all
+    if any(g is None for g in grads) or not state.table["size"].all():
+        use = [i for i, g in enumerate(grads) if g is not None and state.table["size"][i]]
+        if not use:
+            return
+    some_params = params if use is None else [params[i] for i in use]
+    some_grads = grads if use is None else [grads[i] for i in use]
+    some_shapes = state.shapes if use is None else [state.shapes[i] for i in use]
+    _like(some_params, "params", use, state.dtype, some_shapes, dev)
+    kind = some_grads[0].dtype if isinstance(some_grads[0], torch.Tensor) else None
+    if kind not in _FLOATS:
+        raise ValueError(f"grads must be {torch.bfloat16} or {torch.float32} tensors, got {kind}")
+    _like(some_grads, "grads", use, kind, some_shapes, dev)
+    table = state.table if use is None else state.table[use]
+    addresses = list(map(_address, some_params))
+    _distinct(addresses)
+    table["param"] = addresses
+    table["grad"] = list(map(_address, some_grads))
     if isinstance(weight_decay, (int, float)):
         table["decay"] = weight_decay
     else:
         decay = [float(d) for d in weight_decay]
         if len(decay) != n:
             raise ValueError(f"weight_decay must be a number or {n} of them")
-        table["decay"] = [decay[i] for i in use]
+        table["decay"] = decay if use is None else [decay[i] for i in use]
     how = _lib.PACK_ADAMW(_FLOATS[state.dtype], _FLOATS[kind], state.bits, state.seed, float(betas[0]),
                           float(betas[1]), float(lr), float(eps), math.inf if max_norm is None else float(max_norm),
                           _addr(lr_dev), _addr(grad_norm), state.m.data_ptr(), state.v.data_ptr(),
                           _addr(state.m_scale), _addr(state.v_scale), _addr(state.master), state.steps.data_ptr(),
                           state.done.data_ptr())
     with _launch(dev, stream) as handle:
-        _check(_lib.load().pvl_adamw_step(how, table.ctypes.data, len(use), handle))
-    torch.autograd.graph.increment_version([params[i] for i in use])
+        _check(_lib.load().pvl_adamw_step(how, table.ctypes.data, len(table), handle))
+    torch.autograd.graph.increment_version(some_params)
