@@ -279,8 +279,8 @@ def _run_own(st, case):
                                       mean=case["mean"])
         return out.loss, out.rewards, pvl.pack_preference_bwd(None, out.coef, st["ids"])
     if case["op"] == "policy":
-        how = dict(ref_logp=st["ref"], clip_low=case["low"], clip_high=case["high"], kl_weight=case["kl"],
-                   ratio=case["ratio"])
+        how = dict(ref_logp=st["ref"], clip_low=case["low"], clip_high=case["high"],
+                   kl_weight=case["kl"] if case["ref"] else 0.0, ratio=case["ratio"])
         out = pvl.pack_policy_fwd(st["logp"], st["old"], st["adv"], st["ids"], E, mean=case["mean"], **how)
         return out.loss, out.stats, pvl.pack_policy_bwd(None, st["logp"], st["old"], st["adv"], st["ids"], out.coef, **how)
     norm = pvl.grad_norm(st["grads"]) if case["clip"] else None
