@@ -248,8 +248,29 @@ __device__ __forceinline__ float block_top(const float (&f)[8]) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
 }
 
+// a + b, which the compiler may not make a multiply-add of the product that a
+// or b is (it does so with packed additions, rounding by name or not).
+__device__ __forceinline__ float2 sum_of(float2 a, float2 b) {
+  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
+
+// Quotients of a block's values by its scale, rounded to nearest: a product with
+// the reciprocal (itself rounded to nearest), corrected by its remainder, which a
+// multiply-add gives exactly (Markstein's theorem).  0 for a block below 2^-100.
+struct Divisor {
+  float scale, inverse;
+  __device__ __forceinline__ explicit Divisor(float top) {
+    scale = top < 0x1p-100f ? 0.0f : top * (1.0f / kTop);
+    inverse = top < 0x1p-100f ? 0.0f : __frcp_rn(scale);
+  }
+  __device__ __forceinline__ float2 quotient(float2 a) const {
+    const float2 y = make_float2(inverse, inverse), q = fmul2(a, y);
+    return ffma2(ffma2(q, make_float2(-scale, -scale), a), y, q);
+  }
+};
+
 // ---------------------------------------------------------------- step
-// What a chunk's elements share.
+// What a block's elements share.
 struct Shared {
   float clip, rate, second, keep;
   uint32_t key;
@@ -298,11 +319,18 @@ __device__ __forceinline__ void step_block(const StepParams& p, const Shared& c,
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
     const float2 gc = fmul2(make_float2(g[i], g[i + 1]), clip);
-    const float2 mm = ffma2(b1, make_float2(m[i], m[i + 1]), fmul2(c1, gc));
-    float2 vv = make_float2(v[i], v[i + 1]);
-    if constexpr (k8) vv = fmul2(vv, vv);
-    vv = ffma2(fmul2(c2, gc), gc, fmul2(b2, vv));
-    const float2 r = make_float2(root_of(vv.x), root_of(vv.y));
+    float2 mm = make_float2(m[i], m[i + 1]), vv = make_float2(v[i], v[i + 1]), r;
+    if constexpr (k8) {
+      // Each operation rounded by itself, and the root to nearest: moments whose codes are chosen by their last
+      // bits are then what plain fp32 arithmetic gives anywhere.
+      mm = sum_of(fmul2(mm, b1), fmul2(gc, c1));
+      vv = sum_of(fmul2(fmul2(vv, vv), b2), fmul2(fmul2(gc, gc), c2));
+      r = make_float2(__fsqrt_rn(vv.x), __fsqrt_rn(vv.y));
+    } else {
+      mm = ffma2(b1, mm, fmul2(c1, gc));
+      vv = ffma2(fmul2(c2, gc), gc, fmul2(b2, vv));
+      r = make_float2(root_of(vv.x), root_of(vv.y));
+    }
     const float2 d = ffma2(r, second, eps);
     const float2 q = fmul2(mm, make_float2(inverse(d.x), inverse(d.y)));
     const float2 ww = ffma2(make_float2(w[i], w[i + 1]), keep, fmul2(rate, q));
@@ -322,7 +350,7 @@ __device__ __forceinline__ void step_block(const StepParams& p, const Shared& c,
   if constexpr (k8) {
     const float tm = block_top(m), tv = block_top(root);
     // a block below 2^-100 becomes zeros: its scale would not be a normal number
-    const float im = tm < 0x1p-100f ? 0.0f : kTop * inverse(tm), iv = tv < 0x1p-100f ? 0.0f : kTop * inverse(tv);
+    const Divisor by_m(tm), by_v(tv);
     const uint32_t h = mix((static_cast<uint32_t>(sb) * 32u + lane) ^ c.key);
     const uint32_t rm[8] = {chance<1>(h), chance<2>(h), chance<3>(h), chance<4>(h),
                             chance<5>(h), chance<6>(h), chance<7>(h), chance<8>(h)};
@@ -330,8 +358,8 @@ __device__ __forceinline__ void step_block(const StepParams& p, const Shared& c,
                             chance<13>(h), chance<14>(h), chance<15>(h), chance<16>(h)};
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-      const float2 a = fmul2(make_float2(m[i], m[i + 1]), make_float2(im, im));
-      const float2 b = fmul2(make_float2(root[i], root[i + 1]), make_float2(iv, iv));
+      const float2 a = by_m.quotient(make_float2(m[i], m[i + 1]));
+      const float2 b = by_v.quotient(make_float2(root[i], root[i + 1]));
       m[i] = a.x, m[i + 1] = a.y;
       v[i] = b.x, v[i + 1] = b.y;
     }
@@ -353,8 +381,8 @@ __device__ __forceinline__ void step_block(const StepParams& p, const Shared& c,
     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.m) + st) = close_e4m3(m);
     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.v) + st) = close_e4m3(v);
     if (lane == 0) {
-      p.m_scale[sb] = tm < 0x1p-100f ? 0.0f : tm * (1.0f / kTop);
-      p.v_scale[sb] = tv < 0x1p-100f ? 0.0f : tv * (1.0f / kTop);
+      p.m_scale[sb] = by_m.scale;
+      p.v_scale[sb] = by_v.scale;
     }
   } else {
     st32(static_cast<float*>(p.m) + st, m);

@@ -16,7 +16,7 @@ import numpy as np
 import torch
 
 from . import _lib
-from .api import _addr, _check, _launch, _need, _need_cuda
+from .api import _addr, _check, _launch, _need
 
 BLOCK = 256     # elements that share a scale of the 8-bit moments
 
@@ -41,6 +41,8 @@ def _same_floats(tensors, name: str):
     dtype, dev = tensors[0].dtype, tensors[0].device
     if dtype not in _FLOATS:
         raise ValueError(f"{name} must be {torch.bfloat16} or {torch.float32}, got {dtype}")
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be CUDA tensors, got {dev}")
     if set(map(_dtype, tensors)) != {dtype} or set(map(_index, tensors)) != {tensors[0].get_device()} or (
             not all(map(_contiguous, tensors))):
         for i, t in enumerate(tensors):
@@ -128,8 +130,6 @@ def adamw_state(params, *, bits: int = 32, seed: int = 0) -> AdamWState:
         raise ValueError(f"bits must be 8 or 32, got {bits!r}")
     if not 0 <= int(seed) < 1 << 32:
         raise ValueError("seed must fit in 32 bits")
-    if params[0].device.type != "cuda":
-        raise ValueError(f"the kernels run on CUDA devices, not on {params[0].device}")
     dtype, dev = _same_floats(params, "params")
     _distinct([p.data_ptr() for p in params if p.numel()])     # empty ones have no address
     table = np.zeros(len(params), dtype=_TENSOR)
