@@ -539,7 +539,8 @@ PVL_API pvl_status masked_mse_loss_bwd(const pvl_bf16* pred, const pvl_bf16* tar
  * pack_logprob_fwd writes logp, lse and, where it is not null, the entropy.
  * pack_logprob_bwd takes lse (and, for dentropy, entropy) of the forward and
  *   writes dlogits, of the logits' type, at its own strides; it may be the
- *   logits themselves (same address and strides), not a shifted part of them.
+ *   logits themselves (same address and strides); else the spans of the two,
+ *   from the first element to the last, must not overlap.
  *   dlogp or dentropy may be null: zero.
  * Statistics are held in fp32; logp and entropy do not lose to a common offset
  * of a row's logits.  The gradient takes probabilities from lse, whose rounding
@@ -547,7 +548,8 @@ PVL_API pvl_status masked_mse_loss_bwd(const pvl_bf16* pred, const pvl_bf16* tar
  * lowest value has none.  It is rounded once to its type, and probabilities
  * below 2^-126 count as 0 in it.
  * Errors: INVALID_ARG for null pointers, sizes < 1, types, a temperature that
- * is not positive and finite, overlapping rows of dlogits; UNSUPPORTED for
+ * is not positive and finite, rows of dlogits that overlap one another or the
+ * logits; UNSUPPORTED for
  * V > 2^28, B L >= 2^27, B L V >= 2^42 or an address off its elements.
  * ---------------------------------------------------------------------- */
 typedef struct pvl_logprob {

@@ -336,7 +336,8 @@ __device__ __forceinline__ float kl_term(float f) {
     s = fmaf(s, f, 0.5f);
     return s * f * f;
   }
-  return expf(f) - 1.0f - f;
+  // far above, f + 1 is nothing beside exp f, and infinity less infinity is not taken
+  return f > 64.0f ? expf(f) : expf(f) - 1.0f - f;
 }
 
 // a > b, for pairs: the lower parts decide where the upper are equal.

@@ -511,6 +511,12 @@ extern "C" pvl_status pack_logprob_bwd(const pvl_logprob* how, const float* lse,
   if (batch_stride < 0 || token_stride < 0 || batch_stride >= (1ll << 46) || token_stride >= (1ll << 46) ||
       !(tokens_inside || batch_inside))
     return fail(PVL_ERR_INVALID_ARG, "pack_logprob_bwd: rows of dlogits overlap");
+  const uintptr_t from = reinterpret_cast<uintptr_t>(how->logits), to = reinterpret_cast<uintptr_t>(dlogits);
+  const uintptr_t reads = ((B - 1) * how->batch_stride + (L - 1) * how->token_stride + V) * es;
+  const uintptr_t writes = ((B - 1) * batch_stride + (L - 1) * token_stride + V) * es;
+  const bool same = from == to && (B == 1 || batch_stride == how->batch_stride) && (L == 1 || token_stride == how->token_stride);
+  if (!same && from < to + writes && to < from + reads)
+    return fail(PVL_ERR_INVALID_ARG, "pack_logprob_bwd: dlogits reaches into the logits without being them");
   p.lse_in = lse;
   p.ent_in = entropy;
   p.dlogp = dlogp;

@@ -93,7 +93,8 @@ def pack_logprob_bwd(dlogp, logits, targets, lse, seq_id=None, *, temperature: f
     """Gradient of pack_logprob_fwd to the logits, of their type: from dlogp
     (fp32 [B, L], or None for zero) and, with dent, from the gradient of the
     entropy (which needs ent, the forward's).  dlogits, where given, may have
-    strides of its own; it may be the logits, which are then overwritten."""
+    strides of its own; it may be the logits, which are then overwritten, but
+    not otherwise reach into them."""
     how, dev, shape = _logprob(logits, targets, seq_id, temperature)
     if dlogp is None and dent is None:
         raise ValueError("dlogp or dent must be given")

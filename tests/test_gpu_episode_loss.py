@@ -255,6 +255,11 @@ def test_policy_values_that_are_not_finite(pvl):
     out = pvl.pack_policy_fwd(lp, lp, torch.ones(1, 3, device="cuda"), ids, 1, ref_logp=ref)
     assert out.loss.item() == -1.0 and out.stats[0].item() == math.inf
     assert torch.isfinite(pvl.pack_policy_bwd(None, lp, lp, torch.ones(1, 3, device="cuda"), ids, out.coef, ref_logp=ref)).all()
+    # a log-probability of -inf: an infinite divergence, no NaN; one of the reference's too
+    gone = torch.tensor([[-math.inf, 0.0, 0.0]], device="cuda")
+    for a, b in ((gone, lp), (lp, gone)):
+        out = pvl.pack_policy_fwd(a, torch.zeros_like(lp), torch.ones(1, 3, device="cuda"), ids, 1, ref_logp=b, kl_weight=0.1)
+        assert out.loss.item() == math.inf and out.stats[0].item() == math.inf
     # a NaN stays in its token's gradient and reaches the loss
     lp[0, 1] = math.nan
     out = pvl.pack_policy_fwd(lp, torch.zeros_like(lp), torch.ones(1, 3, device="cuda"), ids, 1)

@@ -189,6 +189,18 @@ def test_gradient_over_the_logits(pvl, V):
         assert got is x and torch.equal(x, want)
 
 
+def test_upstream_gradients_of_padding_are_not_used(pvl):
+    x, t = make(2, 5, 333, torch.float32, 14)
+    ids = torch.tensor([[0, 0, -1, 0, -1], [1, 1, 1, 1, -1]], dtype=torch.int32, device="cuda")
+    logp, lse, h = pvl.pack_logprob_fwd(x, t, ids, entropy=True)
+    up, ue = torch.randn(2, 2, 5, device="cuda").unbind(0)
+    want = pvl.pack_logprob_bwd(up, x, t, lse, ids, ent=h, dent=ue)
+    for v in (up, ue, lse, h):
+        v[ids < 0] = math.nan
+    got = pvl.pack_logprob_bwd(up, x, t, lse, ids, ent=h, dent=ue)
+    assert torch.equal(got, want) and not got[ids < 0].any()
+
+
 def test_only_the_entropys_gradient(pvl):
     x, t = make(2, 5, 333, torch.float32, 11)
     logp, lse, h = pvl.pack_logprob_fwd(x, t, entropy=True)

@@ -75,6 +75,11 @@ def test_logprob_outputs(lib):  # noqa: F811
         assert lib.pack_logprob_bwd(how, P, None, P, None, P, sb, sl, None) == INVALID, (sb, sl)
         assert b"overlap" in lib.pvl_last_error_message()
     assert lib.pack_logprob_bwd(how, P, None, P, None, P + 1, 30, 10, None) == UNSUPPORTED
+    # 60 logits of 2 bytes from P on: anything within them but the logits themselves
+    for at, sb, sl in ((P + 2, 30, 10), (P - 2, 30, 10), (P + 118, 30, 10), (P - 118, 30, 10), (P, 30, 20), (P, 60, 10)):
+        assert lib.pack_logprob_bwd(how, P, None, P, None, at, sb, sl, None) == INVALID, (at, sb, sl)
+    assert lib.pack_logprob_bwd(how, P, None, P, None, P, 60, 10, None) == INVALID
+    assert b"reaches into" in lib.pvl_last_error_message()
 
 
 def preference(**kw):
