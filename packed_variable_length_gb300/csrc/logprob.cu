@@ -16,14 +16,17 @@
 // finite value: a logit of -inf then adds 0, and -inf - (-inf) never arises;
 // w clamps the exponent, so that a banned logit adds 0 and not 0 times -inf.
 //   Bound by HBM (V elements read once, 16-byte loads, four in flight a
-// thread).  A row goes to 8 threads (up to 64 vectors), to a warp (up to 256)
-// or to a block; where rows are so few that a block each leaves SMs idle, to a
-// cluster of eight blocks that join their states through shared memory.
+// thread).  A row goes to 8 threads, to a warp, to a block or to a cluster of
+// eight blocks that join their states through shared memory: as few threads as
+// still fill the device (launch rules below).
 //
 // Backward: elementwise, given lse and H: V elements read, V written.  A block
 // takes up to 4096 vectors of a row, so that what it looks up of the row is
 // shared by sixteen vectors a thread, the next four read while four are worked
-// on; rows of up to 512 vectors go to a warp each.
+// on; or a warp takes a row.
+//
+// Measured (one GB300, of the 6793 GB/s of its copy): 65,536 rows of 32,768 bf16
+// logits forward 619 us = 6.94 TB/s (102 %), backward 1227 us = 7.00 TB/s (103 %).
 //
 // Rows need no alignment: the elements up to the first 16-byte boundary and
 // those after the last whole vector go one by one.
@@ -438,21 +441,40 @@ pvl_status launch_fwd(const LogprobParams& p, cudaStream_t s) {
   return check_cuda(e, "pack_logprob_fwd launch");
 }
 
+// How many threads take a row, measured in microseconds (bf16, N rows of V, 8
+// logits a vector; a row's other choice beside it).
+//   8 threads, for up to 256 vectors, once rows are many enough that 8 threads
+// each fill the SMs, the more the longer they are: 20,000 x 256 3.9 (a warp
+// 10.1), x 1024 8.6 (10.4), x 2048 14.6 (15.8); 4864 x 256 2.5 (3.7), x 1024 3.7
+// (3.7), x 2048 5.6 (4.8: a warp); 1216 x 512 2.7 (2.3: a warp).
+//   A warp, for up to 2048 vectors, with eight rows an SM and more: 20,000 x 8192
+// 51 (a block 75), x 16,384 102 (113), x 32,768 195 (193: a block); 1216 x 8192
+// 5.3 (6.0); 300 x 8192 5.2 (2.9: a block).  With fewer rows up to 128 vectors:
+// 64 x 512 2.3 (2.3), 300 x 2048 2.9 (2.9).
+//   A cluster for few long rows, whose eight blocks must be worth their barrier:
+// 8 x 32,768 2.9 (a block 3.7), 64 x 128,000 5.6 (8.6), 152 x 128,000 10.9
+// (14.2); 8 x 16,384 3.1 (2.9: a block), 64 x 32,768 4.7 (3.9: a block).
 template <typename T>
 pvl_status fwd(const LogprobParams& p, cudaStream_t s) {
   const int64_t vectors = p.V / Vec<T>::n;
-  if (vectors <= 64) return launch_fwd<T, 8, false>(p, s);
-  if (vectors <= 256) return launch_fwd<T, 32, false>(p, s);
-  const int sms = sm_count();
+  const int64_t sms = sm_count();
   if (sms <= 0) return fail(PVL_ERR_CUDA, "pack_logprob_fwd: no usable CUDA device");
-  if (p.N <= sms && vectors >= 2048) return launch_fwd<T, kThreads, true>(p, s);
+  if (vectors <= 256 && 4 * p.N >= sms * vectors) return launch_fwd<T, 8, false>(p, s);
+  if (vectors <= 128 || (vectors <= 2048 && p.N >= 8 * sms)) return launch_fwd<T, 32, false>(p, s);
+  if (vectors >= 4096 && 80 * p.N <= vectors) return launch_fwd<T, kThreads, true>(p, s);
   return launch_fwd<T, kThreads, false>(p, s);
 }
 
+// A warp or a block a row (microseconds as above): a warp 20,000 x 2048 26 (a
+// block 67), x 8192 100 (118), x 16,384 207 (196: a block), 1216 x 8192 5.6 (6.2);
+// with fewer rows than eight an SM up to 64 vectors: 300 x 512 2.3 (2.5), x 2048
+// 3.1 (2.6: a block).
 template <typename T, bool kEnt>
 pvl_status launch_bwd(const LogprobParams& p, cudaStream_t s) {
   const int64_t vectors = p.V / Vec<T>::n;
-  if (vectors > 512) {
+  const int64_t sms = sm_count();
+  if (sms <= 0) return fail(PVL_ERR_CUDA, "pack_logprob_bwd: no usable CUDA device");
+  if (vectors > 1024 || (vectors > 64 && p.N < 8 * sms)) {
     const int64_t per_row = (vectors + kSegVec - 1) / kSegVec;
     if (p.N * per_row >= (1ll << 31)) return fail(PVL_ERR_UNSUPPORTED, "pack_logprob_bwd: too many rows");
     logprob_bwd_kernel<T, kEnt, true><<<static_cast<unsigned>(p.N * per_row), kThreads, 0, s>>>(

@@ -99,6 +99,42 @@ def test_few_rows_of_many_logits(pvl, rows, dtype, V):
     check(pvl, x, t, at=[(0, 0), (rows[0] - 1, rows[1] - 1)])
 
 
+@pytest.mark.parametrize("N,V,dtype", [(1215, 256, torch.bfloat16), (1216, 256, torch.bfloat16), (5000, 1009, torch.bfloat16),
+                                       (9727, 2048, torch.bfloat16), (9729, 2055, torch.bfloat16), (9729, 1027, torch.float32),
+                                       (1215, 8191, torch.bfloat16), (1217, 8197, torch.bfloat16), (1217, 16391, torch.bfloat16),
+                                       (1300, 8193, torch.float32), (50, 32768, torch.bfloat16), (52, 32768, torch.bfloat16),
+                                       (200, 128001, torch.bfloat16), (3000, 33000, torch.bfloat16)])
+def test_both_sides_of_the_rules_on_rows(pvl, N, V, dtype):
+    """Many rows, against torch in 64 bits on the device; every thread of a row may add V / 8 terms."""
+    x, t = make(1, N, V, dtype, N)
+    up, ue = randn(1, N, seed=1), randn(1, N, seed=2)
+    logp, lse, h = pvl.pack_logprob_fwd(x, t, entropy=True)
+    d = pvl.pack_logprob_bwd(up, x, t, lse, ent=h, dent=ue)
+    rel = 2.0 ** -20 + V / 8 * 2.0 ** -24
+    unit = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -23
+    for i in range(0, N, 500):
+        at = slice(i, i + 500)
+        logs = torch.log_softmax(x[0, at].double(), 1)
+        p = logs.exp()
+        pick = t[0, at, None].long()
+        top = x[0, at].double().abs().amax(1)
+        s = torch.logsumexp(x[0, at].double(), 1)
+        ent = -(p * logs).sum(1)
+        tol = rel + 2.0 ** -22 * (top + s.abs())
+        assert ((logp[0, at] - logs.gather(1, pick)[:, 0]).abs() <= tol + 2.0 ** -22 * logs.gather(1, pick)[:, 0].abs()).all()
+        assert ((lse[0, at] - s).abs() <= tol).all()
+        assert ((h[0, at] - ent).abs() <= rel * (4 + 2 * math.log(V)) + 2.0 ** -22 * ent).all()
+        g, ge = up[0, at, None].double(), ue[0, at, None].double()
+        want = -p * (g + ge * (logs + ent[:, None]))
+        want.scatter_add_(1, pick, g)
+        slack = p * (tol[:, None] + 2.0 ** -22 * (2 + logs.abs())) * (g.abs() + ge.abs() * (logs.abs() + ent[:, None] + 2))
+        assert ((d[0, at].double() - want).abs() <= unit * want.abs() + slack + 2.0 ** -120).all()
+
+
+def randn(*shape, seed):
+    return torch.randn(*shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+
+
 def test_padding_targets_and_temperature(pvl):
     """Invalid tokens, by id and by target, hold NaN and infinities; int64 targets; temperatures."""
     for T in (0.25, 1.0, 3.0):
