@@ -27,9 +27,17 @@
 // a block at a time, eight elements a lane, all its loads issued before the
 // first is used, and arithmetic in packed pairs; the tables of tensors come as
 // kernel parameters, so a step copies nothing to the device and can be
-// captured.  A tensor's step count is on the
-// device and counted up by the last block of the grid to finish, when all have
-// read it.
+// captured.  A tensor's step count is on the device and counted up by the last
+// block of the grid to finish, when all have read it.
+//
+// Measured (one GB300, of the 6793 GB/s of its copy): 680 M parameters, bf16 over
+// fp32 masters, bf16 gradients: 32-bit moments 2947 us = 6.46 TB/s (95 %), 8-bit
+// 1788 us = 6.11 TB/s (90 %); 28 M parameters in fp32 131 us = 6.13 TB/s; the norm
+// of 680 M bf16 gradients 214 us = 6.37 TB/s (94 %).  With 8-bit moments half the
+// bytes go in pieces of 256 and less a warp and stream (five streams to read,
+// five to write), and issue slots are 63 % full: chunks of four blocks a warp
+// (1861 us), the next block's loads ahead of this one's arithmetic (1866 us) and
+// no random bits at all (1888 us beside 1861) moved it less than what is left.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -43,7 +51,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlock = 256;        // elements that share a scale
-constexpr int kFew = 32, kMany = 512;  // tensors of a launch
+// Tensors of a launch.  The table of 512 is 22 KB of kernel parameters; handing it
+// over for a few tensors costs the caller 4 us a step (36 beside 32).
+constexpr int kFew = 32, kMany = 512;
 constexpr float kTop = 448.0f;     // largest e4m3 value
 constexpr int kNormUnit = 1024;    // elements a warp takes at a time for the norm
 constexpr int kMaxNormCtas = 4096;

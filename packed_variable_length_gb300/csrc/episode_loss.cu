@@ -25,6 +25,14 @@
 // whose tokens belong to several.  The last block to
 // finish turns the episodes' sums into the loss and the table.
 //
+// Measured (one GB300; a captured forward and backward together, with the clear
+// of the sums): the 64k pack's policy loss 16.4 us, 262,144 tokens of 512 episodes
+// 17.5 us, preferences of four episodes of 10,944 tokens 13.1 us, of 512 episodes
+// in 2048 pairs 19.1 us; what they move takes 0.1 to 0.8 us.  One cluster of eight
+// blocks of 1024 threads instead, which needs no clear, took 24 us for the 64k
+// pack: a token costs a hundred instructions, and eight SMs issue them.  Sums in
+// 64-bit floating point took twice the time.
+//
 // Sums are integers, so that they are the same whatever order blocks finish in,
 // and exact.  A token's value in units of 2^-40 (rounded once; differences are
 // taken as exact pairs of fp32 values first) is added in 64 bits within the
