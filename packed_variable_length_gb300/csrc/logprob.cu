@@ -23,7 +23,7 @@
 // Backward: elementwise, given lse and H: V elements read, V written.  A block
 // takes up to 4096 vectors of a row, so that what it looks up of the row is
 // shared by sixteen vectors a thread, the next four read while four are worked
-// on; or a warp takes a row.
+// on; shorter rows go to a warp or 8 threads.
 //
 // Measured (one GB300, of the 6793 GB/s of its copy): 65,536 rows of 32,768 bf16
 // logits forward 619 us = 6.94 TB/s (102 %), backward 1227 us = 7.00 TB/s (103 %).
@@ -352,15 +352,14 @@ __device__ __forceinline__ void grad_vectors(const RowGrad& g, float inv_t, cons
   }
 }
 
-// kBlock: per_row blocks share a row, kSegVec vectors each; else a warp takes a
-// row.
-template <typename T, bool kEnt, bool kBlock>
+// kG threads a row (8, 32), or per_row blocks of kSegVec vectors each.
+template <typename T, bool kEnt, int kG>
 __global__ void __launch_bounds__(kThreads, 3) logprob_bwd_kernel(const LogprobParams p, uint32_t per_row) {
   constexpr int kN = Vec<T>::n;
-  constexpr int kStep = kBlock ? kThreads : 32;
-  const int lane = threadIdx.x % kStep;
+  constexpr bool kBlock = kG == kThreads;
+  const int lane = threadIdx.x % kG;
   const int64_t row = kBlock ? blockIdx.x / per_row
-                             : static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
+                             : static_cast<int64_t>(blockIdx.x) * (kThreads / kG) + threadIdx.x / kG;
   if (row >= p.N) return;
   const int seg = kBlock ? static_cast<int>(blockIdx.x % per_row) : 0;
   const int64_t b = row / p.L, l = row - b * p.L;
@@ -374,16 +373,16 @@ __global__ void __launch_bounds__(kThreads, 3) logprob_bwd_kernel(const LogprobP
   const int end = kBlock ? min(nvec, (seg + 1) * kSegVec) : nvec;
   const RowGrad g = row_grad<kEnt>(p, row);
   if (g.target < 0) {
-    for (int i = first; i < end; i += kStep)
+    for (int i = first; i < end; i += kG)
       *reinterpret_cast<uint4*>(dx + head + static_cast<int64_t>(i) * kN) = make_uint4(0u, 0u, 0u, 0u);
   } else if (same) {
-    grad_vectors<T, kEnt, true>(g, p.inv_t, x + head, dx + head, g.target - head, first, kStep, end);
+    grad_vectors<T, kEnt, true>(g, p.inv_t, x + head, dx + head, g.target - head, first, kG, end);
   } else {
-    grad_vectors<T, kEnt, false>(g, p.inv_t, x + head, dx + head, g.target - head, first, kStep, end);
+    grad_vectors<T, kEnt, false>(g, p.inv_t, x + head, dx + head, g.target - head, first, kG, end);
   }
-  const int rest = p.V - nvec * kN;
-  if (seg == 0 && lane < rest) {
-    const int j = lane < head ? lane : nvec * kN + lane;
+  const int rest = seg == 0 ? p.V - nvec * kN : 0;
+  for (int r = lane; r < rest; r += kG) {
+    const int j = r < head ? r : nvec * kN + r;
     float f = 0.0f;
     if (g.target >= 0) {
       f = grad_of<kEnt>(Vec<T>::one(x + j), p.inv_t, g);
@@ -465,23 +464,27 @@ pvl_status fwd(const LogprobParams& p, cudaStream_t s) {
   return launch_fwd<T, kThreads, false>(p, s);
 }
 
-// A warp or a block a row (microseconds as above): a warp 20,000 x 2048 26 (a
-// block 67), x 8192 100 (118), x 16,384 207 (196: a block), 1216 x 8192 5.6 (6.2);
-// with fewer rows than eight an SM up to 64 vectors: 300 x 512 2.3 (2.5), x 2048
-// 3.1 (2.6: a block).
+// 8 threads, a warp or a block a row (microseconds as above).  8 threads: 20,000 x
+// 256 4.3 (a warp 7.8), x 512 6.4 (9.3), x 1024 12.5 (12.2: a warp), 4864 x 512 3.1
+// (3.2).  A warp: 20,000 x 2048 26 (a block 67), x 8192 100 (118), x 16,384 207
+// (196: a block), 1216 x 8192 5.6 (6.2); with fewer rows than eight an SM up to 64
+// vectors: 300 x 512 2.3 (2.5), x 2048 3.1 (2.6: a block).
 template <typename T, bool kEnt>
 pvl_status launch_bwd(const LogprobParams& p, cudaStream_t s) {
   const int64_t vectors = p.V / Vec<T>::n;
   const int64_t sms = sm_count();
   if (sms <= 0) return fail(PVL_ERR_CUDA, "pack_logprob_bwd: no usable CUDA device");
-  if (vectors > 1024 || (vectors > 64 && p.N < 8 * sms)) {
+  if (vectors <= 64 && 4 * p.N >= sms * vectors) {
+    constexpr int kRows = kThreads / 8;
+    logprob_bwd_kernel<T, kEnt, 8><<<static_cast<unsigned>((p.N + kRows - 1) / kRows), kThreads, 0, s>>>(p, 1);
+  } else if (vectors > 1024 || (vectors > 64 && p.N < 8 * sms)) {
     const int64_t per_row = (vectors + kSegVec - 1) / kSegVec;
     if (p.N * per_row >= (1ll << 31)) return fail(PVL_ERR_UNSUPPORTED, "pack_logprob_bwd: too many rows");
-    logprob_bwd_kernel<T, kEnt, true><<<static_cast<unsigned>(p.N * per_row), kThreads, 0, s>>>(
+    logprob_bwd_kernel<T, kEnt, kThreads><<<static_cast<unsigned>(p.N * per_row), kThreads, 0, s>>>(
         p, static_cast<uint32_t>(per_row));
   } else {
     constexpr int kRows = kThreads / 32;
-    logprob_bwd_kernel<T, kEnt, false><<<static_cast<unsigned>((p.N + kRows - 1) / kRows), kThreads, 0, s>>>(p, 1);
+    logprob_bwd_kernel<T, kEnt, 32><<<static_cast<unsigned>((p.N + kRows - 1) / kRows), kThreads, 0, s>>>(p, 1);
   }
   return check_cuda(cudaGetLastError(), "pack_logprob_bwd launch");
 }
