@@ -99,7 +99,8 @@ def test_few_rows_of_many_logits(pvl, rows, dtype, V):
     check(pvl, x, t, at=[(0, 0), (rows[0] - 1, rows[1] - 1)])
 
 
-@pytest.mark.parametrize("N,V,dtype", [(1215, 256, torch.bfloat16), (1216, 256, torch.bfloat16), (5000, 1009, torch.bfloat16),
+@pytest.mark.parametrize("N,V,dtype", [(20000, 2, torch.bfloat16), (20000, 23, torch.bfloat16), (20000, 509, torch.bfloat16),
+                                       (20000, 253, torch.float32), (1215, 256, torch.bfloat16), (1216, 256, torch.bfloat16), (5000, 1009, torch.bfloat16),
                                        (9727, 2048, torch.bfloat16), (9729, 2055, torch.bfloat16), (9729, 1027, torch.float32),
                                        (1215, 8191, torch.bfloat16), (1217, 8197, torch.bfloat16), (1217, 16391, torch.bfloat16),
                                        (1300, 8193, torch.float32), (50, 32768, torch.bfloat16), (52, 32768, torch.bfloat16),
