@@ -88,6 +88,19 @@ class _Here:
         return False
 
 
+_current_device_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _here(device, stream):
+    """Handle of the current stream where nothing has to be switched for a call on `device`, else None; for calls whose
+    tensors are there already, so that CUDA has been initialised."""
+    if stream is None and device.type == "cuda":
+        index = _current_device_index()
+        if device.index == index:
+            return _current_stream_handle(index)
+    return None
+
+
 @contextlib.contextmanager
 def _there(device, stream):
     with torch.cuda.device(device):

@@ -15,7 +15,7 @@ from typing import NamedTuple
 import torch
 
 from . import _lib
-from .api import _addr, _check, _launch, _need, _need_cuda, _ptr
+from .api import _addr, _check, _here, _launch, _need, _need_cuda, _ptr
 
 _F32, _BF16, _I32, _I64 = torch.float32, torch.bfloat16, torch.int32, torch.int64
 
@@ -81,10 +81,17 @@ def pack_logprob_fwd(logits, targets, seq_id=None, *, temperature: float = 1.0, 
     logits[..., :V]).  Tokens whose seq_id (int32 [B, L], optional) is negative
     or whose target lies outside [0, V) give zeros and are not read."""
     how, dev, shape = _logprob(logits, targets, seq_id, temperature)
-    with _launch(dev, stream) as handle:
-        logp, lse = _rows(logp, "logp", shape, dev), _rows(lse, "lse", shape, dev)
-        ent = _rows(ent, "ent", shape, dev) if entropy else None
-        _check(_lib.load().pack_logprob_fwd(how, logp.data_ptr(), lse.data_ptr(), _ptr(ent), handle))
+    handle = _here(dev, stream)
+    if handle is None:
+        with _launch(dev, stream) as handle:
+            return _run_logprob(how, dev, shape, logp, lse, ent, entropy, handle)
+    return _run_logprob(how, dev, shape, logp, lse, ent, entropy, handle)
+
+
+def _run_logprob(how, dev, shape, logp, lse, ent, entropy, handle):
+    logp, lse = _rows(logp, "logp", shape, dev), _rows(lse, "lse", shape, dev)
+    ent = _rows(ent, "ent", shape, dev) if entropy else None
+    _check(_lib.load().pack_logprob_fwd(how, logp.data_ptr(), lse.data_ptr(), _ptr(ent), handle))
     return logp, lse, ent
 
 
@@ -107,12 +114,19 @@ def pack_logprob_bwd(dlogp, logits, targets, lse, seq_id=None, *, temperature: f
         if not isinstance(dlogits, torch.Tensor) or dlogits.dtype is not logits.dtype or (
                 dlogits.shape != logits.shape or dlogits.device != dev):
             raise ValueError(f"dlogits must be {logits.dtype} {tuple(logits.shape)} on {dev}")
-    with _launch(dev, stream) as handle:
-        if dlogits is None:
-            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-        sb, sl = _row_strides(dlogits, "dlogits")
-        _check(_lib.load().pack_logprob_bwd(how, lse.data_ptr(), _ptr(ent), _ptr(dlogp), _ptr(dent),
-                                            dlogits.data_ptr(), sb, sl, handle))
+    handle = _here(dev, stream)
+    if handle is None:
+        with _launch(dev, stream) as handle:
+            return _run_logprob_bwd(how, logits, lse, ent, dlogp, dent, dlogits, handle)
+    return _run_logprob_bwd(how, logits, lse, ent, dlogp, dent, dlogits, handle)
+
+
+def _run_logprob_bwd(how, logits, lse, ent, dlogp, dent, dlogits, handle):
+    if dlogits is None:
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    sb, sl = _row_strides(dlogits, "dlogits")
+    _check(_lib.load().pack_logprob_bwd(how, lse.data_ptr(), _ptr(ent), _ptr(dlogp), _ptr(dent), dlogits.data_ptr(),
+                                        sb, sl, handle))
     return dlogits
 
 
@@ -135,9 +149,9 @@ def _tokens(seq_id):
     return seq_id.device, seq_id.shape
 
 
-def _of_tokens(tensors, names, shape, dev) -> None:
-    """Every tensor of the list that is there is fp32, of the shape, contiguous and on the device; the first is there."""
-    for t, name in zip(tensors, names):
+def _of_tokens(shape, dev, **tensors) -> None:
+    """Says which of the tensors (None where they are left out) is not fp32, of the shape, contiguous, on the device."""
+    for name, t in tensors.items():
         if t is None and name != "logp":
             continue
         if not isinstance(t, torch.Tensor):
@@ -182,7 +196,7 @@ def pack_preference_fwd(logp, ref_logp, seq_id, pairs, episodes: int, *, beta: f
     sigmoid(-beta h); "squared": (h - 1 / (2 beta))^2; "hinge": max(0, 1 - beta
     h).  A pair with a negative id is left out."""
     dev, shape = _tokens(seq_id)
-    _of_tokens((logp, ref_logp), ("logp", "ref_logp"), shape, dev)
+    _of_tokens(shape, dev, logp=logp, ref_logp=ref_logp)
     if kind not in _PREFERENCES:
         raise ValueError(f"kind must be one of {sorted(_PREFERENCES)}, got {kind!r}")
     if not isinstance(pairs, torch.Tensor) or pairs.dim() != 2 or pairs.shape[1] != 2:
@@ -191,14 +205,20 @@ def pack_preference_fwd(logp, ref_logp, seq_id, pairs, episodes: int, *, beta: f
     E, P = int(episodes), pairs.shape[0]
     how = _lib.PACK_PREFERENCE(seq_id.numel(), E, P, _PREFERENCES[kind], 1 if mean else 0, beta, smoothing, margin,
                                logp.data_ptr(), _addr(ref_logp), seq_id.data_ptr(), pairs.data_ptr())
-    nbytes = _preference_ws_bytes(E)
-    with _launch(dev, stream) as handle:
-        ws = _workspace(ws, nbytes, dev)
-        loss = torch.empty(1, dtype=_F32, device=dev)
-        rewards = torch.empty((P, 2), dtype=_F32, device=dev)
-        coef = torch.empty(max(E, 1), dtype=_F32, device=dev)
-        _check(_lib.load().pack_preference_fwd(how, loss.data_ptr(), rewards.data_ptr(), coef.data_ptr(),
-                                               ws.data_ptr(), ws.numel(), handle))
+    handle = _here(dev, stream)
+    if handle is None:
+        with _launch(dev, stream) as handle:
+            return _run_preference(how, dev, E, P, ws, handle)
+    return _run_preference(how, dev, E, P, ws, handle)
+
+
+def _run_preference(how, dev, E, P, ws, handle):
+    ws = _workspace(ws, _preference_ws_bytes(E), dev)
+    loss = torch.empty(1, dtype=_F32, device=dev)
+    rewards = torch.empty((P, 2), dtype=_F32, device=dev)
+    coef = torch.empty(max(E, 1), dtype=_F32, device=dev)
+    _check(_lib.load().pack_preference_fwd(how, loss.data_ptr(), rewards.data_ptr(), coef.data_ptr(), ws.data_ptr(),
+                                           ws.numel(), handle))
     return PreferenceLoss(loss, rewards, coef)
 
 
@@ -211,10 +231,17 @@ def pack_preference_bwd(dloss, coef, seq_id, *, dlogp=None, stream=None):
     _tensor(coef, "coef", _F32, coef.shape, dev)
     if dloss is not None:
         _scalar(dloss, dev)
-    with _launch(dev, stream) as handle:
-        dlogp = _rows(dlogp, "dlogp", shape, dev)
-        _check(_lib.load().pack_preference_bwd(_ptr(dloss), coef.data_ptr(), seq_id.data_ptr(), seq_id.numel(),
-                                               coef.shape[0], dlogp.data_ptr(), handle))
+    handle = _here(dev, stream)
+    if handle is None:
+        with _launch(dev, stream) as handle:
+            return _run_preference_bwd(dloss, coef, seq_id, dlogp, shape, dev, handle)
+    return _run_preference_bwd(dloss, coef, seq_id, dlogp, shape, dev, handle)
+
+
+def _run_preference_bwd(dloss, coef, seq_id, dlogp, shape, dev, handle):
+    dlogp = _rows(dlogp, "dlogp", shape, dev)
+    _check(_lib.load().pack_preference_bwd(_ptr(dloss), coef.data_ptr(), seq_id.data_ptr(), seq_id.numel(),
+                                           coef.shape[0], dlogp.data_ptr(), handle))
     return dlogp
 
 
@@ -237,7 +264,7 @@ _OVER = {"token": 0, "episode": 1}
 
 def _policy(logp, old_logp, advantages, seq_id, episodes, ref_logp, clip_low, clip_high, kl_weight, ratio, mean):
     dev, shape = _tokens(seq_id)
-    _of_tokens((logp, old_logp, ref_logp), ("logp", "old_logp", "ref_logp"), shape, dev)
+    _of_tokens(shape, dev, logp=logp, old_logp=old_logp, ref_logp=ref_logp)
     if ratio not in _OVER or mean not in _OVER:
         raise ValueError(f"ratio and mean must be 'token' or 'episode', got {ratio!r} and {mean!r}")
     if not isinstance(advantages, torch.Tensor):
@@ -268,14 +295,20 @@ def pack_policy_fwd(logp, old_logp, advantages, seq_id, episodes: int, *, ref_lo
     the episodes' means)."""
     E = int(episodes)
     how, dev, _ = _policy(logp, old_logp, advantages, seq_id, E, ref_logp, clip_low, clip_high, kl_weight, ratio, mean)
-    nbytes = _policy_ws_bytes(E)
-    with _launch(dev, stream) as handle:
-        ws = _workspace(ws, nbytes, dev)
-        loss = torch.empty(1, dtype=_F32, device=dev)
-        stats = torch.empty(2, dtype=_F32, device=dev)
-        coef = torch.empty((max(E, 1), 2), dtype=_F32, device=dev)
-        _check(_lib.load().pack_policy_fwd(how, loss.data_ptr(), stats.data_ptr(), coef.data_ptr(), ws.data_ptr(),
-                                           ws.numel(), handle))
+    handle = _here(dev, stream)
+    if handle is None:
+        with _launch(dev, stream) as handle:
+            return _run_policy(how, dev, E, ws, handle)
+    return _run_policy(how, dev, E, ws, handle)
+
+
+def _run_policy(how, dev, E, ws, handle):
+    ws = _workspace(ws, _policy_ws_bytes(E), dev)
+    loss = torch.empty(1, dtype=_F32, device=dev)
+    stats = torch.empty(2, dtype=_F32, device=dev)
+    coef = torch.empty((max(E, 1), 2), dtype=_F32, device=dev)
+    _check(_lib.load().pack_policy_fwd(how, loss.data_ptr(), stats.data_ptr(), coef.data_ptr(), ws.data_ptr(),
+                                       ws.numel(), handle))
     return PolicyLoss(loss, stats, coef)
 
 
@@ -290,7 +323,14 @@ def pack_policy_bwd(dloss, logp, old_logp, advantages, seq_id, coef, *, ref_logp
     _tensor(coef, "coef", _F32, coef.shape, dev)
     if dloss is not None:
         _scalar(dloss, dev)
-    with _launch(dev, stream) as handle:
-        dlogp = _rows(dlogp, "dlogp", shape, dev)
-        _check(_lib.load().pack_policy_bwd(how, _ptr(dloss), coef.data_ptr(), dlogp.data_ptr(), handle))
+    handle = _here(dev, stream)
+    if handle is None:
+        with _launch(dev, stream) as handle:
+            return _run_policy_bwd(how, dloss, coef, dlogp, shape, dev, handle)
+    return _run_policy_bwd(how, dloss, coef, dlogp, shape, dev, handle)
+
+
+def _run_policy_bwd(how, dloss, coef, dlogp, shape, dev, handle):
+    dlogp = _rows(dlogp, "dlogp", shape, dev)
+    _check(_lib.load().pack_policy_bwd(how, _ptr(dloss), coef.data_ptr(), dlogp.data_ptr(), handle))
     return dlogp

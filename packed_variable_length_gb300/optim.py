@@ -9,6 +9,7 @@ copies nothing to the device, so it can be captured into a CUDA graph.
 from __future__ import annotations
 
 import math
+from array import array
 from dataclasses import dataclass, field
 from operator import attrgetter
 
@@ -16,7 +17,7 @@ import numpy as np
 import torch
 
 from . import _lib
-from .api import _addr, _check, _launch, _need
+from .api import _addr, _check, _here, _launch, _need
 
 BLOCK = 256     # elements that share a scale of the 8-bit moments
 
@@ -33,11 +34,19 @@ _contiguous, _index, _address, _count = (torch.Tensor.is_contiguous, torch.Tenso
                                          torch.Tensor.numel)
 
 
+_KINDS = {torch.Tensor, torch.nn.Parameter}
+
+
+def _tensors(tensors, name: str, use=None) -> None:
+    if not _KINDS.issuperset(map(type, tensors)):
+        for i, t in enumerate(tensors):
+            if not isinstance(t, torch.Tensor):
+                raise ValueError(f"{name}[{i if use is None else use[i]}] must be a tensor")
+
+
 def _same_floats(tensors, name: str):
     """The dtype and device that all of the list share; every tensor contiguous."""
-    for i, t in enumerate(tensors):
-        if not isinstance(t, torch.Tensor):
-            raise ValueError(f"{name}[{i}] must be a tensor")
+    _tensors(tensors, name)
     dtype, dev = tensors[0].dtype, tensors[0].device
     if dtype not in _FLOATS:
         raise ValueError(f"{name} must be {torch.bfloat16} or {torch.float32}, got {dtype}")
@@ -61,21 +70,26 @@ def grad_norm(grads, out=None, ws=None, stream=None) -> torch.Tensor:
         counts = [n for n in counts if n]
     if not grads:
         raise ValueError("grad_norm needs a gradient")
+    handle = _here(dev, stream)
+    if handle is None:
+        with _launch(dev, stream) as handle:
+            return _run_norm(grads, counts, _FLOATS[dtype], dev, out, ws, handle)
+    return _run_norm(grads, counts, _FLOATS[dtype], dev, out, ws, handle)
+
+
+def _run_norm(grads, counts, kind, dev, out, ws, handle):
     lib = _lib.load()
-    with _launch(dev, stream) as handle:
-        if out is None:
-            out = torch.empty(1, dtype=torch.float32, device=dev)
-        else:
-            _need(out, "out", torch.float32, (1,), dev)
-        nbytes = int(lib.pvl_grad_norm_ws_bytes())
-        if ws is None:
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        else:
-            _need(ws, "ws", torch.uint8, ws.shape, dev)
-        ptrs = np.array(list(map(_address, grads)), dtype=np.uint64)
-        sizes = np.array(counts, dtype=np.int64)
-        _check(lib.pvl_grad_norm(ptrs.ctypes.data, sizes.ctypes.data, len(grads), _FLOATS[dtype], out.data_ptr(),
-                                 ws.data_ptr(), ws.numel(), handle))
+    if out is None:
+        out = torch.empty(1, dtype=torch.float32, device=dev)
+    else:
+        _need(out, "out", torch.float32, (1,), dev)
+    if ws is None:
+        ws = torch.empty(lib.pvl_grad_norm_ws_bytes(), dtype=torch.uint8, device=dev)
+    else:
+        _need(ws, "ws", torch.uint8, ws.shape, dev)
+    ptrs, sizes = array("Q", map(_address, grads)), array("q", counts)
+    _check(lib.pvl_grad_norm(ptrs.buffer_info()[0], sizes.buffer_info()[0], len(grads), kind, out.data_ptr(),
+                             ws.data_ptr(), ws.numel(), handle))
     return out
 
 
@@ -99,6 +113,8 @@ class AdamWState:
     dtype: torch.dtype          # of the parameters
     shapes: tuple
     blocks: tuple               # first block of each parameter
+    total: int                  # blocks
+    empty: bool                 # whether a parameter has no elements
     table: np.ndarray = field(repr=False)
 
     def _part(self, t, i: int):
@@ -147,7 +163,8 @@ def adamw_state(params, *, bits: int = 32, seed: int = 0) -> AdamWState:
         scales = tuple(torch.zeros(total, dtype=torch.float32, device=dev) for _ in range(2))
     state = AdamWState(m, v, *scales, None, torch.zeros(len(params), dtype=torch.int32, device=dev),
                        torch.zeros(1, dtype=torch.int32, device=dev), bits, int(seed), dtype,
-                       tuple(tuple(p.shape) for p in params), tuple(int(b) for b in table["block"]), table)
+                       tuple(tuple(p.shape) for p in params), tuple(int(b) for b in table["block"]), total,
+                       not table["size"].all(), table)
     if dtype is torch.bfloat16:
         state.master = torch.zeros(total * BLOCK, dtype=torch.float32, device=dev)
         for i, p in enumerate(params):
@@ -157,9 +174,7 @@ def adamw_state(params, *, bits: int = 32, seed: int = 0) -> AdamWState:
 
 def _like(tensors, name: str, use, dtype, shapes, dev) -> None:
     """Every tensor of the list has the dtype, its shape and the device, and is contiguous; `use`: their places."""
-    for i, t in enumerate(tensors):
-        if not isinstance(t, torch.Tensor):
-            raise ValueError(f"{name}[{i if use is None else use[i]}] must be a tensor")
+    _tensors(tensors, name, use)
     if set(map(_dtype, tensors)) != {dtype} or set(map(_index, tensors)) != {dev.index} or (
             not all(map(_contiguous, tensors)) or list(map(_shape, tensors)) != list(shapes)):
         for i, (t, shape) in enumerate(zip(tensors, shapes)):
@@ -189,17 +204,19 @@ def adamw_step(params, grads, state: AdamWState, lr, *, betas=(0.9, 0.999), eps:
     dev = state.m.device
     if betas is None or len(betas) != 2:
         raise ValueError("betas must be two numbers")
-    moment = torch.float32 if state.bits == 32 else torch.float8_e4m3fn
-    last = state.table[-1]
-    blocks = int(last["block"]) - (-int(last["size"]) // BLOCK)
-    for name in ("m", "v"):
-        _need(getattr(state, name), f"state.{name}", moment, (blocks * BLOCK,), dev)
-        if state.bits == 8:
-            _need(getattr(state, name + "_scale"), f"state.{name}_scale", torch.float32, (blocks,), dev)
+    blocks, elements = (state.total,), (state.total * BLOCK,)
+    if state.bits == 32:
+        parts = (("m", torch.float32, elements), ("v", torch.float32, elements))
+    else:
+        parts = (("m", torch.float8_e4m3fn, elements), ("v", torch.float8_e4m3fn, elements),
+                 ("m_scale", torch.float32, blocks), ("v_scale", torch.float32, blocks))
     if state.dtype is torch.bfloat16:
-        _need(state.master, "state.master", torch.float32, (blocks * BLOCK,), dev)
-    _need(state.steps, "state.steps", torch.int32, (n,), dev)
-    _need(state.done, "state.done", torch.int32, (1,), dev)
+        parts += (("master", torch.float32, elements),)
+    for name, dtype, shape in parts + (("steps", torch.int32, (n,)), ("done", torch.int32, (1,))):
+        t = getattr(state, name)
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.device != dev or (
+                not t.is_contiguous()):
+            _need(t, f"state.{name}", dtype, shape, dev)
     if grad_norm is not None:
         _need(grad_norm, "grad_norm", torch.float32, (1,), dev)
     elif max_norm is not None:
@@ -211,7 +228,7 @@ def adamw_step(params, grads, state: AdamWState, lr, *, betas=(0.9, 0.999), eps:
         _need(lr, "lr", torch.float32, lr.shape, dev)
         lr, lr_dev = 0.0, lr
     use = None      # which parameters step: None for all
-    if any(g is None for g in grads) or not state.table["size"].all():
+    if state.empty or type(None) in set(map(type, grads)):
         use = [i for i, g in enumerate(grads) if g is not None and state.table["size"][i]]
         if not use:
             return
@@ -240,6 +257,10 @@ def adamw_step(params, grads, state: AdamWState, lr, *, betas=(0.9, 0.999), eps:
                           _addr(lr_dev), _addr(grad_norm), state.m.data_ptr(), state.v.data_ptr(),
                           _addr(state.m_scale), _addr(state.v_scale), _addr(state.master), state.steps.data_ptr(),
                           state.done.data_ptr())
-    with _launch(dev, stream) as handle:
+    handle = _here(dev, stream)
+    if handle is None:
+        with _launch(dev, stream) as handle:
+            _check(_lib.load().pvl_adamw_step(how, table.ctypes.data, len(table), handle))
+    else:
         _check(_lib.load().pvl_adamw_step(how, table.ctypes.data, len(table), handle))
     torch.autograd.graph.increment_version(some_params)
