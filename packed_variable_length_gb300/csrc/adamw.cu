@@ -440,12 +440,13 @@ __global__ void __launch_bounds__(kThreads, k8 ? 4 : 2) adamw_kernel(const __gri
       c.key = mix(p.seed + static_cast<uint32_t>(now) * 0x9E3779B9u);
     }
     c.keep = 1.0f - lr * tab.decay[t];
-    const bool whole = left + lane * 8 >= kBlock;
-    const uintptr_t where = reinterpret_cast<uintptr_t>(param) | reinterpret_cast<uintptr_t>(grad);
-    constexpr uintptr_t kSector = sizeof(P) == 4 || sizeof(G) == 4 ? 32 : 16;
-    if (whole && where % kSector == 0)
+    // The same for the whole warp, which takes one way through the block: by the tensors' addresses, not a lane's (a
+    // lane's eight bf16 elements start at every 16 bytes).
+    const bool whole = tab.size[t] - static_cast<long long>(b) * kBlock >= kBlock;
+    const uintptr_t at_p = reinterpret_cast<uintptr_t>(tab.param[t]), at_g = reinterpret_cast<uintptr_t>(tab.grad[t]);
+    if (whole && at_p % (8 * sizeof(P)) == 0 && at_g % (8 * sizeof(G)) == 0)
       step_block<P, G, k8, 32>(p, c, param, grad, sb, 8);
-    else if (kSector == 32 && whole && where % 16 == 0)
+    else if ((sizeof(P) == 4 || sizeof(G) == 4) && whole && (at_p | at_g) % 16 == 0)
       step_block<P, G, k8, 16>(p, c, param, grad, sb, 8);
     else
       step_block<P, G, k8, 0>(p, c, param, grad, sb, left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0);
@@ -509,8 +510,17 @@ __device__ __forceinline__ double unit_squares(const G* grad, long long left) {
 #pragma unroll
       for (int j = 0; j < 8; j += 2) s = ffma2(make_float2(f[j], f[j + 1]), make_float2(f[j], f[j + 1]), s);
     }
+  } else if (left >= kNormUnit) {  // off a boundary: element by element, sixteen on their way at once
+#pragma unroll
+    for (int i = 0; i < kNormUnit; i += 512) {
+      float f[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) f[j] = wide(grad[i + j * 32 + lane]);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s.x = fmaf(f[j], f[j], s.x);
+    }
   } else {
-    for (int i = lane; i < kNormUnit && i < left; i += 32) {
+    for (int i = lane; i < left; i += 32) {
       const float f = wide(grad[i]);
       s.x = fmaf(f, f, s.x);
     }

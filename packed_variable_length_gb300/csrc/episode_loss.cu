@@ -179,8 +179,8 @@ __device__ __forceinline__ Digits digits(const Sum* s) {
   return v;
 }
 
-// A sum's value: a pair, and in 64 bits in *far where its magnitude is kNear and
-// more (or less: never without).
+// A sum's value: a pair, and in 64 bits in *far wherever its magnitude is kNear
+// and more (also for some below, which nothing reads).
 constexpr float kNear = 1e6f;
 
 __device__ __forceinline__ Pair value(const Digits& s, unsigned int flags, int shift, double* far = nullptr) {
