@@ -286,7 +286,8 @@ def pack_policy_fwd(logp, old_logp, advantages, seq_id, episodes: int, *, ref_lo
     """Clipped policy loss with a divergence term over the tokens of a pack that
     have an id (seq_id >= 0; ids below `episodes`).  logp, old_logp (None: logp
     itself, a ratio of 1) and ref_logp are fp32 like seq_id; advantages fp32
-    like seq_id, or one an episode, [episodes].
+    like seq_id, or one an episode, [episodes] (where both shapes are the same:
+    of tokens with ratio="token", of episodes with ratio="episode").
 
     With r = exp(logp - old_logp) (ratio="episode": exp of the mean over the
     token's episode, which needs advantages of episodes) a token's loss is

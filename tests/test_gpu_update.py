@@ -249,6 +249,46 @@ def test_captured_and_replayed(pvl):
         assert all(torch.equal(a, b) for a, b in zip(want[i], outcome(st, outs))), i
 
 
+def test_autograd_captured_and_replayed(pvl):
+    """Forward and backward through autograd in one captured graph, replayed on other logits; no eager graph of the
+    leaves lives while it is captured."""
+    L, E = LAYOUT["L"], LAYOUT["E"]
+    sid = pvl.pack_build_seq_ids(LAYOUT["frames"], LAYOUT["valid"], LAYOUT["tokens"], L)
+    t = torch.randint(0, 65, (1, L), generator=torch.Generator().manual_seed(1)).cuda()
+    old, adv = randn(1, L, seed=71) * 0.1 - 4.2, randn(E, seed=72)
+    pairs = torch.tensor([[0, 1], [2, 1]], dtype=torch.int32, device="cuda")
+    x = randn(1, L, 65, seed=73).requires_grad_()
+
+    def step():
+        logp, ent = pvl.token_logprob(x, t, sid, entropy=True)
+        a, _ = pvl.policy_loss(logp, old, adv, sid, E, mean="episode")
+        b, _ = pvl.preference_loss(logp, old, sid, pairs, E, mean=True)
+        loss = a + b - 0.01 * ent.mean()
+        return loss.detach(), torch.autograd.grad(loss, x)[0]
+
+    fresh = [randn(1, L, 65, seed=80 + i) for i in range(3)]
+    want = []
+    for v in fresh:
+        with torch.no_grad():
+            x.copy_(v)
+        want.append([r.clone() for r in step()])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for i in (2, 0, 1):
+        with torch.no_grad():
+            x.copy_(fresh[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want[i])), i
+
+
 def test_graphs_that_share_a_workspace(pvl):
     """Two captured calls of other sizes with one workspace, replayed in turn: what it holds on entry does not matter."""
     ws = torch.full((max(pvl.pack_policy_ws_bytes(40), pvl.pack_preference_ws_bytes(40)),), 0xAB, dtype=torch.uint8, device="cuda")
