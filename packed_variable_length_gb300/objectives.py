@@ -78,8 +78,9 @@ def pack_logprob_fwd(logits, targets, seq_id=None, *, temperature: float = 1.0, 
     entropy of each row (else None).
 
     Rows may have any strides (logits[:, :-1], or a padded vocabulary's
-    logits[..., :V]).  Tokens whose seq_id (int32 [B, L], optional) is negative
-    or whose target lies outside [0, V) give zeros and are not read."""
+    logits[..., :V]); targets and seq_id have to be contiguous.  Tokens whose
+    seq_id (int32 [B, L], optional) is negative or whose target lies outside
+    [0, V) give zeros and are not read."""
     how, dev, shape = _logprob(logits, targets, seq_id, temperature)
     handle = _here(dev, stream)
     if handle is None:

@@ -11,6 +11,7 @@ from __future__ import annotations
 import math
 from array import array
 from dataclasses import dataclass, field
+from numbers import Real
 from operator import attrgetter
 
 import numpy as np
@@ -245,7 +246,7 @@ def adamw_step(params, grads, state: AdamWState, lr, *, betas=(0.9, 0.999), eps:
     _distinct(addresses)
     table["param"] = addresses
     table["grad"] = list(map(_address, some_grads))
-    if isinstance(weight_decay, (int, float)):
+    if isinstance(weight_decay, Real):
         table["decay"] = weight_decay
     else:
         decay = [float(d) for d in weight_decay]

@@ -184,6 +184,9 @@ def test_device_rate_and_version_counters(pvl):
     pvl.adamw_step(params, grads, a, 2.0 ** -9)
     pvl.adamw_step(other, grads, b, torch.tensor([2.0 ** -9], device="cuda"))
     assert all(torch.equal(x, y) for x, y in zip(params, other))
+    pvl.adamw_step(params, grads, a, np.float32(2.0 ** -9), weight_decay=np.float32(0.5), betas=np.array([0.9, 0.999]))
+    pvl.adamw_step(other, grads, b, 2.0 ** -9, weight_decay=[0.5] * len(other))
+    assert all(torch.equal(x, y) for x, y in zip(params, other))
     assert all(p._version > v for p, v in zip(params, versions))
 
 
@@ -262,6 +265,32 @@ def test_eight_bits_follow_the_averages(pvl):
     assert 0.98 * v_true < v.mean().item() < 1.08 * v_true
     # m of noise: deviation 1e-3 sqrt(0.1 / 1.9), and none in the mean
     assert abs(m.mean().item()) < 6 * 1e-3 / math.sqrt(65536) and 0.9 < m.std().item() / (1e-3 * math.sqrt(0.1 / 1.9)) < 1.1
+
+
+def test_a_state_that_is_saved_and_copied(pvl):
+    """A copy of the state goes on by itself; so does one that was written to a file."""
+    import copy
+    import io
+    for bits in (32, 8):
+        sets = [tensors(SHAPES, torch.bfloat16, 30) for _ in range(3)]
+        grads = tensors(SHAPES, torch.bfloat16, 31)
+        state = pvl.adamw_state(sets[0], bits=bits, seed=4)
+        pvl.adamw_step(sets[0], grads, state, 1e-2)
+        for p in sets[1:]:
+            for a, b in zip(p, sets[0]):
+                a.copy_(b)
+        file = io.BytesIO()
+        torch.save(state, file)
+        file.seek(0)
+        states = [state, copy.deepcopy(state), torch.load(file, weights_only=False)]
+        del state
+        for p, s in zip(sets, states):
+            pvl.adamw_step(p, grads, s, 1e-2)
+        torch.cuda.synchronize()
+        assert all(s.steps.tolist() == [2] * len(SHAPES) for s in states)
+        for p, s in zip(sets[1:], states[1:]):
+            assert all(torch.equal(a, b) for a, b in zip(p, sets[0]))
+            assert torch.equal(s.m.view(torch.uint8), states[0].m.view(torch.uint8)) and s.m.data_ptr() != states[0].m.data_ptr()
 
 
 def test_same_bits_twice(pvl):
