@@ -4,6 +4,8 @@
 // With c = min(1, max_norm / norm) where a norm is given,
 //   g' = c g,  m' = b1 m + (1 - b1) g',  v' = b2 v + (1 - b2) g'^2,
 //   p' = p (1 - lr decay) - lr / (1 - b1^t) m' / (sqrt(v' / (1 - b2^t)) + eps).
+// 1 - lr decay is the sum of two fp32 numbers, so that p is rounded once: one
+// number would be 1, no decay, for lr decay below 2^-25, and 19 % off at 1e-7.
 // The moments of all tensors lie in one buffer, each tensor from a whole block
 // of 256 elements on (zeros after its end); so do fp32 masters of bf16
 // parameters.  Parameters and gradients are wherever their tensors are.
@@ -280,9 +282,29 @@ struct Divisor {
 };
 
 // ---------------------------------------------------------------- step
+// 1 - x as hi + lo: exact up to a rounding of lo, of at most 2^-24 of hi.  Both have one sign and lo is not 0, so that
+// an infinite parameter stays what it is.
+struct Keep {
+  float hi, lo;
+};
+
+__device__ __forceinline__ Keep keep_of(float x) {
+  float hi = __fsub_rn(1.0f, x);
+  const float t = __fsub_rn(hi, 1.0f);
+  float lo = __fsub_rn(__fsub_rn(1.0f, __fsub_rn(hi, t)), __fadd_rn(x, t));  // Knuth's two-sum
+  if (lo != 0.0f && (lo < 0.0f) != (hi < 0.0f)) {
+    const float down = __int_as_float(__float_as_int(hi) - 1);  // the next towards 0
+    lo = __fadd_rn(lo, __fsub_rn(hi, down));
+    hi = down;
+  }
+  if (lo == 0.0f) lo = copysignf(0x1p-100f, hi);
+  return {hi, lo};
+}
+
 // What a block's elements share.
 struct Shared {
-  float clip, rate, second, keep;
+  float clip, rate, second;
+  Keep keep;
   uint32_t key;
 };
 
@@ -325,7 +347,8 @@ __device__ __forceinline__ void step_block(const StepParams& p, const Shared& c,
   }
   const float2 b1 = make_float2(p.b1, p.b1), c1 = make_float2(p.c1, p.c1), b2 = make_float2(p.b2, p.b2),
                c2 = make_float2(p.c2, p.c2), clip = make_float2(c.clip, c.clip), second = make_float2(c.second, c.second),
-               eps = make_float2(p.eps, p.eps), rate = make_float2(-c.rate, -c.rate), keep = make_float2(c.keep, c.keep);
+               eps = make_float2(p.eps, p.eps), rate = make_float2(-c.rate, -c.rate), keep = make_float2(c.keep.hi, c.keep.hi),
+               keep_lo = make_float2(c.keep.lo, c.keep.lo);
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
     const float2 gc = fmul2(make_float2(g[i], g[i + 1]), clip);
@@ -343,7 +366,8 @@ __device__ __forceinline__ void step_block(const StepParams& p, const Shared& c,
     }
     const float2 d = ffma2(r, second, eps);
     const float2 q = fmul2(mm, make_float2(inverse(d.x), inverse(d.y)));
-    const float2 ww = ffma2(make_float2(w[i], w[i + 1]), keep, fmul2(rate, q));
+    const float2 was = make_float2(w[i], w[i + 1]);
+    const float2 ww = ffma2(was, keep, ffma2(was, keep_lo, fmul2(rate, q)));
     m[i] = mm.x, m[i + 1] = mm.y;
     v[i] = vv.x, v[i + 1] = vv.y;
     root[i] = r.x, root[i + 1] = r.y;
@@ -439,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, k8 ? 4 : 2) adamw_kernel(const __gri
       c.second = rsqrtf(-expm1f(s * p.log_b2));
       c.key = mix(p.seed + static_cast<uint32_t>(now) * 0x9E3779B9u);
     }
-    c.keep = 1.0f - lr * tab.decay[t];
+    c.keep = keep_of(lr * tab.decay[t]);
     // The same for the whole warp, which takes one way through the block: by the tensors' addresses, not a lane's (a
     // lane's eight bf16 elements start at every 16 bytes).
     const bool whole = tab.size[t] - static_cast<long long>(b) * kBlock >= kBlock;
