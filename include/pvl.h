@@ -698,7 +698,10 @@ PVL_API pvl_status pvl_grad_norm(const void* const* grads, const int64_t* sizes,
  *   fp32 one a block: m = code m_scale, v = (code v_scale)^2.  Both are rounded
  *   stochastically, by bits that depend on seed, step and place alone; a code
  *   of v that is not 0 stays at least 2^-9; blocks whose largest |m| or sqrt(v)
- *   is below 2^-100 become 0.
+ *   is below 2^-100 become 0.  An infinite or NaN gradient leaves NaN in its own
+ *   element (parameter and moments), and the block's scales to the others.
+ * A v past the largest fp32 number is infinite for good and its element only
+ *   decays (8 bits: the NaN code of v beside m = 0).
  *   master: dev fp32, for bf16 parameters, which are then its rounded copy and
  *   are not read; null for fp32 parameters.
  * steps: dev int32; done: dev uint32 that is 0 before the first step (the

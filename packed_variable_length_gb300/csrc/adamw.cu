@@ -217,11 +217,11 @@ __device__ __forceinline__ float round_normal(float x, uint32_t r) {
   return __uint_as_float((__float_as_uint(x) + r) & 0xFFF00000u);
 }
 
-// The same for magnitudes of 0 to 448: below 2^-6 steps are 2^-9 throughout, as
-// those of [2^-6, 2^-5).
+// The same for magnitudes of 0 to 448 and NaN: below 2^-6 steps are 2^-9
+// throughout, as those of [2^-6, 2^-5).
 __device__ __forceinline__ float round_any(float x, uint32_t r) {
   const float shift = fabsf(x) < 0.015625f ? 0.015625f : 0.0f;
-  return copysignf(round_normal(fabsf(x) + shift, r) - shift, x);
+  return x == x ? copysignf(round_normal(fabsf(x) + shift, r) - shift, x) : x;
 }
 
 __device__ __forceinline__ float smallest(const float (&f)[8]) {
@@ -252,12 +252,39 @@ __device__ __forceinline__ uint2 close_e4m3(const float (&f)[8]) {
   return make_uint2(w[0], w[1]);
 }
 
-// Largest magnitude of a block (NaN aside).
+// The larger of two magnitudes, NaN if one of them is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// Largest magnitude of a block; NaN, whose bits are above those of infinity, if it holds one.
 __device__ __forceinline__ float block_top(const float (&f)[8]) {
-  float top = 0.0f;
+  float top = fabsf(f[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
+  for (int i = 1; i < 8; ++i) top = max_nan(top, fabsf(f[i]));
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+}
+
+// A block that holds what is not finite: such an element takes the NaN code, and the scales are those of the others.
+// An infinite or NaN gradient leaves NaN in both moments.  Where the square of a finite gradient alone left fp32, v is
+// infinite for good: a NaN code of v beside a finite m stands for that, and the update is 0, as with 32-bit moments.
+__device__ __forceinline__ void set_apart(float (&m)[8], float (&root)[8], float& top_m, float& top_root) {
+  const float nan = __int_as_float(0x7FFFFFFF);
+  float a[8], b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool in = fabsf(m[i]) < INFINITY;
+    if (!in || !(root[i] < INFINITY)) {
+      m[i] = in ? 0.0f : nan;
+      root[i] = nan;
+    }
+    a[i] = in ? m[i] : 0.0f;
+    b[i] = root[i] == root[i] ? root[i] : 0.0f;
+  }
+  top_m = block_top(a);
+  top_root = block_top(b);
 }
 
 // a + b, which the compiler may not make a multiply-add of the product that a
@@ -365,7 +392,9 @@ __device__ __forceinline__ void step_block(const StepParams& p, const Shared& c,
       r = make_float2(root_of(vv.x), root_of(vv.y));
     }
     const float2 d = ffma2(r, second, eps);
-    const float2 q = fmul2(mm, make_float2(inverse(d.x), inverse(d.y)));
+    float2 over = make_float2(inverse(d.x), inverse(d.y));
+    if constexpr (k8) over = make_float2(fmaxf(over.x, 0.0f), fmaxf(over.y, 0.0f));  // NaN, an infinite v: 0
+    const float2 q = fmul2(mm, over);
     const float2 was = make_float2(w[i], w[i + 1]);
     const float2 ww = ffma2(was, keep, ffma2(was, keep_lo, fmul2(rate, q)));
     m[i] = mm.x, m[i + 1] = mm.y;
@@ -382,7 +411,9 @@ __device__ __forceinline__ void step_block(const StepParams& p, const Shared& c,
       if (i < n) narrow(param + i, w[i]);
   }
   if constexpr (k8) {
-    const float tm = block_top(m), tv = block_top(root);
+    float tm = block_top(m), tv = block_top(root);
+    const bool odd = !(tm < INFINITY && tv < INFINITY);  // the same for the whole warp
+    if (odd) set_apart(m, root, tm, tv);
     // a block below 2^-100 becomes zeros: its scale would not be a normal number
     const Divisor by_m(tm), by_v(tv);
     const uint32_t h = mix((static_cast<uint32_t>(sb) * 32u + lane) ^ c.key);
@@ -398,14 +429,14 @@ __device__ __forceinline__ void step_block(const StepParams& p, const Shared& c,
       v[i] = b.x, v[i + 1] = b.y;
     }
     // few blocks hold a value below 3e-5 of their largest: a third of the work less for the others
-    if (smallest(m) >= 0.015625f) {
+    if (!odd && smallest(m) >= 0.015625f) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) m[i] = round_normal(m[i], rm[i]);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) m[i] = round_any(m[i], rm[i]);
     }
-    if (smallest(v) >= 0.015625f) {
+    if (!odd && smallest(v) >= 0.015625f) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = round_normal(v[i], rv[i]);
     } else {

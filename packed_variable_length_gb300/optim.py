@@ -101,7 +101,7 @@ class AdamWState:
 
     bits 32: m and v are fp32.  bits 8: they are torch.float8_e4m3fn, with one
     fp32 scale a block, and v holds the root: m = code m_scale, sqrt(v) = code
-    v_scale.  master holds bf16 parameters in fp32 (None for fp32 ones)."""
+    v_scale, infinite where v's code is NaN and m's is not.  master holds bf16 parameters in fp32 (None for fp32 ones)."""
     m: torch.Tensor
     v: torch.Tensor
     m_scale: torch.Tensor | None
@@ -128,6 +128,7 @@ class AdamWState:
         if self.bits == 8:
             at = torch.arange(m.numel(), device=m.device) // BLOCK + self.blocks[i]
             m, v = m * self.m_scale[at], (v * self.v_scale[at]).square()
+            v = torch.where(v.isnan() & m.isfinite(), math.inf, v)
         return m.view(self.shapes[i]), v.view(self.shapes[i])
 
     def masters(self, i: int):
