@@ -1,8 +1,9 @@
-"""AdamW with 8-bit moments where a gradient is not finite or its square leaves fp32: what is wrong with one element
-stays with it (GPU)."""
+"""AdamW where a gradient is not finite or its square leaves fp32: with 8-bit moments what is wrong with one element
+stays with it; with 32-bit ones squares below the normal numbers count (GPU)."""
 
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -81,3 +82,20 @@ def test_a_square_past_fp32_stops_its_element(pvl, dtype, big, spread, at):
     for g in (gradients(spread).index_fill_(0, torch.tensor(at, device="cuda"), big), gradients(spread)):
         pvl.adamw_step([r], [g], wide, 1e-3)
     assert torch.equal(r[own], p[own]) and (wide.moments(0)[1][own] == math.inf).all()
+
+
+@pytest.mark.parametrize("g", [1e-18, 3e-19, 1e-20])
+def test_a_small_denominator(pvl, g):
+    """32-bit moments whose v lies below the normal numbers, and an eps that does not cover it: the first step moves by
+    lr, as the formula has it.  v is a multiple of 2^-149: its root is off by 2^-150 / v of itself, twice (b2 v, c2 g^2)
+    and 2^-19 for the rest."""
+    from oracle import adamw as oa
+    p = torch.zeros(1000, device="cuda")
+    grads = torch.full((1000,), g, device="cuda")
+    state = pvl.adamw_state([p])
+    for t in (1, 2):
+        before, was = p.double().cpu().numpy(), [x.double().cpu().numpy() for x in state.moments(0)]
+        pvl.adamw_step([p], [grads], state, 1e-2, eps=1e-30, weight_decay=0.0)
+        want, _, v, change = oa.step(before, grads.double().cpu().numpy(), *was, t, 1e-2, eps=1e-30, decay=0.0)
+        tol = (2.0 ** -19 + 2 * 2.0 ** -149 / v) * np.abs(change) + 2.0 ** -23 * np.abs(want)
+        assert (np.abs(p.double().cpu().numpy() - want) <= tol).all(), (p[0].item(), want[0])
