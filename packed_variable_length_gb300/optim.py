@@ -30,7 +30,7 @@ _FLOATS = {torch.bfloat16: 0, torch.float32: 1}
 
 # A model has hundreds of parameters and a step looks at each: attributes of
 # whole lists are read by C loops, one list at a time.
-_dtype, _shape = attrgetter("dtype"), attrgetter("shape")
+_dtype, _shape, _version = attrgetter("dtype"), attrgetter("shape"), attrgetter("_version")
 _contiguous, _index, _address, _count = (torch.Tensor.is_contiguous, torch.Tensor.get_device, torch.Tensor.data_ptr,
                                          torch.Tensor.numel)
 
@@ -117,6 +117,7 @@ class AdamWState:
     total: int                  # blocks
     empty: bool                 # whether a parameter has no elements
     table: np.ndarray = field(repr=False)
+    versions: list | None = None    # of bf16 parameters, as of their masters
 
     def _part(self, t, i: int):
         n = math.prod(self.shapes[i])
@@ -140,7 +141,14 @@ def adamw_state(params, *, bits: int = 32, seed: int = 0) -> AdamWState:
     """State of AdamW for a list of parameters, all bf16 or all fp32: moments of
     zero in 32 or 8 bits, step counts of zero and, for bf16 parameters, fp32
     masters that start as their values.  seed chooses the random bits by which
-    8-bit moments are rounded."""
+    8-bit moments are rounded.
+
+    Steps go from the masters and write the parameters.  A bf16 parameter that a
+    program writes in between (a loaded checkpoint, say) is found by its version
+    when it next steps: its master takes each value that is not the rounded
+    master's already.  Writes that torch does not count, through .data or
+    between replays of a captured step, are lost unless they go to masters(i)
+    too."""
     params = list(params)
     if not params:
         raise ValueError("adamw_state needs a parameter")
@@ -171,7 +179,33 @@ def adamw_state(params, *, bits: int = 32, seed: int = 0) -> AdamWState:
         state.master = torch.zeros(total * BLOCK, dtype=torch.float32, device=dev)
         for i, p in enumerate(params):
             state.masters(i).copy_(p.detach())
+        state.versions = _versions(params)
     return state
+
+
+def _versions(params) -> list:
+    """Version of each parameter, None for what has none (tensors of inference mode)."""
+    try:
+        return list(map(_version, params))
+    except RuntimeError:
+        return [None if p.is_inference() else p._version for p in params]
+
+
+def _take_written(state: AdamWState, params, use) -> None:
+    """Masters of the parameters that were written since their last step, on the current stream: values that differ
+    from the rounded master's are taken, the others keep the master's lower bits."""
+    for i, p, version in zip(range(len(params)) if use is None else use, params, _versions(params)):
+        if version != state.versions[i]:
+            for master, value in zip(*(t.detach().reshape(-1).split(1 << 28) for t in (state.masters(i), p))):
+                torch.where(master.to(torch.bfloat16) == value, master, value.float(), out=master)
+
+
+def _keep_versions(state: AdamWState, params, use) -> None:
+    if use is None:
+        state.versions = _versions(params)
+    else:
+        for i, version in zip(use, _versions(params)):
+            state.versions[i] = version
 
 
 def _like(tensors, name: str, use, dtype, shapes, dev) -> None:
@@ -193,6 +227,9 @@ def adamw_step(params, grads, state: AdamWState, lr, *, betas=(0.9, 0.999), eps:
     """One AdamW step of `params` (the list that adamw_state was given) from
     `grads` (bf16 or fp32, of one type, each like its parameter; None leaves
     the parameter, its moments and its step count as they are).
+
+    bf16 parameters step from their fp32 masters; values that were written to
+    them since (see adamw_state) are taken over first.
 
     lr is a number or an fp32 one-element device tensor (read when the kernel
     runs); weight_decay a number or one a parameter, decoupled.  With grad_norm
@@ -262,7 +299,16 @@ def adamw_step(params, grads, state: AdamWState, lr, *, betas=(0.9, 0.999), eps:
     handle = _here(dev, stream)
     if handle is None:
         with _launch(dev, stream) as handle:
-            _check(_lib.load().pvl_adamw_step(how, table.ctypes.data, len(table), handle))
+            _run_step(how, table, state, some_params, use, handle)
     else:
-        _check(_lib.load().pvl_adamw_step(how, table.ctypes.data, len(table), handle))
-    torch.autograd.graph.increment_version(some_params)
+        _run_step(how, table, state, some_params, use, handle)
+
+
+def _run_step(how, table, state, params, use, handle):
+    tracked = state.versions is not None
+    if tracked and (use is not None or _versions(params) != state.versions):
+        _take_written(state, params, use)
+    _check(_lib.load().pvl_adamw_step(how, table.ctypes.data, len(table), handle))
+    torch.autograd.graph.increment_version(params)
+    if tracked:
+        _keep_versions(state, params, use)
