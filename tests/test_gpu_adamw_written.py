@@ -1,4 +1,6 @@
-"""Parameters that a program writes between the steps (GPU)."""
+"""Parameters that a program writes between the steps, or that autograd does not track (GPU)."""
+
+import contextlib
 
 import pytest
 import torch
@@ -92,3 +94,31 @@ def test_written_on_another_stream_and_in_a_graph(pvl):
     torch.cuda.synchronize()
     assert (params[3] == 0.25).all() and (params[0] == 1.5).all()
     assert state.steps.tolist() == [2] * 4
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_inference_tensors(pvl, dtype):
+    """They have no version; they step like the others beside them, in inference mode and outside it."""
+    def run(make, at):
+        p = [torch.ones(300, dtype=dtype, device="cuda"), make(), torch.ones(5, dtype=dtype, device="cuda")]
+        g = [torch.ones_like(x, dtype=torch.float32) for x in p]
+        versions = [p[0]._version, p[2]._version]
+        state = pvl.adamw_state(p)
+        for _ in range(3):
+            with at:
+                pvl.adamw_step(p, g, state, 1e-2)
+        assert p[0]._version > versions[0] and p[2]._version > versions[1]
+        assert state.steps.tolist() == [3] * 3
+        return p
+
+    def ordinary():
+        return torch.ones(70, dtype=dtype, device="cuda")
+
+    def free():
+        with torch.inference_mode():
+            return ordinary()
+
+    want = run(ordinary, contextlib.nullcontext())
+    assert free().is_inference()
+    for at in (contextlib.nullcontext(), torch.inference_mode(), torch.no_grad()):
+        assert all(torch.equal(a, b) for a, b in zip(run(free, at), want))
