@@ -157,7 +157,7 @@ def adamw_state(params, *, bits: int = 32, seed: int = 0) -> AdamWState:
     if not 0 <= int(seed) < 1 << 32:
         raise ValueError("seed must fit in 32 bits")
     dtype, dev = _same_floats(params, "params")
-    _distinct([p.data_ptr() for p in params if p.numel()])     # empty ones have no address
+    _apart([p for p in params if p.numel()])       # empty ones have no address
     table = np.zeros(len(params), dtype=_TENSOR)
     table["size"] = [p.numel() for p in params]
     table["slot"] = np.arange(len(params))
@@ -215,6 +215,16 @@ def _like(tensors, name: str, use, dtype, shapes, dev) -> None:
             not all(map(_contiguous, tensors)) or list(map(_shape, tensors)) != list(shapes)):
         for i, (t, shape) in enumerate(zip(tensors, shapes)):
             _need(t, f"{name}[{i if use is None else use[i]}]", dtype, shape, dev)
+
+
+def _apart(params) -> None:
+    """No two of the tensors share memory, which a step would write twice, in any order."""
+    _distinct(list(map(_address, params)))
+    end = 0
+    for start, size in sorted((p.data_ptr(), p.numel() * p.element_size()) for p in params):
+        if start < end:
+            raise ValueError("two parameters of the list share memory")
+        end = start + size
 
 
 def _distinct(ptrs):

@@ -1,4 +1,4 @@
-"""Parameters that a program writes between the steps, or that autograd does not track (GPU)."""
+"""Parameters that a program writes between the steps, that autograd does not track, or that share memory (GPU)."""
 
 import contextlib
 
@@ -122,3 +122,13 @@ def test_inference_tensors(pvl, dtype):
     assert free().is_inference()
     for at in (contextlib.nullcontext(), torch.inference_mode(), torch.no_grad()):
         assert all(torch.equal(a, b) for a, b in zip(run(free, at), want))
+
+
+def test_parameters_that_share_memory_are_refused(pvl):
+    """Two warps would write the same elements; neighbours are fine."""
+    buf = torch.zeros(600, device="cuda")
+    for pair in ([buf[:300], buf[299:]], [buf[100:], buf[:101]], [buf, buf[256:300]], [buf[256:300], buf]):
+        with pytest.raises(ValueError, match="share memory"):
+            pvl.adamw_state(pair)
+    pvl.adamw_state([buf[300:], buf[:300]])
+    pvl.adamw_state([buf[:0], buf[:5], buf[5:5], buf[5:]])
