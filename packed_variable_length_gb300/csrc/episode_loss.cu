@@ -34,12 +34,13 @@
 // 64-bit floating point took twice the time.
 //
 // Sums are integers, so that they are the same whatever order blocks finish in,
-// and exact.  A token's value in units of 2^-40 (rounded once; differences are
-// taken as exact pairs of fp32 values first) is added in 64 bits within the
-// block; an episode holds digits in base 2^40, from 2^-80 to 2^160, to which a
-// block, warp or run adds by integer atomics.  Values of 2^11 and more go to
-// the digits one by one, infinities and NaN to flags.  With at most 2^23 tokens
-// a digit's sum stays below 2^63.  64-bit floating point, of which this GPU
+// and exact.  A token's value in units of 2^-40 and what is left of it in units
+// of 2^-80 (rounded once; differences are taken as exact pairs of fp32 values
+// first) are added in 64 bits within the block, so that small advantages and
+// divergences count as large ones do; an episode holds digits in base 2^40, from
+// 2^-80 to 2^160, to which a block, warp or run adds by integer atomics.  Values
+// of 2^11 and more go to the digits one by one, infinities and NaN to flags.
+// With at most 2^23 tokens a digit's sum stays below 2^63.  64-bit floating point, of which this GPU
 // does little, is left to values that are large.
 #include <cuda_runtime.h>
 
@@ -186,10 +187,17 @@ constexpr float kNear = 1e6f;
 __device__ __forceinline__ Pair value(const Digits& s, unsigned int flags, int shift, double* far = nullptr) {
   flags = (flags >> shift) & 7u;
   const long long(&d)[6] = s.d;
-  const long long next = d[4] + (d[5] >> 40), top = d[3] + (next >> 40);
+  const long long near = (d[5] + (1ll << 39)) >> 40;  // the last digit to nearest, so that what is left may be negative
+  const long long next = d[4] + near, top = d[3] + (next >> 40), last = d[5] - near * (1ll << 40);
   if (!(flags | d[0] | d[1] | d[2]) && top < (1ll << 19) && top >= -(1ll << 19)) {
     const long long whole = top * (1ll << 40) + (next & kMask);  // units of 2^-40
-    const float rest = __ll2float_rn(d[5] & kMask) * (1.0f / kFine);
+    if (whole < (1ll << 21) && whole > -(1ll << 21)) {
+      constexpr float kUnit = 1.0f / kFine / kFine;
+      const long long all = whole * (1ll << 40) + last;  // units of 2^-80
+      const float hi = __ll2float_rn(all);
+      return {hi * kUnit, __ll2float_rn(all - __float2ll_rn(hi)) * kUnit};
+    }
+    const float rest = __ll2float_rn(last) * (1.0f / kFine);
     const float hi = __ll2float_rn(whole);
     const Pair u = renormal(hi, __ll2float_rn(whole - __float2ll_rn(hi)) + rest);
     return {u.hi * (1.0f / kFine), u.lo * (1.0f / kFine)};
@@ -207,33 +215,24 @@ struct Episode {
 };
 static_assert(sizeof(Episode) == 112, "workspace layout");
 
-// A thread's, warp's or block's part of it, in units of 2^-40.
+// A thread's, warp's or block's part of it: sums in units of 2^-40, what is left
+// of their terms in units of 2^-80.
 struct Part {
-  long long a, b;
+  long long a, b, fine_a, fine_b;
   unsigned int n, cut;
 };
 
 __device__ __forceinline__ void add_part(Episode* e, const Part& p) {
   add_units(&e->a, p.a);
   add_units(&e->b, p.b);
+  add_digit(&e->a.digit[5], p.fine_a);
+  add_digit(&e->b.digit[5], p.fine_b);
   if (p.n) atomicAdd(&e->n, p.n);
   if (p.cut) atomicAdd(&e->cut, p.cut);
 }
 
 __device__ __forceinline__ Part operator+(const Part& x, const Part& y) {
-  return {x.a + y.a, x.b + y.b, x.n + y.n, x.cut + y.cut};
-}
-
-__device__ __forceinline__ Part warp_sum(Part p, bool two) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) p.a += __shfl_xor_sync(kAll, p.a, o);
-  if (two) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) p.b += __shfl_xor_sync(kAll, p.b, o);
-  }
-  p.n = __reduce_add_sync(kAll, p.n);
-  p.cut = __reduce_add_sync(kAll, p.cut);
-  return p;
+  return {x.a + y.a, x.b + y.b, x.fine_a + y.fine_a, x.fine_b + y.fine_b, x.n + y.n, x.cut + y.cut};
 }
 
 // The sum of v over the lanes of `mask`, which all call this: in pieces of 22
@@ -244,6 +243,22 @@ __device__ __forceinline__ long long group_sum(unsigned mask, long long v) {
   const unsigned mid = __reduce_add_sync(mask, static_cast<unsigned>(v >> 22) & kPiece);
   const int hi = __reduce_add_sync(mask, static_cast<int>(v >> 44));
   return (static_cast<long long>(hi) << 44) + (static_cast<long long>(mid) << 22) + lo;
+}
+
+__device__ __forceinline__ Part warp_sum(Part p, bool two) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) p.a += __shfl_xor_sync(kAll, p.a, o);
+  if (two) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) p.b += __shfl_xor_sync(kAll, p.b, o);
+  }
+  if (__any_sync(kAll, (p.fine_a | p.fine_b) != 0)) {  // few warps: terms of 2^-17 and more leave nothing
+    p.fine_a = group_sum(kAll, p.fine_a);
+    if (two) p.fine_b = group_sum(kAll, p.fine_b);
+  }
+  p.n = __reduce_add_sync(kAll, p.n);
+  p.cut = __reduce_add_sync(kAll, p.cut);
+  return p;
 }
 
 // Sums over the block in a fixed order; every thread gets them.
@@ -363,15 +378,24 @@ __device__ __forceinline__ float policy_term(const LossParams& p, float d, float
 }
 
 // Divergences of near policies are small (f^2 / 2): they are summed 64 times as
-// large, in units of 2^-46.
+// large, in units of 2^-46 and 2^-86.
 constexpr float kKlScale = 64.0f;
 
 // ------------------------------------------------------------- forward
-// A value in units of 2^-40; one that does not fit goes to the episode at once.
-__device__ __forceinline__ long long units(Pair v, Sum* s, unsigned int* flags, int shift) {
-  if (fabsf(v.hi) < 2048.0f) return __float2ll_rn(v.hi * kFine) + __float2ll_rn(v.lo * kFine);
-  add_any(s, flags, shift, static_cast<double>(v.hi) + static_cast<double>(v.lo));
-  return 0;
+// A value in units of 2^-40, and what is left of it in units of 2^-80; one that
+// does not fit goes to the episode at once.
+__device__ __forceinline__ void units(Pair v, Sum* s, unsigned int* flags, int shift, long long& whole, long long& fine) {
+  if (fabsf(v.hi) < 2048.0f) {
+    const float x = v.hi * kFine, left = x - rintf(x);
+    whole = __float2ll_rn(x);
+    if (left != 0.0f || v.lo != 0.0f) {
+      const float y = v.lo * kFine;
+      whole += __float2ll_rn(y);
+      fine = __float2ll_rn(left * kFine) + __float2ll_rn((y - rintf(y)) * kFine);
+    }
+  } else {
+    add_any(s, flags, shift, static_cast<double>(v.hi) + static_cast<double>(v.lo));
+  }
 }
 
 // Sums of this block's tokens into the episodes'.
@@ -393,7 +417,7 @@ __device__ void sum_tokens(const LossParams& p) {
   int lo = INT32_MAX, hi = -1;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    t[i] = Part{0, 0, 0, 0};
+    t[i] = Part{};
     if (id[i] >= p.E) {
       report(p.err, kSiteEpisode);
       id[i] = -1;
@@ -417,8 +441,8 @@ __device__ void sum_tokens(const LossParams& p) {
       a = p.ref ? two_sum(logp[i], -ref[i]) : Pair{logp[i], 0.0f};
     }
     Episode* e = p.episodes + to;
-    t[i].a = units(a, &e->a, &e->flags, 0);
-    if (two) t[i].b = units(b, &e->b, &e->flags, 3);
+    units(a, &e->a, &e->flags, 0, t[i].a, t[i].fine_a);
+    if (two) units(b, &e->b, &e->flags, 3, t[i].b, t[i].fine_b);
     lo = min(lo, to);
     hi = max(hi, to);
   }
@@ -436,7 +460,7 @@ __device__ void sum_tokens(const LossParams& p) {
   if (block_hi < 0) return;
   if (block_lo == block_hi) {
     if (w == 0) {
-      sum = lane < kWarps ? warp_part[lane] : Part{0, 0, 0, 0};
+      sum = lane < kWarps ? warp_part[lane] : Part{};
       sum = warp_sum(sum, two);
       if (lane == 0) add_part(p.episodes + block_lo, sum);
     }
@@ -448,7 +472,11 @@ __device__ void sum_tokens(const LossParams& p) {
     if (id[0] < 0) return;
     sum = t[0] + t[1] + t[2] + t[3];
     sum.a = group_sum(mask, sum.a);
-    if (two) sum.b = group_sum(mask, sum.b);
+    sum.fine_a = group_sum(mask, sum.fine_a);
+    if (two) {
+      sum.b = group_sum(mask, sum.b);
+      sum.fine_b = group_sum(mask, sum.fine_b);
+    }
     sum.n = __reduce_add_sync(mask, sum.n);
     sum.cut = __reduce_add_sync(mask, sum.cut);
     if (lane == __ffs(mask) - 1) add_part(p.episodes + id[0], sum);
