@@ -253,18 +253,16 @@ __device__ __forceinline__ uint2 close_e4m3(const float (&f)[8]) {
   return make_uint2(w[0], w[1]);
 }
 
-// The larger of two magnitudes, NaN if one of them is.
-__device__ __forceinline__ float max_nan(float a, float b) {
+// The largest of three magnitudes, NaN if one of them is.
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
   float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 
 // Largest magnitude of a block; NaN, whose bits are above those of infinity, if it holds one.
 __device__ __forceinline__ float block_top(const float (&f)[8]) {
-  float top = fabsf(f[0]);
-#pragma unroll
-  for (int i = 1; i < 8; ++i) top = max_nan(top, fabsf(f[i]));
+  const float top = max_nan(max_nan(max_nan(f[0], f[1], f[2]), f[3], f[4]), max_nan(f[5], f[6], f[7]), 0.0f);
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
 }
 
@@ -392,15 +390,28 @@ __device__ __forceinline__ void step_block(const StepParams& p, const Shared& c,
       vv = ffma2(fmul2(c2, gc), gc, fmul2(b2, vv));
       r = make_float2(root_of(vv.x), root_of(vv.y));
     }
-    const float2 d = ffma2(r, second, eps);
-    float2 over = make_float2(inverse(d.x), inverse(d.y));
-    if constexpr (k8) over = make_float2(fmaxf(over.x, 0.0f), fmaxf(over.y, 0.0f));  // NaN, an infinite v: 0
-    const float2 q = fmul2(mm, over);
-    const float2 was = make_float2(w[i], w[i + 1]);
-    const float2 ww = ffma2(was, keep, ffma2(was, keep_lo, fmul2(rate, q)));
     m[i] = mm.x, m[i + 1] = mm.y;
     v[i] = vv.x, v[i + 1] = vv.y;
     root[i] = r.x, root[i + 1] = r.y;
+  }
+  float tm = 0.0f, tv = 0.0f;
+  bool odd = false;  // whether the block holds what is not finite: the same for the whole warp
+  if constexpr (k8) {
+    tm = block_top(m);
+    tv = block_top(root);
+    odd = !(tm < INFINITY && tv < INFINITY);
+    if (odd) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)  // an infinite v, held as NaN
+        if (fabsf(m[i]) < INFINITY && !(root[i] < INFINITY)) root[i] = INFINITY;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float2 d = ffma2(make_float2(root[i], root[i + 1]), second, eps);
+    const float2 q = fmul2(make_float2(m[i], m[i + 1]), make_float2(inverse(d.x), inverse(d.y)));
+    const float2 was = make_float2(w[i], w[i + 1]);
+    const float2 ww = ffma2(was, keep, ffma2(was, keep_lo, fmul2(rate, q)));
     w[i] = ww.x, w[i + 1] = ww.y;
   }
   if constexpr (kMaster) st32(p.master + st, w);
@@ -412,8 +423,6 @@ __device__ __forceinline__ void step_block(const StepParams& p, const Shared& c,
       if (i < n) narrow(param + i, w[i]);
   }
   if constexpr (k8) {
-    float tm = block_top(m), tv = block_top(root);
-    const bool odd = !(tm < INFINITY && tv < INFINITY);  // the same for the whole warp
     if (odd) set_apart(m, root, tm, tv);
     // a block below 2^-100 becomes zeros: its scale would not be a normal number
     const Divisor by_m(tm), by_v(tv);
