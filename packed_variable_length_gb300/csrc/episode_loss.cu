@@ -377,10 +377,6 @@ __device__ __forceinline__ float policy_term(const LossParams& p, float d, float
   return -(cut ? (adv > 0.0f ? p.bound_high : p.bound_low) : expf(d)) * adv;
 }
 
-// Divergences of near policies are small (f^2 / 2): they are summed 64 times as
-// large, in units of 2^-46 and 2^-86.
-constexpr float kKlScale = 64.0f;
-
 // ------------------------------------------------------------- forward
 // A value in units of 2^-40, and what is left of it in units of 2^-80; one that
 // does not fit goes to the episode at once.
@@ -428,7 +424,7 @@ __device__ void sum_tokens(const LossParams& p) {
     int to = id[i];
     if constexpr (kPolicy) {
       a = p.old ? two_sum(logp[i], -old[i]) : Pair{0.0f, 0.0f};
-      if (p.ref) b = Pair{kKlScale * kl_term(__fsub_rn(ref[i], logp[i])), 0.0f};
+      if (p.ref) b = Pair{kl_term(__fsub_rn(ref[i], logp[i])), 0.0f};
       if (!p.ratio_episode) {
         const float v = p.adv_by_token ? adv[i] : __ldg(p.adv + id[i]);
         const bool cut = clipped(p, a, v);
@@ -656,8 +652,7 @@ __global__ void __launch_bounds__(kThreads) policy_kernel(const LossParams p) {
         cut += __ldcg(&q->cut);
       }
       if (p.ref) {
-        Pair b = value(digits(&q->b), flags, 3);
-        b = {b.hi * (1.0f / kKlScale), b.lo * (1.0f / kKlScale)};
+        const Pair b = value(digits(&q->b), flags, 3);
         kl = add(kl, p.mean_episode ? over(b, fn) : b);
       }
     }

@@ -86,3 +86,16 @@ def test_factors_of_pairs_won_by_far(pvl, gap):
     want = math.exp(-gap) / (1 + math.exp(-gap))
     tol = 2.0 ** -22 * (8 + gap) * want + 2.0 ** -80
     assert abs(out.coef[0].item() + want) <= tol and abs(out.coef[1].item() - want) <= tol
+
+
+@pytest.mark.parametrize("f", [3.0, 4.0, 8.0, 40.0, 84.0, 86.0, 88.0, 88.5])
+def test_large_divergence(pvl, f):
+    """Finite up to the largest fp32; exp carries 2^-22, and 2^-24 |f| for its argument."""
+    ids = torch.full((9,), -1, dtype=torch.int32, device="cuda")
+    ids[4] = 0
+    ref = torch.full((9,), f, device="cuda")
+    zero = torch.zeros_like(ref)
+    out = pvl.pack_policy_fwd(zero, None, zero, ids, 1, ref_logp=ref, kl_weight=1.0)
+    want = math.expm1(f) - f
+    for got in (out.stats[0].item(), out.loss.item()):
+        assert abs(got - want) <= 2.0 ** -19 * want, (got, want)
