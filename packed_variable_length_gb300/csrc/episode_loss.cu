@@ -285,6 +285,44 @@ __device__ unsigned int block_count(unsigned int n) {
   return __reduce_add_sync(kAll, threadIdx.x % 32 < kWarps ? part[threadIdx.x % 32] : 0u);
 }
 
+// A sum of losses.  What is kNear and more is added in 64 bits, where no sum of
+// fp32 values overflows before it is divided by their number.
+struct Total {
+  Pair near;
+  double far;
+  bool any;  // whether there is a far part
+
+  __device__ __forceinline__ void put(Pair v, double wide) {
+    if (fabsf(v.hi) < kNear) {
+      near = add(near, v);
+    } else {
+      far += wide;
+      any = true;
+    }
+  }
+};
+
+// (sum over the block of near and far) / n
+__device__ __noinline__ Pair far_mean(Pair near, double far, float n) {
+  __shared__ double part[kWarps];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) far += __shfl_xor_sync(kAll, far, o);
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = far;
+  __syncthreads();
+  double v = static_cast<double>(near.hi) + static_cast<double>(near.lo);
+  for (int i = 0; i < kWarps; ++i) v += part[i];
+  v /= n;
+  const float hi = static_cast<float>(v);
+  return {hi, finite(hi) ? static_cast<float>(v - hi) : 0.0f};
+}
+
+// The mean of n values whose sum the block's threads hold; every thread gets it.
+__device__ __forceinline__ Pair mean_of(const Total& t, float n) {
+  const Pair near = block_sum(t.near);
+  return __syncthreads_or(t.any) ? far_mean(near, t.far, n) : over(near, n);
+}
+
 // ------------------------------------------------------------- parameters
 struct LossParams {
   const float* logp;
@@ -539,7 +577,7 @@ __global__ void __launch_bounds__(kThreads) preference_kernel(const LossParams p
     }
   }
   __syncthreads();
-  Pair loss{0.0f, 0.0f};
+  Total loss{};
   unsigned int count = 0;
   for (int i = threadIdx.x; i < p.P; i += kThreads) {
     const int c = p.pairs[2 * i], r = p.pairs[2 * i + 1];
@@ -586,7 +624,7 @@ __global__ void __launch_bounds__(kThreads) preference_kernel(const LossParams p
       up = short_of ? -1.0f : 0.0f;
     }
     if (x != x) l = up = x;
-    loss = add(loss, Pair{l, 0.0f});
+    loss.put(Pair{l, 0.0f}, l);
     if (c != r) {  // an episode against itself has no gradient
       if (fabsf(up) < 2048.0f) {
         const float fine = up * kFine;
@@ -602,9 +640,9 @@ __global__ void __launch_bounds__(kThreads) preference_kernel(const LossParams p
     }
   }
   count = block_count(count);
-  loss = block_sum(loss);
   const float share = count ? static_cast<float>(count) : 1.0f;
-  if (threadIdx.x == 0) p.loss[0] = over(loss, share).hi;
+  const Pair mean = mean_of(loss, share);
+  if (threadIdx.x == 0) p.loss[0] = mean.hi;
   __threadfence();
   __syncthreads();
   const float slope = p.kind == PVL_PREFERENCE_SQUARED ? 1.0f : p.beta;
@@ -629,7 +667,7 @@ __global__ void __launch_bounds__(kThreads) policy_kernel(const LossParams p) {
   some = block_count(some);
   // what sums are divided by at the end
   const float whole = static_cast<float>(max(1u, p.mean_episode ? some : tokens));
-  Pair loss{0.0f, 0.0f}, kl{0.0f, 0.0f};
+  Total losses{}, divergences{};
   unsigned int cut = 0;
   for (int e = threadIdx.x; e < E; e += kThreads) {
     const Episode* q = p.episodes + e;
@@ -637,30 +675,31 @@ __global__ void __launch_bounds__(kThreads) policy_kernel(const LossParams p) {
     float slope = 0.0f, weight = 0.0f;
     if (n) {
       const float fn = static_cast<float>(n);
-      const Pair a = value(digits(&q->a), flags, 0);
+      double far = 0.0;
+      const Pair a = value(digits(&q->a), flags, 0, &far);
       weight = p.mean_episode ? 1.0f / (whole * fn) : 1.0f / whole;
       if (p.ratio_episode) {
         const Pair d = over(a, fn);
         const float adv = p.adv[e];
         const bool clip = clipped(p, d, adv);
         const float term = policy_term(p, d.hi, adv, clip);
-        loss = add(loss, p.mean_episode ? Pair{term, 0.0f} : times(term, fn));
+        losses.put(p.mean_episode ? Pair{term, 0.0f} : times(term, fn), p.mean_episode ? term : static_cast<double>(term) * fn);
         slope = clip ? 0.0f : weight * term;
         cut += clip;
       } else {
-        loss = add(loss, p.mean_episode ? over(a, fn) : a);
+        losses.put(p.mean_episode ? over(a, fn) : a, p.mean_episode ? far / fn : far);
         cut += __ldcg(&q->cut);
       }
       if (p.ref) {
-        const Pair b = value(digits(&q->b), flags, 3);
-        kl = add(kl, p.mean_episode ? over(b, fn) : b);
+        const Pair b = value(digits(&q->b), flags, 3, &far);
+        divergences.put(p.mean_episode ? over(b, fn) : b, p.mean_episode ? far / fn : far);
       }
     }
     if (!p.by_token) *reinterpret_cast<float2*>(p.coef + 2 * e) = make_float2(slope, weight);
   }
   cut = block_count(cut);
-  loss = over(block_sum(loss), whole);
-  kl = over(block_sum(kl), whole);
+  Pair loss = mean_of(losses, whole);
+  const Pair kl = mean_of(divergences, whole);
   if (threadIdx.x == 0) {
     // 0 times an infinite divergence is no part of the loss
     if (p.kl_weight != 0.0f) {

@@ -99,3 +99,45 @@ def test_large_divergence(pvl, f):
     want = math.expm1(f) - f
     for got in (out.stats[0].item(), out.loss.item()):
         assert abs(got - want) <= 2.0 ** -19 * want, (got, want)
+
+
+@pytest.mark.parametrize("mean", ["token", "episode"])
+@pytest.mark.parametrize("ratio", ["token", "episode"])
+@pytest.mark.parametrize("N,E", [(64, 1), (5000, 1), (5000, 40), (9000, 700)])
+def test_means_of_large_terms(pvl, mean, ratio, N, E):
+    """Sums past the largest fp32 whose means are not, of the divergence and of the loss, beside small ones."""
+    ids = np.sort(np.arange(N) % E).astype(np.int32)
+    sid = torch.from_numpy(ids).cuda()
+    ref = torch.full((N,), 88.0, device="cuda")
+    ref[::7] = 0.5
+    zero = torch.zeros(N, device="cuda")
+    small = torch.zeros(E, device="cuda")
+    out = pvl.pack_policy_fwd(zero, zero, small, sid, E, ref_logp=ref, kl_weight=0.5, ratio=ratio, mean=mean)
+    loss, kl, _, grad = ob.policy(zero.cpu(), zero.cpu(), small.cpu(), ids, E, ref_logp=ref.cpu(), kl_weight=0.5, ratio=ratio, mean=mean)
+    assert math.isfinite(out.loss.item()) and abs(out.loss.item() - loss) <= 2.0 ** -19 * abs(loss)
+    assert abs(out.stats[0].item() - kl) <= 2.0 ** -19 * kl
+    d = pvl.pack_policy_bwd(None, zero, zero, small, sid, out.coef, ref_logp=ref, kl_weight=0.5, ratio=ratio)
+    assert (np.abs(d.double().cpu().numpy() - grad) <= 2.0 ** -19 * np.abs(grad)).all()
+    adv = torch.full((E,), -3e38, device="cuda")
+    adv[1::3] = 1.0
+    out = pvl.pack_policy_fwd(zero, zero, adv, sid, E, ratio=ratio, mean=mean)
+    loss = ob.policy(zero.cpu(), zero.cpu(), adv.cpu(), ids, E, ratio=ratio, mean=mean)[0]
+    assert abs(out.loss.item() - loss) <= 2.0 ** -19 * abs(loss)
+    # infinities still are
+    ref[3] = 200.0
+    out = pvl.pack_policy_fwd(zero, zero, small, sid, E, ref_logp=ref, kl_weight=0.5, ratio=ratio, mean=mean)
+    assert out.loss.item() == math.inf and out.stats[0].item() == math.inf
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "hinge"])
+def test_mean_of_pairs_lost_by_the_lowest_value(pvl, kind):
+    """Forty pairs, each of a loss of 3.4e37: their sum leaves fp32, their mean does not."""
+    ids = torch.arange(4, dtype=torch.int32, device="cuda").repeat_interleave(10)
+    lp = torch.full((40,), -1.0, device="cuda")
+    low = torch.finfo(torch.float32).min
+    lp[3] = low
+    pairs = torch.tensor([[0, 1]] * 40 + [[2, 3]] * 40, dtype=torch.int32, device="cuda")
+    out = pvl.pack_preference_fwd(lp, None, ids, pairs, 4, kind=kind)
+    assert out.loss.item() == pytest.approx(-0.1 * low / 2, rel=1e-6)
+    own = 0.05 if kind == "sigmoid" else 0.1
+    assert torch.allclose(out.coef.cpu(), torch.tensor([-0.1 / 2, 0.1 / 2, -own / 2, own / 2]), rtol=1e-6)
