@@ -593,7 +593,9 @@ PVL_API pvl_status pack_logprob_bwd(const pvl_logprob* how, const float* lse, co
  * null for 1).  Ids of tokens or pairs at or past `episodes` are left out and
  * reported by pvl_device_error.  ws: pack_preference_ws_bytes(episodes)
  * bytes, 16-byte aligned, contents on entry ignored, one per call in flight.
- * D_e is exact to 2^-41 a token.  The results do not depend on the order in
+ * A sum over tokens is off by at most 2^-41 a token, and by no more than 2^-24
+ * of its terms where these are small, down to 2^-81 a token; the coef of an
+ * episode by 2^-81 beta a pair.  The results do not depend on the order in
  * which blocks run.  Errors: INVALID_ARG for null pointers, counts < 1, a kind
  * or parameters outside their range, a short workspace; UNSUPPORTED for more
  * than 2^23 tokens, 2^16 episodes or 2^20 pairs, or an address off its
@@ -638,7 +640,7 @@ PVL_API pvl_status pack_preference_bwd(const float* dloss, const float* coef, co
  * tokens (with ratio 1: of episodes); coef: dev fp32 [episodes, 2], 8-byte
  * aligned, for pack_policy_bwd, which reads the same inputs and writes dlogp =
  * dloss[0] d loss / d logp, 0 on tokens without an id (dloss null: 1).  Ids,
- * workspace (pack_policy_ws_bytes), limits and errors as pack_preference_*;
+ * sums, workspace (pack_policy_ws_bytes), limits and errors as pack_preference_*;
  * also INVALID_ARG unless 0 <= clip_low < 1, 0 <= clip_high and kl_weight >= 0
  * are finite, and for a kl_weight above 0 without ref_logp.
  * ---------------------------------------------------------------------- */

@@ -22,26 +22,29 @@
 // Both are bound by latency: a 64k pack is 1.6 MB.  One kernel reads the
 // tokens, four a thread; blocks whose tokens belong to one episode add one sum,
 // others one per warp, or one per episode and warp and one per run of a thread
-// whose tokens belong to several.  The last block to
-// finish turns the episodes' sums into the loss and the table.
+// whose tokens belong to several.  The last block to finish turns the episodes'
+// sums into the loss and the table.
 //
 // Measured (one GB300; a captured forward and backward together, with the clear
-// of the sums): the 64k pack's policy loss 16.4 us, 262,144 tokens of 512 episodes
-// 17.5 us, preferences of four episodes of 10,944 tokens 13.1 us, of 512 episodes
-// in 2048 pairs 19.1 us; what they move takes 0.1 to 0.8 us.  One cluster of eight
-// blocks of 1024 threads instead, which needs no clear, took 24 us for the 64k
-// pack: a token costs a hundred instructions, and eight SMs issue them.  Sums in
-// 64-bit floating point took twice the time.
+// of the sums): the 64k pack's policy loss 17.4 us, 262,144 tokens of 512 episodes
+// 18.8 us, preferences of four episodes of 10,944 tokens 12.7 us, of 512 episodes
+// in 2048 pairs 18.9 us, of 4096 in 2048 pairs 47.0 us; what they move takes 0.1
+// to 0.8 us.  (16.5, 17.7, 12.4, 18.6 and 46.9 us without units of 2^-80 and means
+// of large terms.)  One cluster of eight blocks of 1024 threads instead, which
+// needs no clear, took 24 us for the 64k pack: a token costs a hundred
+// instructions, and eight SMs issue them.  Sums in 64-bit floating point took
+// twice the time.
 //
 // Sums are integers, so that they are the same whatever order blocks finish in,
-// and exact.  A token's value in units of 2^-40 and what is left of it in units
-// of 2^-80 (rounded once; differences are taken as exact pairs of fp32 values
-// first) are added in 64 bits within the block, so that small advantages and
-// divergences count as large ones do; an episode holds digits in base 2^40, from
-// 2^-80 to 2^160, to which a block, warp or run adds by integer atomics.  Values
-// of 2^11 and more go to the digits one by one, infinities and NaN to flags.
-// With at most 2^23 tokens a digit's sum stays below 2^63.  64-bit floating point, of which this GPU
-// does little, is left to values that are large.
+// and exact.  A token's value in units of 2^-40, with what is left in units of
+// 2^-80 where that could be 2^-24 of a sum (each rounded once; differences are
+// taken as exact pairs of fp32 values first), is added in 64 bits within the
+// block, so that small advantages and divergences count as large ones do; an
+// episode holds digits in base 2^40, from 2^-80 to 2^160, to which a block, warp
+// or run adds by integer atomics.  Values of 2^11 and more go to the digits one by
+// one, infinities and NaN to flags.  With at most 2^23 tokens a digit's sum stays
+// below 2^63.  64-bit floating point, of which this GPU does little, is left to
+// values that are large or below 2^-19.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -180,23 +183,27 @@ __device__ __forceinline__ Digits digits(const Sum* s) {
   return v;
 }
 
-// A sum's value: a pair, and in 64 bits in *far wherever its magnitude is kNear
-// and more (also for some below, which nothing reads).
+// A sum's value: a pair, and in 64 bits in *far or times kSmall in *small
+// wherever its magnitude is kNear and more (also for others, which nothing
+// reads).
 constexpr float kNear = 1e6f;
+constexpr float kSmall = 1.0f / 4294967296.0f;
 
-__device__ __forceinline__ Pair value(const Digits& s, unsigned int flags, int shift, double* far = nullptr) {
+__device__ __forceinline__ Pair split_of(double v) {
+  const float hi = static_cast<float>(v);
+  return {hi, finite(hi) ? static_cast<float>(v - hi) : 0.0f};
+}
+
+__device__ __forceinline__ Pair value(const Digits& s, unsigned int flags, int shift, double* far = nullptr,
+                                      Pair* small = nullptr) {
   flags = (flags >> shift) & 7u;
   const long long(&d)[6] = s.d;
-  const long long near = (d[5] + (1ll << 39)) >> 40;  // the last digit to nearest, so that what is left may be negative
-  const long long next = d[4] + near, top = d[3] + (next >> 40), last = d[5] - near * (1ll << 40);
-  if (!(flags | d[0] | d[1] | d[2]) && top < (1ll << 19) && top >= -(1ll << 19)) {
-    const long long whole = top * (1ll << 40) + (next & kMask);  // units of 2^-40
-    if (whole < (1ll << 21) && whole > -(1ll << 21)) {
-      constexpr float kUnit = 1.0f / kFine / kFine;
-      const long long all = whole * (1ll << 40) + last;  // units of 2^-80
-      const float hi = __ll2float_rn(all);
-      return {hi * kUnit, __ll2float_rn(all - __float2ll_rn(hi)) * kUnit};
-    }
+  const long long next = d[4] + (d[5] >> 40), top = d[3] + (next >> 40);
+  const long long last = d[5] & kMask;  // units of 2^-80
+  const long long whole = static_cast<long long>(static_cast<unsigned long long>(top) << 40) + (next & kMask);  // 2^-40
+  // below 2^-19 what is left of units of 2^-40 counts, and not to 24 bits
+  const bool fast = !(whole < (1ll << 21) && whole >= -(1ll << 21)) || (whole | last) == 0;
+  if (!(flags | d[0] | d[1] | d[2]) && top < (1ll << 19) && top >= -(1ll << 19) && fast) {
     const float rest = __ll2float_rn(last) * (1.0f / kFine);
     const float hi = __ll2float_rn(whole);
     const Pair u = renormal(hi, __ll2float_rn(whole - __float2ll_rn(hi)) + rest);
@@ -204,8 +211,8 @@ __device__ __forceinline__ Pair value(const Digits& s, unsigned int flags, int s
   }
   const double v = large_value(d, flags);
   if (far) *far = v;
-  const float hi = static_cast<float>(v);
-  return {hi, finite(hi) ? static_cast<float>(v - hi) : 0.0f};
+  if (small) *small = split_of(v * kSmall);
+  return split_of(v);
 }
 
 // What is summed of an episode: two values, valid tokens, clipped tokens.
@@ -245,6 +252,9 @@ __device__ __forceinline__ long long group_sum(unsigned mask, long long v) {
   return (static_cast<long long>(hi) << 44) + (static_cast<long long>(mid) << 22) + lo;
 }
 
+// The same where it is seldom needed: out of the way of the code that always runs.
+__device__ __noinline__ long long rare_sum(unsigned mask, long long v) { return group_sum(mask, v); }
+
 __device__ __forceinline__ Part warp_sum(Part p, bool two) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) p.a += __shfl_xor_sync(kAll, p.a, o);
@@ -252,9 +262,9 @@ __device__ __forceinline__ Part warp_sum(Part p, bool two) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) p.b += __shfl_xor_sync(kAll, p.b, o);
   }
-  if (__any_sync(kAll, (p.fine_a | p.fine_b) != 0)) {  // few warps: terms of 2^-17 and more leave nothing
-    p.fine_a = group_sum(kAll, p.fine_a);
-    if (two) p.fine_b = group_sum(kAll, p.fine_b);
+  if (__any_sync(kAll, (p.fine_a | p.fine_b) != 0)) {
+    p.fine_a = rare_sum(kAll, p.fine_a);
+    p.fine_b = rare_sum(kAll, p.fine_b);
   }
   p.n = __reduce_add_sync(kAll, p.n);
   p.cut = __reduce_add_sync(kAll, p.cut);
@@ -285,42 +295,39 @@ __device__ unsigned int block_count(unsigned int n) {
   return __reduce_add_sync(kAll, threadIdx.x % 32 < kWarps ? part[threadIdx.x % 32] : 0u);
 }
 
-// A sum of losses.  What is kNear and more is added in 64 bits, where no sum of
-// fp32 values overflows before it is divided by their number.
+// A sum of losses.  What is kNear and more is added times kSmall, where no sum
+// of fp32 values overflows before it is divided by their number.
 struct Total {
-  Pair near;
-  double far;
+  Pair near, far;
   bool any;  // whether there is a far part
 
-  __device__ __forceinline__ void put(Pair v, double wide) {
+  // small(): v kSmall, which few calls need
+  template <typename Small>
+  __device__ __forceinline__ void put(Pair v, Small small) {
     if (fabsf(v.hi) < kNear) {
       near = add(near, v);
     } else {
-      far += wide;
+      far = add(far, small());
       any = true;
     }
   }
 };
 
-// (sum over the block of near and far) / n
-__device__ __noinline__ Pair far_mean(Pair near, double far, float n) {
-  __shared__ double part[kWarps];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) far += __shfl_xor_sync(kAll, far, o);
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = far;
-  __syncthreads();
-  double v = static_cast<double>(near.hi) + static_cast<double>(near.lo);
-  for (int i = 0; i < kWarps; ++i) v += part[i];
-  v /= n;
-  const float hi = static_cast<float>(v);
-  return {hi, finite(hi) ? static_cast<float>(v - hi) : 0.0f};
+// Counts with a flag: which warps have a far part.
+constexpr unsigned int kFarFlag = 1u << 24;
+
+__device__ __forceinline__ unsigned int far_flag(bool any) {
+  return __any_sync(kAll, any) && threadIdx.x % 32 == 0 ? kFarFlag : 0u;
 }
 
 // The mean of n values whose sum the block's threads hold; every thread gets it.
-__device__ __forceinline__ Pair mean_of(const Total& t, float n) {
-  const Pair near = block_sum(t.near);
-  return __syncthreads_or(t.any) ? far_mean(near, t.far, n) : over(near, n);
+__device__ __forceinline__ Pair mean_of(const Total& t, float n, bool any) {
+  Pair mean = over(block_sum(t.near), n);
+  if (any) {
+    const Pair far = over(block_sum(t.far), n);
+    mean = add(mean, Pair{far.hi * (1.0f / kSmall), far.lo * (1.0f / kSmall)});
+  }
+  return mean;
 }
 
 // ------------------------------------------------------------- parameters
@@ -416,20 +423,27 @@ __device__ __forceinline__ float policy_term(const LossParams& p, float d, float
 }
 
 // ------------------------------------------------------------- forward
-// A value in units of 2^-40, and what is left of it in units of 2^-80; one that
-// does not fit goes to the episode at once.
-__device__ __forceinline__ void units(Pair v, Sum* s, unsigned int* flags, int shift, long long& whole, long long& fine) {
-  if (fabsf(v.hi) < 2048.0f) {
-    const float x = v.hi * kFine, left = x - rintf(x);
-    whole = __float2ll_rn(x);
-    if (left != 0.0f || v.lo != 0.0f) {
-      const float y = v.lo * kFine;
-      whole += __float2ll_rn(y);
-      fine = __float2ll_rn(left * kFine) + __float2ll_rn((y - rintf(y)) * kFine);
-    }
-  } else {
-    add_any(s, flags, shift, static_cast<double>(v.hi) + static_cast<double>(v.lo));
-  }
+// A value that units of 2^-40 hold, else 0: it went to the episode at once.
+__device__ __forceinline__ Pair ordinary(Pair v, Sum* s, unsigned int* flags, int shift) {
+  if (fabsf(v.hi) < 2048.0f) return v;
+  add_any(s, flags, shift, static_cast<double>(v.hi) + static_cast<double>(v.lo));
+  return {0.0f, 0.0f};
+}
+
+__device__ __forceinline__ long long units(Pair v) {
+  return __float2ll_rn(v.hi * kFine) + __float2ll_rn(v.lo * kFine);
+}
+
+// Whether units of 2^-40 leave anything of hi.
+__device__ __forceinline__ bool leaves(float hi) { return hi != 0.0f && fabsf(hi) < 0x1p-16f; }
+
+// Whether the b of a part's terms are 2^-17 on average.
+__device__ __forceinline__ bool enough(const Part& p) { return p.b >= static_cast<long long>(p.n) << 23; }
+
+// What they leave, in units of 2^-80.
+__device__ __noinline__ long long rest_units(Pair v) {
+  const float x = v.hi * kFine, y = v.lo * kFine;
+  return __float2ll_rn((x - rintf(x)) * kFine) + __float2ll_rn((y - rintf(y)) * kFine);
 }
 
 // Sums of this block's tokens into the episodes'.
@@ -448,10 +462,13 @@ __device__ void sum_tokens(const LossParams& p) {
   if (kPolicy && p.adv_by_token) load4(p.adv, first, p.N, 0.0f, adv);
   const bool two = kPolicy && p.ref;
   Part t[4];
+  Pair va[4], vb[4];
+  bool small_a = false, small_b = false, large_a = false;
   int lo = INT32_MAX, hi = -1;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     t[i] = Part{};
+    va[i] = vb[i] = Pair{0.0f, 0.0f};
     if (id[i] >= p.E) {
       report(p.err, kSiteEpisode);
       id[i] = -1;
@@ -475,8 +492,15 @@ __device__ void sum_tokens(const LossParams& p) {
       a = p.ref ? two_sum(logp[i], -ref[i]) : Pair{logp[i], 0.0f};
     }
     Episode* e = p.episodes + to;
-    units(a, &e->a, &e->flags, 0, t[i].a, t[i].fine_a);
-    if (two) units(b, &e->b, &e->flags, 3, t[i].b, t[i].fine_b);
+    va[i] = ordinary(a, &e->a, &e->flags, 0);
+    t[i].a = units(va[i]);
+    if (two) {
+      vb[i] = ordinary(b, &e->b, &e->flags, 3);
+      t[i].b = units(vb[i]);
+    }
+    small_a = small_a || leaves(va[i].hi);
+    small_b = small_b || leaves(vb[i].hi);
+    large_a = large_a || !(fabsf(a.hi) < 0x1p-10f);
     lo = min(lo, to);
     hi = max(hi, to);
   }
@@ -486,7 +510,24 @@ __device__ void sum_tokens(const LossParams& p) {
     warp_lo[w] = lo;
     warp_hi[w] = hi;
   }
-  Part sum = warp_sum(t[0] + t[1] + t[2] + t[3], two);
+  const Part own = t[0] + t[1] + t[2] + t[3];
+  Part sum = warp_sum(own, two);
+  // What units of 2^-40 leave, where it may count: beside a term of 2^-10, or terms of 2^-17 on average that are none
+  // negative, the 4 or 128 tokens of a thread's or warp's sum lose less than 2^-24 of them.
+  const bool one = lo == hi, alike = id[0] == id[1] && id[1] == id[2] && id[2] == id[3];
+  const bool any_large = __any_sync(kAll, large_a);
+  const bool more_a = small_a && !(alike && large_a) && !(one && any_large);
+  const bool more_b = small_b && !(alike && enough(own)) && !(one && enough(sum));
+  if (__any_sync(kAll, more_a)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i].fine_a = rest_units(va[i]);
+    sum.fine_a = rare_sum(kAll, t[0].fine_a + t[1].fine_a + t[2].fine_a + t[3].fine_a);
+  }
+  if (__any_sync(kAll, more_b)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i].fine_b = rest_units(vb[i]);
+    sum.fine_b = rare_sum(kAll, t[0].fine_b + t[1].fine_b + t[2].fine_b + t[3].fine_b);
+  }
   if (lane == 0) warp_part[w] = sum;
   __syncthreads();
   const int block_lo = __reduce_min_sync(kAll, warp_lo[lane % kWarps]);
@@ -500,16 +541,16 @@ __device__ void sum_tokens(const LossParams& p) {
     }
   } else if (lo == hi) {
     if (lane == 0) add_part(p.episodes + lo, sum);
-  } else if (id[0] == id[1] && id[1] == id[2] && id[2] == id[3]) {
+  } else if (alike) {
     // lanes of one episode each: those of the same one add together
     const unsigned mask = __match_any_sync(__activemask(), id[0]);
     if (id[0] < 0) return;
     sum = t[0] + t[1] + t[2] + t[3];
     sum.a = group_sum(mask, sum.a);
-    sum.fine_a = group_sum(mask, sum.fine_a);
-    if (two) {
-      sum.b = group_sum(mask, sum.b);
-      sum.fine_b = group_sum(mask, sum.fine_b);
+    if (two) sum.b = group_sum(mask, sum.b);
+    if (__any_sync(mask, (sum.fine_a | sum.fine_b) != 0)) {
+      sum.fine_a = rare_sum(mask, sum.fine_a);
+      sum.fine_b = rare_sum(mask, sum.fine_b);
     }
     sum.n = __reduce_add_sync(mask, sum.n);
     sum.cut = __reduce_add_sync(mask, sum.cut);
@@ -598,8 +639,7 @@ __global__ void __launch_bounds__(kThreads) preference_kernel(const LossParams p
       short_of = above(Pair{2.0f * p.target.hi, 2.0f * p.target.lo}, h);
     } else {
       const double dc = wide(p, c, vc), dr = wide(p, r, vr), d = dc - dr - p.margin_d;
-      const float hi = static_cast<float>(d);
-      h = {hi, finite(hi) ? static_cast<float>(d - hi) : 0.0f};
+      h = split_of(d);
       x = static_cast<float>(p.beta_d * d);
       short_of = p.beta_d * d < 1.0;
       rc = static_cast<float>(p.beta_d * dc);
@@ -624,7 +664,7 @@ __global__ void __launch_bounds__(kThreads) preference_kernel(const LossParams p
       up = short_of ? -1.0f : 0.0f;
     }
     if (x != x) l = up = x;
-    loss.put(Pair{l, 0.0f}, l);
+    loss.put(Pair{l, 0.0f}, [&] { return Pair{l * kSmall, 0.0f}; });
     if (c != r) {  // an episode against itself has no gradient
       if (fabsf(up) < 2048.0f) {
         const float fine = up * kFine;
@@ -639,9 +679,11 @@ __global__ void __launch_bounds__(kThreads) preference_kernel(const LossParams p
       }
     }
   }
-  count = block_count(count);
+  count = block_count(count + far_flag(loss.any));
+  const bool any = count >= kFarFlag;
+  count %= kFarFlag;
   const float share = count ? static_cast<float>(count) : 1.0f;
-  const Pair mean = mean_of(loss, share);
+  const Pair mean = mean_of(loss, share, any);
   if (threadIdx.x == 0) p.loss[0] = mean.hi;
   __threadfence();
   __syncthreads();
@@ -675,31 +717,34 @@ __global__ void __launch_bounds__(kThreads) policy_kernel(const LossParams p) {
     float slope = 0.0f, weight = 0.0f;
     if (n) {
       const float fn = static_cast<float>(n);
-      double far = 0.0;
-      const Pair a = value(digits(&q->a), flags, 0, &far);
+      Pair small{0.0f, 0.0f};
+      const Pair a = value(digits(&q->a), flags, 0, nullptr, &small);
       weight = p.mean_episode ? 1.0f / (whole * fn) : 1.0f / whole;
       if (p.ratio_episode) {
         const Pair d = over(a, fn);
         const float adv = p.adv[e];
         const bool clip = clipped(p, d, adv);
         const float term = policy_term(p, d.hi, adv, clip);
-        losses.put(p.mean_episode ? Pair{term, 0.0f} : times(term, fn), p.mean_episode ? term : static_cast<double>(term) * fn);
+        losses.put(p.mean_episode ? Pair{term, 0.0f} : times(term, fn),
+                   [&] { return p.mean_episode ? Pair{term * kSmall, 0.0f} : times(term * kSmall, fn); });
         slope = clip ? 0.0f : weight * term;
         cut += clip;
       } else {
-        losses.put(p.mean_episode ? over(a, fn) : a, p.mean_episode ? far / fn : far);
+        losses.put(p.mean_episode ? over(a, fn) : a, [&] { return p.mean_episode ? over(small, fn) : small; });
         cut += __ldcg(&q->cut);
       }
       if (p.ref) {
-        const Pair b = value(digits(&q->b), flags, 3, &far);
-        divergences.put(p.mean_episode ? over(b, fn) : b, p.mean_episode ? far / fn : far);
+        const Pair b = value(digits(&q->b), flags, 3, nullptr, &small);
+        divergences.put(p.mean_episode ? over(b, fn) : b, [&] { return p.mean_episode ? over(small, fn) : small; });
       }
     }
     if (!p.by_token) *reinterpret_cast<float2*>(p.coef + 2 * e) = make_float2(slope, weight);
   }
-  cut = block_count(cut);
-  Pair loss = mean_of(losses, whole);
-  const Pair kl = mean_of(divergences, whole);
+  cut = block_count(cut + far_flag(losses.any || divergences.any));
+  const bool any = cut >= kFarFlag;
+  cut %= kFarFlag;
+  Pair loss = mean_of(losses, whole, any);
+  const Pair kl = mean_of(divergences, whole, any);
   if (threadIdx.x == 0) {
     // 0 times an infinite divergence is no part of the loss
     if (p.kl_weight != 0.0f) {
