@@ -43,6 +43,9 @@ constexpr int kThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFar = -1e30f;  // stands for -inf where it is multiplied by 0
+// The same in the gradient, whose probabilities are 0 from -88 on: no further than that, so that its product with a
+// large gradient of the entropy stays finite.
+constexpr float kGone = -128.0f;
 constexpr int kCluster = 8;
 constexpr int kSegVec = 16 * kThreads;  // vectors of a row that a backward block takes: sixteen a thread
 
@@ -299,7 +302,7 @@ __device__ __forceinline__ float grad_of(float x, float inv_t, const RowGrad& g)
   const float z = fmaf(x, inv_t, -g.lse);
   const float pr = ex2(z * kLog2e);
   float up = g.up;
-  if (kEnt) up = fmaf(g.dent, fmaxf(z, kFar) + g.ent, up);
+  if (kEnt) up = fmaf(g.dent, fmaxf(z, kGone) + g.ent, up);
   return -pr * up;
 }
 
