@@ -89,10 +89,19 @@ def pack_logprob_fwd(logits, targets, seq_id=None, *, temperature: float = 1.0, 
     return _run_logprob(how, dev, shape, logp, lse, ent, entropy, handle)
 
 
+def _wrote(*outputs) -> None:
+    """Counts the outputs that a caller gave (None for the others) as changed in place, as autograd has it for its own:
+    a graph that needs what they held refuses to go on."""
+    torch.autograd.graph.increment_version([t for t in outputs if t is not None])
+
+
 def _run_logprob(how, dev, shape, logp, lse, ent, entropy, handle):
+    given = (logp, lse, ent if entropy else None) if logp is not None or lse is not None or ent is not None else None
     logp, lse = _rows(logp, "logp", shape, dev), _rows(lse, "lse", shape, dev)
     ent = _rows(ent, "ent", shape, dev) if entropy else None
     _check(_lib.load().pack_logprob_fwd(how, logp.data_ptr(), lse.data_ptr(), _ptr(ent), handle))
+    if given is not None:
+        _wrote(*given)
     return logp, lse, ent
 
 
@@ -101,8 +110,8 @@ def pack_logprob_bwd(dlogp, logits, targets, lse, seq_id=None, *, temperature: f
     """Gradient of pack_logprob_fwd to the logits, of their type: from dlogp
     (fp32 [B, L], or None for zero) and, with dent, from the gradient of the
     entropy (which needs ent, the forward's).  dlogits, where given, may have
-    strides of its own; it may be the logits, which are then overwritten, but
-    not otherwise reach into them."""
+    strides of its own; it may be the logits, which are then overwritten (a
+    change in place to autograd), but not otherwise reach into them."""
     how, dev, shape = _logprob(logits, targets, seq_id, temperature)
     if dlogp is None and dent is None:
         raise ValueError("dlogp or dent must be given")
@@ -123,11 +132,14 @@ def pack_logprob_bwd(dlogp, logits, targets, lse, seq_id=None, *, temperature: f
 
 
 def _run_logprob_bwd(how, logits, lse, ent, dlogp, dent, dlogits, handle):
+    given = dlogits
     if dlogits is None:
         dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
     sb, sl = _row_strides(dlogits, "dlogits")
     _check(_lib.load().pack_logprob_bwd(how, lse.data_ptr(), _ptr(ent), _ptr(dlogp), _ptr(dent), dlogits.data_ptr(),
                                         sb, sl, handle))
+    if given is not None:
+        _wrote(given)
     return dlogits
 
 
@@ -240,9 +252,12 @@ def pack_preference_bwd(dloss, coef, seq_id, *, dlogp=None, stream=None):
 
 
 def _run_preference_bwd(dloss, coef, seq_id, dlogp, shape, dev, handle):
+    given = dlogp
     dlogp = _rows(dlogp, "dlogp", shape, dev)
     _check(_lib.load().pack_preference_bwd(_ptr(dloss), coef.data_ptr(), seq_id.data_ptr(), seq_id.numel(),
                                            coef.shape[0], dlogp.data_ptr(), handle))
+    if given is not None:
+        _wrote(given)
     return dlogp
 
 
@@ -333,6 +348,9 @@ def pack_policy_bwd(dloss, logp, old_logp, advantages, seq_id, coef, *, ref_logp
 
 
 def _run_policy_bwd(how, dloss, coef, dlogp, shape, dev, handle):
+    given = dlogp
     dlogp = _rows(dlogp, "dlogp", shape, dev)
     _check(_lib.load().pack_policy_bwd(how, _ptr(dloss), coef.data_ptr(), dlogp.data_ptr(), handle))
+    if given is not None:
+        _wrote(given)
     return dlogp

@@ -80,6 +80,7 @@ def grad_norm(grads, out=None, ws=None, stream=None) -> torch.Tensor:
 
 def _run_norm(grads, counts, kind, dev, out, ws, handle):
     lib = _lib.load()
+    given = out is not None
     if out is None:
         out = torch.empty(1, dtype=torch.float32, device=dev)
     else:
@@ -91,6 +92,8 @@ def _run_norm(grads, counts, kind, dev, out, ws, handle):
     ptrs, sizes = array("Q", map(_address, grads)), array("q", counts)
     _check(lib.pvl_grad_norm(ptrs.buffer_info()[0], sizes.buffer_info()[0], len(grads), kind, out.data_ptr(),
                              ws.data_ptr(), ws.numel(), handle))
+    if given:
+        torch.autograd.graph.increment_version(out)
     return out
 
 
