@@ -183,6 +183,14 @@ def token_logprob(logits, targets, seq_id=None, *, temperature: float = 1.0, ent
     return _TokenLogprob.apply(logits, targets, seq_id, temperature, entropy)
 
 
+def _constants(op: str, **tensors) -> None:
+    """What an op takes as given may not ask for a gradient, which would be lost."""
+    if torch.is_grad_enabled():
+        for name, t in tensors.items():
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                raise ValueError(f"{op} gives no gradient to {name}, which requires one: pass {name}.detach()")
+
+
 class _PreferenceLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logp, ref_logp, seq_id, pairs, episodes, how):
@@ -202,7 +210,9 @@ def preference_loss(logp, ref_logp, seq_id, pairs, episodes: int, *, beta: float
                     smoothing: float = 0.0, margin: float = 0.0, mean: bool = False):
     """(loss, rewards) of objectives.pack_preference_fwd: the preference loss
     over pairs of packed episodes, differentiable in logp, and the rewards of
-    each pair's episodes."""
+    each pair's episodes.  ref_logp is taken as given: one that requires a
+    gradient is refused."""
+    _constants("preference_loss", ref_logp=ref_logp)
     how = dict(beta=beta, kind=kind, smoothing=smoothing, margin=margin, mean=mean)
     return _PreferenceLoss.apply(logp, ref_logp, seq_id, pairs, episodes, how)
 
@@ -229,6 +239,8 @@ def policy_loss(logp, old_logp, advantages, seq_id, episodes: int, *, ref_logp=N
                 clip_high: float = 0.2, kl_weight: float = 0.0, ratio: str = "token", mean: str = "token"):
     """(loss, stats) of objectives.pack_policy_fwd: the clipped policy loss with
     its divergence term, differentiable in logp, and (divergence, share of
-    clipped ratios)."""
+    clipped ratios).  What it is measured against (old_logp, advantages,
+    ref_logp) is taken as given: tensors that require a gradient are refused."""
+    _constants("policy_loss", old_logp=old_logp, advantages=advantages, ref_logp=ref_logp)
     how = dict(clip_low=clip_low, clip_high=clip_high, kl_weight=kl_weight, ratio=ratio)
     return _PolicyLoss.apply(logp, old_logp, advantages, seq_id, ref_logp, episodes, mean, how)
