@@ -698,14 +698,16 @@ PVL_API pvl_status pvl_grad_norm(const void* const* grads, const int64_t* sizes,
  *   elements of m, v and master; elements after its end are 0 and stay so.
  *   bits 32: m, v dev fp32.  bits 8: m, v dev e4m3 bytes, m_scale, v_scale dev
  *   fp32 one a block: m = code m_scale, v = (code v_scale)^2.  Both are rounded
- *   stochastically, by bits that depend on seed, step and place alone; a code
+ *   stochastically, by bits that depend on seed, step and place alone, so m has
+ *   no bias, and the mean of v, a square, lies up to 6 % high (beta2 0.999); a code
  *   of v that is not 0 stays at least 2^-9; blocks whose largest |m| or sqrt(v)
  *   is below 2^-100 become 0.  An infinite or NaN gradient leaves NaN in its own
  *   element (parameter and moments), and the block's scales to the others.
  * A v past the largest fp32 number is infinite for good and its element only
  *   decays (8 bits: the NaN code of v beside m = 0).
  *   master: dev fp32, for bf16 parameters, which are then its rounded copy and
- *   are not read; null for fp32 parameters.
+ *   are not read (what else is written to them is lost); null for fp32
+ *   parameters.
  * steps: dev int32; done: dev uint32 that is 0 before the first step (the
  *   library leaves it so); lr_dev: dev fp32 [1] or null (then lr).  m, v,
  *   master 32-byte aligned.  Steps that share states must follow one another.

@@ -33,13 +33,15 @@
 // block of the grid to finish, when all have read it.
 //
 // Measured (one GB300, of the 6793 GB/s of its copy): 680 M parameters, bf16 over
-// fp32 masters, bf16 gradients: 32-bit moments 2947-3018 us = 6.46-6.31 TB/s
-// (95-93 %, by box), 8-bit 1788 us = 6.11 TB/s (90 %); 28 M parameters in fp32 131 us = 6.13 TB/s; the norm
-// of 680 M bf16 gradients 214 us = 6.37 TB/s (94 %).  With 8-bit moments half the
-// bytes go in pieces of 256 and less a warp and stream (five streams to read,
-// five to write), and issue slots are 63 % full: chunks of four blocks a warp
-// (1861 us), the next block's loads ahead of this one's arithmetic (1866 us) and
-// no random bits at all (1888 us beside 1861) moved it less than what is left.
+// fp32 masters, bf16 gradients: 32-bit moments 2947-3024 us = 6.46-6.30 TB/s
+// (95-93 %, by box), 8-bit 1814-1821 us = 6.02 TB/s (88 %); 28 M parameters in
+// fp32 131 us = 6.13 TB/s; the norm of 680 M bf16 gradients 204-214 us = 6.67-6.37
+// TB/s (98-94 %).  With 8-bit moments half the bytes go in pieces of 256 and less a
+// warp and stream (five streams to read, five to write), and issue slots are 65 %
+// full.  At 1811 us (63 %), before small decay and what is not finite were seen to,
+// chunks of four blocks a warp (1861 us), the next block's loads ahead of this
+// one's arithmetic (1866 us) and no random bits at all (1888 us beside 1861) moved
+// it less than what is left.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 

@@ -104,7 +104,10 @@ class AdamWState:
 
     bits 32: m and v are fp32.  bits 8: they are torch.float8_e4m3fn, with one
     fp32 scale a block, and v holds the root: m = code m_scale, sqrt(v) = code
-    v_scale, infinite where v's code is NaN and m's is not.  master holds bf16 parameters in fp32 (None for fp32 ones)."""
+    v_scale, infinite where v's code is NaN and m's is not.  Rounding leaves m
+    without bias and raises the mean of v by up to 6 % (betas[1] 0.999): steps are
+    up to 3 % shorter than with 32 bits.  master holds bf16 parameters in fp32
+    (None for fp32 ones)."""
     m: torch.Tensor
     v: torch.Tensor
     m_scale: torch.Tensor | None
