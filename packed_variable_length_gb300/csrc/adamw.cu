@@ -310,8 +310,8 @@ struct Divisor {
 };
 
 // ---------------------------------------------------------------- step
-// 1 - x as hi + lo: exact up to a rounding of lo, of at most 2^-24 of hi.  Both have one sign and lo is not 0, so that
-// an infinite parameter stays what it is.
+// 1 - x as hi + lo: exact up to a rounding of lo, at most 2^-23 of hi.  Both have one sign and lo is not 0 unless
+// 1 - x is, so that an infinite parameter stays what it is.
 struct Keep {
   float hi, lo;
 };
@@ -325,7 +325,7 @@ __device__ __forceinline__ Keep keep_of(float x) {
     lo = __fadd_rn(lo, __fsub_rn(hi, down));
     hi = down;
   }
-  if (lo == 0.0f) lo = copysignf(0x1p-100f, hi);
+  if (lo == 0.0f) lo = hi * 0x1p-100f;
   return {hi, lo};
 }
 

@@ -75,3 +75,12 @@ def test_what_a_step_of_nothing_leaves(pvl, bits, dtype):
         if lr * decay == 0.0:
             bits_of = torch.int32 if dtype == torch.float32 else torch.int16
             assert torch.equal(q.view(bits_of), p.view(bits_of)), (q, p)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_decay_of_all_leaves_nothing(pvl, bits, dtype):
+    p = torch.randn(1000, device="cuda").to(dtype)
+    state = pvl.adamw_state([p], bits=bits)
+    pvl.adamw_step([p], [torch.zeros_like(p)], state, 0.5, weight_decay=2.0)
+    assert not p.any()
